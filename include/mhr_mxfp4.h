@@ -1,0 +1,86 @@
+/*
+ * mhr_mxfp4.h -- microscaled 4-bit floats (MXFP4) in libmhr_gemm.so:
+ * quantisation, products, and a mixture-of-experts layer for a few tokens.
+ *
+ * The format.  A value is an e2m1 code -- 0, 0.5, 1, 1.5, 2, 3, 4 or 6 and a
+ * sign in bit 3 -- times an e8m0 scale 2^(code - 127) that 32 consecutive
+ * values of a row share (code 255: NaN).  A rows x cols matrix is two arrays:
+ *   data    row r starts at r * ld bytes and holds 16 * ceil(cols / 32) bytes,
+ *           two codes a byte, the even column in the low half; the last
+ *           block's columns past cols hold zero codes.  16-byte aligned, ld a
+ *           multiple of 16.
+ *   scales  tiles of 128 rows x 4 blocks, 512 bytes each, row-major over
+ *           ceil(rows / 128) x ceil(blocks / 4) tiles; the scale of row r and
+ *           block b (columns 32 b to 32 b + 31) is byte
+ *           (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile
+ *           (r / 128, b / 4).  Bytes past the last row or block are no code of
+ *           any value; those past the last block must not be 255.
+ *           16-byte aligned, gemm_mxfp4_scale_bytes(rows, cols) bytes.
+ *
+ * Pointers, streams, errors and threads as in mhr_gemm.h: device pointers on
+ * the current device, work enqueued on `stream`, an mhr_status returned,
+ * device-side timeouts reported by gemm_check().  Empty sizes are no-ops.
+ */
+#ifndef MHR_MXFP4_H
+#define MHR_MXFP4_H
+
+#include <stdint.h>
+
+#include "mhr_gemm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* Element types of plain matrices. */
+typedef enum mhr_dtype { MHR_F32 = 0, MHR_BF16 = 1, MHR_F16 = 2 } mhr_dtype;
+
+/* Size of the scales of a rows x cols matrix; -1 for a negative size. */
+int64_t gemm_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Quantise X (rows x cols, row-major, pitch ldx elements, type dtype).
+ * transpose == 0: blocks run along X's rows; the packed matrix is X, rows x
+ * cols.  transpose != 0: blocks run down X's columns; the packed matrix is
+ * X^T, cols x rows -- the form in which gemm_mxfp4 takes its right operand.
+ *
+ * A block's scale is 2^(floor(log2 m) - 2), m its largest magnitude, and no
+ * less than 2^-127; its codes are x / scale rounded to nearest, ties to the
+ * even code, magnitudes above 6 to 6.  A block that holds an infinity or a NaN
+ * gets the scale NaN and zero codes.  Padding rows and blocks of the scales
+ * are written as zero.
+ *
+ * values (or NULL): also writes what the codes stand for, in X's type and
+ * shape with pitch ldv -- exact, since every such value is representable.
+ * data, scales and values must not overlap X or one another.
+ */
+int gemm_mxfp4_quantize(int dtype, const void* X, int64_t rows, int64_t cols, int64_t ldx,
+                        int transpose, uint8_t* data, int64_t ldd, uint8_t* scales, void* values,
+                        int64_t ldv, void* stream);
+
+/*
+ * C = A B: A is M x K in 4 bits, B is given as B^T, N x K in 4 bits (lda, ldb:
+ * bytes a row), C is M x N, row-major, pitch ldc elements, type c_dtype.
+ * Products are exact, sums are held in fp32 on the tensor cores
+ * (tcgen05.mma kind::mxf4, block scales applied there), C is rounded once.
+ * K == 0 writes zeros.  C must not overlap an operand.
+ */
+int gemm_mxfp4(int c_dtype, const uint8_t* A, const uint8_t* A_scales, const uint8_t* Bt,
+               const uint8_t* Bt_scales, void* C, int64_t M, int64_t N, int64_t K, int64_t lda,
+               int64_t ldb, int64_t ldc, void* stream);
+
+/*
+ * The same with A (M x K, row-major, pitch lda elements, type a_dtype)
+ * quantised on the way as gemm_mxfp4_quantize does along its rows: the C of
+ * quantising and then multiplying, bit for bit.  The packed A lives in the
+ * library's workspace (see mhr_gemm.h).
+ */
+int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const uint8_t* Bt,
+                         const uint8_t* Bt_scales, void* C, int64_t M, int64_t N, int64_t K,
+                         int64_t lda, int64_t ldb, int64_t ldc, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MHR_MXFP4_H */

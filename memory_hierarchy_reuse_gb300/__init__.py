@@ -20,7 +20,8 @@ Raw entry points (same names and arguments as the C ABI; pointers are ints,
 
 Tensor-level helper: ``matmul(a, b, path, out=None)`` for row-major CUDA
 tensors (the last dimension contiguous; the leading dimension is the row
-stride).
+stride). 4-bit operands (``include/mhr_mxfp4.h``): ``quantize_mxfp4`` and
+``matmul_mxfp4``, in ``mxfp4.py``.
 """
 from __future__ import annotations
 
@@ -51,7 +52,8 @@ EXPORTS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_bf16_f32acc", "gemm_f32_3xtf32_n
            "gemm_testing_set_zero_a_small", "gemm_testing_set_pair_tile_n",
            "gemm_testing_plan_pair_tile_n", "gemm_testing_set_single_tile_n",
            "gemm_testing_plan_single_tile_n", "gemm_testing_set_simt_wide_mode",
-           "gemm_testing_plan_simt_wide")
+           "gemm_testing_plan_simt_wide",
+           "gemm_mxfp4_scale_bytes", "gemm_mxfp4_quantize", "gemm_mxfp4", "gemm_mxfp4_quantized")
 
 _lib = None
 
@@ -88,6 +90,15 @@ def load(path: str | None = None):
     lib.gemm_release.restype = None
     lib.gemm_version.argtypes = []
     lib.gemm_version.restype = ctypes.c_int
+    ci = ctypes.c_int
+    lib.gemm_mxfp4_scale_bytes.argtypes = [i64, i64]
+    lib.gemm_mxfp4_scale_bytes.restype = i64
+    lib.gemm_mxfp4_quantize.argtypes = [ci, vp, i64, i64, i64, ci, vp, i64, vp, vp, i64, vp]
+    lib.gemm_mxfp4_quantize.restype = ci
+    lib.gemm_mxfp4.argtypes = [ci, vp, vp, vp, vp, vp, i64, i64, i64, i64, i64, i64, vp]
+    lib.gemm_mxfp4.restype = ci
+    lib.gemm_mxfp4_quantized.argtypes = [ci, vp, ci, vp, vp, vp, i64, i64, i64, i64, i64, i64, vp]
+    lib.gemm_mxfp4_quantized.restype = ci
     lib.gemm_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.gemm_testing_set_wait_limit_ns.restype = ctypes.c_uint64
     lib.gemm_testing_set_inject_stall.argtypes = [ctypes.c_int]
@@ -301,3 +312,13 @@ def gemm_testing_plan_simt_wide(M: int, N: int, K: int, sms: int) -> int:
     """The automatic SIMT kernel choice: 0 128 x 128, 1 128 x 256, 2 128 x 256
     on K halves (host logic only)."""
     return load().gemm_testing_plan_simt_wide(M, N, K, int(sms))
+
+
+def __getattr__(name):
+    # the 4-bit calls import torch, which the raw entry points do without
+    if name in ("MxFp4Matrix", "mxfp4_scale_bytes", "quantize_mxfp4", "matmul_mxfp4"):
+        from . import mxfp4
+
+        globals()[name] = getattr(mxfp4, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -311,6 +311,26 @@ int device_ctl_locked(DeviceCtl* ctl, int* dev) {
   return rc;
 }
 
+int workspace_locked(int dev, cudaStream_t s, size_t bytes, void** out, void** token) {
+  Workspace* w = nullptr;
+  const int rc = workspace(dev, s, bytes, out, &w);
+  *token = w;
+  return rc;
+}
+
+void workspace_done_locked(void* token, cudaStream_t s) {
+  workspace_used(static_cast<Workspace*>(token), s);
+}
+
+bool byte_range(const void* p, int64_t rows, int64_t row_bytes, int64_t pitch_bytes,
+                ByteRange* r) {
+  if (rows <= 0 || row_bytes <= 0) {
+    *r = ByteRange{};
+    return true;
+  }
+  return extent(p, rows, row_bytes, pitch_bytes, 1, &r->lo, &r->hi);
+}
+
 void main_events_arm(cudaStream_t s) {
   if (g_main_start && g_main_stop) {
     g_events_stream = s;

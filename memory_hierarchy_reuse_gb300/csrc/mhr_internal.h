@@ -153,6 +153,23 @@ std::mutex& library_mutex();
 // library_mutex().
 int device_ctl_locked(DeviceCtl* ctl, int* dev);
 
+// The library's workspace for entry points in other translation units: at
+// least `bytes` for (device, stream), ready for use on `s`, as an mhr_status;
+// after its launches the caller passes *token to workspace_done_locked().
+// The caller holds library_mutex() throughout.
+int workspace_locked(int dev, cudaStream_t s, size_t bytes, void** out, void** token);
+void workspace_done_locked(void* token, cudaStream_t s);
+
+// The bytes that rows x row_bytes with a pitch span; false where that leaves
+// the address space.  A range of no bytes overlaps nothing.
+struct ByteRange {
+  uintptr_t lo = 0, hi = 0;
+};
+bool byte_range(const void* p, int64_t rows, int64_t row_bytes, int64_t pitch_bytes, ByteRange* r);
+inline bool ranges_overlap(const ByteRange& a, const ByteRange& b) {
+  return a.lo < b.hi && b.lo < a.hi;
+}
+
 // The caller's profiling events around the main kernel of a call
 // (gemm_testing_set_main_kernel_events): while armed, note_main_kernel()
 // records the start event on the call's stream right before the main kernel

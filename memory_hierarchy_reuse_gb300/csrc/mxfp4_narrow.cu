@@ -1,0 +1,315 @@
+// The 4-bit product for few rows of A: C^T tiles of 128 columns of C (rows of
+// B^T) x up to 128 rows of A, one CTA each, with the K blocks of a tile split
+// over a cluster of CTAs when tiles are few.
+//
+// With few rows of A the product is a pass over B: N K 17/32 bytes against
+// M N K multiply-adds.  So B takes the MMA's 128-row side, whole K-tiles of it
+// stream in by TMA, and A's rows are the MMA's N (8 to 128 in steps of 8).
+// The cluster's CTAs each hold a partial sum in TMEM; they meet in distributed
+// shared memory and are added in rank order, so a result is the same from call
+// to call.
+#include "mhr_gemm.h"
+#include "mhr_mxfp4.h"
+#include "mxfp4_common.cuh"
+
+namespace mhr {
+namespace mx {
+namespace {
+
+constexpr int BK_BYTES = 128;         // 256 columns of K a stage: one swizzle row
+constexpr int W_ROWS = 128;           // rows of B^T a tile: the MMA's M
+constexpr int W_BYTES = W_ROWS * BK_BYTES;
+constexpr int SF_BYTES = 1024;        // two scale tiles of 128 rows
+constexpr int MAX_STAGES = 10;
+constexpr int MAX_NT = 128;           // rows of A a tile: the MMA's N
+constexpr int THREADS = 192;
+constexpr int MAX_SPLIT = 8;
+constexpr int SMEM_LIMIT = 227 * 1024;
+
+struct NarrowParams {
+  int32_t M, N;
+  int32_t nt;              // rows of A a tile, a multiple of 8
+  int32_t tiles_n, split;  // tiles along N; CTAs (K parts) a tile
+  int32_t num_kb;          // stages of 256 columns in K
+  int32_t blocks, kt;      // blocks of 32 in K; scale tiles a row
+  int32_t stages, stage_bytes;
+  int32_t early_b;         // B is not written by the kernel before this one
+  const uint8_t* sfa;
+  const uint8_t* sfb;
+  void* C;
+  int64_t ldc;
+  int32_t c_dtype;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  int32_t inject_stall;
+};
+
+__device__ __forceinline__ void store_c(const NarrowParams& p, int64_t at, float v) {
+  if (p.c_dtype == MHR_F32)
+    static_cast<float*>(p.C)[at] = v;
+  else if (p.c_dtype == MHR_BF16)
+    static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
+  else
+    static_cast<__half*>(p.C)[at] = __float2half_rn(v);
+}
+
+// Warp roles: 0 TMA producer, 1 TMEM allocator and MMA issuer, 2-5 epilogue
+// (TMEM lanes 32 * (warp % 4) on).  Every wait is bounded; a role that gives
+// up records it in the status word and raises the CTA's abort flag.
+__global__ void __launch_bounds__(THREADS, 1)
+    mxfp4_narrow_kernel(const __grid_constant__ CUtensorMap tmA,
+                        const __grid_constant__ CUtensorMap tmB, const NarrowParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(8) uint64_t bars[2 * MAX_STAGES + 1];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (MAX_STAGES + s); };
+  const uint32_t acc_bar = bar0 + 8u * (2 * MAX_STAGES);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
+  const int tile = blockIdx.x / p.split;
+  const int tile_m = tile / p.tiles_n;
+  const int n0 = (tile - tile_m * p.tiles_n) * W_ROWS, m0 = tile_m * p.nt;
+  const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / p.split);
+  const int kb1 = static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / p.split);
+  constexpr uint32_t TMEM_COLS = 256;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    mbar_init(acc_bar, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint64_t limit = p.wait_limit_ns;
+  auto give_up = [&](uint32_t bit) {  // by one thread
+    if (!abort_flag) atomicOr(p.status, bit);
+    abort_flag = 1;
+  };
+  const int x_bytes = p.nt * BK_BYTES;
+  const uint32_t off_x = W_BYTES, off_sfb = W_BYTES + x_bytes, off_sfa = off_sfb + SF_BYTES;
+  auto sf_bytes = [&](int kb) { return static_cast<uint32_t>(min(2, p.kt - 2 * kb)) * 512u; };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      auto load_b = [&](uint32_t st, uint32_t bar, int kb) {
+        tma_load_2d(st, &tmB, bar, kb * BK_BYTES, n0);
+        bulk_load(st + off_sfb, p.sfb + (static_cast<int64_t>(n0 / 128) * p.kt + 2 * kb) * 512,
+                  sf_bytes(kb), bar);
+      };
+      auto load_a = [&](uint32_t st, uint32_t bar, int kb) {
+        tma_load_2d(st + off_x, &tmA, bar, kb * BK_BYTES, m0);
+        bulk_load(st + off_sfa, p.sfa + (static_cast<int64_t>(m0 / 128) * p.kt + 2 * kb) * 512,
+                  sf_bytes(kb), bar);
+      };
+      auto tx = [&](int kb) { return W_BYTES + x_bytes + 2u * sf_bytes(kb); };
+      const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
+      // The first stages' B before the kernel before this one (A's
+      // quantisation) has finished, where that is known not to write B.
+      const int ahead = min(p.stages, kb1 - kb0);
+      for (int i = 0; i < ahead; ++i) mbar_arrive_expect_tx(full_bar(i), tx(kb0 + i));
+      if (!p.early_b) grid_dependency_wait();
+      for (int i = stall ? 1 : 0; i < ahead; ++i)
+        load_b(sbase + i * p.stage_bytes, full_bar(i), kb0 + i);
+      if (p.early_b) grid_dependency_wait();
+      for (int i = stall ? 1 : 0; i < ahead; ++i)
+        load_a(sbase + i * p.stage_bytes, full_bar(i), kb0 + i);
+      int it = ahead;
+      for (; kb0 + it < kb1; ++it) {
+        const uint32_t s = it % p.stages, ph = (it / p.stages) & 1u;
+        if (!mbar_wait_bounded(empty_bar(s), ph ^ 1u, limit, &abort_flag)) {
+          give_up(kErrTimeoutProducer);
+          break;
+        }
+        mbar_arrive_expect_tx(full_bar(s), tx(kb0 + it));
+        load_b(sbase + s * p.stage_bytes, full_bar(s), kb0 + it);
+        load_a(sbase + s * p.stage_bytes, full_bar(s), kb0 + it);
+      }
+      // This CTA's copies in flight have landed before it goes on to leave.
+      volatile int never = 0;
+      for (int i = max(0, it - p.stages); i < it; ++i) {
+        if (stall && i == 0) {  // counted as done once the MMA issuer has given up on it
+          mbar_wait_bounded(full_bar(0), 0, 2 * limit, &abort_flag);
+          mbar_complete_tx(full_bar(0), tx(kb0));
+        }
+        if (!mbar_wait_bounded(full_bar(i % p.stages), (i / p.stages) & 1u, limit, &never))
+          atomicOr(p.status, kErrTimeoutDrain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t id0 = make_idesc_mxf4(W_ROWS, p.nt, 0), id2 = make_idesc_mxf4(W_ROWS, p.nt, 2);
+      for (int it = 0; kb0 + it < kb1; ++it) {
+        const uint32_t s = it % p.stages, ph = (it / p.stages) & 1u;
+        // scales alternate between two sets of TMEM columns: the MMAs two
+        // stages back, which read this set last, have finished
+        const bool ok =
+            (it < 2 || mbar_wait_bounded(empty_bar((it - 2) % p.stages),
+                                         ((it - 2) / p.stages) & 1u, limit, &abort_flag)) &&
+            mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag);
+        if (!ok) {
+          give_up(kErrTimeoutMma);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t st = sbase + s * p.stage_bytes;
+        const int kb = kb0 + it;
+        const uint32_t sfb = tmem + MAX_NT + (it & 1) * 16, sfa = sfb + 8;
+        for (int i = 0; i < min(2, p.kt - 2 * kb); ++i) {
+          copy_scale_tile<1>(sfb + 4 * i, st + off_sfb + 512 * i);
+          copy_scale_tile<1>(sfa + 4 * i, st + off_sfa + 512 * i);
+        }
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          if (kb * 8 + kk * 2 < p.blocks)
+            mma_mxf4<1>(tmem, smem_desc_sw128(st + kk * 32, 16, 1024),
+                        smem_desc_sw128(st + off_x + kk * 32, 16, 1024), kk & 1 ? id2 : id0,
+                        sfb + 4 * (kk >> 1), sfa + 4 * (kk >> 1), it > 0 || kk > 0 ? 1u : 0u);
+        }
+        mma_commit(empty_bar(s));
+      }
+      mma_commit(acc_bar);
+      volatile int never = 0;
+      if (!mbar_wait_bounded(acc_bar, 0, limit, &never)) atomicOr(p.status, kErrTimeoutDrain);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3;
+    grid_dependency_wait();  // C may be read or written by the kernel before this one
+    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_bar, 0, limit, &abort_flag));
+    if (!ok && lane == 0) give_up(kErrTimeoutEpilogue);
+    __syncwarp();
+    tc_fence_after();
+    const int n = n0 + q * 32 + lane;
+    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    float* red = reinterpret_cast<float*>(smem);  // [row of A][128]: the ring is idle by now
+    if (ok && kb0 < kb1) {
+      for (int j0 = 0; j0 < p.nt; j0 += 8) {
+        uint32_t r[8];
+        tmem_ld_8cols(taddr + j0, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (p.split > 1)
+            red[(j0 + j) * W_ROWS + q * 32 + lane] = __uint_as_float(r[j]);
+          else if (m0 + j0 + j < p.M && n < p.N)
+            store_c(p, static_cast<int64_t>(m0 + j0 + j) * p.ldc + n, __uint_as_float(r[j]));
+        }
+      }
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (p.split > 1) {
+    cluster_sync_all();
+    if (!abort_flag && warp >= 2) {
+      // Partial sums of the cluster, added in rank order: 4 columns a thread.
+      const int quads = min(p.nt, p.M - m0) * (W_ROWS / 4);
+      for (int g = rank * 128 + threadIdx.x - 64; g < quads; g += p.split * 128) {
+        const uint32_t addr = sbase + g * 16;
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int r = 0; r < p.split; ++r) {
+          float4 v;
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                       : "r"(mapa_shared(addr, r))
+                       : "memory");
+          sum.x += v.x;
+          sum.y += v.y;
+          sum.z += v.z;
+          sum.w += v.w;
+        }
+        const int m = m0 + g / (W_ROWS / 4), n = n0 + g % (W_ROWS / 4) * 4;
+        const int64_t at = static_cast<int64_t>(m) * p.ldc + n;
+        if (n < p.N) store_c(p, at, sum.x);
+        if (n + 1 < p.N) store_c(p, at + 1, sum.y);
+        if (n + 2 < p.N) store_c(p, at + 2, sum.z);
+        if (n + 3 < p.N) store_c(p, at + 3, sum.w);
+      }
+    }
+    cluster_sync_all();  // no CTA leaves while another reads its partial sums
+  }
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
+  NarrowParams p;
+  p.M = static_cast<int32_t>(a.M);
+  p.N = static_cast<int32_t>(a.N);
+  p.nt = a.M >= MAX_NT ? MAX_NT : static_cast<int32_t>((a.M + 7) / 8 * 8);
+  p.tiles_n = static_cast<int32_t>((a.N + W_ROWS - 1) / W_ROWS);
+  p.blocks = static_cast<int32_t>(blocks_of(a.K));
+  p.kt = static_cast<int32_t>(scale_tiles(a.K));
+  p.num_kb = (p.kt + 1) / 2;
+  p.stage_bytes = W_BYTES + p.nt * BK_BYTES + 2 * SF_BYTES;
+  p.stages = (SMEM_LIMIT - 1024 - 2048) / p.stage_bytes;
+  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  p.early_b = a.after_quantize;
+  p.sfa = a.sfa;
+  p.sfb = a.sfb;
+  p.C = a.C;
+  p.ldc = a.ldc;
+  p.c_dtype = a.c_dtype;
+  p.status = ctl.status;
+  p.wait_limit_ns = ctl.wait_limit_ns;
+  p.inject_stall = ctl.inject_stall;
+  const int64_t tiles = (a.M + p.nt - 1) / p.nt * p.tiles_n;
+  p.split = 1;
+  while (p.split < MAX_SPLIT && tiles * p.split * 2 <= ctl.sm_count && p.split * 2 <= p.num_kb)
+    p.split *= 2;
+  if (tiles * p.split > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const int64_t row_bytes = static_cast<int64_t>(p.blocks) * 16;
+  CUtensorMap tmA, tmB;
+  if (encode_tmap_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row_bytes, a.M, a.lda, BK_BYTES,
+                     p.nt, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tmap_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
+                     W_ROWS, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const int smem = p.stages * p.stage_bytes + 1024;
+  cudaError_t e = cudaFuncSetAttribute(
+      mxfp4_narrow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT - 2048);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.split;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  note_main_kernel("mxfp4_narrow_kernel", static_cast<int>(tiles * p.split),
+                   static_cast<int>(tiles));
+  e = cudaLaunchKernelEx(&cfg, mxfp4_narrow_kernel, tmA, tmB, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace mx
+}  // namespace mhr
