@@ -79,6 +79,27 @@ int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const uint8_t*
                          const uint8_t* Bt_scales, void* C, int64_t M, int64_t N, int64_t K,
                          int64_t lda, int64_t ldb, int64_t ldc, void* stream);
 
+/*
+ * A mixture-of-experts layer for a few tokens, in one kernel.  x: T x H bf16;
+ * router: E x H bf16; up: a packed 2 E I x H matrix, expert e's gate rows from
+ * row 2 e I and its up rows from row (2 e + 1) I; down: a packed E H x I
+ * matrix, expert e's rows from row e H; y: T x H bf16; experts, weights:
+ * T x top, contiguous.  For each token t:
+ *   logits = router x_t (fp32), experts = the top largest in descending order
+ *   (ties to the lowest index, a NaN counts as largest), weights = their
+ *   softmax (over the chosen ones: the full softmax renormalised);
+ *   y_t = sum over the chosen of weight * down_e (silu(gate_e x_t) * (up_e x_t)),
+ * rounded once to bf16; sums are fp32, the inner vector is rounded to 11
+ * significant bits.  Limits: T <= 64, top <= 16, E <= 512, H and I <= 16384.
+ * The call needs every SM at once (a cooperative launch): it waits for kernels
+ * before it on the device to leave.
+ */
+int gemm_mxfp4_moe(const uint16_t* x, int64_t ldx, const uint16_t* router, int64_t ldr,
+                   const uint8_t* up, const uint8_t* up_scales, int64_t ldu, const uint8_t* down,
+                   const uint8_t* down_scales, int64_t ldd, uint16_t* y, int64_t ldy,
+                   int32_t* experts, float* weights, int64_t T, int64_t E, int64_t top, int64_t H,
+                   int64_t I, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,8 +20,8 @@ Raw entry points (same names and arguments as the C ABI; pointers are ints,
 
 Tensor-level helper: ``matmul(a, b, path, out=None)`` for row-major CUDA
 tensors (the last dimension contiguous; the leading dimension is the row
-stride). 4-bit operands (``include/mhr_mxfp4.h``): ``quantize_mxfp4`` and
-``matmul_mxfp4``, in ``mxfp4.py``.
+stride). 4-bit operands (``include/mhr_mxfp4.h``): ``quantize_mxfp4``,
+``matmul_mxfp4`` and ``moe_mxfp4``, in ``mxfp4.py``.
 """
 from __future__ import annotations
 
@@ -53,7 +53,8 @@ EXPORTS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_bf16_f32acc", "gemm_f32_3xtf32_n
            "gemm_testing_plan_pair_tile_n", "gemm_testing_set_single_tile_n",
            "gemm_testing_plan_single_tile_n", "gemm_testing_set_simt_wide_mode",
            "gemm_testing_plan_simt_wide",
-           "gemm_mxfp4_scale_bytes", "gemm_mxfp4_quantize", "gemm_mxfp4", "gemm_mxfp4_quantized")
+           "gemm_mxfp4_scale_bytes", "gemm_mxfp4_quantize", "gemm_mxfp4", "gemm_mxfp4_quantized",
+           "gemm_mxfp4_moe")
 
 _lib = None
 
@@ -99,6 +100,9 @@ def load(path: str | None = None):
     lib.gemm_mxfp4.restype = ci
     lib.gemm_mxfp4_quantized.argtypes = [ci, vp, ci, vp, vp, vp, i64, i64, i64, i64, i64, i64, vp]
     lib.gemm_mxfp4_quantized.restype = ci
+    lib.gemm_mxfp4_moe.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp,
+                                   i64, i64, i64, i64, i64, vp]
+    lib.gemm_mxfp4_moe.restype = ci
     lib.gemm_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.gemm_testing_set_wait_limit_ns.restype = ctypes.c_uint64
     lib.gemm_testing_set_inject_stall.argtypes = [ctypes.c_int]
@@ -316,7 +320,8 @@ def gemm_testing_plan_simt_wide(M: int, N: int, K: int, sms: int) -> int:
 
 def __getattr__(name):
     # the 4-bit calls import torch, which the raw entry points do without
-    if name in ("MxFp4Matrix", "mxfp4_scale_bytes", "quantize_mxfp4", "matmul_mxfp4"):
+    if name in ("MxFp4Matrix", "mxfp4_scale_bytes", "quantize_mxfp4", "matmul_mxfp4",
+                "moe_mxfp4"):
         from . import mxfp4
 
         globals()[name] = getattr(mxfp4, name)

@@ -50,6 +50,7 @@ struct DeviceState {
 struct Workspace {
   void* ptr = nullptr;
   size_t bytes = 0;
+  void* control = nullptr;  // counters of the calls that need them (kControlBytes)
   cudaEvent_t last_use = nullptr;
   uint64_t stamp = 0;  // least recently used workspaces are freed first
 };
@@ -177,6 +178,7 @@ void free_workspace(int dev, Workspace& w) {
     cudaEventDestroy(w.last_use);
   }
   if (w.ptr) cudaFree(w.ptr);
+  if (w.control) cudaFree(w.control);
   cudaGetLastError();
   if (cur != dev) cudaSetDevice(cur);
   w = Workspace{};
@@ -320,6 +322,25 @@ int workspace_locked(int dev, cudaStream_t s, size_t bytes, void** out, void** t
 
 void workspace_done_locked(void* token, cudaStream_t s) {
   workspace_used(static_cast<Workspace*>(token), s);
+}
+
+int workspace_control_locked(void* token, cudaStream_t s, void** out) {
+  Workspace* w = static_cast<Workspace*>(token);
+  if (!w->control) {
+    void* p = nullptr;
+    if (cudaMalloc(&p, kControlBytes) != cudaSuccess) {
+      cudaGetLastError();
+      return MHR_ERR_CUDA;
+    }
+    if (cudaMemsetAsync(p, 0, kControlBytes, s) != cudaSuccess) {
+      cudaGetLastError();
+      cudaFree(p);
+      return MHR_ERR_CUDA;
+    }
+    w->control = p;
+  }
+  *out = w->control;
+  return MHR_OK;
 }
 
 bool byte_range(const void* p, int64_t rows, int64_t row_bytes, int64_t pitch_bytes,

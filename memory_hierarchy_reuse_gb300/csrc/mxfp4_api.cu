@@ -162,3 +162,49 @@ MHR_API int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const 
   workspace_done_locked(token, s);
   return from_cuda(e);
 }
+
+MHR_API int gemm_mxfp4_moe(const uint16_t* x, int64_t ldx, const uint16_t* router, int64_t ldr,
+                           const uint8_t* up, const uint8_t* up_scales, int64_t ldu,
+                           const uint8_t* down, const uint8_t* down_scales, int64_t ldd,
+                           uint16_t* y, int64_t ldy, int32_t* experts, float* weights, int64_t T,
+                           int64_t E, int64_t top, int64_t H, int64_t I, void* stream) {
+  static_assert(MOE_CONTROL_BYTES <= kControlBytes, "counters of the widest layer");
+  if (T < 0 || T > MOE_MAX_TOKENS || E < 1 || E > MOE_MAX_EXPERTS || top < 1 ||
+      top > MOE_MAX_TOP || top > E || H < 1 || H > MOE_MAX_WIDTH || I < 1 || I > MOE_MAX_WIDTH)
+    return MHR_ERR_INVALID_ARG;
+  if (T == 0) return MHR_OK;
+  ByteRange in[6], out[3];
+  if (!plain_ok(MHR_BF16, x, T, H, ldx, &in[0]) ||
+      !plain_ok(MHR_BF16, router, E, H, ldr, &in[1]) ||
+      !packed_ok(up, up_scales, 2 * E * I, H, ldu, &in[2], &in[3]) ||
+      !packed_ok(down, down_scales, E * H, I, ldd, &in[4], &in[5]) ||
+      !plain_ok(MHR_BF16, y, T, H, ldy, &out[0]) ||
+      !plain_ok(MHR_F32, experts, 1, T * top, T * top, &out[1]) ||
+      !plain_ok(MHR_F32, weights, 1, T * top, T * top, &out[2]))
+    return MHR_ERR_INVALID_ARG;
+  for (int i = 0; i < 3; ++i) {
+    for (const ByteRange& r : in)
+      if (ranges_overlap(out[i], r)) return MHR_ERR_INVALID_ARG;
+    if (ranges_overlap(out[i], out[(i + 1) % 3])) return MHR_ERR_INVALID_ARG;
+  }
+  begin_call();
+  std::lock_guard<std::mutex> lock(library_mutex());
+  DeviceCtl ctl;
+  int dev = 0;
+  if (const int st = device_ctl_locked(&ctl, &dev); st != MHR_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const MoeArgs a{x,    ldx,         router, ldr, up, up_scales, ldu, down,
+                  down_scales, ldd,  y,      ldy, experts, weights, T, E, top, H, I};
+  size_t at[5];
+  void *ws, *token, *control;
+  if (const int st = workspace_locked(dev, s, moe_workspace(a, at), &ws, &token); st != MHR_OK)
+    return st;
+  if (const int st = workspace_control_locked(token, s, &control); st != MHR_OK) return st;
+  cudaError_t e;
+  {
+    MainKernelEvents ev(s);
+    e = launch_moe(a, ws, static_cast<uint32_t*>(control), ctl, s);
+  }
+  workspace_done_locked(token, s);
+  return from_cuda(e);
+}

@@ -46,5 +46,31 @@ struct ProductArgs {
 // Few rows of A (any M is right).
 cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s);
 
+// One mixture-of-experts layer (gemm_mxfp4_moe).
+constexpr int MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 16, MOE_MAX_EXPERTS = 512;
+constexpr int64_t MOE_MAX_WIDTH = 16384;  // H and I
+// Counters that a call needs zeroed and leaves zeroed: a barrier, exits, and
+// one for every 16 rows of H.
+constexpr size_t MOE_CONTROL_BYTES = (2 + MOE_MAX_WIDTH / 16) * 4;
+struct MoeArgs {
+  const void* x;
+  int64_t ldx;
+  const void* router;
+  int64_t ldr;
+  const uint8_t *up, *up_scales;
+  int64_t ldu;
+  const uint8_t *down, *down_scales;
+  int64_t ldd;
+  void* y;
+  int64_t ldy;
+  int32_t* experts;
+  float* weights;
+  int64_t T, E, top, H, I;
+};
+// Bytes of workspace, and where its five parts start.
+size_t moe_workspace(const MoeArgs& a, size_t (&at)[5]);
+cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, const DeviceCtl& ctl,
+                       cudaStream_t s);
+
 }  // namespace mx
 }  // namespace mhr

@@ -2,6 +2,7 @@
 
     quantize_mxfp4(x, axis=1, values=False, stream=None) -> MxFp4Matrix [, values]
     matmul_mxfp4(a, b, out=None, out_dtype=torch.float32, stream=None) -> C
+    moe_mxfp4(x, router, up, down, top, out=None, stream=None) -> y, experts, weights
 
 As in ``matmul``: argument checks and marshalling only, row-major CUDA tensors
 (the last dimension contiguous), launches on ``stream`` (default: the current
@@ -133,3 +134,37 @@ def matmul_mxfp4(a, b, out=None, out_dtype=torch.float32, stream=None):
              a.data_ptr(), c, b.data.data_ptr(), b.scales.data_ptr(), out.data_ptr(),
              M, N, K, lda, ldb, ldc)
     return out
+
+
+def moe_mxfp4(x, router, up, down, top: int, out=None, stream=None):
+    """A mixture-of-experts layer over 4-bit experts for up to 64 tokens, in one kernel.
+
+    ``x``: T x H bfloat16; ``router``: E x H bfloat16; ``up``: the packed 2 E I x H matrix of
+    the experts' gate and up weights (expert e: I gate rows, then I up rows); ``down``: the
+    packed E H x I matrix (expert e: H rows). Returns ``y`` (T x H bfloat16), the chosen
+    experts (T x top int32, best first, ties to the lowest index) and their weights (T x top
+    float32, a softmax over the chosen): y_t = sum of weight * down_e (silu(gate_e x_t) *
+    (up_e x_t)).
+    """
+    if x.dtype != torch.bfloat16 or router.dtype != torch.bfloat16:
+        raise TypeError("x and router must be bfloat16")
+    ldx, ldr = _rowmajor(x, "x"), _rowmajor(router, "router")
+    (T, H), E, I = x.shape, router.shape[0], down.cols
+    if router.shape[1] != H or up.cols != H or up.rows != 2 * E * I or down.rows != E * H:
+        raise ValueError("sizes differ: x is T x H, router E x H, up 2 E I x H, down E H x I")
+    ldu, ldd = _check_packed(up, "up"), _check_packed(down, "down")
+    device = x.device
+    if out is None:
+        out = torch.empty((T, H), dtype=torch.bfloat16, device=device)
+    if out.dtype != torch.bfloat16 or out.shape != x.shape:
+        raise TypeError("out must be bfloat16 of x's shape")
+    ldy = _rowmajor(out, "out")
+    _same_device(device, router=router, up=up.data, up_scales=up.scales, down=down.data,
+                 down_scales=down.scales, out=out)
+    experts = torch.empty((T, top), dtype=torch.int32, device=device)
+    weights = torch.empty((T, top), dtype=torch.float32, device=device)
+    _run("gemm_mxfp4_moe", device, stream, load().gemm_mxfp4_moe, x.data_ptr(), ldx,
+         router.data_ptr(), ldr, up.data.data_ptr(), up.scales.data_ptr(), ldu,
+         down.data.data_ptr(), down.scales.data_ptr(), ldd, out.data_ptr(), ldy,
+         experts.data_ptr(), weights.data_ptr(), T, E, top, H, I)
+    return out, experts, weights

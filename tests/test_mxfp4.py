@@ -64,6 +64,39 @@ def test_product_refusals(lib):
         assert lib.gemm_mxfp4_quantized(*args, None) == 1, change
 
 
+def test_moe_refusals(lib):
+    # x, ldx, router, ldr, up, up_s, ldu, down, down_s, ldd, y, ldy, experts, weights, T, E, top, H, I
+    a = [0x10000000 * i for i in range(1, 10)]
+    good = [a[0], 64, a[1], 64, a[2], a[3], 32, a[4], a[5], 16, a[6], 64, a[7], a[8], 2, 4, 2, 64, 32]
+    bad = [{0: None}, {0: a[0] + 1}, {1: 63}, {2: None}, {3: 63}, {4: None}, {4: a[2] + 8}, {5: None},
+           {6: 16}, {6: 40}, {7: None}, {8: a[5] + 4}, {9: 8}, {10: None}, {11: 63}, {12: None},
+           {12: a[7] + 2}, {13: None}, {14: -1}, {14: 65}, {15: 0}, {15: 513}, {16: 0}, {16: 5},
+           {15: 32, 16: 17}, {17: 0}, {17: 16385}, {18: 0}, {18: 16385}, {10: a[0]}, {10: a[2]},
+           {12: a[8]}, {13: a[6]}, {12: a[4]}]
+    for change in bad:
+        args = [change.get(i, v) for i, v in enumerate(good)]
+        assert lib.gemm_mxfp4_moe(*args, None) == 1, change
+    assert lib.gemm_mxfp4_moe(*[{14: 0}.get(i, v) for i, v in enumerate(good)], None) == 0
+
+
+def test_moe_tensor_level_refusals():
+    import torch
+
+    import memory_hierarchy_reuse_gb300 as m
+
+    byte = lambda *n: torch.zeros(n, dtype=torch.uint8)  # noqa: E731
+    x, router = torch.zeros(2, 64).bfloat16(), torch.zeros(4, 64).bfloat16()
+    up, down = m.MxFp4Matrix(byte(256, 32), byte(1024), 256, 64), m.MxFp4Matrix(byte(256, 16), byte(1024), 256, 32)
+    for args, kw in [((x.float(), router, up, down, 2), {}), ((x, router.float(), up, down, 2), {}),
+                     ((x[:, :32], router, up, down, 2), {}), ((x, router[:3], up, down, 2), {}),
+                     ((x, router, up._replace(cols=32), down, 2), {}),
+                     ((x, router, up, down._replace(cols=16), 2), {}),
+                     ((x, router, up, down, 2), {"out": torch.zeros(2, 64)}),
+                     ((x, router, up, down, 2), {})]:
+        with pytest.raises((TypeError, ValueError)):
+            m.moe_mxfp4(*args, **kw)
+
+
 def test_tensor_level_refusals():
     import torch
 
