@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmhr_gemm.so")
 SOURCES = ["api.cu", "simt_f32.cu", "tc_gemm.cu", "tc_gemm_1cta.cu", "tc_gemm_pair.cu",
            "tc_prepass.cu", "noalloc.cu", "ladder.cu", "mxfp4_api.cu", "mxfp4_quantize.cu",
-           "mxfp4_narrow.cu", "mxfp4_moe.cu"]
+           "mxfp4_narrow.cu", "mxfp4_pair.cu", "mxfp4_moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

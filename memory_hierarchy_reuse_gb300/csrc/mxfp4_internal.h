@@ -45,6 +45,8 @@ struct ProductArgs {
 };
 // Few rows of A (any M is right).
 cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s);
+// Many rows of A: CTA pairs on 256 x 256 tiles (any M is right).
+cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s);
 
 // One mixture-of-experts layer (gemm_mxfp4_moe).
 constexpr int MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 16, MOE_MAX_EXPERTS = 512;

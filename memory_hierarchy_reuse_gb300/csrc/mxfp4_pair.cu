@@ -1,0 +1,449 @@
+// The 4-bit product for many rows: persistent CTA pairs (tcgen05 cta_group::2)
+// on 256 x 256 tiles of C, K in stages of 256 columns.
+//
+// Bound by the tensor pipe, and next to it by shared memory: a 256 x 256 x 64
+// MMA takes 128 cycles, in which an SM reads 128 rows of A and of B (32 bytes
+// each, 8 KB) and TMA writes as much for the stages ahead: 128 bytes a cycle,
+// all that shared memory moves.  So both operands are staged once a pair (each
+// CTA holds its 128 rows of A and half of B), and nothing else but the scales
+// (1/16 of the operands, through tcgen05.cp) touches shared memory in the main
+// loop.
+//
+// TMEM: two accumulators of 256 columns and two sets of scales (24 columns
+// each: A's 128 rows and B's 256 rows x 8 blocks) would take 560 of the 512
+// columns.  The accumulators overlap by 48: the epilogue drains the columns
+// that the other one needs first, and the next tile's MMAs start while it
+// drains the rest.
+#include "mhr_gemm.h"
+#include "mhr_mxfp4.h"
+#include "mxfp4_common.cuh"
+
+namespace mhr {
+namespace mx {
+namespace {
+
+constexpr int TILE = 256;                    // rows and columns of a pair's tile
+constexpr int HALF = 128;
+constexpr int BK_BYTES = 128;                // 256 columns of K a stage: one swizzle row
+constexpr int OP_BYTES = HALF * BK_BYTES;    // this CTA's A rows, and its half of B
+constexpr int OFF_B = OP_BYTES;
+constexpr int OFF_SFA = 2 * OP_BYTES;        // 2 scale tiles: 128 rows x 8 blocks
+constexpr int OFF_SFB = OFF_SFA + 1024;      // 2 x 2: all 256 columns of C
+constexpr int STAGE_BYTES = OFF_SFB + 2048;  // 35 KB
+constexpr int STAGES = 5;
+constexpr int EPI_WARPS = 4;
+constexpr int EPI_BUF = 32 * 128;            // 32 rows of 128 bytes
+constexpr int EPI_OFF = STAGES * STAGE_BYTES;
+constexpr int SMEM = EPI_OFF + EPI_WARPS * 2 * EPI_BUF + 1024;
+constexpr int THREADS = 192;
+constexpr uint32_t ACC1 = 208;               // the second accumulator's first column
+constexpr uint32_t SF_COL = 464;             // scales: 2 x 24 columns
+constexpr uint32_t TMEM_COLS = 512;
+constexpr int GROUP_M = 8;                   // tile rows a raster group, as in the bf16 kernel
+
+struct PairParams {
+  int32_t M, N;
+  int32_t tiles_m, tiles_n, num_tiles, num_kb;
+  int32_t blocks;
+  void* C;
+  int64_t ldc;
+  int32_t c_dtype;
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  int32_t inject_stall;
+};
+
+__device__ __forceinline__ void tile_at(int t, const PairParams& p, int& tm, int& tn) {
+  const int group_size = GROUP_M * p.tiles_n;
+  const int g = t / group_size, first = g * GROUP_M;
+  const int gm = min(p.tiles_m - first, GROUP_M), r = t - g * group_size;
+  tm = first + r % gm;
+  tn = r / gm;
+}
+
+__device__ __forceinline__ uint32_t pack16(int c_dtype, uint32_t lo, uint32_t hi) {
+  const float a = __uint_as_float(lo), b = __uint_as_float(hi);
+  if (c_dtype == MHR_BF16) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// Warp roles, barriers and the way a timeout unwinds are those of the bf16
+// and tf32 pair kernel (tc_gemm_pair.cu): warp 0 producer, warp 1 MMA issuer
+// (rank 0), warps 2-5 epilogue; full[s] and released[b] in rank 0, empty[s]
+// and acc_full[b] in both CTAs.  released[b]: the columns of accumulator b
+// that the other one overlaps have been read by all 8 epilogue warps.
+// WIDE: C is fp32, else 16 bits.  TMA_STORE: C goes out by TMA.
+template <bool WIDE, bool TMA_STORE>
+__global__ void __launch_bounds__(THREADS, 1)
+    mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
+                      const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmSA,
+                      const __grid_constant__ CUtensorMap tmSB,
+                      const __grid_constant__ CUtensorMap tmC, const PairParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(8) uint64_t bars[2 * STAGES + 6];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ volatile uint32_t peer_loaded;  // rank 0: stages that rank 1 loaded
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
+  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
+  auto acc_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
+  auto released_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
+  const uint32_t peer_done_bar = bar0 + 8u * (2 * STAGES + 5);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const bool leader = rank == 0;
+  const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&abort_flag)), rank ^ 1u);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_bar(b), 1);
+      mbar_init(released_bar(b), 2 * EPI_WARPS);
+    }
+    mbar_init(drain_bar, 1);
+    mbar_init(peer_done_bar, 1);
+    abort_flag = 0;
+    peer_loaded = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmSA);
+    tma_prefetch_desc(&tmSB);
+    if (TMA_STORE) tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&tmem_slot), TMEM_COLS);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint64_t limit = p.wait_limit_ns;
+  grid_dependency_wait();
+
+  auto give_up = [&](uint32_t bit) {  // by one thread: both CTAs unwind
+    if (!abort_flag) atomicOr(p.status, bit);
+    abort_flag = 1;
+    st_shared_cluster_u32(peer_abort, 1u);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t it = 0;
+      const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
+      bool ok = true;
+      for (int u = cluster; ok && u < p.num_tiles; u += clusters) {
+        int tm, tn;
+        tile_at(u, p, tm, tn);
+        const int m0 = tm * TILE + static_cast<int>(rank) * HALF;
+        const int n0 = tn * TILE, nb0 = n0 + static_cast<int>(rank) * HALF;
+        for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
+          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+          if (!mbar_wait_bounded(empty_bar(s), ph ^ 1u, limit, &abort_flag)) {
+            give_up(kErrTimeoutProducer);
+            ok = false;
+            break;
+          }
+          const uint32_t st = sbase + s * STAGE_BYTES;
+          const uint32_t fb = mapa_shared(full_bar(s), 0);
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * STAGE_BYTES);
+          if (stall && it == 0) continue;
+          tma_load_2d_pair(st, &tmA, fb, kb * BK_BYTES, m0);
+          tma_load_2d_pair(st + OFF_B, &tmB, fb, kb * BK_BYTES, nb0);
+          // (boxes past the last row or block are filled with zeros)
+          tma_load_3d_pair(st + OFF_SFA, &tmSA, fb, 0, 2 * kb, m0 / 128);
+          tma_load_3d_pair(st + OFF_SFB, &tmSB, fb, 0, 2 * kb, n0 / 128);
+        }
+      }
+      // Both CTAs' loads complete in rank 0, which waits for all of them --
+      // counting as done what either side never issued -- before either CTA
+      // may leave.
+      volatile int never = 0;
+      if (!leader) {
+        st_shared_cluster_u32(
+            mapa_shared(smem_u32(const_cast<uint32_t*>(&peer_loaded)), 0), it);
+        mbar_arrive_cluster(mapa_shared(peer_done_bar, 0));
+      } else {
+        uint32_t it1 = it;
+        if (mbar_wait_bounded<true>(peer_done_bar, 0, 2 * limit, &never))
+          it1 = peer_loaded;
+        else
+          atomicOr(p.status, kErrTimeoutDrain);
+        const uint32_t hi = it > it1 ? it : it1;
+        for (uint32_t i = hi > STAGES ? hi - STAGES : 0; i < hi; ++i) {
+          const uint32_t s = i % STAGES, ph = (i / STAGES) & 1u;
+          const bool armed = i < it, loaded0 = armed && !(stall && i == 0), loaded1 = i < it1;
+          if (!armed) {
+            mbar_arrive_expect_tx(full_bar(s), STAGE_BYTES);
+          } else {
+            const uint32_t missing = (loaded0 ? 0u : STAGE_BYTES) + (loaded1 ? 0u : STAGE_BYTES);
+            if (missing) {  // once the MMA issuer has given up on the stage
+              mbar_wait_bounded(full_bar(s), ph, 2 * limit, &abort_flag);
+              mbar_complete_tx(full_bar(s), missing);
+            }
+          }
+          if (!mbar_wait_bounded(full_bar(s), ph, limit, &never))
+            atomicOr(p.status, kErrTimeoutDrain);
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (leader && lane == 0) {
+      const uint32_t id0 = make_idesc_mxf4(TILE, TILE, 0), id2 = make_idesc_mxf4(TILE, TILE, 2);
+      uint32_t it = 0, t = 0;
+      bool ok = true;
+      for (int u = cluster; ok && u < p.num_tiles; u += clusters, ++t) {
+        // the other accumulator's overlapping columns have been read (and with
+        // them, by the same warps earlier, all of this one's last tile)
+        if (t > 0 && !mbar_wait_bounded(released_bar((t - 1) & 1u), ((t - 1) >> 1) & 1u, limit,
+                                        &abort_flag)) {
+          give_up(kErrTimeoutMma);
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem + (t & 1u ? ACC1 : 0);
+        for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
+          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
+          // scales alternate between two sets of columns: the MMAs two stages
+          // back, the last to read this set, have finished
+          if ((it >= 2 && !mbar_wait_bounded(empty_bar((it - 2) % STAGES),
+                                             ((it - 2) / STAGES) & 1u, limit, &abort_flag)) ||
+              !mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag)) {
+            give_up(kErrTimeoutMma);
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = sbase + s * STAGE_BYTES;
+          const uint32_t sfa = tmem + SF_COL + (it & 1u) * 24, sfb = sfa + 8;
+          // columns: A's tile 0, tile 1; B's tile 0 of both 128-row parts, then tile 1 of both
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            copy_scale_tile<2>(sfa + 4 * i, st + OFF_SFA + 512 * i);
+            copy_scale_tile<2>(sfb + 8 * i, st + OFF_SFB + 512 * i);
+            copy_scale_tile<2>(sfb + 8 * i + 4, st + OFF_SFB + 1024 + 512 * i);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            if (kb * 8 + kk * 2 < p.blocks)
+              mma_mxf4<2>(d, smem_desc_sw128(st + kk * 32, 16, 1024),
+                          smem_desc_sw128(st + OFF_B + kk * 32, 16, 1024), kk & 1 ? id2 : id0,
+                          sfa + 4 * (kk >> 1), sfb + 8 * (kk >> 1), kb > 0 || kk > 0 ? 1u : 0u);
+          mma_commit_pair_multicast(empty_bar(s), 0x3);
+        }
+        if (!ok) break;
+        mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
+      }
+      mma_commit_pair(drain_bar);
+      volatile int never = 0;
+      if (!mbar_wait_bounded(drain_bar, 0, limit, &never)) atomicOr(p.status, kErrTimeoutDrain);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, ew = warp - 2;
+    constexpr int PIECES = WIDE ? 8 : 4;       // of 32 fp32 or 64 16-bit columns: 128 bytes a row
+    constexpr int COLS = WIDE ? 32 : 64;
+    constexpr int FIRST = WIDE ? 2 : 1;        // pieces that hold the overlapping columns
+    uint32_t t = 0, chunk = 0;
+    for (int u = cluster; u < p.num_tiles; u += clusters, ++t) {
+      const uint32_t b = t & 1u;
+      if (!__all_sync(0xffffffffu,
+                      mbar_wait_bounded(acc_bar(b), (t >> 1) & 1u, limit, &abort_flag, 128))) {
+        if (lane == 0) give_up(kErrTimeoutEpilogue);
+        __syncwarp();
+        break;
+      }
+      tc_fence_after();
+      int tm, tn;
+      tile_at(u, p, tm, tn);
+      const int row0 = tm * TILE + static_cast<int>(rank) * HALF + q * 32, n0 = tn * TILE;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (b ? ACC1 : 0);
+#pragma unroll 1
+      for (int i = 0; i < PIECES; ++i) {
+        // the first accumulator's shared columns are its last, the second's its first
+        const int c = b ? i : (i < FIRST ? PIECES - FIRST + i : i - FIRST);
+        uint32_t r[32];
+        tmem_ld_32cols(taddr + c * COLS, r);
+        if constexpr (!WIDE) {
+          uint32_t r2[32];
+          tmem_ld_32cols(taddr + c * COLS + 32, r2);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = pack16(p.c_dtype, r[2 * j], r[2 * j + 1]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[16 + j] = pack16(p.c_dtype, r2[2 * j], r2[2 * j + 1]);
+        } else {
+          tmem_ld_wait();
+        }
+        if (i == FIRST - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(released_bar(b), 0));
+        }
+        // One row a lane into a 128-byte swizzled box (conflict-free), then
+        // out by TMA, or a row at a time where C is not aligned for it.
+        const uint32_t stg = sbase + EPI_OFF + (ew * 2 + (chunk & 1u)) * EPI_BUF;
+        ++chunk;
+        if (TMA_STORE) {
+          if (lane == 0) bulk_wait_group_read<1>();
+        }
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t at = stg + lane * 128 + ((j ^ (lane & 7)) << 4);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(r[4 * j]),
+                       "r"(r[4 * j + 1]), "r"(r[4 * j + 2]), "r"(r[4 * j + 3])
+                       : "memory");
+        }
+        const int col0 = n0 + c * COLS;
+        if constexpr (TMA_STORE) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmC, stg, col0, row0);
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
+          const int rows = min(32, p.M - row0);
+          for (int rr = 0; rr < rows; ++rr) {
+            uint32_t v;
+            asm volatile("ld.shared.b32 %0, [%1];"
+                         : "=r"(v)
+                         : "r"(stg + rr * 128 + (((lane >> 2) ^ (rr & 7)) << 4) + (lane & 3) * 4)
+                         : "memory");
+            const int64_t row = static_cast<int64_t>(row0 + rr) * p.ldc;
+            if constexpr (WIDE) {
+              if (col0 + lane < p.N) static_cast<uint32_t*>(p.C)[row + col0 + lane] = v;
+            } else {
+              uint16_t* dst = static_cast<uint16_t*>(p.C) + row + col0 + 2 * lane;
+              const int left = p.N - (col0 + 2 * lane);
+              if (left >= 2 && (reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
+                *reinterpret_cast<uint32_t*>(dst) = v;
+              } else {
+                if (left >= 1) dst[0] = static_cast<uint16_t>(v);
+                if (left >= 2) dst[1] = static_cast<uint16_t>(v >> 16);
+              }
+            }
+          }
+          __syncwarp();
+        }
+      }
+    }
+    if (TMA_STORE) {
+      if (lane == 0) bulk_wait_group<0>();
+      __syncwarp();
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc_pair(tmem, TMEM_COLS);
+  }
+}
+
+template <bool WIDE, bool TMA_STORE>
+cudaError_t launch_t(const CUtensorMap (&m)[5], const PairParams& p, const DeviceCtl& ctl,
+                     cudaStream_t s) {
+  auto kern = mxfp4_pair_kernel<WIDE, TMA_STORE>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  cfg.gridDim = dim3(2 * (ctl.sm_count / 2));
+  int max_clusters = 0;
+  if ((e = cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg)) != cudaSuccess) return e;
+  if (max_clusters < 1) return cudaErrorInvalidConfiguration;
+  const int clusters = p.num_tiles < max_clusters ? p.num_tiles : max_clusters;
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.numAttrs = 2;
+  note_main_kernel("mxfp4_pair_kernel", 2 * clusters, p.num_tiles);
+  e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Scales as 512-byte tiles: tile_rows x kt of them, boxes of 2 x `rows`.
+bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t kt, uint32_t box) {
+  const uint64_t dims[3] = {128, static_cast<uint64_t>(kt), static_cast<uint64_t>((rows + 127) / 128)};
+  const uint64_t pitch[2] = {512, static_cast<uint64_t>(kt) * 512};
+  const uint32_t boxes[3] = {128, 2, box};
+  return encode_tmap_3d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, scales, dims, pitch, boxes) ==
+         CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
+  PairParams p;
+  p.M = static_cast<int32_t>(a.M);
+  p.N = static_cast<int32_t>(a.N);
+  p.tiles_m = static_cast<int32_t>((a.M + TILE - 1) / TILE);
+  p.tiles_n = static_cast<int32_t>((a.N + TILE - 1) / TILE);
+  const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
+  if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
+  p.num_tiles = static_cast<int32_t>(tiles);
+  p.blocks = static_cast<int32_t>(blocks_of(a.K));
+  const int64_t kt = scale_tiles(a.K);
+  p.num_kb = static_cast<int32_t>((kt + 1) / 2);
+  p.C = a.C;
+  p.ldc = a.ldc;
+  p.c_dtype = a.c_dtype;
+  p.status = ctl.status;
+  p.wait_limit_ns = ctl.wait_limit_ns;
+  p.inject_stall = ctl.inject_stall;
+  const bool wide = a.c_dtype == MHR_F32;
+  const int64_t size = wide ? 4 : 2;
+  // TMA stores clip a box at C's inner extent in 16-byte units only
+  const bool c_tma = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * size % 16 == 0 &&
+                     a.N * size % 16 == 0;
+  const int64_t row_bytes = static_cast<int64_t>(p.blocks) * 16;
+  CUtensorMap m[5];
+  if (encode_tmap_2d(&m[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row_bytes, a.M, a.lda, BK_BYTES,
+                     HALF, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tmap_2d(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
+                     HALF, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      !scale_map(&m[2], a.sfa, a.M, kt, 1) || !scale_map(&m[3], a.sfb, a.N, kt, 2))
+    return cudaErrorInvalidValue;
+  m[4] = m[0];
+  if (c_tma && encode_tmap_2d(&m[4],
+                              wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              a.C, a.N, a.M, a.ldc * size, 128 / size, 32,
+                              CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  if (wide)
+    return c_tma ? launch_t<true, true>(m, p, ctl, s) : launch_t<true, false>(m, p, ctl, s);
+  return c_tma ? launch_t<false, true>(m, p, ctl, s) : launch_t<false, false>(m, p, ctl, s);
+}
+
+}  // namespace mx
+}  // namespace mhr

@@ -130,21 +130,35 @@ PRODUCTS = [(1, 1, 1), (1, 128, 64), (1, 4096, 4096), (2, 130, 32), (7, 257, 96)
             (512, 768, 1056), (1000, 1111, 640)]
 
 
+@pytest.fixture(params=[0, 1, 2], ids=["auto", "narrow", "pair"])
+def kernel(mhr, request):
+    """The product's kernel: the library's choice, and each of them for every shape."""
+    old = mhr.gemm_testing_set_cta_pair_mode(request.param)
+    yield request.param
+    mhr.gemm_testing_set_cta_pair_mode(old)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
 @pytest.mark.parametrize("M,N,K", PRODUCTS)
-def test_product(mhr, M, N, K, dtype):
+def test_product(mhr, kernel, M, N, K, dtype):
     product_case(mhr, M, N, K, dtype, seed=M + N + K)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_product_of_many_tiles(mhr, kernel, dtype):
+    """More tiles than run at once: accumulators alternate, ragged last ones."""
+    product_case(mhr, 2600, 3300, 300, dtype)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(5, 200, 300), (140, 200, 300), (300, 260, 520)])
-def test_product_strides_and_offsets(mhr, M, N, K, dtype):
+def test_product_strides_and_offsets(mhr, kernel, M, N, K, dtype):
     product_case(mhr, M, N, K, dtype, ldc=N + 3, offset=1)
     product_case(mhr, M, N, K, dtype, ldc=N + 8, offset=8, lda=-(-K // 32) * 16 + 48)
 
 
 @pytest.mark.parametrize("M", [3, 200, 520])
-def test_product_repeats_bit_for_bit(mhr, M):
+def test_product_repeats_bit_for_bit(mhr, kernel, M):
     import torch
 
     first = product_case(mhr, M, 384, 4096, "f32").clone()
@@ -152,7 +166,7 @@ def test_product_repeats_bit_for_bit(mhr, M):
         assert torch.equal(product_case(mhr, M, 384, 4096, "f32"), first)
 
 
-def test_product_integers_are_exact(mhr):
+def test_product_integers_are_exact(mhr, kernel):
     """Codes of whole values and scales of 1: every sum is a whole number below 2^24."""
     import torch
 
@@ -167,7 +181,7 @@ def test_product_integers_are_exact(mhr):
         assert np.array_equal(mhr.matmul_mxfp4(A, B).double().cpu().numpy(), want)
 
 
-def test_product_scales_reach_every_block(mhr):
+def test_product_scales_reach_every_block(mhr, kernel):
     """One nonzero block per row, each with a scale of its own."""
     import torch
 
@@ -202,7 +216,7 @@ def test_product_quantized_on_the_way(mhr, M, N, K, dtype):
     assert torch.equal(got, want) and bool(torch.isfinite(got).all())
 
 
-def test_product_nan_scale_reaches_its_rows_only(mhr):
+def test_product_nan_scale_reaches_its_rows_only(mhr, kernel):
     import torch
 
     for M in (40, 300):
@@ -260,7 +274,7 @@ def test_streams(mhr):
     assert all(torch.equal(g, w) for g, w in zip(got, want))
 
 
-def test_timeout_is_reported_and_cleared(mhr):
+def test_timeout_is_reported_and_cleared(mhr, kernel):
     """A first ring stage that is never filled: the call ends, the status says so, and the next
     call is right."""
     import torch
