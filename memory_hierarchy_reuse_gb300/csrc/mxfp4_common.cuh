@@ -115,27 +115,53 @@ __host__ __device__ constexpr uint32_t make_idesc_mxf4(uint32_t m, uint32_t n, u
          ((m >> 7) << 27) | (sf_id << 29);
 }
 
+// The issuing warp runs its loop converged, so that addresses and descriptors
+// stay in uniform registers, and one elected lane issues: with the loop inside
+// an `if (lane == 0)`, each MMA cost some 114 cycles to issue (GB300), nearly
+// the 128 that it takes.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+
+// Low word of a shared-memory descriptor: the address in 16-byte units and,
+// for operands, the K-major leading offset (unused by swizzled layouts, 1).
+__device__ __forceinline__ uint32_t desc_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFFu) >> 4) | (1u << 16);
+}
+// High words: 128-byte swizzle with 1024 bytes between groups of 8 rows
+// (operands); no swizzle with 128 bytes between them (scale tiles).
+constexpr uint32_t DESC_HI_SW128 = (1024u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t DESC_HI_SCALES = (128u >> 4) | (1u << 14);
+
 // D (+)= (A * scales) (B * scales) over 64 columns of K: two blocks of 32 a
 // row, the scales in TMEM.
 template <int GROUP>
-__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                          uint32_t idesc, uint32_t sfa_tmem, uint32_t sfb_tmem,
                                          uint32_t accumulate) {
   if constexpr (GROUP == 1)
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        " [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate),
+        "r"(DESC_HI_SW128)
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
         "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
-        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate)
+        " [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(sfa_tmem), "r"(sfb_tmem), "r"(accumulate),
+        "r"(DESC_HI_SW128)
         : "memory");
 }
 
@@ -145,15 +171,19 @@ __device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint6
 // (128 bytes) a group.  GROUP 2 copies in both CTAs, each from its own shared
 // memory at the same offset.
 template <int GROUP>
-__device__ __forceinline__ void copy_scale_tile(uint32_t d_tmem, uint32_t saddr) {
-  const uint64_t desc = static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) |
-                        (static_cast<uint64_t>(128 >> 4) << 32) | (1ull << 46);
+__device__ __forceinline__ void copy_scale_tile(uint32_t d_tmem, uint32_t s_lo) {
   if constexpr (GROUP == 1)
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(d_tmem), "l"(desc)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], s;\n\t}" ::"r"(d_tmem),
+        "r"(s_lo), "r"(DESC_HI_SCALES)
+        : "memory");
   else
-    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(d_tmem), "l"(desc)
-                 : "memory");
+    asm volatile(
+        "{\n\t.reg .b64 s;\n\tmov.b64 s, {%1, %2};\n\t"
+        "tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], s;\n\t}" ::"r"(d_tmem),
+        "r"(s_lo), "r"(DESC_HI_SCALES)
+        : "memory");
 }
 
 // Untiled bulk copy: both addresses and the size multiples of 16 bytes.

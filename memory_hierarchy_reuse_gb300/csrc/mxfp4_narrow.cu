@@ -154,42 +154,48 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t id0 = make_idesc_mxf4(W_ROWS, p.nt, 0), id2 = make_idesc_mxf4(W_ROWS, p.nt, 2);
-      for (int it = 0; kb0 + it < kb1; ++it) {
-        const uint32_t s = it % p.stages, ph = (it / p.stages) & 1u;
-        // scales alternate between two sets of TMEM columns: the MMAs two
-        // stages back, which read this set last, have finished
-        const bool ok =
-            (it < 2 || mbar_wait_bounded(empty_bar((it - 2) % p.stages),
-                                         ((it - 2) / p.stages) & 1u, limit, &abort_flag)) &&
-            mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag);
-        if (!ok) {
-          give_up(kErrTimeoutMma);
-          break;
+    const uint32_t id0 = make_idesc_mxf4(W_ROWS, p.nt, 0), id2 = make_idesc_mxf4(W_ROWS, p.nt, 2);
+    uint32_t s = 0, ph = 0, s2 = p.stages - 2, ph2 = 1;  // ring position; two stages back
+    for (int it = 0; kb0 + it < kb1; ++it) {
+      // scales alternate between two sets of TMEM columns: the MMAs two
+      // stages back, which read this set last, have finished
+      const bool ok = (it < 2 || mbar_wait_bounded(empty_bar(s2), ph2, limit, &abort_flag)) &&
+                      mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag);
+      if (!__all_sync(0xffffffffu, ok)) {
+        if (lane == 0) give_up(kErrTimeoutMma);
+        break;
+      }
+      tc_fence_after();
+      const int kb = kb0 + it;
+      const uint32_t w = desc_lo(sbase + s * p.stage_bytes), x = w + (off_x >> 4);
+      const uint32_t cb = w + (off_sfb >> 4), ca = w + (off_sfa >> 4);
+      const uint32_t sfb = tmem + MAX_NT + (it & 1) * 16, sfa = sfb + 8;
+      const int tiles = min(2, p.kt - 2 * kb), mmas = min(4, (p.blocks - kb * 8 + 1) / 2);
+      if (elect_one()) {
+        for (int i = 0; i < tiles; ++i) {
+          copy_scale_tile<1>(sfb + 4 * i, cb + 32 * i);
+          copy_scale_tile<1>(sfa + 4 * i, ca + 32 * i);
         }
-        tc_fence_after();
-        const uint32_t st = sbase + s * p.stage_bytes;
-        const int kb = kb0 + it;
-        const uint32_t sfb = tmem + MAX_NT + (it & 1) * 16, sfa = sfb + 8;
-        for (int i = 0; i < min(2, p.kt - 2 * kb); ++i) {
-          copy_scale_tile<1>(sfb + 4 * i, st + off_sfb + 512 * i);
-          copy_scale_tile<1>(sfa + 4 * i, st + off_sfa + 512 * i);
-        }
-#pragma unroll
-        for (int kk = 0; kk < 4; ++kk) {
-          if (kb * 8 + kk * 2 < p.blocks)
-            mma_mxf4<1>(tmem, smem_desc_sw128(st + kk * 32, 16, 1024),
-                        smem_desc_sw128(st + off_x + kk * 32, 16, 1024), kk & 1 ? id2 : id0,
-                        sfb + 4 * (kk >> 1), sfa + 4 * (kk >> 1), it > 0 || kk > 0 ? 1u : 0u);
-        }
+        for (int kk = 0; kk < mmas; ++kk)
+          mma_mxf4<1>(tmem, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfb + 4 * (kk >> 1),
+                      sfa + 4 * (kk >> 1), it > 0 || kk > 0 ? 1u : 0u);
         mma_commit(empty_bar(s));
       }
-      mma_commit(acc_bar);
-      volatile int never = 0;
-      if (!mbar_wait_bounded(acc_bar, 0, limit, &never)) atomicOr(p.status, kErrTimeoutDrain);
+      __syncwarp();
+      if (++s == static_cast<uint32_t>(p.stages)) {
+        s = 0;
+        ph ^= 1u;
+      }
+      if (++s2 == static_cast<uint32_t>(p.stages)) {
+        s2 = 0;
+        ph2 ^= 1u;
+      }
     }
+    if (elect_one()) mma_commit(acc_bar);
     __syncwarp();
+    volatile int never = 0;
+    if (!mbar_wait_bounded(acc_bar, 0, limit, &never) && lane == 0)
+      atomicOr(p.status, kErrTimeoutDrain);
   } else {
     const int q = warp & 3;
     grid_dependency_wait();  // C may be read or written by the kernel before this one

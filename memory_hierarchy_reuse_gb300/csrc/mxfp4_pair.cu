@@ -203,55 +203,77 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else if (warp == 1) {
-    if (leader && lane == 0) {
+    if (leader) {
       const uint32_t id0 = make_idesc_mxf4(TILE, TILE, 0), id2 = make_idesc_mxf4(TILE, TILE, 2);
-      uint32_t it = 0, t = 0;
+      const int tail = (p.blocks - (p.num_kb - 1) * 8 + 1) / 2;  // MMAs of a tile's last stage
+      uint32_t it = 0, t = 0, s = 0, ph = 0;       // stages done; ring position and its phase
+      uint32_t s2 = STAGES - 2, ph2 = 1;           // the same two stages back
       bool ok = true;
+      // a warp-uniform outcome: every lane polls
+      auto wait = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit, &abort_flag)) != 0;
+      };
       for (int u = cluster; ok && u < p.num_tiles; u += clusters, ++t) {
         // the other accumulator's overlapping columns have been read (and with
         // them, by the same warps earlier, all of this one's last tile)
-        if (t > 0 && !mbar_wait_bounded(released_bar((t - 1) & 1u), ((t - 1) >> 1) & 1u, limit,
-                                        &abort_flag)) {
-          give_up(kErrTimeoutMma);
+        if (t > 0 && !wait(released_bar((t - 1) & 1u), ((t - 1) >> 1) & 1u)) {
+          if (lane == 0) give_up(kErrTimeoutMma);
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem + (t & 1u ? ACC1 : 0);
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
           // scales alternate between two sets of columns: the MMAs two stages
           // back, the last to read this set, have finished
-          if ((it >= 2 && !mbar_wait_bounded(empty_bar((it - 2) % STAGES),
-                                             ((it - 2) / STAGES) & 1u, limit, &abort_flag)) ||
-              !mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag)) {
-            give_up(kErrTimeoutMma);
+          if ((it >= 2 && !wait(empty_bar(s2), ph2)) || !wait(full_bar(s), ph)) {
+            if (lane == 0) give_up(kErrTimeoutMma);
             ok = false;
             break;
           }
           tc_fence_after();
           const uint32_t st = sbase + s * STAGE_BYTES;
+          const uint32_t a = desc_lo(st), bb = a + (OFF_B >> 4);
+          const uint32_t ca = a + (OFF_SFA >> 4), cb = a + (OFF_SFB >> 4);
           const uint32_t sfa = tmem + SF_COL + (it & 1u) * 24, sfb = sfa + 8;
-          // columns: A's tile 0, tile 1; B's tile 0 of both 128-row parts, then tile 1 of both
+          const uint32_t first = kb > 0 ? 1u : 0u;
+          const bool full = kb + 1 < p.num_kb || tail == 4;
+          if (elect_one()) {
+            // columns: A's tile 0, tile 1; B's tile 0 of both 128-row parts, then tile 1 of both
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            copy_scale_tile<2>(sfa + 4 * i, st + OFF_SFA + 512 * i);
-            copy_scale_tile<2>(sfb + 8 * i, st + OFF_SFB + 512 * i);
-            copy_scale_tile<2>(sfb + 8 * i + 4, st + OFF_SFB + 1024 + 512 * i);
+            for (int i = 0; i < 2; ++i) {
+              copy_scale_tile<2>(sfa + 4 * i, ca + 32 * i);
+              copy_scale_tile<2>(sfb + 8 * i, cb + 32 * i);
+              copy_scale_tile<2>(sfb + 8 * i + 4, cb + 64 + 32 * i);
+            }
+            if (full) {
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_mxf4<2>(d, a + 2 * kk, bb + 2 * kk, kk & 1 ? id2 : id0, sfa + 4 * (kk >> 1),
+                            sfb + 8 * (kk >> 1), kk > 0 ? 1u : first);
+            } else {
+              for (int kk = 0; kk < tail; ++kk)
+                mma_mxf4<2>(d, a + 2 * kk, bb + 2 * kk, kk & 1 ? id2 : id0, sfa + 4 * (kk >> 1),
+                            sfb + 8 * (kk >> 1), kk > 0 ? 1u : first);
+            }
+            mma_commit_pair_multicast(empty_bar(s), 0x3);
+            if (kb + 1 == p.num_kb) mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
           }
-#pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            if (kb * 8 + kk * 2 < p.blocks)
-              mma_mxf4<2>(d, smem_desc_sw128(st + kk * 32, 16, 1024),
-                          smem_desc_sw128(st + OFF_B + kk * 32, 16, 1024), kk & 1 ? id2 : id0,
-                          sfa + 4 * (kk >> 1), sfb + 8 * (kk >> 1), kb > 0 || kk > 0 ? 1u : 0u);
-          mma_commit_pair_multicast(empty_bar(s), 0x3);
+          __syncwarp();
+          if (++s == STAGES) {
+            s = 0;
+            ph ^= 1u;
+          }
+          if (++s2 == STAGES) {
+            s2 = 0;
+            ph2 ^= 1u;
+          }
         }
-        if (!ok) break;
-        mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
       }
-      mma_commit_pair(drain_bar);
+      if (elect_one()) mma_commit_pair(drain_bar);
+      __syncwarp();
       volatile int never = 0;
-      if (!mbar_wait_bounded(drain_bar, 0, limit, &never)) atomicOr(p.status, kErrTimeoutDrain);
+      if (!mbar_wait_bounded(drain_bar, 0, limit, &never) && lane == 0)
+        atomicOr(p.status, kErrTimeoutDrain);
     }
     __syncwarp();
   } else {
