@@ -166,7 +166,7 @@ int workspace_locked(int dev, cudaStream_t s, size_t bytes, void** out, void** t
 void workspace_done_locked(void* token, cudaStream_t s);
 // Beside a workspace got by workspace_locked(): kControlBytes of device memory
 // that no other call writes, zero before its first use.
-constexpr size_t kControlBytes = 8192;
+constexpr size_t kControlBytes = 256;
 int workspace_control_locked(void* token, cudaStream_t s, void** out);
 
 // The bytes that rows x row_bytes with a pitch span; false where that leaves

@@ -170,7 +170,7 @@ MHR_API int gemm_mxfp4_moe(const uint16_t* x, int64_t ldx, const uint16_t* route
                            const uint8_t* down, const uint8_t* down_scales, int64_t ldd,
                            uint16_t* y, int64_t ldy, int32_t* experts, float* weights, int64_t T,
                            int64_t E, int64_t top, int64_t H, int64_t I, void* stream) {
-  static_assert(MOE_CONTROL_BYTES <= kControlBytes, "counters of the widest layer");
+  static_assert(MOE_CONTROL_BYTES <= kControlBytes, "the layer's counters");
   if (T < 0 || T > MOE_MAX_TOKENS || E < 1 || E > MOE_MAX_EXPERTS || top < 1 ||
       top > MOE_MAX_TOP || top > E || H < 1 || H > MOE_MAX_WIDTH || I < 1 || I > MOE_MAX_WIDTH)
     return MHR_ERR_INVALID_ARG;

@@ -51,9 +51,8 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
 // One mixture-of-experts layer (gemm_mxfp4_moe).
 constexpr int MOE_MAX_TOKENS = 64, MOE_MAX_TOP = 16, MOE_MAX_EXPERTS = 512;
 constexpr int64_t MOE_MAX_WIDTH = 16384;  // H and I
-// Counters that a call needs zeroed and leaves zeroed: a barrier, exits, and
-// one for every 16 rows of H.
-constexpr size_t MOE_CONTROL_BYTES = (2 + MOE_MAX_WIDTH / 16) * 4;
+// Counters that a call needs zeroed and leaves zeroed: barrier arrivals, exits.
+constexpr size_t MOE_CONTROL_BYTES = 2 * 4;
 struct MoeArgs {
   const void* x;
   int64_t ldx;

@@ -14,15 +14,14 @@
 // The product.  Weights are the 16-row side of mma.sync m16n8k16 (f16 inputs,
 // fp32 sums), pairs its 8 columns: at this few columns the tensor core idles
 // whichever instruction feeds it, and mma.sync takes its operands from the
-// registers that the weights are unpacked into.  A warp walks K in steps of
-// 128 columns, four blocks of 32; lane 4 g + q loads the 16 bytes of block q
-// of rows g and g + 8 straight from global memory, four steps ahead.  The
-// sum over k does not mind an order, so lane q's k indices are its own block's
-// and an operand needs no shuffle; the columns side is laid out in shared
-// memory in that order.  e2m1 is exact in f16, and so is its product with the
-// block's scale relative to the largest of the four (a power of two not above
-// 1; below 2^-24 of the row's largest block it vanishes, which is below fp32's
-// rounding of the sum).  The largest scale multiplies the fp32 sum of the step.
+// registers that the weights are unpacked into.  Each warp walks 16 rows at a
+// time, K in steps of 128 columns (four blocks of 32), which it fetches itself
+// by cp.async into its own ring in shared memory, several steps ahead and
+// across units: no barrier between warps, and the grid barriers pass while the
+// next weights are under way.  In a block, lane 4 g + q takes the 8 codes
+// 8 q .. 8 q + 7 of rows g and g + 8: the sum over k does not mind an order, so
+// they stand for the instruction's own k indices and need no shuffle.  A
+// block's two MMAs start from zero and its scale multiplies the fp32 sum.
 //
 // Columns in f16: x in bf16 (8 significant bits) and h in fp32 are scaled by a
 // power of two per token or pair that puts the largest magnitude in [2^12,
@@ -30,9 +29,9 @@
 // stays exact but for values below 2^-29 of its largest.  h is rounded to 11
 // bits, an eighth of the final rounding to bf16.
 //
-// The partial outputs of a pair go to the workspace; the group of warps that
-// finishes the last expert of 16 rows adds a token's pairs in their order and
-// rounds: results do not depend on the schedule.
+// The partial outputs of a pair go to the workspace, and after a third barrier
+// a token's pairs are added in their order and rounded: results do not depend
+// on the schedule.
 #include "mhr_gemm.h"
 #include "mhr_mxfp4.h"
 #include "mxfp4_common.cuh"
@@ -43,8 +42,11 @@ namespace {
 
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
-constexpr int DEPTH = 4;                       // steps of 128 columns a warp has in flight
+constexpr int DEPTH = 6;                       // steps of 128 columns in a warp's ring
+constexpr int STEP_BYTES = 16 * 64 + 16 * 4;   // 16 rows' codes and scales
+constexpr int RING_BYTES = WARPS * DEPTH * STEP_BYTES;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
+constexpr int MAX_SEGMENTS = 256;
 constexpr uint32_t kErrTimeoutGrid = 1u << 4;  // status word: a grid barrier's wait ran out
 
 struct MoeParams {
@@ -65,60 +67,77 @@ struct MoeParams {
   uint32_t* h_max;         // T * top: bits of the largest |h| of a pair
   float* h;                // T * top x 128 kt_i
   float* part;             // T * top x H: weight_p D_e h_p
-  uint32_t* control;       // [0] barrier arrivals, [1] exits, [2 ..] finished experts of 16 rows
-  int32_t row_tiles;       // ceil(H / 16)
+  uint32_t* control;       // [0] barrier arrivals, [1] exits
   int32_t stage_bytes;     // shared memory for staged columns
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t inject_stall;
 };
 
-struct Routing {  // shared memory
-  int32_t expert[MAX_PAIRS];          // of pair t * top + k
-  float weight[MAX_PAIRS];
-  int32_t list[MAX_PAIRS];            // pairs, expert by expert
-  int32_t count[MOE_MAX_EXPERTS];     // pairs of an expert
-  int32_t offset[MOE_MAX_EXPERTS];    // its first place in list
-  int32_t active[MOE_MAX_EXPERTS];    // the experts that some pair has
-  int32_t num_active;
-  int32_t fill[MOE_MAX_EXPERTS];
-  int32_t last;                       // (by group) whether this was a tile's last expert
-  int32_t abort;
+// A CTA's part of an expert's units, for some of its pairs.
+struct Segment {
+  int32_t expert, first, count;   // pairs list[first .. first + count)
+  int32_t tile;                   // first unit of the expert
+  int32_t item, items;            // place in the CTA's walk, units
+  int32_t column;                 // where the pairs' columns are staged
+  int32_t run;                    // staged together with the others of its run
 };
 
-__device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
-}
+struct Routing {  // shared memory
+  float weight[MAX_PAIRS];
+  int16_t expert[MAX_PAIRS];      // of pair t * top + k
+  int16_t list[MAX_PAIRS];        // pairs, expert by expert
+  int32_t count[MOE_MAX_EXPERTS];    // pairs of an expert
+  int16_t offset[MOE_MAX_EXPERTS];   // its first place in list
+  int16_t active[MOE_MAX_EXPERTS];   // the experts that some pair has
+  Segment seg[MAX_SEGMENTS];
+  int32_t num_active, segments, items;
+  int32_t last, abort;
+};
 
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// c = a b, and c += a b.
+__device__ __forceinline__ void mma_f16_16x8x16_first(float (&c)[4], uint32_t a0, uint32_t a1,
+                                                      uint32_t a2, uint32_t a3, uint32_t b0,
+                                                      uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void mma_f16_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1,
                                                 uint32_t a2, uint32_t a3, uint32_t b0,
                                                 uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
       "{%8, %9}, {%0, %1, %2, %3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// The largest of four scale codes, and 2^(code q - largest) as f16x2.
-__device__ __forceinline__ uint32_t step_scale(uint32_t codes, int q, uint32_t& largest) {
-  const uint32_t m = max(max(codes & 255u, (codes >> 8) & 255u),
-                         max((codes >> 16) & 255u, codes >> 24));
-  largest = m;
-  const uint32_t d = min(m - ((codes >> (8 * q)) & 255u), 126u);
-  const __half h = __float2half_rn(__uint_as_float((127u - d) << 23));
-  const uint32_t b = __half_as_ushort(h);
-  return b | (b << 16);
+// Four scale codes of a row as floats (code 0 is 2^-127, 255 NaN; exact).
+__device__ __forceinline__ void scales4(uint32_t codes, float (&f)[4]) {
+  uint32_t lo, hi;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
+  f[0] = __uint_as_float(lo << 16);
+  f[1] = __uint_as_float(lo & 0xffff0000u);
+  f[2] = __uint_as_float(hi << 16);
+  f[3] = __uint_as_float(hi & 0xffff0000u);
 }
 
 // The power of two that puts a magnitude with these fp32 bits in [2^12, 2^13);
@@ -128,22 +147,6 @@ __device__ __forceinline__ float f16_multiplier(uint32_t amax) {
   if (amax == 0 || e == 255) return 1.f;
   const int m = 127 + 12 - (e - 127);  // biased exponent of the multiplier
   return __uint_as_float(static_cast<uint32_t>(min(max(m, 1), 254)) << 23);
-}
-
-__device__ __forceinline__ void load8_bf16(const __nv_bfloat16* p, int left, bool vec,
-                                           float (&v)[8]) {
-  if (vec && left >= 8) {
-    const uint4 w = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u[i] << 16);
-      v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? __bfloat162float(p[i]) : 0.f;
-  }
 }
 
 __device__ __forceinline__ uint4 to_f16x8(const float (&v)[8], float mult) {
@@ -180,103 +183,160 @@ __device__ bool grid_barrier(const MoeParams& p, Routing& r, uint32_t round) {
   return r.abort == 0;
 }
 
-// Step 1, all warps of the grid: router logits (a warp takes one expert and
-// four tokens), each token's f16 multiplier, and zeroed pair maxima.
-__device__ void route_logits(const MoeParams& p) {
-  const int lane = threadIdx.x & 31;
-  const int warp = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbours on other SMs
-  const int warps = gridDim.x * WARPS;
-  const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
-  const bool vr = reinterpret_cast<uintptr_t>(p.router) % 16 == 0 && p.ldr % 8 == 0;
-  const int quads = (p.T + 3) / 4;
-  for (int task = warp; task < p.E * quads; task += warps) {
-    const int e = task / quads, t0 = (task - e * quads) * 4;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-    for (int k = lane * 8; k < p.H; k += 256) {
-      float w[8];
-      load8_bf16(p.router + e * p.ldr + k, p.H - k, vr, w);
+// N times 8 columns k, k + 256, ... of a bf16 row (zeros past the end), as
+// loaded: all loads are under way before the first is used.
+template <int N>
+__device__ __forceinline__ void load_row(const __nv_bfloat16* row, int k, int cols, bool vec,
+                                         uint4 (&v)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int left = cols - (k + 256 * i);
+    if (vec && left >= 8) {
+      v[i] = __ldg(reinterpret_cast<const uint4*>(row + k + 256 * i));
+    } else {
+      uint32_t u[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        if (t0 + j < p.T) {
-          float v[8];
-          load8_bf16(p.x + (t0 + j) * p.ldx + k, p.H - k, vx, v);
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(row + k + 256 * i + 2 * j);
+        u[j] = (2 * j < left ? h[0] : 0u) | ((2 * j + 1 < left ? h[1] : 0u) << 16);
+      }
+      v[i] = make_uint4(u[0], u[1], u[2], u[3]);
+    }
+  }
+}
+__device__ __forceinline__ void unpack_bf16(const uint4& w, float (&v)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum[j] = fmaf(w[i], v[i], sum[j]);
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+
+// Step 1, all warps of the grid: router logits, a warp one expert and TT tokens.
+template <int TT>
+__device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, bool vr) {
+  const int lane = threadIdx.x & 31;
+  const int sets = (p.T + TT - 1) / TT;
+  constexpr int N = TT == 1 ? 8 : 4;  // loads of 8 columns a row in flight
+  for (int task = warp; task < p.E * sets; task += warps) {
+    const int e = task / sets, t0 = (task - e * sets) * TT;
+    float sum[TT];
+#pragma unroll
+    for (int j = 0; j < TT; ++j) sum[j] = 0.f;
+    for (int k = lane * 8; k < p.H; k += 256 * N) {
+      uint4 w[N], x[TT][N];
+      load_row<N>(p.router + e * p.ldr, k, p.H, vr, w);
+#pragma unroll
+      for (int j = 0; j < TT; ++j) load_row<N>(p.x + min(t0 + j, p.T - 1) * p.ldx, k, p.H, vx, x[j]);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float wf[8];
+        unpack_bf16(w[i], wf);
+#pragma unroll
+        for (int j = 0; j < TT; ++j) {
+          float xf[8];
+          unpack_bf16(x[j][i], xf);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) sum[j] = fmaf(wf[c], xf[c], sum[j]);
         }
       }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < TT; ++j) {
 #pragma unroll
       for (int d = 16; d; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
       if (lane == 0 && t0 + j < p.T) p.logits[(t0 + j) * p.E + e] = sum[j];
     }
   }
-  for (int t = warps - 1 - warp; t < p.T; t += warps) {  // from the warps with no logits left
+}
+
+// Step 1 also: each token's f16 multiplier and zeroed maxima of its pairs.
+__device__ void route_start(const MoeParams& p) {
+  const int lane = threadIdx.x & 31;
+  const int warp = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbours on other SMs
+  const int warps = gridDim.x * WARPS;
+  const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
+  const bool vr = reinterpret_cast<uintptr_t>(p.router) % 16 == 0 && p.ldr % 8 == 0;
+  for (int t = warps - 1 - warp; t < p.T; t += warps) {  // the warps with fewest logits
     uint32_t amax = 0;
-    for (int k = lane * 8; k < p.H; k += 256) {
-      float v[8];
-      load8_bf16(p.x + t * p.ldx + k, p.H - k, vx, v);
+    for (int k = lane * 8; k < p.H; k += 256 * 8) {
+      uint4 x[8];
+      load_row<8>(p.x + t * p.ldx, k, p.H, vx, x);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          amax = max(amax, max((u[j] << 16) & 0x7fffffffu, u[j] & 0x7fff0000u));
+      }
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, d));
+    amax = __reduce_max_sync(0xffffffffu, amax);
     if (lane == 0) p.x_mult[t] = f16_multiplier(amax);
     if (lane < p.top) p.h_max[t * p.top + lane] = 0;
   }
+  if (p.E * p.T <= warps)
+    route_logits<1>(p, warp, warps, vx, vr);
+  else
+    route_logits<4>(p, warp, warps, vx, vr);
+}
+
+// The chosen experts of one token and their weights, by one warp; PER_LANE x 32
+// experts at most.  Logits become unsigned keys of the same order (a NaN
+// largest, -0 and 0 alike), 0 for one taken or none.
+template <int PER_LANE>
+__device__ void choose_token(const MoeParams& p, Routing& r, int t) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[PER_LANE];
+#pragma unroll
+  for (int i = 0; i < PER_LANE; ++i) {
+    const int e = lane + 32 * i;
+    const float v = e < p.E ? __ldcg(p.logits + t * p.E + e) + 0.f : 0.f;
+    const uint32_t b = __float_as_uint(v);
+    key[i] = e >= p.E ? 0u : v != v ? 0xffffffffu : b >> 31 ? ~b : b | 0x80000000u;
+  }
+  uint32_t chosen = 0, first = 0;
+  for (int k = 0; k < p.top; ++k) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i) m = max(m, key[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    uint32_t e = 0xffffffffu;
+#pragma unroll
+    for (int i = PER_LANE - 1; i >= 0; --i)
+      if (key[i] == m) e = lane + 32 * i;
+    e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i)
+      if (e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+    if (k == 0) first = m;
+    if (lane == k) {
+      chosen = m;
+      r.expert[t * p.top + k] = static_cast<int16_t>(e);
+    }
+  }
+  auto logit = [](uint32_t key) {
+    return __uint_as_float(key == 0xffffffffu ? key : key >> 31 ? key & 0x7fffffffu : ~key);
+  };
+  const float w = lane < p.top ? expf(logit(chosen) - logit(first)) : 0.f;
+  float sum = w;
+#pragma unroll
+  for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  if (lane < p.top) r.weight[t * p.top + lane] = w / sum;
 }
 
 // Step 2, in every CTA alike: the top experts of each token, ties to the lowest
 // index, their weights, and the pairs sorted by expert.
 __device__ void route_choose(const MoeParams& p, Routing& r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int PER_LANE = MOE_MAX_EXPERTS / 32;
   for (int t = warp; t < p.T; t += WARPS) {
-    // keys that order as (logit, then lowest expert); a NaN counts as largest
-    uint64_t key[PER_LANE];
-#pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) {
-      const int e = lane + 32 * i;
-      key[i] = 0;
-      if (e < p.E) {
-        float v = __ldcg(p.logits + t * p.E + e);
-        if (v == 0.f) v = 0.f;  // -0 and 0 tie
-        const uint32_t b = __float_as_uint(v);
-        const uint32_t o = v != v ? 0xffffffffu : (b >> 31 ? ~b : b | 0x80000000u);
-        key[i] = (static_cast<uint64_t>(o) << 32) | (0xffffffffu - e);
-      }
-    }
-    float chosen = 0.f, first = 0.f;
-    for (int k = 0; k < p.top; ++k) {
-      uint64_t best = 0;
-#pragma unroll
-      for (int i = 0; i < PER_LANE; ++i) best = key[i] > best ? key[i] : best;
-#pragma unroll
-      for (int d = 16; d; d >>= 1) {
-        const uint64_t o = __shfl_xor_sync(0xffffffffu, best, d);
-        best = o > best ? o : best;
-      }
-#pragma unroll
-      for (int i = 0; i < PER_LANE; ++i)
-        if (key[i] == best) key[i] = 0;
-      const int e = static_cast<int>(0xffffffffu - static_cast<uint32_t>(best));
-      const float logit = __ldcg(p.logits + t * p.E + e);
-      if (k == 0) first = logit;
-      if (lane == k) {
-        chosen = logit;
-        r.expert[t * p.top + k] = e;
-      }
-    }
-    const float w = lane < p.top ? expf(chosen - first) : 0.f;
-    float sum = w;
-#pragma unroll
-    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane < p.top) r.weight[t * p.top + lane] = w / sum;
+    if (p.E <= 128)
+      choose_token<4>(p, r, t);
+    else
+      choose_token<MOE_MAX_EXPERTS / 32>(p, r, t);
   }
   const int pairs = p.T * p.top;
-  for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[e] = r.fill[e] = 0;
+  for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[e] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += THREADS) atomicAdd(&r.count[r.expert[i]], 1);
   __syncthreads();
@@ -291,8 +351,9 @@ __device__ void route_choose(const MoeParams& p, Routing& r) {
         const int o = __shfl_up_sync(0xffffffffu, scan, d);
         if (lane >= d) scan += o;
       }
-      if (e0 + lane < p.E) r.offset[e0 + lane] = offset + scan - c;
-      if (c > 0) r.active[active + __popc(has & ((1u << lane) - 1))] = e0 + lane;
+      if (e0 + lane < p.E) r.offset[e0 + lane] = static_cast<int16_t>(offset + scan - c);
+      if (c > 0)
+        r.active[active + __popc(has & ((1u << lane) - 1))] = static_cast<int16_t>(e0 + lane);
       active += __popc(has);
       offset += __shfl_sync(0xffffffffu, scan, 31);
     }
@@ -301,8 +362,9 @@ __device__ void route_choose(const MoeParams& p, Routing& r) {
   __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += THREADS) {
     const int e = r.expert[i];
-    // (an expert's pairs in any order: each is a column of its own)
-    r.list[r.offset[e] + atomicAdd(&r.fill[e], 1)] = i;
+    // an expert's pairs, from its list's end down, in any order: each is a
+    // column of its own (this takes count to zero)
+    r.list[r.offset[e] + atomicSub(&r.count[e], 1) - 1] = static_cast<int16_t>(i);
     if (blockIdx.x == 0) {
       p.experts[i] = e;
       p.weights[i] = r.weight[i];
@@ -311,256 +373,337 @@ __device__ void route_choose(const MoeParams& p, Routing& r) {
   __syncthreads();
 }
 
+// The CTA's equal share of all units (of `tiles` per active expert) as
+// segments: expert by expert, at most `most` of an expert's pairs at a time (more
+// pairs take its units again), in runs whose columns fit `capacity` together.
+__device__ void plan_segments(Routing& r, int pairs, int tiles, int most, int capacity) {
+  if (threadIdx.x == 0) {
+    // (at most 512 experts x 2048 units x some hundred CTAs: 32 bits)
+    const uint32_t units = static_cast<uint32_t>(r.num_active) * tiles;
+    const int begin = static_cast<int>(units * blockIdx.x / gridDim.x);
+    const int end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
+    int n = 0, item = 0, run = 0, column = 0;
+    for (int u = begin; u < end;) {
+      const int ai = u / tiles, e = r.active[ai], tile = u - ai * tiles;
+      const int items = min(tiles - tile, end - u);
+      const int first = r.offset[e];
+      const int last = ai + 1 < r.num_active ? r.offset[r.active[ai + 1]] : pairs;
+      for (int c = first; c < last && n < MAX_SEGMENTS; c += most) {
+        const int count = min(most, last - c);
+        if (column + count > capacity) {
+          ++run;
+          column = 0;
+        }
+        r.seg[n++] = Segment{e, c, count, tile, item, items, column, run};
+        column += count;
+        item += items;
+      }
+      u += items;
+    }
+    r.segments = n;
+    r.items = item;
+  }
+  __syncthreads();
+}
+
 // Steps 3 and 4.  UP: units of 8 gate rows and the same 8 up rows, columns x,
 // K = H; otherwise units of 16 rows of the down matrix, columns h, K = I.
-// The CTA takes an equal run of all units, expert by expert; for each expert
-// it stages up to 8 NT of its pairs' columns, and groups of warps take the
-// units in turn, each warp an equal part of K.
+// Warps take the CTA's units in turn; of the units left when no full round
+// remains, groups of ws warps take one each, every warp an equal part of K.
 template <int NT, bool UP>
-__device__ void product(const MoeParams& p, Routing& r, uint8_t* staged, float* red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
-  const int kt = UP ? p.kt_h : p.kt_i;
-  const int blocks = UP ? (p.H + 31) / 32 : (p.I + 31) / 32;
-  const int tiles = UP ? (p.I + 7) / 8 : p.row_tiles;
-  const int64_t units = static_cast<int64_t>(r.num_active) * tiles;
-  const int64_t u_begin = units * blockIdx.x / gridDim.x;
-  const int64_t u_end = units * (blockIdx.x + 1) / gridDim.x;
-  const uint8_t* data = UP ? p.up : p.down;
-  const uint8_t* scales = UP ? p.up_s : p.down_s;
-  const int64_t ld = UP ? p.ldu : p.ldd;
-  const int pitch = kt * 256 + 64;  // 64 past a multiple of 128: neighbouring rows' banks differ
-  const int capacity = min(8 * NT, p.stage_bytes / pitch);
-  // warps a unit: as many units at once as the CTA has, down to one warp each
-  int ws = WARPS;
-  while (ws > 1 && (WARPS / ws < u_end - u_begin || ws > kt)) ws >>= 1;
-  ws = max(ws, WARPS / 8);  // (named barriers 1 to 8)
-  const int groups = WARPS / ws, group = warp / ws, part = warp - group * ws;
-  const int k_begin = kt * part / ws, k_end = kt * (part + 1) / ws;
-  const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
+struct Product {
+  const MoeParams& p;
+  Routing& r;
+  uint8_t* staged;
+  uint8_t* ring;       // this warp's
+  float* red;          // partial sums of groups: WARPS x NT x 128
+  int lane, warp, g, q;
+  int kt, blocks, pitch;
+  int rounds;                  // the first `rounds` units a whole warp each
+  int groups, ws, group, part, k_begin, k_end;  // the others
+  // the fetching cursor: unit `item` of the walk, in segment seg, at step lk
+  // up to l_end
+  int item, seg, lk, l_end, fetched;
+  const uint8_t *pa, *pb, *ps;
 
-  for (int64_t seg = u_begin; seg < u_end;) {
-    const int ai = static_cast<int>(seg / tiles), e = r.active[ai];
-    const int t_begin = static_cast<int>(seg - static_cast<int64_t>(ai) * tiles);
-    const int t_end = static_cast<int>(min(static_cast<int64_t>(tiles), t_begin + u_end - seg));
-    for (int c0 = 0; c0 < r.count[e]; c0 += capacity) {
-      const int cols = min(capacity, r.count[e] - c0);
-      const int32_t* list = r.list + r.offset[e] + c0;
-      __syncthreads();  // the staged columns before these have been read
-      for (int i = threadIdx.x; i < cols * kt * 16; i += THREADS) {
-        const int c = i / (kt * 16), piece = i - c * (kt * 16), k = piece * 8;
-        float v[8];
-        float mult;
-        if (UP) {
-          const int t = list[c] / p.top;
-          mult = __ldcg(p.x_mult + t);
-          if (k < p.H)
-            load8_bf16(p.x + t * p.ldx + k, p.H - k, vx, v);
-          else
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = 0.f;
-        } else {
-          mult = f16_multiplier(__ldcg(p.h_max + list[c]));
-          const float4* src = reinterpret_cast<const float4*>(
-              p.h + static_cast<int64_t>(list[c]) * p.kt_i * 128 + k);
-          const float4 a = __ldcg(src), b = __ldcg(src + 1);
-          const float f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) v[j] = k + j < p.I ? f[j] : 0.f;
-        }
-        // piece 4 q + c of a step at place 4 c + q: a load of the four lanes
-        // of a row is then 64 contiguous bytes
-        const int step = piece >> 4, at = piece & 15;
-        *reinterpret_cast<uint4*>(staged + c * pitch + step * 256 +
-                                  ((at & 3) * 4 + (at >> 2)) * 16) = to_f16x8(v, mult);
+  __device__ Product(const MoeParams& p_, Routing& r_, uint8_t* staged_, uint8_t* ring0,
+                     float* red_)
+      : p(p_), r(r_), staged(staged_), red(red_) {
+    lane = threadIdx.x & 31;
+    warp = threadIdx.x >> 5;
+    g = lane >> 2;
+    q = lane & 3;
+    ring = ring0 + warp * (DEPTH * STEP_BYTES);
+    kt = UP ? p.kt_h : p.kt_i;
+    blocks = UP ? (p.H + 31) / 32 : (p.I + 31) / 32;
+    pitch = kt * 256 + 64;  // 64 past a multiple of 128: neighbouring columns' banks differ
+    plan_segments(r, p.T * p.top, UP ? (p.I + 7) / 8 : (p.H + 15) / 16,
+                  min(8 * NT, p.stage_bytes / pitch), p.stage_bytes / pitch);
+    rounds = r.items & ~(WARPS - 1);
+    ws = WARPS;
+    while (ws > 2 && (WARPS / ws < r.items - rounds || ws > kt)) ws >>= 1;
+    groups = WARPS / ws;
+    group = warp / ws;
+    part = warp - group * ws;
+    k_begin = kt * part / ws;
+    k_end = kt * (part + 1) / ws;
+    item = rounds ? warp : group;
+    seg = 0;
+    fetched = 0;
+    find();
+    for (int d = 0; d < DEPTH - 1; ++d) fetch();
+  }
+
+  // The segment and rows of `item`.
+  __device__ void find() {
+    lk = item < rounds ? 0 : k_begin;
+    l_end = item < rounds ? kt : k_end;
+    if (item >= r.items || lk == l_end) {
+      item = 0x7fffffff;
+      return;
+    }
+    while (item >= r.seg[seg].item + r.seg[seg].items) ++seg;
+    const Segment& sg = r.seg[seg];
+    const int tile = sg.tile + item - sg.item;
+    const int64_t e = sg.expert;
+    const uint8_t* data = UP ? p.up : p.down;
+    const int64_t ld = UP ? p.ldu : p.ldd;
+    auto row_of = [&](int i) {  // row i of the unit's 16; past the last row: the last
+      return UP ? (e * 2 + (i >> 3)) * p.I + min(tile * 8 + (i & 7), p.I - 1)
+                : e * p.H + min(tile * 16 + i, p.H - 1);
+    };
+    pa = data + row_of(g) * ld + q * 16;
+    pb = data + row_of(g + 8) * ld + q * 16;
+    ps = (UP ? p.up_s : p.down_s) + scale_offset(row_of(lane & 15), 0, kt);
+  }
+
+  // The warp's unit after `item`.
+  __device__ int next(int item) const {
+    if (item >= rounds) return item + groups;
+    return item + WARPS < rounds ? item + WARPS : rounds + group;
+  }
+
+  // One step of 128 columns into the ring (an empty group past the end): row
+  // i's block b at place b ^ (i / 2 % 4) of its 64 bytes, so that eight rows'
+  // words of a block fall into different banks.
+  __device__ void fetch() {
+    if (item != 0x7fffffff) {
+      const uint32_t st = smem_u32(ring) + fetched * STEP_BYTES;
+      const uint32_t at = st + g * 64 + ((q ^ ((g >> 1) & 3)) << 4);
+      const uint32_t bytes = lk * 4 + q < blocks ? 16 : 0;  // 0: zero codes
+      const int64_t step = bytes ? lk * 64 : 0;
+      cp_async_16(at, pa + step, bytes);
+      cp_async_16(at + 512, pb + step, bytes);
+      if (lane < 16) cp_async_4(st + 1024 + lane * 4, ps + static_cast<int64_t>(lk) * 512);
+      if (++fetched == DEPTH) fetched = 0;
+      if (++lk == l_end) {
+        item = next(item);
+        find();
       }
-      __syncthreads();
-      const int ntiles = (cols + 7) / 8;
+    }
+    cp_async_commit();
+  }
 
-      // the warp's walk: units t_begin + group, + groups, ...; steps k_begin to k_end of each
-      struct Slot {
-        uint4 a, b;
-        uint32_t sa, sb;
-      } slot[DEPTH];
-      int lt = t_begin + group, lk = k_begin;
-      const uint8_t *pa, *pb, *psa, *psb;
-      auto rows_of = [&](int tile) {
-        int64_t ra, rb;
-        if (UP) {
-          ra = static_cast<int64_t>(e) * 2 * p.I + min(tile * 8 + g, p.I - 1);
-          rb = ra + p.I;
-        } else {
-          ra = static_cast<int64_t>(e) * p.H + min(tile * 16 + g, p.H - 1);
-          rb = static_cast<int64_t>(e) * p.H + min(tile * 16 + 8 + g, p.H - 1);
-        }
-        pa = data + ra * ld + q * 16;
-        pb = data + rb * ld + q * 16;
-        psa = scales + scale_offset(ra, 0, kt);
-        psb = scales + scale_offset(rb, 0, kt);
-      };
-      auto load = [&](Slot& s) {
-        if (lt >= t_end) return;
-        if (lk * 4 + q < blocks) {
-          s.a = ldg_stream(pa + lk * 64);
-          s.b = ldg_stream(pb + lk * 64);
-        } else {
-          s.a = s.b = make_uint4(0, 0, 0, 0);
-        }
-        s.sa = __ldg(reinterpret_cast<const uint32_t*>(psa + static_cast<int64_t>(lk) * 512));
-        s.sb = __ldg(reinterpret_cast<const uint32_t*>(psb + static_cast<int64_t>(lk) * 512));
-        if (++lk == k_end) {
-          lk = k_begin;
-          lt += groups;
-          if (lt < t_end) rows_of(lt);
-        }
-      };
-      float acc[NT][4];
-      auto clear = [&] {
+  // The columns of a run's pairs in f16, in batches of loads.
+  __device__ void stage(int run) {
+    const int pieces = kt * 16;  // of 8 columns
+    const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
+    constexpr int BATCH = UP ? 4 : 2;
+    for (int s = 0; s < r.segments; ++s) {
+      const Segment sg = r.seg[s];
+      if (sg.run != run) continue;
+      for (int i0 = threadIdx.x; i0 < sg.count * pieces; i0 += THREADS * BATCH) {
+        uint4 raw[BATCH][UP ? 1 : 2];
+        float mult[BATCH];
+        uint32_t to[BATCH];
+        int left[BATCH];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-      };
-      auto step = [&](const Slot& s, int k) {
-        uint32_t la, lb;
-        const uint32_t ma = step_scale(s.sa, q, la), mb = step_scale(s.sb, q, lb);
-        float sum[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sum[n][i] = 0.f;
-        const uint32_t wa[4] = {s.a.x, s.a.y, s.a.z, s.a.w};
-        const uint32_t wb[4] = {s.b.x, s.b.y, s.b.z, s.b.w};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const uint32_t a0 = hmul2(e2m1_to_f16x2<0>(wa[c]), ma);
-          const uint32_t a1 = hmul2(e2m1_to_f16x2<1>(wa[c]), ma);
-          const uint32_t a2 = hmul2(e2m1_to_f16x2<2>(wa[c]), ma);
-          const uint32_t a3 = hmul2(e2m1_to_f16x2<3>(wa[c]), ma);
-          const uint32_t b0 = hmul2(e2m1_to_f16x2<0>(wb[c]), mb);
-          const uint32_t b1 = hmul2(e2m1_to_f16x2<1>(wb[c]), mb);
-          const uint32_t b2 = hmul2(e2m1_to_f16x2<2>(wb[c]), mb);
-          const uint32_t b3 = hmul2(e2m1_to_f16x2<3>(wb[c]), mb);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n < ntiles) {
-              const int col = min(n * 8 + g, cols - 1);
-              const uint4 x = *reinterpret_cast<const uint4*>(staged + col * pitch + k * 256 +
-                                                              c * 64 + q * 16);
-              mma_f16_16x8x16(sum[n], a0, b0, a1, b1, x.x, x.y);
-              mma_f16_16x8x16(sum[n], a2, b2, a3, b3, x.z, x.w);
-            }
+        for (int j = 0; j < BATCH; ++j) {
+          const int i = min(i0 + j * THREADS, sg.count * pieces - 1);  // (past the end: the last)
+          const int c = i / pieces, k = (i - c * pieces) * 8, pair = r.list[sg.first + c];
+          to[j] = (sg.column + c) * pitch + k * 2;
+          if (UP) {
+            const int t = pair / p.top;
+            mult[j] = __ldcg(p.x_mult + t);
+            load_row<1>(p.x + t * p.ldx, k, p.H, vx, *reinterpret_cast<uint4(*)[1]>(raw[j]));
+          } else {
+            mult[j] = __uint_as_float(__ldcg(p.h_max + pair));
+            left[j] = p.I - k;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                p.h + static_cast<int64_t>(pair) * p.kt_i * 128 + k);
+            raw[j][0] = __ldcg(src);
+            raw[j][UP ? 0 : 1] = __ldcg(src + 1);
           }
         }
-        const float fa = scale_value(la), fb = scale_value(lb);
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          acc[n][0] = fmaf(sum[n][0], fa, acc[n][0]);
-          acc[n][1] = fmaf(sum[n][1], fa, acc[n][1]);
-          acc[n][2] = fmaf(sum[n][2], fb, acc[n][2]);
-          acc[n][3] = fmaf(sum[n][3], fb, acc[n][3]);
-        }
-      };
-      uint32_t turn = 0;
-      // A finished unit: the group's parts of K meet in shared memory (two
-      // buffers in turn, so one barrier a unit) and are added in their order.
-      auto finish = [&](int tile) {
-        float* buf = red + (turn & 1) * (WARPS * NT * 128);
-        ++turn;
+        for (int j = 0; j < BATCH; ++j) {
+          float v[8];
+          if (UP) {
+            unpack_bf16(raw[j][0], v);
+          } else {
+            const uint4 a = raw[j][0], b = raw[j][UP ? 0 : 1];
+            const uint32_t f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            mult[j] = f16_multiplier(__float_as_uint(mult[j]));
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          if (n < ntiles)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              buf[warp * (NT * 128) + (n * 4 + i) * 32 + lane] = acc[n][i];
-        asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(ws * 32) : "memory");
-        const float* mine = buf + group * ws * (NT * 128);
-        if (UP) {
-          // 64 outputs of a column tile: (i, lane) -> row lane / 4, column 2 (lane % 4) + i
-          for (int o = part; o < ntiles * 2; o += ws) {
-            const int n = o >> 1, i = o & 1, col = n * 8 + q * 2 + i;
-            float gate = 0.f, value = 0.f;
-            for (int w = 0; w < ws; ++w) {
-              gate += mine[w * (NT * 128) + (n * 4 + i) * 32 + lane];
-              value += mine[w * (NT * 128) + (n * 4 + 2 + i) * 32 + lane];
-            }
-            const int row = tile * 8 + g;
-            const bool in = col < cols && row < p.I;
-            const int pair = list[min(col, cols - 1)];
-            const float back = 1.f / __ldcg(p.x_mult + pair / p.top);  // a power of two
-            gate *= back;
-            value *= back;
-            const float hv = gate / (1.f + expf(-gate)) * value;
-            if (in) p.h[static_cast<int64_t>(pair) * p.kt_i * 128 + row] = hv;
-            uint32_t m = in ? __float_as_uint(hv) & 0x7fffffffu : 0u;
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-            if (g == 0 && col < cols) atomicMax(p.h_max + pair, m);
+            for (int c = 0; c < 8; ++c) v[c] = c < left[j] ? __uint_as_float(f[c]) : 0.f;
           }
-        } else {
-          // 128 outputs of a column tile: i picks row lane / 4 (+ 8) and the column's parity
-          for (int o = part; o < ntiles * 4; o += ws) {
-            const int n = o >> 2, i = o & 3, col = n * 8 + q * 2 + (i & 1);
-            float v = 0.f;
-            for (int w = 0; w < ws; ++w) v += mine[w * (NT * 128) + (n * 4 + i) * 32 + lane];
-            const int row = tile * 16 + g + (i >> 1) * 8;
-            if (col < cols && row < p.H) {
-              const int pair = list[col];
-              const float back = 1.f / f16_multiplier(__ldcg(p.h_max + pair));
-              p.part[static_cast<int64_t>(pair) * p.H + row] = v * back * r.weight[pair];
-            }
-          }
-          // the last expert (and the last of its column runs) of these 16
-          // rows adds each token's pairs in their order
-          if (c0 + cols < r.count[e]) return;
-          __threadfence();
-          asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(ws * 32) : "memory");
-          int done = 0;
-          if (part == 0 && lane == 0)
-            done = atomicAdd(p.control + 2 + tile, 1u) == static_cast<uint32_t>(r.num_active - 1);
-          int* flag = reinterpret_cast<int*>(red + 2 * (WARPS * NT * 128)) + group;
-          if (part == 0 && lane == 0) *flag = done;
-          asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(ws * 32) : "memory");
-          if (*flag) {
-            __threadfence();
-            for (int o = part * 32 + lane; o < p.T * 16; o += ws * 32) {
-              const int t = o >> 4, row = tile * 16 + (o & 15);
-              if (row < p.H) {
-                float sum = 0.f;
-                for (int k = 0; k < p.top; ++k)
-                  sum += __ldcg(p.part + static_cast<int64_t>(t * p.top + k) * p.H + row);
-                p.y[t * p.ldy + row] = __float2bfloat16_rn(sum);
-              }
-            }
-          }
-        }
-      };
-
-      if (lt < t_end) rows_of(lt);
-      int ct = t_begin + group, ck = k_begin;
-      clear();
-      if (k_begin == k_end) {  // fewer steps than warps: this one only adds
-        for (; ct < t_end; ct += groups) finish(ct);
-      } else {
-#pragma unroll
-        for (int d = 0; d < DEPTH; ++d) load(slot[d]);
-        while (ct < t_end) {
-#pragma unroll
-          for (int d = 0; d < DEPTH; ++d) {
-            if (ct < t_end) {
-              step(slot[d], ck);
-              load(slot[d]);
-              if (++ck == k_end) {
-                finish(ct);
-                clear();
-                ck = k_begin;
-                ct += groups;
-              }
-            }
-          }
+          *reinterpret_cast<uint4*>(staged + to[j]) = to_f16x8(v, mult[j]);
         }
       }
     }
-    seg += t_end - t_begin;
+  }
+
+  // Sums of row g (0) or g + 8 (1) of the unit, column n * 8 + 2 q + i.
+  __device__ void up_output(const Segment& sg, int tile, int n, int i, float gate, float value) {
+    const int col = n * 8 + q * 2 + i, row = tile * 8 + g;
+    const bool in = col < sg.count && row < p.I;
+    const int pair = r.list[sg.first + min(col, sg.count - 1)];
+    const float back = 1.f / __ldcg(p.x_mult + pair / p.top);  // a power of two
+    gate *= back;
+    value *= back;
+    const float h = gate / (1.f + expf(-gate)) * value;
+    if (in) p.h[static_cast<int64_t>(pair) * p.kt_i * 128 + row] = h;
+    uint32_t m = in ? __float_as_uint(h) & 0x7fffffffu : 0u;
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
+    if (g == 0 && col < sg.count) atomicMax(p.h_max + pair, m);
+  }
+  __device__ void down_output(const Segment& sg, int tile, int n, int i, float v) {
+    const int col = n * 8 + q * 2 + (i & 1), row = tile * 16 + g + (i >> 1) * 8;
+    if (col < sg.count && row < p.H) {
+      const int pair = r.list[sg.first + col];
+      const float back = 1.f / f16_multiplier(__ldcg(p.h_max + pair));
+      p.part[static_cast<int64_t>(pair) * p.H + row] = v * back * r.weight[pair];
+    }
+  }
+
+  __device__ void finish(const Segment& sg, int tile, int ntiles, bool whole, float (&acc)[NT][4]) {
+    if (whole) {
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        if (n >= ntiles) break;
+        if (UP) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) up_output(sg, tile, n, i, acc[n][i], acc[n][2 + i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) down_output(sg, tile, n, i, acc[n][i]);
+        }
+      }
+      return;
+    }
+    // the group's parts of K, added in their order
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      if (n < ntiles)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) red[warp * (NT * 128) + (n * 4 + i) * 32 + lane] = acc[n][i];
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(ws * 32) : "memory");
+    const float* mine = red + group * ws * (NT * 128);
+    for (int o = part; o < ntiles * (UP ? 2 : 4); o += ws) {
+      const int n = UP ? o >> 1 : o >> 2, i = UP ? o & 1 : o & 3;
+      float a = 0.f, b = 0.f;
+      for (int w = 0; w < ws; ++w) {
+        a += mine[w * (NT * 128) + (n * 4 + i) * 32 + lane];
+        if (UP) b += mine[w * (NT * 128) + (n * 4 + 2 + i) * 32 + lane];
+      }
+      if (UP)
+        up_output(sg, tile, n, i, a, b);
+      else
+        down_output(sg, tile, n, i, a);
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(ws * 32) : "memory");
+  }
+
+  __device__ void run() {
+    int at = 0, run = 0, s = 0;  // ring position; staged run; segment
+    if (r.segments) stage(0);
+    __syncthreads();
+    for (int it = rounds ? warp : group; it < r.items; it = next(it)) {
+      const bool whole = it < rounds;
+      while (it >= r.seg[s].item + r.seg[s].items) ++s;
+      const Segment sg = r.seg[s];
+      while (run < sg.run) restage(++run);
+      const int ntiles = (sg.count + 7) / 8;
+      const uint8_t* column[NT];  // this lane's columns (past the last: the last)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        column[n] = staged + (sg.column + min(n * 8 + g, sg.count - 1)) * pitch + q * 16;
+      float acc[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
+#pragma unroll 1
+      for (int k = whole ? 0 : k_begin; k < (whole ? kt : k_end); ++k) {
+        cp_async_wait<DEPTH - 2>();
+        __syncwarp();  // the step is there for all lanes, and all have read the one before it,
+        fetch();       // whose place this takes
+        const uint8_t* st = ring + at * STEP_BYTES;
+        if (++at == DEPTH) at = 0;
+        // everything of the step first, then four blocks with nothing to wait for
+        const uint32_t sa = *reinterpret_cast<const uint32_t*>(st + 1024 + g * 4);
+        const uint32_t sb = *reinterpret_cast<const uint32_t*>(st + 1024 + g * 4 + 32);
+        const uint8_t* row = st + g * 64 + q * 4;
+        uint32_t wa[4], wb[4];
+        uint4 x[NT][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          wa[b] = *reinterpret_cast<const uint32_t*>(row + ((b ^ ((g >> 1) & 3)) << 4));
+          wb[b] = *reinterpret_cast<const uint32_t*>(row + 512 + ((b ^ ((g >> 1) & 3)) << 4));
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int b = 0; b < 4; ++b)
+            if (n < ntiles) x[n][b] = *reinterpret_cast<const uint4*>(column[n] + k * 256 + b * 64);
+        float fa[4], fb[4];
+        scales4(sa, fa);
+        scales4(sb, fb);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const uint32_t a0 = e2m1_to_f16x2<0>(wa[b]), a1 = e2m1_to_f16x2<1>(wa[b]);
+          const uint32_t a2 = e2m1_to_f16x2<2>(wa[b]), a3 = e2m1_to_f16x2<3>(wa[b]);
+          const uint32_t b0 = e2m1_to_f16x2<0>(wb[b]), b1 = e2m1_to_f16x2<1>(wb[b]);
+          const uint32_t b2 = e2m1_to_f16x2<2>(wb[b]), b3 = e2m1_to_f16x2<3>(wb[b]);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            if (n < ntiles) {
+              float sum[4];
+              mma_f16_16x8x16_first(sum, a0, b0, a1, b1, x[n][b].x, x[n][b].y);
+              mma_f16_16x8x16(sum, a2, b2, a3, b3, x[n][b].z, x[n][b].w);
+              acc[n][0] = fmaf(sum[0], fa[b], acc[n][0]);
+              acc[n][1] = fmaf(sum[1], fa[b], acc[n][1]);
+              acc[n][2] = fmaf(sum[2], fb[b], acc[n][2]);
+              acc[n][3] = fmaf(sum[3], fb[b], acc[n][3]);
+            }
+          }
+        }
+      }
+      finish(sg, sg.tile + it - sg.item, ntiles, whole, acc);
+    }
+    const int runs = r.segments ? r.seg[r.segments - 1].run : 0;
+    while (run < runs) restage(++run);  // (warps that have no unit in the last runs)
+    cp_async_wait<0>();
+  }
+  __device__ void restage(int run) {
+    __syncthreads();  // the columns staged before have been read
+    stage(run);
+    __syncthreads();
+  }
+};
+
+// Step 5, all threads of the grid: a token's pairs added in their order.
+__device__ void combine(const MoeParams& p) {
+  const int64_t n = static_cast<int64_t>(p.T) * p.H;
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < n;
+       i += static_cast<int64_t>(gridDim.x) * THREADS) {
+    const int t = static_cast<int>(i / p.H), row = static_cast<int>(i - static_cast<int64_t>(t) * p.H);
+    const float* src = p.part + static_cast<int64_t>(t) * p.top * p.H + row;
+    float sum = 0.f;
+#pragma unroll 4
+    for (int k = 0; k < p.top; ++k) sum += __ldcg(src + static_cast<int64_t>(k) * p.H);
+    p.y[t * p.ldy + row] = __float2bfloat16_rn(sum);
   }
 }
 
@@ -570,38 +713,39 @@ __global__ void __launch_bounds__(THREADS, 1) moe_mxfp4_kernel(const MoeParams p
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                              ~static_cast<uintptr_t>(127));
   __shared__ Routing r;
-  uint8_t* staged = smem;
-  float* red = reinterpret_cast<float*>(smem + p.stage_bytes);
+  float* red = reinterpret_cast<float*>(smem + RING_BYTES);
+  uint8_t* staged = smem + RING_BYTES + WARPS * NT * 128 * 4;
   if (threadIdx.x == 0) r.abort = 0;
-  route_logits(p);
+  route_start(p);
   if (grid_barrier(p, r, 1)) {
     route_choose(p, r);
-    product<NT, true>(p, r, staged, red);
-    if (grid_barrier(p, r, 2)) product<NT, false>(p, r, staged, red);
+    Product<NT, true>(p, r, staged, smem, red).run();
+    __syncthreads();
+    // (fetches its first weights, then waits for every h)
+    Product<NT, false> down(p, r, staged, smem, red);
+    if (grid_barrier(p, r, 2)) {
+      down.run();
+      if (grid_barrier(p, r, 3)) combine(p);
+    }
+    cp_async_wait<0>();
   }
   // The last CTA to leave clears the counters for the next call.
   __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
-    r.last = atomicAdd(p.control + 1, 1u) == gridDim.x - 1;
+    if (atomicAdd(p.control + 1, 1u) == gridDim.x - 1) p.control[0] = p.control[1] = 0;
   }
-  __syncthreads();
-  if (r.last)
-    for (int i = threadIdx.x; i < 2 + p.row_tiles; i += THREADS) p.control[i] = 0;
 }
 
 template <int NT>
 cudaError_t launch_t(MoeParams p, const DeviceCtl& ctl, cudaStream_t s) {
   constexpr int kSmem = 227 * 1024 - static_cast<int>(sizeof(Routing)) - 256;
-  constexpr int kRed = 2 * WARPS * NT * 128 * 4 + 64;
+  constexpr int kFixed = 128 + RING_BYTES + WARPS * NT * 128 * 4;
   auto kern = moe_mxfp4_kernel<NT>;
-  // no more shared memory than the columns need: the rest is L1
   const int pitch = (p.kt_h > p.kt_i ? p.kt_h : p.kt_i) * 256 + 64;
-  const int cols = p.T < 8 * NT ? p.T : 8 * NT;
-  const int room = (kSmem - 128 - kRed) / 16 * 16;
-  if (room < pitch) return cudaErrorInvalidValue;
-  p.stage_bytes = static_cast<int64_t>(cols) * pitch < room ? cols * pitch : room;
-  const int smem = p.stage_bytes + kRed + 128;
+  p.stage_bytes = (kSmem - kFixed) / 16 * 16;
+  if (p.stage_bytes < pitch) return cudaErrorInvalidValue;
+  const int smem = kFixed + p.stage_bytes;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
@@ -670,14 +814,12 @@ cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, con
   p.h = reinterpret_cast<float*>(ws + at[3]);
   p.part = reinterpret_cast<float*>(ws + at[4]);
   p.control = control;
-  p.row_tiles = static_cast<int32_t>((a.H + 15) / 16);
   p.status = ctl.status;
   p.wait_limit_ns = ctl.wait_limit_ns;
   p.inject_stall = ctl.inject_stall;
-  // columns an expert can have are at most T: tiles of 8
-  if (a.T <= 8) return launch_t<1>(p, ctl, s);
-  if (a.T <= 16) return launch_t<2>(p, ctl, s);
-  return launch_t<4>(p, ctl, s);
+  // an expert has at most T columns, and rarely more than 16: one or two tiles
+  // of 8 at a time
+  return a.T <= 8 ? launch_t<1>(p, ctl, s) : launch_t<2>(p, ctl, s);
 }
 
 }  // namespace mx
