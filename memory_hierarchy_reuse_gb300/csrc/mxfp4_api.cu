@@ -197,7 +197,7 @@ MHR_API int gemm_mxfp4_moe(const uint16_t* x, int64_t ldx, const uint16_t* route
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const MoeArgs a{x,    ldx,         router, ldr, up, up_scales, ldu, down,
                   down_scales, ldd,  y,      ldy, experts, weights, T, E, top, H, I};
-  size_t at[5];
+  size_t at[3];
   void *ws, *token, *control;
   if (const int st = workspace_locked(dev, s, moe_workspace(a, at), &ws, &token); st != MHR_OK)
     return st;

@@ -68,8 +68,8 @@ struct MoeArgs {
   float* weights;
   int64_t T, E, top, H, I;
 };
-// Bytes of workspace, and where its five parts start.
-size_t moe_workspace(const MoeArgs& a, size_t (&at)[5]);
+// Bytes of workspace, and where its three parts start.
+size_t moe_workspace(const MoeArgs& a, size_t (&at)[3]);
 cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, const DeviceCtl& ctl,
                        cudaStream_t s);
 

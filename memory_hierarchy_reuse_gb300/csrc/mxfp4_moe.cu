@@ -7,31 +7,29 @@
 //
 // Bound by HBM: the chosen experts' weights pass once, 17/32 byte each, with a
 // few multiply-adds a weight (as many as tokens chose the expert); the
-// smallest calls by the latency of the three dependent steps.  So one
-// persistent cooperative grid, a CTA an SM, walks routing, the up product and
-// the down product with a grid barrier between each.
+// smallest calls by the latency of the dependent steps.  So one persistent
+// cooperative grid, a CTA an SM, walks routing, the up product, the down
+// product and the sum, with a grid barrier between each.
 //
-// The product.  Weights are the 16-row side of mma.sync m16n8k16 (f16 inputs,
-// fp32 sums), pairs its 8 columns: at this few columns the tensor core idles
-// whichever instruction feeds it, and mma.sync takes its operands from the
-// registers that the weights are unpacked into.  Each warp walks 16 rows at a
-// time, K in steps of 128 columns (four blocks of 32), which it fetches itself
-// by cp.async into its own ring in shared memory, several steps ahead and
-// across units: no barrier between warps, and the grid barriers pass while the
-// next weights are under way.  In a block, lane 4 g + q takes the 8 codes
-// 8 q .. 8 q + 7 of rows g and g + 8: the sum over k does not mind an order, so
-// they stand for the instruction's own k indices and need no shuffle.  A
-// block's two MMAs start from zero and its scale multiplies the fp32 sum.
+// The product.  Weights are the 128-row side of tcgen05.mma kind::mxf4 as they
+// lie in memory: TMA moves their codes, and tcgen05.cp their scales, with no
+// instruction spent on a weight (unpacking them in registers for mma.sync took
+// some 200 issue slots per 16 x 128 weights and held the layer to 4.7 TB/s).
+// That takes e2m1 columns too, so a column is written as a sum of six: in each
+// block of 32 the first is x over s = 2^ceil(log2(max / 6)) rounded to e2m1,
+// and each further one the rest, over s / 4, s / 32, s / 256 and so on --
+// after the first, whose largest values are 2 apart, the rest is at most 1 s,
+// and after every other at most half its own unit.  The sixth leaves less
+// than 2^-15 s, 2^-16 of the block's largest magnitude.  The six are columns of
+// the MMA like any others, each with its own scales, and their fp32 sums are
+// added in the epilogue: at this few columns the MMA's time is the reading of
+// the 128 weight rows.
 //
-// Columns in f16: x in bf16 (8 significant bits) and h in fp32 are scaled by a
-// power of two per token or pair that puts the largest magnitude in [2^12,
-// 2^13), so that values down to 2^-26 of the largest keep f16's 11 bits.  x
-// stays exact but for values below 2^-29 of its largest.  h is rounded to 11
-// bits, an eighth of the final rounding to bf16.
-//
-// The partial outputs of a pair go to the workspace, and after a third barrier
-// a token's pairs are added in their order and rounded: results do not depend
-// on the schedule.
+// Work is cut into items of 128 weight rows x a part of K of one expert, and
+// every CTA takes an equal run of them; the number of parts of K (up to 16) is
+// picked so that the runs come out even.  A part's sums go to a buffer of
+// their own, and whoever reads them adds the parts in order: results do not
+// depend on the schedule.
 #include "mhr_gemm.h"
 #include "mhr_mxfp4.h"
 #include "mxfp4_common.cuh"
@@ -42,31 +40,44 @@ namespace {
 
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
-constexpr int DEPTH = 6;                       // steps of 128 columns in a warp's ring
-constexpr int STEP_BYTES = 16 * 64 + 16 * 4;   // 16 rows' codes and scales
-constexpr int RING_BYTES = WARPS * DEPTH * STEP_BYTES;
+constexpr int CONSUMERS = THREADS - 32;        // all but warp 0, the producer
+constexpr int TERMS = 6;                       // e2m1 columns a bf16 or fp32 column is written as
+constexpr int MAX_COLS = 128 / TERMS;          // columns an MMA takes at once: N <= 128
+constexpr int W_BYTES = 128 * 128;             // 128 rows x 256 columns of weights
+constexpr int RING_STAGE = W_BYTES + 1024;     // and their scales
+constexpr int STAGES = 4;
+constexpr int RING_BYTES = STAGES * RING_STAGE;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
-constexpr int MAX_SEGMENTS = 256;
+constexpr int MAX_SEGMENTS = 160;
+constexpr uint32_t ACC_COLS = 128;             // TMEM: two accumulators, two sets of scales
+constexpr uint32_t SF_COL = 2 * ACC_COLS;
+constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t kErrTimeoutGrid = 1u << 4;  // status word: a grid barrier's wait ran out
+
+// One of the two products: rows of an expert in the packed matrix, K, and the
+// partial sums it writes.
+struct MoeProduct {
+  const uint8_t* scales;
+  int32_t rows;            // rows an expert has: 2 I or H
+  int32_t tiles;           // tiles of 128 matrix rows that they can overlap
+  int32_t blocks, kt, stages;  // of K: blocks of 32, scale tiles of 128, ring stages of 256
+  float* sums;             // [part of K][pair][pitch]
+  int32_t pitch;
+};
 
 struct MoeParams {
   const __nv_bfloat16* x;
   const __nv_bfloat16* router;
   int64_t ldx, ldr;
-  const uint8_t *up, *up_s, *down, *down_s;
-  int64_t ldu, ldd;
   __nv_bfloat16* y;
   int64_t ldy;
   int32_t* experts;
   float* weights;
   int32_t T, E, top, H, I;
-  int32_t kt_h, kt_i;      // steps of 128 columns along H and I
+  MoeProduct up, down;
+  int32_t max_parts;       // of K
   // workspace
   float* logits;           // T x E
-  float* x_mult;           // T: the power of two that x is scaled by for f16
-  uint32_t* h_max;         // T * top: bits of the largest |h| of a pair
-  float* h;                // T * top x 128 kt_i
-  float* part;             // T * top x H: weight_p D_e h_p
   uint32_t* control;       // [0] barrier arrivals, [1] exits
   int32_t stage_bytes;     // shared memory for staged columns
   uint32_t* status;
@@ -74,114 +85,32 @@ struct MoeParams {
   int32_t inject_stall;
 };
 
-// A CTA's part of an expert's units, for some of its pairs.
+// A CTA's run of items that share an expert, a part of K and their columns.
 struct Segment {
-  int32_t expert, first, count;   // pairs list[first .. first + count)
-  int32_t tile;                   // first unit of the expert
-  int32_t item, items;            // place in the CTA's walk, units
-  int32_t column;                 // where the pairs' columns are staged
-  int32_t run;                    // staged together with the others of its run
+  int16_t expert, first, count;   // pairs list[first .. first + count)
+  int16_t k0, kn;                 // ring stages of K
+  int16_t part;
+  int16_t items;                  // tiles of 128 rows, from matrix row 128 * tile on
+  int16_t run;                    // staged together with the others of its run
+  int32_t tile;
+  int32_t offset;                 // of the staged columns: scales, then codes
+};
+
+struct Plan {
+  int32_t segments, parts;
+  Segment seg[MAX_SEGMENTS];
 };
 
 struct Routing {  // shared memory
   float weight[MAX_PAIRS];
   int16_t expert[MAX_PAIRS];      // of pair t * top + k
   int16_t list[MAX_PAIRS];        // pairs, expert by expert
-  int32_t count[MOE_MAX_EXPERTS];    // pairs of an expert
+  int32_t count[MOE_MAX_EXPERTS];    // pairs of an expert (while they are counted)
   int16_t offset[MOE_MAX_EXPERTS];   // its first place in list
   int16_t active[MOE_MAX_EXPERTS];   // the experts that some pair has
-  Segment seg[MAX_SEGMENTS];
-  int32_t num_active, segments, items;
-  int32_t last, abort;
+  int32_t num_active;
+  Plan up, down;
 };
-
-__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-// c = a b, and c += a b.
-__device__ __forceinline__ void mma_f16_16x8x16_first(float (&c)[4], uint32_t a0, uint32_t a1,
-                                                      uint32_t a2, uint32_t a3, uint32_t b0,
-                                                      uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %10, %10, %10};"
-      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
-}
-__device__ __forceinline__ void mma_f16_16x8x16(float (&c)[4], uint32_t a0, uint32_t a1,
-                                                uint32_t a2, uint32_t a3, uint32_t b0,
-                                                uint32_t b1) {
-  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// Four scale codes of a row as floats (code 0 is 2^-127, 255 NaN; exact).
-__device__ __forceinline__ void scales4(uint32_t codes, float (&f)[4]) {
-  uint32_t lo, hi;
-  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-      "cvt.rn.bf16x2.ue8m0x2 %0, l;\n\tcvt.rn.bf16x2.ue8m0x2 %1, h;\n\t}"
-      : "=r"(lo), "=r"(hi)
-      : "r"(codes));
-  f[0] = __uint_as_float(lo << 16);
-  f[1] = __uint_as_float(lo & 0xffff0000u);
-  f[2] = __uint_as_float(hi << 16);
-  f[3] = __uint_as_float(hi & 0xffff0000u);
-}
-
-// The power of two that puts a magnitude with these fp32 bits in [2^12, 2^13);
-// 1 for zero, infinities and NaNs (which f16 keeps).
-__device__ __forceinline__ float f16_multiplier(uint32_t amax) {
-  const int e = static_cast<int>(amax >> 23);
-  if (amax == 0 || e == 255) return 1.f;
-  const int m = 127 + 12 - (e - 127);  // biased exponent of the multiplier
-  return __uint_as_float(static_cast<uint32_t>(min(max(m, 1), 254)) << 23);
-}
-
-__device__ __forceinline__ uint4 to_f16x8(const float (&v)[8], float mult) {
-  uint32_t u[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __half2 h = __floats2half2_rn(v[2 * i] * mult, v[2 * i + 1] * mult);
-    u[i] = *reinterpret_cast<const uint32_t*>(&h);
-  }
-  return make_uint4(u[0], u[1], u[2], u[3]);
-}
-
-// All CTAs of the (cooperative) grid; bounded.  Returns false when the wait
-// ran out or another thread of the CTA had given up.
-__device__ bool grid_barrier(const MoeParams& p, Routing& r, uint32_t round) {
-  __syncthreads();
-  if (threadIdx.x == 0 && !r.abort) {
-    __threadfence();
-    const bool absent = p.inject_stall && blockIdx.x == 0 && round == 1;  // test hook
-    if (!absent) atomicAdd(p.control, 1u);
-    const uint32_t want = round * gridDim.x;
-    const uint64_t t0 = global_timer_ns();
-    volatile uint32_t* arrivals = p.control;
-    while (*arrivals < want) {
-      if (global_timer_ns() - t0 > p.wait_limit_ns) {
-        atomicOr(p.status, kErrTimeoutGrid);
-        r.abort = 1;
-        break;
-      }
-    }
-    __threadfence();
-  }
-  __syncthreads();
-  return r.abort == 0;
-}
 
 // N times 8 columns k, k + 256, ... of a bf16 row (zeros past the end), as
 // loaded: all loads are under way before the first is used.
@@ -251,90 +180,82 @@ __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, b
   }
 }
 
-// Step 1 also: each token's f16 multiplier and zeroed maxima of its pairs.
+// Step 1, all warps of the grid.
 __device__ void route_start(const MoeParams& p) {
-  const int lane = threadIdx.x & 31;
   const int warp = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbours on other SMs
   const int warps = gridDim.x * WARPS;
   const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
   const bool vr = reinterpret_cast<uintptr_t>(p.router) % 16 == 0 && p.ldr % 8 == 0;
-  for (int t = warps - 1 - warp; t < p.T; t += warps) {  // the warps with fewest logits
-    uint32_t amax = 0;
-    for (int k = lane * 8; k < p.H; k += 256 * 8) {
-      uint4 x[8];
-      load_row<8>(p.x + t * p.ldx, k, p.H, vx, x);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint32_t u[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          amax = max(amax, max((u[j] << 16) & 0x7fffffffu, u[j] & 0x7fff0000u));
-      }
-    }
-    amax = __reduce_max_sync(0xffffffffu, amax);
-    if (lane == 0) p.x_mult[t] = f16_multiplier(amax);
-    if (lane < p.top) p.h_max[t * p.top + lane] = 0;
-  }
   if (p.E * p.T <= warps)
     route_logits<1>(p, warp, warps, vx, vr);
   else
     route_logits<4>(p, warp, warps, vx, vr);
 }
 
-// The chosen experts of one token and their weights, by one warp; PER_LANE x 32
+// The chosen experts of a warp's tokens and their weights; PER_LANE x 32
 // experts at most.  Logits become unsigned keys of the same order (a NaN
 // largest, -0 and 0 alike), 0 for one taken or none.
 template <int PER_LANE>
-__device__ void choose_token(const MoeParams& p, Routing& r, int t) {
+__device__ void choose_tokens(const MoeParams& p, Routing& r) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[PER_LANE];
-#pragma unroll
-  for (int i = 0; i < PER_LANE; ++i) {
-    const int e = lane + 32 * i;
-    const float v = e < p.E ? __ldcg(p.logits + t * p.E + e) + 0.f : 0.f;
-    const uint32_t b = __float_as_uint(v);
-    key[i] = e >= p.E ? 0u : v != v ? 0xffffffffu : b >> 31 ? ~b : b | 0x80000000u;
-  }
-  uint32_t chosen = 0, first = 0;
-  for (int k = 0; k < p.top; ++k) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) m = max(m, key[i]);
-    m = __reduce_max_sync(0xffffffffu, m);
-    uint32_t e = 0xffffffffu;
-#pragma unroll
-    for (int i = PER_LANE - 1; i >= 0; --i)
-      if (key[i] == m) e = lane + 32 * i;
-    e = __reduce_min_sync(0xffffffffu, e);
+  float next[PER_LANE];
+  auto load = [&](int t) {
 #pragma unroll
     for (int i = 0; i < PER_LANE; ++i)
-      if (e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
-    if (k == 0) first = m;
-    if (lane == k) {
-      chosen = m;
-      r.expert[t * p.top + k] = static_cast<int16_t>(e);
-    }
-  }
-  auto logit = [](uint32_t key) {
-    return __uint_as_float(key == 0xffffffffu ? key : key >> 31 ? key & 0x7fffffffu : ~key);
+      next[i] = t < p.T && lane + 32 * i < p.E ? __ldcg(p.logits + t * p.E + lane + 32 * i) : 0.f;
   };
-  const float w = lane < p.top ? expf(logit(chosen) - logit(first)) : 0.f;
-  float sum = w;
+  int t = threadIdx.x >> 5;
+  load(t);
+#pragma unroll 1
+  for (; t < p.T; t += WARPS) {
+    uint32_t key[PER_LANE];
 #pragma unroll
-  for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-  if (lane < p.top) r.weight[t * p.top + lane] = w / sum;
+    for (int i = 0; i < PER_LANE; ++i) {
+      const float v = next[i] + 0.f;
+      const uint32_t b = __float_as_uint(v);
+      key[i] = lane + 32 * i >= p.E ? 0u : v != v ? 0xffffffffu : b >> 31 ? ~b : b | 0x80000000u;
+    }
+    load(t + WARPS);
+    uint32_t chosen = 0, first = 0;
+#pragma unroll 1
+    for (int k = 0; k < p.top; ++k) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < PER_LANE; ++i) m = max(m, key[i]);
+      m = __reduce_max_sync(0xffffffffu, m);
+      uint32_t e = 0xffffffffu;
+#pragma unroll
+      for (int i = PER_LANE - 1; i >= 0; --i)
+        if (key[i] == m) e = lane + 32 * i;
+      e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+      for (int i = 0; i < PER_LANE; ++i)
+        if (e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+      if (k == 0) first = m;
+      if (lane == k) {
+        chosen = m;
+        r.expert[t * p.top + k] = static_cast<int16_t>(e);
+      }
+    }
+    auto logit = [](uint32_t key) {
+      return __uint_as_float(key == 0xffffffffu ? key : key >> 31 ? key & 0x7fffffffu : ~key);
+    };
+    const float w = lane < p.top ? expf(logit(chosen) - logit(first)) : 0.f;
+    float sum = w;
+#pragma unroll
+    for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane < p.top) r.weight[t * p.top + lane] = w / sum;
+  }
 }
 
 // Step 2, in every CTA alike: the top experts of each token, ties to the lowest
 // index, their weights, and the pairs sorted by expert.
 __device__ void route_choose(const MoeParams& p, Routing& r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int t = warp; t < p.T; t += WARPS) {
-    if (p.E <= 128)
-      choose_token<4>(p, r, t);
-    else
-      choose_token<MOE_MAX_EXPERTS / 32>(p, r, t);
-  }
+  if (p.E <= 128)
+    choose_tokens<4>(p, r);
+  else
+    choose_tokens<MOE_MAX_EXPERTS / 32>(p, r);
   const int pairs = p.T * p.top;
   for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[e] = 0;
   __syncthreads();
@@ -373,411 +294,508 @@ __device__ void route_choose(const MoeParams& p, Routing& r) {
   __syncthreads();
 }
 
-// The CTA's equal share of all units (of `tiles` per active expert) as
-// segments: expert by expert, at most `most` of an expert's pairs at a time (more
-// pairs take its units again), in runs whose columns fit `capacity` together.
-__device__ void plan_segments(Routing& r, int pairs, int tiles, int most, int capacity) {
-  if (threadIdx.x == 0) {
-    // (at most 512 experts x 2048 units x some hundred CTAs: 32 bits)
-    const uint32_t units = static_cast<uint32_t>(r.num_active) * tiles;
-    const int begin = static_cast<int>(units * blockIdx.x / gridDim.x);
-    const int end = static_cast<int>(units * (blockIdx.x + 1) / gridDim.x);
-    int n = 0, item = 0, run = 0, column = 0;
-    for (int u = begin; u < end;) {
-      const int ai = u / tiles, e = r.active[ai], tile = u - ai * tiles;
-      const int items = min(tiles - tile, end - u);
-      const int first = r.offset[e];
-      const int last = ai + 1 < r.num_active ? r.offset[r.active[ai + 1]] : pairs;
-      for (int c = first; c < last && n < MAX_SEGMENTS; c += most) {
-        const int count = min(most, last - c);
-        if (column + count > capacity) {
-          ++run;
-          column = 0;
-        }
-        r.seg[n++] = Segment{e, c, count, tile, item, items, column, run};
-        column += count;
-        item += items;
-      }
-      u += items;
-    }
-    r.segments = n;
-    r.items = item;
-  }
-  __syncthreads();
+// Bytes that `cols` columns over `stages` stages of K take when staged: the
+// scales' tiles, then 128 bytes a row and stage.
+__device__ __forceinline__ int staged_rows(int cols) { return (cols * TERMS + 7) / 8 * 8; }
+__device__ __forceinline__ int staged_bytes(int cols, int stages) {
+  return stages * (1024 + staged_rows(cols) * 128);
 }
 
-// Steps 3 and 4.  UP: units of 8 gate rows and the same 8 up rows, columns x,
-// K = H; otherwise units of 16 rows of the down matrix, columns h, K = I.
-// Warps take the CTA's units in turn; of the units left when no full round
-// remains, groups of ws warps take one each, every warp an equal part of K.
-template <int NT, bool UP>
-struct Product {
+// By one warp: the parts of K, then the CTA's equal run of all items -- expert by
+// expert, part by part, tile by tile -- as segments.  At most `most` of an
+// expert's pairs go into an MMA (more pairs take its items again), and segments
+// are staged together as far as they fit.
+__device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Routing& r, Plan& plan) {
+  const int lane = threadIdx.x & 31;
+  const int pairs = p.T * p.top, active = r.num_active;
+  auto end_of = [&](int ai) {
+    return ai + 1 < active ? static_cast<int>(r.offset[r.active[ai + 1]]) : pairs;
+  };
+  int most = 0;  // pairs of the busiest expert
+  for (int a = lane; a < active; a += 32) most = max(most, end_of(a) - r.offset[r.active[a]]);
+  most = min(__reduce_max_sync(0xffffffffu, most), MAX_COLS);
+  // Time of the longest run, in stages, with half a stage for an item's ends;
+  // parts that are too long to stage all columns at once count twice.
+  const int parts = lane + 1;
+  uint32_t cost = 0xffffffffu;
+  if (parts <= p.max_parts && parts <= m.stages) {
+    const uint32_t items = static_cast<uint32_t>(active) * parts * m.tiles;
+    const uint32_t longest = (items + gridDim.x - 1) / gridDim.x;
+    const int stages = (m.stages + parts - 1) / parts;
+    cost = longest * (2 * stages + 1) * 32;
+    if (staged_bytes(most, stages) > p.stage_bytes) cost *= 2;
+    cost = min(cost, 0x7ffffffu) / 32 * 32 + lane;  // ties: the fewest parts
+  }
+  const int chosen = static_cast<int>(__reduce_min_sync(0xffffffffu, cost) & 31u) + 1;
+  if (lane == 0) {
+    int fit = most;
+    const int stages = (m.stages + chosen - 1) / chosen;
+    while (fit > 1 && staged_bytes(fit, stages) > p.stage_bytes) --fit;
+    const uint32_t items = static_cast<uint32_t>(active) * chosen * m.tiles;
+    // (at most 512 experts x 16 parts x 258 tiles x some hundred CTAs: 32 bits)
+    const int begin = static_cast<int>(items * blockIdx.x / gridDim.x);
+    const int end = static_cast<int>(items * (blockIdx.x + 1) / gridDim.x);
+    int n = 0, run = 0, offset = 0;
+    for (int u = begin; u < end;) {
+      const int row = u / m.tiles, t = u - row * m.tiles;
+      const int ai = row / chosen, part = row - ai * chosen, e = r.active[ai];
+      const int items = min(m.tiles - t, end - u);
+      u += items;
+      const int64_t r0 = static_cast<int64_t>(e) * m.rows;
+      const int tile0 = static_cast<int>(r0 / 128);
+      const int tiles = min(items, static_cast<int>((r0 + m.rows - 1) / 128) + 1 - (tile0 + t));
+      if (tiles <= 0) continue;
+      const int k0 = m.stages * part / chosen, k1 = m.stages * (part + 1) / chosen;
+      for (int c = r.offset[e]; c < end_of(ai) && n < MAX_SEGMENTS; c += fit) {
+        const int count = min(fit, end_of(ai) - c), bytes = staged_bytes(count, k1 - k0);
+        if (offset + bytes > p.stage_bytes) {
+          ++run;
+          offset = 0;
+        }
+        Segment& s = plan.seg[n++];
+        s.expert = static_cast<int16_t>(e);
+        s.first = static_cast<int16_t>(c);
+        s.count = static_cast<int16_t>(count);
+        s.k0 = static_cast<int16_t>(k0);
+        s.kn = static_cast<int16_t>(k1 - k0);
+        s.part = static_cast<int16_t>(part);
+        s.items = static_cast<int16_t>(tiles);
+        s.run = static_cast<int16_t>(run);
+        s.tile = tile0 + t;
+        s.offset = offset;
+        offset += bytes;
+      }
+    }
+    plan.segments = n;
+    plan.parts = chosen;
+  }
+}
+
+// 8 columns as TERMS rows of e2m1 codes, and their scales (of the block of 32
+// that four neighbouring lanes hold), into a stage of `rows` rows: row n is 128
+// bytes, its 16-byte pieces (a block each) swizzled by n % 8.
+__device__ __forceinline__ void split_terms(float (&v)[8], uint8_t* codes, uint8_t* scales, int n,
+                                            int lane) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // the least power of two that is not below max / 6 = max / (1.5 * 4)
+  const bool finite = amax < 0x7f800000u;
+  int c = static_cast<int>(amax >> 23) - 2 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0);
+  const int block = lane >> 2;
+  scales += (block >> 2) * 512 + (block & 3);
+  codes += (lane & 3) * 4;
+#pragma unroll 1
+  for (int j = 0; j < TERMS; ++j, ++n) {
+    // below 2^-126: nothing that an fp32 sum would see; a block with an
+    // infinity or a NaN: NaN
+    const bool some = c >= 1 && finite;
+    const float inv = __uint_as_float(some ? static_cast<uint32_t>(254 - c) << 23 : 0u);
+    const float scale = __uint_as_float(some ? static_cast<uint32_t>(c) << 23 : 0u);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
+    const uint32_t word = some ? e2m1x8(y) : 0u;
+    *reinterpret_cast<uint32_t*>(codes + n * 128 + ((block ^ (n & 7)) << 4)) = word;
+    if ((lane & 3) == 0)
+      scales[(n & 31) * 16 + (n >> 5) * 4] = static_cast<uint8_t>(!finite ? 255 : some ? c : 0);
+    const uint32_t h[4] = {e2m1_to_f16x2<0>(word), e2m1_to_f16x2<1>(word), e2m1_to_f16x2<2>(word),
+                           e2m1_to_f16x2<3>(word)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // the rest: exact
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      v[2 * i] = fmaf(-f.x, scale, v[2 * i]);
+      v[2 * i + 1] = fmaf(-f.y, scale, v[2 * i + 1]);
+    }
+    c -= j == 0 ? 2 : 3;
+  }
+}
+
+// Everything the warps of a CTA share.
+struct Cta {
   const MoeParams& p;
   Routing& r;
+  volatile int* abort_flag;
   uint8_t* staged;
-  uint8_t* ring;       // this warp's
-  float* red;          // partial sums of groups: WARPS x NT x 128
-  int lane, warp, g, q;
-  int kt, blocks, pitch;
-  int rounds;                  // the first `rounds` units a whole warp each
-  int groups, ws, group, part, k_begin, k_end;  // the others
-  // the fetching cursor: unit `item` of the walk, in segment seg, at step lk
-  // up to l_end
-  int item, seg, lk, l_end, fetched;
-  const uint8_t *pa, *pb, *ps;
+  uint32_t ring, bar0, tmem;
+  int warp, lane;
+  uint32_t it, ph_items;  // of this warp's role: ring stages, items
 
-  __device__ Product(const MoeParams& p_, Routing& r_, uint8_t* staged_, uint8_t* ring0,
-                     float* red_)
-      : p(p_), r(r_), staged(staged_), red(red_) {
-    lane = threadIdx.x & 31;
-    warp = threadIdx.x >> 5;
-    g = lane >> 2;
-    q = lane & 3;
-    ring = ring0 + warp * (DEPTH * STEP_BYTES);
-    kt = UP ? p.kt_h : p.kt_i;
-    blocks = UP ? (p.H + 31) / 32 : (p.I + 31) / 32;
-    pitch = kt * 256 + 64;  // 64 past a multiple of 128: neighbouring columns' banks differ
-    plan_segments(r, p.T * p.top, UP ? (p.I + 7) / 8 : (p.H + 15) / 16,
-                  min(8 * NT, p.stage_bytes / pitch), p.stage_bytes / pitch);
-    rounds = r.items & ~(WARPS - 1);
-    ws = WARPS;
-    while (ws > 2 && (WARPS / ws < r.items - rounds || ws > kt)) ws >>= 1;
-    groups = WARPS / ws;
-    group = warp / ws;
-    part = warp - group * ws;
-    k_begin = kt * part / ws;
-    k_end = kt * (part + 1) / ws;
-    item = rounds ? warp : group;
-    seg = 0;
-    fetched = 0;
-    find();
-    for (int d = 0; d < DEPTH - 1; ++d) fetch();
+  __device__ uint32_t full_bar(uint32_t s) const { return bar0 + 8u * s; }
+  __device__ uint32_t empty_bar(uint32_t s) const { return bar0 + 8u * (STAGES + s); }
+  __device__ uint32_t acc_full(uint32_t b) const { return bar0 + 8u * (2 * STAGES + b); }
+  __device__ uint32_t acc_empty(uint32_t b) const { return bar0 + 8u * (2 * STAGES + 2 + b); }
+  __device__ void give_up(uint32_t bit) const {  // by one thread
+    if (!*abort_flag) atomicOr(p.status, bit);
+    *abort_flag = 1;
   }
-
-  // The segment and rows of `item`.
-  __device__ void find() {
-    lk = item < rounds ? 0 : k_begin;
-    l_end = item < rounds ? kt : k_end;
-    if (item >= r.items || lk == l_end) {
-      item = 0x7fffffff;
-      return;
-    }
-    while (item >= r.seg[seg].item + r.seg[seg].items) ++seg;
-    const Segment& sg = r.seg[seg];
-    const int tile = sg.tile + item - sg.item;
-    const int64_t e = sg.expert;
-    const uint8_t* data = UP ? p.up : p.down;
-    const int64_t ld = UP ? p.ldu : p.ldd;
-    auto row_of = [&](int i) {  // row i of the unit's 16; past the last row: the last
-      return UP ? (e * 2 + (i >> 3)) * p.I + min(tile * 8 + (i & 7), p.I - 1)
-                : e * p.H + min(tile * 16 + i, p.H - 1);
-    };
-    pa = data + row_of(g) * ld + q * 16;
-    pb = data + row_of(g + 8) * ld + q * 16;
-    ps = (UP ? p.up_s : p.down_s) + scale_offset(row_of(lane & 15), 0, kt);
-  }
-
-  // The warp's unit after `item`.
-  __device__ int next(int item) const {
-    if (item >= rounds) return item + groups;
-    return item + WARPS < rounds ? item + WARPS : rounds + group;
-  }
-
-  // One step of 128 columns into the ring (an empty group past the end): row
-  // i's block b at place b ^ (i / 2 % 4) of its 64 bytes, so that eight rows'
-  // words of a block fall into different banks.
-  __device__ void fetch() {
-    if (item != 0x7fffffff) {
-      const uint32_t st = smem_u32(ring) + fetched * STEP_BYTES;
-      const uint32_t at = st + g * 64 + ((q ^ ((g >> 1) & 3)) << 4);
-      const uint32_t bytes = lk * 4 + q < blocks ? 16 : 0;  // 0: zero codes
-      const int64_t step = bytes ? lk * 64 : 0;
-      cp_async_16(at, pa + step, bytes);
-      cp_async_16(at + 512, pb + step, bytes);
-      if (lane < 16) cp_async_4(st + 1024 + lane * 4, ps + static_cast<int64_t>(lk) * 512);
-      if (++fetched == DEPTH) fetched = 0;
-      if (++lk == l_end) {
-        item = next(item);
-        find();
-      }
-    }
-    cp_async_commit();
-  }
-
-  // The columns of a run's pairs in f16, in batches of loads.
-  __device__ void stage(int run) {
-    const int pieces = kt * 16;  // of 8 columns
-    const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
-    constexpr int BATCH = UP ? 4 : 2;
-    for (int s = 0; s < r.segments; ++s) {
-      const Segment sg = r.seg[s];
-      if (sg.run != run) continue;
-      for (int i0 = threadIdx.x; i0 < sg.count * pieces; i0 += THREADS * BATCH) {
-        uint4 raw[BATCH][UP ? 1 : 2];
-        float mult[BATCH];
-        uint32_t to[BATCH];
-        int left[BATCH];
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          const int i = min(i0 + j * THREADS, sg.count * pieces - 1);  // (past the end: the last)
-          const int c = i / pieces, k = (i - c * pieces) * 8, pair = r.list[sg.first + c];
-          to[j] = (sg.column + c) * pitch + k * 2;
-          if (UP) {
-            const int t = pair / p.top;
-            mult[j] = __ldcg(p.x_mult + t);
-            load_row<1>(p.x + t * p.ldx, k, p.H, vx, *reinterpret_cast<uint4(*)[1]>(raw[j]));
-          } else {
-            mult[j] = __uint_as_float(__ldcg(p.h_max + pair));
-            left[j] = p.I - k;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                p.h + static_cast<int64_t>(pair) * p.kt_i * 128 + k);
-            raw[j][0] = __ldcg(src);
-            raw[j][UP ? 0 : 1] = __ldcg(src + 1);
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < BATCH; ++j) {
-          float v[8];
-          if (UP) {
-            unpack_bf16(raw[j][0], v);
-          } else {
-            const uint4 a = raw[j][0], b = raw[j][UP ? 0 : 1];
-            const uint32_t f[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-            mult[j] = f16_multiplier(__float_as_uint(mult[j]));
-#pragma unroll
-            for (int c = 0; c < 8; ++c) v[c] = c < left[j] ? __uint_as_float(f[c]) : 0.f;
-          }
-          *reinterpret_cast<uint4*>(staged + to[j]) = to_f16x8(v, mult[j]);
-        }
-      }
-    }
-  }
-
-  // Sums of row g (0) or g + 8 (1) of the unit, column n * 8 + 2 q + i.
-  __device__ void up_output(const Segment& sg, int tile, int n, int i, float gate, float value) {
-    const int col = n * 8 + q * 2 + i, row = tile * 8 + g;
-    const bool in = col < sg.count && row < p.I;
-    const int pair = r.list[sg.first + min(col, sg.count - 1)];
-    const float back = 1.f / __ldcg(p.x_mult + pair / p.top);  // a power of two
-    gate *= back;
-    value *= back;
-    const float h = gate / (1.f + expf(-gate)) * value;
-    if (in) p.h[static_cast<int64_t>(pair) * p.kt_i * 128 + row] = h;
-    uint32_t m = in ? __float_as_uint(h) & 0x7fffffffu : 0u;
-#pragma unroll
-    for (int d = 4; d < 32; d <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, d));
-    if (g == 0 && col < sg.count) atomicMax(p.h_max + pair, m);
-  }
-  __device__ void down_output(const Segment& sg, int tile, int n, int i, float v) {
-    const int col = n * 8 + q * 2 + (i & 1), row = tile * 16 + g + (i >> 1) * 8;
-    if (col < sg.count && row < p.H) {
-      const int pair = r.list[sg.first + col];
-      const float back = 1.f / f16_multiplier(__ldcg(p.h_max + pair));
-      p.part[static_cast<int64_t>(pair) * p.H + row] = v * back * r.weight[pair];
-    }
-  }
-
-  __device__ void finish(const Segment& sg, int tile, int ntiles, bool whole, float (&acc)[NT][4]) {
-    if (whole) {
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-        if (n >= ntiles) break;
-        if (UP) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) up_output(sg, tile, n, i, acc[n][i], acc[n][2 + i]);
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) down_output(sg, tile, n, i, acc[n][i]);
-        }
-      }
-      return;
-    }
-    // the group's parts of K, added in their order
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-      if (n < ntiles)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) red[warp * (NT * 128) + (n * 4 + i) * 32 + lane] = acc[n][i];
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(ws * 32) : "memory");
-    const float* mine = red + group * ws * (NT * 128);
-    for (int o = part; o < ntiles * (UP ? 2 : 4); o += ws) {
-      const int n = UP ? o >> 1 : o >> 2, i = UP ? o & 1 : o & 3;
-      float a = 0.f, b = 0.f;
-      for (int w = 0; w < ws; ++w) {
-        a += mine[w * (NT * 128) + (n * 4 + i) * 32 + lane];
-        if (UP) b += mine[w * (NT * 128) + (n * 4 + 2 + i) * 32 + lane];
-      }
-      if (UP)
-        up_output(sg, tile, n, i, a, b);
-      else
-        down_output(sg, tile, n, i, a);
-    }
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(ws * 32) : "memory");
-  }
-
-  __device__ void run() {
-    int at = 0, run = 0, s = 0;  // ring position; staged run; segment
-    if (r.segments) stage(0);
-    __syncthreads();
-    for (int it = rounds ? warp : group; it < r.items; it = next(it)) {
-      const bool whole = it < rounds;
-      while (it >= r.seg[s].item + r.seg[s].items) ++s;
-      const Segment sg = r.seg[s];
-      while (run < sg.run) restage(++run);
-      const int ntiles = (sg.count + 7) / 8;
-      const uint8_t* column[NT];  // this lane's columns (past the last: the last)
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        column[n] = staged + (sg.column + min(n * 8 + g, sg.count - 1)) * pitch + q * 16;
-      float acc[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] = 0.f;
-#pragma unroll 1
-      for (int k = whole ? 0 : k_begin; k < (whole ? kt : k_end); ++k) {
-        cp_async_wait<DEPTH - 2>();
-        __syncwarp();  // the step is there for all lanes, and all have read the one before it,
-        fetch();       // whose place this takes
-        const uint8_t* st = ring + at * STEP_BYTES;
-        if (++at == DEPTH) at = 0;
-        // everything of the step first, then four blocks with nothing to wait for
-        const uint32_t sa = *reinterpret_cast<const uint32_t*>(st + 1024 + g * 4);
-        const uint32_t sb = *reinterpret_cast<const uint32_t*>(st + 1024 + g * 4 + 32);
-        const uint8_t* row = st + g * 64 + q * 4;
-        uint32_t wa[4], wb[4];
-        uint4 x[NT][4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          wa[b] = *reinterpret_cast<const uint32_t*>(row + ((b ^ ((g >> 1) & 3)) << 4));
-          wb[b] = *reinterpret_cast<const uint32_t*>(row + 512 + ((b ^ ((g >> 1) & 3)) << 4));
-        }
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int b = 0; b < 4; ++b)
-            if (n < ntiles) x[n][b] = *reinterpret_cast<const uint4*>(column[n] + k * 256 + b * 64);
-        float fa[4], fb[4];
-        scales4(sa, fa);
-        scales4(sb, fb);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const uint32_t a0 = e2m1_to_f16x2<0>(wa[b]), a1 = e2m1_to_f16x2<1>(wa[b]);
-          const uint32_t a2 = e2m1_to_f16x2<2>(wa[b]), a3 = e2m1_to_f16x2<3>(wa[b]);
-          const uint32_t b0 = e2m1_to_f16x2<0>(wb[b]), b1 = e2m1_to_f16x2<1>(wb[b]);
-          const uint32_t b2 = e2m1_to_f16x2<2>(wb[b]), b3 = e2m1_to_f16x2<3>(wb[b]);
-#pragma unroll
-          for (int n = 0; n < NT; ++n) {
-            if (n < ntiles) {
-              float sum[4];
-              mma_f16_16x8x16_first(sum, a0, b0, a1, b1, x[n][b].x, x[n][b].y);
-              mma_f16_16x8x16(sum, a2, b2, a3, b3, x[n][b].z, x[n][b].w);
-              acc[n][0] = fmaf(sum[0], fa[b], acc[n][0]);
-              acc[n][1] = fmaf(sum[1], fa[b], acc[n][1]);
-              acc[n][2] = fmaf(sum[2], fb[b], acc[n][2]);
-              acc[n][3] = fmaf(sum[3], fb[b], acc[n][3]);
-            }
-          }
-        }
-      }
-      finish(sg, sg.tile + it - sg.item, ntiles, whole, acc);
-    }
-    const int runs = r.segments ? r.seg[r.segments - 1].run : 0;
-    while (run < runs) restage(++run);  // (warps that have no unit in the last runs)
-    cp_async_wait<0>();
-  }
-  __device__ void restage(int run) {
-    __syncthreads();  // the columns staged before have been read
-    stage(run);
-    __syncthreads();
+  __device__ bool wait(uint32_t bar, uint32_t parity, uint32_t bit) const {  // by a warp
+    const bool ok = __all_sync(
+        0xffffffffu, mbar_wait_bounded(bar, parity, p.wait_limit_ns, abort_flag)) != 0;
+    if (!ok && lane == 0) give_up(bit);
+    __syncwarp();
+    return ok;
   }
 };
 
-// Step 5, all threads of the grid: a token's pairs added in their order.
-__device__ void combine(const MoeParams& p) {
-  const int64_t n = static_cast<int64_t>(p.T) * p.H;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * THREADS + threadIdx.x; i < n;
-       i += static_cast<int64_t>(gridDim.x) * THREADS) {
-    const int t = static_cast<int>(i / p.H), row = static_cast<int>(i - static_cast<int64_t>(t) * p.H);
-    const float* src = p.part + static_cast<int64_t>(t) * p.top * p.H + row;
-    float sum = 0.f;
-#pragma unroll 4
-    for (int k = 0; k < p.top; ++k) sum += __ldcg(src + static_cast<int64_t>(k) * p.H);
-    p.y[t * p.ldy + row] = __float2bfloat16_rn(sum);
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(CONSUMERS) : "memory");
+}
+
+// All CTAs of the (cooperative) grid, by the consumer warps; bounded.
+__device__ void grid_barrier(Cta& c, uint32_t round) {
+  consumers_sync();
+  if (threadIdx.x == 32 && !*c.abort_flag) {
+    __threadfence();
+    const bool absent = c.p.inject_stall && blockIdx.x == 0 && round == 1;  // test hook
+    if (!absent) atomicAdd(c.p.control, 1u);
+    const uint32_t want = round * gridDim.x;
+    const uint64_t t0 = global_timer_ns();
+    volatile uint32_t* arrivals = c.p.control;
+    while (*arrivals < want) {
+      if (global_timer_ns() - t0 > c.p.wait_limit_ns) {
+        c.give_up(kErrTimeoutGrid);
+        break;
+      }
+    }
+    __threadfence();
+  }
+  consumers_sync();
+}
+
+// The weights of a plan's items, into the ring.  By one thread.
+__device__ bool produce(Cta& c, const CUtensorMap* map, const MoeProduct& m, const Plan& plan) {
+  for (int s = 0; s < plan.segments; ++s) {
+    const Segment sg = plan.seg[s];
+    for (int t = sg.tile; t < sg.tile + sg.items; ++t)
+      for (int k = sg.k0; k < sg.k0 + sg.kn; ++k, ++c.it) {
+        const uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
+        if (!mbar_wait_bounded(c.empty_bar(st), ph ^ 1u, c.p.wait_limit_ns, c.abort_flag)) {
+          c.give_up(kErrTimeoutProducer);
+          return false;
+        }
+        const uint32_t bytes = static_cast<uint32_t>(min(2, m.kt - 2 * k)) * 512u;
+        const uint32_t at = c.ring + st * RING_STAGE;
+        mbar_arrive_expect_tx(c.full_bar(st), W_BYTES + bytes);
+        tma_load_2d(at, map, c.full_bar(st), k * 128, t * 128);
+        bulk_load(at + W_BYTES, m.scales + (static_cast<int64_t>(t) * m.kt + 2 * k) * 512, bytes,
+                  c.full_bar(st));
+      }
+  }
+  return true;
+}
+
+// 8 columns of K of a pair: x as loaded, or h from the parts' sums.
+template <bool UP>
+struct Piece {
+  uint4 x;
+  float h[8];
+  __device__ __forceinline__ void load(const Cta& c, int pair, int k, bool vx) {
+    const MoeParams& p = c.p;
+    if (UP) {
+      load_row<1>(p.x + (pair / p.top) * p.ldx, k, p.H, vx, *reinterpret_cast<uint4(*)[1]>(&x));
+      return;
+    }
+    const float* g = p.up.sums + static_cast<int64_t>(pair) * p.up.pitch + k;
+    const int half = p.up.pitch / 2;
+    const int64_t parts = static_cast<int64_t>(p.T) * p.top * p.up.pitch;
+    float gate[8], value[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gate[i] = value[i] = 0.f;
+    if (k < p.I)
+      for (int q = 0; q < c.r.up.parts; ++q, g += parts) {
+        const float4* a = reinterpret_cast<const float4*>(g);
+        const float4* b = reinterpret_cast<const float4*>(g + half);
+        const float4 a0 = __ldcg(a), a1 = __ldcg(a + 1), b0 = __ldcg(b), b1 = __ldcg(b + 1);
+        gate[0] += a0.x, gate[1] += a0.y, gate[2] += a0.z, gate[3] += a0.w;
+        gate[4] += a1.x, gate[5] += a1.y, gate[6] += a1.z, gate[7] += a1.w;
+        value[0] += b0.x, value[1] += b0.y, value[2] += b0.z, value[3] += b0.w;
+        value[4] += b1.x, value[5] += b1.y, value[6] += b1.z, value[7] += b1.w;
+      }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      h[i] = k + i < p.I ? gate[i] / (1.f + expf(-gate[i])) * value[i] : 0.f;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if (UP)
+      unpack_bf16(x, v);
+    else
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = h[i];
+  }
+};
+
+// The columns of a run's segments, by the consumer warps: a warp a stage of 256
+// columns of K of one pair, 8 a lane, the next one's loads under way meanwhile.
+template <bool UP>
+__device__ void stage_columns(Cta& c, const Plan& plan, int run) {
+  const MoeParams& p = c.p;
+  const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
+  constexpr int TEAM = CONSUMERS / 32;
+  for (int s = 0; s < plan.segments; ++s) {
+    const Segment sg = plan.seg[s];
+    if (sg.run != run) continue;
+    uint8_t* scales = c.staged + sg.offset;
+    uint8_t* codes = scales + sg.kn * 1024;
+    const int rows = staged_rows(sg.count), tasks = sg.count * sg.kn;
+    Piece<UP> next;
+    auto fetch = [&](int t) {
+      const int col = t / sg.kn;
+      if (t < tasks)
+        next.load(c, c.r.list[sg.first + col], (sg.k0 + t - col * sg.kn) * 256 + c.lane * 8, vx);
+    };
+    int t = c.warp - 1;
+    fetch(t);
+#pragma unroll 1
+    for (; t < tasks; t += TEAM) {
+      const int col = t / sg.kn, stage = t - col * sg.kn;
+      float v[8];
+      next.get(v);
+      fetch(t + TEAM);
+      split_terms(v, codes + stage * rows * 128, scales + stage * 1024, col * TERMS, c.lane);
+    }
   }
 }
 
-template <int NT>
-__global__ void __launch_bounds__(THREADS, 1) moe_mxfp4_kernel(const MoeParams p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
-                                             ~static_cast<uintptr_t>(127));
-  __shared__ Routing r;
-  float* red = reinterpret_cast<float*>(smem + RING_BYTES);
-  uint8_t* staged = smem + RING_BYTES + WARPS * NT * 128 * 4;
-  if (threadIdx.x == 0) r.abort = 0;
-  route_start(p);
-  if (grid_barrier(p, r, 1)) {
-    route_choose(p, r);
-    Product<NT, true>(p, r, staged, smem, red).run();
-    __syncthreads();
-    // (fetches its first weights, then waits for every h)
-    Product<NT, false> down(p, r, staged, smem, red);
-    if (grid_barrier(p, r, 2)) {
-      down.run();
-      if (grid_barrier(p, r, 3)) combine(p);
+// The MMAs of a segment, by one warp.
+__device__ bool multiply(Cta& c, const MoeProduct& m, const Segment& sg) {
+  const int rows = staged_rows(sg.count);
+  const uint32_t id0 = make_idesc_mxf4(128, rows, 0), id2 = make_idesc_mxf4(128, rows, 2);
+  const uint32_t scales = desc_lo(smem_u32(c.staged) + sg.offset);
+  const uint32_t codes = scales + sg.kn * (1024 >> 4);
+  for (int t = 0; t < sg.items; ++t, ++c.ph_items) {
+    const uint32_t b = c.ph_items & 1u;
+    if (!c.wait(c.acc_empty(b), ((c.ph_items >> 1) & 1u) ^ 1u, kErrTimeoutMma)) return false;
+    tc_fence_after();
+    const uint32_t d = c.tmem + b * ACC_COLS;
+    for (int k = 0; k < sg.kn; ++k, ++c.it) {
+      const uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
+      // scales alternate between two sets of TMEM columns: the MMAs two stages
+      // back, which read this set last, have finished
+      if ((c.it >= 2 &&
+           !c.wait(c.empty_bar((c.it - 2) % STAGES), ((c.it - 2) / STAGES) & 1u, kErrTimeoutMma)) ||
+          !c.wait(c.full_bar(st), ph, kErrTimeoutMma))
+        return false;
+      tc_fence_after();
+      const uint32_t w = desc_lo(c.ring + st * RING_STAGE), cw = w + (W_BYTES >> 4);
+      const uint32_t x = codes + k * rows * (128 >> 4), cx = scales + k * (1024 >> 4);
+      const uint32_t sfw = c.tmem + SF_COL + (c.it & 1u) * 16, sfx = sfw + 8;
+      const int kb = sg.k0 + k;
+      const int tiles = min(2, m.kt - 2 * kb), mmas = min(4, (m.blocks - kb * 8 + 1) / 2);
+      if (elect_one()) {
+        for (int i = 0; i < tiles; ++i) {
+          copy_scale_tile<1>(sfw + 4 * i, cw + 32 * i);
+          copy_scale_tile<1>(sfx + 4 * i, cx + 32 * i);
+        }
+        for (int kk = 0; kk < mmas; ++kk)
+          mma_mxf4<1>(d, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
+                      sfx + 4 * (kk >> 1), k > 0 || kk > 0 ? 1u : 0u);
+        mma_commit(c.empty_bar(st));
+        if (k + 1 == sg.kn) mma_commit(c.acc_full(b));
+      }
+      __syncwarp();
     }
-    cp_async_wait<0>();
+  }
+  return true;
+}
+
+// A segment's sums out of TMEM: the terms of a column added, smallest first, one
+// matrix row a lane.  By four warps.
+template <bool UP>
+__device__ bool write_sums(Cta& c, const MoeProduct& m, const Segment& sg) {
+  const int q = c.warp & 3;
+  const int pairs = c.p.T * c.p.top;
+  const int64_t row0 = static_cast<int64_t>(sg.expert) * m.rows;
+  for (int t = 0; t < sg.items; ++t, ++c.ph_items) {
+    const uint32_t b = c.ph_items & 1u;
+    if (!c.wait(c.acc_full(b), (c.ph_items >> 1) & 1u, kErrTimeoutEpilogue)) return false;
+    tc_fence_after();
+    const uint32_t taddr = c.tmem + b * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
+    const int64_t row = static_cast<int64_t>(sg.tile + t) * 128 + q * 32 + c.lane - row0;
+    const bool in = row >= 0 && row < m.rows;
+    // up: gate rows, then up rows at half the pitch
+    const int at = static_cast<int>(UP && row >= c.p.I ? row - c.p.I + m.pitch / 2 : row);
+    float* sums = m.sums + static_cast<int64_t>(sg.part) * pairs * m.pitch + at;
+    for (int c0 = 0; c0 < sg.count; c0 += 4) {  // 4 columns: 24 TMEM columns
+      uint32_t v[3][8];
+#pragma unroll
+      for (int i = 0; i < 3; ++i) tmem_ld_8cols(taddr + c0 * TERMS + 8 * i, v[i]);
+      tmem_ld_wait();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float sum = 0.f;
+#pragma unroll
+        for (int i = TERMS - 1; i >= 0; --i)
+          sum += __uint_as_float(v[(j * TERMS + i) / 8][(j * TERMS + i) % 8]);
+        if (in && c0 + j < sg.count)
+          sums[static_cast<int64_t>(c.r.list[sg.first + c0 + j]) * m.pitch] = sum;
+      }
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (c.lane == 0) mbar_arrive(c.acc_empty(b));
+  }
+  return true;
+}
+
+// Steps 3 and 4, by the consumer warps.
+template <bool UP>
+__device__ void product(Cta& c, const MoeProduct& m, const Plan& plan) {
+  const int runs = plan.segments ? plan.seg[plan.segments - 1].run + 1 : 0;
+  int s = 0;
+  for (int run = 0; run < runs; ++run) {
+    if (run) consumers_sync();  // the columns staged before have been read
+    if (!*c.abort_flag) stage_columns<UP>(c, plan, run);
+    fence_proxy_async_smem();
+    consumers_sync();
+    bool ok = !*c.abort_flag;
+    for (; s < plan.segments && plan.seg[s].run == run; ++s) {
+      if (!ok) continue;
+      if (c.warp == 1) {
+        ok = multiply(c, m, plan.seg[s]);
+      } else if (c.warp >= 4 && c.warp < 8) {
+        ok = write_sums<UP>(c, m, plan.seg[s]);
+      }
+    }
+    // The MMA warp waits for its own, which read the staged columns.
+    if (c.warp == 1 && ok && c.it > 0)
+      c.wait(c.empty_bar((c.it - 1) % STAGES), ((c.it - 1) / STAGES) & 1u, kErrTimeoutMma);
+  }
+}
+
+// Step 5, the consumers of the grid: a token's pairs added in their order,
+// four rows a thread.
+__device__ void combine(const Cta& c) {
+  const MoeParams& p = c.p;
+  const int quads = (p.H + 3) / 4, n = p.T * quads;
+  const int64_t part = static_cast<int64_t>(p.T) * p.top * p.down.pitch;
+  for (int i = blockIdx.x * CONSUMERS + threadIdx.x - 32; i < n; i += gridDim.x * CONSUMERS) {
+    const int t = i / quads, row = (i - t * quads) * 4;
+    const float* src = p.down.sums + static_cast<int64_t>(t) * p.top * p.down.pitch + row;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+    for (int k = 0; k < p.top; ++k, src += p.down.pitch) {
+      const float w = c.r.weight[t * p.top + k];
+      float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      for (int q = 1; q < c.r.down.parts; ++q) {
+        const float4 o = __ldcg(reinterpret_cast<const float4*>(src + q * part));
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+      }
+      sum[0] = fmaf(w, v.x, sum[0]);
+      sum[1] = fmaf(w, v.y, sum[1]);
+      sum[2] = fmaf(w, v.z, sum[2]);
+      sum[3] = fmaf(w, v.w, sum[3]);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (row + j < p.H) p.y[t * p.ldy + row + j] = __float2bfloat16_rn(sum[j]);
+  }
+}
+
+__global__ void __launch_bounds__(THREADS, 1)
+    moe_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_up,
+                     const __grid_constant__ CUtensorMap tm_down, const MoeParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Routing r;
+  __shared__ alignas(8) uint64_t bars[2 * STAGES + 4];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Cta c{p, r, &abort_flag, smem + RING_BYTES, smem_u32(smem), smem_u32(bars), 0,
+        static_cast<int>(threadIdx.x >> 5), static_cast<int>(threadIdx.x & 31), 0, 0};
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(c.full_bar(s), 1);
+      mbar_init(c.empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(c.acc_full(b), 1);
+      mbar_init(c.acc_empty(b), 4);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&tm_up);
+    tma_prefetch_desc(&tm_down);
+  }
+  if (c.warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  route_start(p);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  c.tmem = tmem_slot;
+  if (c.warp) grid_barrier(c, 1);
+  __syncthreads();
+  if (!abort_flag) {
+    route_choose(p, r);
+    if (c.warp == 0) plan_product(p, p.up, r, r.up);
+    if (c.warp == 1) plan_product(p, p.down, r, r.down);
+  } else if (threadIdx.x == 0) {
+    r.up.segments = r.down.segments = 0;
+  }
+  __syncthreads();
+  if (c.warp == 0) {
+    // The producer runs ahead through both products: weights wait for nothing
+    // but their place in the ring.
+    if (c.lane == 0) {
+      if (produce(c, &tm_up, p.up, r.up)) produce(c, &tm_down, p.down, r.down);
+      volatile int never = 0;  // its copies in flight have landed before it leaves
+      for (uint32_t i = c.it > STAGES ? c.it - STAGES : 0; i < c.it; ++i)
+        if (!mbar_wait_bounded(c.full_bar(i % STAGES), (i / STAGES) & 1u, p.wait_limit_ns, &never))
+          atomicOr(p.status, kErrTimeoutDrain);
+    }
+    __syncwarp();
+  } else {
+    product<true>(c, p.up, r.up);
+    grid_barrier(c, 2);
+    product<false>(c, p.down, r.down);
+    grid_barrier(c, 3);
+    if (!abort_flag) combine(c);
+    if (c.warp == 1 && c.it > 0) {  // the last MMAs issued have finished
+      volatile int never = 0;
+      if (!mbar_wait_bounded(c.empty_bar((c.it - 1) % STAGES), ((c.it - 1) / STAGES) & 1u,
+                             p.wait_limit_ns, &never) && c.lane == 0)
+        atomicOr(p.status, kErrTimeoutDrain);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (c.warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(c.tmem, TMEM_COLS);
   }
   // The last CTA to leave clears the counters for the next call.
-  __syncthreads();
   if (threadIdx.x == 0) {
     __threadfence();
     if (atomicAdd(p.control + 1, 1u) == gridDim.x - 1) p.control[0] = p.control[1] = 0;
   }
 }
 
-template <int NT>
-cudaError_t launch_t(MoeParams p, const DeviceCtl& ctl, cudaStream_t s) {
-  constexpr int kSmem = 227 * 1024 - static_cast<int>(sizeof(Routing)) - 256;
-  constexpr int kFixed = 128 + RING_BYTES + WARPS * NT * 128 * 4;
-  auto kern = moe_mxfp4_kernel<NT>;
-  const int pitch = (p.kt_h > p.kt_i ? p.kt_h : p.kt_i) * 256 + 64;
-  p.stage_bytes = (kSmem - kFixed) / 16 * 16;
-  if (p.stage_bytes < pitch) return cudaErrorInvalidValue;
-  const int smem = kFixed + p.stage_bytes;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctl.sm_count);
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  note_main_kernel("moe_mxfp4_kernel", ctl.sm_count, p.T * p.top);
-  e = cudaLaunchKernelEx(&cfg, kern, p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+int max_parts(int64_t pairs) {  // of K: the partial sums' memory
+  const int64_t n = 2048 / pairs;
+  return static_cast<int>(n < 2 ? 2 : n > 16 ? 16 : n);
 }
+int64_t up_pitch(int64_t I) { return 2 * ((I + 7) / 8 * 8); }
+int64_t down_pitch(int64_t H) { return (H + 3) / 4 * 4; }
 
 }  // namespace
 
-size_t moe_workspace(const MoeArgs& a, size_t (&at)[5]) {
-  const size_t pairs = static_cast<size_t>(a.T) * a.top;
+size_t moe_workspace(const MoeArgs& a, size_t (&at)[3]) {
+  const int64_t pairs = a.T * a.top;
   size_t n = 0;
-  auto take = [&](size_t bytes) {
+  auto take = [&](int64_t floats) {
     const size_t here = n;
-    n += (bytes + 255) / 256 * 256;
+    n += (static_cast<size_t>(floats) * 4 + 255) / 256 * 256;
     return here;
   };
-  at[0] = take(static_cast<size_t>(a.T) * a.E * 4);
-  at[1] = take(static_cast<size_t>(a.T) * 4);
-  at[2] = take(pairs * 4);
-  at[3] = take(pairs * scale_tiles(a.I) * 128 * 4);
-  at[4] = take(pairs * a.H * 4);
+  at[0] = take(a.T * a.E);
+  at[1] = take(max_parts(pairs) * pairs * up_pitch(a.I));
+  at[2] = take(max_parts(pairs) * pairs * down_pitch(a.H));
   return n;
 }
 
@@ -788,12 +806,6 @@ cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, con
   p.router = static_cast<const __nv_bfloat16*>(a.router);
   p.ldx = a.ldx;
   p.ldr = a.ldr;
-  p.up = a.up;
-  p.up_s = a.up_scales;
-  p.down = a.down;
-  p.down_s = a.down_scales;
-  p.ldu = a.ldu;
-  p.ldd = a.ldd;
   p.y = static_cast<__nv_bfloat16*>(a.y);
   p.ldy = a.ldy;
   p.experts = a.experts;
@@ -803,23 +815,54 @@ cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, con
   p.top = static_cast<int32_t>(a.top);
   p.H = static_cast<int32_t>(a.H);
   p.I = static_cast<int32_t>(a.I);
-  p.kt_h = static_cast<int32_t>(scale_tiles(a.H));
-  p.kt_i = static_cast<int32_t>(scale_tiles(a.I));
-  size_t at[5];
+  p.max_parts = max_parts(a.T * a.top);
+  size_t at[3];
   moe_workspace(a, at);
   char* ws = static_cast<char*>(workspace);
+  auto product_of = [&](const uint8_t* scales, int64_t rows, int64_t K, size_t sums, int64_t pitch) {
+    MoeProduct m;
+    m.scales = scales;
+    m.rows = static_cast<int32_t>(rows);
+    // an expert's rows may start anywhere in a tile, unless they are whole tiles
+    m.tiles = static_cast<int32_t>(rows % 128 == 0 ? rows / 128 : (rows - 1 + 127) / 128 + 1);
+    m.blocks = static_cast<int32_t>(blocks_of(K));
+    m.kt = static_cast<int32_t>(scale_tiles(K));
+    m.stages = (m.kt + 1) / 2;
+    m.sums = reinterpret_cast<float*>(ws + sums);
+    m.pitch = static_cast<int32_t>(pitch);
+    return m;
+  };
+  p.up = product_of(a.up_scales, 2 * a.I, a.H, at[1], up_pitch(a.I));
+  p.down = product_of(a.down_scales, a.H, a.I, at[2], down_pitch(a.H));
   p.logits = reinterpret_cast<float*>(ws + at[0]);
-  p.x_mult = reinterpret_cast<float*>(ws + at[1]);
-  p.h_max = reinterpret_cast<uint32_t*>(ws + at[2]);
-  p.h = reinterpret_cast<float*>(ws + at[3]);
-  p.part = reinterpret_cast<float*>(ws + at[4]);
   p.control = control;
   p.status = ctl.status;
   p.wait_limit_ns = ctl.wait_limit_ns;
   p.inject_stall = ctl.inject_stall;
-  // an expert has at most T columns, and rarely more than 16: one or two tiles
-  // of 8 at a time
-  return a.T <= 8 ? launch_t<1>(p, ctl, s) : launch_t<2>(p, ctl, s);
+  CUtensorMap up, down;
+  if (encode_tmap_2d(&up, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.up, p.up.blocks * 16, 2 * a.E * a.I,
+                     a.ldu, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      encode_tmap_2d(&down, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.down, p.down.blocks * 16, a.E * a.H,
+                     a.ldd, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  constexpr int kSmem = 227 * 1024 - static_cast<int>(sizeof(Routing)) - 512;
+  p.stage_bytes = (kSmem - 1024 - RING_BYTES) / 1024 * 1024;
+  cudaError_t e = cudaFuncSetAttribute(moe_mxfp4_kernel,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctl.sm_count);
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_main_kernel("moe_mxfp4_kernel", ctl.sm_count, p.T * p.top);
+  e = cudaLaunchKernelEx(&cfg, moe_mxfp4_kernel, up, down, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace mx
