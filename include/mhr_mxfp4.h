@@ -72,8 +72,9 @@ int gemm_mxfp4(int c_dtype, const uint8_t* A, const uint8_t* A_scales, const uin
 /*
  * The same with A (M x K, row-major, pitch lda elements, type a_dtype)
  * quantised on the way as gemm_mxfp4_quantize does along its rows: the C of
- * quantising and then multiplying, bit for bit.  The packed A lives in the
- * library's workspace (see mhr_gemm.h).
+ * quantising and then multiplying, bit for bit.  Few rows are quantised inside
+ * the product's kernel; the packed A of more lives in the library's workspace
+ * (see mhr_gemm.h).
  */
 int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const uint8_t* Bt,
                          const uint8_t* Bt_scales, void* C, int64_t M, int64_t N, int64_t K,

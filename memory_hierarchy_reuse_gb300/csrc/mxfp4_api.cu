@@ -146,6 +146,12 @@ MHR_API int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const 
   if (const int st = device_ctl_locked(&ctl, &dev); st != MHR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0) return from_cuda(zero_c(c_dtype, C, M, N, ldc, s));
+  if (ctl.pair_mode != 2 && narrow_quantizes(M, N, K, ctl.sm_count)) {
+    ProductArgs a{nullptr, nullptr, lda, Bt, Bt_scales, ldb, C, ldc, c_dtype, M, N, K};
+    a.a_plain = A;
+    a.a_dtype = a_dtype;
+    return from_cuda(launch_product(a, ctl, s));
+  }
   const int64_t row_bytes = blocks_of(K) * 16;
   size_t data_bytes;
   if (__builtin_mul_overflow(static_cast<size_t>(M), static_cast<size_t>(row_bytes), &data_bytes))
@@ -197,7 +203,7 @@ MHR_API int gemm_mxfp4_moe(const uint16_t* x, int64_t ldx, const uint16_t* route
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const MoeArgs a{x,    ldx,         router, ldr, up, up_scales, ldu, down,
                   down_scales, ldd,  y,      ldy, experts, weights, T, E, top, H, I};
-  size_t at[3];
+  size_t at[5];
   void *ws, *token, *control;
   if (const int st = workspace_locked(dev, s, moe_workspace(a, at), &ws, &token); st != MHR_OK)
     return st;

@@ -41,8 +41,15 @@ struct ProductArgs {
   int64_t M, N, K;
   // A was quantised by a kernel of the same call just before, itself launched
   // in plain stream order: B is complete once this kernel starts.
-  bool after_quantize;
+  bool after_quantize = false;
+  // launch_narrow only, where narrow_quantizes: A as a plain matrix (pitch lda
+  // elements) instead of packed.
+  const void* a_plain = nullptr;
+  int a_dtype = 0;
 };
+// Whether launch_narrow takes a plain A and quantises it on the way: at most
+// 32 rows whose part of K fits beside the ring.
+bool narrow_quantizes(int64_t M, int64_t N, int64_t K, int sms);
 // Few rows of A (any M is right).
 cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s);
 // Many rows of A: CTA pairs on 256 x 256 tiles (any M is right).
@@ -68,8 +75,8 @@ struct MoeArgs {
   float* weights;
   int64_t T, E, top, H, I;
 };
-// Bytes of workspace, and where its three parts start.
-size_t moe_workspace(const MoeArgs& a, size_t (&at)[3]);
+// Bytes of workspace, and where its five parts start.
+size_t moe_workspace(const MoeArgs& a, size_t (&at)[5]);
 cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, const DeviceCtl& ctl,
                        cudaStream_t s);
 

@@ -8,7 +8,7 @@
 // Bound by HBM: the chosen experts' weights pass once, 17/32 byte each, with a
 // few multiply-adds a weight (as many as tokens chose the expert); the
 // smallest calls by the latency of the dependent steps.  So one persistent
-// cooperative grid, a CTA an SM, walks routing, the up product, the down
+// cooperative grid, a CTA an SM, walks logits, the up product, h, the down
 // product and the sum, with a grid barrier between each.
 //
 // The product.  Weights are the 128-row side of tcgen05.mma kind::mxf4 as they
@@ -45,10 +45,11 @@ constexpr int TERMS = 6;                       // e2m1 columns a bf16 or fp32 co
 constexpr int MAX_COLS = 128 / TERMS;          // columns an MMA takes at once: N <= 128
 constexpr int W_BYTES = 128 * 128;             // 128 rows x 256 columns of weights
 constexpr int RING_STAGE = W_BYTES + 1024;     // and their scales
-constexpr int STAGES = 4;
+constexpr int STAGES = 6;
 constexpr int RING_BYTES = STAGES * RING_STAGE;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MAX_SEGMENTS = 160;
+constexpr int PIECE = TERMS * (128 + 8);       // 256 columns of K as terms: codes, then scales
 constexpr uint32_t ACC_COLS = 128;             // TMEM: two accumulators, two sets of scales
 constexpr uint32_t SF_COL = 2 * ACC_COLS;
 constexpr uint32_t TMEM_COLS = 512;
@@ -78,6 +79,8 @@ struct MoeParams {
   int32_t max_parts;       // of K
   // workspace
   float* logits;           // T x E
+  uint8_t* x_terms;        // T x up.stages pieces
+  uint8_t* h_terms;        // T * top x down.stages pieces
   uint32_t* control;       // [0] barrier arrivals, [1] exits
   int32_t stage_bytes;     // shared memory for staged columns
   uint32_t* status;
@@ -108,7 +111,7 @@ struct Routing {  // shared memory
   int32_t count[MOE_MAX_EXPERTS];    // pairs of an expert (while they are counted)
   int16_t offset[MOE_MAX_EXPERTS];   // its first place in list
   int16_t active[MOE_MAX_EXPERTS];   // the experts that some pair has
-  int32_t num_active;
+  int32_t num_active, most;          // and the most pairs that one has
   Plan up, down;
 };
 
@@ -180,71 +183,121 @@ __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, b
   }
 }
 
-// Step 1, all warps of the grid.
+// 256 columns of K, 8 a lane, as TERMS rows of e2m1 codes and their scales:
+// row j is 128 bytes from 128 j on, its 8 scales follow all rows.
+__device__ __forceinline__ void split_terms(float (&v)[8], uint8_t* piece, int lane) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+  // the least power of two that is not below max / 6 = max / (1.5 * 4)
+  const bool finite = amax < 0x7f800000u;
+  int c = static_cast<int>(amax >> 23) - 2 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0);
+#pragma unroll 1
+  for (int j = 0; j < TERMS; ++j) {
+    // below 2^-126: nothing that an fp32 sum would see; a block with an
+    // infinity or a NaN: NaN
+    const bool some = c >= 1 && finite;
+    const float inv = __uint_as_float(some ? static_cast<uint32_t>(254 - c) << 23 : 0u);
+    const float scale = __uint_as_float(some ? static_cast<uint32_t>(c) << 23 : 0u);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
+    const uint32_t word = some ? e2m1x8(y) : 0u;
+    reinterpret_cast<uint32_t*>(piece)[j * 32 + lane] = word;
+    if ((lane & 3) == 0)
+      piece[TERMS * 128 + j * 8 + (lane >> 2)] = static_cast<uint8_t>(!finite ? 255 : some ? c : 0);
+    const uint32_t h[4] = {e2m1_to_f16x2<0>(word), e2m1_to_f16x2<1>(word), e2m1_to_f16x2<2>(word),
+                           e2m1_to_f16x2<3>(word)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // the rest: exact
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
+      v[2 * i] = fmaf(-f.x, scale, v[2 * i]);
+      v[2 * i + 1] = fmaf(-f.y, scale, v[2 * i + 1]);
+    }
+    c -= j == 0 ? 2 : 3;
+  }
+}
+
+// Step 1, all warps of the grid: x as terms, and the logits.
 __device__ void route_start(const MoeParams& p) {
   const int warp = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbours on other SMs
   const int warps = gridDim.x * WARPS;
   const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
   const bool vr = reinterpret_cast<uintptr_t>(p.router) % 16 == 0 && p.ldr % 8 == 0;
+  const int lane = threadIdx.x & 31;
+  for (int i = warps - 1 - warp; i < p.T * p.up.stages; i += warps) {  // the warps with fewest logits
+    const int t = i / p.up.stages, k = (i - t * p.up.stages) * 256 + lane * 8;
+    uint4 x[1];
+    load_row<1>(p.x + t * p.ldx, k, p.H, vx, x);
+    float v[8];
+    unpack_bf16(x[0], v);
+    split_terms(v, p.x_terms + static_cast<int64_t>(i) * PIECE, lane);
+  }
   if (p.E * p.T <= warps)
     route_logits<1>(p, warp, warps, vx, vr);
   else
     route_logits<4>(p, warp, warps, vx, vr);
 }
 
-// The chosen experts of a warp's tokens and their weights; PER_LANE x 32
-// experts at most.  Logits become unsigned keys of the same order (a NaN
-// largest, -0 and 0 alike), 0 for one taken or none.
-template <int PER_LANE>
+// The chosen experts of a warp's tokens, NT at a time (their chains of reductions
+// side by side), and their weights; PER_LANE x 32 experts at most.  Logits become
+// unsigned keys of the same order (a NaN largest, -0 and 0 alike), 0 for one
+// taken or none.
+template <int PER_LANE, int NT>
 __device__ void choose_tokens(const MoeParams& p, Routing& r) {
   const int lane = threadIdx.x & 31;
-  float next[PER_LANE];
-  auto load = [&](int t) {
-#pragma unroll
-    for (int i = 0; i < PER_LANE; ++i)
-      next[i] = t < p.T && lane + 32 * i < p.E ? __ldcg(p.logits + t * p.E + lane + 32 * i) : 0.f;
-  };
-  int t = threadIdx.x >> 5;
-  load(t);
 #pragma unroll 1
-  for (; t < p.T; t += WARPS) {
-    uint32_t key[PER_LANE];
+  for (int t0 = threadIdx.x >> 5; t0 < p.T; t0 += WARPS * NT) {
+    uint32_t key[NT][PER_LANE];
 #pragma unroll
-    for (int i = 0; i < PER_LANE; ++i) {
-      const float v = next[i] + 0.f;
-      const uint32_t b = __float_as_uint(v);
-      key[i] = lane + 32 * i >= p.E ? 0u : v != v ? 0xffffffffu : b >> 31 ? ~b : b | 0x80000000u;
+    for (int j = 0; j < NT; ++j) {
+      const int t = min(t0 + j * WARPS, p.T - 1);  // (past the end: the last, again)
+#pragma unroll
+      for (int i = 0; i < PER_LANE; ++i) {
+        const int e = lane + 32 * i;
+        const float v = e < p.E ? __ldcg(p.logits + t * p.E + e) + 0.f : 0.f;
+        const uint32_t b = __float_as_uint(v);
+        key[j][i] = e >= p.E ? 0u : v != v ? 0xffffffffu : b >> 31 ? ~b : b | 0x80000000u;
+      }
     }
-    load(t + WARPS);
-    uint32_t chosen = 0, first = 0;
+    uint32_t chosen[NT], first[NT];
 #pragma unroll 1
     for (int k = 0; k < p.top; ++k) {
-      uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < PER_LANE; ++i) m = max(m, key[i]);
-      m = __reduce_max_sync(0xffffffffu, m);
-      uint32_t e = 0xffffffffu;
+      for (int j = 0; j < NT; ++j) {
+        uint32_t m = 0;
 #pragma unroll
-      for (int i = PER_LANE - 1; i >= 0; --i)
-        if (key[i] == m) e = lane + 32 * i;
-      e = __reduce_min_sync(0xffffffffu, e);
+        for (int i = 0; i < PER_LANE; ++i) m = max(m, key[j][i]);
+        m = __reduce_max_sync(0xffffffffu, m);
+        uint32_t e = 0xffffffffu;
 #pragma unroll
-      for (int i = 0; i < PER_LANE; ++i)
-        if (e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
-      if (k == 0) first = m;
-      if (lane == k) {
-        chosen = m;
-        r.expert[t * p.top + k] = static_cast<int16_t>(e);
+        for (int i = PER_LANE - 1; i >= 0; --i)
+          if (key[j][i] == m) e = lane + 32 * i;
+        e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+        for (int i = 0; i < PER_LANE; ++i)
+          if (e == static_cast<uint32_t>(lane + 32 * i)) key[j][i] = 0;
+        if (k == 0) first[j] = m;
+        if (lane == k) {
+          chosen[j] = m;
+          if (t0 + j * WARPS < p.T)
+            r.expert[(t0 + j * WARPS) * p.top + k] = static_cast<int16_t>(e);
+        }
       }
     }
     auto logit = [](uint32_t key) {
       return __uint_as_float(key == 0xffffffffu ? key : key >> 31 ? key & 0x7fffffffu : ~key);
     };
-    const float w = lane < p.top ? expf(logit(chosen) - logit(first)) : 0.f;
-    float sum = w;
 #pragma unroll
-    for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (lane < p.top) r.weight[t * p.top + lane] = w / sum;
+    for (int j = 0; j < NT; ++j) {
+      const float w = lane < p.top ? expf(logit(chosen[j]) - logit(first[j])) : 0.f;
+      float sum = w;
+#pragma unroll
+      for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      if (lane < p.top && t0 + j * WARPS < p.T) r.weight[(t0 + j * WARPS) * p.top + lane] = w / sum;
+    }
   }
 }
 
@@ -252,17 +305,19 @@ __device__ void choose_tokens(const MoeParams& p, Routing& r) {
 // index, their weights, and the pairs sorted by expert.
 __device__ void route_choose(const MoeParams& p, Routing& r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (p.E <= 128)
-    choose_tokens<4>(p, r);
+  if (p.E > 128)
+    choose_tokens<MOE_MAX_EXPERTS / 32, 1>(p, r);
+  else if (p.T > WARPS)
+    choose_tokens<4, 4>(p, r);
   else
-    choose_tokens<MOE_MAX_EXPERTS / 32>(p, r);
+    choose_tokens<4, 1>(p, r);
   const int pairs = p.T * p.top;
   for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[e] = 0;
   __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += THREADS) atomicAdd(&r.count[r.expert[i]], 1);
   __syncthreads();
   if (warp == 0) {
-    int active = 0, offset = 0;
+    int active = 0, offset = 0, most = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
       const int c = e0 + lane < p.E ? r.count[e0 + lane] : 0;
       const uint32_t has = __ballot_sync(0xffffffffu, c > 0);
@@ -276,9 +331,14 @@ __device__ void route_choose(const MoeParams& p, Routing& r) {
       if (c > 0)
         r.active[active + __popc(has & ((1u << lane) - 1))] = static_cast<int16_t>(e0 + lane);
       active += __popc(has);
+      most = max(most, c);
       offset += __shfl_sync(0xffffffffu, scan, 31);
     }
-    if (lane == 0) r.num_active = active;
+    most = __reduce_max_sync(0xffffffffu, most);
+    if (lane == 0) {
+      r.num_active = active;
+      r.most = most;
+    }
   }
   __syncthreads();
   for (int i = threadIdx.x; i < pairs; i += THREADS) {
@@ -311,9 +371,7 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
   auto end_of = [&](int ai) {
     return ai + 1 < active ? static_cast<int>(r.offset[r.active[ai + 1]]) : pairs;
   };
-  int most = 0;  // pairs of the busiest expert
-  for (int a = lane; a < active; a += 32) most = max(most, end_of(a) - r.offset[r.active[a]]);
-  most = min(__reduce_max_sync(0xffffffffu, most), MAX_COLS);
+  const int most = min(r.most, MAX_COLS);
   // Time of the longest run, in stages, with half a stage for an item's ends;
   // parts that are too long to stage all columns at once count twice.
   const int parts = lane + 1;
@@ -368,48 +426,6 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
     }
     plan.segments = n;
     plan.parts = chosen;
-  }
-}
-
-// 8 columns as TERMS rows of e2m1 codes, and their scales (of the block of 32
-// that four neighbouring lanes hold), into a stage of `rows` rows: row n is 128
-// bytes, its 16-byte pieces (a block each) swizzled by n % 8.
-__device__ __forceinline__ void split_terms(float (&v)[8], uint8_t* codes, uint8_t* scales, int n,
-                                            int lane) {
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-  // the least power of two that is not below max / 6 = max / (1.5 * 4)
-  const bool finite = amax < 0x7f800000u;
-  int c = static_cast<int>(amax >> 23) - 2 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0);
-  const int block = lane >> 2;
-  scales += (block >> 2) * 512 + (block & 3);
-  codes += (lane & 3) * 4;
-#pragma unroll 1
-  for (int j = 0; j < TERMS; ++j, ++n) {
-    // below 2^-126: nothing that an fp32 sum would see; a block with an
-    // infinity or a NaN: NaN
-    const bool some = c >= 1 && finite;
-    const float inv = __uint_as_float(some ? static_cast<uint32_t>(254 - c) << 23 : 0u);
-    const float scale = __uint_as_float(some ? static_cast<uint32_t>(c) << 23 : 0u);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
-    const uint32_t word = some ? e2m1x8(y) : 0u;
-    *reinterpret_cast<uint32_t*>(codes + n * 128 + ((block ^ (n & 7)) << 4)) = word;
-    if ((lane & 3) == 0)
-      scales[(n & 31) * 16 + (n >> 5) * 4] = static_cast<uint8_t>(!finite ? 255 : some ? c : 0);
-    const uint32_t h[4] = {e2m1_to_f16x2<0>(word), e2m1_to_f16x2<1>(word), e2m1_to_f16x2<2>(word),
-                           e2m1_to_f16x2<3>(word)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {  // the rest: exact
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-      v[2 * i] = fmaf(-f.x, scale, v[2 * i]);
-      v[2 * i + 1] = fmaf(-f.y, scale, v[2 * i + 1]);
-    }
-    c -= j == 0 ? 2 : 3;
   }
 }
 
@@ -487,25 +503,63 @@ __device__ bool produce(Cta& c, const CUtensorMap* map, const MoeProduct& m, con
   return true;
 }
 
-// 8 columns of K of a pair: x as loaded, or h from the parts' sums.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// The columns of a run's segments into shared memory, by the consumer warps, all
+// copies under way at once: of each pair and stage of 256 columns of K, TERMS
+// rows of 8 pieces of 16 bytes (row n's swizzled by n % 8), and their scales as
+// words of 4 into the tiles that tcgen05.cp takes.
 template <bool UP>
-struct Piece {
-  uint4 x;
-  float h[8];
-  __device__ __forceinline__ void load(const Cta& c, int pair, int k, bool vx) {
-    const MoeParams& p = c.p;
-    if (UP) {
-      load_row<1>(p.x + (pair / p.top) * p.ldx, k, p.H, vx, *reinterpret_cast<uint4(*)[1]>(&x));
-      return;
+__device__ void stage_columns(Cta& c, const MoeProduct& m, const Plan& plan, int run) {
+  const MoeParams& p = c.p;
+  constexpr int COPIES = TERMS * 10, STRIDE = 64;  // 8 pieces and 2 words a row
+  for (int s = 0; s < plan.segments; ++s) {
+    const Segment sg = plan.seg[s];
+    if (sg.run != run) continue;
+    const uint32_t scales = smem_u32(c.staged) + sg.offset, codes = scales + sg.kn * 1024;
+    const int rows = staged_rows(sg.count);
+    for (int i = threadIdx.x - 32; i < sg.count * sg.kn * STRIDE; i += CONSUMERS) {
+      const int task = i / STRIDE, copy = i % STRIDE;
+      if (copy >= COPIES) continue;
+      const int col = task / sg.kn, stage = task - col * sg.kn;
+      const int pair = c.r.list[sg.first + col];
+      const uint8_t* src =
+          UP ? p.x_terms + (static_cast<int64_t>(pair / p.top) * m.stages + sg.k0 + stage) * PIECE
+             : p.h_terms + (static_cast<int64_t>(pair) * m.stages + sg.k0 + stage) * PIECE;
+      if (copy < TERMS * 8) {
+        const int n = col * TERMS + (copy >> 3), block = copy & 7;
+        cp_async_16(codes + (stage * rows + n) * 128 + ((block ^ (n & 7)) << 4), src + copy * 16);
+      } else {
+        const int w = copy - TERMS * 8, n = col * TERMS + (w >> 1);
+        cp_async_4(scales + stage * 1024 + (w & 1) * 512 + (n & 31) * 16 + (n >> 5) * 4,
+                   src + TERMS * 128 + w * 4);
+      }
     }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Step 3b, the consumers of the grid: h of every pair as terms, from the parts'
+// sums of gate and up in their order.
+__device__ void make_h(const Cta& c) {
+  const MoeParams& p = c.p;
+  const int64_t part = static_cast<int64_t>(p.T) * p.top * p.up.pitch;
+  const int half = p.up.pitch / 2, tasks = p.T * p.top * p.down.stages;
+  const int team = gridDim.x * (CONSUMERS / 32);
+  for (int i = (c.warp - 1) * gridDim.x + blockIdx.x; i < tasks; i += team) {
+    const int pair = i / p.down.stages, k = (i - pair * p.down.stages) * 256 + c.lane * 8;
     const float* g = p.up.sums + static_cast<int64_t>(pair) * p.up.pitch + k;
-    const int half = p.up.pitch / 2;
-    const int64_t parts = static_cast<int64_t>(p.T) * p.top * p.up.pitch;
     float gate[8], value[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) gate[i] = value[i] = 0.f;
+    for (int j = 0; j < 8; ++j) gate[j] = value[j] = 0.f;
     if (k < p.I)
-      for (int q = 0; q < c.r.up.parts; ++q, g += parts) {
+#pragma unroll 2
+      for (int q = 0; q < c.r.up.parts; ++q, g += part) {
         const float4* a = reinterpret_cast<const float4*>(g);
         const float4* b = reinterpret_cast<const float4*>(g + half);
         const float4 a0 = __ldcg(a), a1 = __ldcg(a + 1), b0 = __ldcg(b), b1 = __ldcg(b + 1);
@@ -514,48 +568,11 @@ struct Piece {
         value[0] += b0.x, value[1] += b0.y, value[2] += b0.z, value[3] += b0.w;
         value[4] += b1.x, value[5] += b1.y, value[6] += b1.z, value[7] += b1.w;
       }
+    float h[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      h[i] = k + i < p.I ? gate[i] / (1.f + expf(-gate[i])) * value[i] : 0.f;
-  }
-  __device__ __forceinline__ void get(float (&v)[8]) const {
-    if (UP)
-      unpack_bf16(x, v);
-    else
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = h[i];
-  }
-};
-
-// The columns of a run's segments, by the consumer warps: a warp a stage of 256
-// columns of K of one pair, 8 a lane, the next one's loads under way meanwhile.
-template <bool UP>
-__device__ void stage_columns(Cta& c, const Plan& plan, int run) {
-  const MoeParams& p = c.p;
-  const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
-  constexpr int TEAM = CONSUMERS / 32;
-  for (int s = 0; s < plan.segments; ++s) {
-    const Segment sg = plan.seg[s];
-    if (sg.run != run) continue;
-    uint8_t* scales = c.staged + sg.offset;
-    uint8_t* codes = scales + sg.kn * 1024;
-    const int rows = staged_rows(sg.count), tasks = sg.count * sg.kn;
-    Piece<UP> next;
-    auto fetch = [&](int t) {
-      const int col = t / sg.kn;
-      if (t < tasks)
-        next.load(c, c.r.list[sg.first + col], (sg.k0 + t - col * sg.kn) * 256 + c.lane * 8, vx);
-    };
-    int t = c.warp - 1;
-    fetch(t);
-#pragma unroll 1
-    for (; t < tasks; t += TEAM) {
-      const int col = t / sg.kn, stage = t - col * sg.kn;
-      float v[8];
-      next.get(v);
-      fetch(t + TEAM);
-      split_terms(v, codes + stage * rows * 128, scales + stage * 1024, col * TERMS, c.lane);
-    }
+    for (int j = 0; j < 8; ++j)
+      h[j] = k + j < p.I ? gate[j] / (1.f + expf(-gate[j])) * value[j] : 0.f;
+    split_terms(h, p.h_terms + static_cast<int64_t>(i) * PIECE, c.lane);
   }
 }
 
@@ -647,7 +664,7 @@ __device__ void product(Cta& c, const MoeProduct& m, const Plan& plan) {
   int s = 0;
   for (int run = 0; run < runs; ++run) {
     if (run) consumers_sync();  // the columns staged before have been read
-    if (!*c.abort_flag) stage_columns<UP>(c, plan, run);
+    if (!*c.abort_flag) stage_columns<UP>(c, m, plan, run);
     fence_proxy_async_smem();
     consumers_sync();
     bool ok = !*c.abort_flag;
@@ -753,8 +770,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     product<true>(c, p.up, r.up);
     grid_barrier(c, 2);
-    product<false>(c, p.down, r.down);
+    if (!abort_flag) make_h(c);
     grid_barrier(c, 3);
+    product<false>(c, p.down, r.down);
+    grid_barrier(c, 4);
     if (!abort_flag) combine(c);
     if (c.warp == 1 && c.it > 0) {  // the last MMAs issued have finished
       volatile int never = 0;
@@ -785,17 +804,19 @@ int64_t down_pitch(int64_t H) { return (H + 3) / 4 * 4; }
 
 }  // namespace
 
-size_t moe_workspace(const MoeArgs& a, size_t (&at)[3]) {
+size_t moe_workspace(const MoeArgs& a, size_t (&at)[5]) {
   const int64_t pairs = a.T * a.top;
   size_t n = 0;
-  auto take = [&](int64_t floats) {
+  auto take = [&](int64_t bytes) {
     const size_t here = n;
-    n += (static_cast<size_t>(floats) * 4 + 255) / 256 * 256;
+    n += (static_cast<size_t>(bytes) + 255) / 256 * 256;
     return here;
   };
-  at[0] = take(a.T * a.E);
-  at[1] = take(max_parts(pairs) * pairs * up_pitch(a.I));
-  at[2] = take(max_parts(pairs) * pairs * down_pitch(a.H));
+  at[0] = take(a.T * a.E * 4);
+  at[1] = take(max_parts(pairs) * pairs * up_pitch(a.I) * 4);
+  at[2] = take(max_parts(pairs) * pairs * down_pitch(a.H) * 4);
+  at[3] = take(a.T * ((scale_tiles(a.H) + 1) / 2) * PIECE);
+  at[4] = take(pairs * ((scale_tiles(a.I) + 1) / 2) * PIECE);
   return n;
 }
 
@@ -816,7 +837,7 @@ cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, con
   p.H = static_cast<int32_t>(a.H);
   p.I = static_cast<int32_t>(a.I);
   p.max_parts = max_parts(a.T * a.top);
-  size_t at[3];
+  size_t at[5];
   moe_workspace(a, at);
   char* ws = static_cast<char*>(workspace);
   auto product_of = [&](const uint8_t* scales, int64_t rows, int64_t K, size_t sums, int64_t pitch) {
@@ -835,6 +856,8 @@ cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, con
   p.up = product_of(a.up_scales, 2 * a.I, a.H, at[1], up_pitch(a.I));
   p.down = product_of(a.down_scales, a.H, a.I, at[2], down_pitch(a.H));
   p.logits = reinterpret_cast<float*>(ws + at[0]);
+  p.x_terms = reinterpret_cast<uint8_t*>(ws + at[3]);
+  p.h_terms = reinterpret_cast<uint8_t*>(ws + at[4]);
   p.control = control;
   p.status = ctl.status;
   p.wait_limit_ns = ctl.wait_limit_ns;

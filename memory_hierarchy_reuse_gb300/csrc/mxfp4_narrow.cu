@@ -8,6 +8,12 @@
 // The cluster's CTAs each hold a partial sum in TMEM; they meet in distributed
 // shared memory and are added in rank order, so a result is the same from call
 // to call.
+//
+// A plain A of at most 32 rows is quantised on the way by the CTA's other
+// warps, each CTA its part of K: one launch instead of two, and
+// no packed A in memory.
+#include <type_traits>
+
 #include "mhr_gemm.h"
 #include "mhr_mxfp4.h"
 #include "mxfp4_common.cuh"
@@ -22,7 +28,10 @@ constexpr int W_BYTES = W_ROWS * BK_BYTES;
 constexpr int SF_BYTES = 1024;        // two scale tiles of 128 rows
 constexpr int MAX_STAGES = 10;
 constexpr int MAX_NT = 128;           // rows of A a tile: the MMA's N
-constexpr int THREADS = 192;
+constexpr int THREADS = 192;           // packed A
+constexpr int PLAIN_THREADS = 512;     // A quantised here
+constexpr int PLAIN_ROWS = 32;
+constexpr int PLAIN_BYTES = 64 * 1024;  // of the quantised part of A
 constexpr int MAX_SPLIT = 8;
 constexpr int SMEM_LIMIT = 227 * 1024;
 
@@ -34,6 +43,10 @@ struct NarrowParams {
   int32_t blocks, kt;      // blocks of 32 in K; scale tiles a row
   int32_t stages, stage_bytes;
   int32_t early_b;         // B is not written by the kernel before this one
+  const void* a;           // plain A, its pitch, and whether its rows take 16-byte loads
+  int64_t lda;
+  int32_t K, vec_a;
+  int32_t a_bytes;         // shared memory of its quantised part, before the ring
   const uint8_t* sfa;
   const uint8_t* sfb;
   void* C;
@@ -53,22 +66,75 @@ __device__ __forceinline__ void store_c(const NarrowParams& p, int64_t at, float
     static_cast<__half*>(p.C)[at] = __float2half_rn(v);
 }
 
+// 8 values of a row from column k on; zeros past the end.
+template <typename T>
+__device__ __forceinline__ void load_row8(const T* row, int k, int K, bool vec, float (&v)[8]) {
+  if (vec && k + 8 <= K) {
+    alignas(16) T t[8];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(t) / 16); ++i)
+      reinterpret_cast<uint4*>(t)[i] = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? to_float(row[k + i]) : 0.f;
+  }
+}
+
+// Rows of a plain A into `staged`, as gemm_mxfp4_quantize would pack them and TMA
+// and the scales' copies would bring them: per stage of 256 columns a scale tile
+// pair (1 KB), and for all stages behind them 128 bytes a row, swizzled.  A warp
+// takes a stage of a row, 8 columns a lane.
+template <typename T>
+__device__ __forceinline__ void quantize_part(const NarrowParams& p, uint8_t* staged, int m0,
+                                              int kb0, int kb1, int warp, int warps, int lane) {
+  const int kn = kb1 - kb0, rows = min(p.nt, p.M - m0);
+  uint8_t* codes = staged + kn * SF_BYTES;
+  for (int t = warp; t < rows * kn; t += warps) {
+    const int m = t / kn, s = t - m * kn;
+    const T* row = static_cast<const T*>(p.a) + (m0 + m) * p.lda;
+    float v[8];
+    load_row8<T>(row, (kb0 + s) * 256 + lane * 8, p.K, p.vec_a != 0, v);
+    uint32_t amax = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const uint32_t code = scale_code(amax);
+    const float inv = scale_inverse(code);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] *= inv;
+    const int block = lane >> 2;
+    *reinterpret_cast<uint32_t*>(codes + (s * p.nt + m) * 128 + ((block ^ (m & 7)) << 4) +
+                                 (lane & 3) * 4) = code == 255u ? 0u : e2m1x8(v);
+    if ((lane & 3) == 0)
+      staged[s * SF_BYTES + (block >> 2) * 512 + (m & 31) * 16 + (m >> 5) * 4 + (block & 3)] =
+          static_cast<uint8_t>(code);
+  }
+}
+
 // Warp roles: 0 TMA producer, 1 TMEM allocator and MMA issuer, 2-5 epilogue
-// (TMEM lanes 32 * (warp % 4) on).  Every wait is bounded; a role that gives
-// up records it in the status word and raises the CTA's abort flag.
-__global__ void __launch_bounds__(THREADS, 1)
+// (TMEM lanes 32 * (warp % 4) on); with a plain A (type T), 2-15 quantise it
+// first.  Every wait is bounded; a role that gives up records it in the status
+// word and raises the CTA's abort flag.
+template <typename T>
+__global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREADS, 1)
     mxfp4_narrow_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB, const NarrowParams p) {
+  constexpr bool PLAIN = !std::is_void<T>::value;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t bars[2 * MAX_STAGES + 1];
+  __shared__ alignas(8) uint64_t bars[2 * MAX_STAGES + 2];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
+  const uint32_t abase = smem_u32(smem), sbase = abase + (PLAIN ? p.a_bytes : 0);
+  const uint32_t bar0 = smem_u32(bars);
   auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
   auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (MAX_STAGES + s); };
   const uint32_t acc_bar = bar0 + 8u * (2 * MAX_STAGES);
+  const uint32_t a_bar = bar0 + 8u * (2 * MAX_STAGES + 1);  // plain A: quantised
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = p.split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = blockIdx.x / p.split;
@@ -84,9 +150,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(empty_bar(s), 1);
     }
     mbar_init(acc_bar, 1);
+    mbar_init(a_bar, PLAIN_THREADS / 32 - 2);
     abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&tmA);
+    if (!PLAIN) tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
   if (warp == 1) {
@@ -102,7 +169,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     if (!abort_flag) atomicOr(p.status, bit);
     abort_flag = 1;
   };
-  const int x_bytes = p.nt * BK_BYTES;
+  const int x_bytes = PLAIN ? 0 : p.nt * BK_BYTES;  // of A in a ring stage
   const uint32_t off_x = W_BYTES, off_sfb = W_BYTES + x_bytes, off_sfa = off_sfb + SF_BYTES;
   auto sf_bytes = [&](int kb) { return static_cast<uint32_t>(min(2, p.kt - 2 * kb)) * 512u; };
 
@@ -114,11 +181,12 @@ __global__ void __launch_bounds__(THREADS, 1)
                   sf_bytes(kb), bar);
       };
       auto load_a = [&](uint32_t st, uint32_t bar, int kb) {
+        if (PLAIN) return;
         tma_load_2d(st + off_x, &tmA, bar, kb * BK_BYTES, m0);
         bulk_load(st + off_sfa, p.sfa + (static_cast<int64_t>(m0 / 128) * p.kt + 2 * kb) * 512,
                   sf_bytes(kb), bar);
       };
-      auto tx = [&](int kb) { return W_BYTES + x_bytes + 2u * sf_bytes(kb); };
+      auto tx = [&](int kb) { return W_BYTES + x_bytes + (PLAIN ? 1u : 2u) * sf_bytes(kb); };
       const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
       // The first stages' B before the kernel before this one (A's
       // quantisation) has finished, where that is known not to write B.
@@ -156,10 +224,12 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else if (warp == 1) {
     const uint32_t id0 = make_idesc_mxf4(W_ROWS, p.nt, 0), id2 = make_idesc_mxf4(W_ROWS, p.nt, 2);
     uint32_t s = 0, ph = 0, s2 = p.stages - 2, ph2 = 1;  // ring position; two stages back
+    bool ready = true;
+    if (PLAIN) ready = mbar_wait_bounded(a_bar, 0, limit, &abort_flag);
     for (int it = 0; kb0 + it < kb1; ++it) {
       // scales alternate between two sets of TMEM columns: the MMAs two
       // stages back, which read this set last, have finished
-      const bool ok = (it < 2 || mbar_wait_bounded(empty_bar(s2), ph2, limit, &abort_flag)) &&
+      const bool ok = ready && (it < 2 || mbar_wait_bounded(empty_bar(s2), ph2, limit, &abort_flag)) &&
                       mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) give_up(kErrTimeoutMma);
@@ -167,8 +237,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       }
       tc_fence_after();
       const int kb = kb0 + it;
-      const uint32_t w = desc_lo(sbase + s * p.stage_bytes), x = w + (off_x >> 4);
-      const uint32_t cb = w + (off_sfb >> 4), ca = w + (off_sfa >> 4);
+      const uint32_t w = desc_lo(sbase + s * p.stage_bytes), cb = w + (off_sfb >> 4);
+      const uint32_t part = desc_lo(abase);
+      const uint32_t x = PLAIN ? part + (((kb1 - kb0) * SF_BYTES + it * p.nt * BK_BYTES) >> 4)
+                               : w + (off_x >> 4);
+      const uint32_t ca = PLAIN ? part + ((it * SF_BYTES) >> 4) : w + (off_sfa >> 4);
       const uint32_t sfb = tmem + MAX_NT + (it & 1) * 16, sfa = sfb + 8;
       const int tiles = min(2, p.kt - 2 * kb), mmas = min(4, (p.blocks - kb * 8 + 1) / 2);
       if (elect_one()) {
@@ -199,33 +272,42 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     const int q = warp & 3;
     grid_dependency_wait();  // C may be read or written by the kernel before this one
-    const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_bar, 0, limit, &abort_flag));
-    if (!ok && lane == 0) give_up(kErrTimeoutEpilogue);
-    __syncwarp();
-    tc_fence_after();
-    const int n = n0 + q * 32 + lane;
-    const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    float* red = reinterpret_cast<float*>(smem);  // [row of A][128]: the ring is idle by now
-    if (ok && kb0 < kb1) {
-      for (int j0 = 0; j0 < p.nt; j0 += 8) {
-        uint32_t r[8];
-        tmem_ld_8cols(taddr + j0, r);
-        tmem_ld_wait();
+    if constexpr (PLAIN) {
+      quantize_part<T>(p, smem, m0, kb0, kb1, warp - 2, PLAIN_THREADS / 32 - 2, lane);
+      fence_proxy_async_smem();  // for the MMAs and scale copies that read it
+      __syncwarp();
+      if (lane == 0) mbar_arrive(a_bar);
+    }
+    if (warp < 6) {
+      const bool ok = __all_sync(0xffffffffu, mbar_wait_bounded(acc_bar, 0, limit, &abort_flag));
+      if (!ok && lane == 0) give_up(kErrTimeoutEpilogue);
+      __syncwarp();
+      tc_fence_after();
+      const int n = n0 + q * 32 + lane;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16);
+      // [row of A][128]: the ring is idle by now
+      float* red = reinterpret_cast<float*>(smem + (PLAIN ? p.a_bytes : 0));
+      if (ok && kb0 < kb1) {
+        for (int j0 = 0; j0 < p.nt; j0 += 8) {
+          uint32_t r[8];
+          tmem_ld_8cols(taddr + j0, r);
+          tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (p.split > 1)
-            red[(j0 + j) * W_ROWS + q * 32 + lane] = __uint_as_float(r[j]);
-          else if (m0 + j0 + j < p.M && n < p.N)
-            store_c(p, static_cast<int64_t>(m0 + j0 + j) * p.ldc + n, __uint_as_float(r[j]));
+          for (int j = 0; j < 8; ++j) {
+            if (p.split > 1)
+              red[(j0 + j) * W_ROWS + q * 32 + lane] = __uint_as_float(r[j]);
+            else if (m0 + j0 + j < p.M && n < p.N)
+              store_c(p, static_cast<int64_t>(m0 + j0 + j) * p.ldc + n, __uint_as_float(r[j]));
+          }
         }
       }
+      tc_fence_before();
     }
-    tc_fence_before();
   }
   __syncthreads();
   if (p.split > 1) {
     cluster_sync_all();
-    if (!abort_flag && warp >= 2) {
+    if (!abort_flag && warp >= 2 && warp < 6) {
       // Partial sums of the cluster, added in rank order: 4 columns a thread.
       const int quads = min(p.nt, p.M - m0) * (W_ROWS / 4);
       for (int g = rank * 128 + threadIdx.x - 64; g < quads; g += p.split * 128) {
@@ -260,43 +342,20 @@ __global__ void __launch_bounds__(THREADS, 1)
 
 }  // namespace
 
-cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
-  NarrowParams p;
-  p.M = static_cast<int32_t>(a.M);
-  p.N = static_cast<int32_t>(a.N);
-  p.nt = a.M >= MAX_NT ? MAX_NT : static_cast<int32_t>((a.M + 7) / 8 * 8);
-  p.tiles_n = static_cast<int32_t>((a.N + W_ROWS - 1) / W_ROWS);
-  p.blocks = static_cast<int32_t>(blocks_of(a.K));
-  p.kt = static_cast<int32_t>(scale_tiles(a.K));
-  p.num_kb = (p.kt + 1) / 2;
-  p.stage_bytes = W_BYTES + p.nt * BK_BYTES + 2 * SF_BYTES;
-  p.stages = (SMEM_LIMIT - 1024 - 2048) / p.stage_bytes;
-  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
-  p.early_b = a.after_quantize;
-  p.sfa = a.sfa;
-  p.sfb = a.sfb;
-  p.C = a.C;
-  p.ldc = a.ldc;
-  p.c_dtype = a.c_dtype;
-  p.status = ctl.status;
-  p.wait_limit_ns = ctl.wait_limit_ns;
-  p.inject_stall = ctl.inject_stall;
-  const int64_t tiles = (a.M + p.nt - 1) / p.nt * p.tiles_n;
-  p.split = 1;
-  while (p.split < MAX_SPLIT && tiles * p.split * 2 <= ctl.sm_count && p.split * 2 <= p.num_kb)
-    p.split *= 2;
-  if (tiles * p.split > 0x7fffffff) return cudaErrorInvalidConfiguration;
-  const int64_t row_bytes = static_cast<int64_t>(p.blocks) * 16;
-  CUtensorMap tmA, tmB;
-  if (encode_tmap_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row_bytes, a.M, a.lda, BK_BYTES,
-                     p.nt, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
-      encode_tmap_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
-                     W_ROWS, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
-    return cudaErrorInvalidValue;
-  const int smem = p.stages * p.stage_bytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(
-      mxfp4_narrow_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT - 2048);
-  if (e != cudaSuccess) return e;
+namespace {
+
+template <typename T>
+cudaError_t launch_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const NarrowParams& p,
+                     int64_t tiles, int smem, int device, cudaStream_t s) {
+  constexpr bool PLAIN = !std::is_void<T>::value;
+  auto kern = mxfp4_narrow_kernel<T>;
+  static bool set[64];  // by device; under the library's lock
+  if (device >= 64 || !set[device]) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               SMEM_LIMIT - 1024);
+    if (e != cudaSuccess) return e;
+    if (device < 64) set[device] = true;
+  }
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -306,15 +365,86 @@ cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream
   attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
-  cfg.blockDim = dim3(THREADS);
+  cfg.blockDim = dim3(PLAIN ? PLAIN_THREADS : THREADS);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  note_main_kernel("mxfp4_narrow_kernel", static_cast<int>(tiles * p.split),
-                   static_cast<int>(tiles));
-  e = cudaLaunchKernelEx(&cfg, mxfp4_narrow_kernel, tmA, tmB, p);
+  note_main_kernel(PLAIN ? "mxfp4_narrow_kernel<plain>" : "mxfp4_narrow_kernel",
+                   static_cast<int>(tiles * p.split), static_cast<int>(tiles));
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, tmA, tmB, p);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+// Tiles and K parts of a product; the part of A that a CTA quantises if it does.
+void plan_narrow(int64_t M, int64_t N, int64_t K, int sms, NarrowParams* p, int64_t* tiles) {
+  p->M = static_cast<int32_t>(M);
+  p->N = static_cast<int32_t>(N);
+  p->K = static_cast<int32_t>(K);
+  p->nt = M >= MAX_NT ? MAX_NT : static_cast<int32_t>((M + 7) / 8 * 8);
+  p->tiles_n = static_cast<int32_t>((N + W_ROWS - 1) / W_ROWS);
+  p->blocks = static_cast<int32_t>(blocks_of(K));
+  p->kt = static_cast<int32_t>(scale_tiles(K));
+  p->num_kb = (p->kt + 1) / 2;
+  *tiles = (M + p->nt - 1) / p->nt * p->tiles_n;
+  p->split = 1;
+  while (p->split < MAX_SPLIT && *tiles * p->split * 2 <= sms && p->split * 2 <= p->num_kb)
+    p->split *= 2;
+  p->a_bytes = (p->num_kb + p->split - 1) / p->split * (SF_BYTES + p->nt * BK_BYTES);
+}
+
+}  // namespace
+
+bool narrow_quantizes(int64_t M, int64_t N, int64_t K, int sms) {
+  if (M > PLAIN_ROWS) return false;
+  NarrowParams p;
+  int64_t tiles;
+  plan_narrow(M, N, K, sms, &p, &tiles);
+  return p.a_bytes <= PLAIN_BYTES;
+}
+
+cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
+  NarrowParams p;
+  int64_t tiles;
+  plan_narrow(a.M, a.N, a.K, ctl.sm_count, &p, &tiles);
+  if (tiles * p.split > 0x7fffffff) return cudaErrorInvalidConfiguration;
+  const bool plain = a.a_plain != nullptr;
+  const int room = SMEM_LIMIT - 1024 - 1024 - (plain ? p.a_bytes : 0);
+  p.stage_bytes = W_BYTES + (plain ? SF_BYTES : p.nt * BK_BYTES + 2 * SF_BYTES);
+  p.stages = room / p.stage_bytes;
+  if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
+  p.early_b = a.after_quantize;
+  p.sfa = a.sfa;
+  p.sfb = a.sfb;
+  p.a = a.a_plain;
+  p.lda = a.lda;
+  const int64_t size = a.a_dtype == MHR_F32 ? 4 : 2;
+  p.vec_a = reinterpret_cast<uintptr_t>(a.a_plain) % 16 == 0 && a.lda * size % 16 == 0;
+  p.C = a.C;
+  p.ldc = a.ldc;
+  p.c_dtype = a.c_dtype;
+  p.status = ctl.status;
+  p.wait_limit_ns = ctl.wait_limit_ns;
+  p.inject_stall = ctl.inject_stall;
+  const int64_t row_bytes = static_cast<int64_t>(p.blocks) * 16;
+  CUtensorMap tmA, tmB;
+  if (encode_tmap_2d(&tmB, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
+                     W_ROWS, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  tmA = tmB;
+  if (!plain && encode_tmap_2d(&tmA, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row_bytes, a.M, a.lda,
+                               BK_BYTES, p.nt, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
+    return cudaErrorInvalidValue;
+  const int smem = p.stages * p.stage_bytes + (plain ? p.a_bytes : 0) + 1024;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  if (!plain) return launch_t<void>(tmA, tmB, p, tiles, smem, device, s);
+  switch (a.a_dtype) {
+    case MHR_F32: return launch_t<float>(tmA, tmB, p, tiles, smem, device, s);
+    case MHR_BF16: return launch_t<__nv_bfloat16>(tmA, tmB, p, tiles, smem, device, s);
+    default: return launch_t<__half>(tmA, tmB, p, tiles, smem, device, s);
+  }
 }
 
 }  // namespace mx

@@ -202,7 +202,8 @@ def test_product_scales_reach_every_block(mhr, kernel):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
-@pytest.mark.parametrize("M,N,K", [(1, 512, 1000), (5, 77, 4096), (48, 300, 600), (333, 500, 1032)])
+@pytest.mark.parametrize("M,N,K", [(1, 512, 1000), (5, 77, 4096), (17, 130, 33), (32, 300, 9000),
+                                   (33, 200, 512), (9, 40, 33000), (48, 300, 600), (333, 500, 1032)])
 def test_product_quantized_on_the_way(mhr, M, N, K, dtype):
     """The same C, bit for bit, as quantising first; a strided, unaligned A."""
     import torch
