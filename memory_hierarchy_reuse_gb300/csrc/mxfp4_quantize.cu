@@ -36,36 +36,46 @@ __device__ __forceinline__ void decode8(uint32_t w, float scale, float (&v)[8]) 
   }
 }
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void load8(const T* p, int64_t left, float (&v)[8]) {
-  if (VEC && left >= 8) {
+// 8 values of type T as loaded, and as floats.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) / 2];
+  __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+      w[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+  }
+  // one value at a time, zeros from `left` on
+  __device__ __forceinline__ void load(const T* p, int64_t left) {
     alignas(16) T t[8];
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(t) / 16); ++i)
-      reinterpret_cast<uint4*>(t)[i] = __ldcs(reinterpret_cast<const uint4*>(p) + i);
+    for (int i = 0; i < 8; ++i) t[i] = i < left ? p[i] : from_float<T>(0.f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = i < left ? to_float(p[i]) : 0.f;
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+      w[i] = reinterpret_cast<const uint4*>(t)[i];
   }
-}
-
-template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, int64_t left, const float (&v)[8]) {
-  if (VEC && left >= 8) {
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_float(reinterpret_cast<const T*>(w)[i]);
+  }
+  __device__ __forceinline__ void set(const float (&v)[8]) {
     alignas(16) T t[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) t[i] = from_float<T>(v[i]);
 #pragma unroll
-    for (int i = 0; i < static_cast<int>(sizeof(t) / 16); ++i)
-      reinterpret_cast<uint4*>(p)[i] = reinterpret_cast<const uint4*>(t)[i];
-  } else {
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i)
+      w[i] = reinterpret_cast<const uint4*>(t)[i];
+  }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(T) / 2); ++i) reinterpret_cast<uint4*>(p)[i] = w[i];
+  }
+  __device__ __forceinline__ void store(T* p, int64_t left) const {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < left) p[i] = from_float<T>(v[i]);
+      if (i < left) p[i] = reinterpret_cast<const T*>(w)[i];
   }
-}
+};
 
 struct RowParams {
   const void* x;
@@ -76,7 +86,7 @@ struct RowParams {
   void* values;
   int64_t ldv;
   int64_t kt;     // scale tiles along a row
-  int64_t spans;  // warps along a row
+  uint32_t spans;  // warps along a row
 };
 
 constexpr int ROW_CHUNK = 256;  // columns of a warp's step: 8 a lane
@@ -91,10 +101,11 @@ template <typename T, bool VEC, bool VALUES>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowParams p) {
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int64_t task = blockIdx.x * int64_t{8} + (threadIdx.x >> 5);
-  const int64_t row = task / p.spans;
+  // (32-bit division: fewer than 2^31 warps of a launch, see launch_t)
+  const uint32_t task = blockIdx.x * 8u + (threadIdx.x >> 5), r = task / p.spans;
+  const int64_t row = r;
   if (row >= (p.rows + 127) / 128 * 128) return;
-  const int64_t span0 = (task - row * p.spans) * ROW_SPAN;
+  const int64_t span0 = static_cast<int64_t>(task - r * p.spans) * ROW_SPAN;
   uint8_t* srow = p.scales + scale_offset(row, 0, p.kt);
   if (row >= p.rows) {
     if ((lane & 15) == 0)
@@ -105,38 +116,52 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowParams p) {
     return;
   }
   const T* xrow = static_cast<const T*>(p.x) + row * p.ldx;
-  float v[ROW_STEPS][8];
+  // A whole span takes its loads in one go, with no branch and no conversion
+  // between them (either makes each wait for the one before).
+  const bool whole = VEC && span0 + ROW_SPAN <= p.cols;
+  Raw8<T> raw[ROW_STEPS];
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < ROW_STEPS; ++i) {
-    const int64_t c = span0 + i * ROW_CHUNK + lane * 8;
-    if (c < p.cols)
-      load8<T, VEC>(xrow + c, p.cols - c, v[i]);
-    else
+    for (int i = 0; i < ROW_STEPS; ++i) raw[i].load(xrow + span0 + i * ROW_CHUNK + lane * 8);
+  } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = 0.f;
+    for (int i = 0; i < ROW_STEPS; ++i) {
+      const int64_t c = span0 + i * ROW_CHUNK + lane * 8;
+      if (VEC && c + 8 <= p.cols)
+        raw[i].load(xrow + c);
+      else
+        raw[i].load(xrow + c, p.cols - c);
+    }
   }
 #pragma unroll
   for (int i = 0; i < ROW_STEPS; ++i) {
     const int64_t c = span0 + i * ROW_CHUNK + lane * 8;
+    float v[8];
+    raw[i].get(v);
     uint32_t amax = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(v[i][j]));
+    for (int j = 0; j < 8; ++j) amax = max(amax, abs_bits(v[j]));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint32_t code = scale_code(amax);
-    const uint32_t codes = code == 255u ? 0u : encode8(v[i], scale_inverse(code));
-    if (c < (p.cols + 31) / 32 * 32)
+    const uint32_t codes = code == 255u ? 0u : encode8(v, scale_inverse(code));
+    if (whole || c < (p.cols + 31) / 32 * 32)
       *reinterpret_cast<uint32_t*>(p.data + row * p.ldd + c / 2) = codes;
     // the scales of 4 blocks (16 lanes) as one word
     uint32_t word = code << (8 * ((lane >> 2) & 3));
     word |= __shfl_xor_sync(0xffffffffu, word, 4);
     word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if ((lane & 15) == 0 && c / 128 < p.kt)
+    if ((lane & 15) == 0 && (whole || c / 128 < p.kt))
       *reinterpret_cast<uint32_t*>(srow + c / 128 * 512) = word;
-    if (VALUES && c < p.cols) {
-      float w[8];
-      decode8(codes, scale_value(code), w);
-      store8<T, VEC>(static_cast<T*>(p.values) + row * p.ldv + c, p.cols - c, w);
+    if (VALUES) {
+      decode8(codes, scale_value(code), v);
+      Raw8<T> out;
+      out.set(v);
+      T* dst = static_cast<T*>(p.values) + row * p.ldv + c;
+      if (whole || (VEC && c + 8 <= p.cols))
+        out.store(dst);
+      else
+        out.store(dst, p.cols - c);
     }
   }
 }
@@ -166,70 +191,68 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(const ColParams p) {
   __shared__ alignas(8) uint8_t scale_s[COLS][8];
   grid_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t ty = blockIdx.x / p.tiles_n;
-  const int64_t n0 = (blockIdx.x - ty * p.tiles_n) * COLS;
+  const uint32_t tn = static_cast<uint32_t>(p.tiles_n);
+  const int64_t ty = blockIdx.x / tn;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x - ty * tn) * COLS;
   const int64_t block = ty * 8 + warp;
   const int64_t k0 = block * 32, n = n0 + lane * CPT;
-  const T* x = static_cast<const T*>(p.x);
-  T v[32][CPT];
+  // 32 rows of one fp32 value or of two 16-bit ones, as words; a whole block's
+  // loads in one go
+  const T* src = static_cast<const T*>(p.x) + k0 * p.ldx + n;
+  const bool whole = VEC && k0 + 32 <= p.rows && n0 + COLS <= p.cols;
+  uint32_t raw[32];
+  if (whole) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    const int64_t k = k0 + i;
-    const T* src = x + k * p.ldx + n;
-    if (VEC && CPT == 2 && k < p.rows && n + 1 < p.cols) {
-      *reinterpret_cast<uint32_t*>(v[i]) = __ldcs(reinterpret_cast<const uint32_t*>(src));
-    } else {
+    for (int i = 0; i < 32; ++i) raw[i] = __ldcs(reinterpret_cast<const uint32_t*>(src + i * p.ldx));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      alignas(4) T t[CPT];
 #pragma unroll
       for (int j = 0; j < CPT; ++j)
-        v[i][j] = k < p.rows && n + j < p.cols ? src[j] : from_float<T>(0.f);
+        t[j] = k0 + i < p.rows && n + j < p.cols ? src[i * p.ldx + j] : from_float<T>(0.f);
+      raw[i] = *reinterpret_cast<const uint32_t*>(t);
     }
   }
-  float scale[CPT];
-  uint4 packed[CPT];
+  auto value = [&](int i, int j) { return to_float(reinterpret_cast<const T*>(&raw[i])[j]); };
+  uint32_t code[CPT], packed[CPT][4];
 #pragma unroll
   for (int j = 0; j < CPT; ++j) {
     uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) amax = max(amax, abs_bits(to_float(v[i][j])));
-    const uint32_t code = scale_code(amax);
-    const float inv = scale_inverse(code);
-    scale[j] = scale_value(code);
-    uint32_t w[4];
+    for (int i = 0; i < 32; ++i) amax = max(amax, abs_bits(value(i, j)));
+    code[j] = scale_code(amax);
+    const float inv = scale_inverse(code[j]);
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       float f[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = to_float(v[8 * g + i][j]);
-      w[g] = code == 255u ? 0u : encode8(f, inv);
+      for (int i = 0; i < 8; ++i) f[i] = value(8 * g + i, j);
+      packed[j][g] = code[j] == 255u ? 0u : encode8(f, inv);
     }
-    packed[j] = make_uint4(w[0], w[1], w[2], w[3]);
-    codes_s[lane * CPT + j][warp] = packed[j];
-    scale_s[lane * CPT + j][warp] = static_cast<uint8_t>(code);
+    codes_s[lane * CPT + j][warp] =
+        make_uint4(packed[j][0], packed[j][1], packed[j][2], packed[j][3]);
+    scale_s[lane * CPT + j][warp] = static_cast<uint8_t>(code[j]);
   }
   if (VALUES) {
+    T* dst = static_cast<T*>(p.values) + k0 * p.ldv + n;
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       float f[CPT][8];
 #pragma unroll
-      for (int j = 0; j < CPT; ++j) {
-        const uint32_t w = g == 0   ? packed[j].x
-                           : g == 1 ? packed[j].y
-                           : g == 2 ? packed[j].z
-                                    : packed[j].w;
-        decode8(w, scale[j], f[j]);
-      }
+      for (int j = 0; j < CPT; ++j) decode8(packed[j][g], scale_value(code[j]), f[j]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int64_t k = k0 + 8 * g + i;
-        if (k >= p.rows) break;
-        T* dst = static_cast<T*>(p.values) + k * p.ldv + n;
-        if (VEC && CPT == 2 && n + 1 < p.cols) {
-          T t[2] = {from_float<T>(f[0][i]), from_float<T>(f[CPT - 1][i])};
-          *reinterpret_cast<uint32_t*>(dst) = *reinterpret_cast<const uint32_t*>(t);
+        alignas(4) T t[CPT];
+#pragma unroll
+        for (int j = 0; j < CPT; ++j) t[j] = from_float<T>(f[j][i]);
+        T* at = dst + (8 * g + i) * p.ldv;
+        if (whole) {
+          *reinterpret_cast<uint32_t*>(at) = *reinterpret_cast<const uint32_t*>(t);
         } else {
 #pragma unroll
           for (int j = 0; j < CPT; ++j)
-            if (n + j < p.cols) dst[j] = from_float<T>(f[j][i]);
+            if (k0 + 8 * g + i < p.rows && n + j < p.cols) at[j] = t[j];
         }
       }
     }
@@ -265,9 +288,9 @@ cudaError_t launch_t(const void* X, int64_t rows, int64_t cols, int64_t ldx, boo
   note_launch();
   if (!transpose) {
     const RowParams p{X,      ldx, rows, cols, data, ldd, scales, values, ldv, scale_tiles(cols),
-                      (scale_tiles(cols) * 128 + ROW_SPAN - 1) / ROW_SPAN};
+                      static_cast<uint32_t>((scale_tiles(cols) * 128 + ROW_SPAN - 1) / ROW_SPAN)};
     const int64_t tasks = (rows + 127) / 128 * 128 * p.spans;
-    if ((tasks + 7) / 8 > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    if (tasks + 8 > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>((tasks + 7) / 8));
     const bool vec = vec_ok<T>(X, ldx, 16) && (!values || vec_ok<T>(values, ldv, 16));
     auto kern = vec ? (values ? quantize_rows_kernel<T, true, true>
