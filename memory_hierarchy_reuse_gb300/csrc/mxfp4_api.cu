@@ -66,7 +66,7 @@ cudaError_t zero_c(int c_dtype, void* C, int64_t M, int64_t N, int64_t ldc, cuda
 cudaError_t launch_product(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
   MainKernelEvents ev(s);
   // (gemm_testing_set_cta_pair_mode picks a kernel, as for the other products)
-  const bool pair = ctl.pair_mode ? ctl.pair_mode == 2 : a.M > 256;
+  const bool pair = ctl.pair_mode ? ctl.pair_mode == 2 : a.M > 64;
   return pair ? launch_pair(a, ctl, s) : launch_narrow(a, ctl, s);
 }
 

@@ -48,7 +48,7 @@ struct ProductArgs {
   int a_dtype = 0;
 };
 // Whether launch_narrow takes a plain A and quantises it on the way: at most
-// 32 rows whose part of K fits beside the ring.
+// 8 rows whose part of K fits beside the ring.
 bool narrow_quantizes(int64_t M, int64_t N, int64_t K, int sms);
 // Few rows of A (any M is right).
 cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s);

@@ -9,7 +9,7 @@
 // shared memory and are added in rank order, so a result is the same from call
 // to call.
 //
-// A plain A of at most 32 rows is quantised on the way by the CTA's other
+// A plain A of at most 8 rows is quantised on the way by the CTA's other
 // warps, each CTA its part of K: one launch instead of two, and
 // no packed A in memory.
 #include <type_traits>
@@ -30,10 +30,11 @@ constexpr int MAX_STAGES = 10;
 constexpr int MAX_NT = 128;           // rows of A a tile: the MMA's N
 constexpr int THREADS = 192;           // packed A
 constexpr int PLAIN_THREADS = 512;     // A quantised here
-constexpr int PLAIN_ROWS = 32;
-constexpr int PLAIN_BYTES = 64 * 1024;  // of the quantised part of A
+constexpr int PLAIN_ROWS = 8;
+constexpr int PLAIN_BYTES = 32 * 1024;  // of the quantised part of A
 constexpr int MAX_SPLIT = 8;
 constexpr int SMEM_LIMIT = 227 * 1024;
+constexpr int PAIR_NT = 32;             // up to this many rows two CTAs share an SM
 
 struct NarrowParams {
   int32_t M, N;
@@ -119,7 +120,7 @@ __device__ __forceinline__ void quantize_part(const NarrowParams& p, uint8_t* st
 // first.  Every wait is bounded; a role that gives up records it in the status
 // word and raises the CTA's abort flag.
 template <typename T>
-__global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREADS, 1)
+__global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREADS, 2)
     mxfp4_narrow_kernel(const __grid_constant__ CUtensorMap tmA,
                         const __grid_constant__ CUtensorMap tmB, const NarrowParams p) {
   constexpr bool PLAIN = !std::is_void<T>::value;
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint64_t limit = p.wait_limit_ns;
+  grid_launch_dependents();  // (they wait for this grid's end before they read or write)
   auto give_up = [&](uint32_t bit) {  // by one thread
     if (!abort_flag) atomicOr(p.status, bit);
     abort_flag = 1;
@@ -387,9 +389,19 @@ void plan_narrow(int64_t M, int64_t N, int64_t K, int sms, NarrowParams* p, int6
   p->kt = static_cast<int32_t>(scale_tiles(K));
   p->num_kb = (p->kt + 1) / 2;
   *tiles = (M + p->nt - 1) / p->nt * p->tiles_n;
+  // K parts: the stages that the busiest SM takes, an end for each of its CTAs,
+  // and the meeting of the parts.
   p->split = 1;
-  while (p->split < MAX_SPLIT && *tiles * p->split * 2 <= sms && p->split * 2 <= p->num_kb)
-    p->split *= 2;
+  double best = 0;
+  for (int split = 1; split <= MAX_SPLIT && split <= p->num_kb; ++split) {
+    const int64_t each = (*tiles * split + sms - 1) / sms;
+    const double t = static_cast<double>(each) * ((p->num_kb + split - 1) / split + 0.5) +
+                     (split > 1 ? 1.0 + 0.1 * split : 0.0);
+    if (split == 1 || t < best) {
+      best = t;
+      p->split = split;
+    }
+  }
   p->a_bytes = (p->num_kb + p->split - 1) / p->split * (SF_BYTES + p->nt * BK_BYTES);
 }
 
@@ -409,7 +421,8 @@ cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream
   plan_narrow(a.M, a.N, a.K, ctl.sm_count, &p, &tiles);
   if (tiles * p.split > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const bool plain = a.a_plain != nullptr;
-  const int room = SMEM_LIMIT - 1024 - 1024 - (plain ? p.a_bytes : 0);
+  const int room = (p.nt <= PAIR_NT ? SMEM_LIMIT / 2 : SMEM_LIMIT) - 1024 - 1024 -
+                   (plain ? p.a_bytes : 0);
   p.stage_bytes = W_BYTES + (plain ? SF_BYTES : p.nt * BK_BYTES + 2 * SF_BYTES);
   p.stages = room / p.stage_bytes;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;

@@ -1,5 +1,5 @@
 // The 4-bit product for many rows: persistent CTA pairs (tcgen05 cta_group::2)
-// on 256 x 256 tiles of C, K in stages of 256 columns.
+// on tiles of 256 rows x 256 (or fewer) columns of C, K in stages of 256.
 //
 // Bound by the tensor pipe, and next to it by shared memory: a 256 x 256 x 64
 // MMA takes 128 cycles, in which an SM reads 128 rows of A and of B (32 bytes
@@ -13,7 +13,12 @@
 // each: A's 128 rows and B's 256 rows x 8 blocks) would take 560 of the 512
 // columns.  The accumulators overlap by 48: the epilogue drains the columns
 // that the other one needs first, and the next tile's MMAs start while it
-// drains the rest.
+// drains the rest.  Narrower tiles have both accumulators side by side; tiles of
+// 192 columns start in the middle of a scale tile every other time, and address
+// B's scales from there on (64 rows are two TMEM columns; widths that would
+// start at an odd column are not used).
+#include <cstdio>
+
 #include "mhr_gemm.h"
 #include "mhr_mxfp4.h"
 #include "mxfp4_common.cuh"
@@ -22,13 +27,14 @@ namespace mhr {
 namespace mx {
 namespace {
 
-constexpr int TILE = 256;                    // rows and columns of a pair's tile
+constexpr int TILE_M = 256;                  // rows of a pair's tile
+constexpr int MAX_BN = 256;                  // its columns: 256, 192 or 128
 constexpr int HALF = 128;
 constexpr int BK_BYTES = 128;                // 256 columns of K a stage: one swizzle row
-constexpr int OP_BYTES = HALF * BK_BYTES;    // this CTA's A rows, and its half of B
+constexpr int OP_BYTES = HALF * BK_BYTES;    // this CTA's A rows, and its half of B at most
 constexpr int OFF_B = OP_BYTES;
 constexpr int OFF_SFA = 2 * OP_BYTES;        // 2 scale tiles: 128 rows x 8 blocks
-constexpr int OFF_SFB = OFF_SFA + 1024;      // 2 x 2: all 256 columns of C
+constexpr int OFF_SFB = OFF_SFA + 1024;      // up to 2 x 2: all columns of the tile
 constexpr int STAGE_BYTES = OFF_SFB + 2048;  // 35 KB
 constexpr int STAGES = 5;
 constexpr int EPI_WARPS = 4;
@@ -36,13 +42,14 @@ constexpr int EPI_BUF = 32 * 128;            // 32 rows of 128 bytes
 constexpr int EPI_OFF = STAGES * STAGE_BYTES;
 constexpr int SMEM = EPI_OFF + EPI_WARPS * 2 * EPI_BUF + 1024;
 constexpr int THREADS = 192;
-constexpr uint32_t ACC1 = 208;               // the second accumulator's first column
-constexpr uint32_t SF_COL = 464;             // scales: 2 x 24 columns
+constexpr uint32_t OVERLAP = 48;             // columns that two accumulators of 256 share
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_M = 8;                   // tile rows a raster group, as in the bf16 kernel
 
 struct PairParams {
   int32_t M, N;
+  int32_t bn;                                // columns of a tile
+  int32_t sf_tiles;                          // 128-row scale tiles of B that a tile brings
   int32_t tiles_m, tiles_n, num_tiles, num_kb;
   int32_t blocks;
   void* C;
@@ -74,8 +81,9 @@ __device__ __forceinline__ uint32_t pack16(int c_dtype, uint32_t lo, uint32_t hi
 // Warp roles, barriers and the way a timeout unwinds are those of the bf16
 // and tf32 pair kernel (tc_gemm_pair.cu): warp 0 producer, warp 1 MMA issuer
 // (rank 0), warps 2-5 epilogue; full[s] and released[b] in rank 0, empty[s]
-// and acc_full[b] in both CTAs.  released[b]: the columns of accumulator b
-// that the other one overlaps have been read by all 8 epilogue warps.
+// and acc_full[b] in both CTAs.  released[b]: accumulator b -- of two that
+// overlap, the columns that the other one shares -- has been read by all 8
+// epilogue warps.
 // WIDE: C is fp32, else 16 bits.  TMA_STORE: C goes out by TMA.
 template <bool WIDE, bool TMA_STORE>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -102,6 +110,10 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
+  const bool overlap = p.bn == MAX_BN;
+  const uint32_t acc1 = overlap ? MAX_BN - OVERLAP : p.bn;  // the second accumulator
+  const uint32_t sf_set = 8 + 8 * p.sf_tiles;               // columns of a set of scales
+  const uint32_t stage_tx = OP_BYTES + p.bn / 2 * BK_BYTES + 1024 * (1 + p.sf_tiles);
   const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&abort_flag)), rank ^ 1u);
 
   if (threadIdx.x == 0) {
@@ -133,6 +145,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint64_t limit = p.wait_limit_ns;
+  grid_launch_dependents();  // (they wait for this grid's end before they read or write)
   grid_dependency_wait();
 
   auto give_up = [&](uint32_t bit) {  // by one thread: both CTAs unwind
@@ -149,8 +162,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       for (int u = cluster; ok && u < p.num_tiles; u += clusters) {
         int tm, tn;
         tile_at(u, p, tm, tn);
-        const int m0 = tm * TILE + static_cast<int>(rank) * HALF;
-        const int n0 = tn * TILE, nb0 = n0 + static_cast<int>(rank) * HALF;
+        const int m0 = tm * TILE_M + static_cast<int>(rank) * HALF;
+        const int n0 = tn * p.bn, nb0 = n0 + static_cast<int>(rank) * (p.bn / 2);
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
           if (!mbar_wait_bounded(empty_bar(s), ph ^ 1u, limit, &abort_flag)) {
@@ -160,7 +173,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const uint32_t st = sbase + s * STAGE_BYTES;
           const uint32_t fb = mapa_shared(full_bar(s), 0);
-          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * STAGE_BYTES);
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * stage_tx);
           if (stall && it == 0) continue;
           tma_load_2d_pair(st, &tmA, fb, kb * BK_BYTES, m0);
           tma_load_2d_pair(st + OFF_B, &tmB, fb, kb * BK_BYTES, nb0);
@@ -188,9 +201,9 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t s = i % STAGES, ph = (i / STAGES) & 1u;
           const bool armed = i < it, loaded0 = armed && !(stall && i == 0), loaded1 = i < it1;
           if (!armed) {
-            mbar_arrive_expect_tx(full_bar(s), STAGE_BYTES);
+            mbar_arrive_expect_tx(full_bar(s), stage_tx);
           } else {
-            const uint32_t missing = (loaded0 ? 0u : STAGE_BYTES) + (loaded1 ? 0u : STAGE_BYTES);
+            const uint32_t missing = (loaded0 ? 0u : stage_tx) + (loaded1 ? 0u : stage_tx);
             if (missing) {  // once the MMA issuer has given up on the stage
               mbar_wait_bounded(full_bar(s), ph, 2 * limit, &abort_flag);
               mbar_complete_tx(full_bar(s), missing);
@@ -204,7 +217,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (leader) {
-      const uint32_t id0 = make_idesc_mxf4(TILE, TILE, 0), id2 = make_idesc_mxf4(TILE, TILE, 2);
+      const uint32_t id0 = make_idesc_mxf4(TILE_M, p.bn, 0), id2 = make_idesc_mxf4(TILE_M, p.bn, 2);
+      const uint32_t sf_k = 4 * p.sf_tiles;        // columns of B's scales for 128 columns of K
       const int tail = (p.blocks - (p.num_kb - 1) * 8 + 1) / 2;  // MMAs of a tile's last stage
       uint32_t it = 0, t = 0, s = 0, ph = 0;       // stages done; ring position and its phase
       uint32_t s2 = STAGES - 2, ph2 = 1;           // the same two stages back
@@ -214,14 +228,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit, &abort_flag)) != 0;
       };
       for (int u = cluster; ok && u < p.num_tiles; u += clusters, ++t) {
-        // the other accumulator's overlapping columns have been read (and with
-        // them, by the same warps earlier, all of this one's last tile)
-        if (t > 0 && !wait(released_bar((t - 1) & 1u), ((t - 1) >> 1) & 1u)) {
+        // this accumulator's last tile but one has been read; of two that
+        // overlap, the other one's shared columns (and with them, by the same
+        // warps earlier, all of this one)
+        const uint32_t before = overlap ? t - 1 : t - 2;
+        if (t >= (overlap ? 1u : 2u) &&
+            !wait(released_bar(before & 1u), (before >> 1) & 1u)) {
           if (lane == 0) give_up(kErrTimeoutMma);
           break;
         }
         tc_fence_after();
-        const uint32_t d = tmem + (t & 1u ? ACC1 : 0);
+        const uint32_t d = tmem + (t & 1u ? acc1 : 0);
+        int tm, tn;
+        tile_at(u, p, tm, tn);
+        const uint32_t sf_row = (tn * p.bn & 127) >> 5;  // the tile's first row in its scale tile
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           // scales alternate between two sets of columns: the MMAs two stages
           // back, the last to read this set, have finished
@@ -234,26 +254,27 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t st = sbase + s * STAGE_BYTES;
           const uint32_t a = desc_lo(st), bb = a + (OFF_B >> 4);
           const uint32_t ca = a + (OFF_SFA >> 4), cb = a + (OFF_SFB >> 4);
-          const uint32_t sfa = tmem + SF_COL + (it & 1u) * 24, sfb = sfa + 8;
+          const uint32_t sfa = tmem + TMEM_COLS - (1 + (it & 1u)) * sf_set, sfb = sfa + 8;
           const uint32_t first = kb > 0 ? 1u : 0u;
           const bool full = kb + 1 < p.num_kb || tail == 4;
           if (elect_one()) {
-            // columns: A's tile 0, tile 1; B's tile 0 of both 128-row parts, then tile 1 of both
+            // columns: A's tiles 0 and 1 of K; B's for tile 0 of K, then for tile 1
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               copy_scale_tile<2>(sfa + 4 * i, ca + 32 * i);
-              copy_scale_tile<2>(sfb + 8 * i, cb + 32 * i);
-              copy_scale_tile<2>(sfb + 8 * i + 4, cb + 64 + 32 * i);
+              for (int j = 0; j < p.sf_tiles; ++j)
+                copy_scale_tile<2>(sfb + sf_k * i + 4 * j, cb + 64 * j + 32 * i);
             }
+            const uint32_t sb = sfb + sf_row;
             if (full) {
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk)
                 mma_mxf4<2>(d, a + 2 * kk, bb + 2 * kk, kk & 1 ? id2 : id0, sfa + 4 * (kk >> 1),
-                            sfb + 8 * (kk >> 1), kk > 0 ? 1u : first);
+                            sb + sf_k * (kk >> 1), kk > 0 ? 1u : first);
             } else {
               for (int kk = 0; kk < tail; ++kk)
                 mma_mxf4<2>(d, a + 2 * kk, bb + 2 * kk, kk & 1 ? id2 : id0, sfa + 4 * (kk >> 1),
-                            sfb + 8 * (kk >> 1), kk > 0 ? 1u : first);
+                            sb + sf_k * (kk >> 1), kk > 0 ? 1u : first);
             }
             mma_commit_pair_multicast(empty_bar(s), 0x3);
             if (kb + 1 == p.num_kb) mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
@@ -278,9 +299,10 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else {
     const int q = warp & 3, ew = warp - 2;
-    constexpr int PIECES = WIDE ? 8 : 4;       // of 32 fp32 or 64 16-bit columns: 128 bytes a row
-    constexpr int COLS = WIDE ? 32 : 64;
+    constexpr int COLS = WIDE ? 32 : 64;       // columns of a piece: 128 bytes a row
     constexpr int FIRST = WIDE ? 2 : 1;        // pieces that hold the overlapping columns
+    const int pieces = p.bn / COLS;
+    const int release = overlap ? FIRST - 1 : pieces - 1;  // the piece that frees the accumulator
     uint32_t t = 0, chunk = 0;
     for (int u = cluster; u < p.num_tiles; u += clusters, ++t) {
       const uint32_t b = t & 1u;
@@ -293,12 +315,13 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       int tm, tn;
       tile_at(u, p, tm, tn);
-      const int row0 = tm * TILE + static_cast<int>(rank) * HALF + q * 32, n0 = tn * TILE;
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (b ? ACC1 : 0);
+      const int row0 = tm * TILE_M + static_cast<int>(rank) * HALF + q * 32, n0 = tn * p.bn;
+      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (b ? acc1 : 0);
 #pragma unroll 1
-      for (int i = 0; i < PIECES; ++i) {
-        // the first accumulator's shared columns are its last, the second's its first
-        const int c = b ? i : (i < FIRST ? PIECES - FIRST + i : i - FIRST);
+      for (int i = 0; i < pieces; ++i) {
+        // of two that overlap, the first accumulator's shared columns are its
+        // last, the second's its first
+        const int c = b || !overlap ? i : (i < FIRST ? pieces - FIRST + i : i - FIRST);
         uint32_t r[32];
         tmem_ld_32cols(taddr + c * COLS, r);
         if constexpr (!WIDE) {
@@ -312,7 +335,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         } else {
           tmem_ld_wait();
         }
-        if (i == FIRST - 1) {
+        if (i == release) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(released_bar(b), 0));
@@ -382,35 +405,22 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
+// As many clusters as can run at once.
 template <bool WIDE, bool TMA_STORE>
-cudaError_t launch_t(const CUtensorMap (&m)[5], const PairParams& p, const DeviceCtl& ctl,
-                     cudaStream_t s) {
+cudaError_t prepare_t(int device, int sms, cudaLaunchConfig_t* cfg, int* clusters) {
   auto kern = mxfp4_pair_kernel<WIDE, TMA_STORE>;
+  static int most[64];  // by device; under the library's lock
+  if (device < 64 && most[device]) {
+    *clusters = most[device];
+    return cudaSuccess;
+  }
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  cfg.gridDim = dim3(2 * (ctl.sm_count / 2));
-  int max_clusters = 0;
-  if ((e = cudaOccupancyMaxActiveClusters(&max_clusters, kern, &cfg)) != cudaSuccess) return e;
-  if (max_clusters < 1) return cudaErrorInvalidConfiguration;
-  const int clusters = p.num_tiles < max_clusters ? p.num_tiles : max_clusters;
-  cfg.gridDim = dim3(2 * clusters);
-  cfg.numAttrs = 2;
-  note_main_kernel("mxfp4_pair_kernel", 2 * clusters, p.num_tiles);
-  e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  cfg->gridDim = dim3(2 * (sms / 2));
+  if ((e = cudaOccupancyMaxActiveClusters(clusters, kern, cfg)) != cudaSuccess) return e;
+  if (*clusters < 1) return cudaErrorInvalidConfiguration;
+  if (device < 64) most[device] = *clusters;
+  return cudaSuccess;
 }
 
 // Scales as 512-byte tiles: tile_rows x kt of them, boxes of 2 x `rows`.
@@ -424,12 +434,62 @@ bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t kt
 
 }  // namespace
 
+// Tile columns.  A tile takes num_kb stages of c0 + c1 bn and ends; the time is
+// that of the busiest cluster.  Narrower tiles fill a last round better and put
+// more clusters to work on few tiles; wider ones do more with a stage's fixed
+// part.
+int plan_pair_bn(int64_t M, int64_t N, int64_t K, int clusters) {
+  const int64_t stages = (scale_tiles(K) + 1) / 2;
+  int best = MAX_BN;
+  double best_t = 0;
+  for (int bn = MAX_BN; bn >= 128; bn -= 64) {
+    const int64_t tiles = (M + TILE_M - 1) / TILE_M * ((N + bn - 1) / bn);
+    const int64_t rounds = (tiles + clusters - 1) / clusters;
+    const double t = static_cast<double>(rounds) * stages * (180.0 + 2.0 * bn) + 6.0 * bn;
+    if (bn == MAX_BN || t < best_t) {
+      best_t = t;
+      best = bn;
+    }
+  }
+  return best;
+}
+
 cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
+  const bool wide = a.c_dtype == MHR_F32;
+  const int64_t size = wide ? 4 : 2;
+  // TMA stores clip a box at C's inner extent in 16-byte units only
+  const bool c_tma = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * size % 16 == 0 &&
+                     a.N * size % 16 == 0;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int device = 0, clusters = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  e = wide ? (c_tma ? prepare_t<true, true>(device, ctl.sm_count, &cfg, &clusters)
+                    : prepare_t<true, false>(device, ctl.sm_count, &cfg, &clusters))
+           : (c_tma ? prepare_t<false, true>(device, ctl.sm_count, &cfg, &clusters)
+                    : prepare_t<false, false>(device, ctl.sm_count, &cfg, &clusters));
+  if (e != cudaSuccess) return e;
+
   PairParams p;
   p.M = static_cast<int32_t>(a.M);
   p.N = static_cast<int32_t>(a.N);
-  p.tiles_m = static_cast<int32_t>((a.M + TILE - 1) / TILE);
-  p.tiles_n = static_cast<int32_t>((a.N + TILE - 1) / TILE);
+  // (gemm_testing_set_pair_tile_n forces a width, rounded to one that exists)
+  p.bn = ctl.pair_tile_n ? ctl.pair_tile_n / 64 * 64 : plan_pair_bn(a.M, a.N, a.K, clusters);
+  p.sf_tiles = (p.bn + 127) / 128;  // (64 + 192 rows are 2 as well)
+  p.tiles_m = static_cast<int32_t>((a.M + TILE_M - 1) / TILE_M);
+  p.tiles_n = static_cast<int32_t>((a.N + p.bn - 1) / p.bn);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
   p.num_tiles = static_cast<int32_t>(tiles);
@@ -442,18 +502,13 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
   p.status = ctl.status;
   p.wait_limit_ns = ctl.wait_limit_ns;
   p.inject_stall = ctl.inject_stall;
-  const bool wide = a.c_dtype == MHR_F32;
-  const int64_t size = wide ? 4 : 2;
-  // TMA stores clip a box at C's inner extent in 16-byte units only
-  const bool c_tma = reinterpret_cast<uintptr_t>(a.C) % 16 == 0 && a.ldc * size % 16 == 0 &&
-                     a.N * size % 16 == 0;
   const int64_t row_bytes = static_cast<int64_t>(p.blocks) * 16;
   CUtensorMap m[5];
   if (encode_tmap_2d(&m[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row_bytes, a.M, a.lda, BK_BYTES,
                      HALF, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
       encode_tmap_2d(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
-                     HALF, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
-      !scale_map(&m[2], a.sfa, a.M, kt, 1) || !scale_map(&m[3], a.sfb, a.N, kt, 2))
+                     p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      !scale_map(&m[2], a.sfa, a.M, kt, 1) || !scale_map(&m[3], a.sfb, a.N, kt, p.sf_tiles))
     return cudaErrorInvalidValue;
   m[4] = m[0];
   if (c_tma && encode_tmap_2d(&m[4],
@@ -462,9 +517,16 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
                               a.C, a.N, a.M, a.ldc * size, 128 / size, 32,
                               CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  if (wide)
-    return c_tma ? launch_t<true, true>(m, p, ctl, s) : launch_t<true, false>(m, p, ctl, s);
-  return c_tma ? launch_t<false, true>(m, p, ctl, s) : launch_t<false, false>(m, p, ctl, s);
+  if (p.num_tiles < clusters) clusters = p.num_tiles;
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.numAttrs = 2;
+  char name[48];
+  snprintf(name, sizeof(name), "mxfp4_pair_kernel<n%d>", p.bn);
+  note_main_kernel(name, 2 * clusters, p.num_tiles);
+  auto kern = wide ? (c_tma ? mxfp4_pair_kernel<true, true> : mxfp4_pair_kernel<true, false>)
+                   : (c_tma ? mxfp4_pair_kernel<false, true> : mxfp4_pair_kernel<false, false>);
+  e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], p);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace mx

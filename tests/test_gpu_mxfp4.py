@@ -150,6 +150,22 @@ def test_product_of_many_tiles(mhr, kernel, dtype):
     product_case(mhr, 2600, 3300, 300, dtype)
 
 
+@pytest.mark.parametrize("width", [128, 192, 256])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_product_tile_widths(mhr, width, dtype):
+    """The pair kernel at every tile width, aligned and unaligned C, several tiles a pair."""
+    old_mode = mhr.gemm_testing_set_cta_pair_mode(2)
+    old = mhr.gemm_testing_set_pair_tile_n(width)
+    try:
+        product_case(mhr, 300, 1000, 776, dtype)
+        product_case(mhr, 300, 1001, 776, dtype, ldc=1003, offset=1)
+        product_case(mhr, 2100, 2560, 640, dtype)
+        assert f"<n{width}>" in mhr.gemm_testing_last_main_kernel()
+    finally:
+        mhr.gemm_testing_set_pair_tile_n(old)
+        mhr.gemm_testing_set_cta_pair_mode(old_mode)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(5, 200, 300), (140, 200, 300), (300, 260, 520)])
 def test_product_strides_and_offsets(mhr, kernel, M, N, K, dtype):
