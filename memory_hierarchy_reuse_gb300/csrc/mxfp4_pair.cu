@@ -46,10 +46,12 @@ constexpr uint32_t OVERLAP = 48;             // columns that two accumulators of
 constexpr uint32_t TMEM_COLS = 512;
 constexpr int GROUP_M = 8;                   // tile rows a raster group, as in the bf16 kernel
 
+// 128-row scale tiles of B that a tile of bn columns brings (192 rows that start
+// 64 into one end with the second).
+__host__ __device__ constexpr int sf_tiles(int bn) { return (bn + 127) / 128; }
+
 struct PairParams {
   int32_t M, N;
-  int32_t bn;                                // columns of a tile
-  int32_t sf_tiles;                          // 128-row scale tiles of B that a tile brings
   int32_t tiles_m, tiles_n, num_tiles, num_kb;
   int32_t blocks;
   void* C;
@@ -85,7 +87,7 @@ __device__ __forceinline__ uint32_t pack16(int c_dtype, uint32_t lo, uint32_t hi
 // overlap, the columns that the other one shares -- has been read by all 8
 // epilogue warps.
 // WIDE: C is fp32, else 16 bits.  TMA_STORE: C goes out by TMA.
-template <bool WIDE, bool TMA_STORE>
+template <int BN, bool WIDE, bool TMA_STORE>
 __global__ void __launch_bounds__(THREADS, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
@@ -110,10 +112,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
   const int cluster = blockIdx.x >> 1, clusters = gridDim.x >> 1;
-  const bool overlap = p.bn == MAX_BN;
-  const uint32_t acc1 = overlap ? MAX_BN - OVERLAP : p.bn;  // the second accumulator
-  const uint32_t sf_set = 8 + 8 * p.sf_tiles;               // columns of a set of scales
-  const uint32_t stage_tx = OP_BYTES + p.bn / 2 * BK_BYTES + 1024 * (1 + p.sf_tiles);
+  constexpr bool overlap = BN == MAX_BN;
+  constexpr uint32_t acc1 = overlap ? MAX_BN - OVERLAP : BN;  // the second accumulator
+  constexpr int SF_TILES = sf_tiles(BN);
+  constexpr uint32_t sf_set = 8 + 8 * SF_TILES;               // columns of a set of scales
+  constexpr uint32_t stage_tx = OP_BYTES + BN / 2 * BK_BYTES + 1024 * (1 + SF_TILES);
   const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&abort_flag)), rank ^ 1u);
 
   if (threadIdx.x == 0) {
@@ -163,7 +166,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         int tm, tn;
         tile_at(u, p, tm, tn);
         const int m0 = tm * TILE_M + static_cast<int>(rank) * HALF;
-        const int n0 = tn * p.bn, nb0 = n0 + static_cast<int>(rank) * (p.bn / 2);
+        const int n0 = tn * BN, nb0 = n0 + static_cast<int>(rank) * (BN / 2);
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
           if (!mbar_wait_bounded(empty_bar(s), ph ^ 1u, limit, &abort_flag)) {
@@ -217,8 +220,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (leader) {
-      const uint32_t id0 = make_idesc_mxf4(TILE_M, p.bn, 0), id2 = make_idesc_mxf4(TILE_M, p.bn, 2);
-      const uint32_t sf_k = 4 * p.sf_tiles;        // columns of B's scales for 128 columns of K
+      const uint32_t id0 = make_idesc_mxf4(TILE_M, BN, 0), id2 = make_idesc_mxf4(TILE_M, BN, 2);
+      constexpr uint32_t sf_k = 4 * SF_TILES;      // columns of B's scales for 128 columns of K
       const int tail = (p.blocks - (p.num_kb - 1) * 8 + 1) / 2;  // MMAs of a tile's last stage
       uint32_t it = 0, t = 0, s = 0, ph = 0;       // stages done; ring position and its phase
       uint32_t s2 = STAGES - 2, ph2 = 1;           // the same two stages back
@@ -239,13 +242,20 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         tc_fence_after();
         const uint32_t d = tmem + (t & 1u ? acc1 : 0);
-        int tm, tn;
-        tile_at(u, p, tm, tn);
-        const uint32_t sf_row = (tn * p.bn & 127) >> 5;  // the tile's first row in its scale tile
+        uint32_t sf_row = 0;  // TMEM column of the tile's first row in its scale tile
+        if constexpr (BN % 128 != 0) {
+          int tm, tn;
+          tile_at(u, p, tm, tn);
+          sf_row = (tn * BN & 127) >> 5;
+        }
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           // scales alternate between two sets of columns: the MMAs two stages
           // back, the last to read this set, have finished
-          if ((it >= 2 && !wait(empty_bar(s2), ph2)) || !wait(full_bar(s), ph)) {
+          // (both barriers polled once together; mostly that is all)
+          bool there = mbar_try_wait(full_bar(s), ph);
+          there = (it < 2 || mbar_try_wait(empty_bar(s2), ph2)) && there;
+          if (!__all_sync(0xffffffffu, there) &&
+              ((it >= 2 && !wait(empty_bar(s2), ph2)) || !wait(full_bar(s), ph))) {
             if (lane == 0) give_up(kErrTimeoutMma);
             ok = false;
             break;
@@ -262,7 +272,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               copy_scale_tile<2>(sfa + 4 * i, ca + 32 * i);
-              for (int j = 0; j < p.sf_tiles; ++j)
+              #pragma unroll
+              for (int j = 0; j < SF_TILES; ++j)
                 copy_scale_tile<2>(sfb + sf_k * i + 4 * j, cb + 64 * j + 32 * i);
             }
             const uint32_t sb = sfb + sf_row;
@@ -301,8 +312,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int q = warp & 3, ew = warp - 2;
     constexpr int COLS = WIDE ? 32 : 64;       // columns of a piece: 128 bytes a row
     constexpr int FIRST = WIDE ? 2 : 1;        // pieces that hold the overlapping columns
-    const int pieces = p.bn / COLS;
-    const int release = overlap ? FIRST - 1 : pieces - 1;  // the piece that frees the accumulator
+    constexpr int pieces = BN / COLS;
+    constexpr int release = overlap ? FIRST - 1 : pieces - 1;  // the piece that frees the accumulator
     uint32_t t = 0, chunk = 0;
     for (int u = cluster; u < p.num_tiles; u += clusters, ++t) {
       const uint32_t b = t & 1u;
@@ -315,7 +326,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       tc_fence_after();
       int tm, tn;
       tile_at(u, p, tm, tn);
-      const int row0 = tm * TILE_M + static_cast<int>(rank) * HALF + q * 32, n0 = tn * p.bn;
+      const int row0 = tm * TILE_M + static_cast<int>(rank) * HALF + q * 32, n0 = tn * BN;
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (b ? acc1 : 0);
 #pragma unroll 1
       for (int i = 0; i < pieces; ++i) {
@@ -405,22 +416,38 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// As many clusters as can run at once.
-template <bool WIDE, bool TMA_STORE>
-cudaError_t prepare_t(int device, int sms, cudaLaunchConfig_t* cfg, int* clusters) {
-  auto kern = mxfp4_pair_kernel<WIDE, TMA_STORE>;
+// One launch on as many clusters as can run at once (at most one a tile).
+template <int BN, bool WIDE, bool TMA_STORE>
+cudaError_t launch_t(const CUtensorMap (&m)[5], const PairParams& p, int device,
+                     cudaLaunchConfig_t cfg) {
+  auto kern = mxfp4_pair_kernel<BN, WIDE, TMA_STORE>;
   static int most[64];  // by device; under the library's lock
-  if (device < 64 && most[device]) {
-    *clusters = most[device];
-    return cudaSuccess;
+  int clusters = device < 64 ? most[device] : 0;
+  if (!clusters) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg)) != cudaSuccess) return e;
+    if (clusters < 1) return cudaErrorInvalidConfiguration;
+    if (device < 64) most[device] = clusters;
   }
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-  if (e != cudaSuccess) return e;
-  cfg->gridDim = dim3(2 * (sms / 2));
-  if ((e = cudaOccupancyMaxActiveClusters(clusters, kern, cfg)) != cudaSuccess) return e;
-  if (*clusters < 1) return cudaErrorInvalidConfiguration;
-  if (device < 64) most[device] = *clusters;
-  return cudaSuccess;
+  if (p.num_tiles < clusters) clusters = p.num_tiles;
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.numAttrs = 2;
+  char name[48];
+  snprintf(name, sizeof(name), "mxfp4_pair_kernel<n%d>", BN);
+  note_main_kernel(name, 2 * clusters, p.num_tiles);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int BN>
+cudaError_t launch_bn(const CUtensorMap (&m)[5], const PairParams& p, bool wide, bool c_tma,
+                      int device, const cudaLaunchConfig_t& cfg) {
+  if (wide)
+    return c_tma ? launch_t<BN, true, true>(m, p, device, cfg)
+                 : launch_t<BN, true, false>(m, p, device, cfg);
+  return c_tma ? launch_t<BN, false, true>(m, p, device, cfg)
+               : launch_t<BN, false, false>(m, p, device, cfg);
 }
 
 // Scales as 512-byte tiles: tile_rows x kt of them, boxes of 2 x `rows`.
@@ -473,23 +500,18 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  int device = 0, clusters = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  e = wide ? (c_tma ? prepare_t<true, true>(device, ctl.sm_count, &cfg, &clusters)
-                    : prepare_t<true, false>(device, ctl.sm_count, &cfg, &clusters))
-           : (c_tma ? prepare_t<false, true>(device, ctl.sm_count, &cfg, &clusters)
-                    : prepare_t<false, false>(device, ctl.sm_count, &cfg, &clusters));
-  if (e != cudaSuccess) return e;
+  cfg.gridDim = dim3(2 * (ctl.sm_count / 2));
+  int device = 0;
+  if (const cudaError_t e = cudaGetDevice(&device); e != cudaSuccess) return e;
 
   PairParams p;
   p.M = static_cast<int32_t>(a.M);
   p.N = static_cast<int32_t>(a.N);
   // (gemm_testing_set_pair_tile_n forces a width, rounded to one that exists)
-  p.bn = ctl.pair_tile_n ? ctl.pair_tile_n / 64 * 64 : plan_pair_bn(a.M, a.N, a.K, clusters);
-  p.sf_tiles = (p.bn + 127) / 128;  // (64 + 192 rows are 2 as well)
+  const int bn = ctl.pair_tile_n ? ctl.pair_tile_n / 64 * 64
+                                 : plan_pair_bn(a.M, a.N, a.K, ctl.sm_count / 2);
   p.tiles_m = static_cast<int32_t>((a.M + TILE_M - 1) / TILE_M);
-  p.tiles_n = static_cast<int32_t>((a.N + p.bn - 1) / p.bn);
+  p.tiles_n = static_cast<int32_t>((a.N + bn - 1) / bn);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
   p.num_tiles = static_cast<int32_t>(tiles);
@@ -507,8 +529,8 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
   if (encode_tmap_2d(&m[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row_bytes, a.M, a.lda, BK_BYTES,
                      HALF, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
       encode_tmap_2d(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
-                     p.bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
-      !scale_map(&m[2], a.sfa, a.M, kt, 1) || !scale_map(&m[3], a.sfb, a.N, kt, p.sf_tiles))
+                     bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      !scale_map(&m[2], a.sfa, a.M, kt, 1) || !scale_map(&m[3], a.sfb, a.N, kt, sf_tiles(bn)))
     return cudaErrorInvalidValue;
   m[4] = m[0];
   if (c_tma && encode_tmap_2d(&m[4],
@@ -517,16 +539,9 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
                               a.C, a.N, a.M, a.ldc * size, 128 / size, 32,
                               CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
-  if (p.num_tiles < clusters) clusters = p.num_tiles;
-  cfg.gridDim = dim3(2 * clusters);
-  cfg.numAttrs = 2;
-  char name[48];
-  snprintf(name, sizeof(name), "mxfp4_pair_kernel<n%d>", p.bn);
-  note_main_kernel(name, 2 * clusters, p.num_tiles);
-  auto kern = wide ? (c_tma ? mxfp4_pair_kernel<true, true> : mxfp4_pair_kernel<true, false>)
-                   : (c_tma ? mxfp4_pair_kernel<false, true> : mxfp4_pair_kernel<false, false>);
-  e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], p);
-  return e != cudaSuccess ? e : cudaGetLastError();
+  if (bn == 256) return launch_bn<256>(m, p, wide, c_tma, device, cfg);
+  if (bn == 192) return launch_bn<192>(m, p, wide, c_tma, device, cfg);
+  return launch_bn<128>(m, p, wide, c_tma, device, cfg);
 }
 
 }  // namespace mx
