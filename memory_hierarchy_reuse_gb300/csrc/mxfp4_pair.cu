@@ -158,33 +158,41 @@ __global__ void __launch_bounds__(THREADS, 1)
   };
 
   if (warp == 0) {
-    if (lane == 0) {
-      uint32_t it = 0;
-      const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
-      bool ok = true;
-      for (int u = cluster; ok && u < p.num_tiles; u += clusters) {
-        int tm, tn;
-        tile_at(u, p, tm, tn);
-        const int m0 = tm * TILE_M + static_cast<int>(rank) * HALF;
-        const int n0 = tn * BN, nb0 = n0 + static_cast<int>(rank) * (BN / 2);
-        for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-          const uint32_t s = it % STAGES, ph = (it / STAGES) & 1u;
-          if (!mbar_wait_bounded(empty_bar(s), ph ^ 1u, limit, &abort_flag)) {
-            give_up(kErrTimeoutProducer);
-            ok = false;
-            break;
-          }
-          const uint32_t st = sbase + s * STAGE_BYTES;
-          const uint32_t fb = mapa_shared(full_bar(s), 0);
+    uint32_t it = 0, s = 0, ph = 1;  // stages armed and loaded; ring position, phase to wait for
+    const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
+    const uint32_t fb0 = mapa_shared(full_bar(0), 0);
+    bool ok = true;
+    for (int u = cluster; ok && u < p.num_tiles; u += clusters) {
+      int tm, tn;
+      tile_at(u, p, tm, tn);
+      const int m0 = tm * TILE_M + static_cast<int>(rank) * HALF;
+      const int n0 = tn * BN, nb0 = n0 + static_cast<int>(rank) * (BN / 2);
+      for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
+        if (!__all_sync(0xffffffffu,
+                        mbar_wait_bounded(empty_bar(s), ph, limit, &abort_flag))) {
+          if (lane == 0) give_up(kErrTimeoutProducer);
+          ok = false;
+          break;
+        }
+        const uint32_t st = sbase + s * STAGE_BYTES, fb = fb0 + 8u * s;
+        if (elect_one()) {
           if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * stage_tx);
-          if (stall && it == 0) continue;
-          tma_load_2d_pair(st, &tmA, fb, kb * BK_BYTES, m0);
-          tma_load_2d_pair(st + OFF_B, &tmB, fb, kb * BK_BYTES, nb0);
-          // (boxes past the last row or block are filled with zeros)
-          tma_load_3d_pair(st + OFF_SFA, &tmSA, fb, 0, 2 * kb, m0 / 128);
-          tma_load_3d_pair(st + OFF_SFB, &tmSB, fb, 0, 2 * kb, n0 / 128);
+          if (!(stall && it == 0)) {
+            tma_load_2d_pair(st, &tmA, fb, kb * BK_BYTES, m0);
+            tma_load_2d_pair(st + OFF_B, &tmB, fb, kb * BK_BYTES, nb0);
+            // (boxes past the last row or block are filled with zeros)
+            tma_load_3d_pair(st + OFF_SFA, &tmSA, fb, 0, 2 * kb, m0 / 128);
+            tma_load_3d_pair(st + OFF_SFB, &tmSB, fb, 0, 2 * kb, n0 / 128);
+          }
+        }
+        __syncwarp();
+        if (++s == STAGES) {
+          s = 0;
+          ph ^= 1u;
         }
       }
+    }
+    if (lane == 0) {
       // Both CTAs' loads complete in rank 0, which waits for all of them --
       // counting as done what either side never issued -- before either CTA
       // may leave.
