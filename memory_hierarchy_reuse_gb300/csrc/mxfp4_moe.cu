@@ -145,6 +145,52 @@ __device__ __forceinline__ void unpack_bf16(const uint4& w, float (&v)[8]) {
   }
 }
 
+// The chosen experts and weights of a token, by one warp; PER_LANE x 32 experts at
+// most.  Logits become unsigned keys of the same order (a NaN largest, -0 and 0
+// alike), 0 for one taken or none.  Lane k < top gets the k-th.
+template <int PER_LANE>
+__device__ __forceinline__ void choose_token(const MoeParams& p, int t, int& expert,
+                                             float& weight) {
+  const int lane = threadIdx.x & 31;
+  uint32_t key[PER_LANE];
+#pragma unroll
+  for (int i = 0; i < PER_LANE; ++i) {
+    const int e = lane + 32 * i;
+    const float v = e < p.E ? __ldcg(p.logits + t * p.E + e) + 0.f : 0.f;
+    const uint32_t b = __float_as_uint(v);
+    key[i] = e >= p.E ? 0u : v != v ? 0xffffffffu : b >> 31 ? ~b : b | 0x80000000u;
+  }
+  uint32_t chosen = 0, first = 0;
+#pragma unroll 1
+  for (int k = 0; k < p.top; ++k) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i) m = max(m, key[i]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    uint32_t e = 0xffffffffu;
+#pragma unroll
+    for (int i = PER_LANE - 1; i >= 0; --i)
+      if (key[i] == m) e = lane + 32 * i;
+    e = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+    for (int i = 0; i < PER_LANE; ++i)
+      if (e == static_cast<uint32_t>(lane + 32 * i)) key[i] = 0;
+    if (k == 0) first = m;
+    if (lane == k) {
+      chosen = m;
+      expert = static_cast<int>(e);
+    }
+  }
+  auto logit = [](uint32_t key) {
+    return __uint_as_float(key == 0xffffffffu ? key : key >> 31 ? key & 0x7fffffffu : ~key);
+  };
+  weight = lane < p.top ? expf(logit(chosen) - logit(first)) : 0.f;
+  float sum = weight;
+#pragma unroll 1
+  for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  weight /= sum;
+}
+
 // Step 1, all warps of the grid: router logits, a warp one expert and TT tokens.
 template <int TT>
 __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, bool vr) {
@@ -185,7 +231,17 @@ __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, b
 
 // 256 columns of K, 8 a lane, as TERMS rows of e2m1 codes and their scales:
 // row j is 128 bytes from 128 j on, its 8 scales follow all rows.
-__device__ __forceinline__ void split_terms(float (&v)[8], uint8_t* piece, int lane) {
+//
+//
+// Here and below, code that runs twice a call is one copy of it, and loops stay
+// rolled: between the grid barriers a CTA runs little code, and most of it for
+// the first time in the launch, so that fetching instructions is what these steps
+// wait for (choosing experts unrolled over four tokens took twice as long as one
+// at a time).
+__device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3, float v4,
+                                         float v5, float v6, float v7, uint8_t* piece) {
+  const int lane = threadIdx.x & 31;
+  float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
   uint32_t amax = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
@@ -233,7 +289,8 @@ __device__ void route_start(const MoeParams& p) {
     load_row<1>(p.x + t * p.ldx, k, p.H, vx, x);
     float v[8];
     unpack_bf16(x[0], v);
-    split_terms(v, p.x_terms + static_cast<int64_t>(i) * PIECE, lane);
+    split_terms(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7],
+                p.x_terms + static_cast<int64_t>(i) * PIECE);
   }
   if (p.E * p.T <= warps)
     route_logits<1>(p, warp, warps, vx, vr);
@@ -241,76 +298,32 @@ __device__ void route_start(const MoeParams& p) {
     route_logits<4>(p, warp, warps, vx, vr);
 }
 
-// The chosen experts of a warp's tokens, NT at a time (their chains of reductions
-// side by side), and their weights; PER_LANE x 32 experts at most.  Logits become
-// unsigned keys of the same order (a NaN largest, -0 and 0 alike), 0 for one
-// taken or none.
-template <int PER_LANE, int NT>
-__device__ void choose_tokens(const MoeParams& p, Routing& r) {
+// Step 2: the top experts of the tokens t0, t0 + step, ..., and their weights.
+__device__ void choose_experts(const MoeParams& p, Routing& r, int t0, int step, bool write) {
   const int lane = threadIdx.x & 31;
 #pragma unroll 1
-  for (int t0 = threadIdx.x >> 5; t0 < p.T; t0 += WARPS * NT) {
-    uint32_t key[NT][PER_LANE];
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int t = min(t0 + j * WARPS, p.T - 1);  // (past the end: the last, again)
-#pragma unroll
-      for (int i = 0; i < PER_LANE; ++i) {
-        const int e = lane + 32 * i;
-        const float v = e < p.E ? __ldcg(p.logits + t * p.E + e) + 0.f : 0.f;
-        const uint32_t b = __float_as_uint(v);
-        key[j][i] = e >= p.E ? 0u : v != v ? 0xffffffffu : b >> 31 ? ~b : b | 0x80000000u;
+  for (int t = t0; t < p.T; t += step) {
+    int e;
+    float w;
+    if (p.E <= 128)
+      choose_token<4>(p, t, e, w);
+    else
+      choose_token<MOE_MAX_EXPERTS / 32>(p, t, e, w);
+    if (lane < p.top) {
+      const int i = t * p.top + lane;
+      r.expert[i] = static_cast<int16_t>(e);
+      r.weight[i] = w;
+      if (write) {
+        p.experts[i] = e;
+        p.weights[i] = w;
       }
-    }
-    uint32_t chosen[NT], first[NT];
-#pragma unroll 1
-    for (int k = 0; k < p.top; ++k) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        uint32_t m = 0;
-#pragma unroll
-        for (int i = 0; i < PER_LANE; ++i) m = max(m, key[j][i]);
-        m = __reduce_max_sync(0xffffffffu, m);
-        uint32_t e = 0xffffffffu;
-#pragma unroll
-        for (int i = PER_LANE - 1; i >= 0; --i)
-          if (key[j][i] == m) e = lane + 32 * i;
-        e = __reduce_min_sync(0xffffffffu, e);
-#pragma unroll
-        for (int i = 0; i < PER_LANE; ++i)
-          if (e == static_cast<uint32_t>(lane + 32 * i)) key[j][i] = 0;
-        if (k == 0) first[j] = m;
-        if (lane == k) {
-          chosen[j] = m;
-          if (t0 + j * WARPS < p.T)
-            r.expert[(t0 + j * WARPS) * p.top + k] = static_cast<int16_t>(e);
-        }
-      }
-    }
-    auto logit = [](uint32_t key) {
-      return __uint_as_float(key == 0xffffffffu ? key : key >> 31 ? key & 0x7fffffffu : ~key);
-    };
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const float w = lane < p.top ? expf(logit(chosen[j]) - logit(first[j])) : 0.f;
-      float sum = w;
-#pragma unroll
-      for (int d = 8; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-      if (lane < p.top && t0 + j * WARPS < p.T) r.weight[(t0 + j * WARPS) * p.top + lane] = w / sum;
     }
   }
 }
 
-// Step 2, in every CTA alike: the top experts of each token, ties to the lowest
-// index, their weights, and the pairs sorted by expert.
-__device__ void route_choose(const MoeParams& p, Routing& r) {
+// Step 2, in every CTA alike: the pairs sorted by expert.
+__device__ void sort_pairs(const MoeParams& p, Routing& r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (p.E > 128)
-    choose_tokens<MOE_MAX_EXPERTS / 32, 1>(p, r);
-  else if (p.T > WARPS)
-    choose_tokens<4, 4>(p, r);
-  else
-    choose_tokens<4, 1>(p, r);
   const int pairs = p.T * p.top;
   for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[e] = 0;
   __syncthreads();
@@ -346,10 +359,6 @@ __device__ void route_choose(const MoeParams& p, Routing& r) {
     // an expert's pairs, from its list's end down, in any order: each is a
     // column of its own (this takes count to zero)
     r.list[r.offset[e] + atomicSub(&r.count[e], 1) - 1] = static_cast<int16_t>(i);
-    if (blockIdx.x == 0) {
-      p.experts[i] = e;
-      p.weights[i] = r.weight[i];
-    }
   }
   __syncthreads();
 }
@@ -461,7 +470,7 @@ __device__ __forceinline__ void consumers_sync() {
 }
 
 // All CTAs of the (cooperative) grid, by the consumer warps; bounded.
-__device__ void grid_barrier(Cta& c, uint32_t round) {
+__device__ __forceinline__ void grid_barrier(const Cta& c, uint32_t round) {
   consumers_sync();
   if (threadIdx.x == 32 && !*c.abort_flag) {
     __threadfence();
@@ -469,35 +478,39 @@ __device__ void grid_barrier(Cta& c, uint32_t round) {
     if (!absent) atomicAdd(c.p.control, 1u);
     const uint32_t want = round * gridDim.x;
     const uint64_t t0 = global_timer_ns();
-    volatile uint32_t* arrivals = c.p.control;
-    while (*arrivals < want) {
-      if (global_timer_ns() - t0 > c.p.wait_limit_ns) {
+    for (uint32_t n = 1;; ++n) {
+      uint32_t arrived;
+      asm volatile("ld.acquire.gpu.global.u32 %0, [%1];"
+                   : "=r"(arrived)
+                   : "l"(c.p.control)
+                   : "memory");
+      if (arrived >= want) break;
+      if ((n & 63u) == 0 && global_timer_ns() - t0 > c.p.wait_limit_ns) {
         c.give_up(kErrTimeoutGrid);
         break;
       }
     }
-    __threadfence();
   }
   consumers_sync();
 }
 
-// The weights of a plan's items, into the ring.  By one thread.
-__device__ bool produce(Cta& c, const CUtensorMap* map, const MoeProduct& m, const Plan& plan) {
+// The weights of a plan's items, into the ring.  By one warp, converged.
+__device__ __forceinline__ bool produce(Cta& c, const CUtensorMap* map, const MoeProduct& m, const Plan& plan) {
   for (int s = 0; s < plan.segments; ++s) {
     const Segment sg = plan.seg[s];
     for (int t = sg.tile; t < sg.tile + sg.items; ++t)
       for (int k = sg.k0; k < sg.k0 + sg.kn; ++k, ++c.it) {
         const uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
-        if (!mbar_wait_bounded(c.empty_bar(st), ph ^ 1u, c.p.wait_limit_ns, c.abort_flag)) {
-          c.give_up(kErrTimeoutProducer);
-          return false;
-        }
+        if (!c.wait(c.empty_bar(st), ph ^ 1u, kErrTimeoutProducer)) return false;
         const uint32_t bytes = static_cast<uint32_t>(min(2, m.kt - 2 * k)) * 512u;
         const uint32_t at = c.ring + st * RING_STAGE;
-        mbar_arrive_expect_tx(c.full_bar(st), W_BYTES + bytes);
-        tma_load_2d(at, map, c.full_bar(st), k * 128, t * 128);
-        bulk_load(at + W_BYTES, m.scales + (static_cast<int64_t>(t) * m.kt + 2 * k) * 512, bytes,
-                  c.full_bar(st));
+        if (elect_one()) {
+          mbar_arrive_expect_tx(c.full_bar(st), W_BYTES + bytes);
+          tma_load_2d(at, map, c.full_bar(st), k * 128, t * 128);
+          bulk_load(at + W_BYTES, m.scales + (static_cast<int64_t>(t) * m.kt + 2 * k) * 512, bytes,
+                    c.full_bar(st));
+        }
+        __syncwarp();
       }
   }
   return true;
@@ -514,8 +527,8 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
 // copies under way at once: of each pair and stage of 256 columns of K, TERMS
 // rows of 8 pieces of 16 bytes (row n's swizzled by n % 8), and their scales as
 // words of 4 into the tiles that tcgen05.cp takes.
-template <bool UP>
-__device__ void stage_columns(Cta& c, const MoeProduct& m, const Plan& plan, int run) {
+__device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m, const Plan& plan, bool up,
+                              int run) {
   const MoeParams& p = c.p;
   constexpr int COPIES = TERMS * 10, STRIDE = 64;  // 8 pieces and 2 words a row
   for (int s = 0; s < plan.segments; ++s) {
@@ -529,8 +542,8 @@ __device__ void stage_columns(Cta& c, const MoeProduct& m, const Plan& plan, int
       const int col = task / sg.kn, stage = task - col * sg.kn;
       const int pair = c.r.list[sg.first + col];
       const uint8_t* src =
-          UP ? p.x_terms + (static_cast<int64_t>(pair / p.top) * m.stages + sg.k0 + stage) * PIECE
-             : p.h_terms + (static_cast<int64_t>(pair) * m.stages + sg.k0 + stage) * PIECE;
+          (up ? p.x_terms : p.h_terms) +
+          (static_cast<int64_t>(up ? pair / p.top : pair) * m.stages + sg.k0 + stage) * PIECE;
       if (copy < TERMS * 8) {
         const int n = col * TERMS + (copy >> 3), block = copy & 7;
         cp_async_16(codes + (stage * rows + n) * 128 + ((block ^ (n & 7)) << 4), src + copy * 16);
@@ -545,8 +558,10 @@ __device__ void stage_columns(Cta& c, const MoeProduct& m, const Plan& plan, int
 }
 
 // Step 3b, the consumers of the grid: h of every pair as terms, from the parts'
-// sums of gate and up in their order.
-__device__ void make_h(const Cta& c) {
+// sums of gate and up in their order.  (The fast exponential and division are
+// off by some 2^-21 of silu, a quarter of what two roundings of the sums are; in
+// the exact ones' code the step spent its time on fetching instructions.)
+__device__ __forceinline__ void make_h(const Cta& c) {
   const MoeParams& p = c.p;
   const int64_t part = static_cast<int64_t>(p.T) * p.top * p.up.pitch;
   const int half = p.up.pitch / 2, tasks = p.T * p.top * p.down.stages;
@@ -571,13 +586,14 @@ __device__ void make_h(const Cta& c) {
     float h[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      h[j] = k + j < p.I ? gate[j] / (1.f + expf(-gate[j])) * value[j] : 0.f;
-    split_terms(h, p.h_terms + static_cast<int64_t>(i) * PIECE, c.lane);
+      h[j] = k + j < p.I ? __fdividef(gate[j], 1.f + __expf(-gate[j])) * value[j] : 0.f;
+    split_terms(h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7],
+                p.h_terms + static_cast<int64_t>(i) * PIECE);
   }
 }
 
 // The MMAs of a segment, by one warp.
-__device__ bool multiply(Cta& c, const MoeProduct& m, const Segment& sg) {
+__device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segment& sg) {
   const int rows = staged_rows(sg.count);
   const uint32_t id0 = make_idesc_mxf4(128, rows, 0), id2 = make_idesc_mxf4(128, rows, 2);
   const uint32_t scales = desc_lo(smem_u32(c.staged) + sg.offset);
@@ -620,8 +636,7 @@ __device__ bool multiply(Cta& c, const MoeProduct& m, const Segment& sg) {
 
 // A segment's sums out of TMEM: the terms of a column added, smallest first, one
 // matrix row a lane.  By four warps.
-template <bool UP>
-__device__ bool write_sums(Cta& c, const MoeProduct& m, const Segment& sg) {
+__device__ __forceinline__ bool write_sums(Cta& c, const MoeProduct& m, const Segment& sg, bool up) {
   const int q = c.warp & 3;
   const int pairs = c.p.T * c.p.top;
   const int64_t row0 = static_cast<int64_t>(sg.expert) * m.rows;
@@ -633,7 +648,7 @@ __device__ bool write_sums(Cta& c, const MoeProduct& m, const Segment& sg) {
     const int64_t row = static_cast<int64_t>(sg.tile + t) * 128 + q * 32 + c.lane - row0;
     const bool in = row >= 0 && row < m.rows;
     // up: gate rows, then up rows at half the pitch
-    const int at = static_cast<int>(UP && row >= c.p.I ? row - c.p.I + m.pitch / 2 : row);
+    const int at = static_cast<int>(up && row >= c.p.I ? row - c.p.I + m.pitch / 2 : row);
     float* sums = m.sums + static_cast<int64_t>(sg.part) * pairs * m.pitch + at;
     for (int c0 = 0; c0 < sg.count; c0 += 4) {  // 4 columns: 24 TMEM columns
       uint32_t v[3][8];
@@ -658,13 +673,12 @@ __device__ bool write_sums(Cta& c, const MoeProduct& m, const Segment& sg) {
 }
 
 // Steps 3 and 4, by the consumer warps.
-template <bool UP>
-__device__ void product(Cta& c, const MoeProduct& m, const Plan& plan) {
+__device__ __forceinline__ void product(Cta& c, const MoeProduct& m, const Plan& plan, bool up) {
   const int runs = plan.segments ? plan.seg[plan.segments - 1].run + 1 : 0;
   int s = 0;
   for (int run = 0; run < runs; ++run) {
     if (run) consumers_sync();  // the columns staged before have been read
-    if (!*c.abort_flag) stage_columns<UP>(c, m, plan, run);
+    if (!*c.abort_flag) stage_columns(c, m, plan, up, run);
     fence_proxy_async_smem();
     consumers_sync();
     bool ok = !*c.abort_flag;
@@ -673,7 +687,7 @@ __device__ void product(Cta& c, const MoeProduct& m, const Plan& plan) {
       if (c.warp == 1) {
         ok = multiply(c, m, plan.seg[s]);
       } else if (c.warp >= 4 && c.warp < 8) {
-        ok = write_sums<UP>(c, m, plan.seg[s]);
+        ok = write_sums(c, m, plan.seg[s], up);
       }
     }
     // The MMA warp waits for its own, which read the staged columns.
@@ -684,7 +698,7 @@ __device__ void product(Cta& c, const MoeProduct& m, const Plan& plan) {
 
 // Step 5, the consumers of the grid: a token's pairs added in their order,
 // four rows a thread.
-__device__ void combine(const Cta& c) {
+__device__ __forceinline__ void combine(const Cta& c) {
   const MoeParams& p = c.p;
   const int quads = (p.H + 3) / 4, n = p.T * quads;
   const int64_t part = static_cast<int64_t>(p.T) * p.top * p.down.pitch;
@@ -713,7 +727,8 @@ __device__ void combine(const Cta& c) {
 
 __global__ void __launch_bounds__(THREADS, 1)
     moe_mxfp4_kernel(const __grid_constant__ CUtensorMap tm_up,
-                     const __grid_constant__ CUtensorMap tm_down, const MoeParams p) {
+                     const __grid_constant__ CUtensorMap tm_down,
+                     const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ Routing r;
   __shared__ alignas(8) uint64_t bars[2 * STAGES + 4];
@@ -748,8 +763,23 @@ __global__ void __launch_bounds__(THREADS, 1)
   c.tmem = tmem_slot;
   if (c.warp) grid_barrier(c, 1);
   __syncthreads();
+  uint32_t round = 2;
+  if (p.T <= WARPS) {  // every CTA chooses for all tokens, a warp one token
+    if (!abort_flag) choose_experts(p, r, c.warp, WARPS, blockIdx.x == 0);
+  } else {
+    // a warp of the grid each, then a barrier (64 tokens in every CTA took 5.4 us)
+    if (!abort_flag && c.warp)
+      choose_experts(p, r, blockIdx.x + (c.warp - 1) * gridDim.x, CONSUMERS / 32 * gridDim.x, true);
+    if (c.warp) grid_barrier(c, round++);
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.T * p.top && !abort_flag; i += THREADS) {
+      r.expert[i] = static_cast<int16_t>(__ldcg(p.experts + i));
+      r.weight[i] = __ldcg(p.weights + i);
+    }
+  }
+  __syncthreads();
   if (!abort_flag) {
-    route_choose(p, r);
+    sort_pairs(p, r);
     if (c.warp == 0) plan_product(p, p.up, r, r.up);
     if (c.warp == 1) plan_product(p, p.down, r, r.down);
   } else if (threadIdx.x == 0) {
@@ -759,8 +789,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (c.warp == 0) {
     // The producer runs ahead through both products: weights wait for nothing
     // but their place in the ring.
+    bool ok = true;
+#pragma unroll 1
+    for (int i = 0; ok && i < 2; ++i)
+      ok = produce(c, i ? &tm_down : &tm_up, i ? p.down : p.up, i ? r.down : r.up);
     if (c.lane == 0) {
-      if (produce(c, &tm_up, p.up, r.up)) produce(c, &tm_down, p.down, r.down);
       volatile int never = 0;  // its copies in flight have landed before it leaves
       for (uint32_t i = c.it > STAGES ? c.it - STAGES : 0; i < c.it; ++i)
         if (!mbar_wait_bounded(c.full_bar(i % STAGES), (i / STAGES) & 1u, p.wait_limit_ns, &never))
@@ -768,13 +801,18 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     __syncwarp();
   } else {
-    product<true>(c, p.up, r.up);
-    grid_barrier(c, 2);
-    if (!abort_flag) make_h(c);
-    grid_barrier(c, 3);
-    product<false>(c, p.down, r.down);
-    grid_barrier(c, 4);
-    if (!abort_flag) combine(c);
+    // up, barrier, h, barrier; down, barrier, sum
+#pragma unroll 1
+    for (int i = 0; i < 2; ++i) {
+      product(c, i ? p.down : p.up, i ? r.down : r.up, i == 0);
+      grid_barrier(c, round++);
+      if (i == 0) {
+        if (!abort_flag) make_h(c);
+        grid_barrier(c, round++);
+      } else if (!abort_flag) {
+        combine(c);
+      }
+    }
     if (c.warp == 1 && c.it > 0) {  // the last MMAs issued have finished
       volatile int never = 0;
       if (!mbar_wait_bounded(c.empty_bar((c.it - 1) % STAGES), ((c.it - 1) / STAGES) & 1u,

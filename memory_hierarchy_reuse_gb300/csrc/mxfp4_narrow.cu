@@ -176,41 +176,55 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
   auto sf_bytes = [&](int kb) { return static_cast<uint32_t>(min(2, p.kt - 2 * kb)) * 512u; };
 
   if (warp == 0) {
-    if (lane == 0) {
-      auto load_b = [&](uint32_t st, uint32_t bar, int kb) {
-        tma_load_2d(st, &tmB, bar, kb * BK_BYTES, n0);
-        bulk_load(st + off_sfb, p.sfb + (static_cast<int64_t>(n0 / 128) * p.kt + 2 * kb) * 512,
-                  sf_bytes(kb), bar);
-      };
-      auto load_a = [&](uint32_t st, uint32_t bar, int kb) {
-        if (PLAIN) return;
-        tma_load_2d(st + off_x, &tmA, bar, kb * BK_BYTES, m0);
-        bulk_load(st + off_sfa, p.sfa + (static_cast<int64_t>(m0 / 128) * p.kt + 2 * kb) * 512,
-                  sf_bytes(kb), bar);
-      };
-      auto tx = [&](int kb) { return W_BYTES + x_bytes + (PLAIN ? 1u : 2u) * sf_bytes(kb); };
-      const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
-      // The first stages' B before the kernel before this one (A's
-      // quantisation) has finished, where that is known not to write B.
-      const int ahead = min(p.stages, kb1 - kb0);
-      for (int i = 0; i < ahead; ++i) mbar_arrive_expect_tx(full_bar(i), tx(kb0 + i));
-      if (!p.early_b) grid_dependency_wait();
-      for (int i = stall ? 1 : 0; i < ahead; ++i)
-        load_b(sbase + i * p.stage_bytes, full_bar(i), kb0 + i);
-      if (p.early_b) grid_dependency_wait();
+    auto load_b = [&](uint32_t st, uint32_t bar, int kb) {
+      tma_load_2d(st, &tmB, bar, kb * BK_BYTES, n0);
+      bulk_load(st + off_sfb, p.sfb + (static_cast<int64_t>(n0 / 128) * p.kt + 2 * kb) * 512,
+                sf_bytes(kb), bar);
+    };
+    auto load_a = [&](uint32_t st, uint32_t bar, int kb) {
+      if (PLAIN) return;
+      tma_load_2d(st + off_x, &tmA, bar, kb * BK_BYTES, m0);
+      bulk_load(st + off_sfa, p.sfa + (static_cast<int64_t>(m0 / 128) * p.kt + 2 * kb) * 512,
+                sf_bytes(kb), bar);
+    };
+    auto tx = [&](int kb) { return W_BYTES + x_bytes + (PLAIN ? 1u : 2u) * sf_bytes(kb); };
+    const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
+    // The first stages' B before the kernel before this one (A's quantisation)
+    // has finished, where that is known not to write B.
+    const int ahead = min(p.stages, kb1 - kb0);
+    if (!p.early_b) grid_dependency_wait();
+    if (elect_one()) {
+      for (int i = 0; i < ahead; ++i) {
+        mbar_arrive_expect_tx(full_bar(i), tx(kb0 + i));
+        if (!(stall && i == 0)) load_b(sbase + i * p.stage_bytes, full_bar(i), kb0 + i);
+      }
+    }
+    __syncwarp();
+    if (p.early_b) grid_dependency_wait();
+    if (elect_one()) {
       for (int i = stall ? 1 : 0; i < ahead; ++i)
         load_a(sbase + i * p.stage_bytes, full_bar(i), kb0 + i);
-      int it = ahead;
-      for (; kb0 + it < kb1; ++it) {
-        const uint32_t s = it % p.stages, ph = (it / p.stages) & 1u;
-        if (!mbar_wait_bounded(empty_bar(s), ph ^ 1u, limit, &abort_flag)) {
-          give_up(kErrTimeoutProducer);
-          break;
-        }
+    }
+    __syncwarp();
+    int it = ahead;
+    uint32_t s = 0, ph = 0;  // of the stage to fill again: its first MMAs done
+    for (; kb0 + it < kb1; ++it) {
+      if (!__all_sync(0xffffffffu, mbar_wait_bounded(empty_bar(s), ph, limit, &abort_flag))) {
+        if (lane == 0) give_up(kErrTimeoutProducer);
+        break;
+      }
+      if (elect_one()) {
         mbar_arrive_expect_tx(full_bar(s), tx(kb0 + it));
         load_b(sbase + s * p.stage_bytes, full_bar(s), kb0 + it);
         load_a(sbase + s * p.stage_bytes, full_bar(s), kb0 + it);
       }
+      __syncwarp();
+      if (++s == static_cast<uint32_t>(p.stages)) {
+        s = 0;
+        ph ^= 1u;
+      }
+    }
+    if (lane == 0) {
       // This CTA's copies in flight have landed before it goes on to leave.
       volatile int never = 0;
       for (int i = max(0, it - p.stages); i < it; ++i) {

@@ -469,10 +469,13 @@ bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t kt
 
 }  // namespace
 
-// Tile columns.  A tile takes num_kb stages of c0 + c1 bn and ends; the time is
-// that of the busiest cluster.  Narrower tiles fill a last round better and put
-// more clusters to work on few tiles; wider ones do more with a stage's fixed
-// part.
+// Tile columns.  The time is that of the busiest cluster: its rounds of tiles of
+// num_kb stages, each a fixed part and one that grows with the columns, and the
+// last tile's epilogue.  GB300, a stage of 256 / 192 / 128 columns with all
+// clusters at work (8192^3): 0.347 / 0.282 / 0.255 us, that is 226 + bn units of
+// 0.72 ns.  Narrower tiles put more clusters to work on few tiles (2000 x 300 x
+// 4000: 11.3 us with 128 columns, 15.4 with 256) and wider ones do more with a
+// stage's fixed part (8192^3: 155 us with 256, 220 with 128).
 int plan_pair_bn(int64_t M, int64_t N, int64_t K, int clusters) {
   const int64_t stages = (scale_tiles(K) + 1) / 2;
   int best = MAX_BN;
@@ -480,7 +483,7 @@ int plan_pair_bn(int64_t M, int64_t N, int64_t K, int clusters) {
   for (int bn = MAX_BN; bn >= 128; bn -= 64) {
     const int64_t tiles = (M + TILE_M - 1) / TILE_M * ((N + bn - 1) / bn);
     const int64_t rounds = (tiles + clusters - 1) / clusters;
-    const double t = static_cast<double>(rounds) * stages * (180.0 + 2.0 * bn) + 6.0 * bn;
+    const double t = static_cast<double>(rounds) * stages * (226.0 + bn) + 6.0 * bn;
     if (bn == MAX_BN || t < best_t) {
       best_t = t;
       best = bn;
