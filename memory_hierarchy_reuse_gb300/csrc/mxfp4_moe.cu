@@ -50,9 +50,10 @@ constexpr int RING_BYTES = STAGES * RING_STAGE;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MAX_SEGMENTS = 160;
 constexpr int PIECE = TERMS * (128 + 8);       // 256 columns of K as terms: codes, then scales
-constexpr uint32_t ACC_COLS = 128;             // TMEM: two accumulators, two sets of scales
+constexpr uint32_t ACC_COLS = 128;             // TMEM: two accumulators, scales of each stage
 constexpr uint32_t SF_COL = 2 * ACC_COLS;
 constexpr uint32_t TMEM_COLS = 512;
+static_assert(SF_COL + STAGES * 16 <= TMEM_COLS, "scales fit");
 constexpr uint32_t kErrTimeoutGrid = 1u << 4;  // status word: a grid barrier's wait ran out
 
 // One of the two products: rows of an expert in the packed matrix, K, and the
@@ -605,16 +606,13 @@ __device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segm
     const uint32_t d = c.tmem + b * ACC_COLS;
     for (int k = 0; k < sg.kn; ++k, ++c.it) {
       const uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
-      // scales alternate between two sets of TMEM columns: the MMAs two stages
-      // back, which read this set last, have finished
-      if ((c.it >= 2 &&
-           !c.wait(c.empty_bar((c.it - 2) % STAGES), ((c.it - 2) / STAGES) & 1u, kErrTimeoutMma)) ||
-          !c.wait(c.full_bar(st), ph, kErrTimeoutMma))
-        return false;
+      // (a stage's scales have TMEM columns of their own: whoever read them last
+      // had finished before the producer filled the stage again)
+      if (!c.wait(c.full_bar(st), ph, kErrTimeoutMma)) return false;
       tc_fence_after();
       const uint32_t w = desc_lo(c.ring + st * RING_STAGE), cw = w + (W_BYTES >> 4);
       const uint32_t x = codes + k * rows * (128 >> 4), cx = scales + k * (1024 >> 4);
-      const uint32_t sfw = c.tmem + SF_COL + (c.it & 1u) * 16, sfx = sfw + 8;
+      const uint32_t sfw = c.tmem + SF_COL + st * 16, sfx = sfw + 8;
       const int kb = sg.k0 + k;
       const int tiles = min(2, m.kt - 2 * kb), mmas = min(4, (m.blocks - kb * 8 + 1) / 2);
       if (elect_one()) {

@@ -34,6 +34,7 @@ constexpr int PLAIN_ROWS = 8;
 constexpr int PLAIN_BYTES = 32 * 1024;  // of the quantised part of A
 constexpr int MAX_SPLIT = 8;
 constexpr int SMEM_LIMIT = 227 * 1024;
+constexpr uint32_t TMEM_COLS = 256;     // so that two CTAs fit an SM
 constexpr int PAIR_NT = 32;             // up to this many rows two CTAs share an SM
 
 struct NarrowParams {
@@ -43,6 +44,7 @@ struct NarrowParams {
   int32_t num_kb;          // stages of 256 columns in K
   int32_t blocks, kt;      // blocks of 32 in K; scale tiles a row
   int32_t stages, stage_bytes;
+  uint32_t sf_col;         // TMEM: the accumulator, then 16 columns of scales a stage
   int32_t early_b;         // B is not written by the kernel before this one
   const void* a;           // plain A, its pitch, and whether its rows take 16-byte loads
   int64_t lda;
@@ -143,7 +145,6 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
   const int n0 = (tile - tile_m * p.tiles_n) * W_ROWS, m0 = tile_m * p.nt;
   const int kb0 = static_cast<int>(static_cast<int64_t>(p.num_kb) * rank / p.split);
   const int kb1 = static_cast<int>(static_cast<int64_t>(p.num_kb) * (rank + 1) / p.split);
-  constexpr uint32_t TMEM_COLS = 256;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.stages; ++s) {
@@ -239,14 +240,13 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
     __syncwarp();
   } else if (warp == 1) {
     const uint32_t id0 = make_idesc_mxf4(W_ROWS, p.nt, 0), id2 = make_idesc_mxf4(W_ROWS, p.nt, 2);
-    uint32_t s = 0, ph = 0, s2 = p.stages - 2, ph2 = 1;  // ring position; two stages back
+    uint32_t s = 0, ph = 0;  // ring position
     bool ready = true;
     if (PLAIN) ready = mbar_wait_bounded(a_bar, 0, limit, &abort_flag);
     for (int it = 0; kb0 + it < kb1; ++it) {
-      // scales alternate between two sets of TMEM columns: the MMAs two
-      // stages back, which read this set last, have finished
-      const bool ok = ready && (it < 2 || mbar_wait_bounded(empty_bar(s2), ph2, limit, &abort_flag)) &&
-                      mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag);
+      // (a stage's scales have TMEM columns of their own: whoever read them
+      // last had finished before the producer filled the stage again)
+      const bool ok = ready && mbar_wait_bounded(full_bar(s), ph, limit, &abort_flag);
       if (!__all_sync(0xffffffffu, ok)) {
         if (lane == 0) give_up(kErrTimeoutMma);
         break;
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
       const uint32_t x = PLAIN ? part + (((kb1 - kb0) * SF_BYTES + it * p.nt * BK_BYTES) >> 4)
                                : w + (off_x >> 4);
       const uint32_t ca = PLAIN ? part + ((it * SF_BYTES) >> 4) : w + (off_sfa >> 4);
-      const uint32_t sfb = tmem + MAX_NT + (it & 1) * 16, sfa = sfb + 8;
+      const uint32_t sfb = tmem + p.sf_col + s * 16, sfa = sfb + 8;
       const int tiles = min(2, p.kt - 2 * kb), mmas = min(4, (p.blocks - kb * 8 + 1) / 2);
       if (elect_one()) {
         for (int i = 0; i < tiles; ++i) {
@@ -274,10 +274,6 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
       if (++s == static_cast<uint32_t>(p.stages)) {
         s = 0;
         ph ^= 1u;
-      }
-      if (++s2 == static_cast<uint32_t>(p.stages)) {
-        s2 = 0;
-        ph2 ^= 1u;
       }
     }
     if (elect_one()) mma_commit(acc_bar);
@@ -439,6 +435,9 @@ cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream
                    (plain ? p.a_bytes : 0);
   p.stage_bytes = W_BYTES + (plain ? SF_BYTES : p.nt * BK_BYTES + 2 * SF_BYTES);
   p.stages = room / p.stage_bytes;
+  p.sf_col = (p.nt + 31) / 32 * 32;
+  const int sets = static_cast<int>(TMEM_COLS - p.sf_col) / 16;
+  if (p.stages > sets) p.stages = sets;
   if (p.stages > MAX_STAGES) p.stages = MAX_STAGES;
   p.early_b = a.after_quantize;
   p.sfa = a.sfa;

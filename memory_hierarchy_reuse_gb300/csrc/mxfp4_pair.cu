@@ -116,6 +116,8 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr uint32_t acc1 = overlap ? MAX_BN - OVERLAP : BN;  // the second accumulator
   constexpr int SF_TILES = sf_tiles(BN);
   constexpr uint32_t sf_set = 8 + 8 * SF_TILES;               // columns of a set of scales
+  constexpr uint32_t SF_SETS = overlap ? 2 : STAGES;
+  static_assert(acc1 + BN + SF_SETS * sf_set <= TMEM_COLS, "TMEM");
   constexpr uint32_t stage_tx = OP_BYTES + BN / 2 * BK_BYTES + 1024 * (1 + SF_TILES);
   const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&abort_flag)), rank ^ 1u);
 
@@ -257,13 +259,16 @@ __global__ void __launch_bounds__(THREADS, 1)
           sf_row = (tn * BN & 127) >> 5;
         }
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
-          // scales alternate between two sets of columns: the MMAs two stages
-          // back, the last to read this set, have finished
-          // (both barriers polled once together; mostly that is all)
+          // A stage's scales have columns of their own -- whoever read them last
+          // had finished before the stage was filled again -- or alternate
+          // between two sets: then the MMAs two stages back, the last to read
+          // this one, have to have finished.  (Both barriers polled once
+          // together; mostly that is all.)
+          const bool older = SF_SETS < STAGES && it >= 2;
           bool there = mbar_try_wait(full_bar(s), ph);
-          there = (it < 2 || mbar_try_wait(empty_bar(s2), ph2)) && there;
+          there = (!older || mbar_try_wait(empty_bar(s2), ph2)) && there;
           if (!__all_sync(0xffffffffu, there) &&
-              ((it >= 2 && !wait(empty_bar(s2), ph2)) || !wait(full_bar(s), ph))) {
+              ((older && !wait(empty_bar(s2), ph2)) || !wait(full_bar(s), ph))) {
             if (lane == 0) give_up(kErrTimeoutMma);
             ok = false;
             break;
@@ -272,7 +277,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t st = sbase + s * STAGE_BYTES;
           const uint32_t a = desc_lo(st), bb = a + (OFF_B >> 4);
           const uint32_t ca = a + (OFF_SFA >> 4), cb = a + (OFF_SFB >> 4);
-          const uint32_t sfa = tmem + TMEM_COLS - (1 + (it & 1u)) * sf_set, sfb = sfa + 8;
+          const uint32_t sfa = tmem + acc1 + BN + (SF_SETS < STAGES ? it & 1u : s) * sf_set;
+          const uint32_t sfb = sfa + 8;
           const uint32_t first = kb > 0 ? 1u : 0u;
           const bool full = kb + 1 < p.num_kb || tail == 4;
           if (elect_one()) {
