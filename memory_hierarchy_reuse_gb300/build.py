@@ -2,7 +2,8 @@
 
 Each translation unit is compiled in parallel, then linked into a shared
 library inside this package directory (the CUDA runtime is linked statically,
-so the library needs only the NVIDIA driver at run time).
+so the library needs only the NVIDIA driver at run time). Beside it g++ compiles
+the tensor-level calls' binding (_torch_binding.so) against the installed torch.
 """
 from __future__ import annotations
 
@@ -21,6 +22,8 @@ LIB = os.path.join(PKG, "libmhr_gemm.so")
 SOURCES = ["api.cu", "simt_f32.cu", "tc_gemm.cu", "tc_gemm_1cta.cu", "tc_gemm_pair.cu",
            "tc_prepass.cu", "noalloc.cu", "ladder.cu", "mxfp4_api.cu", "mxfp4_quantize.cu",
            "mxfp4_narrow.cu", "mxfp4_pair.cu", "mxfp4_moe.cu"]
+BINDING = os.path.join(PKG, "_torch_binding.so")
+BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -38,10 +41,33 @@ def _inputs() -> list[str]:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _build_binding() -> None:
+    """The torch binding: host code only, against torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    lib = os.path.join(root, "lib")
+    tmp = BINDING + f".tmp{os.getpid()}"
+    cmd = ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(root, "include"),
+           "-I", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-I", os.path.join(cuda, "include"), "-I", sysconfig.get_paths()["include"],
+           "-I", INCLUDE, BINDING_SOURCE, "-o", tmp, "-L", lib, f"-Wl,-rpath,{lib}",
+           "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on torch_binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
@@ -65,8 +91,10 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        binding = ex.submit(_build_binding)
         objs = list(ex.map(compile_one, SOURCES))
+        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
