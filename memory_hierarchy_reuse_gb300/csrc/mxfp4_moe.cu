@@ -382,7 +382,7 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
     return ai + 1 < active ? static_cast<int>(r.offset[r.active[ai + 1]]) : pairs;
   };
   const int most = min(r.most, MAX_COLS);
-  // Time of the longest run, in stages, with half a stage for an item's ends;
+  // Time of the longest run, in stages, with a quarter of one for an item's ends;
   // parts that are too long to stage all columns at once count twice.
   const int parts = lane + 1;
   uint32_t cost = 0xffffffffu;
@@ -390,7 +390,7 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
     const uint32_t items = static_cast<uint32_t>(active) * parts * m.tiles;
     const uint32_t longest = (items + gridDim.x - 1) / gridDim.x;
     const int stages = (m.stages + parts - 1) / parts;
-    cost = longest * (2 * stages + 1) * 32;
+    cost = longest * (4 * stages + 1) * 32;
     if (staged_bytes(most, stages) > p.stage_bytes) cost *= 2;
     cost = min(cost, 0x7ffffffu) / 32 * 32 + lane;  // ties: the fewest parts
   }

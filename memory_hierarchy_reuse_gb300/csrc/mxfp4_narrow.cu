@@ -54,7 +54,7 @@ struct NarrowParams {
   const uint8_t* sfb;
   void* C;
   int64_t ldc;
-  int32_t c_dtype;
+  int32_t c_dtype, vec_c;  // vec_c: 4 columns of C from a multiple of 4 on may be stored at once
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t inject_stall;
@@ -67,6 +67,34 @@ __device__ __forceinline__ void store_c(const NarrowParams& p, int64_t at, float
     static_cast<__nv_bfloat16*>(p.C)[at] = __float2bfloat16_rn(v);
   else
     static_cast<__half*>(p.C)[at] = __float2half_rn(v);
+}
+
+// Four neighbouring columns, the first `left` of them.
+__device__ __forceinline__ void store_c4(const NarrowParams& p, int64_t at, int left,
+                                         const float (&v)[4]) {
+  if (p.vec_c && left >= 4) {
+    if (p.c_dtype == MHR_F32) {
+      *reinterpret_cast<float4*>(static_cast<float*>(p.C) + at) =
+          make_float4(v[0], v[1], v[2], v[3]);
+      return;
+    }
+    uint32_t w[2];
+    if (p.c_dtype == MHR_BF16) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]);
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2], v[3]);
+      w[0] = *reinterpret_cast<const uint32_t*>(&a);
+      w[1] = *reinterpret_cast<const uint32_t*>(&b);
+    } else {
+      const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
+      w[0] = *reinterpret_cast<const uint32_t*>(&a);
+      w[1] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.C) + at) = make_uint2(w[0], w[1]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (i < left) store_c(p, at + i, v[i]);
 }
 
 // 8 values of a row from column k on; zeros past the end.
@@ -324,24 +352,25 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
       const int quads = min(p.nt, p.M - m0) * (W_ROWS / 4);
       for (int g = rank * 128 + threadIdx.x - 64; g < quads; g += p.split * 128) {
         const uint32_t addr = sbase + g * 16;
-        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int r = 0; r < p.split; ++r) {
-          float4 v;
-          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                       : "r"(mapa_shared(addr, r))
-                       : "memory");
-          sum.x += v.x;
-          sum.y += v.y;
-          sum.z += v.z;
-          sum.w += v.w;
-        }
+        float4 part[MAX_SPLIT];  // (all reads on their way before the first is added)
+#pragma unroll
+        for (int r = 0; r < MAX_SPLIT; ++r)
+          if (r < p.split)
+            asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                         : "=f"(part[r].x), "=f"(part[r].y), "=f"(part[r].z), "=f"(part[r].w)
+                         : "r"(mapa_shared(addr, r))
+                         : "memory");
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int r = 0; r < MAX_SPLIT; ++r)
+          if (r < p.split) {
+            sum[0] += part[r].x;
+            sum[1] += part[r].y;
+            sum[2] += part[r].z;
+            sum[3] += part[r].w;
+          }
         const int m = m0 + g / (W_ROWS / 4), n = n0 + g % (W_ROWS / 4) * 4;
-        const int64_t at = static_cast<int64_t>(m) * p.ldc + n;
-        if (n < p.N) store_c(p, at, sum.x);
-        if (n + 1 < p.N) store_c(p, at + 1, sum.y);
-        if (n + 2 < p.N) store_c(p, at + 2, sum.z);
-        if (n + 3 < p.N) store_c(p, at + 3, sum.w);
+        store_c4(p, static_cast<int64_t>(m) * p.ldc + n, p.N - n, sum);
       }
     }
     cluster_sync_all();  // no CTA leaves while another reads its partial sums
@@ -449,6 +478,8 @@ cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream
   p.C = a.C;
   p.ldc = a.ldc;
   p.c_dtype = a.c_dtype;
+  const int64_t c_size = a.c_dtype == MHR_F32 ? 4 : 2;
+  p.vec_c = reinterpret_cast<uintptr_t>(a.C) % (4 * c_size) == 0 && a.ldc % 4 == 0;
   p.status = ctl.status;
   p.wait_limit_ns = ctl.wait_limit_ns;
   p.inject_stall = ctl.inject_stall;
