@@ -63,10 +63,21 @@ cudaError_t zero_c(int c_dtype, void* C, int64_t M, int64_t N, int64_t ldc, cuda
                            static_cast<size_t>(M), s);
 }
 
-cudaError_t launch_product(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
+// Up to 32 rows the narrow kernel runs, two CTAs an SM (GB300, narrow against
+// pair: 32 x 4096 x 4096 7.3 / 8.6 us, 32 x 28672 x 4096 13.8 / 18.0); more by the
+// two kernels' estimates (64 x 4096 x 4096 7.7 / 8.7, 64 x 28672 x 4096 23.1 /
+// 16.0; 200 x 300 x 8192 8.0 / 13.2, 128 x 4096 x 4096 9.4 / 9.0).
+// gemm_testing_set_cta_pair_mode picks a kernel, as for the other products.
+cudaError_t launch_product(const ProductArgs& a, const DeviceCtl& ctl, int device,
+                           cudaStream_t s) {
+  bool pair = ctl.pair_mode == 2;
+  if (ctl.pair_mode == 0 && a.M > 32) {
+    double narrow = 0;
+    const cudaError_t e = narrow_time(a.M, a.N, a.K, ctl.sm_count, device, &narrow);
+    if (e != cudaSuccess) return e;
+    pair = pair_time(a.M, a.N, a.K, ctl.sm_count / 2) < narrow;
+  }
   MainKernelEvents ev(s);
-  // (gemm_testing_set_cta_pair_mode picks a kernel, as for the other products)
-  const bool pair = ctl.pair_mode ? ctl.pair_mode == 2 : a.M > 64;
   return pair ? launch_pair(a, ctl, s) : launch_narrow(a, ctl, s);
 }
 
@@ -124,7 +135,7 @@ MHR_API int gemm_mxfp4(int c_dtype, const uint8_t* A, const uint8_t* A_scales, c
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0) return from_cuda(zero_c(c_dtype, C, M, N, ldc, s));
   return from_cuda(launch_product(
-      {A, A_scales, lda, Bt, Bt_scales, ldb, C, ldc, c_dtype, M, N, K, false}, ctl, s));
+      {A, A_scales, lda, Bt, Bt_scales, ldb, C, ldc, c_dtype, M, N, K, false}, ctl, dev, s));
 }
 
 MHR_API int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const uint8_t* Bt,
@@ -146,11 +157,15 @@ MHR_API int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const 
   if (const int st = device_ctl_locked(&ctl, &dev); st != MHR_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (K == 0) return from_cuda(zero_c(c_dtype, C, M, N, ldc, s));
-  if (ctl.pair_mode != 2 && narrow_quantizes(M, N, K, ctl.sm_count)) {
+  bool fused = false;
+  if (ctl.pair_mode != 2)
+    if (const cudaError_t e = narrow_quantizes(M, N, K, a_dtype, dev, &fused); e != cudaSuccess)
+      return from_cuda(e);
+  if (fused) {
     ProductArgs a{nullptr, nullptr, lda, Bt, Bt_scales, ldb, C, ldc, c_dtype, M, N, K};
     a.a_plain = A;
     a.a_dtype = a_dtype;
-    return from_cuda(launch_product(a, ctl, s));
+    return from_cuda(launch_product(a, ctl, dev, s));
   }
   const int64_t row_bytes = blocks_of(K) * 16;
   size_t data_bytes;
@@ -166,7 +181,7 @@ MHR_API int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const 
       launch_quantize(a_dtype, A, M, K, lda, false, data, row_bytes, scales, nullptr, 0, s);
   if (e == cudaSuccess)
     e = launch_product(
-        {data, scales, row_bytes, Bt, Bt_scales, ldb, C, ldc, c_dtype, M, N, K, true}, ctl, s);
+        {data, scales, row_bytes, Bt, Bt_scales, ldb, C, ldc, c_dtype, M, N, K, true}, ctl, dev, s);
   workspace_done_locked(token, s);
   return from_cuda(e);
 }

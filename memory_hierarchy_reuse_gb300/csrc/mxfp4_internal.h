@@ -49,7 +49,11 @@ struct ProductArgs {
 };
 // Whether launch_narrow takes a plain A and quantises it on the way: at most
 // 8 rows whose part of K fits beside the ring.
-bool narrow_quantizes(int64_t M, int64_t N, int64_t K, int sms);
+cudaError_t narrow_quantizes(int64_t M, int64_t N, int64_t K, int a_dtype, int device, bool* yes);
+// What either kernel takes for a product of packed operands, in us: fits of the
+// times measured on GB300, for the choice between the two.
+cudaError_t narrow_time(int64_t M, int64_t N, int64_t K, int sms, int device, double* us);
+double pair_time(int64_t M, int64_t N, int64_t K, int clusters);
 // Few rows of A (any M is right).
 cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s);
 // Many rows of A: CTA pairs on 256 x 256 tiles (any M is right).

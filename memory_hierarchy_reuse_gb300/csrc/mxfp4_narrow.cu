@@ -385,18 +385,64 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
 
 namespace {
 
+// (static state: by device, under the library's lock)
+// CTAs that run at once in clusters of `split`, one an SM.  (Clusters pack into an
+// SM group or leave some of its SMs out, so it is less than the SMs: of 128 CTAs
+// in clusters of 8, eight wait.)
+template <typename T>
+cudaError_t allow_smem(int device) {
+  static bool done[64];
+  if (device < 64 && done[device]) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      mxfp4_narrow_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM_LIMIT - 1024);
+  if (e == cudaSuccess && device < 64) done[device] = true;
+  return e;
+}
+template <typename T>
+cudaError_t slots_t(int device, int split, int* slots) {
+  constexpr bool PLAIN = !std::is_void<T>::value;
+  auto kern = mxfp4_narrow_kernel<T>;
+  static int known[64][MAX_SPLIT + 1];
+  int* at = device < 64 ? &known[device][split] : nullptr;
+  if (!at || !*at) {
+    cudaError_t e = allow_smem<T>(device);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = split;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(split * 256);
+    cfg.blockDim = dim3(PLAIN ? PLAIN_THREADS : THREADS);
+    cfg.dynamicSmemBytes = SMEM_LIMIT - 1024;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int clusters = 0;
+    if ((e = cudaOccupancyMaxActiveClusters(&clusters, kern, &cfg)) != cudaSuccess) return e;
+    *slots = clusters * split;
+    if (at) *at = *slots;
+  } else {
+    *slots = *at;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t slots_of(bool plain, int a_dtype, int device, int split, int* slots) {
+  if (!plain) return slots_t<void>(device, split, slots);
+  switch (a_dtype) {
+    case MHR_F32: return slots_t<float>(device, split, slots);
+    case MHR_BF16: return slots_t<__nv_bfloat16>(device, split, slots);
+    default: return slots_t<__half>(device, split, slots);
+  }
+}
+
 template <typename T>
 cudaError_t launch_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const NarrowParams& p,
                      int64_t tiles, int smem, int device, cudaStream_t s) {
   constexpr bool PLAIN = !std::is_void<T>::value;
   auto kern = mxfp4_narrow_kernel<T>;
-  static bool set[64];  // by device; under the library's lock
-  if (device >= 64 || !set[device]) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               SMEM_LIMIT - 1024);
-    if (e != cudaSuccess) return e;
-    if (device < 64) set[device] = true;
-  }
+  if (const cudaError_t e = allow_smem<T>(device); e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -418,7 +464,11 @@ cudaError_t launch_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const Narro
 }
 
 // Tiles and K parts of a product; the part of A that a CTA quantises if it does.
-void plan_narrow(int64_t M, int64_t N, int64_t K, int sms, NarrowParams* p, int64_t* tiles) {
+// As many parts as can run at once: GB300, 1 x 4096 x 4096 in 1 / 2 / 4 / 8 parts
+// 8.3 / 7.2 / 6.3 / 5.5 us, 24 x 11008 x 4096 in 1 / 2 / 3 10.0 / 9.8 / 9.3 us and
+// in 4, which do not all run at once, 14.0 us.
+cudaError_t plan_narrow(int64_t M, int64_t N, int64_t K, bool plain, int a_dtype, int device,
+                        NarrowParams* p, int64_t* tiles) {
   p->M = static_cast<int32_t>(M);
   p->N = static_cast<int32_t>(N);
   p->K = static_cast<int32_t>(K);
@@ -428,38 +478,48 @@ void plan_narrow(int64_t M, int64_t N, int64_t K, int sms, NarrowParams* p, int6
   p->kt = static_cast<int32_t>(scale_tiles(K));
   p->num_kb = (p->kt + 1) / 2;
   *tiles = (M + p->nt - 1) / p->nt * p->tiles_n;
-  // K parts: the stages that the busiest SM takes, an end for each of its CTAs,
-  // and the meeting of the parts.
-  p->split = 1;
-  double best = 0;
-  for (int split = 1; split <= MAX_SPLIT && split <= p->num_kb; ++split) {
-    const int64_t each = (*tiles * split + sms - 1) / sms;
-    const double t = static_cast<double>(each) * ((p->num_kb + split - 1) / split + 0.5) +
-                     (split > 1 ? 1.0 + 0.1 * split : 0.0);
-    if (split == 1 || t < best) {
-      best = t;
-      p->split = split;
-    }
+  for (p->split = p->num_kb < MAX_SPLIT ? p->num_kb : MAX_SPLIT; p->split > 1; --p->split) {
+    int slots = 0;
+    const cudaError_t e = slots_of(plain, a_dtype, device, p->split, &slots);
+    if (e != cudaSuccess) return e;
+    if (*tiles * p->split <= (p->nt <= PAIR_NT ? 2 : 1) * slots) break;
   }
   p->a_bytes = (p->num_kb + p->split - 1) / p->split * (SF_BYTES + p->nt * BK_BYTES);
+  return cudaSuccess;
 }
 
 }  // namespace
 
-bool narrow_quantizes(int64_t M, int64_t N, int64_t K, int sms) {
-  if (M > PLAIN_ROWS) return false;
+cudaError_t narrow_quantizes(int64_t M, int64_t N, int64_t K, int a_dtype, int device, bool* yes) {
+  *yes = false;
+  if (M > PLAIN_ROWS) return cudaSuccess;
   NarrowParams p;
   int64_t tiles;
-  plan_narrow(M, N, K, sms, &p, &tiles);
-  return p.a_bytes <= PLAIN_BYTES;
+  const cudaError_t e = plan_narrow(M, N, K, true, a_dtype, device, &p, &tiles);
+  *yes = p.a_bytes <= PLAIN_BYTES;
+  return e;
+}
+
+cudaError_t narrow_time(int64_t M, int64_t N, int64_t K, int sms, int device, double* us) {
+  NarrowParams p;
+  int64_t tiles;
+  const cudaError_t e = plan_narrow(M, N, K, false, 0, device, &p, &tiles);
+  if (e != cudaSuccess) return e;
+  const int64_t rounds = (tiles * p.split + sms - 1) / sms;
+  const int stages = (p.num_kb + p.split - 1) / p.split;
+  *us = 4.8 + 0.018 * p.nt + static_cast<double>(rounds) * stages * (0.26 + 0.0008 * p.nt);
+  return cudaSuccess;
 }
 
 cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
   NarrowParams p;
   int64_t tiles;
-  plan_narrow(a.M, a.N, a.K, ctl.sm_count, &p, &tiles);
-  if (tiles * p.split > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const bool plain = a.a_plain != nullptr;
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e == cudaSuccess) e = plan_narrow(a.M, a.N, a.K, plain, a.a_dtype, device, &p, &tiles);
+  if (e != cudaSuccess) return e;
+  if (tiles * p.split > 0x7fffffff) return cudaErrorInvalidConfiguration;
   const int room = (p.nt <= PAIR_NT ? SMEM_LIMIT / 2 : SMEM_LIMIT) - 1024 - 1024 -
                    (plain ? p.a_bytes : 0);
   p.stage_bytes = W_BYTES + (plain ? SF_BYTES : p.nt * BK_BYTES + 2 * SF_BYTES);
@@ -493,9 +553,6 @@ cudaError_t launch_narrow(const ProductArgs& a, const DeviceCtl& ctl, cudaStream
                                BK_BYTES, p.nt, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const int smem = p.stages * p.stage_bytes + (plain ? p.a_bytes : 0) + 1024;
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
   if (!plain) return launch_t<void>(tmA, tmB, p, tiles, smem, device, s);
   switch (a.a_dtype) {
     case MHR_F32: return launch_t<float>(tmA, tmB, p, tiles, smem, device, s);

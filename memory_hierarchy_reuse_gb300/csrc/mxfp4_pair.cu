@@ -482,20 +482,25 @@ bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t kt
 // 0.72 ns.  Narrower tiles put more clusters to work on few tiles (2000 x 300 x
 // 4000: 11.3 us with 128 columns, 15.4 with 256) and wider ones do more with a
 // stage's fixed part (8192^3: 155 us with 256, 220 with 128).
-int plan_pair_bn(int64_t M, int64_t N, int64_t K, int clusters) {
+int plan_pair_bn(int64_t M, int64_t N, int64_t K, int clusters, double* best_t) {
   const int64_t stages = (scale_tiles(K) + 1) / 2;
   int best = MAX_BN;
-  double best_t = 0;
   for (int bn = MAX_BN; bn >= 128; bn -= 64) {
     const int64_t tiles = (M + TILE_M - 1) / TILE_M * ((N + bn - 1) / bn);
     const int64_t rounds = (tiles + clusters - 1) / clusters;
     const double t = static_cast<double>(rounds) * stages * (226.0 + bn) + 6.0 * bn;
-    if (bn == MAX_BN || t < best_t) {
-      best_t = t;
+    if (bn == MAX_BN || t < *best_t) {
+      *best_t = t;
       best = bn;
     }
   }
   return best;
+}
+
+double pair_time(int64_t M, int64_t N, int64_t K, int clusters) {
+  double t = 0;
+  plan_pair_bn(M, N, K, clusters, &t);
+  return 4.1 + 0.72e-3 * t;
 }
 
 cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t s) {
@@ -525,8 +530,9 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
   p.M = static_cast<int32_t>(a.M);
   p.N = static_cast<int32_t>(a.N);
   // (gemm_testing_set_pair_tile_n forces a width, rounded to one that exists)
+  double t;
   const int bn = ctl.pair_tile_n ? ctl.pair_tile_n / 64 * 64
-                                 : plan_pair_bn(a.M, a.N, a.K, ctl.sm_count / 2);
+                                 : plan_pair_bn(a.M, a.N, a.K, ctl.sm_count / 2, &t);
   p.tiles_m = static_cast<int32_t>((a.M + TILE_M - 1) / TILE_M);
   p.tiles_n = static_cast<int32_t>((a.N + bn - 1) / bn);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
