@@ -48,7 +48,7 @@ struct ProductArgs {
   int a_dtype = 0;
 };
 // Whether launch_narrow takes a plain A and quantises it on the way: at most
-// 8 rows whose part of K fits beside the ring.
+// 32 rows whose part of K fits beside the ring and is little work.
 cudaError_t narrow_quantizes(int64_t M, int64_t N, int64_t K, int a_dtype, int device, bool* yes);
 // What either kernel takes for a product of packed operands, in us: fits of the
 // times measured on GB300, for the choice between the two.

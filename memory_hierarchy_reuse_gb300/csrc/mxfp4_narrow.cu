@@ -9,9 +9,9 @@
 // shared memory and are added in rank order, so a result is the same from call
 // to call.
 //
-// A plain A of at most 8 rows is quantised on the way by the CTA's other
-// warps, each CTA its part of K: one launch instead of two, and
-// no packed A in memory.
+// A plain A of few rows is quantised on the way by the CTA's other warps, each CTA
+// its part of K, where that is little work (every tile of columns repeats it): one
+// launch instead of two, and no packed A in memory.
 #include <type_traits>
 
 #include "mhr_gemm.h"
@@ -30,7 +30,11 @@ constexpr int MAX_STAGES = 10;
 constexpr int MAX_NT = 128;           // rows of A a tile: the MMA's N
 constexpr int THREADS = 192;           // packed A
 constexpr int PLAIN_THREADS = 512;     // A quantised here
-constexpr int PLAIN_ROWS = 8;
+constexpr int PLAIN_ROWS = 32;
+// Rows x stages of K that a CTA quantises at most.  GB300, quantised here against by
+// a kernel before: 1 x 4096 x 4096 (3 of them) 6.0 / 9.2 us, 8 x 11008 x 4096 (48)
+// 10.0 / 12.3, 16 x 11008 x 4096 (96) 12.2 / 12.3, 24 x 11008 x 4096 (144) 14.6 / 12.3.
+constexpr int PLAIN_TASKS = 90;
 constexpr int PLAIN_BYTES = 32 * 1024;  // of the quantised part of A
 constexpr int MAX_SPLIT = 8;
 constexpr int SMEM_LIMIT = 227 * 1024;
@@ -496,7 +500,7 @@ cudaError_t narrow_quantizes(int64_t M, int64_t N, int64_t K, int a_dtype, int d
   NarrowParams p;
   int64_t tiles;
   const cudaError_t e = plan_narrow(M, N, K, true, a_dtype, device, &p, &tiles);
-  *yes = p.a_bytes <= PLAIN_BYTES;
+  *yes = p.a_bytes <= PLAIN_BYTES && M * ((p.num_kb + p.split - 1) / p.split) <= PLAIN_TASKS;
   return e;
 }
 

@@ -85,57 +85,49 @@ struct RowParams {
   uint8_t* scales;
   void* values;
   int64_t ldv;
-  int64_t kt;     // scale tiles along a row
-  uint32_t spans;  // warps along a row
+  int64_t kt;       // scale tiles along a row
+  uint32_t chunks;  // of 256 columns along a row
 };
 
-constexpr int ROW_CHUNK = 256;  // columns of a warp's step: 8 a lane
-constexpr int ROW_STEPS = 4;    // steps a warp has in flight at once
-constexpr int ROW_SPAN = ROW_CHUNK * ROW_STEPS;
+constexpr int ROW_CHUNK = 256;  // columns of a warp: 8 a lane
+constexpr int ROW_STEPS = 4;    // rows of a warp
 
-// Blocks along the rows.  A warp takes 1024 columns of a row in four steps of
-// 8 columns a lane (16 bytes of a 16-bit type), all loads first; a block is
-// four neighbouring lanes, its maximum two shuffles.  Rows past the last up to
-// a multiple of 128 get zero scales (the tiles are written whole).
+// Blocks along the rows.  A warp takes 256 columns (16 bytes a lane of a 16-bit
+// type) of the four rows r, r + 32, r + 64 and r + 96 of a tile of 128: their
+// scales are neighbours in the tile and go out 16 bytes at a time.  All loads
+// first; a block is four neighbouring lanes, its maximum two shuffles.  Rows past
+// the last up to a multiple of 128 get zero scales (the tiles are written whole).
 template <typename T, bool VEC, bool VALUES>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowParams p) {
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   // (32-bit division: fewer than 2^31 warps of a launch, see launch_t)
-  const uint32_t task = blockIdx.x * 8u + (threadIdx.x >> 5), r = task / p.spans;
-  const int64_t row = r;
-  if (row >= (p.rows + 127) / 128 * 128) return;
-  const int64_t span0 = static_cast<int64_t>(task - r * p.spans) * ROW_SPAN;
-  uint8_t* srow = p.scales + scale_offset(row, 0, p.kt);
-  if (row >= p.rows) {
-    if ((lane & 15) == 0)
-      for (int i = 0; i < ROW_STEPS; ++i) {
-        const int64_t tile = (span0 + i * ROW_CHUNK + lane * 8) / 128;
-        if (tile < p.kt) *reinterpret_cast<uint32_t*>(srow + tile * 512) = 0u;
-      }
-    return;
-  }
-  const T* xrow = static_cast<const T*>(p.x) + row * p.ldx;
-  // A whole span takes its loads in one go, with no branch and no conversion
+  const uint32_t task = blockIdx.x * 8u + (threadIdx.x >> 5), set = task / p.chunks;
+  const int64_t row0 = static_cast<int64_t>(set >> 5) * 128 + (set & 31);
+  if (row0 >= (p.rows + 127) / 128 * 128) return;
+  const int64_t c = static_cast<int64_t>(task - set * p.chunks) * ROW_CHUNK + lane * 8;
+  const T* x = static_cast<const T*>(p.x) + c;
+  // Whole rows take their loads in one go, with no branch and no conversion
   // between them (either makes each wait for the one before).
-  const bool whole = VEC && span0 + ROW_SPAN <= p.cols;
+  const bool whole = VEC && row0 + 96 < p.rows && c - lane * 8 + ROW_CHUNK <= p.cols;
   Raw8<T> raw[ROW_STEPS];
   if (whole) {
 #pragma unroll
-    for (int i = 0; i < ROW_STEPS; ++i) raw[i].load(xrow + span0 + i * ROW_CHUNK + lane * 8);
+    for (int i = 0; i < ROW_STEPS; ++i) raw[i].load(x + (row0 + 32 * i) * p.ldx);
   } else {
 #pragma unroll
     for (int i = 0; i < ROW_STEPS; ++i) {
-      const int64_t c = span0 + i * ROW_CHUNK + lane * 8;
-      if (VEC && c + 8 <= p.cols)
-        raw[i].load(xrow + c);
+      const int64_t row = row0 + 32 * i, left = row < p.rows ? p.cols - c : 0;
+      if (VEC && left >= 8)
+        raw[i].load(x + row * p.ldx);
       else
-        raw[i].load(xrow + c, p.cols - c);
+        raw[i].load(x + row * p.ldx, left);
     }
   }
+  uint32_t words[ROW_STEPS];
 #pragma unroll
   for (int i = 0; i < ROW_STEPS; ++i) {
-    const int64_t c = span0 + i * ROW_CHUNK + lane * 8;
+    const int64_t row = row0 + 32 * i;
     float v[8];
     raw[i].get(v);
     uint32_t amax = 0;
@@ -145,14 +137,13 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowParams p) {
     amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     const uint32_t code = scale_code(amax);
     const uint32_t codes = code == 255u ? 0u : encode8(v, scale_inverse(code));
+    // the scales of 4 blocks (16 lanes) as one word
+    words[i] = code << (8 * ((lane >> 2) & 3));
+    words[i] |= __shfl_xor_sync(0xffffffffu, words[i], 4);
+    words[i] |= __shfl_xor_sync(0xffffffffu, words[i], 8);
+    if (!whole && row >= p.rows) continue;
     if (whole || c < (p.cols + 31) / 32 * 32)
       *reinterpret_cast<uint32_t*>(p.data + row * p.ldd + c / 2) = codes;
-    // the scales of 4 blocks (16 lanes) as one word
-    uint32_t word = code << (8 * ((lane >> 2) & 3));
-    word |= __shfl_xor_sync(0xffffffffu, word, 4);
-    word |= __shfl_xor_sync(0xffffffffu, word, 8);
-    if ((lane & 15) == 0 && (whole || c / 128 < p.kt))
-      *reinterpret_cast<uint32_t*>(srow + c / 128 * 512) = word;
     if (VALUES) {
       decode8(codes, scale_value(code), v);
       Raw8<T> out;
@@ -164,6 +155,9 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowParams p) {
         out.store(dst, p.cols - c);
     }
   }
+  if ((lane & 15) == 0 && c / 128 < p.kt)
+    *reinterpret_cast<uint4*>(p.scales + scale_offset(row0, 0, p.kt) + c / 128 * 512) =
+        make_uint4(words[0], words[1], words[2], words[3]);
 }
 
 struct ColParams {
@@ -288,8 +282,8 @@ cudaError_t launch_t(const void* X, int64_t rows, int64_t cols, int64_t ldx, boo
   note_launch();
   if (!transpose) {
     const RowParams p{X,      ldx, rows, cols, data, ldd, scales, values, ldv, scale_tiles(cols),
-                      static_cast<uint32_t>((scale_tiles(cols) * 128 + ROW_SPAN - 1) / ROW_SPAN)};
-    const int64_t tasks = (rows + 127) / 128 * 128 * p.spans;
+                      static_cast<uint32_t>((scale_tiles(cols) + 1) / 2)};
+    const int64_t tasks = (rows + 127) / 128 * 32 * p.chunks;
     if (tasks + 8 > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const dim3 grid(static_cast<unsigned>((tasks + 7) / 8));
     const bool vec = vec_ok<T>(X, ldx, 16) && (!values || vec_ok<T>(values, ldv, 16));
