@@ -236,9 +236,10 @@ __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, b
   }
 }
 
-// 256 columns of K, 8 a lane, as TERMS rows of e2m1 codes and their scales:
-// row j is 128 bytes from 128 j on, its 8 scales follow all rows.
-//
+// 256 columns of K, 8 a lane, as TERMS rows of e2m1 codes and their scales, into a
+// piece in memory (row j is 128 bytes from 128 j on, its 8 scales follow all rows)
+// or, staged, into rows n on of a stage in shared memory (16-byte pieces
+// swizzled by n % 8, scales in the tiles that tcgen05.cp takes).
 //
 // Here and below, code that runs twice a call is one copy of it, and loops stay
 // rolled: between the grid barriers a CTA runs little code, and most of it for
@@ -246,8 +247,9 @@ __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, b
 // wait for (choosing experts unrolled over four tokens took twice as long as one
 // at a time).
 __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3, float v4,
-                                         float v5, float v6, float v7, uint8_t* piece) {
-  const int lane = threadIdx.x & 31;
+                                         float v5, float v6, float v7, uint8_t* codes,
+                                         uint8_t* scales, int n, bool staged) {
+  const int lane = threadIdx.x & 31, block = lane >> 2;
   float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
   uint32_t amax = 0;
 #pragma unroll
@@ -258,7 +260,7 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
   const bool finite = amax < 0x7f800000u;
   int c = static_cast<int>(amax >> 23) - 2 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0);
 #pragma unroll 1
-  for (int j = 0; j < TERMS; ++j) {
+  for (int j = 0; j < TERMS; ++j, ++n) {
     // below 2^-126: nothing that an fp32 sum would see; a block with an
     // infinity or a NaN: NaN
     const bool some = c >= 1 && finite;
@@ -268,9 +270,11 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
     const uint32_t word = some ? e2m1x8(y) : 0u;
-    reinterpret_cast<uint32_t*>(piece)[j * 32 + lane] = word;
+    *reinterpret_cast<uint32_t*>(codes + n * 128 + ((block ^ (staged ? n & 7 : 0)) << 4) +
+                                 (lane & 3) * 4) = word;
     if ((lane & 3) == 0)
-      piece[TERMS * 128 + j * 8 + (lane >> 2)] = static_cast<uint8_t>(!finite ? 255 : some ? c : 0);
+      scales[staged ? (block >> 2) * 512 + (n & 31) * 16 + (n >> 5) * 4 + (block & 3)
+                    : n * 8 + block] = static_cast<uint8_t>(!finite ? 255 : some ? c : 0);
     const uint32_t h[4] = {e2m1_to_f16x2<0>(word), e2m1_to_f16x2<1>(word), e2m1_to_f16x2<2>(word),
                            e2m1_to_f16x2<3>(word)};
 #pragma unroll
@@ -282,6 +286,11 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
     c -= j == 0 ? 2 : 3;
   }
 }
+
+// Whether each CTA makes the h that it needs as it stages it, or all of them are
+// made once, between two barriers.  GB300: 16 pairs 22.7 against 24.4 us a call, 32
+// pairs 37.1 / 36.4, 64 pairs 49.5 / 49.3, 512 pairs 261 / 255.
+__device__ __forceinline__ bool direct_h(const MoeParams& p) { return p.T * p.top <= 16; }
 
 // Step 1, all warps of the grid: x as terms, and the logits.
 __device__ void route_start(const MoeParams& p) {
@@ -296,8 +305,9 @@ __device__ void route_start(const MoeParams& p) {
     load_row<1>(p.x + t * p.ldx, k, p.H, vx, x);
     float v[8];
     unpack_bf16(x[0], v);
-    split_terms(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7],
-                p.x_terms + static_cast<int64_t>(i) * PIECE);
+    uint8_t* piece = p.x_terms + static_cast<int64_t>(i) * PIECE;
+    split_terms(v[0], v[1], v[2], v[3], v[4], v[5], v[6], v[7], piece, piece + TERMS * 128, 0,
+                false);
   }
   if (p.E * p.T <= warps)
     route_logits<1>(p, warp, warps, vx, vr);
@@ -581,38 +591,79 @@ __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m,
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Step 3b, the consumers of the grid: h of every pair as terms, from the parts'
-// sums of gate and up in their order.  (The fast exponential and division are
-// off by some 2^-21 of silu, a quarter of what two roundings of the sums are; in
-// the exact ones' code the step spent its time on fetching instructions.)
-__device__ __forceinline__ void make_h(const Cta& c) {
+// h of a pair for 8 columns from k on: the parts' sums of gate and up in their
+// order.  (The fast exponential and division are off by some 2^-21 of silu, a
+// quarter of what two roundings of the sums are; the exact ones' code takes longer
+// to fetch than the step to run.)
+__device__ __forceinline__ void h_of(const Cta& c, int pair, int k, float (&h)[8]) {
   const MoeParams& p = c.p;
   const int64_t part = static_cast<int64_t>(p.T) * p.top * p.up.pitch;
-  const int half = p.up.pitch / 2, tasks = p.T * p.top * p.down.stages;
-  const int team = gridDim.x * (CONSUMERS / 32);
-  for (int i = (c.warp - 1) * gridDim.x + blockIdx.x; i < tasks; i += team) {
-    const int pair = i / p.down.stages, k = (i - pair * p.down.stages) * 256 + c.lane * 8;
-    const float* g = p.up.sums + static_cast<int64_t>(pair) * p.up.pitch + k;
-    float gate[8], value[8];
+  const int half = p.up.pitch / 2;
+  const float* g = p.up.sums + static_cast<int64_t>(pair) * p.up.pitch + k;
+  float gate[8], value[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) gate[j] = value[j] = 0.f;
-    if (k < p.I)
-#pragma unroll 2
-      for (int q = 0; q < c.r.up.parts; ++q, g += part) {
-        const float4* a = reinterpret_cast<const float4*>(g);
-        const float4* b = reinterpret_cast<const float4*>(g + half);
-        const float4 a0 = __ldcg(a), a1 = __ldcg(a + 1), b0 = __ldcg(b), b1 = __ldcg(b + 1);
-        gate[0] += a0.x, gate[1] += a0.y, gate[2] += a0.z, gate[3] += a0.w;
-        gate[4] += a1.x, gate[5] += a1.y, gate[6] += a1.z, gate[7] += a1.w;
-        value[0] += b0.x, value[1] += b0.y, value[2] += b0.z, value[3] += b0.w;
-        value[4] += b1.x, value[5] += b1.y, value[6] += b1.z, value[7] += b1.w;
+  for (int j = 0; j < 8; ++j) gate[j] = value[j] = 0.f;
+  if (k < p.I)
+#pragma unroll 1
+    for (int q = 0; q < c.r.up.parts; q += 2) {  // two at once
+      const bool both = q + 1 < c.r.up.parts;
+      float4 a[2][2], b[2][2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float* at = g + (i && both ? part : 0);
+        a[i][0] = __ldcg(reinterpret_cast<const float4*>(at));
+        a[i][1] = __ldcg(reinterpret_cast<const float4*>(at) + 1);
+        b[i][0] = __ldcg(reinterpret_cast<const float4*>(at + half));
+        b[i][1] = __ldcg(reinterpret_cast<const float4*>(at + half) + 1);
       }
-    float h[8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      h[j] = k + j < p.I ? __fdividef(gate[j], 1.f + __expf(-gate[j])) * value[j] : 0.f;
-    split_terms(h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7],
-                p.h_terms + static_cast<int64_t>(i) * PIECE);
+      for (int i = 0; i < 2; ++i) {
+        if (i && !both) break;
+        gate[0] += a[i][0].x, gate[1] += a[i][0].y, gate[2] += a[i][0].z, gate[3] += a[i][0].w;
+        gate[4] += a[i][1].x, gate[5] += a[i][1].y, gate[6] += a[i][1].z, gate[7] += a[i][1].w;
+        value[0] += b[i][0].x, value[1] += b[i][0].y, value[2] += b[i][0].z, value[3] += b[i][0].w;
+        value[4] += b[i][1].x, value[5] += b[i][1].y, value[6] += b[i][1].z, value[7] += b[i][1].w;
+      }
+      g += 2 * part;
+    }
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    h[j] = k + j < p.I ? __fdividef(gate[j], 1.f + __expf(-gate[j])) * value[j] : 0.f;
+}
+
+// h of some pairs as terms, 256 columns a warp: of all pairs into memory, by the
+// consumers of the grid (run < 0), or of a run's segments straight into shared
+// memory, by this CTA's.
+__device__ __forceinline__ void make_h(const Cta& c, const Plan& plan, int run) {
+  const MoeParams& p = c.p;
+  const int stages = p.down.stages;
+  constexpr int TEAM = CONSUMERS / 32;
+  const int segments = run < 0 ? 1 : plan.segments;
+#pragma unroll 1
+  for (int s = 0; s < segments; ++s) {
+    if (run >= 0 && plan.seg[s].run != run) continue;
+    const int first = run < 0 ? (c.warp - 1) * gridDim.x + blockIdx.x : c.warp - 1;
+    const int step = run < 0 ? TEAM * gridDim.x : TEAM;
+    const int k0 = run < 0 ? 0 : plan.seg[s].k0, kn = run < 0 ? stages : plan.seg[s].kn;
+    const int tasks = run < 0 ? p.T * p.top * stages : plan.seg[s].count * kn;
+#pragma unroll 1
+    for (int i = first; i < tasks; i += step) {
+      const int col = i / kn, stage = i - col * kn;
+      const int pair = run < 0 ? col : c.r.list[plan.seg[s].first + col];
+      float h[8];
+      h_of(c, pair, (k0 + stage) * 256 + c.lane * 8, h);
+      uint8_t *codes, *scales;
+      if (run < 0) {
+        codes = p.h_terms + static_cast<int64_t>(i) * PIECE;
+        scales = codes + TERMS * 128;
+      } else {
+        uint8_t* at = c.staged + plan.seg[s].offset;
+        codes = at + kn * 1024 + stage * staged_rows(plan.seg[s].count) * 128;
+        scales = at + stage * 1024;
+      }
+      split_terms(h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7], codes, scales,
+                  run < 0 ? 0 : col * TERMS, run >= 0);
+    }
   }
 }
 
@@ -699,7 +750,12 @@ __device__ __forceinline__ void product(Cta& c, const MoeProduct& m, const Plan&
   int s = 0;
   for (int run = 0; run < runs; ++run) {
     if (run) consumers_sync();  // the columns staged before have been read
-    if (!*c.abort_flag) stage_columns(c, m, plan, up, run);
+    if (!*c.abort_flag) {
+      if (!up && direct_h(c.p))
+        make_h(c, plan, run);
+      else
+        stage_columns(c, m, plan, up, run);
+    }
     fence_proxy_async_smem();
     consumers_sync();
     bool ok = !*c.abort_flag;
@@ -727,18 +783,34 @@ __device__ __forceinline__ void combine(const Cta& c) {
     const int t = i / quads, row = (i - t * quads) * 4;
     const float* src = p.down.sums + static_cast<int64_t>(t) * p.top * p.down.pitch + row;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int k = 0; k < p.top; ++k, src += p.down.pitch) {
-      const float w = c.r.weight[t * p.top + k];
-      float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-      for (int q = 1; q < c.r.down.parts; ++q) {
-        const float4 o = __ldcg(reinterpret_cast<const float4*>(src + q * part));
-        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+    // a pair's parts are added first; four loads are under way at once
+    const int parts = c.r.down.parts, loads = p.top * parts;
+    float pair[4] = {0.f, 0.f, 0.f, 0.f};
+    int k = 0, q = 0;  // pair and part of the load to be added
+#pragma unroll 1
+    for (int l0 = 0; l0 < loads; l0 += 4) {
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int l = min(l0 + j, loads - 1), lk = l / parts;
+        v[j] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(lk) * p.down.pitch +
+                                                      (l - lk * parts) * part));
       }
-      sum[0] = fmaf(w, v.x, sum[0]);
-      sum[1] = fmaf(w, v.y, sum[1]);
-      sum[2] = fmaf(w, v.z, sum[2]);
-      sum[3] = fmaf(w, v.w, sum[3]);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (l0 + j >= loads) break;
+        pair[0] += v[j].x, pair[1] += v[j].y, pair[2] += v[j].z, pair[3] += v[j].w;
+        if (++q == parts) {
+          const float w = c.r.weight[t * p.top + k];
+#pragma unroll
+          for (int i4 = 0; i4 < 4; ++i4) {
+            sum[i4] = fmaf(w, pair[i4], sum[i4]);
+            pair[i4] = 0.f;
+          }
+          q = 0;
+          ++k;
+        }
+      }
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -828,10 +900,15 @@ __global__ void __launch_bounds__(THREADS, 1)
       product(c, i ? p.down : p.up, i ? r.down : r.up, i == 0);
       grid_barrier(c, round++);
       if (i == 0) {
-        if (!abort_flag) make_h(c);
+        if (direct_h(p)) continue;
+        if (!abort_flag) make_h(c, r.down, -1);
         grid_barrier(c, round++);
-      } else if (!abort_flag) {
-        combine(c);
+      } else {
+        // No CTA polls any more once it is here: the last one clears the counters
+        // for the next call.
+        if (threadIdx.x == 32 && atomicAdd(p.control + 1, 1u) == gridDim.x - 1)
+          p.control[0] = p.control[1] = 0;
+        if (!abort_flag) combine(c);
       }
     }
     if (c.warp == 1 && c.it > 0) {  // the last MMAs issued have finished
@@ -846,11 +923,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   if (c.warp == 1) {
     tc_fence_after();
     tmem_dealloc(c.tmem, TMEM_COLS);
-  }
-  // The last CTA to leave clears the counters for the next call.
-  if (threadIdx.x == 0) {
-    __threadfence();
-    if (atomicAdd(p.control + 1, 1u) == gridDim.x - 1) p.control[0] = p.control[1] = 0;
   }
 }
 
