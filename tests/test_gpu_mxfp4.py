@@ -272,6 +272,75 @@ def test_quantized_product_matches_plain_product(mhr):
     assert bool(((got - want).abs() <= 2 * (640 + 8) * 2.0 ** -23 * S).all())
 
 
+def test_offsets_past_32_bits(mhr):
+    """Rows more than 2^32 bytes apart in x, the values, the packed data and C."""
+    import torch
+
+    far = 2_300_000_000
+    x = torch.empty(far + 4096, dtype=torch.bfloat16, device="cuda").as_strided((2, 700), (far, 1))
+    near = torch.randn(2, 700, device="cuda").bfloat16()
+    x.copy_(near)
+    for axis in (1, 0):
+        q, v = mhr.quantize_mxfp4(x, axis=axis, values=True)
+        want, wv = mhr.quantize_mxfp4(near, axis=axis, values=True)
+        assert torch.equal(q.data, want.data) and torch.equal(q.scales, want.scales)
+        assert torch.equal(v, wv)
+    del x
+    qa, qb = mhr.quantize_mxfp4(torch.randn(300, 700, device="cuda")), mhr.quantize_mxfp4(torch.randn(2, 700, device="cuda"))
+    want = mhr.matmul_mxfp4(qa, qb)
+    wide = torch.empty(2 * far + 4096, dtype=torch.uint8, device="cuda").as_strided((2, 352), (2 * far // 16 * 16, 1))
+    wide.copy_(qb.data)
+    b = mhr.MxFp4Matrix(wide, qb.scales, 2, 700)
+    assert torch.equal(mhr.matmul_mxfp4(qa, b), want)
+    got = mhr.matmul_mxfp4(b, qa)
+    out = torch.empty(far + 4096, dtype=torch.float32, device="cuda").as_strided((2, 300), (far, 1))
+    for a in (b, qb):
+        out.zero_()
+        assert torch.equal(mhr.matmul_mxfp4(a, qa, out=out), got)
+    assert torch.allclose(got, want.t(), rtol=1e-5, atol=1e-5 * float(want.abs().max()))
+
+
+def test_graph_capture(mhr):
+    """Quantisation, and products that need no workspace, replay from a CUDA graph."""
+    import torch
+
+    x = torch.randn(16, 1024, device="cuda").bfloat16()
+    big = torch.randn(300, 1024, device="cuda").bfloat16()
+    B = mhr.quantize_mxfp4(torch.randn(1024, 384, device="cuda"), axis=0)
+
+    def step():
+        return mhr.matmul_mxfp4(x, B), mhr.matmul_mxfp4(mhr.quantize_mxfp4(big), B)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (1, 2):
+        torch.manual_seed(seed)
+        x.copy_(torch.randn_like(x))
+        big.copy_(torch.randn_like(big))
+        graph.replay()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(g, w) for g, w in zip(got, want))
+
+
+def test_another_device_stream_argument(mhr):
+    """A raw stream handle in place of the current stream."""
+    import torch
+
+    x = torch.randn(40, 512, device="cuda")
+    B = mhr.quantize_mxfp4(torch.randn(512, 96, device="cuda"), axis=0)
+    want = mhr.matmul_mxfp4(x, B)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    out = torch.empty_like(want)
+    mhr.matmul_mxfp4(x, B, out=out, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(out, want)
+
+
 def test_streams(mhr):
     """Calls on several streams at once, each with its own packed activations."""
     import torch

@@ -123,6 +123,17 @@ def test_tensor_level_refusals():
             m.matmul_mxfp4(bad_a, bad_b, **kw)
 
 
+def test_rows_that_overlap_are_refused():
+    import torch
+
+    import memory_hierarchy_reuse_gb300 as m
+
+    with pytest.raises(ValueError):
+        m.quantize_mxfp4(torch.zeros(1, 64).expand(4, 64))
+    with pytest.raises(ValueError):
+        m.quantize_mxfp4(torch.zeros(200).as_strided((4, 64), (32, 1)))
+
+
 def test_reference_format_round_trip():
     """The numpy statement that the GPU tests compare with: packing, the tile order against a
     second way of writing it, and rounding at the ties."""
