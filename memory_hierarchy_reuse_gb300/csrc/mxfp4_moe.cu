@@ -48,7 +48,7 @@ constexpr int RING_STAGE = W_BYTES + 1024;     // and their scales
 constexpr int STAGES = 6;
 constexpr int RING_BYTES = STAGES * RING_STAGE;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
-constexpr int MAX_SEGMENTS = 160;
+constexpr int MAX_SEGMENTS = 256;
 constexpr int PIECE = TERMS * (128 + 8);       // 256 columns of K as terms: codes, then scales
 constexpr uint32_t ACC_COLS = 128;             // TMEM: two accumulators, scales of each stage
 constexpr uint32_t SF_COL = 2 * ACC_COLS;
@@ -88,7 +88,7 @@ struct MoeParams {
   uint8_t* x_terms;        // T x up.stages pieces
   uint8_t* h_terms;        // T * top x down.stages pieces
   uint32_t* control;       // [0] barrier arrivals, [1] exits
-  int32_t stage_bytes;     // shared memory for staged columns
+  int32_t stage_kb;        // shared memory for staged columns
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t inject_stall;
@@ -96,13 +96,14 @@ struct MoeParams {
 
 // A CTA's run of items that share an expert, a part of K and their columns.
 struct Segment {
-  int16_t expert, first, count;   // pairs list[first .. first + count)
-  int16_t k0, kn;                 // ring stages of K
-  int16_t part;
-  int16_t items;                  // tiles of 128 rows, from matrix row 128 * tile on
+  int16_t expert, first;          // pairs list[first .. first + count)
+  uint8_t count, part;
+  uint8_t k0, kn;                 // ring stages of K
+  int16_t tile, items;            // tiles of 128 rows, from the expert's tile `tile` on
   int16_t run;                    // staged together with the others of its run
-  int32_t tile;
-  int32_t offset;                 // of the staged columns: scales, then codes
+  uint16_t offset;                // of the staged columns in KB: scales, then codes
+
+  __device__ int first_tile(const MoeProduct& m) const { return expert * m.rows / 128 + tile; }
 };
 
 struct Plan {
@@ -344,6 +345,37 @@ __device__ void sort_pairs(const MoeParams& p, Routing& r) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = threadIdx.x;
   static_assert(THREADS >= MOE_MAX_EXPERTS, "a thread an expert");
   const int pairs = p.T * p.top;
+  // Up to 32 pairs by one warp, a lane a pair; experts in the order of their first
+  // pairs.  GB300: 4 pairs 20.1 against 20.5 us a call, 32 pairs the same as below.
+  if (pairs <= 32) {
+    if (warp == 0) {
+      const int x = lane < pairs ? r.expert[lane] : -1 - lane;
+      const uint32_t same = __match_any_sync(0xffffffffu, x), before = (1u << lane) - 1;
+      const bool first = lane < pairs && (same & before) == 0;
+      const uint32_t firsts = __ballot_sync(0xffffffffu, first);
+      const int count = __popc(same);
+      int scan = first ? count : 0;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, scan, d);
+        if (lane >= d) scan += o;
+      }
+      // the first pair's lane holds its expert's place in the list
+      const int offset = __shfl_sync(0xffffffffu, scan - count, __ffs(same) - 1);
+      if (first) {
+        r.offset[x] = static_cast<int16_t>(offset);
+        r.active[__popc(firsts & before)] = static_cast<int16_t>(x);
+      }
+      if (lane < pairs) r.list[offset + __popc(same & before)] = static_cast<int16_t>(lane);
+      const int most = __reduce_max_sync(0xffffffffu, first ? count : 0);
+      if (lane == 0) {
+        r.num_active = __popc(firsts);
+        r.most = most;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   for (int i = threadIdx.x; i < pairs; i += THREADS) atomicAdd(&r.count[r.expert[i]], 1);
   __syncthreads();
   const int count = e < p.E ? r.count[e] : 0;
@@ -382,41 +414,46 @@ __device__ void sort_pairs(const MoeParams& p, Routing& r) {
   __syncthreads();
 }
 
-// Bytes that `cols` columns over `stages` stages of K take when staged: the
-// scales' tiles, then 128 bytes a row and stage.
+// KB that `cols` columns over `stages` stages of K take when staged -- the scales'
+// tiles, then 128 bytes a row and stage -- and how many columns fit into `kb` KB.
 __device__ __forceinline__ int staged_rows(int cols) { return (cols * TERMS + 7) / 8 * 8; }
-__device__ __forceinline__ int staged_bytes(int cols, int stages) {
-  return stages * (1024 + staged_rows(cols) * 128);
+__device__ __forceinline__ int staged_kb(int cols, int stages) {
+  return stages * (1 + staged_rows(cols) / 8);
+}
+__host__ __device__ __forceinline__ int columns_that_fit(int kb, int stages) {
+  const int n = (kb / stages - 1) * 8 / TERMS;
+  return n < 0 ? 0 : n < MAX_COLS ? n : MAX_COLS;
 }
 
 // By one warp: the parts of K, then the CTA's equal run of all items -- expert by
-// expert, part by part, tile by tile -- as segments.  At most `most` of an
-// expert's pairs go into an MMA (more pairs take its items again), and segments
-// are staged together as far as they fit.
+// expert, part by part, tile by tile -- as segments.  An expert's items are taken
+// again when more pairs have it than fit an MMA or shared memory, and segments are
+// staged together as far as they fit.
 __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Routing& r, Plan& plan) {
   const int lane = threadIdx.x & 31;
   const int pairs = p.T * p.top, active = r.num_active;
   auto end_of = [&](int ai) {
     return ai + 1 < active ? static_cast<int>(r.offset[r.active[ai + 1]]) : pairs;
   };
-  const int most = min(r.most, MAX_COLS);
-  // Time of the longest run, in stages, with a quarter of one for an item's ends;
-  // parts that are too long to stage all columns at once count twice.
+  // Time of the longest run, in stages, with a quarter of one for an item's ends,
+  // times the passes that the expert with the most pairs takes.  (One column at a
+  // time serves experts of one pair only: MAX_SEGMENTS counts on two, which fit 2
+  // parts of any K.)
   const int parts = lane + 1;
   uint32_t cost = 0xffffffffu;
   if (parts <= p.max_parts && parts <= m.stages) {
     const uint32_t items = static_cast<uint32_t>(active) * parts * m.tiles;
     const uint32_t longest = (items + gridDim.x - 1) / gridDim.x;
     const int stages = (m.stages + parts - 1) / parts;
-    cost = longest * (4 * stages + 1) * 32;
-    if (staged_bytes(most, stages) > p.stage_bytes) cost *= 2;
-    cost = min(cost, 0x7ffffffu) / 32 * 32 + lane;  // ties: the fewest parts
+    const int fit = columns_that_fit(p.stage_kb, stages);
+    if (fit >= min(r.most, 2)) {
+      cost = longest * (4 * stages + 1) * ((r.most + fit - 1) / fit);
+      cost = min(cost, 0x7fffffeu) * 32 + lane;  // ties: the fewest parts
+    }
   }
   const int chosen = static_cast<int>(__reduce_min_sync(0xffffffffu, cost) & 31u) + 1;
   if (lane == 0) {
-    int fit = most;
-    const int stages = (m.stages + chosen - 1) / chosen;
-    while (fit > 1 && staged_bytes(fit, stages) > p.stage_bytes) --fit;
+    const int fit = columns_that_fit(p.stage_kb, (m.stages + chosen - 1) / chosen);
     const uint32_t items = static_cast<uint32_t>(active) * chosen * m.tiles;
     // (at most 512 experts x 16 parts x 258 tiles x some hundred CTAs: 32 bits)
     const int begin = static_cast<int>(items * blockIdx.x / gridDim.x);
@@ -432,24 +469,24 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
       const int tiles = min(items, static_cast<int>((r0 + m.rows - 1) / 128) + 1 - (tile0 + t));
       if (tiles <= 0) continue;
       const int k0 = m.stages * part / chosen, k1 = m.stages * (part + 1) / chosen;
-      for (int c = r.offset[e]; c < end_of(ai) && n < MAX_SEGMENTS; c += fit) {
-        const int count = min(fit, end_of(ai) - c), bytes = staged_bytes(count, k1 - k0);
-        if (offset + bytes > p.stage_bytes) {
+      for (int c = r.offset[e]; c < end_of(ai); c += fit) {
+        const int count = min(fit, end_of(ai) - c), kb = staged_kb(count, k1 - k0);
+        if (offset + kb > p.stage_kb) {
           ++run;
           offset = 0;
         }
         Segment& s = plan.seg[n++];
         s.expert = static_cast<int16_t>(e);
         s.first = static_cast<int16_t>(c);
-        s.count = static_cast<int16_t>(count);
-        s.k0 = static_cast<int16_t>(k0);
-        s.kn = static_cast<int16_t>(k1 - k0);
-        s.part = static_cast<int16_t>(part);
+        s.count = static_cast<uint8_t>(count);
+        s.part = static_cast<uint8_t>(part);
+        s.k0 = static_cast<uint8_t>(k0);
+        s.kn = static_cast<uint8_t>(k1 - k0);
+        s.tile = static_cast<int16_t>(t);
         s.items = static_cast<int16_t>(tiles);
         s.run = static_cast<int16_t>(run);
-        s.tile = tile0 + t;
-        s.offset = offset;
-        offset += bytes;
+        s.offset = static_cast<uint16_t>(offset);
+        offset += kb;
       }
     }
     plan.segments = n;
@@ -524,7 +561,8 @@ __device__ __forceinline__ bool produce(Cta& c, const CUtensorMap* whole,
   for (int s = 0; s < plan.segments; ++s) {
     const Segment sg = plan.seg[s];
     const int row0 = sg.expert * m.rows, row1 = row0 + m.rows;
-    for (int t = sg.tile; t < sg.tile + sg.items; ++t) {
+    const int t0 = sg.first_tile(m);
+    for (int t = t0; t < t0 + sg.items; ++t) {
       // quarters [q0, q1) of the tile
       const int q0 = max(row0 - t * 128, 0) >> 5, q1 = min(row1 - t * 128 + 31, 128) >> 5;
       for (int k = sg.k0; k < sg.k0 + sg.kn; ++k, ++c.it) {
@@ -568,7 +606,8 @@ __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m,
   for (int s = 0; s < plan.segments; ++s) {
     const Segment sg = plan.seg[s];
     if (sg.run != run) continue;
-    const uint32_t scales = smem_u32(c.staged) + sg.offset, codes = scales + sg.kn * 1024;
+    const uint32_t scales = smem_u32(c.staged) + sg.offset * 1024,
+                   codes = scales + sg.kn * 1024;
     const int rows = staged_rows(sg.count);
     for (int i = threadIdx.x - 32; i < sg.count * sg.kn * STRIDE; i += CONSUMERS) {
       const int task = i / STRIDE, copy = i % STRIDE;
@@ -657,7 +696,7 @@ __device__ __forceinline__ void make_h(const Cta& c, const Plan& plan, int run) 
         codes = p.h_terms + static_cast<int64_t>(i) * PIECE;
         scales = codes + TERMS * 128;
       } else {
-        uint8_t* at = c.staged + plan.seg[s].offset;
+        uint8_t* at = c.staged + plan.seg[s].offset * 1024;
         codes = at + kn * 1024 + stage * staged_rows(plan.seg[s].count) * 128;
         scales = at + stage * 1024;
       }
@@ -671,7 +710,7 @@ __device__ __forceinline__ void make_h(const Cta& c, const Plan& plan, int run) 
 __device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segment& sg) {
   const int rows = staged_rows(sg.count);
   const uint32_t id0 = make_idesc_mxf4(128, rows, 0), id2 = make_idesc_mxf4(128, rows, 2);
-  const uint32_t scales = desc_lo(smem_u32(c.staged) + sg.offset);
+  const uint32_t scales = desc_lo(smem_u32(c.staged) + sg.offset * 1024);
   const uint32_t codes = scales + sg.kn * (1024 >> 4);
   for (int t = 0; t < sg.items; ++t, ++c.ph_items) {
     const uint32_t b = c.ph_items & 1u;
@@ -711,16 +750,16 @@ __device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segm
 __device__ __forceinline__ bool write_sums(Cta& c, const MoeProduct& m, const Segment& sg, bool up) {
   const int q = c.warp & 3;
   const int pairs = c.p.T * c.p.top;
-  const int64_t row0 = static_cast<int64_t>(sg.expert) * m.rows;
+  const int row0 = sg.first_tile(m) * 128 - sg.expert * m.rows + q * 32 + c.lane;  // of the expert
   for (int t = 0; t < sg.items; ++t, ++c.ph_items) {
     const uint32_t b = c.ph_items & 1u;
     if (!c.wait(c.acc_full(b), (c.ph_items >> 1) & 1u, kErrTimeoutEpilogue)) return false;
     tc_fence_after();
     const uint32_t taddr = c.tmem + b * ACC_COLS + (static_cast<uint32_t>(q * 32) << 16);
-    const int64_t row = static_cast<int64_t>(sg.tile + t) * 128 + q * 32 + c.lane - row0;
+    const int row = row0 + t * 128;
     const bool in = row >= 0 && row < m.rows;
     // up: gate rows, then up rows at half the pitch
-    const int at = static_cast<int>(up && row >= c.p.I ? row - c.p.I + m.pitch / 2 : row);
+    const int at = up && row >= c.p.I ? row - c.p.I + m.pitch / 2 : row;
     float* sums = m.sums + static_cast<int64_t>(sg.part) * pairs * m.pitch + at;
     for (int c0 = 0; c0 < sg.count; c0 += 4) {  // 4 columns: 24 TMEM columns
       uint32_t v[3][8];
@@ -783,21 +822,26 @@ __device__ __forceinline__ void combine(const Cta& c) {
     const int t = i / quads, row = (i - t * quads) * 4;
     const float* src = p.down.sums + static_cast<int64_t>(t) * p.top * p.down.pitch + row;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    // a pair's parts are added first; four loads are under way at once
+    // a pair's parts are added first; eight loads are under way at once
     const int parts = c.r.down.parts, loads = p.top * parts;
     float pair[4] = {0.f, 0.f, 0.f, 0.f};
     int k = 0, q = 0;  // pair and part of the load to be added
 #pragma unroll 1
-    for (int l0 = 0; l0 < loads; l0 += 4) {
-      float4 v[4];
+    for (int l0 = 0; l0 < loads; l0 += 8) {
+      float4 v[8];
+      int lk = l0 / parts, lq = l0 - lk * parts;  // pair and part of the load
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int l = min(l0 + j, loads - 1), lk = l / parts;
+      for (int j = 0; j < 8; ++j) {
+        if (l0 + j >= loads) break;
         v[j] = __ldcg(reinterpret_cast<const float4*>(src + static_cast<int64_t>(lk) * p.down.pitch +
-                                                      (l - lk * parts) * part));
+                                                      lq * part));
+        if (++lq == parts) {
+          lq = 0;
+          ++lk;
+        }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < 8; ++j) {
         if (l0 + j >= loads) break;
         pair[0] += v[j].x, pair[1] += v[j].y, pair[2] += v[j].z, pair[3] += v[j].w;
         if (++q == parts) {
@@ -1003,7 +1047,18 @@ cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, con
       return cudaErrorInvalidValue;
   }
   constexpr int kSmem = 227 * 1024 - static_cast<int>(sizeof(Routing)) - 512;
-  p.stage_bytes = (kSmem - 1024 - RING_BYTES) / 1024 * 1024;
+  p.stage_kb = (kSmem - 1024 - RING_BYTES) / 1024;
+  // A CTA's run touches at most ceil(rows / CTAs) + 1 rows of items (an expert's
+  // part of K each), of at most T pairs each; on 152 or 148 SMs that is never more
+  // than 256 segments, reached by 64 tokens x 16 of 512 experts at K above 12800.
+  for (const MoeProduct* m : {&p.up, &p.down})
+    for (int parts = 1; parts <= p.max_parts && parts <= m->stages; ++parts) {
+      const int fit = columns_that_fit(p.stage_kb, (m->stages + parts - 1) / parts);
+      const int rows = ((p.E < p.T * p.top ? p.E : p.T * p.top) * parts + ctl.sm_count - 1) /
+                           ctl.sm_count + 1;
+      if (rows * (fit > 1 ? (p.T + fit - 1) / fit : 1) > MAX_SEGMENTS)
+        return cudaErrorNotSupported;
+    }
   cudaError_t e = cudaFuncSetAttribute(moe_mxfp4_kernel,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;

@@ -7,7 +7,7 @@ import mxfp4_ref as ref
 pytestmark = pytest.mark.gpu
 
 
-def layer(T, E, top, H, I, seed):
+def layer(T, E, top, H, I, seed, favoured=0):
     """x and router as float64 bf16 values whose chosen experts are clear of ties by 1e-4 (fp32
     sums of H products of order 1 / sqrt(H) stay within H 2^-24 of that order), packed experts."""
     import torch
@@ -17,6 +17,11 @@ def layer(T, E, top, H, I, seed):
         bf = lambda a: torch.from_numpy(a).bfloat16().double().numpy()  # noqa: E731
         x = bf(rng.standard_normal((T, H)))
         router = bf(rng.standard_normal((E, H)) * H ** -0.5)
+        if favoured:  # experts that every token chooses: logits from 4 on
+            x[:, 0] = 2
+            first = E // 3
+            router[first:first + favoured] = 0
+            router[first:first + favoured, 0] = bf(2 + np.arange(favoured) / 16)
         order = np.sort(x @ router.T, 1)[:, ::-1]
         if E == 1 or np.min(order[:, :top + 1][:, :-1] - order[:, :top + 1][:, 1:]) > 1e-4:
             break
@@ -31,8 +36,8 @@ def expected(x, router, upv, downv, top, E, H, I):
     """y, its error bound, experts and weights, from the definition in 64 bits.
 
     The bound: gate and up are fp32 sums over H (at most H / 16 + 64 roundings of 2^-22 of the sum
-    of magnitudes); |silu'| <= 1.1 and silu is off by a few units (2^-20); h is rounded to 11 bits
-    (2^-11); the down sums likewise over I and top; weights carry 2^-18; y is rounded to bf16."""
+    of magnitudes); |silu'| <= 1.1 and silu is off by a few units (2^-20); h is rounded to no
+    less than 11 bits (2^-11); the down sums likewise over I and top; weights carry 2^-18; y is rounded to bf16."""
     T = x.shape[0]
     logits = x @ router.T
     experts = np.argsort(-logits, axis=1, kind="stable")[:, :top]
@@ -58,10 +63,10 @@ def expected(x, router, upv, downv, top, E, H, I):
     return y, bound, experts, w
 
 
-def run_case(mhr, T, E, top, H, I, seed=0, shift=0, check=True):
+def run_case(mhr, T, E, top, H, I, seed=0, shift=0, favoured=0):
     import torch
 
-    x, router, (up, ups, upv), (down, downs, downv) = layer(T, E, top, H, I, seed)
+    x, router, (up, ups, upv), (down, downs, downv) = layer(T, E, top, H, I, seed, favoured)
     dev = lambda a: torch.from_numpy(a).cuda()  # noqa: E731
 
     def strided(a):  # a bf16 matrix in a wider buffer, `shift` elements in
@@ -107,6 +112,17 @@ def test_more_columns_than_are_staged_at_once(mhr):
     """Every token on the same experts and wide rows: several passes over an expert's pairs."""
     run_case(mhr, 64, 2, 2, 8192, 96, seed=5)
     run_case(mhr, 40, 1, 1, 128, 9000, seed=6)
+
+
+@pytest.mark.parametrize("T,E,top,H,I,favoured", [
+    (64, 340, 16, 13000, 2, 8),   # columns too long for shared memory in one part of K, and more
+                                  # passes over experts than any other shape has
+    (64, 20, 16, 16384, 8, 0),
+    (64, 20, 8, 8, 16384, 4),     # the same of the down product
+    (64, 24, 16, 40, 13000, 8),
+    (1, 16, 16, 16384, 16, 0)])
+def test_longest_columns(mhr, T, E, top, H, I, favoured):
+    run_case(mhr, T, E, top, H, I, seed=T + E, favoured=favoured)
 
 
 def test_ties_go_to_the_lowest_expert(mhr):
