@@ -39,8 +39,8 @@ struct ProductArgs {
   int64_t ldc;
   int c_dtype;
   int64_t M, N, K;
-  // A was quantised by a kernel of the same call just before, itself launched
-  // in plain stream order: B is complete once this kernel starts.
+  // A was quantised by a kernel of the same call just before, which lets this
+  // one start only after everything before it: B is complete then.
   bool after_quantize = false;
   // launch_narrow only, where narrow_quantizes: A as a plain matrix (pitch lda
   // elements) instead of packed.

@@ -13,6 +13,15 @@ namespace mhr {
 namespace mx {
 namespace {
 
+// Launched as a programmatic dependent: the kernel before has to finish before
+// anything is read or written here, and only then may the kernel after this one
+// start -- whatever came before this kernel is complete by then, as the narrow
+// product's early loads of B need (ProductArgs::after_quantize).
+__device__ __forceinline__ void start_in_order() {
+  grid_dependency_wait();
+  grid_launch_dependents();
+}
+
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // 8 codes in a word, column i in bits [4 i, 4 i + 4).
@@ -99,7 +108,7 @@ constexpr int ROW_STEPS = 4;    // rows of a warp
 // the last up to a multiple of 128 get zero scales (the tiles are written whole).
 template <typename T, bool VEC, bool VALUES>
 __global__ void __launch_bounds__(256) quantize_rows_kernel(const RowParams p) {
-  grid_launch_dependents();
+  start_in_order();
   const int lane = threadIdx.x & 31;
   // (32-bit division: fewer than 2^31 warps of a launch, see launch_t)
   const uint32_t task = blockIdx.x * 8u + (threadIdx.x >> 5), set = task / p.chunks;
@@ -183,7 +192,7 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(const ColParams p) {
   constexpr int COLS = 32 * CPT;
   __shared__ uint4 codes_s[COLS][9];   // 8 blocks a column, padded against bank conflicts
   __shared__ alignas(8) uint8_t scale_s[COLS][8];
-  grid_launch_dependents();
+  start_in_order();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const uint32_t tn = static_cast<uint32_t>(p.tiles_n);
   const int64_t ty = blockIdx.x / tn;
@@ -269,6 +278,21 @@ __global__ void __launch_bounds__(256) quantize_cols_kernel(const ColParams p) {
   }
 }
 
+template <typename P>
+cudaError_t launch(void (*kern)(P), dim3 grid, const P& p, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 template <typename T>
 bool vec_ok(const void* p, int64_t ld, int64_t bytes) {
   return reinterpret_cast<uintptr_t>(p) % bytes == 0 &&
@@ -291,8 +315,7 @@ cudaError_t launch_t(const void* X, int64_t rows, int64_t cols, int64_t ldx, boo
                               : quantize_rows_kernel<T, true, false>)
                     : (values ? quantize_rows_kernel<T, false, true>
                               : quantize_rows_kernel<T, false, false>);
-    kern<<<grid, 256, 0, s>>>(p);
-    return cudaGetLastError();
+    return launch(kern, grid, p, s);
   }
   constexpr int64_t COLS = 32 * 4 / sizeof(T);
   const ColParams p{X,    ldx,    rows,   cols, data,
@@ -305,8 +328,7 @@ cudaError_t launch_t(const void* X, int64_t rows, int64_t cols, int64_t ldx, boo
                             : quantize_cols_kernel<T, true, false>)
                   : (values ? quantize_cols_kernel<T, false, true>
                             : quantize_cols_kernel<T, false, false>);
-  kern<<<dim3(static_cast<unsigned>(ctas)), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch(kern, dim3(static_cast<unsigned>(ctas)), p, s);
 }
 
 }  // namespace
