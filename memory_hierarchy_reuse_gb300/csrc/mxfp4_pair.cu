@@ -7,17 +7,21 @@
 // all that shared memory moves.  So both operands are staged once a pair (each
 // CTA holds its 128 rows of A and half of B), and nothing else but the scales
 // (1/16 of the operands, through tcgen05.cp) touches shared memory in the main
-// loop.
+// loop.  GB300: 8192^3 in 154 us, 7.1 PFLOP/s (a stage at 7.5, the rest is the last
+// round and the ends), 4096^3 in 26.9; 333 x 5000 x 4104 in 11.0, most of it the
+// 16 stages' and the launch's latency.
 //
 // TMEM: two accumulators of 256 columns and two sets of scales (24 columns
 // each: A's 128 rows and B's 256 rows x 8 blocks) would take 560 of the 512
 // columns.  The accumulators overlap by 48: the epilogue drains the columns
 // that the other one needs first, and the next tile's MMAs start while it
-// drains the rest.  Narrower tiles have both accumulators side by side; tiles of
+// drains the rest.  A last round that leaves half of the pairs idle is done as
+// halves of 128 columns.  Narrower tiles have both accumulators side by side; tiles of
 // 192 columns start in the middle of a scale tile every other time, and address
 // B's scales from there on (64 rows are two TMEM columns; widths that would
 // start at an odd column are not used).
 #include <cstdio>
+#include <type_traits>
 
 #include "mhr_gemm.h"
 #include "mhr_mxfp4.h"
@@ -52,7 +56,8 @@ __host__ __device__ constexpr int sf_tiles(int bn) { return (bn + 127) / 128; }
 
 struct PairParams {
   int32_t M, N;
-  int32_t tiles_m, tiles_n, num_tiles, num_kb;
+  int32_t tiles_m, tiles_n, num_kb;
+  int32_t whole, units;    // units of work: tiles done whole, then halves (128 columns) of the rest
   int32_t blocks;
   void* C;
   int64_t ldc;
@@ -68,6 +73,14 @@ __device__ __forceinline__ void tile_at(int t, const PairParams& p, int& tm, int
   const int gm = min(p.tiles_m - first, GROUP_M), r = t - g * group_size;
   tm = first + r % gm;
   tn = r / gm;
+}
+
+// First column of unit u, and its tile row.  Halves are of tiles of 256 columns.
+__device__ __forceinline__ int unit_at(int u, int bn, const PairParams& p, int& tm) {
+  int tn;
+  const int half = u < p.whole ? 0 : (u - p.whole) & 1;
+  tile_at(u < p.whole ? u : p.whole + ((u - p.whole) >> 1), p, tm, tn);
+  return tn * bn + half * 128;
 }
 
 __device__ __forceinline__ uint32_t pack16(int c_dtype, uint32_t lo, uint32_t hi) {
@@ -91,6 +104,7 @@ template <int BN, bool WIDE, bool TMA_STORE>
 __global__ void __launch_bounds__(THREADS, 1)
     mxfp4_pair_kernel(const __grid_constant__ CUtensorMap tmA,
                       const __grid_constant__ CUtensorMap tmB,
+                      const __grid_constant__ CUtensorMap tmBHalf,
                       const __grid_constant__ CUtensorMap tmSA,
                       const __grid_constant__ CUtensorMap tmSB,
                       const __grid_constant__ CUtensorMap tmC, const PairParams p) {
@@ -118,7 +132,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   constexpr uint32_t sf_set = 8 + 8 * SF_TILES;               // columns of a set of scales
   constexpr uint32_t SF_SETS = overlap ? 2 : STAGES;
   static_assert(acc1 + BN + SF_SETS * sf_set <= TMEM_COLS, "TMEM");
+  static_assert(!overlap || 128 + STAGES * 16 <= acc1, "a half and its scales");
   constexpr uint32_t stage_tx = OP_BYTES + BN / 2 * BK_BYTES + 1024 * (1 + SF_TILES);
+  constexpr uint32_t half_tx = stage_tx - (BN / 2 - 64) * BK_BYTES;
   const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&abort_flag)), rank ^ 1u);
 
   if (threadIdx.x == 0) {
@@ -150,6 +166,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
   const uint64_t limit = p.wait_limit_ns;
+  // (No grid_launch_dependents(): a quantisation let in early, call after call, cost
+  // more -- 8192^3 with its quantisation 195 us against 186, 333 x 5000 x 4104 13.9
+  // / 13.6 -- than a product let in early gains: 10.7 / 11.0 us for the latter.)
   grid_dependency_wait();
 
   auto give_up = [&](uint32_t bit) {  // by one thread: both CTAs unwind
@@ -163,11 +182,13 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
     const uint32_t fb0 = mapa_shared(full_bar(0), 0);
     bool ok = true;
-    for (int u = cluster; ok && u < p.num_tiles; u += clusters) {
-      int tm, tn;
-      tile_at(u, p, tm, tn);
+    auto load_unit = [&](auto half, int u) {
+      constexpr bool HALF_UNIT = decltype(half)::value;
+      constexpr uint32_t tx = HALF_UNIT ? half_tx : stage_tx;
+      int tm;
+      const int n0 = unit_at(u, BN, p, tm);
       const int m0 = tm * TILE_M + static_cast<int>(rank) * HALF;
-      const int n0 = tn * BN, nb0 = n0 + static_cast<int>(rank) * (BN / 2);
+      const int nb0 = n0 + static_cast<int>(rank) * (HALF_UNIT ? 64 : BN / 2);
       for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
         if (!__all_sync(0xffffffffu,
                         mbar_wait_bounded(empty_bar(s), ph, limit, &abort_flag))) {
@@ -177,10 +198,10 @@ __global__ void __launch_bounds__(THREADS, 1)
         }
         const uint32_t st = sbase + s * STAGE_BYTES, fb = fb0 + 8u * s;
         if (elect_one()) {
-          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * stage_tx);
+          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * tx);
           if (!(stall && it == 0)) {
             tma_load_2d_pair(st, &tmA, fb, kb * BK_BYTES, m0);
-            tma_load_2d_pair(st + OFF_B, &tmB, fb, kb * BK_BYTES, nb0);
+            tma_load_2d_pair(st + OFF_B, HALF_UNIT ? &tmBHalf : &tmB, fb, kb * BK_BYTES, nb0);
             // (boxes past the last row or block are filled with zeros)
             tma_load_3d_pair(st + OFF_SFA, &tmSA, fb, 0, 2 * kb, m0 / 128);
             tma_load_3d_pair(st + OFF_SFB, &tmSB, fb, 0, 2 * kb, n0 / 128);
@@ -192,11 +213,11 @@ __global__ void __launch_bounds__(THREADS, 1)
           ph ^= 1u;
         }
       }
-    }
-    // The next kernel's blocks wait for this grid's end before they read or
-    // write.  Let in at the start they wait beside it all the time: 8192^3 with
-    // its quantisation, call after call, 200 us instead of 195.
-    grid_launch_dependents();
+    };
+    int u = cluster;
+    for (; ok && u < p.whole; u += clusters) load_unit(std::false_type{}, u);
+    if constexpr (BN == MAX_BN)
+      if (ok && u < p.units) load_unit(std::true_type{}, u);
     if (lane == 0) {
       // Both CTAs' loads complete in rank 0, which waits for all of them --
       // counting as done what either side never issued -- before either CTA
@@ -213,13 +234,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         else
           atomicOr(p.status, kErrTimeoutDrain);
         const uint32_t hi = it > it1 ? it : it1;
+        const uint32_t whole_stages =
+            cluster < p.whole ? ((p.whole - 1 - cluster) / clusters + 1) * p.num_kb : 0;
         for (uint32_t i = hi > STAGES ? hi - STAGES : 0; i < hi; ++i) {
           const uint32_t s = i % STAGES, ph = (i / STAGES) & 1u;
           const bool armed = i < it, loaded0 = armed && !(stall && i == 0), loaded1 = i < it1;
+          const uint32_t tx = i < whole_stages ? stage_tx : half_tx;
           if (!armed) {
-            mbar_arrive_expect_tx(full_bar(s), stage_tx);
+            mbar_arrive_expect_tx(full_bar(s), tx);
           } else {
-            const uint32_t missing = (loaded0 ? 0u : stage_tx) + (loaded1 ? 0u : stage_tx);
+            const uint32_t missing = (loaded0 ? 0u : tx) + (loaded1 ? 0u : tx);
             if (missing) {  // once the MMA issuer has given up on the stage
               mbar_wait_bounded(full_bar(s), ph, 2 * limit, &abort_flag);
               mbar_complete_tx(full_bar(s), missing);
@@ -233,8 +257,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (leader) {
-      const uint32_t id0 = make_idesc_mxf4(TILE_M, BN, 0), id2 = make_idesc_mxf4(TILE_M, BN, 2);
-      constexpr uint32_t sf_k = 4 * SF_TILES;      // columns of B's scales for 128 columns of K
       const int tail = (p.blocks - (p.num_kb - 1) * 8 + 1) / 2;  // MMAs of a tile's last stage
       uint32_t it = 0, t = 0, s = 0, ph = 0;       // stages done; ring position and its phase
       uint32_t s2 = STAGES - 2, ph2 = 1;           // the same two stages back
@@ -243,7 +265,12 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto wait = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, limit, &abort_flag)) != 0;
       };
-      for (int u = cluster; ok && u < p.num_tiles; u += clusters, ++t) {
+      auto multiply_unit = [&](auto half, int u) {
+        constexpr bool HALF_UNIT = decltype(half)::value;
+        constexpr int COLS = HALF_UNIT ? 128 : BN, TILES = HALF_UNIT ? 1 : SF_TILES;
+        constexpr uint32_t sf_k = 4 * TILES;  // columns of B's scales for 128 columns of K
+        const uint32_t id0 = make_idesc_mxf4(TILE_M, COLS, 0);
+        const uint32_t id2 = make_idesc_mxf4(TILE_M, COLS, 2);
         // this accumulator's last tile but one has been read; of two that
         // overlap, the other one's shared columns (and with them, by the same
         // warps earlier, all of this one)
@@ -251,15 +278,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (t >= (overlap ? 1u : 2u) &&
             !wait(released_bar(before & 1u), (before >> 1) & 1u)) {
           if (lane == 0) give_up(kErrTimeoutMma);
-          break;
+          ok = false;
+          return;
         }
         tc_fence_after();
         const uint32_t d = tmem + (t & 1u ? acc1 : 0);
         uint32_t sf_row = 0;  // TMEM column of the tile's first row in its scale tile
         if constexpr (BN % 128 != 0) {
-          int tm, tn;
-          tile_at(u, p, tm, tn);
-          sf_row = (tn * BN & 127) >> 5;
+          int tm;
+          sf_row = (unit_at(u, BN, p, tm) & 127) >> 5;
         }
         for (int kb = 0; kb < p.num_kb; ++kb, ++it) {
           // A stage's scales have columns of their own -- whoever read them last
@@ -267,7 +294,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           // between two sets: then the MMAs two stages back, the last to read
           // this one, have to have finished.  (Both barriers polled once
           // together; mostly that is all.)
-          const bool older = SF_SETS < STAGES && it >= 2;
+          const bool older = !HALF_UNIT && SF_SETS < STAGES && it >= 2;
           bool there = mbar_try_wait(full_bar(s), ph);
           there = (!older || mbar_try_wait(empty_bar(s2), ph2)) && there;
           if (!__all_sync(0xffffffffu, there) &&
@@ -280,7 +307,10 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t st = sbase + s * STAGE_BYTES;
           const uint32_t a = desc_lo(st), bb = a + (OFF_B >> 4);
           const uint32_t ca = a + (OFF_SFA >> 4), cb = a + (OFF_SFB >> 4);
-          const uint32_t sfa = tmem + acc1 + BN + (SF_SETS < STAGES ? it & 1u : s) * sf_set;
+          // (a half's are next to it: the columns that its accumulator leaves free)
+          const uint32_t sfa = HALF_UNIT ? d + 128 + s * 16
+                                         : tmem + acc1 + BN +
+                                               (SF_SETS < STAGES ? it & 1u : s) * sf_set;
           const uint32_t sfb = sfa + 8;
           const uint32_t first = kb > 0 ? 1u : 0u;
           const bool full = kb + 1 < p.num_kb || tail == 4;
@@ -290,7 +320,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int i = 0; i < 2; ++i) {
               copy_scale_tile<2>(sfa + 4 * i, ca + 32 * i);
               #pragma unroll
-              for (int j = 0; j < SF_TILES; ++j)
+              for (int j = 0; j < TILES; ++j)
                 copy_scale_tile<2>(sfb + sf_k * i + 4 * j, cb + 64 * j + 32 * i);
             }
             const uint32_t sb = sfb + sf_row;
@@ -317,7 +347,11 @@ __global__ void __launch_bounds__(THREADS, 1)
             ph2 ^= 1u;
           }
         }
-      }
+      };
+      int u = cluster;
+      for (; ok && u < p.whole; u += clusters, ++t) multiply_unit(std::false_type{}, u);
+      if constexpr (BN == MAX_BN)
+        if (ok && u < p.units) multiply_unit(std::true_type{}, u);
       if (elect_one()) mma_commit_pair(drain_bar);
       __syncwarp();
       volatile int never = 0;
@@ -332,7 +366,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     constexpr int pieces = BN / COLS;
     constexpr int release = overlap ? FIRST - 1 : pieces - 1;  // the piece that frees the accumulator
     uint32_t t = 0, chunk = 0;
-    for (int u = cluster; u < p.num_tiles; u += clusters, ++t) {
+    for (int u = cluster; u < p.units; u += clusters, ++t) {
       const uint32_t b = t & 1u;
       if (!__all_sync(0xffffffffu,
                       mbar_wait_bounded(acc_bar(b), (t >> 1) & 1u, limit, &abort_flag, 128))) {
@@ -341,15 +375,16 @@ __global__ void __launch_bounds__(THREADS, 1)
         break;
       }
       tc_fence_after();
-      int tm, tn;
-      tile_at(u, p, tm, tn);
-      const int row0 = tm * TILE_M + static_cast<int>(rank) * HALF + q * 32, n0 = tn * BN;
+      int tm;
+      const int n0 = unit_at(u, BN, p, tm);
+      const int row0 = tm * TILE_M + static_cast<int>(rank) * HALF + q * 32;
+      const bool half = u >= p.whole;  // (the cluster's last unit)
       const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + (b ? acc1 : 0);
 #pragma unroll 1
-      for (int i = 0; i < pieces; ++i) {
+      for (int i = 0; i < (half ? 128 / COLS : pieces); ++i) {
         // of two that overlap, the first accumulator's shared columns are its
         // last, the second's its first
-        const int c = b || !overlap ? i : (i < FIRST ? pieces - FIRST + i : i - FIRST);
+        const int c = b || half || !overlap ? i : (i < FIRST ? pieces - FIRST + i : i - FIRST);
         uint32_t r[32];
         tmem_ld_32cols(taddr + c * COLS, r);
         if constexpr (!WIDE) {
@@ -433,9 +468,18 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// One launch on as many clusters as can run at once (at most one a tile).
+// Tiles of the last round that are done as two halves of 128 columns each, by two
+// clusters: all of them where that many are free, of tiles of 256 columns.  GB300,
+// with halves and without: 4096^3 (28 tiles left of 256) 26.8 / 28.1 us, 8192^3 (36
+// of 1024) 155.1 / 157.2.
+int64_t halves(int bn, int64_t tiles, int clusters) {
+  const int64_t rest = tiles % clusters;
+  return bn == MAX_BN && 2 * rest <= clusters ? rest : 0;
+}
+
+// One launch on as many clusters as can run at once (at most one a unit).
 template <int BN, bool WIDE, bool TMA_STORE>
-cudaError_t launch_t(const CUtensorMap (&m)[5], const PairParams& p, int device,
+cudaError_t launch_t(const CUtensorMap (&m)[6], PairParams p, int device,
                      cudaLaunchConfig_t cfg) {
   auto kern = mxfp4_pair_kernel<BN, WIDE, TMA_STORE>;
   static int most[64];  // by device; under the library's lock
@@ -447,18 +491,21 @@ cudaError_t launch_t(const CUtensorMap (&m)[5], const PairParams& p, int device,
     if (clusters < 1) return cudaErrorInvalidConfiguration;
     if (device < 64) most[device] = clusters;
   }
-  if (p.num_tiles < clusters) clusters = p.num_tiles;
+  const int rest = static_cast<int>(halves(BN, p.whole, clusters));
+  p.units = p.whole + rest;
+  p.whole -= rest;
+  if (p.units < clusters) clusters = p.units;
   cfg.gridDim = dim3(2 * clusters);
   cfg.numAttrs = 2;
   char name[48];
   snprintf(name, sizeof(name), "mxfp4_pair_kernel<n%d>", BN);
-  note_main_kernel(name, 2 * clusters, p.num_tiles);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], p);
+  note_main_kernel(name, 2 * clusters, p.units);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 template <int BN>
-cudaError_t launch_bn(const CUtensorMap (&m)[5], const PairParams& p, bool wide, bool c_tma,
+cudaError_t launch_bn(const CUtensorMap (&m)[6], const PairParams& p, bool wide, bool c_tma,
                       int device, const cudaLaunchConfig_t& cfg) {
   if (wide)
     return c_tma ? launch_t<BN, true, true>(m, p, device, cfg)
@@ -479,19 +526,22 @@ bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t kt
 }  // namespace
 
 // Tile columns.  The time is that of the busiest cluster: its rounds of tiles of
-// num_kb stages, each a fixed part and one that grows with the columns, and the
-// last tile's epilogue.  GB300, a stage of 256 / 192 / 128 columns with all
-// clusters at work (8192^3): 0.347 / 0.282 / 0.255 us, that is 226 + bn units of
-// 0.72 ns.  Narrower tiles put more clusters to work on few tiles (2000 x 300 x
-// 4000: 11.3 us with 128 columns, 15.4 with 256) and wider ones do more with a
-// stage's fixed part (8192^3: 155 us with 256, 220 with 128).
+// num_kb stages each, a last round of halves, and the last tile's epilogue, in
+// units of 0.72 ns.  GB300: a stage of 256 / 192 / 128 columns takes 470 / 376 /
+// 345 of them with all clusters at work (8192^3 in 155 / 170 / 220 us), one of a
+// half 414.  Narrower tiles put more clusters to work on few tiles (2000 x 300 x
+// 4000: 11.3 us with 128 columns, 15.4 with 256; 6144 x 4096 x 4096: 35.4 with
+// 192, 38.0 with 256), wider ones load less.
 int plan_pair_bn(int64_t M, int64_t N, int64_t K, int clusters, double* best_t) {
   const int64_t stages = (scale_tiles(K) + 1) / 2;
   int best = MAX_BN;
   for (int bn = MAX_BN; bn >= 128; bn -= 64) {
+    const double stage = bn == 256 ? 470 : bn == 192 ? 376 : 345;
     const int64_t tiles = (M + TILE_M - 1) / TILE_M * ((N + bn - 1) / bn);
-    const int64_t rounds = (tiles + clusters - 1) / clusters;
-    const double t = static_cast<double>(rounds) * stages * (226.0 + bn) + 6.0 * bn;
+    const int64_t rest = halves(bn, tiles, clusters);
+    const int64_t rounds = (tiles - rest + clusters - 1) / clusters;
+    const double t = static_cast<double>(stages) * (rounds * stage + (rest ? 414 : 0)) +
+                     6.0 * (rest ? 128 : bn);
     if (bn == MAX_BN || t < *best_t) {
       *best_t = t;
       best = bn;
@@ -540,7 +590,7 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
   p.tiles_n = static_cast<int32_t>((a.N + bn - 1) / bn);
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
-  p.num_tiles = static_cast<int32_t>(tiles);
+  p.whole = static_cast<int32_t>(tiles);  // (launch_t takes off those that are halved)
   p.blocks = static_cast<int32_t>(blocks_of(a.K));
   const int64_t kt = scale_tiles(a.K);
   p.num_kb = static_cast<int32_t>((kt + 1) / 2);
@@ -551,15 +601,17 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
   p.wait_limit_ns = ctl.wait_limit_ns;
   p.inject_stall = ctl.inject_stall;
   const int64_t row_bytes = static_cast<int64_t>(p.blocks) * 16;
-  CUtensorMap m[5];
+  CUtensorMap m[6];
   if (encode_tmap_2d(&m[0], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.A, row_bytes, a.M, a.lda, BK_BYTES,
                      HALF, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
       encode_tmap_2d(&m[1], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
                      bn / 2, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
-      !scale_map(&m[2], a.sfa, a.M, kt, 1) || !scale_map(&m[3], a.sfb, a.N, kt, sf_tiles(bn)))
+      encode_tmap_2d(&m[2], CU_TENSOR_MAP_DATA_TYPE_UINT8, a.B, row_bytes, a.N, a.ldb, BK_BYTES,
+                     64, CU_TENSOR_MAP_SWIZZLE_128B) != CUDA_SUCCESS ||
+      !scale_map(&m[3], a.sfa, a.M, kt, 1) || !scale_map(&m[4], a.sfb, a.N, kt, sf_tiles(bn)))
     return cudaErrorInvalidValue;
-  m[4] = m[0];
-  if (c_tma && encode_tmap_2d(&m[4],
+  m[5] = m[0];
+  if (c_tma && encode_tmap_2d(&m[5],
                               wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                               a.C, a.N, a.M, a.ldc * size, 128 / size, 32,

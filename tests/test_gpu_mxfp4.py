@@ -167,6 +167,20 @@ def test_product_tile_widths(mhr, width, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("M,N,K", [(2300, 2300, 300), (4000, 2500, 300), (4000, 2428, 1100)])
+def test_product_last_round_in_halves(mhr, M, N, K, dtype):
+    """Tiles of 256 columns over one and two rounds (81 and 160 of them on 76 pairs), and the
+    halves of what is left: on either accumulator, one of them past the last column."""
+    old_mode = mhr.gemm_testing_set_cta_pair_mode(2)
+    old = mhr.gemm_testing_set_pair_tile_n(256)
+    try:
+        product_case(mhr, M, N, K, dtype)
+    finally:
+        mhr.gemm_testing_set_pair_tile_n(old)
+        mhr.gemm_testing_set_cta_pair_mode(old_mode)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("M,N,K", [(5, 200, 300), (140, 200, 300), (300, 260, 520)])
 def test_product_strides_and_offsets(mhr, kernel, M, N, K, dtype):
     product_case(mhr, M, N, K, dtype, ldc=N + 3, offset=1)
