@@ -7,9 +7,9 @@
 // all that shared memory moves.  So both operands are staged once a pair (each
 // CTA holds its 128 rows of A and half of B), and nothing else but the scales
 // (1/16 of the operands, through tcgen05.cp) touches shared memory in the main
-// loop.  GB300: 8192^3 in 154 us, 7.1 PFLOP/s (a stage at 7.5, the rest is the last
-// round and the ends), 4096^3 in 26.9; 333 x 5000 x 4104 in 11.0, most of it the
-// 16 stages' and the launch's latency.
+// loop.  GB300: 8192^3 in 150 us, 7.3 PFLOP/s (a stage at 7.7, the rest is the last
+// round and the ends), 4096^3 in 27.0; 333 x 5000 x 4104 in 11.0, most of it the
+// 17 stages' and the launch's latency.
 //
 // TMEM: two accumulators of 256 columns and two sets of scales (24 columns
 // each: A's 128 rows and B's 256 rows x 8 blocks) would take 560 of the 512
@@ -48,7 +48,6 @@ constexpr int SMEM = EPI_OFF + EPI_WARPS * 2 * EPI_BUF + 1024;
 constexpr int THREADS = 192;
 constexpr uint32_t OVERLAP = 48;             // columns that two accumulators of 256 share
 constexpr uint32_t TMEM_COLS = 512;
-constexpr int GROUP_M = 8;                   // tile rows a raster group, as in the bf16 kernel
 
 // 128-row scale tiles of B that a tile of bn columns brings (192 rows that start
 // 64 into one end with the second).
@@ -57,6 +56,7 @@ __host__ __device__ constexpr int sf_tiles(int bn) { return (bn + 127) / 128; }
 struct PairParams {
   int32_t M, N;
   int32_t tiles_m, tiles_n, num_kb;
+  int32_t group;           // tile rows walked together, column by column
   int32_t whole, units;    // units of work: tiles done whole, then halves (128 columns) of the rest
   int32_t blocks;
   void* C;
@@ -68,9 +68,9 @@ struct PairParams {
 };
 
 __device__ __forceinline__ void tile_at(int t, const PairParams& p, int& tm, int& tn) {
-  const int group_size = GROUP_M * p.tiles_n;
-  const int g = t / group_size, first = g * GROUP_M;
-  const int gm = min(p.tiles_m - first, GROUP_M), r = t - g * group_size;
+  const int group_size = p.group * p.tiles_n;
+  const int g = t / group_size, first = g * p.group;
+  const int gm = min(p.tiles_m - first, p.group), r = t - g * group_size;
   tm = first + r % gm;
   tn = r / gm;
 }
@@ -588,6 +588,12 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
                                  : plan_pair_bn(a.M, a.N, a.K, ctl.sm_count / 2, &t);
   p.tiles_m = static_cast<int32_t>((a.M + TILE_M - 1) / TILE_M);
   p.tiles_n = static_cast<int32_t>((a.N + bn - 1) / bn);
+  // The order of the tiles, for L2: whole columns of up to 32 tiles, but two rows at
+  // a time of a tall C.  GB300, groups of 32 / 8 / 2 rows: 8192^3 150.7 / 155.5 /
+  // 152.9 us, 8192 x 16384 x 4096 169.0 / 181.2 / 177.5, 4096 x 11008 x 4096 64.1 /
+  // 68.0 / 66.1; 32768 x 4096 x 4096 173.5 / 168.8 / 167.8, 16384 x 8192 x 4096 171.6
+  // / 175.9 / 170.8.
+  p.group = p.tiles_m > 32 && p.tiles_n <= 32 ? 2 : 32;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
   p.whole = static_cast<int32_t>(tiles);  // (launch_t takes off those that are halved)
