@@ -20,6 +20,9 @@
  * Pointers, streams, errors and threads as in mhr_gemm.h: device pointers on
  * the current device, work enqueued on `stream`, an mhr_status returned,
  * device-side timeouts reported by gemm_check().  Empty sizes are no-ops.
+ * gemm_mxfp4_quantize, gemm_mxfp4 and the gemm_mxfp4_quantized that quantises
+ * inside the product's kernel can be captured into a graph; calls that use the
+ * library's workspace order it by events of their own and cannot.
  */
 #ifndef MHR_MXFP4_H
 #define MHR_MXFP4_H
@@ -90,8 +93,10 @@ int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const uint8_t*
  *   (ties to the lowest index, a NaN counts as largest), weights = their
  *   softmax (over the chosen ones: the full softmax renormalised);
  *   y_t = sum over the chosen of weight * down_e (silu(gate_e x_t) * (up_e x_t)),
- * rounded once to bf16; sums are fp32, the inner vector is rounded to 11
- * significant bits.  Limits: T <= 64, top <= 16, E <= 512, H and I <= 16384.
+ * rounded once to bf16; sums are fp32.  For the tensor cores x and the inner
+ * vector are written as sums of six 4-bit values a block of 32, which leaves
+ * less than 2^-16 of the block's largest magnitude.
+ * Limits: T <= 64, top <= 16, E <= 512, H and I <= 16384.
  * The call needs every SM at once (a cooperative launch): it waits for kernels
  * before it on the device to leave.
  */

@@ -252,9 +252,7 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
                                          uint8_t* scales, int n, bool staged) {
   const int lane = threadIdx.x & 31, block = lane >> 2;
   float v[8] = {v0, v1, v2, v3, v4, v5, v6, v7};
-  uint32_t amax = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) amax = max(amax, __float_as_uint(v[i]) & 0x7fffffffu);
+  uint32_t amax = __float_as_uint(max_abs8(v));
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   // the least power of two that is not below max / 6 = max / (1.5 * 4)
@@ -267,10 +265,7 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
     const bool some = c >= 1 && finite;
     const float inv = __uint_as_float(some ? static_cast<uint32_t>(254 - c) << 23 : 0u);
     const float scale = __uint_as_float(some ? static_cast<uint32_t>(c) << 23 : 0u);
-    float y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = v[i] * inv;
-    const uint32_t word = some ? e2m1x8(y) : 0u;
+    const uint32_t word = some ? encode8(v, inv) : 0u;
     *reinterpret_cast<uint32_t*>(codes + n * 128 + ((block ^ (staged ? n & 7 : 0)) << 4) +
                                  (lane & 3) * 4) = word;
     if ((lane & 3) == 0)
