@@ -528,10 +528,10 @@ bool scale_map(CUtensorMap* map, const uint8_t* scales, int64_t rows, int64_t kt
 // Tile columns.  The time is that of the busiest cluster: its rounds of tiles of
 // num_kb stages each, a last round of halves, and the last tile's epilogue, in
 // units of 0.72 ns.  GB300: a stage of 256 / 192 / 128 columns takes 470 / 376 /
-// 345 of them with all clusters at work (8192^3 in 155 / 170 / 220 us), one of a
-// half 414.  Narrower tiles put more clusters to work on few tiles (2000 x 300 x
-// 4000: 11.3 us with 128 columns, 15.4 with 256; 6144 x 4096 x 4096: 35.4 with
-// 192, 38.0 with 256), wider ones load less.
+// 345 of them with all clusters at work, one of a half 414 (4096^3 in 26.4 / 26.6 /
+// 32.2 us, 8192^3 in 149.7 / 155.4 / 202.5).  Narrower tiles put more clusters to
+// work on few tiles (2000 x 300 x 4000: 11.6 us with 128 columns, 14.0 with 192; 6144
+// x 4096 x 4096: 36.0 with 192, 38.2 with 256), wider ones load less.
 int plan_pair_bn(int64_t M, int64_t N, int64_t K, int clusters, double* best_t) {
   const int64_t stages = (scale_tiles(K) + 1) / 2;
   int best = MAX_BN;
@@ -588,18 +588,19 @@ cudaError_t launch_pair(const ProductArgs& a, const DeviceCtl& ctl, cudaStream_t
                                  : plan_pair_bn(a.M, a.N, a.K, ctl.sm_count / 2, &t);
   p.tiles_m = static_cast<int32_t>((a.M + TILE_M - 1) / TILE_M);
   p.tiles_n = static_cast<int32_t>((a.N + bn - 1) / bn);
-  // The order of the tiles, for L2: whole columns of up to 32 tiles, but two rows at
-  // a time of a tall C.  GB300, groups of 32 / 8 / 2 rows: 8192^3 150.7 / 155.5 /
-  // 152.9 us, 8192 x 16384 x 4096 169.0 / 181.2 / 177.5, 4096 x 11008 x 4096 64.1 /
-  // 68.0 / 66.1; 32768 x 4096 x 4096 173.5 / 168.8 / 167.8, 16384 x 8192 x 4096 171.6
-  // / 175.9 / 170.8.
-  p.group = p.tiles_m > 32 && p.tiles_n <= 32 ? 2 : 32;
+  const int64_t kt = scale_tiles(a.K);
+  p.num_kb = static_cast<int32_t>((kt + 1) / 2);
+  // The order of the tiles, for L2: whole columns of up to 32 tiles; two rows at a
+  // time of a tall C; rows where K is short, and C's stores, in longer runs along a
+  // row, are much of the traffic.  GB300, groups of 32 / 8 / 2 / 1 rows: 8192^3 150.7
+  // / 155.5 / 152.9 / 153.4 us, 8192 x 16384 x 4096 169.0 / 181.2 / 177.5 / 175.7;
+  // 32768 x 4096 x 4096 173.5 / 168.8 / 167.8 for the first three; 7000 x 9000 x 3000
+  // 80.8 / 78.8 / 77.0 / 77.2, 16384 x 16384 x 2048 220.8 / 238.8 / 228.6 / 212.3.
+  p.group = p.tiles_m > 32 && p.tiles_n <= 32 ? 2 : p.num_kb < 16 ? 1 : 32;
   const int64_t tiles = static_cast<int64_t>(p.tiles_m) * p.tiles_n;
   if (tiles > 0x3fffffff) return cudaErrorInvalidConfiguration;
   p.whole = static_cast<int32_t>(tiles);  // (launch_t takes off those that are halved)
   p.blocks = static_cast<int32_t>(blocks_of(a.K));
-  const int64_t kt = scale_tiles(a.K);
-  p.num_kb = static_cast<int32_t>((kt + 1) / 2);
   p.C = a.C;
   p.ldc = a.ldc;
   p.c_dtype = a.c_dtype;
