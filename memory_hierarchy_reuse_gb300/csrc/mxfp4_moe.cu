@@ -199,41 +199,78 @@ __device__ __forceinline__ void choose_token(const MoeParams& p, int t, int& exp
   weight /= sum;
 }
 
-// Step 1, all warps of the grid: router logits, a warp one expert and TT tokens.
-template <int TT>
+// Step 1, all warps of the grid: router logits, a warp one of them.
 __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, bool vr) {
   const int lane = threadIdx.x & 31;
-  const int sets = (p.T + TT - 1) / TT;
-  constexpr int N = TT == 1 ? 8 : 4;  // loads of 8 columns a row in flight
-  for (int task = warp; task < p.E * sets; task += warps) {
-    const int e = task / sets, t0 = (task - e * sets) * TT;
-    float sum[TT];
+  for (int task = warp; task < p.E * p.T; task += warps) {
+    const int e = task / p.T, t = task - e * p.T;
+    float sum = 0.f;
+    for (int k = lane * 8; k - lane * 8 < p.H; k += 8 * 256) {
+      uint4 w[8], x[8];
+      load_row<8>(p.router + e * p.ldr, k, p.H, vr, w);
+      load_row<8>(p.x + t * p.ldx, k, p.H, vx, x);
 #pragma unroll
-    for (int j = 0; j < TT; ++j) sum[j] = 0.f;
-    for (int k = lane * 8; k < p.H; k += 256 * N) {
-      uint4 w[N], x[TT][N];
-      load_row<N>(p.router + e * p.ldr, k, p.H, vr, w);
-#pragma unroll
-      for (int j = 0; j < TT; ++j) load_row<N>(p.x + min(t0 + j, p.T - 1) * p.ldx, k, p.H, vx, x[j]);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        float wf[8];
+      for (int i = 0; i < 8; ++i) {
+        float wf[8], xf[8];
         unpack_bf16(w[i], wf);
+        unpack_bf16(x[i], xf);
 #pragma unroll
-        for (int j = 0; j < TT; ++j) {
-          float xf[8];
-          unpack_bf16(x[j][i], xf);
-#pragma unroll
-          for (int c = 0; c < 8; ++c) sum[j] = fmaf(wf[c], xf[c], sum[j]);
-        }
+        for (int c = 0; c < 8; ++c) sum = fmaf(wf[c], xf[c], sum);
       }
     }
 #pragma unroll
-    for (int j = 0; j < TT; ++j) {
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (lane == 0) p.logits[t * p.E + e] = sum;
+  }
+}
+
+// The same where there are more of them than warps: a CTA 16 tokens x 8 experts, its
+// warps K in turns, added in their order.  On mma.sync (there is too little work for
+// a tcgen05 tile's set-up): a lane's 8 columns of a row are its operands of two MMAs,
+// of x and the router alike, whichever columns the MMA takes them for.
+// GB300, a call with this and with a warp a logit: 24 tokens x 128 experts of 1024
+// 28.7 / 32.7 us, 64 x 64 of 4096 53.6 / 57.3; fewer than the warps, 24 x 40 of 3000,
+// 63.5 / 62.6.
+__device__ void route_tiles(const MoeParams& p, float* parts, bool vx, bool vr) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
+  const int sets = (p.T + 15) / 16, tiles = (p.E + 7) / 8 * sets;
+#pragma unroll 1
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int e0 = tile / sets * 8, t0 = (tile - tile / sets * sets) * 16;
+    const __nv_bfloat16* w = p.router + min(e0 + g, p.E - 1) * p.ldr;
+    const __nv_bfloat16* x0 = p.x + min(t0 + g, p.T - 1) * p.ldx;
+    const __nv_bfloat16* x1 = p.x + min(t0 + g + 8, p.T - 1) * p.ldx;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+    for (int k0 = (warp & 7) * 32 + (warp >> 3) * 1024; k0 < p.H; k0 += 2048) {
+      const int k = k0 + (lane & 3) * 8;
+      uint4 b[4], a0[4], a1[4];
+      load_row<4>(w, k, p.H, vr, b);
+      load_row<4>(x0, k, p.H, vx, a0);
+      load_row<4>(x1, k, p.H, vx, a1);
+      auto mma = [&](uint32_t p0, uint32_t p1, uint32_t p2, uint32_t p3, uint32_t q0, uint32_t q1) {
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+            "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(sum[0]), "+f"(sum[1]), "+f"(sum[2]), "+f"(sum[3])
+            : "r"(p0), "r"(p1), "r"(p2), "r"(p3), "r"(q0), "r"(q1));
+      };
 #pragma unroll
-      for (int d = 16; d; d >>= 1) sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], d);
-      if (lane == 0 && t0 + j < p.T) p.logits[(t0 + j) * p.E + e] = sum[j];
+      for (int i = 0; i < 4; ++i) {
+        mma(a0[i].x, a1[i].x, a0[i].y, a1[i].y, b[i].x, b[i].y);
+        mma(a0[i].z, a1[i].z, a0[i].w, a1[i].w, b[i].z, b[i].w);
+      }
     }
+    float* mine = parts + warp * 128 + g * 8 + (lane & 3) * 2;
+    mine[0] = sum[0], mine[1] = sum[1], mine[64] = sum[2], mine[65] = sum[3];
+    __syncthreads();
+    const int t = t0 + (threadIdx.x >> 3), e = e0 + (threadIdx.x & 7);
+    if (threadIdx.x < 128 && t < p.T && e < p.E) {
+      float all = 0.f;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) all += parts[i * 128 + threadIdx.x];
+      p.logits[t * p.E + e] = all;
+    }
+    __syncthreads();
   }
 }
 
@@ -289,7 +326,7 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
 __device__ __forceinline__ bool direct_h(const MoeParams& p) { return p.T * p.top <= 16; }
 
 // Step 1, all warps of the grid: x as terms, and the logits.
-__device__ void route_start(const MoeParams& p) {
+__device__ void route_start(const MoeParams& p, float* parts) {
   const int warp = (threadIdx.x >> 5) * gridDim.x + blockIdx.x;  // neighbours on other SMs
   const int warps = gridDim.x * WARPS;
   const bool vx = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && p.ldx % 8 == 0;
@@ -306,9 +343,9 @@ __device__ void route_start(const MoeParams& p) {
                 false);
   }
   if (p.E * p.T <= warps)
-    route_logits<1>(p, warp, warps, vx, vr);
+    route_logits(p, warp, warps, vx, vr);
   else
-    route_logits<4>(p, warp, warps, vx, vr);
+    route_tiles(p, parts, vx, vr);
 }
 
 // Step 2: the top experts of the tokens t0, t0 + step, ..., and their weights.
@@ -807,24 +844,26 @@ __device__ __forceinline__ void product(Cta& c, const MoeProduct& m, const Plan&
   }
 }
 
-// Step 5, the consumers of the grid: a token's pairs added in their order,
-// four rows a thread.
+// Step 5, the consumers of the grid: a token's pairs added, four rows for four
+// lanes, which take every fourth pair each.
 __device__ __forceinline__ void combine(const Cta& c) {
   const MoeParams& p = c.p;
-  const int quads = (p.H + 3) / 4, n = p.T * quads;
+  const int quads = (p.H + 3) / 4, n = p.T * quads * 4;
   const int64_t part = static_cast<int64_t>(p.T) * p.top * p.down.pitch;
-  for (int i = blockIdx.x * CONSUMERS + threadIdx.x - 32; i < n; i += gridDim.x * CONSUMERS) {
-    const int t = i / quads, row = (i - t * quads) * 4;
+  const int parts = c.r.down.parts, sub = c.lane & 3;
+  const int loads = (p.top - sub + 3) / 4 * parts;
+  for (int i = blockIdx.x * CONSUMERS + threadIdx.x - 32; i - c.lane < n;
+       i += gridDim.x * CONSUMERS) {
+    const int at = min(i, n - 1) >> 2, t = at / quads, row = (at - t * quads) * 4;
     const float* src = p.down.sums + static_cast<int64_t>(t) * p.top * p.down.pitch + row;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     // a pair's parts are added first; eight loads are under way at once
-    const int parts = c.r.down.parts, loads = p.top * parts;
     float pair[4] = {0.f, 0.f, 0.f, 0.f};
-    int k = 0, q = 0;  // pair and part of the load to be added
+    int k = sub, q = 0;  // pair and part of the load to be added
 #pragma unroll 1
     for (int l0 = 0; l0 < loads; l0 += 8) {
       float4 v[8];
-      int lk = l0 / parts, lq = l0 - lk * parts;  // pair and part of the load
+      int lk = k, lq = q;  // pair and part of the load
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         if (l0 + j >= loads) break;
@@ -832,7 +871,7 @@ __device__ __forceinline__ void combine(const Cta& c) {
                                                       lq * part));
         if (++lq == parts) {
           lq = 0;
-          ++lk;
+          lk += 4;
         }
       }
 #pragma unroll
@@ -847,13 +886,19 @@ __device__ __forceinline__ void combine(const Cta& c) {
             pair[i4] = 0.f;
           }
           q = 0;
-          ++k;
+          k += 4;
         }
       }
     }
+    __syncwarp();
+    float y = 0.f;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (row + j < p.H) p.y[t * p.ldy + row + j] = __float2bfloat16_rn(sum[j]);
+    for (int j = 0; j < 4; ++j) {
+      sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 1);
+      sum[j] += __shfl_xor_sync(0xffffffffu, sum[j], 2);
+      if (sub == j) y = sum[j];
+    }
+    if (i < n && row + sub < p.H) p.y[t * p.ldy + row + sub] = __float2bfloat16_rn(y);
   }
 }
 
@@ -888,7 +933,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     tmem_relinquish();
   }
   for (int e = threadIdx.x; e < p.E; e += THREADS) r.count[e] = 0;
-  route_start(p);
+  route_start(p, reinterpret_cast<float*>(c.staged));
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
