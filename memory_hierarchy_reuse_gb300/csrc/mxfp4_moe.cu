@@ -590,6 +590,7 @@ __device__ __forceinline__ void grid_barrier(const Cta& c, uint32_t round) {
 __device__ __forceinline__ bool produce(Cta& c, const CUtensorMap* whole,
                                         const CUtensorMap* quarter, const MoeProduct& m,
                                         const Plan& plan) {
+  uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
   for (int s = 0; s < plan.segments; ++s) {
     const Segment sg = plan.seg[s];
     const int row0 = sg.expert * m.rows, row1 = row0 + m.rows;
@@ -597,9 +598,10 @@ __device__ __forceinline__ bool produce(Cta& c, const CUtensorMap* whole,
     for (int t = t0; t < t0 + sg.items; ++t) {
       // quarters [q0, q1) of the tile
       const int q0 = max(row0 - t * 128, 0) >> 5, q1 = min(row1 - t * 128 + 31, 128) >> 5;
-      for (int k = sg.k0; k < sg.k0 + sg.kn; ++k, ++c.it) {
-        const uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
-        if (!c.wait(c.empty_bar(st), ph ^ 1u, kErrTimeoutProducer)) return false;
+      for (int k = sg.k0; k < sg.k0 + sg.kn; ++k) {
+        if (!__all_sync(0xffffffffu, mbar_try_wait(c.empty_bar(st), ph ^ 1u)) &&
+            !c.wait(c.empty_bar(st), ph ^ 1u, kErrTimeoutProducer))
+          return false;
         const uint32_t bytes = static_cast<uint32_t>(min(2, m.kt - 2 * k)) * 512u;
         const uint32_t at = c.ring + st * RING_STAGE;
         if (elect_one()) {
@@ -614,6 +616,11 @@ __device__ __forceinline__ bool produce(Cta& c, const CUtensorMap* whole,
                     c.full_bar(st));
         }
         __syncwarp();
+        ++c.it;
+        if (++st == STAGES) {
+          st = 0;
+          ph ^= 1u;
+        }
       }
     }
   }
@@ -634,28 +641,29 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
 __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m, const Plan& plan, bool up,
                               int run) {
   const MoeParams& p = c.p;
-  constexpr int COPIES = TERMS * 10, STRIDE = 64;  // 8 pieces and 2 words a row
+  static_assert(TERMS * 10 <= 64, "two copies a lane");
   for (int s = 0; s < plan.segments; ++s) {
     const Segment sg = plan.seg[s];
     if (sg.run != run) continue;
     const uint32_t scales = smem_u32(c.staged) + sg.offset * 1024,
                    codes = scales + sg.kn * 1024;
     const int rows = staged_rows(sg.count);
-    for (int i = threadIdx.x - 32; i < sg.count * sg.kn * STRIDE; i += CONSUMERS) {
-      const int task = i / STRIDE, copy = i % STRIDE;
-      if (copy >= COPIES) continue;
-      const int col = task / sg.kn, stage = task - col * sg.kn;
+    for (int i = c.warp - 1; i < sg.count * sg.kn; i += CONSUMERS / 32) {  // a pair's stage a warp
+      const int col = i / sg.kn, stage = i - col * sg.kn;
       const int pair = c.r.list[sg.first + col];
       const uint8_t* src =
           (up ? p.x_terms : p.h_terms) +
           (static_cast<int64_t>(up ? pair / p.top : pair) * m.stages + sg.k0 + stage) * PIECE;
-      if (copy < TERMS * 8) {
-        const int n = col * TERMS + (copy >> 3), block = copy & 7;
-        cp_async_16(codes + (stage * rows + n) * 128 + ((block ^ (n & 7)) << 4), src + copy * 16);
-      } else {
-        const int w = copy - TERMS * 8, n = col * TERMS + (w >> 1);
-        cp_async_4(scales + stage * 1024 + (w & 1) * 512 + (n & 31) * 16 + (n >> 5) * 4,
-                   src + TERMS * 128 + w * 4);
+#pragma unroll
+      for (int copy = c.lane; copy < 64; copy += 32) {  // 8 pieces and 2 words a row
+        if (copy < TERMS * 8) {
+          const int n = col * TERMS + (copy >> 3), block = copy & 7;
+          cp_async_16(codes + (stage * rows + n) * 128 + ((block ^ (n & 7)) << 4), src + copy * 16);
+        } else if (copy < TERMS * 10) {
+          const int w = copy - TERMS * 8, n = col * TERMS + (w >> 1);
+          cp_async_4(scales + stage * 1024 + (w & 1) * 512 + (n & 31) * 16 + (n >> 5) * 4,
+                     src + TERMS * 128 + w * 4);
+        }
       }
     }
   }
@@ -744,34 +752,54 @@ __device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segm
   const uint32_t id0 = make_idesc_mxf4(128, rows, 0), id2 = make_idesc_mxf4(128, rows, 2);
   const uint32_t scales = desc_lo(smem_u32(c.staged) + sg.offset * 1024);
   const uint32_t codes = scales + sg.kn * (1024 >> 4);
+  uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
   for (int t = 0; t < sg.items; ++t, ++c.ph_items) {
     const uint32_t b = c.ph_items & 1u;
     if (!c.wait(c.acc_empty(b), ((c.ph_items >> 1) & 1u) ^ 1u, kErrTimeoutMma)) return false;
     tc_fence_after();
     const uint32_t d = c.tmem + b * ACC_COLS;
-    for (int k = 0; k < sg.kn; ++k, ++c.it) {
-      const uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
+    for (int k = 0; k < sg.kn; ++k) {
       // (a stage's scales have TMEM columns of their own: whoever read them last
       // had finished before the producer filled the stage again)
-      if (!c.wait(c.full_bar(st), ph, kErrTimeoutMma)) return false;
+      if (!__all_sync(0xffffffffu, mbar_try_wait(c.full_bar(st), ph)) &&
+          !c.wait(c.full_bar(st), ph, kErrTimeoutMma))
+        return false;
       tc_fence_after();
       const uint32_t w = desc_lo(c.ring + st * RING_STAGE), cw = w + (W_BYTES >> 4);
       const uint32_t x = codes + k * rows * (128 >> 4), cx = scales + k * (1024 >> 4);
       const uint32_t sfw = c.tmem + SF_COL + st * 16, sfx = sfw + 8;
-      const int kb = sg.k0 + k;
-      const int tiles = min(2, m.kt - 2 * kb), mmas = min(4, (m.blocks - kb * 8 + 1) / 2);
+      const int left = m.blocks - (sg.k0 + k) * 8;
+      const uint32_t first = k > 0 ? 1u : 0u;
       if (elect_one()) {
-        for (int i = 0; i < tiles; ++i) {
-          copy_scale_tile<1>(sfw + 4 * i, cw + 32 * i);
-          copy_scale_tile<1>(sfx + 4 * i, cx + 32 * i);
+        if (left >= 8) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            copy_scale_tile<1>(sfw + 4 * i, cw + 32 * i);
+            copy_scale_tile<1>(sfx + 4 * i, cx + 32 * i);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_mxf4<1>(d, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
+                        sfx + 4 * (kk >> 1), kk > 0 ? 1u : first);
+        } else {  // the last stage of K
+          const int kts = left > 4 ? 2 : 1, mmas = (left + 1) / 2;
+          for (int i = 0; i < kts; ++i) {
+            copy_scale_tile<1>(sfw + 4 * i, cw + 32 * i);
+            copy_scale_tile<1>(sfx + 4 * i, cx + 32 * i);
+          }
+          for (int kk = 0; kk < mmas; ++kk)
+            mma_mxf4<1>(d, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
+                        sfx + 4 * (kk >> 1), kk > 0 ? 1u : first);
         }
-        for (int kk = 0; kk < mmas; ++kk)
-          mma_mxf4<1>(d, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
-                      sfx + 4 * (kk >> 1), k > 0 || kk > 0 ? 1u : 0u);
         mma_commit(c.empty_bar(st));
         if (k + 1 == sg.kn) mma_commit(c.acc_full(b));
       }
       __syncwarp();
+      ++c.it;
+      if (++st == STAGES) {
+        st = 0;
+        ph ^= 1u;
+      }
     }
   }
   return true;
