@@ -64,9 +64,9 @@ cudaError_t zero_c(int c_dtype, void* C, int64_t M, int64_t N, int64_t ldc, cuda
 }
 
 // Up to 32 rows the narrow kernel runs, two CTAs an SM (GB300, narrow against
-// pair: 32 x 4096 x 4096 7.3 / 8.6 us, 32 x 28672 x 4096 13.8 / 18.0); more by the
-// two kernels' estimates (64 x 4096 x 4096 7.7 / 8.7, 64 x 28672 x 4096 23.1 /
-// 16.0; 200 x 300 x 8192 8.0 / 13.2, 128 x 4096 x 4096 9.4 / 9.0).
+// pair: 32 x 4096 x 4096 6.9 / 8.8 us, 32 x 28672 x 4096 13.7 / 19.1); more by the
+// two kernels' estimates (64 x 4096 x 4096 7.4 / 8.9, 64 x 28672 x 4096 20.7 /
+// 16.4; 200 x 300 x 8192 7.8 / 13.5, 200 x 4096 x 4096 11.8 / 9.1).
 // gemm_testing_set_cta_pair_mode picks a kernel, as for the other products.
 cudaError_t launch_product(const ProductArgs& a, const DeviceCtl& ctl, int device,
                            cudaStream_t s) {

@@ -14,8 +14,10 @@
 // launch instead of two, and no packed A in memory.
 //
 // Bound by HBM, or by its latency where B is small.  GB300, packed A, weights out of
-// cache: 24 x 11008 x 4096 9.2 us (2.7 TB/s), 32 x 8192 x 8192 10.7 (3.4 TB/s),
-// 1 x 4096 x 4096 5.8; an empty launch with clusters takes 2.5 of them.
+// cache: 24 x 11008 x 4096 8.8 us (2.8 TB/s), 32 x 28672 x 4096 13.7 (4.7 TB/s), 1 x
+// 4096 x 4096 5.6; an empty launch of clusters takes 2.1 of them.  (The stage's MMAs
+// are issued unrolled: with loops of a count known at run time only, a stage took 20 %
+// longer.)
 #include <type_traits>
 
 #include "mhr_gemm.h"
@@ -36,9 +38,9 @@ constexpr int THREADS = 192;           // packed A
 constexpr int PLAIN_THREADS = 512;     // A quantised here
 constexpr int PLAIN_ROWS = 32;
 // Rows x stages of K that a CTA quantises at most.  GB300, quantised here against by
-// a kernel before: 1 x 4096 x 4096 (3 of them) 6.0 / 9.2 us, 8 x 11008 x 4096 (48)
-// 10.0 / 12.3, 16 x 11008 x 4096 (96) 12.2 / 12.3, 24 x 11008 x 4096 (144) 14.6 / 12.3.
-constexpr int PLAIN_TASKS = 90;
+// a kernel before: 1 x 4096 x 4096 (3 of them) 5.9 / 7.0 us, 8 x 11008 x 4096 (48)
+// 9.5 / 10.0, 12 x 11008 x 4096 (72) 10.5 / 10.3, 24 x 11008 x 4096 (144) 13.6 / 10.7.
+constexpr int PLAIN_TASKS = 50;
 constexpr int PLAIN_BYTES = 32 * 1024;  // of the quantised part of A
 constexpr int MAX_SPLIT = 8;
 constexpr int SMEM_LIMIT = 227 * 1024;
@@ -291,15 +293,29 @@ __global__ void __launch_bounds__(std::is_void<T>::value ? THREADS : PLAIN_THREA
                                : w + (off_x >> 4);
       const uint32_t ca = PLAIN ? part + ((it * SF_BYTES) >> 4) : w + (off_sfa >> 4);
       const uint32_t sfb = tmem + p.sf_col + s * 16, sfa = sfb + 8;
-      const int tiles = min(2, p.kt - 2 * kb), mmas = min(4, (p.blocks - kb * 8 + 1) / 2);
+      const int left = p.blocks - kb * 8;
+      const uint32_t first = it > 0 ? 1u : 0u;
       if (elect_one()) {
-        for (int i = 0; i < tiles; ++i) {
-          copy_scale_tile<1>(sfb + 4 * i, cb + 32 * i);
-          copy_scale_tile<1>(sfa + 4 * i, ca + 32 * i);
+        if (left >= 8) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            copy_scale_tile<1>(sfb + 4 * i, cb + 32 * i);
+            copy_scale_tile<1>(sfa + 4 * i, ca + 32 * i);
+          }
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_mxf4<1>(tmem, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfb + 4 * (kk >> 1),
+                        sfa + 4 * (kk >> 1), kk > 0 ? 1u : first);
+        } else {  // the last stage of K
+          const int tiles = left > 4 ? 2 : 1, mmas = (left + 1) / 2;
+          for (int i = 0; i < tiles; ++i) {
+            copy_scale_tile<1>(sfb + 4 * i, cb + 32 * i);
+            copy_scale_tile<1>(sfa + 4 * i, ca + 32 * i);
+          }
+          for (int kk = 0; kk < mmas; ++kk)
+            mma_mxf4<1>(tmem, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfb + 4 * (kk >> 1),
+                        sfa + 4 * (kk >> 1), kk > 0 ? 1u : first);
         }
-        for (int kk = 0; kk < mmas; ++kk)
-          mma_mxf4<1>(tmem, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfb + 4 * (kk >> 1),
-                      sfa + 4 * (kk >> 1), it > 0 || kk > 0 ? 1u : 0u);
         mma_commit(empty_bar(s));
       }
       __syncwarp();
@@ -468,9 +484,9 @@ cudaError_t launch_t(const CUtensorMap& tmA, const CUtensorMap& tmB, const Narro
 }
 
 // Tiles and K parts of a product; the part of A that a CTA quantises if it does.
-// As many parts as can run at once: GB300, 1 x 4096 x 4096 in 1 / 2 / 4 / 8 parts
-// 8.3 / 7.2 / 6.3 / 5.5 us, 24 x 11008 x 4096 in 1 / 2 / 3 10.0 / 9.8 / 9.3 us and
-// in 4, which do not all run at once, 14.0 us.
+// As many parts as can run at once: GB300, 1 x 4096 x 4096 in 1 / 2 / 4 / 6 parts
+// 7.0 / 6.5 / 6.0 / 5.6 us, 24 x 11008 x 4096 in 1 / 2 / 3 8.6 / 8.9 / 8.8 us; in 4,
+// which do not all run at once, it took half as long again as in 3.
 cudaError_t plan_narrow(int64_t M, int64_t N, int64_t K, bool plain, int a_dtype, int device,
                         NarrowParams* p, int64_t* tiles) {
   p->M = static_cast<int32_t>(M);
@@ -511,7 +527,7 @@ cudaError_t narrow_time(int64_t M, int64_t N, int64_t K, int sms, int device, do
   if (e != cudaSuccess) return e;
   const int64_t rounds = (tiles * p.split + sms - 1) / sms;
   const int stages = (p.num_kb + p.split - 1) / p.split;
-  *us = 4.8 + 0.018 * p.nt + static_cast<double>(rounds) * stages * (0.26 + 0.0008 * p.nt);
+  *us = 4.9 + 0.018 * p.nt + static_cast<double>(rounds) * stages * (0.2 + 0.0009 * p.nt);
   return cudaSuccess;
 }
 
