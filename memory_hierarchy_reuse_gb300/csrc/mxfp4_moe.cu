@@ -30,6 +30,12 @@
 // picked so that the runs come out even.  A part's sums go to a buffer of
 // their own, and whoever reads them adds the parts in order: results do not
 // depend on the schedule.
+//
+// GB300, call after call: 64 tokens on 127 experts of 4096 x 1536 232 us (5.5 TB/s; 6.9
+// while the products run), 13 on 47 of 2600 x 1416 71 us, 8 on 51 of 2048 x 768 43 us,
+// one on 4 of 1024 x 512 18.6 us, of which the weights are one.  (A stage's MMAs are
+// issued unrolled: with loops of a count known at run time only, a CTA took 0.41 us a
+// stage, 43 GB/s, whatever the others did, and 64 tokens 253 us.)
 #include "mhr_gemm.h"
 #include "mhr_mxfp4.h"
 #include "mxfp4_common.cuh"
@@ -321,8 +327,8 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
 }
 
 // Whether each CTA makes the h that it needs as it stages it, or all of them are
-// made once, between two barriers.  GB300: 16 pairs 22.7 against 24.4 us a call, 32
-// pairs 37.1 / 36.4, 64 pairs 49.5 / 49.3, 512 pairs 261 / 255.
+// made once, between two barriers.  GB300: 16 pairs 20.5 against 22.6 us a call, 32
+// pairs 30.8 / 30.8, 64 pairs of 8 tokens 44.4 / 43.9, of 32 tokens 61.4 / 54.4.
 __device__ __forceinline__ bool direct_h(const MoeParams& p) { return p.T * p.top <= 16; }
 
 // Step 1, all warps of the grid: x as terms, and the logits.
@@ -467,8 +473,10 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
   auto end_of = [&](int ai) {
     return ai + 1 < active ? static_cast<int>(r.offset[r.active[ai + 1]]) : pairs;
   };
-  // Time of the longest run, in stages, with a quarter of one for an item's ends,
-  // times the passes that the expert with the most pairs takes.  (One column at a
+  // Time of the longest run, in stages, with half of one for an item's ends (GB300:
+  // with a quarter, 2 tokens on 7 experts of 2048 x 1024 took 24.6 us instead of
+  // 22.5, 64 tokens on 59 of 4096 x 256 49.4 instead of 47.6), times the passes that
+  // the expert with the most pairs takes.  (One column at a
   // time serves experts of one pair only: MAX_SEGMENTS counts on two, which fit 2
   // parts of any K.)
   const int parts = lane + 1;
@@ -479,7 +487,7 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
     const int stages = (m.stages + parts - 1) / parts;
     const int fit = columns_that_fit(p.stage_kb, stages);
     if (fit >= min(r.most, 2)) {
-      cost = longest * (4 * stages + 1) * ((r.most + fit - 1) / fit);
+      cost = longest * (2 * stages + 1) * ((r.most + fit - 1) / fit);
       cost = min(cost, 0x7fffffeu) * 32 + lane;  // ties: the fewest parts
     }
   }
