@@ -108,6 +108,14 @@ def test_layer_strides(mhr, shift):
     run_case(mhr, 20, 10, 3, 256, 96, shift=shift)
 
 
+@pytest.mark.parametrize("T,E,top,H,I,shift", [
+    (50, 61, 3, 203, 40, 0), (50, 61, 3, 203, 40, 1), (64, 45, 2, 2104, 33, 8),
+    (41, 120, 4, 4100, 16, 0), (17, 511, 1, 31, 8, 0)])
+def test_more_logits_than_warps(mhr, T, E, top, H, I, shift):
+    """Ragged sets of tokens and experts, rows that take no 16-byte loads, several rounds of K."""
+    run_case(mhr, T, E, top, H, I, seed=H, shift=shift)
+
+
 def test_more_columns_than_are_staged_at_once(mhr):
     """Every token on the same experts and wide rows: several passes over an expert's pairs."""
     run_case(mhr, 64, 2, 2, 8192, 96, seed=5)
