@@ -15,13 +15,15 @@
 // lie in memory: TMA moves their codes, and tcgen05.cp their scales, with no
 // instruction spent on a weight (unpacking them in registers for mma.sync took
 // some 200 issue slots per 16 x 128 weights and held the layer to 4.7 TB/s).
-// That takes e2m1 columns too, so a column is written as a sum of six: in each
+// That takes e2m1 columns too, so a column is written as a sum of eight: in each
 // block of 32 the first is x over s = 2^ceil(log2(max / 6)) rounded to e2m1,
 // and each further one the rest, over s / 4, s / 32, s / 256 and so on --
 // after the first, whose largest values are 2 apart, the rest is at most 1 s,
-// and after every other at most half its own unit.  The sixth leaves less
-// than 2^-15 s, 2^-16 of the block's largest magnitude.  The six are columns of
-// the MMA like any others, each with its own scales, and their fp32 sums are
+// and after every other at most half its own unit.  The eighth leaves at most
+// 2^-21 s, less than 2^-22 of the block's largest magnitude: what the fp32 sums
+// lose is more (2048 x 768 with loud channels, before y's rounding, six / seven /
+// eight terms 9e-6 / 1.1e-6 / 1.4e-7 of y, fp32 sums 6e-7).  The eight are columns
+// of the MMA like any others, each with its own scales, and their fp32 sums are
 // added in the epilogue: at this few columns the MMA's time is the reading of
 // the 128 weight rows.
 //
@@ -47,14 +49,14 @@ namespace {
 constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int CONSUMERS = THREADS - 32;        // all but warp 0, the producer
-constexpr int TERMS = 6;                       // e2m1 columns a bf16 or fp32 column is written as
+constexpr int TERMS = 8;                       // e2m1 columns a bf16 or fp32 column is written as
 constexpr int MAX_COLS = 128 / TERMS;          // columns an MMA takes at once: N <= 128
 constexpr int W_BYTES = 128 * 128;             // 128 rows x 256 columns of weights
 constexpr int RING_STAGE = W_BYTES + 1024;     // and their scales
 constexpr int STAGES = 6;
 constexpr int RING_BYTES = STAGES * RING_STAGE;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
-constexpr int MAX_SEGMENTS = 256;
+constexpr int MAX_SEGMENTS = 272;
 constexpr int PIECE = TERMS * (128 + 8);       // 256 columns of K as terms: codes, then scales
 constexpr uint32_t ACC_COLS = 128;             // TMEM: two accumulators, scales of each stage
 constexpr uint32_t SF_COL = 2 * ACC_COLS;
@@ -649,7 +651,7 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src) {
 __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m, const Plan& plan, bool up,
                               int run) {
   const MoeParams& p = c.p;
-  static_assert(TERMS * 10 <= 64, "two copies a lane");
+  static_assert(TERMS * 10 <= 96, "three copies a lane");
   for (int s = 0; s < plan.segments; ++s) {
     const Segment sg = plan.seg[s];
     if (sg.run != run) continue;
@@ -663,7 +665,7 @@ __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m,
           (up ? p.x_terms : p.h_terms) +
           (static_cast<int64_t>(up ? pair / p.top : pair) * m.stages + sg.k0 + stage) * PIECE;
 #pragma unroll
-      for (int copy = c.lane; copy < 64; copy += 32) {  // 8 pieces and 2 words a row
+      for (int copy = c.lane; copy < 96; copy += 32) {  // 8 pieces and 2 words a row
         if (copy < TERMS * 8) {
           const int n = col * TERMS + (copy >> 3), block = copy & 7;
           cp_async_16(codes + (stage * rows + n) * 128 + ((block ^ (n & 7)) << 4), src + copy * 16);
@@ -829,10 +831,10 @@ __device__ __forceinline__ bool write_sums(Cta& c, const MoeProduct& m, const Se
     // up: gate rows, then up rows at half the pitch
     const int at = up && row >= c.p.I ? row - c.p.I + m.pitch / 2 : row;
     float* sums = m.sums + static_cast<int64_t>(sg.part) * pairs * m.pitch + at;
-    for (int c0 = 0; c0 < sg.count; c0 += 4) {  // 4 columns: 24 TMEM columns
-      uint32_t v[3][8];
+    for (int c0 = 0; c0 < sg.count; c0 += 4) {  // 4 columns: 32 TMEM columns
+      uint32_t v[TERMS / 2][8];
 #pragma unroll
-      for (int i = 0; i < 3; ++i) tmem_ld_8cols(taddr + c0 * TERMS + 8 * i, v[i]);
+      for (int i = 0; i < TERMS / 2; ++i) tmem_ld_8cols(taddr + c0 * TERMS + 8 * i, v[i]);
       tmem_ld_wait();
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -1126,7 +1128,7 @@ cudaError_t launch_moe(const MoeArgs& a, void* workspace, uint32_t* control, con
   p.stage_kb = (kSmem - 1024 - RING_BYTES) / 1024;
   // A CTA's run touches at most ceil(rows / CTAs) + 1 rows of items (an expert's
   // part of K each), of at most T pairs each; on 152 or 148 SMs that is never more
-  // than 256 segments, reached by 64 tokens x 16 of 512 experts at K above 12800.
+  // than 264 segments, reached by 64 tokens x 8 of 512 experts at K above 15360.
   for (const MoeProduct* m : {&p.up, &p.down})
     for (int parts = 1; parts <= p.max_parts && parts <= m->stages; ++parts) {
       const int fit = columns_that_fit(p.stage_kb, (m->stages + parts - 1) / parts);
