@@ -681,9 +681,8 @@ __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m,
 }
 
 // h of a pair for 8 columns from k on: the parts' sums of gate and up in their
-// order.  (The fast exponential and division are off by some 2^-21 of silu, a
-// quarter of what two roundings of the sums are; the exact ones' code takes longer
-// to fetch than the step to run.)
+// order.  (expf and a division: the error of the fast exponential grows with the
+// gate's magnitude, some 30 units in the last place of silu at -80.)
 __device__ __forceinline__ void h_of(const Cta& c, int pair, int k, float (&h)[8]) {
   const MoeParams& p = c.p;
   const int64_t part = static_cast<int64_t>(p.T) * p.top * p.up.pitch;
@@ -717,7 +716,7 @@ __device__ __forceinline__ void h_of(const Cta& c, int pair, int k, float (&h)[8
     }
 #pragma unroll
   for (int j = 0; j < 8; ++j)
-    h[j] = k + j < p.I ? __fdividef(gate[j], 1.f + __expf(-gate[j])) * value[j] : 0.f;
+    h[j] = k + j < p.I ? gate[j] / (1.f + expf(-gate[j])) * value[j] : 0.f;
 }
 
 // h of some pairs as terms, 256 columns a warp: of all pairs into memory, by the

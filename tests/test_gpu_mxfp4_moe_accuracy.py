@@ -101,6 +101,42 @@ def test_small_values_beside_loud_ones(mhr, T, E, top, H, I):
         check(y[t], want, bound)
 
 
+def test_silu_of_gates_far_below_zero(mhr):
+    """Pairs of inner values that cancel to 16 bits, one of a gate from -10 to -85 and one of a gate
+    of 32 (whose silu is 32): what is left shows the error of the first's silu."""
+    import torch
+
+    n, H, I = 32, 128, 64
+    gates = bf16(-np.linspace(10, 85, n))
+    silu = gates / (1 + np.exp(-gates))
+    shift = np.ceil(np.log2(16 / np.abs(silu))).astype(int)  # h in [16, 32)
+    h = silu * np.exp2(shift)
+    high = bf16(-h / 32)
+    low = bf16(-h / 32 - high)
+    # x: a gate of 32 and a one, the gates, the high and the low parts of the others' up values
+    x = np.zeros((1, H))
+    x[0, :2], x[0, 32:64], x[0, 64:96], x[0, 96:] = (32, 1), gates, high, low
+    j = np.arange(n)
+    codes, scales = np.zeros((2 * I, H), np.uint8), np.full((2 * I, H // 32), 127, np.uint8)
+    codes[j, 32 + j] = 2               # (code 2: one)
+    codes[n + j, 0] = 2
+    codes[I + j, 1], scales[I + j, 0] = 2, 127 + shift
+    codes[I + n + j, 64 + j] = codes[I + n + j, 96 + j] = 2
+    up, _ = matrix(codes, scales)
+    codes = np.zeros((H, I), np.uint8)
+    codes[j, j] = codes[j, n + j] = 2
+    down, _ = matrix(codes, np.full((H, I // 32), 127, np.uint8))
+    y, _, weights = mhr.moe_mxfp4(torch.from_numpy(x).bfloat16().cuda(),
+                                  torch.zeros(1, H, device="cuda").bfloat16(), up, down, 1)
+    assert mhr.gemm_check(None) == mhr.MHR_OK and float(weights) == 1
+    want = h + 32 * (high + low)
+    # silu and its product 2.5 x 2^-23 (gate and up are exact); both h in 8 terms 2^-22 of at most
+    # 32; the sums of the terms, eight of them twice, 2^-23 each of at most 64
+    bound = 2.5 * 2.0 ** -23 * 32 + 2 * 2.0 ** -22 * 32 + 4 * 2.0 ** -23 * 64
+    check(y[0, :n], want, np.full(n, bound))
+    assert bool((y[0, n:] == 0).all())
+
+
 def test_the_most_segments(mhr):
     """The shape whose blocks get the most runs of items that share an expert and a part of K:
     64 tokens in one call against 8 at a time (both fp32 sums rounded to bf16, in other orders)."""
