@@ -95,7 +95,8 @@ int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const uint8_t*
  *   y_t = sum over the chosen of weight * down_e (silu(gate_e x_t) * (up_e x_t)),
  * rounded once to bf16; sums are fp32.  For the tensor cores x and the inner
  * vector are written as sums of eight 4-bit values a block of 32, which leaves
- * less than 2^-22 of the block's largest magnitude.
+ * less than 2^-22 of the block's largest magnitude, or 2^-129 where that is
+ * more (blocks below some 2^-107).
  * Limits: T <= 64, top <= 16, E <= 512, H and I <= 16384.
  * The call needs every SM at once (a cooperative launch): it waits for kernels
  * before it on the device to leave.

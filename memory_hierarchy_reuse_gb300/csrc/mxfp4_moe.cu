@@ -20,7 +20,8 @@
 // and each further one the rest, over s / 4, s / 32, s / 256 and so on --
 // after the first, whose largest values are 2 apart, the rest is at most 1 s,
 // and after every other at most half its own unit.  The eighth leaves at most
-// 2^-21 s, less than 2^-22 of the block's largest magnitude: what the fp32 sums
+// 2^-21 s, less than 2^-22 of the block's largest magnitude (or 2^-129, a quarter of
+// the smallest scale, where that is more): what the fp32 sums
 // lose is more (2048 x 768 with loud channels, before y's rounding, six / seven /
 // eight terms 9e-6 / 1.1e-6 / 1.4e-7 of y, fp32 sums 6e-7).  The eight are columns
 // of the MMA like any others, each with its own scales, and their fp32 sums are
@@ -301,21 +302,21 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
   amax = max(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
   // the least power of two that is not below max / 6 = max / (1.5 * 4)
-  const bool finite = amax < 0x7f800000u;
+  const bool finite = amax < 0x7f800000u;  // else the block's scales are NaN
   int c = static_cast<int>(amax >> 23) - 2 + ((amax & 0x7fffffu) > 0x400000u ? 1 : 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = finite ? v[i] : 0.f;
 #pragma unroll 1
   for (int j = 0; j < TERMS; ++j, ++n) {
-    // below 2^-126: nothing that an fp32 sum would see; a block with an
-    // infinity or a NaN: NaN
-    const bool some = c >= 1 && finite;
-    const float inv = __uint_as_float(some ? static_cast<uint32_t>(254 - c) << 23 : 0u);
-    const float scale = __uint_as_float(some ? static_cast<uint32_t>(c) << 23 : 0u);
-    const uint32_t word = some ? encode8(v, inv) : 0u;
+    // (no unit is below 2^-127, code 0: the terms leave 2^-129 where that is more)
+    const uint32_t code = static_cast<uint32_t>(max(c, 0));
+    const float scale = __uint_as_float(code ? code << 23 : 1u << 22);
+    const uint32_t word = encode8(v, __uint_as_float((254u - code) << 23));
     *reinterpret_cast<uint32_t*>(codes + n * 128 + ((block ^ (staged ? n & 7 : 0)) << 4) +
                                  (lane & 3) * 4) = word;
     if ((lane & 3) == 0)
       scales[staged ? (block >> 2) * 512 + (n & 31) * 16 + (n >> 5) * 4 + (block & 3)
-                    : n * 8 + block] = static_cast<uint8_t>(!finite ? 255 : some ? c : 0);
+                    : n * 8 + block] = static_cast<uint8_t>(finite ? code : 255u);
     const uint32_t h[4] = {e2m1_to_f16x2<0>(word), e2m1_to_f16x2<1>(word), e2m1_to_f16x2<2>(word),
                            e2m1_to_f16x2<3>(word)};
 #pragma unroll

@@ -2,7 +2,8 @@
 
 x and the inner vector h reach the tensor cores as eight e2m1 values a block of 32: with a first
 unit s, max <= 6 s < 2 max, the first leaves at most s, the second (unit s / 4) at most s / 8 and
-each further one an eighth of that, so that eight leave s 2^-21 < 2^-22 max. Everything else is fp32.
+each further one an eighth of that, so that eight leave s 2^-21 < 2^-22 max, or 2^-129 (a quarter of
+the smallest unit, 2^-127) where that is more. Everything else is fp32.
 """
 import numpy as np
 import pytest
@@ -10,6 +11,8 @@ import pytest
 import mxfp4_ref as ref
 
 pytestmark = pytest.mark.gpu
+
+FLOOR = 2.0 ** -129
 
 
 def bf16(a):
@@ -42,7 +45,7 @@ def sparse(rng, rows, cols, exponent, taboo=None):
 def left_over(w, v, ev):
     """What the terms of a vector v (known to within ev) leave of w v, a row of w at a time."""
     largest = (np.abs(v) + ev).reshape(-1, 32).max(1)
-    return (2.0 ** -22 * largest).repeat(32) @ np.abs(w).T
+    return np.maximum(2.0 ** -22 * largest, FLOOR).repeat(32) @ np.abs(w).T
 
 
 def expected(x, G, U, D):
@@ -135,6 +138,29 @@ def test_silu_of_gates_far_below_zero(mhr):
     bound = 2.5 * 2.0 ** -23 * 32 + 2 * 2.0 ** -22 * 32 + 4 * 2.0 ** -23 * 64
     check(y[0, :n], want, np.full(n, bound))
     assert bool((y[0, n:] == 0).all())
+
+
+@pytest.mark.parametrize("m", [96, 104, 108, 112, 116, 120, 124, 126])
+def test_blocks_near_the_smallest_numbers(mhr, m):
+    """x of some 2^-m times weights of some 2^m, and the same of h."""
+    import torch
+
+    rng = np.random.default_rng(m)
+    T, H, I = 3, 64, 64
+    x = bf16(rng.standard_normal((T, H)) * np.exp2(-m))
+    up, upv = matrix(*sparse(rng, 2 * I, H, m))
+    down, downv = matrix(*sparse(rng, H, I, 0))
+    router = torch.zeros(1, H, device="cuda").bfloat16()
+    y = mhr.moe_mxfp4(torch.from_numpy(x).bfloat16().cuda(), router, up, down, 1)[0]
+    for t in range(T):
+        check(y[t], *expected(x[t], upv[:I], upv[I:], downv))
+    x = bf16(rng.standard_normal((T, H)))
+    up, upv = matrix(*sparse(rng, 2 * I, H, -(m // 2)))
+    down, downv = matrix(*sparse(rng, H, I, m))
+    y = mhr.moe_mxfp4(torch.from_numpy(x).bfloat16().cuda(), router, up, down, 1)[0]
+    assert mhr.gemm_check(None) == mhr.MHR_OK
+    for t in range(T):
+        check(y[t], *expected(x[t], upv[:I], upv[I:], downv))
 
 
 def test_the_most_segments(mhr):
