@@ -26,7 +26,8 @@
 // eight terms 9e-6 / 1.1e-6 / 1.4e-7 of y, fp32 sums 6e-7).  The eight are columns
 // of the MMA like any others, each with its own scales, and their fp32 sums are
 // added in the epilogue: at this few columns the MMA's time is the reading of
-// the 128 weight rows.
+// the 128 weight rows.  22 columns (176 of the MMA's N) are what two accumulators and
+// the scales leave room for in TMEM.
 //
 // Work is cut into items of 128 weight rows x a part of K of one expert, and
 // every CTA takes an equal run of them; the number of parts of K (up to 16) is
@@ -51,7 +52,7 @@ constexpr int THREADS = 512;
 constexpr int WARPS = THREADS / 32;
 constexpr int CONSUMERS = THREADS - 32;        // all but warp 0, the producer
 constexpr int TERMS = 8;                       // e2m1 columns a bf16 or fp32 column is written as
-constexpr int MAX_COLS = 128 / TERMS;          // columns an MMA takes at once: N <= 128
+constexpr int MAX_COLS = 22;                   // columns an MMA takes at once, each TERMS of its N
 constexpr int W_BYTES = 128 * 128;             // 128 rows x 256 columns of weights
 constexpr int RING_STAGE = W_BYTES + 1024;     // and their scales
 constexpr int STAGES = 6;
@@ -59,10 +60,12 @@ constexpr int RING_BYTES = STAGES * RING_STAGE;
 constexpr int MAX_PAIRS = MOE_MAX_TOKENS * MOE_MAX_TOP;
 constexpr int MAX_SEGMENTS = 272;
 constexpr int PIECE = TERMS * (128 + 8);       // 256 columns of K as terms: codes, then scales
-constexpr uint32_t ACC_COLS = 128;             // TMEM: two accumulators, scales of each stage
+constexpr uint32_t ACC_COLS = MAX_COLS * TERMS;  // TMEM: two accumulators, scales of each stage
 constexpr uint32_t SF_COL = 2 * ACC_COLS;
+constexpr uint32_t SF_SET = 24;                // 128 rows of weights, up to 256 of columns
 constexpr uint32_t TMEM_COLS = 512;
-static_assert(SF_COL + STAGES * 16 <= TMEM_COLS, "scales fit");
+static_assert(SF_COL + STAGES * SF_SET <= TMEM_COLS, "scales fit");
+static_assert(ACC_COLS <= 256 && TERMS == 8, "columns in groups of 8, scales in two tiles");
 constexpr uint32_t kErrTimeoutGrid = 1u << 4;  // status word: a grid barrier's wait ran out
 
 // One of the two products: rows of an expert in the packed matrix, K, and the
@@ -455,15 +458,17 @@ __device__ void sort_pairs(const MoeParams& p, Routing& r) {
   __syncthreads();
 }
 
-// KB that `cols` columns over `stages` stages of K take when staged -- the scales'
-// tiles, then 128 bytes a row and stage -- and how many columns fit into `kb` KB.
-__device__ __forceinline__ int staged_rows(int cols) { return (cols * TERMS + 7) / 8 * 8; }
+// KB that `cols` columns over `stages` stages of K take when staged -- a stage's
+// scale tiles, 1 KB for each 128 rows, then 128 bytes a row and stage -- and how many
+// columns fit into `kb` KB.
+__device__ __forceinline__ int staged_rows(int cols) { return cols * TERMS; }
+__device__ __forceinline__ int scales_kb(int cols) { return cols > 128 / TERMS ? 2 : 1; }
 __device__ __forceinline__ int staged_kb(int cols, int stages) {
-  return stages * (1 + staged_rows(cols) / 8);
+  return stages * (scales_kb(cols) + cols);
 }
 __host__ __device__ __forceinline__ int columns_that_fit(int kb, int stages) {
-  const int n = (kb / stages - 1) * 8 / TERMS;
-  return n < 0 ? 0 : n < MAX_COLS ? n : MAX_COLS;
+  const int one = kb / stages - 1, n = one > 128 / TERMS ? one - 1 : one;
+  return n < MAX_COLS ? n : MAX_COLS;
 }
 
 // By one warp: the parts of K, then the CTA's equal run of all items -- expert by
@@ -656,9 +661,9 @@ __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m,
   for (int s = 0; s < plan.segments; ++s) {
     const Segment sg = plan.seg[s];
     if (sg.run != run) continue;
+    const int rows = staged_rows(sg.count), stage_scales = scales_kb(sg.count) * 1024;
     const uint32_t scales = smem_u32(c.staged) + sg.offset * 1024,
-                   codes = scales + sg.kn * 1024;
-    const int rows = staged_rows(sg.count);
+                   codes = scales + sg.kn * stage_scales;
     for (int i = c.warp - 1; i < sg.count * sg.kn; i += CONSUMERS / 32) {  // a pair's stage a warp
       const int col = i / sg.kn, stage = i - col * sg.kn;
       const int pair = c.r.list[sg.first + col];
@@ -672,7 +677,8 @@ __device__ __forceinline__ void stage_columns(const Cta& c, const MoeProduct& m,
           cp_async_16(codes + (stage * rows + n) * 128 + ((block ^ (n & 7)) << 4), src + copy * 16);
         } else if (copy < TERMS * 10) {
           const int w = copy - TERMS * 8, n = col * TERMS + (w >> 1);
-          cp_async_4(scales + stage * 1024 + (w & 1) * 512 + (n & 31) * 16 + (n >> 5) * 4,
+          cp_async_4(scales + stage * stage_scales + (n >> 7) * 1024 + (w & 1) * 512 +
+                         (n & 31) * 16 + (n >> 5 & 3) * 4,
                      src + TERMS * 128 + w * 4);
         }
       }
@@ -747,7 +753,7 @@ __device__ __forceinline__ void make_h(const Cta& c, const Plan& plan, int run) 
         scales = codes + TERMS * 128;
       } else {
         uint8_t* at = c.staged + plan.seg[s].offset * 1024;
-        codes = at + kn * 1024 + stage * staged_rows(plan.seg[s].count) * 128;
+        codes = at + kn * 1024 + stage * staged_rows(plan.seg[s].count) * 128;  // (up to 16 pairs)
         scales = at + stage * 1024;
       }
       split_terms(h[0], h[1], h[2], h[3], h[4], h[5], h[6], h[7], codes, scales,
@@ -760,8 +766,11 @@ __device__ __forceinline__ void make_h(const Cta& c, const Plan& plan, int run) 
 __device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segment& sg) {
   const int rows = staged_rows(sg.count);
   const uint32_t id0 = make_idesc_mxf4(128, rows, 0), id2 = make_idesc_mxf4(128, rows, 2);
+  // above 128 rows: two scale tiles for every 128 columns of K, 1 KB apart in a stage
+  const bool two = scales_kb(sg.count) == 2;
+  const uint32_t stage_scales = (two ? 2048 : 1024) >> 4, sf_k = two ? 8 : 4;
   const uint32_t scales = desc_lo(smem_u32(c.staged) + sg.offset * 1024);
-  const uint32_t codes = scales + sg.kn * (1024 >> 4);
+  const uint32_t codes = scales + sg.kn * stage_scales;
   uint32_t st = c.it % STAGES, ph = (c.it / STAGES) & 1u;
   for (int t = 0; t < sg.items; ++t, ++c.ph_items) {
     const uint32_t b = c.ph_items & 1u;
@@ -776,8 +785,8 @@ __device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segm
         return false;
       tc_fence_after();
       const uint32_t w = desc_lo(c.ring + st * RING_STAGE), cw = w + (W_BYTES >> 4);
-      const uint32_t x = codes + k * rows * (128 >> 4), cx = scales + k * (1024 >> 4);
-      const uint32_t sfw = c.tmem + SF_COL + st * 16, sfx = sfw + 8;
+      const uint32_t x = codes + k * rows * (128 >> 4), cx = scales + k * stage_scales;
+      const uint32_t sfw = c.tmem + SF_COL + st * SF_SET, sfx = sfw + 8;
       const int left = m.blocks - (sg.k0 + k) * 8;
       const uint32_t first = k > 0 ? 1u : 0u;
       if (elect_one()) {
@@ -785,21 +794,23 @@ __device__ __forceinline__ bool multiply(Cta& c, const MoeProduct& m, const Segm
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             copy_scale_tile<1>(sfw + 4 * i, cw + 32 * i);
-            copy_scale_tile<1>(sfx + 4 * i, cx + 32 * i);
+            copy_scale_tile<1>(sfx + sf_k * i, cx + 32 * i);
+            if (two) copy_scale_tile<1>(sfx + sf_k * i + 4, cx + 64 + 32 * i);
           }
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             mma_mxf4<1>(d, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
-                        sfx + 4 * (kk >> 1), kk > 0 ? 1u : first);
+                        sfx + sf_k * (kk >> 1), kk > 0 ? 1u : first);
         } else {  // the last stage of K
           const int kts = left > 4 ? 2 : 1, mmas = (left + 1) / 2;
           for (int i = 0; i < kts; ++i) {
             copy_scale_tile<1>(sfw + 4 * i, cw + 32 * i);
-            copy_scale_tile<1>(sfx + 4 * i, cx + 32 * i);
+            copy_scale_tile<1>(sfx + sf_k * i, cx + 32 * i);
+            if (two) copy_scale_tile<1>(sfx + sf_k * i + 4, cx + 64 + 32 * i);
           }
           for (int kk = 0; kk < mmas; ++kk)
             mma_mxf4<1>(d, w + 2 * kk, x + 2 * kk, kk & 1 ? id2 : id0, sfw + 4 * (kk >> 1),
-                        sfx + 4 * (kk >> 1), kk > 0 ? 1u : first);
+                        sfx + sf_k * (kk >> 1), kk > 0 ? 1u : first);
         }
         mma_commit(c.empty_bar(st));
         if (k + 1 == sg.kn) mma_commit(c.acc_full(b));

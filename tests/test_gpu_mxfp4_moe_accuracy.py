@@ -74,7 +74,8 @@ def check(y, want, bound):
 
 
 @pytest.mark.parametrize("T,E,top,H,I", [(1, 2, 1, 256, 96), (3, 3, 2, 2048, 64), (20, 4, 2, 544, 192),
-                                         (64, 2, 2, 128, 32)])
+                                         (64, 2, 2, 128, 32), (16, 1, 1, 256, 64), (17, 1, 1, 256, 64),
+                                         (22, 1, 1, 512, 64), (23, 1, 1, 1024, 96), (45, 1, 1, 256, 64)])
 def test_small_values_beside_loud_ones(mhr, T, E, top, H, I):
     """A value 2^12 times the others in every block of x, and of h, that no weight multiplies: y is
     made of what the first terms leave."""
