@@ -160,6 +160,7 @@ PyObject* quantize(PyObject* const* a, Py_ssize_t n) {
   if (axis == -1 && PyErr_Occurred()) throw Raised{};
   if (axis != 0 && axis != 1) raise(PyExc_ValueError, "%saxis must be 0 or 1");
   const int with_values = PyObject_IsTrue(a[2]);
+  if (with_values < 0) throw Raised{};
   const Plain p = plain(x, "x");
   const int device = device_of({&x});
   void* stream = stream_of(a[3], device);
