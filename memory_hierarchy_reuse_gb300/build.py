@@ -3,14 +3,17 @@
 Each translation unit is compiled in parallel, then linked into a shared
 library inside this package directory (the CUDA runtime is linked statically,
 so the library needs only the NVIDIA driver at run time). Beside it g++ compiles
-the tensor-level calls' binding (_torch_binding.so) against the installed torch.
+the 4-bit tensor-level calls' binding (_torch_binding.so) against the installed
+torch, again whenever that is another one; without torch it is left out.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -34,23 +37,40 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found")
 
 
-def _inputs() -> list[str]:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    files += [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
-    return files + [os.path.abspath(__file__)]
-
-
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _stale(target: str, folders: list[str], names: tuple[str, ...]) -> bool:
+    """Whether `target` is missing or older than a file of `folders` with one of the endings."""
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    files = [os.path.join(d, f) for d in folders for f in os.listdir(d) if f.endswith(names)]
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(f) > t for f in files + [os.path.abspath(__file__)])
+
+
+def _torch_root() -> str | None:
+    """The folder of the installed torch, found without importing it."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(os.path.abspath(spec.origin)) if spec and spec.origin else None
+
+
+def _torch_stamp(root: str) -> str:
+    """What a binding is compiled against: this interpreter, and torch's place and version."""
+    with open(os.path.join(root, "version.py")) as f:
+        return f"{sys.version}\n{root}\n{f.read()}"
+
+
+def _stamp_file() -> str:
+    return os.path.join(BUILD_DIR, "torch_binding.stamp")
+
+
+def _binding_stale(stamp: str) -> bool:
+    if _stale(BINDING, [CSRC, INCLUDE], (".cpp", ".h")) or not os.path.exists(_stamp_file()):
+        return True
+    with open(_stamp_file()) as f:
+        return f.read() != stamp
 
 
 def _build_binding() -> None:
     """The torch binding: host code only, against torch's headers and libraries."""
-    import sysconfig
-
     import torch
 
     root = os.path.dirname(os.path.abspath(torch.__file__))
@@ -71,10 +91,28 @@ def _build_binding() -> None:
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile and link the library if any source changed; returns its path."""
-    if not force and not _stale():
-        return LIB
-    os.makedirs(BUILD_DIR, exist_ok=True)
+    """Compile and link what changed; returns the library's path. The library is linked before an
+    error of the binding is raised."""
+    root = _torch_root()
+    stamp = _torch_stamp(root) if root else ""
+    library = force or _stale(LIB, [CSRC, INCLUDE], (".cu", ".cuh", ".h"))
+    bind = root is not None and (force or _binding_stale(stamp))
+    if library or bind:
+        os.makedirs(BUILD_DIR, exist_ok=True)
+    with ThreadPoolExecutor(max_workers=1) as ex:
+        binding = ex.submit(_build_binding) if bind else None
+        if library:
+            if not root:
+                sys.stderr.write("no torch: libmhr_gemm.so is built without the 4-bit tensor calls\n")
+            _build_library(verbose_ptxas)
+        if binding:
+            binding.result()
+            with open(_stamp_file(), "w") as f:
+                f.write(stamp)
+    return LIB
+
+
+def _build_library(verbose_ptxas: bool) -> None:
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden",
                     "-I", INCLUDE, "-I", CSRC]
     if verbose_ptxas or os.environ.get("MHR_PTXAS_VERBOSE"):
@@ -91,16 +129,13 @@ def build(force: bool = False, verbose_ptxas: bool = False) -> str:
             sys.stderr.write(r.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        binding = ex.submit(_build_binding)
+    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
         objs = list(ex.map(compile_one, SOURCES))
-        binding.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([cc, *ARCH, "-shared", "-o", tmp, *objs], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
