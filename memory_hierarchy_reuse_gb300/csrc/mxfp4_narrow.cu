@@ -107,14 +107,15 @@ __device__ __forceinline__ void store_c4(const NarrowParams& p, int64_t at, int 
     if (i < left) store_c(p, at + i, v[i]);
 }
 
-// 8 values of a row from column k on; zeros past the end.
+// 8 values of a row from column k on; zeros past the end.  (No read-only loads: the
+// kernel before, which may write them, still runs when this one starts.)
 template <typename T>
 __device__ __forceinline__ void load_row8(const T* row, int k, int K, bool vec, float (&v)[8]) {
   if (vec && k + 8 <= K) {
     alignas(16) T t[8];
 #pragma unroll
     for (int i = 0; i < static_cast<int>(sizeof(t) / 16); ++i)
-      reinterpret_cast<uint4*>(t)[i] = __ldg(reinterpret_cast<const uint4*>(row + k) + i);
+      reinterpret_cast<uint4*>(t)[i] = reinterpret_cast<const uint4*>(row + k)[i];
 #pragma unroll
     for (int i = 0; i < 8; ++i) v[i] = to_float(t[i]);
   } else {
