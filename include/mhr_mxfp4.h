@@ -20,9 +20,12 @@
  * Pointers, streams, errors and threads as in mhr_gemm.h: device pointers on
  * the current device, work enqueued on `stream`, an mhr_status returned,
  * device-side timeouts reported by gemm_check().  Empty sizes are no-ops.
- * gemm_mxfp4_quantize, gemm_mxfp4 and the gemm_mxfp4_quantized that quantises
- * inside the product's kernel can be captured into a graph; calls that use the
- * library's workspace order it by events of their own and cannot.
+ * gemm_mxfp4_quantize and gemm_mxfp4 can be captured into a graph, and so can a
+ * gemm_mxfp4_quantized with M <= 32, K <= 4096 and M ceil(K / 256) <= 50, which
+ * quantises inside the product's kernel at any N.  Others may use the library's
+ * workspace, ordered by events of its own, and cannot; their C comes, bit for
+ * bit, from gemm_mxfp4_quantize and gemm_mxfp4 with buffers of the caller's.
+ * gemm_mxfp4_moe always uses the workspace and cannot be captured.
  */
 #ifndef MHR_MXFP4_H
 #define MHR_MXFP4_H
@@ -97,6 +100,9 @@ int gemm_mxfp4_quantized(int a_dtype, const void* A, int c_dtype, const uint8_t*
  * vector are written as sums of eight 4-bit values a block of 32, which leaves
  * less than 2^-22 of the block's largest magnitude, or 2^-129 where that is
  * more (blocks below some 2^-107).
+ * A token whose x holds an infinity or a NaN has weights of NaN, as the softmax
+ * of such logits, and a y of NaN.  So has one with an inner value that is not
+ * finite (a product past fp32's range; the sum above could be an infinity).
  * Limits: T <= 64, top <= 16, E <= 512, H and I <= 16384.
  * The call needs every SM at once (a cooperative launch): it waits for kernels
  * before it on the device to leave.

@@ -1,7 +1,28 @@
-"""Edges of the 4-bit products: calls that start early."""
+"""Edges of the 4-bit products: what can be captured, calls that start early, pitches past 2^31 bytes."""
 import pytest
 
 pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("N", [1, 130, 40000])
+@pytest.mark.parametrize("M,K", [(1, 4096), (3, 4096), (8, 1536), (12, 1024), (16, 768), (25, 512), (32, 256)])
+def test_small_quantized_products_can_be_captured(mhr, M, K, N):
+    """The rule that the header gives: K <= 4096, at most 32 rows, rows x ceil(K / 256) <= 50."""
+    import torch
+
+    assert K <= 4096 and M <= 32 and M * -(-K // 256) <= 50
+    x = torch.randn(M, K, device="cuda").bfloat16()
+    B = mhr.quantize_mxfp4(torch.randn(N, K, device="cuda"))
+    mhr.matmul_mxfp4(x, B)
+    mhr.gemm_release()  # no workspace is left that a captured call could take
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = mhr.matmul_mxfp4(x, B)
+    x.copy_(torch.randn_like(x))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, mhr.matmul_mxfp4(x, B))
 
 
 @pytest.mark.parametrize("rows,size", [(1, 256), (4, 512), (1, 4096)])
@@ -60,3 +81,21 @@ def test_dense_products_of_what_the_call_before_wrote(mhr, size):
     assert bool(torch.isfinite(want).all()) and bool((want[-1] != 0).any())
     for _ in range(20):
         assert torch.equal(chain(False), want)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+def test_zero_k_with_rows_far_apart(mhr, dtype):
+    import torch
+
+    far = 2_300_000_000
+    buf = torch.empty(far + 4096, dtype=getattr(torch, dtype), device="cuda")
+    out = buf.as_strided((2, 300), (far, 1))
+    out.fill_(3)
+    buf[300:600] = 5
+    e = torch.empty((0,), dtype=torch.uint8, device="cuda")
+    A, B = (mhr.MxFp4Matrix(e.new_empty((n, 0)), e, n, 0) for n in (2, 300))
+    mhr.matmul_mxfp4(A, B, out=out)
+    assert bool((out == 0).all()) and bool((buf[300:600] == 5).all())
+    out.fill_(3)
+    mhr.matmul_mxfp4(torch.empty((2, 0), device="cuda"), B, out=out)
+    assert bool((out == 0).all()) and bool((buf[300:600] == 5).all())

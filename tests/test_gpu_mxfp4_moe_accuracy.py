@@ -164,6 +164,26 @@ def test_blocks_near_the_smallest_numbers(mhr, m):
         check(y[t], *expected(x[t], upv[:I], upv[I:], downv))
 
 
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_infinite_token(mhr, value):
+    """Its logits are infinities or NaN, so its weights and y are NaN; other tokens keep theirs."""
+    import torch
+
+    rng = np.random.default_rng(2)
+    T, E, H, I = 5, 6, 96, 64
+    x = torch.from_numpy(bf16(rng.standard_normal((T, H)))).bfloat16().cuda()
+    router = torch.from_numpy(bf16(rng.standard_normal((E, H)))).bfloat16().cuda()
+    up, _ = matrix(*sparse(rng, 2 * E * I, H, -2))
+    down, _ = matrix(*sparse(rng, E * H, I, 0))
+    want = mhr.moe_mxfp4(x, router, up, down, 2)
+    x[3, 40] = value
+    y, experts, weights = mhr.moe_mxfp4(x, router, up, down, 2)
+    keep = [0, 1, 2, 4]
+    assert all(torch.equal(g[keep], w[keep]) for g, w in zip((y, experts, weights), want))
+    assert bool(torch.isnan(y[3]).all()) and bool(torch.isnan(weights[3]).all())
+    assert bool(((experts >= 0) & (experts < E)).all())
+
+
 def test_the_most_segments(mhr):
     """The shape whose blocks get the most runs of items that share an expert and a part of K:
     64 tokens in one call against 8 at a time (both fp32 sums rounded to bf16, in other orders)."""
