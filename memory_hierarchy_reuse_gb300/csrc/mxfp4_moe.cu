@@ -22,8 +22,8 @@
 // and after every other at most half its own unit.  The eighth leaves at most
 // 2^-21 s, less than 2^-22 of the block's largest magnitude (or 2^-129, a quarter of
 // the smallest scale, where that is more): what the fp32 sums
-// lose is more (2048 x 768 with loud channels, before y's rounding, six / seven /
-// eight terms 9e-6 / 1.1e-6 / 1.4e-7 of y, fp32 sums 6e-7).  The eight are columns
+// lose is more (a model in 64 bits of 2048 x 768 with loud channels, before y's
+// rounding: six / seven / eight terms 9e-6 / 1.1e-6 / 1.4e-7 of y, fp32 sums 6e-7).  The eight are columns
 // of the MMA like any others, each with its own scales, and their fp32 sums are
 // added in the epilogue: at this few columns the MMA's time is the reading of
 // the 128 weight rows.  22 columns (176 of the MMA's N) are what two accumulators and
@@ -35,9 +35,10 @@
 // their own, and whoever reads them adds the parts in order: results do not
 // depend on the schedule.
 //
-// GB300, call after call: 64 tokens on 127 experts of 4096 x 1536 232 us (5.5 TB/s; 6.9
-// while the products run), 13 on 47 of 2600 x 1416 71 us, 8 on 51 of 2048 x 768 43 us,
-// one on 4 of 1024 x 512 18.6 us, of which the weights are one.  (A stage's MMAs are
+// GB300, call after call: 64 tokens on 127 experts of 4096 x 1536 234 us (5.4 TB/s; 6.9
+// while the products run, by stamps of six terms a column), 13 on 47 of 2600 x 1416 71
+// us, 8 on 51 of 2048 x 768 45 us, one on 4 of 1024 x 512 18.5 us, of which the weights
+// are one.  64 on 8 of 4096 x 1536, 16 pairs each: 53 us (six terms, 21 pairs an MMA: 49).  (A stage's MMAs are
 // issued unrolled: with loops of a count known at run time only, a CTA took 0.41 us a
 // stage, 43 GB/s, whatever the others did, and 64 tokens 253 us.)
 #include "mhr_gemm.h"
@@ -241,8 +242,8 @@ __device__ void route_logits(const MoeParams& p, int warp, int warps, bool vx, b
 // a tcgen05 tile's set-up): a lane's 8 columns of a row are its operands of two MMAs,
 // of x and the router alike, whichever columns the MMA takes them for.
 // GB300, a call with this and with a warp a logit: 24 tokens x 128 experts of 1024
-// 28.7 / 32.7 us, 64 x 64 of 4096 53.6 / 57.3; fewer than the warps, 24 x 40 of 3000,
-// 63.5 / 62.6.
+// 28.7 / 31.9 us, 64 x 64 of 4096 57.3 / 57.4; fewer than the warps, 24 x 40 of 3000 45.3
+// / 47.3, though with six terms a column 63.5 / 62.6.
 __device__ void route_tiles(const MoeParams& p, float* parts, bool vx, bool vr) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2;
   const int sets = (p.T + 15) / 16, tiles = (p.E + 7) / 8 * sets;
@@ -333,8 +334,9 @@ __device__ __noinline__ void split_terms(float v0, float v1, float v2, float v3,
 }
 
 // Whether each CTA makes the h that it needs as it stages it, or all of them are
-// made once, between two barriers.  GB300: 16 pairs 20.5 against 22.6 us a call, 32
-// pairs 30.8 / 30.8, 64 pairs of 8 tokens 44.4 / 43.9, of 32 tokens 61.4 / 54.4.
+// made once, between two barriers.  GB300, experts of 2048 x 768: 16 pairs 26.1 against
+// 26.7 us a call, 32 pairs 30.8 / 30.7, 64 pairs of 8 tokens 43.4 / 43.1, of 32 tokens
+// 45.9 / 45.1.  (Up to 16 pairs also keep to one scale tile a stage, as make_h has it.)
 __device__ __forceinline__ bool direct_h(const MoeParams& p) { return p.T * p.top <= 16; }
 
 // Step 1, all warps of the grid: x as terms, and the logits.
@@ -482,8 +484,8 @@ __device__ void plan_product(const MoeParams& p, const MoeProduct& m, const Rout
     return ai + 1 < active ? static_cast<int>(r.offset[r.active[ai + 1]]) : pairs;
   };
   // Time of the longest run, in stages, with half of one for an item's ends (GB300:
-  // with a quarter, 2 tokens on 7 experts of 2048 x 1024 took 24.6 us instead of
-  // 22.5, 64 tokens on 59 of 4096 x 256 49.4 instead of 47.6), times the passes that
+  // with a quarter, 2 tokens on 7 experts of 2048 x 1024 took 26.6 us instead of
+  // 22.6, 64 tokens with one each of 59 of 4096 x 256 39.0 instead of 37.1), times the passes that
   // the expert with the most pairs takes.  (One column at a
   // time serves experts of one pair only: MAX_SEGMENTS counts on two, which fit 2
   // parts of any K.)
