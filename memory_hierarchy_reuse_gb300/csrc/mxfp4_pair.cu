@@ -8,7 +8,7 @@
 // CTA holds its 128 rows of A and half of B), and nothing else but the scales
 // (1/16 of the operands, through tcgen05.cp) touches shared memory in the main
 // loop.  GB300, call after call on the same operands: 8192^3 in 149 us, 7.4 PFLOP/s (a
-// stage at 7.7, the rest is the last round and the ends), 4096^3 in 26.2 (29.1 on other
+// stage at 7.7, the rest is the last round and the ends), 4096^3 in 26.2 (29.3 on other
 // operands every call, which come from HBM); 333 x 5000 x 4104 in 11.2, most of it the 17
 // stages' and the launch's latency.
 //
