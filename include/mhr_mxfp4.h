@@ -23,9 +23,9 @@
  * gemm_mxfp4_quantize and gemm_mxfp4 can be captured into a graph, and so can a
  * gemm_mxfp4_quantized with M <= 32, K <= 4096 and M ceil(K / 256) <= 50, which
  * quantises inside the product's kernel at any N.  Others may use the library's
- * workspace, ordered by events of its own, and cannot; their C comes, bit for
- * bit, from gemm_mxfp4_quantize and gemm_mxfp4 with buffers of the caller's.
- * gemm_mxfp4_moe always uses the workspace and cannot be captured.
+ * workspace, which no graph may hold, and return MHR_ERR_CUDA in a capture (which
+ * goes on); their C comes, bit for bit, from gemm_mxfp4_quantize and gemm_mxfp4
+ * with buffers of the caller's.  gemm_mxfp4_moe always uses the workspace.
  */
 #ifndef MHR_MXFP4_H
 #define MHR_MXFP4_H

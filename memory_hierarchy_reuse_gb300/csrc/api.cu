@@ -328,6 +328,13 @@ int device_ctl_locked(DeviceCtl* ctl, int* dev) {
 }
 
 int workspace_locked(int dev, cudaStream_t s, size_t bytes, void** out, void** token) {
+  // A graph would keep the buffer's address after the library has freed it.
+  cudaStreamCaptureStatus capture = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &capture) != cudaSuccess) {
+    cudaGetLastError();
+    return MHR_ERR_CUDA;
+  }
+  if (capture != cudaStreamCaptureStatusNone) return MHR_ERR_CUDA;
   Workspace* w = nullptr;
   const int rc = workspace(dev, s, bytes, out, &w);
   *token = w;

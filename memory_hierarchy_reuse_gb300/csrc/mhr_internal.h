@@ -160,7 +160,8 @@ int device_ctl_locked(DeviceCtl* ctl, int* dev);
 
 // The library's workspace for entry points in other translation units: at
 // least `bytes` for (device, stream), ready for use on `s`, as an mhr_status;
-// after its launches the caller passes *token to workspace_done_locked().
+// after its launches the caller passes *token to workspace_done_locked().  Not
+// for a stream that is being captured: MHR_ERR_CUDA, with the capture untouched.
 // The caller holds library_mutex() throughout.
 int workspace_locked(int dev, cudaStream_t s, size_t bytes, void** out, void** token);
 void workspace_done_locked(void* token, cudaStream_t s);

@@ -25,6 +25,34 @@ def test_small_quantized_products_can_be_captured(mhr, M, K, N):
     assert torch.equal(got, mhr.matmul_mxfp4(x, B))
 
 
+def test_calls_with_a_workspace_are_refused_in_a_capture(mhr):
+    """A graph would keep the address of a workspace that later calls may free. The capture goes on."""
+    import torch
+
+    E, H, I = 4, 256, 64
+    big, x = torch.randn(300, 1024, device="cuda"), torch.randn(2, H, device="cuda").bfloat16()
+    B = mhr.quantize_mxfp4(torch.randn(130, 1024, device="cuda"))
+    up = mhr.quantize_mxfp4(torch.randn(2 * E * I, H, device="cuda"))
+    down = mhr.quantize_mxfp4(torch.randn(E * H, I, device="cuda"))
+    router = torch.randn(E, H, device="cuda").bfloat16()
+    want = mhr.moe_mxfp4(x, router, up, down, 2)[0], mhr.matmul_mxfp4(big, B)
+    torch.cuda.synchronize()
+    for mode in ("global", "relaxed"):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, capture_error_mode=mode):
+            with pytest.raises(mhr.GemmError):
+                mhr.moe_mxfp4(x, router, up, down, 2)
+            with pytest.raises(mhr.GemmError):
+                mhr.matmul_mxfp4(big, B)
+            got = mhr.matmul_mxfp4(mhr.quantize_mxfp4(big), B)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want[1])
+    assert torch.equal(mhr.moe_mxfp4(x, router, up, down, 2)[0], want[0])
+    assert torch.equal(mhr.matmul_mxfp4(big, B), want[1])
+    assert mhr.gemm_check(None) == mhr.MHR_OK
+
+
 @pytest.mark.parametrize("rows,size", [(1, 256), (4, 512), (1, 4096)])
 def test_products_that_read_what_the_call_before_wrote(mhr, rows, size):
     """A chain over two buffers, whose kernels start before the ones in front of them have ended:
