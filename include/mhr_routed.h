@@ -1,0 +1,90 @@
+/*
+ * mhr_routed.h -- products that go by an index per row, in libmhr_gemm.so: the
+ * router of a mixture of experts and its gradient, the sort of its rows by
+ * expert, the experts' products with their gradients, and low-rank adapters of
+ * many requests.
+ *
+ * Pointers, streams, errors and threads as in mhr_gemm.h: device pointers on
+ * the current device, work enqueued on `stream`, an mhr_status returned,
+ * device-side timeouts reported by gemm_check().  Element types are mhr_dtype
+ * (mhr_mxfp4.h).  Outputs must not overlap inputs or one another, except where
+ * a call says so.  Empty sizes are no-ops.  No call here uses the library's
+ * workspace: each can be captured into a graph, and what scratch it needs is
+ * the caller's (16-byte aligned; its contents are undefined before and after).
+ *
+ * What indices on the device hold is not known to the host: an index outside
+ * its range never causes an access; each call says what it does instead.
+ */
+#ifndef MHR_ROUTED_H
+#define MHR_ROUTED_H
+
+#include <stdint.h>
+
+#include "mhr_mxfp4.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+/* A router's scores of one token's logits: over all experts, or each by itself. */
+typedef enum mhr_score { MHR_SOFTMAX = 0, MHR_SIGMOID = 1 } mhr_score;
+/* A group's worth: its best key, or the sum of its two best. */
+typedef enum mhr_group_score { MHR_GROUP_MAX = 0, MHR_GROUP_TOP2 = 1 } mhr_group_score;
+
+/*
+ * Choose `top` of E experts for each of T tokens.  logits: T x E, pitch ld, of
+ * type dtype.  For each token
+ *   s     = softmax or sigmoid of its logits;
+ *   key   = s + bias (bias: E floats), or without one (NULL) the logit itself,
+ *           which orders as s does;
+ *   with groups > 1 (E / groups neighbours each): the group_top best groups by
+ *           group_score stay (without a bias MHR_GROUP_TOP2 sums two s);
+ *   experts = the top largest keys in descending order;
+ *   weights = s of the chosen, divided by their sum if `renormalize`, times scale.
+ * Ties go to the lowest index and NaN counts as largest, for groups as well.
+ * Keys of scores are compared as in 64 bits: where neighbours are too near for
+ * 32 the token is done again in double.  A token whose logits are all -inf has
+ * scores of zero; a sum of zero leaves weights of zero.  Renormalised weights
+ * are taken from the chosen logits alone, so that far below zero they do not
+ * underflow together.
+ * experts, weights: T x top, contiguous.
+ * Limits: E <= 512, top <= 16, groups <= 32 and a divisor of E, top <=
+ * group_top * E / groups.
+ */
+int gemm_routed_choose(int dtype, const void* logits, int64_t T, int64_t E, int64_t ld, int score,
+                       const float* bias, int64_t groups, int64_t group_top, int group_score,
+                       int64_t top, int renormalize, float scale, int32_t* experts,
+                       float* weights, void* stream);
+
+/*
+ * The gradient of the logits for one of the weights (grad_weights: T x top
+ * floats, contiguous), the choice held fixed; neither it nor the bias has one.
+ * grad_logits: T x E, pitch ldg, of type dtype; every element is written.
+ * With p the weights over scale:
+ *   softmax, renormalised   dl_j = scale p_j (g_j - sum p g) at the chosen, else 0
+ *   softmax                 dl_e = scale s_e (g_e [e chosen] - sum p g)
+ *   sigmoid, renormalised   dl_j = scale p_j (1 - s_j) (g_j - sum p g)
+ *   sigmoid                 dl_j = scale g_j s_j (1 - s_j)
+ * An entry of experts outside 0 .. E-1 takes no part; one expert twice in a row
+ * adds up.  Scores of zero (see above) have gradients of zero.
+ */
+int gemm_routed_choose_grad(int dtype, const void* logits, int64_t ld, const int32_t* experts,
+                            const float* grad_weights, int64_t T, int64_t E, int64_t top,
+                            int score, int renormalize, float scale, void* grad_logits,
+                            int64_t ldg, void* stream);
+
+/*
+ * The stable order of n entries by expert: order (n) lists the positions of
+ * those of expert 0, then of expert 1, and so on, each expert's in ascending
+ * order, and last those outside 0 .. E-1; offsets (E + 1) says where each
+ * expert's part starts, offsets[E] where the last one ends.  E <= 1024,
+ * n < 2^31.
+ */
+int gemm_routed_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* offsets,
+                     int32_t* order, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* MHR_ROUTED_H */

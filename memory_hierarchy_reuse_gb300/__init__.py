@@ -21,7 +21,9 @@ Raw entry points (same names and arguments as the C ABI; pointers are ints,
 Tensor-level helper: ``matmul(a, b, path, out=None)`` for row-major CUDA
 tensors (the last dimension contiguous; the leading dimension is the row
 stride). 4-bit operands (``include/mhr_mxfp4.h``): ``quantize_mxfp4``,
-``matmul_mxfp4`` and ``moe_mxfp4``, in ``mxfp4.py``.
+``matmul_mxfp4`` and ``moe_mxfp4``, in ``mxfp4.py``. Products by an index per
+row (``include/mhr_routed.h``): ``choose_experts``, ``choose_experts_grad`` and
+``sort_by_expert``, in ``routed.py``.
 """
 from __future__ import annotations
 
@@ -54,7 +56,8 @@ EXPORTS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_bf16_f32acc", "gemm_f32_3xtf32_n
            "gemm_testing_plan_single_tile_n", "gemm_testing_set_simt_wide_mode",
            "gemm_testing_plan_simt_wide",
            "gemm_mxfp4_scale_bytes", "gemm_mxfp4_quantize", "gemm_mxfp4", "gemm_mxfp4_quantized",
-           "gemm_mxfp4_moe")
+           "gemm_mxfp4_moe",
+           "gemm_routed_choose", "gemm_routed_choose_grad", "gemm_routed_sort")
 
 _lib = None
 
@@ -103,6 +106,15 @@ def load(path: str | None = None):
     lib.gemm_mxfp4_moe.argtypes = [vp, i64, vp, i64, vp, vp, i64, vp, vp, i64, vp, i64, vp, vp,
                                    i64, i64, i64, i64, i64, vp]
     lib.gemm_mxfp4_moe.restype = ci
+    cf = ctypes.c_float
+    lib.gemm_routed_choose.argtypes = [ci, vp, i64, i64, i64, ci, vp, i64, i64, ci, i64, ci, cf,
+                                       vp, vp, vp]
+    lib.gemm_routed_choose.restype = ci
+    lib.gemm_routed_choose_grad.argtypes = [ci, vp, i64, vp, vp, i64, i64, i64, ci, ci, cf, vp,
+                                            i64, vp]
+    lib.gemm_routed_choose_grad.restype = ci
+    lib.gemm_routed_sort.argtypes = [vp, i64, i64, vp, vp, vp]
+    lib.gemm_routed_sort.restype = ci
     lib.gemm_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.gemm_testing_set_wait_limit_ns.restype = ctypes.c_uint64
     lib.gemm_testing_set_inject_stall.argtypes = [ctypes.c_int]
@@ -319,11 +331,16 @@ def gemm_testing_plan_simt_wide(M: int, N: int, K: int, sms: int) -> int:
 
 
 def __getattr__(name):
-    # the 4-bit calls import torch, which the raw entry points do without
+    # these calls import torch, which the raw entry points do without
     if name in ("MxFp4Matrix", "mxfp4_scale_bytes", "quantize_mxfp4", "matmul_mxfp4",
                 "moe_mxfp4"):
         from . import mxfp4
 
         globals()[name] = getattr(mxfp4, name)
+        return globals()[name]
+    if name in ("choose_experts", "choose_experts_grad", "sort_by_expert"):
+        from . import routed
+
+        globals()[name] = getattr(routed, name)
         return globals()[name]
     raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

@@ -1,0 +1,124 @@
+// C-ABI front end of the operators that go by an index per row
+// (include/mhr_routed.h): argument checks and dispatch.
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <initializer_list>
+#include <mutex>
+
+#include "mhr_gemm.h"
+#include "mhr_routed.h"
+#include "routed_internal.h"
+
+#define MHR_API extern "C" __attribute__((visibility("default")))
+
+namespace mhr {
+namespace routed {
+namespace {
+
+constexpr int64_t kMaxDim = (int64_t{1} << 31) - 512;  // row and column numbers are int32
+
+int from_cuda(cudaError_t e) {
+  if (e == cudaSuccess) return MHR_OK;
+  cudaGetLastError();
+  return MHR_ERR_CUDA;
+}
+
+bool dim_ok(int64_t n) { return n >= 0 && n <= kMaxDim; }
+bool dtype_ok(int d) { return d == MHR_F32 || d == MHR_BF16 || d == MHR_F16; }
+int64_t size_of(int dtype) { return dtype == MHR_F32 ? 4 : 2; }
+bool aligned(const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// A plain matrix of elements of `size` bytes: pointer, pitch and alignment.
+bool plain_ok(const void* p, int64_t size, int64_t rows, int64_t cols, int64_t ld, ByteRange* r) {
+  int64_t pitch;
+  return p && ld >= cols && aligned(p, size) && !__builtin_mul_overflow(ld, size, &pitch) &&
+         byte_range(p, rows, cols * size, pitch, r);
+}
+bool array_ok(const void* p, int64_t size, int64_t n, ByteRange* r) {
+  return plain_ok(p, size, 1, n, n, r);
+}
+
+bool apart(std::initializer_list<ByteRange> out, std::initializer_list<ByteRange> in) {
+  for (auto o = out.begin(); o != out.end(); ++o) {
+    for (const ByteRange& i : in)
+      if (ranges_overlap(*o, i)) return false;
+    for (auto q = out.begin(); q != o; ++q)
+      if (ranges_overlap(*o, *q)) return false;
+  }
+  return true;
+}
+
+// The launch of a validated call on the current device.
+template <typename F>
+int launched(const F& f) {
+  begin_call();
+  std::lock_guard<std::mutex> lock(library_mutex());
+  DeviceCtl ctl;
+  int dev = 0;
+  if (const int rc = device_ctl_locked(&ctl, &dev); rc != MHR_OK) return rc;
+  return from_cuda(f(ctl));
+}
+
+bool router_ok(int64_t T, int64_t E, int64_t top, int score) {
+  return dim_ok(T) && E >= 1 && E <= MAX_EXPERTS && top >= 1 && top <= MAX_TOP && top <= E &&
+         (score == MHR_SOFTMAX || score == MHR_SIGMOID);
+}
+
+}  // namespace
+}  // namespace routed
+}  // namespace mhr
+
+using namespace mhr;
+using namespace mhr::routed;
+
+MHR_API int gemm_routed_choose(int dtype, const void* logits, int64_t T, int64_t E, int64_t ld,
+                               int score, const float* bias, int64_t groups, int64_t group_top,
+                               int group_score, int64_t top, int renormalize, float scale,
+                               int32_t* experts, float* weights, void* stream) {
+  if (!dtype_ok(dtype) || !router_ok(T, E, top, score) || groups < 1 || groups > MAX_GROUPS ||
+      E % groups || group_top < 1 || group_top > groups || top > group_top * (E / groups) ||
+      (group_score != MHR_GROUP_MAX && group_score != MHR_GROUP_TOP2))
+    return MHR_ERR_INVALID_ARG;
+  if (T == 0) return MHR_OK;
+  ByteRange rl, rb, re, rw;
+  if (!plain_ok(logits, size_of(dtype), T, E, ld, &rl) ||
+      (bias && !array_ok(bias, 4, E, &rb)) || !array_ok(experts, 4, T * top, &re) ||
+      !array_ok(weights, 4, T * top, &rw) || !apart({re, rw}, {rl, rb}))
+    return MHR_ERR_INVALID_ARG;
+  return launched([&](const DeviceCtl&) {
+    return launch_choose({dtype, logits, T, E, ld, score, bias, groups, group_top, group_score,
+                          top, renormalize != 0, scale, experts, weights},
+                         static_cast<cudaStream_t>(stream));
+  });
+}
+
+MHR_API int gemm_routed_choose_grad(int dtype, const void* logits, int64_t ld,
+                                    const int32_t* experts, const float* grad_weights, int64_t T,
+                                    int64_t E, int64_t top, int score, int renormalize,
+                                    float scale, void* grad_logits, int64_t ldg, void* stream) {
+  if (!dtype_ok(dtype) || !router_ok(T, E, top, score)) return MHR_ERR_INVALID_ARG;
+  if (T == 0) return MHR_OK;
+  ByteRange rl, re, rw, rg;
+  if (!plain_ok(logits, size_of(dtype), T, E, ld, &rl) || !array_ok(experts, 4, T * top, &re) ||
+      !array_ok(grad_weights, 4, T * top, &rw) ||
+      !plain_ok(grad_logits, size_of(dtype), T, E, ldg, &rg) || !apart({rg}, {rl, re, rw}))
+    return MHR_ERR_INVALID_ARG;
+  return launched([&](const DeviceCtl&) {
+    return launch_choose_grad({dtype, logits, ld, experts, grad_weights, T, E, top, score,
+                               renormalize != 0, scale, grad_logits, ldg},
+                              static_cast<cudaStream_t>(stream));
+  });
+}
+
+MHR_API int gemm_routed_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* offsets,
+                             int32_t* order, void* stream) {
+  if (!dim_ok(n) || E < 1 || E > MAX_PARTS) return MHR_ERR_INVALID_ARG;
+  ByteRange re, ro, rr;
+  if ((n > 0 && (!array_ok(experts, 4, n, &re) || !array_ok(order, 4, n, &rr))) ||
+      !array_ok(offsets, 4, E + 1, &ro) || !apart({ro, rr}, {re}))
+    return MHR_ERR_INVALID_ARG;
+  return launched([&](const DeviceCtl&) {
+    return launch_sort(experts, n, E, offsets, order, static_cast<cudaStream_t>(stream));
+  });
+}

@@ -1,0 +1,492 @@
+// The router: which experts a token goes to, with what weights, and the gradient
+// of the logits (gemm_routed_choose, gemm_routed_choose_grad).
+//
+// A warp takes a token.  Its lanes split into `groups` runs of `per` lanes (a power
+// of two), a run holds one group's logits in registers, neighbours in neighbouring
+// registers; so a group's two best are a few shuffles inside the run, and the first
+// lane and register with a value is the one of the lowest index.  The best keys are
+// taken one by one: the largest of a lane's, then of the warp's.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+#include <type_traits>
+
+#include "mhr_mxfp4.h"
+#include "mhr_routed.h"
+#include "mxfp4_common.cuh"
+#include "routed_internal.h"
+
+namespace mhr {
+namespace routed {
+namespace {
+
+using mx::from_float;
+using mx::to_float;
+
+constexpr uint32_t ALL = 0xffffffffu;
+constexpr int WARPS = 4;  // tokens a block
+
+__device__ __forceinline__ float infinity() { return __int_as_float(0x7f800000); }
+
+// Keys as unsigned numbers in the same order: -0 and 0 are one, every NaN is the
+// largest, and 0 (below -inf) stands for what cannot be chosen.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v + 0.f);
+  return v != v ? ALL : b ^ (b >> 31 ? ALL : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t ordered(double v) {
+  const uint64_t b = static_cast<uint64_t>(__double_as_longlong(v + 0.0));
+  return v != v ? ~0ull : b ^ (b >> 63 ? ~0ull : 1ull << 63);
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+  return k == ALL ? __uint_as_float(0x7fffffffu)
+                  : __uint_as_float(k >> 31 ? k ^ 0x80000000u : ~k);
+}
+__device__ __forceinline__ double key_value(uint64_t k) {
+  return k == ~0ull ? __longlong_as_double(0x7fffffffffffffffll)
+                    : __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ (1ull << 63) : ~k));
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(ALL, k); }
+__device__ __forceinline__ uint64_t warp_max(uint64_t k) {
+  const uint32_t hi = __reduce_max_sync(ALL, static_cast<uint32_t>(k >> 32));
+  const uint32_t lo =
+      __reduce_max_sync(ALL, static_cast<uint32_t>(k >> 32) == hi ? static_cast<uint32_t>(k) : 0u);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+
+__device__ __forceinline__ float warp_max_float(float v) {
+  return key_value(__reduce_max_sync(ALL, ordered(v)));
+}
+template <typename F>
+__device__ __forceinline__ F warp_sum(F v) {
+#pragma unroll
+  for (int m = 16; m; m >>= 1) v += __shfl_xor_sync(ALL, v, m);
+  return v;
+}
+
+__device__ __forceinline__ float exp_of(float x) { return expf(x); }
+__device__ __forceinline__ double exp_of(double x) { return exp(x); }
+// e^x / (1 + e^x) from the side on which nothing overflows.
+template <typename F>
+__device__ __forceinline__ F sigmoid(F x) {
+  const F e = exp_of(x < 0 ? x : -x);
+  return x < 0 ? e / (1 + e) : 1 / (1 + e);
+}
+
+struct ChooseParams {
+  const void* logits;
+  const float* bias;
+  int32_t* experts;
+  float* weights;
+  int64_t ld;
+  int32_t T, E, top, groups, group_top;
+  int32_t size, per, each;  // experts a group, lanes a group, experts a lane
+  int32_t score, top2, renormalize, vec;
+  float scale;
+};
+
+// V logits of a lane from `at` on; those past `left` are -inf.
+template <typename T, int V>
+__device__ __forceinline__ void load_lane(const T* at, int left, bool vec, float (&l)[V]) {
+  constexpr int BYTES = V * sizeof(T) < 16 ? V * sizeof(T) : 16, N = BYTES / sizeof(T);
+  if (vec && left >= V) {
+    using Word = std::conditional_t<BYTES == 16, uint4,
+                                    std::conditional_t<BYTES == 8, uint2,
+                                    std::conditional_t<BYTES == 4, uint32_t, uint16_t>>>;
+#pragma unroll
+    for (int i = 0; i < V; i += N) {
+      const Word w = *reinterpret_cast<const Word*>(at + i);
+      T e[N];
+      memcpy(e, &w, sizeof(w));
+#pragma unroll
+      for (int j = 0; j < N; ++j) l[i + j] = to_float(e[j]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = i < left ? to_float(at[i]) : -infinity();
+  }
+}
+
+// What a choice leaves in lane j <= top: the j-th best key, its expert and logit
+// (expert -1 past the last); `near`: whether groups were too near one another.
+template <typename F>
+struct Chosen {
+  F key;
+  int expert;
+  float logit;
+  bool near;
+};
+
+// Of a softmax: the row's maximum and its sum; 0 for both where all are -inf.
+template <typename F, int V>
+__device__ __forceinline__ void softmax_sums(const float (&l)[V], int count, float& most, F& sum) {
+  most = -infinity();
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (i < count) most = key_value(max(ordered(most), ordered(l[i])));
+  most = warp_max_float(most);
+  F part = 0;
+  if (most > -infinity() || most != most) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < count) part += exp_of(static_cast<F>(l[i]) - static_cast<F>(most));
+  }
+  sum = warp_sum(part);
+  if (sum == 0) most = 0;
+}
+
+template <typename F>
+__device__ __forceinline__ F score_of(float l, int kind, float most, F sum) {
+  if (kind == MHR_SIGMOID) return sigmoid(static_cast<F>(l));
+  return sum == 0 ? F(0) : exp_of(static_cast<F>(l) - static_cast<F>(most)) / sum;
+}
+
+// How far a key of 32 bits may lie from its value: the score's few roundings (expf
+// 2 ulp, sums of up to 32 + 5 terms, a division: below 2^-20 of the score together),
+// the sum with the bias 2^-24 of the key.  Twice that between two of them.
+constexpr float NEAR = 0x1p-19f;
+
+template <typename F, int V>
+__device__ __forceinline__ Chosen<F> choose(const float (&l)[V], const ChooseParams& p, int lane,
+                                            int first, int count, bool scored, float most,
+                                            F sum) {
+  using Key = std::conditional_t<sizeof(F) == 4, uint32_t, uint64_t>;
+  Key key[V];
+  Key score1 = 0, score2 = 0;  // the lane's two best scores, where groups add up scores
+  const bool sums = p.groups > 1 && p.top2;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    key[i] = 0;
+    if (i < count) {
+      F v = static_cast<F>(l[i]);
+      if (scored || sums) {
+        const F s = score_of<F>(l[i], p.score, most, sum) +
+                    (p.bias ? static_cast<F>(p.bias[first + i]) : F(0));
+        if (scored) v = s;
+        const Key k = ordered(s);
+        score2 = max(score2, min(score1, k));
+        score1 = max(score1, k);
+      }
+      key[i] = ordered(v);
+    }
+  }
+  Chosen<F> c;
+  c.near = false;
+  if (p.groups > 1) {
+    Key worth;
+    if (sums) {
+      for (int m = 1; m < p.per; m <<= 1) {
+        const Key o1 = __shfl_xor_sync(ALL, score1, m), o2 = __shfl_xor_sync(ALL, score2, m);
+        score2 = max(max(score2, o2), min(score1, o1));
+        score1 = max(score1, o1);
+      }
+      // (a group of one has no second)
+      worth = score1 ? ordered(p.size > 1 ? key_value(score1) + key_value(score2)
+                                          : key_value(score1))
+                     : Key(0);
+    } else {
+      worth = 0;
+#pragma unroll
+      for (int i = 0; i < V; ++i) worth = max(worth, key[i]);
+      for (int m = 1; m < p.per; m <<= 1) worth = max(worth, __shfl_xor_sync(ALL, worth, m));
+    }
+    const int mine = lane / p.per;
+    bool open = false;
+    Key last = 0;
+    for (int g = 0; g < p.group_top; ++g) {
+      last = warp_max(open ? Key(0) : worth);
+      const int winner = (__ffs(__ballot_sync(ALL, !open && worth == last)) - 1) / p.per;
+      if (mine == winner) open = true;
+    }
+    if (scored || sums) {  // is the best of the closed ones as good?
+      const Key next = warp_max(open ? Key(0) : worth);
+      const float a = static_cast<float>(key_value(last)), b = static_cast<float>(key_value(next));
+      // (scores are at most 1, and a group's are at least its worth less its biases)
+      const float room = NEAR * (fabsf(a) + 2.f);
+      c.near = next && !(a - b > room) && a == a;
+    }
+    if (!open) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = 0;
+    }
+  }
+  c.key = 0;
+  c.expert = -1;
+  c.logit = 0;
+  for (int j = 0; j <= p.top; ++j) {
+    Key best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i)
+      if (key[i] >= best) {
+        best = key[i];
+        at = i;
+      }
+    const Key m = warp_max(best);
+    if (m == 0) break;
+    const int owner = __ffs(__ballot_sync(ALL, best == m)) - 1;
+    float logit = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (at == i) {
+        logit = l[i];
+        if (lane == owner) key[i] = 0;
+      }
+    const int expert = __shfl_sync(ALL, first + at, owner);
+    logit = __shfl_sync(ALL, logit, owner);
+    if (lane == j) {
+      c.key = key_value(m);
+      c.expert = expert;
+      c.logit = logit;
+    }
+  }
+  return c;
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(WARPS * 32) choose_kernel(const ChooseParams p) {
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * WARPS + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const int group = lane / p.per, sub = lane - group * p.per;
+  int count = group < p.groups ? min(p.each, p.size - sub * p.each) : 0;
+  if (count < 0) count = 0;
+  const int first = count ? group * p.size + sub * p.each : 0;
+  float l[V];
+  load_lane<T, V>(static_cast<const T*>(p.logits) + t * p.ld + first, count, p.vec != 0, l);
+
+  // Without a bias the logits' own order is the scores'.
+  const bool scored = p.bias != nullptr, sums = p.groups > 1 && p.top2;
+  const bool softmax = p.score == MHR_SOFTMAX;
+  float most = 0, sum = 0;
+  if (softmax && (scored || sums || !p.renormalize)) softmax_sums<float>(l, count, most, sum);
+  Chosen<float> c = choose<float, V>(l, p, lane, first, count, scored, most, sum);
+  float s = c.expert >= 0 ? score_of<float>(c.logit, p.score, most, sum) : 0.f;
+
+  // Neighbours that 32 bits do not tell apart, unless they are the same numbers.
+  bool near = c.near;
+  if (scored) {
+    const float k1 = __shfl_down_sync(ALL, c.key, 1), l1 = __shfl_down_sync(ALL, c.logit, 1);
+    const float s1 = __shfl_down_sync(ALL, s, 1);
+    const int e1 = __shfl_down_sync(ALL, c.expert, 1);
+    if (lane < p.top && e1 >= 0) {
+      const bool same = c.logit == l1 && p.bias[c.expert] == p.bias[e1];
+      near |= !same && !(c.key - k1 > NEAR * (s + s1 + fabsf(c.key))) && c.key == c.key;
+    }
+  }
+  if (__any_sync(ALL, near)) {
+    double sum64 = 0;
+    if (softmax) softmax_sums<double>(l, count, most, sum64);
+    const Chosen<double> d = choose<double, V>(l, p, lane, first, count, scored, most, sum64);
+    c.expert = d.expert;
+    c.logit = d.logit;
+    if (softmax) sum = static_cast<float>(sum64);
+    s = c.expert >= 0 ? score_of<float>(c.logit, p.score, most, sum) : 0.f;
+  }
+
+  float w = s;
+  if (p.renormalize) {
+    const bool in = lane < p.top;
+    const float high = warp_max_float(in ? c.logit : -infinity());
+    // sigmoids of logits this low are e^x but for 1e-26 of them
+    if (softmax || high < -60.f) {
+      w = in && high != -infinity() ? expf(c.logit - high) : 0.f;
+    } else {
+      w = in ? s : 0.f;
+    }
+    const float total = warp_sum(w);
+    w = total == 0 ? 0.f : w / total;
+  }
+  if (lane < p.top) {
+    const int64_t at = static_cast<int64_t>(t) * p.top + lane;
+    p.experts[at] = c.expert;
+    p.weights[at] = p.scale * w;
+  }
+}
+
+// ------------------------------------------------------------------ gradient
+
+struct GradParams {
+  const void* logits;
+  const int32_t* experts;
+  const float* grad;
+  void* out;
+  int64_t ld, ldg;
+  int32_t T, E, top;
+  int32_t score, renormalize, vec, vec_out;
+  float scale;
+};
+
+// A warp takes a token: lane j its j-th expert, every lane V neighbouring columns of
+// the row, which the chosen ones' gradients reach through shared memory.
+template <typename T, int V>
+__global__ void __launch_bounds__(WARPS * 32) choose_grad_kernel(const GradParams p) {
+  __shared__ alignas(16) float rows[WARPS][V * 32];
+  const int lane = threadIdx.x & 31;
+  float* row = rows[threadIdx.x >> 5];
+  const int t = blockIdx.x * WARPS + (threadIdx.x >> 5);
+  if (t >= p.T) return;
+  const T* logits = static_cast<const T*>(p.logits) + t * p.ld;
+  const int first = lane * V, count = max(0, min(V, p.E - first));
+  const bool whole = p.score == MHR_SOFTMAX && !p.renormalize;
+
+  int e = -1;
+  float g = 0, l = -infinity();
+  if (lane < p.top) {
+    const int64_t at = static_cast<int64_t>(t) * p.top + lane;
+    e = p.experts[at];
+    g = p.grad[at];
+    if (e < 0 || e >= p.E) e = -1;
+    if (e >= 0) l = to_float(logits[e]);
+  }
+  float base[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) base[i] = 0;
+  float d = 0;  // of this lane's expert
+  const bool in = e >= 0;
+  if (whole) {
+    float x[V], most, sum;
+    load_lane<T, V>(logits + (count ? first : 0), count, p.vec != 0, x);
+    softmax_sums<float>(x, count, most, sum);
+    const float s = in ? score_of<float>(l, MHR_SOFTMAX, most, sum) : 0.f;
+    const float dot = warp_sum(in ? s * g : 0.f);
+    const float r = sum == 0 ? 0.f : 1.f / sum;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < count) base[i] = sum == 0 ? 0.f : -p.scale * dot * (expf(x[i] - most) * r);
+    d = in ? p.scale * s * g : 0.f;
+  } else if (p.renormalize) {
+    const float high = warp_max_float(in ? l : -infinity());
+    const bool as_softmax = p.score == MHR_SOFTMAX || high < -60.f;
+    const float s = p.score == MHR_SIGMOID && in ? sigmoid(l) : 0.f;
+    float w = 0;
+    if (as_softmax)
+      w = in && high != -infinity() ? expf(l - high) : 0.f;
+    else
+      w = s;
+    const float total = warp_sum(w);
+    w = total == 0 ? 0.f : w / total;
+    const float dot = warp_sum(in ? w * g : 0.f);
+    // (1 - s is 1 / (1 + e^l): not lost where s is next to 1)
+    const float slope = p.score == MHR_SIGMOID && in ? sigmoid(-l) : 1.f;
+    d = in ? p.scale * w * slope * (g - dot) : 0.f;
+  } else {
+    d = in ? p.scale * g * sigmoid(l) * sigmoid(-l) : 0.f;
+  }
+#pragma unroll
+  for (int i = 0; i < V; ++i) row[first + i] = base[i];
+  __syncwarp();
+  // One expert twice in a row: its first lane adds all of them up.
+  const uint32_t same = __match_any_sync(ALL, in ? e : -1 - lane);
+  if (__any_sync(ALL, (same & (same - 1)) != 0)) {
+    float total = 0;
+    for (int j = 0; j < p.top; ++j) {
+      const float dj = __shfl_sync(ALL, d, j);
+      if (same >> j & 1) total += dj;
+    }
+    d = total;
+  }
+  if (in && __ffs(same) - 1 == lane) row[e] += d;
+  __syncwarp();
+  T* out = static_cast<T*>(p.out) + t * p.ldg;
+  constexpr int N = 16 / sizeof(T);
+  if (p.vec_out) {  // 16 bytes a lane, neighbours next to one another
+    for (int c = lane * N; c + N <= p.E; c += 32 * N) {
+      T v[N];
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = from_float<T>(row[c + i]);
+      uint4 w;
+      memcpy(&w, v, sizeof(w));
+      *reinterpret_cast<uint4*>(out + c) = w;
+    }
+    for (int c = p.E / N * N + lane; c < p.E; c += 32) out[c] = from_float<T>(row[c]);
+  } else {
+    for (int c = lane; c < p.E; c += 32) out[c] = from_float<T>(row[c]);
+  }
+}
+
+bool aligned16(const void* p, int64_t pitch_bytes) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && pitch_bytes % 16 == 0;
+}
+int size_of(int dtype) { return dtype == MHR_F32 ? 4 : 2; }
+
+// f(type tag, values a lane) for the smallest V that holds `each`.
+template <typename F>
+cudaError_t by_type_and_width(int dtype, int each, const F& f) {
+  auto width = [&](auto tag) {
+    if (each <= 1) return f(tag, std::integral_constant<int, 1>{});
+    if (each <= 2) return f(tag, std::integral_constant<int, 2>{});
+    if (each <= 4) return f(tag, std::integral_constant<int, 4>{});
+    if (each <= 8) return f(tag, std::integral_constant<int, 8>{});
+    if (each <= 16) return f(tag, std::integral_constant<int, 16>{});
+    return f(tag, std::integral_constant<int, 32>{});
+  };
+  if (dtype == MHR_F32) return width(float{});
+  if (dtype == MHR_BF16) return width(__nv_bfloat16{});
+  return width(__half{});
+}
+
+}  // namespace
+
+cudaError_t launch_choose(const ChooseArgs& a, cudaStream_t s) {
+  ChooseParams p;
+  p.logits = a.logits;
+  p.bias = a.bias;
+  p.experts = a.experts;
+  p.weights = a.weights;
+  p.ld = a.ld;
+  p.T = static_cast<int32_t>(a.T);
+  p.E = static_cast<int32_t>(a.E);
+  p.top = static_cast<int32_t>(a.top);
+  p.groups = a.group_top == a.groups ? 1 : static_cast<int32_t>(a.groups);  // all stay: no choice
+  p.group_top = static_cast<int32_t>(a.group_top);
+  p.size = p.E / p.groups;
+  p.per = 32;
+  while (p.per * p.groups > 32) p.per >>= 1;
+  p.each = (p.size + p.per - 1) / p.per;
+  p.score = a.score;
+  p.top2 = a.group_score == MHR_GROUP_TOP2;
+  p.renormalize = a.renormalize;
+  p.scale = a.scale;
+  return by_type_and_width(a.dtype, p.each, [&](auto tag, auto width) {
+    constexpr int V = decltype(width)::value;
+    // lanes take whole vectors where a group splits into them
+    if (p.size % V == 0 && p.size / V <= p.per) p.each = V;
+    p.vec = aligned16(a.logits, a.ld * size_of(a.dtype)) && p.each == V && p.size % V == 0;
+    choose_kernel<decltype(tag), V>
+        <<<static_cast<unsigned>((a.T + WARPS - 1) / WARPS), WARPS * 32, 0, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  });
+}
+
+cudaError_t launch_choose_grad(const ChooseGradArgs& a, cudaStream_t s) {
+  GradParams p;
+  p.logits = a.logits;
+  p.experts = a.experts;
+  p.grad = a.grad_weights;
+  p.out = a.grad_logits;
+  p.ld = a.ld;
+  p.ldg = a.ldg;
+  p.T = static_cast<int32_t>(a.T);
+  p.E = static_cast<int32_t>(a.E);
+  p.top = static_cast<int32_t>(a.top);
+  p.score = a.score;
+  p.renormalize = a.renormalize;
+  p.scale = a.scale;
+  p.vec = aligned16(a.logits, a.ld * size_of(a.dtype));
+  p.vec_out = aligned16(a.grad_logits, a.ldg * size_of(a.dtype));
+  return by_type_and_width(a.dtype, (p.E + 31) / 32, [&](auto tag, auto width) {
+    constexpr int V = decltype(width)::value;
+    choose_grad_kernel<decltype(tag), V>
+        <<<static_cast<unsigned>((a.T + WARPS - 1) / WARPS), WARPS * 32, 0, s>>>(p);
+    note_launch();
+    return cudaGetLastError();
+  });
+}
+
+}  // namespace routed
+}  // namespace mhr

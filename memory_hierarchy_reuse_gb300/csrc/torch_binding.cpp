@@ -1,5 +1,6 @@
-// The tensor-level calls of mxfp4.py: argument checks, output allocation and
-// marshalling to the C ABI (include/mhr_mxfp4.h), nothing else.
+// The tensor-level calls of mxfp4.py and routed.py: argument checks, output
+// allocation and marshalling to the C ABI (include/mhr_mxfp4.h, mhr_routed.h),
+// nothing else.
 //
 // They are compiled because a 4-bit product of one token takes 6 us on the GPU,
 // and the same steps as Python statements on tensors took 9 us on the Grace host
@@ -15,6 +16,7 @@
 #include <cstdint>
 
 #include "mhr_mxfp4.h"
+#include "mhr_routed.h"
 
 namespace {
 
@@ -23,6 +25,9 @@ decltype(&gemm_mxfp4_quantize) g_quantize;
 decltype(&gemm_mxfp4) g_product;
 decltype(&gemm_mxfp4_quantized) g_quantized;
 decltype(&gemm_mxfp4_moe) g_moe;
+decltype(&gemm_routed_choose) g_choose;
+decltype(&gemm_routed_choose_grad) g_choose_grad;
+decltype(&gemm_routed_sort) g_sort;
 PyObject* g_matrix;  // MxFp4Matrix
 PyObject* g_error;   // GemmError
 
@@ -285,6 +290,141 @@ PyObject* moe(PyObject* const* v, Py_ssize_t n) {
                        THPVariable_Wrap(weights));
 }
 
+// ------------------------------------------------------ by an index per row (routed.py)
+
+int64_t integer(PyObject* o) {
+  const long long v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Raised{};
+  return v;
+}
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw Raised{};
+  return v != 0;
+}
+float number(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw Raised{};
+  return static_cast<float>(v);
+}
+
+// A contiguous tensor of one type.
+const at::Tensor& array(PyObject* o, at::ScalarType type, const char* name) {
+  const at::Tensor& t = tensor(o, name);
+  if (t.scalar_type() != type)
+    raise(PyExc_TypeError, type == at::kInt ? "%s must be int32" : "%s must be float32", name);
+  if (!t.is_contiguous()) raise(PyExc_ValueError, "%s must be contiguous", name);
+  return t;
+}
+
+// score and group_score as numbers of the C enums, -1 for another name
+void score_ok(int64_t score) {
+  if (score < 0) raise(PyExc_ValueError, "%sscore must be 'softmax' or 'sigmoid'");
+}
+
+// choose(logits, top, score, bias or None, groups, group_top, group_score, renormalize, scale,
+//        stream) -> experts, weights
+PyObject* choose(PyObject* const* v, Py_ssize_t n) {
+  count(n, 10);
+  const at::Tensor& logits = tensor(v[0], "logits");
+  const int type = dtype_of(logits, "logits");
+  const Plain p = plain(logits, "logits");
+  const int64_t top = integer(v[1]), score = integer(v[2]);
+  score_ok(score);
+  int device = device_of({&logits});
+  const float* bias = nullptr;
+  if (v[3] != Py_None) {
+    const at::Tensor& b = array(v[3], at::kFloat, "bias");
+    if (b.dim() != 1 || b.size(0) != p.cols) raise(PyExc_ValueError, "%sbias must be of E values");
+    device = device_of({&logits, &b});
+    bias = static_cast<const float*>(b.data_ptr());
+  }
+  const int64_t groups = integer(v[4]), group_top = integer(v[5]), group_score = integer(v[6]);
+  if (groups < 1 || p.cols % groups || group_top < 1 || group_top > groups)
+    raise(PyExc_ValueError, "%sgroups must divide the experts, group_top be 1 to groups");
+  if (group_score < 0) raise(PyExc_ValueError, "%sgroup_score must be 'max' or 'top2'");
+  if (top < 1 || top > group_top * (p.cols / groups))
+    raise(PyExc_ValueError, "%stop must be 1 to the number of experts in group_top groups");
+  const bool renormalize = truth(v[7]);
+  const float scale = number(v[8]);
+  void* stream = stream_of(v[9], device);
+  at::Tensor experts = empty({p.rows, top}, at::kInt, device);
+  at::Tensor weights = empty({p.rows, top}, at::kFloat, device);
+  run("gemm_routed_choose", device, [&] {
+    return g_choose(type, logits.data_ptr(), p.rows, p.cols, p.ld, static_cast<int>(score), bias,
+                    groups, group_top, static_cast<int>(group_score), top, renormalize, scale,
+                    static_cast<int32_t*>(experts.data_ptr()),
+                    static_cast<float*>(weights.data_ptr()), stream);
+  });
+  return Py_BuildValue("NN", THPVariable_Wrap(experts), THPVariable_Wrap(weights));
+}
+
+// choose_grad(logits, experts, grad_weights, score, renormalize, scale, out or None, stream)
+PyObject* choose_grad(PyObject* const* v, Py_ssize_t n) {
+  count(n, 8);
+  const at::Tensor& logits = tensor(v[0], "logits");
+  const int type = dtype_of(logits, "logits");
+  const Plain p = plain(logits, "logits");
+  const at::Tensor& experts = array(v[1], at::kInt, "experts");
+  const at::Tensor& grad = array(v[2], at::kFloat, "grad_weights");
+  if (experts.dim() != 2 || experts.size(0) != p.rows || grad.sizes() != experts.sizes())
+    raise(PyExc_ValueError, "%sexperts and grad_weights must be T x top");
+  const int64_t top = experts.size(1), score = integer(v[3]);
+  score_ok(score);
+  const bool renormalize = truth(v[4]);
+  const float scale = number(v[5]);
+  const int device = device_of({&logits, &experts, &grad});
+  at::Tensor out;
+  if (v[6] == Py_None) {
+    out = empty({p.rows, p.cols}, logits.scalar_type(), device);
+  } else {
+    out = tensor(v[6], "out");
+    device_of({&logits, &out});
+  }
+  const Plain po = plain(out, "out");
+  if (out.scalar_type() != logits.scalar_type() || po.rows != p.rows || po.cols != p.cols)
+    raise(PyExc_TypeError, "%sout must be of the logits' type and shape");
+  void* stream = stream_of(v[7], device);
+  run("gemm_routed_choose_grad", device, [&] {
+    return g_choose_grad(type, logits.data_ptr(), p.ld,
+                         static_cast<const int32_t*>(experts.data_ptr()),
+                         static_cast<const float*>(grad.data_ptr()), p.rows, p.cols, top,
+                         static_cast<int>(score), renormalize, scale, out.data_ptr(), po.ld,
+                         stream);
+  });
+  return THPVariable_Wrap(out);
+}
+
+// sort(experts, count, stream) -> offsets, order
+PyObject* sort(PyObject* const* v, Py_ssize_t n) {
+  count(n, 3);
+  const at::Tensor& experts = array(v[0], at::kInt, "experts");
+  const int64_t E = integer(v[1]);
+  if (E < 1) raise(PyExc_ValueError, "%scount must be at least 1");
+  const int device = device_of({&experts});
+  void* stream = stream_of(v[2], device);
+  at::Tensor offsets = empty({E + 1}, at::kInt, device);
+  at::Tensor order = empty({experts.numel()}, at::kInt, device);
+  run("gemm_routed_sort", device, [&] {
+    return g_sort(static_cast<const int32_t*>(experts.data_ptr()), experts.numel(), E,
+                  static_cast<int32_t*>(offsets.data_ptr()),
+                  static_cast<int32_t*>(order.data_ptr()), stream);
+  });
+  return Py_BuildValue("NN", THPVariable_Wrap(offsets), THPVariable_Wrap(order));
+}
+
+// init_routed(addresses of the entry points)
+PyObject* init_routed(PyObject* const* a, Py_ssize_t n) {
+  count(n, 3);
+  void* p[3];
+  for (int i = 0; i < 3; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  if (PyErr_Occurred()) throw Raised{};
+  g_choose = reinterpret_cast<decltype(g_choose)>(p[0]);
+  g_choose_grad = reinterpret_cast<decltype(g_choose_grad)>(p[1]);
+  g_sort = reinterpret_cast<decltype(g_sort)>(p[2]);
+  Py_RETURN_NONE;
+}
+
 // init(addresses of the four entry points, MxFp4Matrix, GemmError)
 PyObject* init(PyObject* const* a, Py_ssize_t n) {
   count(n, 6);
@@ -310,6 +450,8 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<init>("init"), method<quantize>("quantize"),
                            method<matmul>("matmul"), method<moe>("moe"),
+                           method<init_routed>("init_routed"), method<choose>("choose"),
+                           method<choose_grad>("choose_grad"), method<sort>("sort"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,64 @@
+"""Products by an index per row: the tensor-level calls over ``include/mhr_routed.h``.
+
+    choose_experts(logits, top, ...) -> experts, weights
+    choose_experts_grad(logits, experts, grad_weights, ...) -> grad_logits
+    sort_by_expert(experts, count) -> offsets, order
+
+As in ``mxfp4.py``: argument checks and marshalling only (in the compiled
+``csrc/torch_binding.cpp``), launches on ``stream`` (default: the current torch
+stream) without synchronising, ``GemmError`` for a status other than ``MHR_OK``.
+On a stream other than the current one the caller orders the use of the returned
+tensors itself. All calls can be captured into a graph.
+"""
+from __future__ import annotations
+
+import ctypes
+
+from . import load
+from .mxfp4 import _torch_binding
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
+_GROUP_SCORES = {"max": 0, "top2": 1}
+
+_lib = load()
+_torch_binding.init_routed(*(ctypes.cast(f, ctypes.c_void_p).value
+                             for f in (_lib.gemm_routed_choose, _lib.gemm_routed_choose_grad,
+                                       _lib.gemm_routed_sort)))
+
+
+def choose_experts(logits, top: int, score: str = "softmax", bias=None, groups: int = 1,
+                   group_top: int = 1, group_score: str = "max", renormalize: bool = True,
+                   scale: float = 1.0, stream=None):
+    """The ``top`` experts of each token (T x top int32, best first) and their weights (float32).
+
+    ``logits``: T x E float32, bfloat16 or float16. ``score``: "softmax" over all experts, or
+    "sigmoid". ``bias`` (E float32) is added to the scores for the choice, not for the weights.
+    With ``groups`` > 1, the ``group_top`` groups of neighbouring experts with the best
+    ``group_score`` ("max", or "top2": the sum of the two best) stay in the choice. Ties go to the
+    lowest index. Weights are the chosen scores, divided by their sum with ``renormalize``, times
+    ``scale``. Limits: E <= 512, top <= 16, groups <= 32.
+    """
+    return _torch_binding.choose(logits, top, _SCORES.get(score, -1), bias, groups, group_top,
+                                 _GROUP_SCORES.get(group_score, -1), renormalize, scale, stream)
+
+
+def choose_experts_grad(logits, experts, grad_weights, score: str = "softmax",
+                        renormalize: bool = True, scale: float = 1.0, out=None, stream=None):
+    """The gradient of ``choose_experts``' logits (their type and shape) for one of its weights.
+
+    ``experts``: as chosen (T x top int32); ``grad_weights``: T x top float32. The choice itself
+    has no gradient, and so the bias and the groups have none.
+    """
+    return _torch_binding.choose_grad(logits, experts, grad_weights, _SCORES.get(score, -1),
+                                      renormalize, scale, out, stream)
+
+
+def sort_by_expert(experts, count: int, stream=None):
+    """The (token, slot) pairs one expert after the other.
+
+    ``experts``: int32 of any shape, contiguous. Returns ``offsets`` (count + 1 int32; expert e's
+    pairs are at offsets[e] to offsets[e + 1]) and ``order`` (int32): the pairs' positions in
+    ``experts`` (as a flat array), ascending within an expert; those of entries outside
+    0 .. count-1 come last, from offsets[count] on. ``count`` <= 1024.
+    """
+    return _torch_binding.sort(experts, count, stream)
