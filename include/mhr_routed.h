@@ -83,6 +83,60 @@ int gemm_routed_choose_grad(int dtype, const void* logits, int64_t ld, const int
 int gemm_routed_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* offsets,
                      int32_t* order, void* stream);
 
+/*
+ * Scratch for an operand of 16-bit elements -- `parts` matrices rows x cols,
+ * pitch ld, `stride` elements apart -- of the two products below: 0 where its
+ * address, pitch and stride are multiples of 16 bytes, else the bytes of a copy
+ * that they make of it (-1: none fits the address space).
+ */
+int64_t gemm_routed_scratch_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols,
+                                  int64_t ld, int64_t stride);
+
+/*
+ * The experts' products.  For expert e and each sorted position q, offsets[e]
+ * <= q < offsets[e + 1]:
+ *   out[scatter ? scatter[q] : q] = x[gather ? gather[q] / top : q] W_e,
+ * W_e the K x N matrix at w + e * stride_w, pitch ldw; transposed != 0: W_e^T
+ * of the N x K matrix there (the gradient of x: the forward product's weights
+ * and the gradient of its output; scatter and gather change places).
+ * x: x_rows x K, pitch ldx; out: out_rows x N, pitch ldo; `rows` sorted
+ * positions, which is also x_rows without gather and out_rows without scatter.
+ * dtype, of x and w: MHR_BF16 or MHR_F16; out_dtype: any.  Sums are held in
+ * fp32 on the tensor cores (tcgen05.mma kind::f16) and rounded once.
+ *
+ * gather and scatter (or NULL): `rows` entries each, as gemm_routed_sort gives
+ * them in `order`; `top` divides gather's, so that a (token, slot) pair's row is
+ * its token's.  A row of x outside 0 .. x_rows-1 counts as zeros, one of out
+ * outside 0 .. out_rows-1 is not written; entries of scatter are distinct.
+ * Rows of out of no sorted position, and those at offsets[E] and after, stay as
+ * they were.  Offsets below the one before or past `rows` count as that.
+ * K == 0 writes zeros.  E <= 1024.
+ *
+ * scratch: gemm_routed_scratch_bytes of x (one part) plus that of w (E parts);
+ * the copy of w holds the experts that have rows.
+ */
+int gemm_routed_product(int dtype, const void* x, int64_t x_rows, int64_t ldx,
+                        const int32_t* gather, int64_t top, const void* w, int64_t ldw,
+                        int64_t stride_w, int transposed, const int32_t* offsets, int64_t E,
+                        int out_dtype, void* out, int64_t out_rows, int64_t ldo,
+                        const int32_t* scatter, int64_t rows, int64_t K, int64_t N,
+                        void* scratch, int64_t scratch_bytes, void* stream);
+
+/*
+ * The gradient of the weights of gemm_routed_product: for each expert
+ *   out_e = sum over q, offsets[e] <= q < offsets[e + 1], of
+ *           x[gather ? gather[q] / top : q]^T grad[scatter ? scatter[q] : q],
+ * K x N at out + e * stride_o, pitch ldo; zeros for an expert without rows.
+ * grad: grad_rows x N, pitch ldg, of x's type; the rest, and rows outside x or
+ * grad, as above.  scratch: gemm_routed_scratch_bytes of x plus that of grad.
+ */
+int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, int64_t ldx,
+                            const int32_t* gather, int64_t top, const void* grad,
+                            int64_t grad_rows, int64_t ldg, const int32_t* scatter,
+                            const int32_t* offsets, int64_t E, int out_dtype, void* out,
+                            int64_t ldo, int64_t stride_o, int64_t rows, int64_t K, int64_t N,
+                            void* scratch, int64_t scratch_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

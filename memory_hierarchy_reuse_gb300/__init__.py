@@ -22,8 +22,9 @@ Tensor-level helper: ``matmul(a, b, path, out=None)`` for row-major CUDA
 tensors (the last dimension contiguous; the leading dimension is the row
 stride). 4-bit operands (``include/mhr_mxfp4.h``): ``quantize_mxfp4``,
 ``matmul_mxfp4`` and ``moe_mxfp4``, in ``mxfp4.py``. Products by an index per
-row (``include/mhr_routed.h``): ``choose_experts``, ``choose_experts_grad`` and
-``sort_by_expert``, in ``routed.py``.
+row (``include/mhr_routed.h``): ``choose_experts``, ``choose_experts_grad``,
+``sort_by_expert``, ``matmul_experts`` and ``matmul_experts_grad``, in
+``routed.py``.
 """
 from __future__ import annotations
 
@@ -57,7 +58,8 @@ EXPORTS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_bf16_f32acc", "gemm_f32_3xtf32_n
            "gemm_testing_plan_simt_wide",
            "gemm_mxfp4_scale_bytes", "gemm_mxfp4_quantize", "gemm_mxfp4", "gemm_mxfp4_quantized",
            "gemm_mxfp4_moe",
-           "gemm_routed_choose", "gemm_routed_choose_grad", "gemm_routed_sort")
+           "gemm_routed_choose", "gemm_routed_choose_grad", "gemm_routed_sort",
+           "gemm_routed_scratch_bytes", "gemm_routed_product", "gemm_routed_weight_grad")
 
 _lib = None
 
@@ -115,6 +117,14 @@ def load(path: str | None = None):
     lib.gemm_routed_choose_grad.restype = ci
     lib.gemm_routed_sort.argtypes = [vp, i64, i64, vp, vp, vp]
     lib.gemm_routed_sort.restype = ci
+    lib.gemm_routed_scratch_bytes.argtypes = [vp, i64, i64, i64, i64, i64]
+    lib.gemm_routed_scratch_bytes.restype = i64
+    lib.gemm_routed_product.argtypes = [ci, vp, i64, i64, vp, i64, vp, i64, i64, ci, vp, i64, ci,
+                                        vp, i64, i64, vp, i64, i64, i64, vp, i64, vp]
+    lib.gemm_routed_product.restype = ci
+    lib.gemm_routed_weight_grad.argtypes = [ci, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64,
+                                            ci, vp, i64, i64, i64, i64, i64, vp, i64, vp]
+    lib.gemm_routed_weight_grad.restype = ci
     lib.gemm_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.gemm_testing_set_wait_limit_ns.restype = ctypes.c_uint64
     lib.gemm_testing_set_inject_stall.argtypes = [ctypes.c_int]
@@ -338,7 +348,8 @@ def __getattr__(name):
 
         globals()[name] = getattr(mxfp4, name)
         return globals()[name]
-    if name in ("choose_experts", "choose_experts_grad", "sort_by_expert"):
+    if name in ("choose_experts", "choose_experts_grad", "sort_by_expert", "matmul_experts",
+                "matmul_experts_grad"):
         from . import routed
 
         globals()[name] = getattr(routed, name)

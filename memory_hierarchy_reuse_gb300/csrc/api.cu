@@ -282,7 +282,7 @@ CUresult encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void*
 
 CUresult encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                         const uint64_t (&dims)[3], const uint64_t (&pitch_bytes)[2],
-                        const uint32_t (&box)[3]) {
+                        const uint32_t (&box)[3], CUtensorMapSwizzle swizzle) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return CUDA_ERROR_NOT_FOUND;
   const cuuint64_t d[3] = {dims[0], dims[1], dims[2]};
@@ -290,8 +290,7 @@ CUresult encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void*
   const cuuint32_t b[3] = {box[0], box[1], box[2]};
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, dtype, 3, const_cast<void*>(base), d, strides, b, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+            CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 namespace {

@@ -128,10 +128,11 @@ CUresult encode_tmap_2d(CUtensorMap* map, CUtensorMapDataType dtype, const void*
                         uint64_t inner, uint64_t outer, uint64_t row_pitch_bytes,
                         uint32_t box_inner, uint32_t box_outer, CUtensorMapSwizzle swizzle);
 
-// The same for three dimensions (pitches of the second and third), unswizzled.
+// The same for three dimensions (pitches of the second and third).
 CUresult encode_tmap_3d(CUtensorMap* map, CUtensorMapDataType dtype, const void* base,
                         const uint64_t (&dims)[3], const uint64_t (&pitch_bytes)[2],
-                        const uint32_t (&box)[3]);
+                        const uint32_t (&box)[3],
+                        CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE);
 
 // Name of the main kernel the last tensor-core or SIMT launch used, with its
 // grid (for profiling labels; static storage).  Called right before that

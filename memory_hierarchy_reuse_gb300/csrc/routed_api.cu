@@ -65,6 +65,41 @@ bool router_ok(int64_t T, int64_t E, int64_t top, int score) {
          (score == MHR_SOFTMAX || score == MHR_SIGMOID);
 }
 
+// `parts` matrices, `stride` elements apart, that do not reach into one another.
+bool parts_ok(const void* p, int64_t size, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
+              int64_t stride, ByteRange* r) {
+  int64_t all, span, bytes;
+  if (parts == 1) return plain_ok(p, size, rows, cols, ld, r);
+  ByteRange one;
+  return plain_ok(p, size, rows, cols, ld, &one) && !__builtin_mul_overflow(rows - 1, ld, &span) &&
+         !__builtin_add_overflow(span, cols, &span) && stride >= span &&
+         !__builtin_mul_overflow(stride, size, &bytes) &&
+         !__builtin_mul_overflow(parts, bytes, &all) && byte_range(p, parts, span * size, bytes, r);
+}
+
+// Scratch of `need` bytes (each repack_bytes, -1 if there is no such).
+int scratch_ok(const void* scratch, int64_t have, int64_t need_a, int64_t need_b, ByteRange* r) {
+  int64_t need;
+  if (need_a < 0 || need_b < 0 || __builtin_add_overflow(need_a, need_b, &need))
+    return MHR_ERR_CUDA;
+  if (need == 0) return MHR_OK;
+  return scratch && aligned(scratch, 16) && have >= need && byte_range(scratch, 1, need, need, r)
+             ? MHR_OK
+             : MHR_ERR_INVALID_ARG;
+}
+
+// What both products ask of the types, the sizes and the indices.
+bool indexed_ok(int dtype, int out_dtype, int64_t x_rows, const int32_t* gather, int64_t top,
+                int64_t other_rows, const int32_t* scatter, const int32_t* offsets, int64_t E,
+                int64_t rows, int64_t K, int64_t N, ByteRange (&r)[3]) {
+  return (dtype == MHR_BF16 || dtype == MHR_F16) && dtype_ok(out_dtype) && dim_ok(x_rows) &&
+         dim_ok(other_rows) && dim_ok(rows) && dim_ok(K) && dim_ok(N) && E >= 1 &&
+         E <= MAX_PARTS && top >= 1 && top <= kMaxDim && (gather || x_rows == rows) &&
+         (scatter || other_rows == rows) && array_ok(offsets, 4, E + 1, &r[0]) &&
+         (!gather || rows == 0 || array_ok(gather, 4, rows, &r[1])) &&
+         (!scatter || rows == 0 || array_ok(scatter, 4, rows, &r[2]));
+}
+
 }  // namespace
 }  // namespace routed
 }  // namespace mhr
@@ -120,5 +155,71 @@ MHR_API int gemm_routed_sort(const int32_t* experts, int64_t n, int64_t E, int32
     return MHR_ERR_INVALID_ARG;
   return launched([&](const DeviceCtl&) {
     return launch_sort(experts, n, E, offsets, order, static_cast<cudaStream_t>(stream));
+  });
+}
+
+MHR_API int64_t gemm_routed_scratch_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols,
+                                          int64_t ld, int64_t stride) {
+  if (parts < 1 || parts > MAX_PARTS || !dim_ok(rows) || !dim_ok(cols)) return -1;
+  return repack_bytes(p, parts, rows, cols, ld, stride);
+}
+
+MHR_API int gemm_routed_product(int dtype, const void* x, int64_t x_rows, int64_t ldx,
+                                const int32_t* gather, int64_t top, const void* w, int64_t ldw,
+                                int64_t stride_w, int transposed, const int32_t* offsets,
+                                int64_t E, int out_dtype, void* out, int64_t out_rows,
+                                int64_t ldo, const int32_t* scatter, int64_t rows, int64_t K,
+                                int64_t N, void* scratch, int64_t scratch_bytes, void* stream) {
+  ByteRange index[3], rx, rw, ro, rs;
+  if (!indexed_ok(dtype, out_dtype, x_rows, gather, top, out_rows, scatter, offsets, E, rows, K, N,
+                  index))
+    return MHR_ERR_INVALID_ARG;
+  if (rows == 0 || N == 0 || out_rows == 0) return MHR_OK;
+  if (!plain_ok(out, size_of(out_dtype), out_rows, N, ldo, &ro)) return MHR_ERR_INVALID_ARG;
+  if (K > 0 && x_rows > 0) {
+    const int64_t wr = transposed ? N : K, wc = transposed ? K : N;
+    if (!plain_ok(x, 2, x_rows, K, ldx, &rx) || !parts_ok(w, 2, E, wr, wc, ldw, stride_w, &rw))
+      return MHR_ERR_INVALID_ARG;
+    if (const int rc = scratch_ok(scratch, scratch_bytes, repack_bytes(x, 1, x_rows, K, ldx, 0),
+                                  repack_bytes(w, E, wr, wc, ldw, stride_w), &rs);
+        rc != MHR_OK)
+      return rc;
+  }
+  if (!apart({ro, rs}, {index[0], index[1], index[2], rx, rw})) return MHR_ERR_INVALID_ARG;
+  return launched([&](const DeviceCtl& ctl) {
+    return launch_product({transposed ? ProductKind::transposed : ProductKind::product, dtype, x,
+                           x_rows, ldx, gather, top, w, ldw, stride_w, offsets, E, out_dtype, out,
+                           out_rows, ldo, 0, scatter, rows, K, N},
+                          scratch, ctl, static_cast<cudaStream_t>(stream));
+  });
+}
+
+MHR_API int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, int64_t ldx,
+                                    const int32_t* gather, int64_t top, const void* grad,
+                                    int64_t grad_rows, int64_t ldg, const int32_t* scatter,
+                                    const int32_t* offsets, int64_t E, int out_dtype, void* out,
+                                    int64_t ldo, int64_t stride_o, int64_t rows, int64_t K,
+                                    int64_t N, void* scratch, int64_t scratch_bytes,
+                                    void* stream) {
+  ByteRange index[3], rx, rg, ro, rs;
+  if (!indexed_ok(dtype, out_dtype, x_rows, gather, top, grad_rows, scatter, offsets, E, rows, K,
+                  N, index))
+    return MHR_ERR_INVALID_ARG;
+  if (K == 0 || N == 0) return MHR_OK;
+  if (!parts_ok(out, size_of(out_dtype), E, K, N, ldo, stride_o, &ro)) return MHR_ERR_INVALID_ARG;
+  if (rows > 0 && x_rows > 0 && grad_rows > 0) {
+    if (!plain_ok(x, 2, x_rows, K, ldx, &rx) || !plain_ok(grad, 2, grad_rows, N, ldg, &rg))
+      return MHR_ERR_INVALID_ARG;
+    if (const int rc = scratch_ok(scratch, scratch_bytes, repack_bytes(x, 1, x_rows, K, ldx, 0),
+                                  repack_bytes(grad, 1, grad_rows, N, ldg, 0), &rs);
+        rc != MHR_OK)
+      return rc;
+  }
+  if (!apart({ro, rs}, {index[0], index[1], index[2], rx, rg})) return MHR_ERR_INVALID_ARG;
+  return launched([&](const DeviceCtl& ctl) {
+    return launch_product({ProductKind::gradient, dtype, x, x_rows, ldx, gather, top, grad, ldg, 0,
+                           offsets, E, out_dtype, out, grad_rows, ldo, stride_o, scatter, rows, K,
+                           N},
+                          scratch, ctl, static_cast<cudaStream_t>(stream));
   });
 }

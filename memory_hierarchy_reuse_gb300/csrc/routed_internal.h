@@ -46,6 +46,37 @@ struct ChooseGradArgs {
 };
 cudaError_t launch_choose_grad(const ChooseGradArgs& a, cudaStream_t s);
 
+// Bytes of scratch that `parts` matrices (rows x cols, 16-bit elements, pitch ld,
+// `stride` elements apart) take to be read by TMA: 0 for those that it reads as they
+// are; -1 where they leave the address space.
+int64_t repack_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
+                     int64_t stride);
+
+// One gemm_routed_product (product, transposed) or gemm_routed_weight_grad
+// (gradient).  K: columns of x; N: the output's columns.  `w` is the weights, or the
+// gradient rows (out_rows x N) that `scatter` picks from.
+enum class ProductKind { product, transposed, gradient };
+struct ProductArgs {
+  ProductKind kind;
+  int dtype;
+  const void* x;
+  int64_t x_rows, ldx;
+  const int32_t* gather;
+  int64_t top;
+  const void* w;
+  int64_t ldw, stride_w;
+  const int32_t* offsets;
+  int64_t E;
+  int out_dtype;
+  void* out;
+  int64_t out_rows, ldo, stride_o;
+  const int32_t* scatter;
+  int64_t rows, K, N;
+};
+// scratch: repack_bytes of x, then of w.
+cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl& ctl,
+                           cudaStream_t s);
+
 cudaError_t launch_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* offsets,
                         int32_t* order, cudaStream_t s);
 

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -28,6 +29,9 @@ decltype(&gemm_mxfp4_moe) g_moe;
 decltype(&gemm_routed_choose) g_choose;
 decltype(&gemm_routed_choose_grad) g_choose_grad;
 decltype(&gemm_routed_sort) g_sort;
+decltype(&gemm_routed_scratch_bytes) g_scratch_bytes;
+decltype(&gemm_routed_product) g_routed_product;
+decltype(&gemm_routed_weight_grad) g_weight_grad;
 PyObject* g_matrix;  // MxFp4Matrix
 PyObject* g_error;   // GemmError
 
@@ -413,15 +417,170 @@ PyObject* sort(PyObject* const* v, Py_ssize_t n) {
   return Py_BuildValue("NN", THPVariable_Wrap(offsets), THPVariable_Wrap(order));
 }
 
+// An int32 index per sorted position, or none; *rows is their number once one says it.
+const int32_t* index_of(PyObject* o, const char* name, int device, int64_t* rows) {
+  if (o == Py_None) return nullptr;
+  const at::Tensor& t = array(o, at::kInt, name);
+  if (t.device() != at::Device(at::kCUDA, static_cast<at::DeviceIndex>(device)))
+    raise(PyExc_ValueError, "%soperands must be on one device");
+  if (*rows >= 0 && t.numel() != *rows)
+    raise(PyExc_ValueError, "%s: as many entries as sorted rows", name);
+  *rows = t.numel();
+  return static_cast<const int32_t*>(t.data_ptr());
+}
+
+// Matrices of one shape: the sizes and strides of a 3-D tensor.
+struct Parts {
+  int64_t parts, rows, cols, ld, stride;
+};
+Parts parts(const at::Tensor& t, const char* name) {
+  if (t.dim() != 3) raise(PyExc_ValueError, "%s must be 3-D", name);
+  Parts p{t.size(0), t.size(1), t.size(2), 0, 0};
+  const bool some = p.parts > 0 && p.rows > 0 && p.cols > 0;
+  if (some && p.cols > 1 && t.stride(2) != 1)
+    raise(PyExc_ValueError, "%s must be row-major (last dimension contiguous)", name);
+  p.ld = some && p.rows > 1 ? t.stride(1) : p.cols;
+  p.stride = some && p.parts > 1 ? t.stride(0) : p.rows * p.ld;
+  if (some && (p.ld < p.cols || p.stride < (p.rows - 1) * p.ld + p.cols))
+    raise(PyExc_ValueError, "%s must be row-major (rows or parts overlap)", name);
+  return p;
+}
+
+// 16-bit operands of one type.
+int half_type(const at::Tensor& x, const at::Tensor& w, const char* names) {
+  const at::ScalarType t = x.scalar_type();
+  if ((t != at::kBFloat16 && t != at::kHalf) || w.scalar_type() != t)
+    raise(PyExc_TypeError, "%s must both be bfloat16, or both float16", names);
+  return t == at::kBFloat16 ? MHR_BF16 : MHR_F16;
+}
+at::ScalarType type_number(PyObject* o, at::ScalarType same) {
+  if (o == Py_None) return same;
+  const long type = PyLong_AsLong(o);
+  if (type < MHR_F32 || type > MHR_F16) {
+    PyErr_Clear();
+    raise(PyExc_TypeError, "%sout_dtype must be float32, bfloat16 or float16");
+  }
+  return type == MHR_F32 ? at::kFloat : type == MHR_BF16 ? at::kBFloat16 : at::kHalf;
+}
+
+// Scratch of a call on `stream`, kept until the stream has passed it.
+at::Tensor scratch_for(int64_t bytes, int device, void* stream) {
+  at::Tensor t = empty({bytes}, at::kByte, device);
+  if (bytes > 0 && stream != static_cast<void*>(c10::cuda::getCurrentCUDAStream(device).stream()))
+    c10::cuda::CUDACachingAllocator::recordStream(
+        t.storage().data_ptr(), c10::cuda::getStreamFromExternal(
+                                    static_cast<cudaStream_t>(stream),
+                                    static_cast<c10::DeviceIndex>(device)));
+  return t;
+}
+
+// experts(x, w, offsets, gather, scatter, top, transposed, out or None, out_dtype or None,
+//         stream) -> out
+PyObject* experts(PyObject* const* v, Py_ssize_t n) {
+  count(n, 10);
+  const at::Tensor &x = tensor(v[0], "x"), &w = tensor(v[1], "w");
+  const int type = half_type(x, w, "x and w");
+  const Plain px = plain(x, "x");
+  const Parts pw = parts(w, "w");
+  const at::Tensor& offsets = array(v[2], at::kInt, "offsets");
+  const int device = device_of({&x, &w, &offsets});
+  int64_t rows = -1;
+  const int32_t* gather = index_of(v[3], "gather", device, &rows);
+  const int32_t* scatter = index_of(v[4], "scatter", device, &rows);
+  if (rows < 0) rows = px.rows;
+  const int64_t top = integer(v[5]);
+  if (top < 1) raise(PyExc_ValueError, "%stop must be at least 1");
+  const bool transposed = truth(v[6]);
+  const int64_t K = transposed ? pw.cols : pw.rows, N = transposed ? pw.rows : pw.cols;
+  if (px.cols != K) raise(PyExc_ValueError, "%sinner dimensions of x and w differ");
+  if (offsets.dim() != 1 || offsets.numel() != pw.parts + 1)
+    raise(PyExc_ValueError, "%soffsets must be of experts + 1 values");
+  if (!gather && px.rows != rows) raise(PyExc_ValueError, "%sx must have as many rows as scatter");
+  at::Tensor out;
+  if (v[7] == Py_None) {
+    out = empty({rows, N}, type_number(v[8], x.scalar_type()), device);
+  } else {
+    out = tensor(v[7], "out");
+    device_of({&x, &out});
+  }
+  const int out_type = dtype_of(out, "out");
+  const Plain po = plain(out, "out");
+  if (po.cols != N || (!scatter && po.rows != rows))
+    raise(PyExc_TypeError, "%sout must be of shape (rows, N)");
+  void* stream = stream_of(v[9], device);
+  const int64_t need_x = g_scratch_bytes(x.data_ptr(), 1, px.rows, px.cols, px.ld, 0);
+  const int64_t need_w =
+      pw.parts ? g_scratch_bytes(w.data_ptr(), pw.parts, pw.rows, pw.cols, pw.ld, pw.stride) : 0;
+  const int64_t need = (need_x > 0 ? need_x : 0) + (need_w > 0 ? need_w : 0);
+  at::Tensor scratch;
+  if (need) scratch = scratch_for(need, device, stream);
+  run("gemm_routed_product", device, [&] {
+    return g_routed_product(type, x.data_ptr(), px.rows, px.ld, gather, top, w.data_ptr(), pw.ld,
+                            pw.stride, transposed, static_cast<const int32_t*>(offsets.data_ptr()),
+                            pw.parts, out_type, out.data_ptr(), po.rows, po.ld, scatter, rows, K,
+                            N, need ? scratch.data_ptr() : nullptr, need, stream);
+  });
+  return THPVariable_Wrap(out);
+}
+
+// experts_grad(x, grad, offsets, gather, scatter, top, out or None, out_dtype or None, stream)
+//     -> out
+PyObject* experts_grad(PyObject* const* v, Py_ssize_t n) {
+  count(n, 9);
+  const at::Tensor &x = tensor(v[0], "x"), &grad = tensor(v[1], "grad");
+  const int type = half_type(x, grad, "x and grad");
+  const Plain px = plain(x, "x"), pg = plain(grad, "grad");
+  const at::Tensor& offsets = array(v[2], at::kInt, "offsets");
+  const int device = device_of({&x, &grad, &offsets});
+  int64_t rows = -1;
+  const int32_t* gather = index_of(v[3], "gather", device, &rows);
+  const int32_t* scatter = index_of(v[4], "scatter", device, &rows);
+  if (rows < 0) rows = px.rows;
+  const int64_t top = integer(v[5]);
+  if (top < 1) raise(PyExc_ValueError, "%stop must be at least 1");
+  if ((!gather && px.rows != rows) || (!scatter && pg.rows != rows))
+    raise(PyExc_ValueError, "%sx and grad must have as many rows as there are sorted ones");
+  const int64_t E = offsets.numel() - 1;
+  if (offsets.dim() != 1 || E < 1)
+    raise(PyExc_ValueError, "%soffsets must be of experts + 1 values");
+  at::Tensor out;
+  if (v[6] == Py_None) {
+    out = empty({E, px.cols, pg.cols}, type_number(v[7], x.scalar_type()), device);
+  } else {
+    out = tensor(v[6], "out");
+    device_of({&x, &out});
+  }
+  const int out_type = dtype_of(out, "out");
+  const Parts po = parts(out, "out");
+  if (po.parts != E || po.rows != px.cols || po.cols != pg.cols)
+    raise(PyExc_TypeError, "%sout must be of shape (experts, K, N)");
+  void* stream = stream_of(v[8], device);
+  const int64_t need_x = g_scratch_bytes(x.data_ptr(), 1, px.rows, px.cols, px.ld, 0);
+  const int64_t need_g = g_scratch_bytes(grad.data_ptr(), 1, pg.rows, pg.cols, pg.ld, 0);
+  const int64_t need = (need_x > 0 ? need_x : 0) + (need_g > 0 ? need_g : 0);
+  at::Tensor scratch;
+  if (need) scratch = scratch_for(need, device, stream);
+  run("gemm_routed_weight_grad", device, [&] {
+    return g_weight_grad(type, x.data_ptr(), px.rows, px.ld, gather, top, grad.data_ptr(), pg.rows,
+                         pg.ld, scatter, static_cast<const int32_t*>(offsets.data_ptr()), E,
+                         out_type, out.data_ptr(), po.ld, po.stride, rows, px.cols, pg.cols,
+                         need ? scratch.data_ptr() : nullptr, need, stream);
+  });
+  return THPVariable_Wrap(out);
+}
+
 // init_routed(addresses of the entry points)
 PyObject* init_routed(PyObject* const* a, Py_ssize_t n) {
-  count(n, 3);
-  void* p[3];
-  for (int i = 0; i < 3; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  count(n, 6);
+  void* p[6];
+  for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) throw Raised{};
   g_choose = reinterpret_cast<decltype(g_choose)>(p[0]);
   g_choose_grad = reinterpret_cast<decltype(g_choose_grad)>(p[1]);
   g_sort = reinterpret_cast<decltype(g_sort)>(p[2]);
+  g_scratch_bytes = reinterpret_cast<decltype(g_scratch_bytes)>(p[3]);
+  g_routed_product = reinterpret_cast<decltype(g_routed_product)>(p[4]);
+  g_weight_grad = reinterpret_cast<decltype(g_weight_grad)>(p[5]);
   Py_RETURN_NONE;
 }
 
@@ -452,6 +611,7 @@ PyMethodDef g_methods[] = {method<init>("init"), method<quantize>("quantize"),
                            method<matmul>("matmul"), method<moe>("moe"),
                            method<init_routed>("init_routed"), method<choose>("choose"),
                            method<choose_grad>("choose_grad"), method<sort>("sort"),
+                           method<experts>("experts"), method<experts_grad>("experts_grad"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

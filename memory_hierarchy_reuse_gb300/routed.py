@@ -3,6 +3,8 @@
     choose_experts(logits, top, ...) -> experts, weights
     choose_experts_grad(logits, experts, grad_weights, ...) -> grad_logits
     sort_by_expert(experts, count) -> offsets, order
+    matmul_experts(x, w, offsets, ...) -> out
+    matmul_experts_grad(x, grad, offsets, ...) -> gradient of w
 
 As in ``mxfp4.py``: argument checks and marshalling only (in the compiled
 ``csrc/torch_binding.cpp``), launches on ``stream`` (default: the current torch
@@ -15,7 +17,7 @@ from __future__ import annotations
 import ctypes
 
 from . import load
-from .mxfp4 import _torch_binding
+from .mxfp4 import DTYPES, _torch_binding
 
 _SCORES = {"softmax": 0, "sigmoid": 1}
 _GROUP_SCORES = {"max": 0, "top2": 1}
@@ -23,7 +25,8 @@ _GROUP_SCORES = {"max": 0, "top2": 1}
 _lib = load()
 _torch_binding.init_routed(*(ctypes.cast(f, ctypes.c_void_p).value
                              for f in (_lib.gemm_routed_choose, _lib.gemm_routed_choose_grad,
-                                       _lib.gemm_routed_sort)))
+                                       _lib.gemm_routed_sort, _lib.gemm_routed_scratch_bytes,
+                                       _lib.gemm_routed_product, _lib.gemm_routed_weight_grad)))
 
 
 def choose_experts(logits, top: int, score: str = "softmax", bias=None, groups: int = 1,
@@ -62,3 +65,35 @@ def sort_by_expert(experts, count: int, stream=None):
     0 .. count-1 come last, from offsets[count] on. ``count`` <= 1024.
     """
     return _torch_binding.sort(experts, count, stream)
+
+
+def _out_dtype(dtype):
+    return None if dtype is None else DTYPES.get(dtype, -1)
+
+
+def matmul_experts(x, w, offsets, gather=None, scatter=None, top: int = 1,
+                   transposed: bool = False, out=None, out_dtype=None, stream=None):
+    """out[q] = x[q] @ w[e] for the sorted rows q of each expert, offsets[e] <= q < offsets[e + 1].
+
+    ``x``: rows x K and ``w``: experts x K x N (experts x N x K with ``transposed``, whose product
+    is with ``w[e].T``: the gradient of x), both bfloat16 or both float16. ``gather`` and
+    ``scatter`` (int32, one entry a sorted row: ``sort_by_expert``'s ``order``): row q is
+    ``x[gather[q] // top]``, and is written to ``out[scatter[q]]`` -- with ``top`` the router's,
+    ``x`` is the tokens, and ``out`` in (token, slot) order. ``out`` (of ``out_dtype``, x's when
+    omitted; or given, float32, bfloat16 or float16) is returned. Its rows that no expert has stay
+    as they were: undefined when it is allocated here.
+    """
+    return _torch_binding.experts(x, w, offsets, gather, scatter, top, transposed, out,
+                                  _out_dtype(out_dtype), stream)
+
+
+def matmul_experts_grad(x, grad, offsets, gather=None, scatter=None, top: int = 1, out=None,
+                        out_dtype=None, stream=None):
+    """The gradient of ``matmul_experts``' weights (experts x K x N): the sum of
+    ``x[row].T @ grad[row]`` over each expert's sorted rows, zeros for one without.
+
+    ``grad``: the gradient of the product's output, of x's type, rows x N; the indices as there
+    (``grad``'s rows are ``scatter``'s). ``out_dtype``: x's when omitted.
+    """
+    return _torch_binding.experts_grad(x, grad, offsets, gather, scatter, top, out,
+                                       _out_dtype(out_dtype), stream)

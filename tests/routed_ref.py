@@ -83,3 +83,27 @@ def sort(experts, count):
     flat = np.where((experts >= 0) & (experts < count), experts, count).reshape(-1)
     offsets = np.searchsorted(np.sort(flat), np.arange(count + 1))
     return offsets.astype(np.int32), np.argsort(flat, kind="stable").astype(np.int32)
+
+
+def product(x, w, offsets, rows, gather=None, scatter=None, top=1, transposed=False, out=None):
+    """`out` (float64, left as it is where nothing is written) for float64 x and w."""
+    for e in range(w.shape[0]):
+        for q in range(offsets[e], offsets[e + 1]):
+            r = q if gather is None else (gather[q] // top if gather[q] >= 0 else -1)
+            to = q if scatter is None else scatter[q]
+            if 0 <= to < out.shape[0]:
+                row = x[r] if 0 <= r < x.shape[0] else np.zeros(x.shape[1])
+                out[to] = row @ (w[e].T if transposed else w[e])
+    return out
+
+
+def weight_grad(x, g, offsets, gather=None, scatter=None, top=1):
+    E = len(offsets) - 1
+    out = np.zeros((E, x.shape[1], g.shape[1]))
+    for e in range(E):
+        for q in range(offsets[e], offsets[e + 1]):
+            r = q if gather is None else (gather[q] // top if gather[q] >= 0 else -1)
+            to = q if scatter is None else scatter[q]
+            if 0 <= r < x.shape[0] and 0 <= to < g.shape[0]:
+                out[e] += np.outer(x[r], g[to])
+    return out
