@@ -137,6 +137,31 @@ int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, int64_t ld
                             int64_t ldo, int64_t stride_o, int64_t rows, int64_t K, int64_t N,
                             void* scratch, int64_t scratch_bytes, void* stream);
 
+/*
+ * Low-rank adapters of many requests, added to a shared projection's result:
+ *   out_t = y_t + scales[a] (x_t down_a^T) up_a,  a = which[t], t < T.
+ * x: T x K, pitch ldx; down_a: rank x K at down + a * stride_d, pitch ldd; up_a:
+ * rank x N at up + a * stride_u, pitch ldu, all of type dtype (MHR_BF16 or
+ * MHR_F16); scales: L floats, or NULL for 1; y, out: T x N, of type out_dtype
+ * (any).  out may be y itself (the same address and pitch).  A row whose which
+ * lies outside 0 .. L-1 has no adapter: out_t = y_t.  Both sums are held in fp32,
+ * and so is x_t down_a^T between them; out is rounded once.
+ * Limits: L <= 1024, rank <= 128.
+ *
+ * scratch: gemm_routed_adapters_scratch bytes (0 for few rows; -1 for arguments
+ * that the call refuses).
+ */
+int64_t gemm_routed_adapters_scratch(int dtype, const void* x, int64_t ldx, const void* down,
+                                     int64_t ldd, int64_t stride_d, const void* up, int64_t ldu,
+                                     int64_t stride_u, int64_t L, int64_t rank, int out_dtype,
+                                     int64_t T, int64_t K, int64_t N);
+int gemm_routed_adapters(int dtype, const void* x, int64_t ldx, const void* down, int64_t ldd,
+                         int64_t stride_d, const void* up, int64_t ldu, int64_t stride_u,
+                         const int32_t* which, const float* scales, int64_t L, int64_t rank,
+                         int out_dtype, const void* y, int64_t ldy, void* out, int64_t ldo,
+                         int64_t T, int64_t K, int64_t N, void* scratch, int64_t scratch_bytes,
+                         void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,8 +23,8 @@ tensors (the last dimension contiguous; the leading dimension is the row
 stride). 4-bit operands (``include/mhr_mxfp4.h``): ``quantize_mxfp4``,
 ``matmul_mxfp4`` and ``moe_mxfp4``, in ``mxfp4.py``. Products by an index per
 row (``include/mhr_routed.h``): ``choose_experts``, ``choose_experts_grad``,
-``sort_by_expert``, ``matmul_experts`` and ``matmul_experts_grad``, in
-``routed.py``.
+``sort_by_expert``, ``matmul_experts``, ``matmul_experts_grad`` and
+``add_adapters``, in ``routed.py``.
 """
 from __future__ import annotations
 
@@ -59,7 +59,8 @@ EXPORTS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_bf16_f32acc", "gemm_f32_3xtf32_n
            "gemm_mxfp4_scale_bytes", "gemm_mxfp4_quantize", "gemm_mxfp4", "gemm_mxfp4_quantized",
            "gemm_mxfp4_moe",
            "gemm_routed_choose", "gemm_routed_choose_grad", "gemm_routed_sort",
-           "gemm_routed_scratch_bytes", "gemm_routed_product", "gemm_routed_weight_grad")
+           "gemm_routed_scratch_bytes", "gemm_routed_product", "gemm_routed_weight_grad",
+           "gemm_routed_adapters_scratch", "gemm_routed_adapters")
 
 _lib = None
 
@@ -125,6 +126,12 @@ def load(path: str | None = None):
     lib.gemm_routed_weight_grad.argtypes = [ci, vp, i64, i64, vp, i64, vp, i64, i64, vp, vp, i64,
                                             ci, vp, i64, i64, i64, i64, i64, vp, i64, vp]
     lib.gemm_routed_weight_grad.restype = ci
+    lib.gemm_routed_adapters_scratch.argtypes = [ci, vp, i64, vp, i64, i64, vp, i64, i64, i64, i64,
+                                                 ci, i64, i64, i64]
+    lib.gemm_routed_adapters_scratch.restype = i64
+    lib.gemm_routed_adapters.argtypes = [ci, vp, i64, vp, i64, i64, vp, i64, i64, vp, vp, i64, i64,
+                                         ci, vp, i64, vp, i64, i64, i64, i64, vp, i64, vp]
+    lib.gemm_routed_adapters.restype = ci
     lib.gemm_testing_set_wait_limit_ns.argtypes = [ctypes.c_uint64]
     lib.gemm_testing_set_wait_limit_ns.restype = ctypes.c_uint64
     lib.gemm_testing_set_inject_stall.argtypes = [ctypes.c_int]
@@ -349,7 +356,7 @@ def __getattr__(name):
         globals()[name] = getattr(mxfp4, name)
         return globals()[name]
     if name in ("choose_experts", "choose_experts_grad", "sort_by_expert", "matmul_experts",
-                "matmul_experts_grad"):
+                "matmul_experts_grad", "add_adapters"):
         from . import routed
 
         globals()[name] = getattr(routed, name)

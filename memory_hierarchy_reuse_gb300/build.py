@@ -25,7 +25,7 @@ LIB = os.path.join(PKG, "libmhr_gemm.so")
 SOURCES = ["api.cu", "simt_f32.cu", "tc_gemm.cu", "tc_gemm_1cta.cu", "tc_gemm_pair.cu",
            "tc_prepass.cu", "noalloc.cu", "ladder.cu", "mxfp4_api.cu", "mxfp4_quantize.cu",
            "mxfp4_narrow.cu", "mxfp4_pair.cu", "mxfp4_moe.cu", "routed_api.cu", "routed_choose.cu",
-           "routed_sort.cu", "routed_product.cu"]
+           "routed_sort.cu", "routed_product.cu", "routed_adapters.cu"]
 BINDING = os.path.join(PKG, "_torch_binding.so")
 BINDING_SOURCE = os.path.join(CSRC, "torch_binding.cpp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -223,3 +223,51 @@ MHR_API int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, in
                           scratch, ctl, static_cast<cudaStream_t>(stream));
   });
 }
+
+namespace {
+bool adapters_ok(int dtype, int out_dtype, int64_t L, int64_t rank, int64_t T, int64_t K,
+                 int64_t N) {
+  return (dtype == MHR_BF16 || dtype == MHR_F16) && dtype_ok(out_dtype) && L >= 1 &&
+         L <= MAX_PARTS && rank >= 1 && rank <= MAX_RANK && dim_ok(T) && T <= kMaxDim / 8 &&
+         dim_ok(K) && dim_ok(N);
+}
+}  // namespace
+
+MHR_API int64_t gemm_routed_adapters_scratch(int dtype, const void* x, int64_t ldx,
+                                             const void* down, int64_t ldd, int64_t stride_d,
+                                             const void* up, int64_t ldu, int64_t stride_u,
+                                             int64_t L, int64_t rank, int out_dtype, int64_t T,
+                                             int64_t K, int64_t N) {
+  if (!adapters_ok(dtype, out_dtype, L, rank, T, K, N)) return -1;
+  if (T == 0 || N == 0) return 0;
+  return adapters_scratch({dtype, x, ldx, down, ldd, stride_d, up, ldu, stride_u, nullptr, nullptr,
+                           L, rank, out_dtype, nullptr, 0, nullptr, 0, T, K, N});
+}
+
+MHR_API int gemm_routed_adapters(int dtype, const void* x, int64_t ldx, const void* down,
+                                 int64_t ldd, int64_t stride_d, const void* up, int64_t ldu,
+                                 int64_t stride_u, const int32_t* which, const float* scales,
+                                 int64_t L, int64_t rank, int out_dtype, const void* y,
+                                 int64_t ldy, void* out, int64_t ldo, int64_t T, int64_t K,
+                                 int64_t N, void* scratch, int64_t scratch_bytes, void* stream) {
+  if (!adapters_ok(dtype, out_dtype, L, rank, T, K, N)) return MHR_ERR_INVALID_ARG;
+  if (T == 0 || N == 0) return MHR_OK;
+  ByteRange rx, rd, ru, rw, rc, ry, ro, rs;
+  const int64_t size = size_of(out_dtype);
+  if (!plain_ok(y, size, T, N, ldy, &ry) || !plain_ok(out, size, T, N, ldo, &ro) ||
+      !array_ok(which, 4, T, &rw) || (scales && !array_ok(scales, 4, L, &rc)) ||
+      (K > 0 && (!plain_ok(x, 2, T, K, ldx, &rx) ||
+                 !parts_ok(down, 2, L, rank, K, ldd, stride_d, &rd))) ||
+      !parts_ok(up, 2, L, rank, N, ldu, stride_u, &ru))
+    return MHR_ERR_INVALID_ARG;
+  const AdapterArgs a{dtype, x, ldx, down, ldd, stride_d, up, ldu, stride_u, which, scales, L,
+                      rank, out_dtype, y, ldy, out, ldo, T, K, N};
+  if (const int rc2 = scratch_ok(scratch, scratch_bytes, adapters_scratch(a), 0, &rs);
+      rc2 != MHR_OK)
+    return rc2;
+  if (out == y && (ldo == ldy || T == 1)) ry = ByteRange{};  // in place
+  if (!apart({ro, rs}, {rx, rd, ru, rw, rc, ry})) return MHR_ERR_INVALID_ARG;
+  return launched([&](const DeviceCtl& ctl) {
+    return launch_adapters(a, scratch, ctl, static_cast<cudaStream_t>(stream));
+  });
+}

@@ -14,6 +14,7 @@ namespace routed {
 
 constexpr int64_t MAX_EXPERTS = 512, MAX_TOP = 16, MAX_GROUPS = 32;  // of a router
 constexpr int64_t MAX_PARTS = 1024;                                 // of a sort, and its products
+constexpr int64_t MAX_RANK = 128;                                   // of an adapter
 
 struct ChooseArgs {
   int dtype;
@@ -76,6 +77,29 @@ struct ProductArgs {
 // scratch: repack_bytes of x, then of w.
 cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl& ctl,
                            cudaStream_t s);
+
+// One gemm_routed_adapters.
+struct AdapterArgs {
+  int dtype;
+  const void* x;
+  int64_t ldx;
+  const void* down;
+  int64_t ldd, stride_d;
+  const void* up;
+  int64_t ldu, stride_u;
+  const int32_t* which;
+  const float* scales;
+  int64_t L, rank;
+  int out_dtype;
+  const void* y;
+  int64_t ldy;
+  void* out;
+  int64_t ldo;
+  int64_t T, K, N;
+};
+int64_t adapters_scratch(const AdapterArgs& a);
+cudaError_t launch_adapters(const AdapterArgs& a, void* scratch, const DeviceCtl& ctl,
+                            cudaStream_t s);
 
 cudaError_t launch_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* offsets,
                         int32_t* order, cudaStream_t s);

@@ -32,6 +32,8 @@ decltype(&gemm_routed_sort) g_sort;
 decltype(&gemm_routed_scratch_bytes) g_scratch_bytes;
 decltype(&gemm_routed_product) g_routed_product;
 decltype(&gemm_routed_weight_grad) g_weight_grad;
+decltype(&gemm_routed_adapters_scratch) g_adapters_scratch;
+decltype(&gemm_routed_adapters) g_adapters;
 PyObject* g_matrix;  // MxFp4Matrix
 PyObject* g_error;   // GemmError
 
@@ -569,11 +571,64 @@ PyObject* experts_grad(PyObject* const* v, Py_ssize_t n) {
   return THPVariable_Wrap(out);
 }
 
+// adapters(y, x, down, up, which, scales or None, out or None, stream) -> out
+PyObject* adapters(PyObject* const* v, Py_ssize_t n) {
+  count(n, 8);
+  const at::Tensor &y = tensor(v[0], "y"), &x = tensor(v[1], "x");
+  const at::Tensor &down = tensor(v[2], "down"), &up = tensor(v[3], "up");
+  const int out_type = dtype_of(y, "y");
+  const int type = half_type(x, down, "x and the adapters");
+  half_type(x, up, "x and the adapters");
+  const Plain py = plain(y, "y"), px = plain(x, "x");
+  const Parts pd = parts(down, "down"), pu = parts(up, "up");
+  if (px.rows != py.rows || pd.cols != px.cols || pu.cols != py.cols || pu.parts != pd.parts ||
+      pu.rows != pd.rows)
+    raise(PyExc_ValueError,
+          "%ssizes differ: y is T x N, x T x K, down adapters x rank x K, up adapters x rank x N");
+  const at::Tensor& which = array(v[4], at::kInt, "which");
+  if (which.dim() != 1 || which.numel() != py.rows)
+    raise(PyExc_ValueError, "%swhich must be of T values");
+  const int device = device_of({&y, &x, &down, &up, &which});
+  const float* scales = nullptr;
+  if (v[5] != Py_None) {
+    const at::Tensor& s = array(v[5], at::kFloat, "scales");
+    if (s.dim() != 1 || s.numel() != pd.parts)
+      raise(PyExc_ValueError, "%sscales must be of one value an adapter");
+    device_of({&y, &s});
+    scales = static_cast<const float*>(s.data_ptr());
+  }
+  at::Tensor out;
+  if (v[6] == Py_None) {
+    out = empty({py.rows, py.cols}, y.scalar_type(), device);
+  } else {
+    out = tensor(v[6], "out");
+    device_of({&y, &out});
+  }
+  const Plain po = plain(out, "out");
+  if (out.scalar_type() != y.scalar_type() || po.rows != py.rows || po.cols != py.cols)
+    raise(PyExc_TypeError, "%sout must be of y's type and shape");
+  void* stream = stream_of(v[7], device);
+  const int64_t bytes =
+      g_adapters_scratch(type, x.data_ptr(), px.ld, down.data_ptr(), pd.ld, pd.stride,
+                         up.data_ptr(), pu.ld, pu.stride, pd.parts, pd.rows, out_type, py.rows,
+                         px.cols, py.cols);
+  const int64_t need = bytes > 0 ? bytes : 0;  // (the call says what -1 is about)
+  at::Tensor scratch;
+  if (need) scratch = scratch_for(need, device, stream);
+  run("gemm_routed_adapters", device, [&] {
+    return g_adapters(type, x.data_ptr(), px.ld, down.data_ptr(), pd.ld, pd.stride, up.data_ptr(),
+                      pu.ld, pu.stride, static_cast<const int32_t*>(which.data_ptr()), scales,
+                      pd.parts, pd.rows, out_type, y.data_ptr(), py.ld, out.data_ptr(), po.ld,
+                      py.rows, px.cols, py.cols, need ? scratch.data_ptr() : nullptr, need, stream);
+  });
+  return THPVariable_Wrap(out);
+}
+
 // init_routed(addresses of the entry points)
 PyObject* init_routed(PyObject* const* a, Py_ssize_t n) {
-  count(n, 6);
-  void* p[6];
-  for (int i = 0; i < 6; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  count(n, 8);
+  void* p[8];
+  for (int i = 0; i < 8; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) throw Raised{};
   g_choose = reinterpret_cast<decltype(g_choose)>(p[0]);
   g_choose_grad = reinterpret_cast<decltype(g_choose_grad)>(p[1]);
@@ -581,6 +636,8 @@ PyObject* init_routed(PyObject* const* a, Py_ssize_t n) {
   g_scratch_bytes = reinterpret_cast<decltype(g_scratch_bytes)>(p[3]);
   g_routed_product = reinterpret_cast<decltype(g_routed_product)>(p[4]);
   g_weight_grad = reinterpret_cast<decltype(g_weight_grad)>(p[5]);
+  g_adapters_scratch = reinterpret_cast<decltype(g_adapters_scratch)>(p[6]);
+  g_adapters = reinterpret_cast<decltype(g_adapters)>(p[7]);
   Py_RETURN_NONE;
 }
 
@@ -612,6 +669,7 @@ PyMethodDef g_methods[] = {method<init>("init"), method<quantize>("quantize"),
                            method<init_routed>("init_routed"), method<choose>("choose"),
                            method<choose_grad>("choose_grad"), method<sort>("sort"),
                            method<experts>("experts"), method<experts_grad>("experts_grad"),
+                           method<adapters>("adapters"),
                            {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_torch_binding", nullptr, -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};

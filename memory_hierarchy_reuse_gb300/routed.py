@@ -5,6 +5,7 @@
     sort_by_expert(experts, count) -> offsets, order
     matmul_experts(x, w, offsets, ...) -> out
     matmul_experts_grad(x, grad, offsets, ...) -> gradient of w
+    add_adapters(y, x, down, up, which, ...) -> out
 
 As in ``mxfp4.py``: argument checks and marshalling only (in the compiled
 ``csrc/torch_binding.cpp``), launches on ``stream`` (default: the current torch
@@ -26,7 +27,9 @@ _lib = load()
 _torch_binding.init_routed(*(ctypes.cast(f, ctypes.c_void_p).value
                              for f in (_lib.gemm_routed_choose, _lib.gemm_routed_choose_grad,
                                        _lib.gemm_routed_sort, _lib.gemm_routed_scratch_bytes,
-                                       _lib.gemm_routed_product, _lib.gemm_routed_weight_grad)))
+                                       _lib.gemm_routed_product, _lib.gemm_routed_weight_grad,
+                                       _lib.gemm_routed_adapters_scratch,
+                                       _lib.gemm_routed_adapters)))
 
 
 def choose_experts(logits, top: int, score: str = "softmax", bias=None, groups: int = 1,
@@ -97,3 +100,15 @@ def matmul_experts_grad(x, grad, offsets, gather=None, scatter=None, top: int = 
     """
     return _torch_binding.experts_grad(x, grad, offsets, gather, scatter, top, out,
                                        _out_dtype(out_dtype), stream)
+
+
+def add_adapters(y, x, down, up, which, scales=None, out=None, stream=None):
+    """out[t] = y[t] + scales[a] * (x[t] @ down[a].T) @ up[a] with a = which[t].
+
+    ``y`` (T x N, float32, bfloat16 or float16): the shared projection's result. ``x``: T x K,
+    ``down``: adapters x rank x K, ``up``: adapters x rank x N, all bfloat16 or all float16.
+    ``which``: T int32; a row outside 0 .. adapters-1 has no adapter. ``scales``: one float32 an
+    adapter (1 when omitted). ``out``: of y's type and shape, y itself for a sum in place, or
+    allocated. Limits: 1024 adapters of rank 128.
+    """
+    return _torch_binding.adapters(y, x, down, up, which, scales, out, stream)

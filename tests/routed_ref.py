@@ -107,3 +107,11 @@ def weight_grad(x, g, offsets, gather=None, scatter=None, top=1):
             if 0 <= r < x.shape[0] and 0 <= to < g.shape[0]:
                 out[e] += np.outer(x[r], g[to])
     return out
+
+
+def adapters(y, x, down, up, which, scales=None):
+    out = y.copy()
+    for t, a in enumerate(which):
+        if 0 <= a < down.shape[0]:
+            out[t] += (1 if scales is None else scales[a]) * ((x[t] @ down[a].T) @ up[a])
+    return out
