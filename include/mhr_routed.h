@@ -84,15 +84,6 @@ int gemm_routed_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* offs
                      int32_t* order, void* stream);
 
 /*
- * Scratch for an operand of 16-bit elements -- `parts` matrices rows x cols,
- * pitch ld, `stride` elements apart -- of the two products below: 0 where its
- * address, pitch and stride are multiples of 16 bytes, else the bytes of a copy
- * that they make of it (-1: none fits the address space).
- */
-int64_t gemm_routed_scratch_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols,
-                                  int64_t ld, int64_t stride);
-
-/*
  * The experts' products.  For expert e and each sorted position q, offsets[e]
  * <= q < offsets[e + 1]:
  *   out[scatter ? scatter[q] : q] = x[gather ? gather[q] / top : q] W_e,
@@ -112,9 +103,14 @@ int64_t gemm_routed_scratch_bytes(const void* p, int64_t parts, int64_t rows, in
  * they were.  Offsets below the one before or past `rows` count as that.
  * K == 0 writes zeros.  E <= 1024.
  *
- * scratch: gemm_routed_scratch_bytes of x (one part) plus that of w (E parts);
- * the copy of w holds the experts that have rows.
+ * scratch: gemm_routed_product_scratch bytes, for x's rows in the order of gather
+ * (more than 256 of them), and for an x or w whose address, pitch or stride is no
+ * multiple of 16 bytes (of w, the experts that have rows); -1: none fits the
+ * address space.
  */
+int64_t gemm_routed_product_scratch(const void* x, int64_t x_rows, int64_t ldx, int gathered,
+                                    const void* w, int64_t ldw, int64_t stride_w, int transposed,
+                                    int64_t E, int64_t rows, int64_t K, int64_t N);
 int gemm_routed_product(int dtype, const void* x, int64_t x_rows, int64_t ldx,
                         const int32_t* gather, int64_t top, const void* w, int64_t ldw,
                         int64_t stride_w, int transposed, const int32_t* offsets, int64_t E,
@@ -128,8 +124,12 @@ int gemm_routed_product(int dtype, const void* x, int64_t x_rows, int64_t ldx,
  *           x[gather ? gather[q] / top : q]^T grad[scatter ? scatter[q] : q],
  * K x N at out + e * stride_o, pitch ldo; zeros for an expert without rows.
  * grad: grad_rows x N, pitch ldg, of x's type; the rest, and rows outside x or
- * grad, as above.  scratch: gemm_routed_scratch_bytes of x plus that of grad.
+ * grad, as above.  scratch: gemm_routed_weight_grad_scratch bytes, for rows in the
+ * order of gather and of scatter, and for operands as above.
  */
+int64_t gemm_routed_weight_grad_scratch(const void* x, int64_t x_rows, int64_t ldx, int gathered,
+                                        const void* grad, int64_t grad_rows, int64_t ldg,
+                                        int scattered, int64_t rows, int64_t K, int64_t N);
 int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, int64_t ldx,
                             const int32_t* gather, int64_t top, const void* grad,
                             int64_t grad_rows, int64_t ldg, const int32_t* scatter,

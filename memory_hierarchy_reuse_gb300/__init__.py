@@ -59,7 +59,8 @@ EXPORTS = ("gemm_f32", "gemm_f32_3xtf32", "gemm_bf16_f32acc", "gemm_f32_3xtf32_n
            "gemm_mxfp4_scale_bytes", "gemm_mxfp4_quantize", "gemm_mxfp4", "gemm_mxfp4_quantized",
            "gemm_mxfp4_moe",
            "gemm_routed_choose", "gemm_routed_choose_grad", "gemm_routed_sort",
-           "gemm_routed_scratch_bytes", "gemm_routed_product", "gemm_routed_weight_grad",
+           "gemm_routed_product_scratch", "gemm_routed_product",
+           "gemm_routed_weight_grad_scratch", "gemm_routed_weight_grad",
            "gemm_routed_adapters_scratch", "gemm_routed_adapters")
 
 _lib = None
@@ -118,8 +119,12 @@ def load(path: str | None = None):
     lib.gemm_routed_choose_grad.restype = ci
     lib.gemm_routed_sort.argtypes = [vp, i64, i64, vp, vp, vp]
     lib.gemm_routed_sort.restype = ci
-    lib.gemm_routed_scratch_bytes.argtypes = [vp, i64, i64, i64, i64, i64]
-    lib.gemm_routed_scratch_bytes.restype = i64
+    lib.gemm_routed_product_scratch.argtypes = [vp, i64, i64, ci, vp, i64, i64, ci, i64, i64, i64,
+                                                i64]
+    lib.gemm_routed_product_scratch.restype = i64
+    lib.gemm_routed_weight_grad_scratch.argtypes = [vp, i64, i64, ci, vp, i64, i64, ci, i64, i64,
+                                                    i64]
+    lib.gemm_routed_weight_grad_scratch.restype = i64
     lib.gemm_routed_product.argtypes = [ci, vp, i64, i64, vp, i64, vp, i64, i64, ci, vp, i64, ci,
                                         vp, i64, i64, vp, i64, i64, i64, vp, i64, vp]
     lib.gemm_routed_product.restype = ci

@@ -77,7 +77,7 @@ bool parts_ok(const void* p, int64_t size, int64_t parts, int64_t rows, int64_t 
          !__builtin_mul_overflow(parts, bytes, &all) && byte_range(p, parts, span * size, bytes, r);
 }
 
-// Scratch of `need` bytes (each repack_bytes, -1 if there is no such).
+// Scratch of `need` bytes (each operand_bytes, -1 if there is no such).
 int scratch_ok(const void* scratch, int64_t have, int64_t need_a, int64_t need_b, ByteRange* r) {
   int64_t need;
   if (need_a < 0 || need_b < 0 || __builtin_add_overflow(need_a, need_b, &need))
@@ -158,10 +158,32 @@ MHR_API int gemm_routed_sort(const int32_t* experts, int64_t n, int64_t E, int32
   });
 }
 
-MHR_API int64_t gemm_routed_scratch_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols,
-                                          int64_t ld, int64_t stride) {
-  if (parts < 1 || parts > MAX_PARTS || !dim_ok(rows) || !dim_ok(cols)) return -1;
-  return repack_bytes(p, parts, rows, cols, ld, stride);
+MHR_API int64_t gemm_routed_product_scratch(const void* x, int64_t x_rows, int64_t ldx,
+                                            int gathered, const void* w, int64_t ldw,
+                                            int64_t stride_w, int transposed, int64_t E,
+                                            int64_t rows, int64_t K, int64_t N) {
+  if (E < 1 || E > MAX_PARTS || !dim_ok(x_rows) || !dim_ok(rows) || !dim_ok(K) || !dim_ok(N))
+    return -1;
+  if (rows == 0 || N == 0 || K == 0 || x_rows == 0) return 0;
+  const int64_t a =
+      operand_bytes(x, 1, x_rows, K, ldx, 0, gathered && rows > FEW_ROWS ? rows : 0);
+  const int64_t b =
+      operand_bytes(w, E, transposed ? N : K, transposed ? K : N, ldw, stride_w, 0);
+  int64_t both;
+  return a < 0 || b < 0 || __builtin_add_overflow(a, b, &both) ? -1 : both;
+}
+
+MHR_API int64_t gemm_routed_weight_grad_scratch(const void* x, int64_t x_rows, int64_t ldx,
+                                                int gathered, const void* grad,
+                                                int64_t grad_rows, int64_t ldg, int scattered,
+                                                int64_t rows, int64_t K, int64_t N) {
+  if (!dim_ok(x_rows) || !dim_ok(grad_rows) || !dim_ok(rows) || !dim_ok(K) || !dim_ok(N))
+    return -1;
+  if (rows == 0 || N == 0 || K == 0 || x_rows == 0 || grad_rows == 0) return 0;
+  const int64_t a = operand_bytes(x, 1, x_rows, K, ldx, 0, gathered ? rows : 0);
+  const int64_t b = operand_bytes(grad, 1, grad_rows, N, ldg, 0, scattered ? rows : 0);
+  int64_t both;
+  return a < 0 || b < 0 || __builtin_add_overflow(a, b, &both) ? -1 : both;
 }
 
 MHR_API int gemm_routed_product(int dtype, const void* x, int64_t x_rows, int64_t ldx,
@@ -180,8 +202,10 @@ MHR_API int gemm_routed_product(int dtype, const void* x, int64_t x_rows, int64_
     const int64_t wr = transposed ? N : K, wc = transposed ? K : N;
     if (!plain_ok(x, 2, x_rows, K, ldx, &rx) || !parts_ok(w, 2, E, wr, wc, ldw, stride_w, &rw))
       return MHR_ERR_INVALID_ARG;
-    if (const int rc = scratch_ok(scratch, scratch_bytes, repack_bytes(x, 1, x_rows, K, ldx, 0),
-                                  repack_bytes(w, E, wr, wc, ldw, stride_w), &rs);
+    if (const int rc = scratch_ok(
+            scratch, scratch_bytes,
+            operand_bytes(x, 1, x_rows, K, ldx, 0, gather && rows > FEW_ROWS ? rows : 0),
+            operand_bytes(w, E, wr, wc, ldw, stride_w, 0), &rs);
         rc != MHR_OK)
       return rc;
   }
@@ -210,8 +234,9 @@ MHR_API int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, in
   if (rows > 0 && x_rows > 0 && grad_rows > 0) {
     if (!plain_ok(x, 2, x_rows, K, ldx, &rx) || !plain_ok(grad, 2, grad_rows, N, ldg, &rg))
       return MHR_ERR_INVALID_ARG;
-    if (const int rc = scratch_ok(scratch, scratch_bytes, repack_bytes(x, 1, x_rows, K, ldx, 0),
-                                  repack_bytes(grad, 1, grad_rows, N, ldg, 0), &rs);
+    if (const int rc = scratch_ok(
+            scratch, scratch_bytes, operand_bytes(x, 1, x_rows, K, ldx, 0, gather ? rows : 0),
+            operand_bytes(grad, 1, grad_rows, N, ldg, 0, scatter ? rows : 0), &rs);
         rc != MHR_OK)
       return rc;
   }

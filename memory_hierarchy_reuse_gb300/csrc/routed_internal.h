@@ -49,9 +49,12 @@ cudaError_t launch_choose_grad(const ChooseGradArgs& a, cudaStream_t s);
 
 // Bytes of scratch that `parts` matrices (rows x cols, 16-bit elements, pitch ld,
 // `stride` elements apart) take to be read by TMA: 0 for those that it reads as they
-// are; -1 where they leave the address space.
-int64_t repack_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
-                     int64_t stride);
+// are; -1 where they leave the address space.  picked: rows of the (one) matrix that an
+// index picks, which are put in order there; 0 without.
+int64_t operand_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
+                      int64_t stride, int64_t picked);
+// Up to so many rows a product picks by TMA's gather, without that.
+constexpr int64_t FEW_ROWS = 256;
 
 // One gemm_routed_product (product, transposed) or gemm_routed_weight_grad
 // (gradient).  K: columns of x; N: the output's columns.  `w` is the weights, or the
@@ -74,7 +77,7 @@ struct ProductArgs {
   const int32_t* scatter;
   int64_t rows, K, N;
 };
-// scratch: repack_bytes of x, then of w.
+// scratch: operand_bytes of x, then of w.
 cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl& ctl,
                            cudaStream_t s);
 

@@ -13,12 +13,17 @@
 //   product           W_e (K x N): MN-major       x rows, K-major
 //   transposed        W_e (N x K): K-major        x rows, K-major
 //   weight gradient   gradient rows, MN-major     x rows, MN-major
-// Rows that an index picks come by TMA's gather of four rows, a lane four rows; a row
-// outside its matrix -- past an expert's last, or an index out of range -- is zeros.
+// All come by TMA.  Rows that an index picks are put in order first by a kernel of their
+// own; of few rows, TMA's gather of four rows brings them, a lane four rows.  (The gather
+// takes some 60 cycles for its 512 bytes: 8192 tokens, 8 of 16 experts of 4096 x 4096,
+// 4283 us with it against 1143 for rows in order; copies by the threads into the same
+// layout were as slow.)  A row outside its matrix -- past an expert's last, or an index
+// out of range -- is zeros.
 #include <cuda_runtime.h>
 
 #include <cstdint>
 #include <cstdio>
+#include <type_traits>
 
 #include "mhr_gemm.h"
 #include "mhr_mxfp4.h"
@@ -35,24 +40,35 @@ using mx::tma_load_3d_pair;
 constexpr uint32_t ALL = 0xffffffffu;
 constexpr int TILE_F = 256;                  // features of a pair's tile
 constexpr int HALF = 128;
-constexpr int MAX_ROWS = 256;                // rows of a pair's tile
 constexpr int BK = 64;                       // of the sum a stage: one swizzle row of 128 bytes
 constexpr int A_BYTES = HALF * BK * 2;       // this CTA's features
 constexpr int BOX = 64 * 128;                // 64 rows of 128 bytes
-constexpr int B_BYTES = HALF * BK * 2;       // this CTA's half of the rows, at most
-constexpr int STAGE_BYTES = A_BYTES + B_BYTES;  // 32 KB
-constexpr int STAGES = 6;
-constexpr int EPI_WARPS = 4;
-constexpr int THREADS = 192;
-constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
-constexpr uint32_t TMEM_COLS = 2 * MAX_ROWS;
+constexpr int EPI_WARPS = 8;
+constexpr int CLASSES = 8;                   // of experts, by what their units cost
+constexpr int THREADS = 32 * (2 + EPI_WARPS);
 
 enum Mode { PRODUCT = 0, TRANSPOSED = 1, GRADIENT = 2 };
+
+// LONG: fp32 results.  The tensor cores add into their fp32 accumulators by truncation,
+// which takes some 4e-8 of a sum off for every 16 terms (6e-7 after 256, 4e-6 after
+// 4096, where fp32 in any order would leave 2e-7): the sum goes on in registers, rounded
+// to nearest, after every SEGMENT stages.  16-bit results, 2e-3 or 2e-4 off by their own
+// rounding, do without.  An epilogue thread holds 64 of a tile's 128 columns.
+template <bool LONG>
+struct Shape {
+  static constexpr int ROWS = LONG ? 128 : 256;            // rows of a pair's tile, at most
+  static constexpr int B_BYTES = ROWS / 2 * BK * 2;        // this CTA's half of them
+  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;    // 24 or 32 KB
+  static constexpr int STAGES = LONG ? 8 : 6;
+  static constexpr int SEGMENT = LONG ? 4 : 1 << 30;       // stages an accumulator takes
+  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+  static constexpr uint32_t TMEM_COLS = 2 * ROWS;
+};
 
 struct Params {
   const int32_t* offsets;
   const int32_t* gather;   // rows of x over `top`, or null
-  const int32_t* scatter;  // rows of the output (of the gradient rows), or null
+  const int32_t* scatter;  // rows of the output, or null
   void* out;
   int64_t ldo, stride_o;   // stride_o: of one expert's gradient
   int32_t E, rows, x_rows, out_rows;
@@ -85,41 +101,62 @@ struct Unit {
   int sum0, sum;       // gradient: the expert's sorted positions, summed over
 };
 
-// parts[e]: first unit of expert e; lo[e], n[e]: its sorted positions.
+// Experts in descending order of what their units cost: expert[i] has the units from
+// parts[i] on (parts has one more); its sorted positions are n[e] from lo[e] on.
 struct Table {
   const uint32_t* parts;
+  const int32_t* expert;
   const int32_t* lo;
   const int32_t* n;
 };
 
-__device__ __forceinline__ int row_tiles(int n) { return (n + MAX_ROWS - 1) / MAX_ROWS; }
+template <int ROWS>
+__device__ __forceinline__ int row_tiles(int n) {
+  return (n + ROWS - 1) / ROWS;
+}
+// Rows of an expert's tiles: all of one size.
+template <int ROWS>
+__device__ __forceinline__ int tile_rows(int n) {
+  const int tiles = row_tiles<ROWS>(n);
+  return tiles ? ((n + tiles - 1) / tiles + 31) & ~31 : 32;
+}
 
-template <int MODE>
+// How much a unit of an expert of n rows costs: the steps of an MMA's columns; of a
+// gradient, the stages, by powers of two.  Clusters take units in turn, the dearest
+// first, so that two clusters' work differs by one unit's at most (in turn in the
+// experts' order, clusters of skewed counts were up to a fifth apart).  Runs of units
+// of like cost for each cluster would be as even, but scatter the experts over time:
+// 8192 tokens, 8 of 16 experts of 4096 x 4096, 2624 us against 1143, from HBM.
+template <int MODE, int ROWS>
+__device__ __forceinline__ int cost_class(int n) {
+  if (n == 0) return 0;
+  if constexpr (MODE == GRADIENT) return min(CLASSES - 1, 32 - __clz((n + BK - 1) / BK));
+  return tile_rows<ROWS>(n) * CLASSES / ROWS - 1;
+}
+
+template <int MODE, int ROWS>
 __device__ __forceinline__ Unit unit_at(uint32_t u, const Params& p, const Table& t) {
+  int i = 0;  // the last place whose first unit is at most u
+  for (int end = p.E; end - i > 1;) {
+    const int mid = (i + end) >> 1;
+    if (t.parts[mid] <= u)
+      i = mid;
+    else
+      end = mid;
+  }
+  const int e = t.expert[i];
   Unit w;
+  const uint32_t r = u - t.parts[i];
+  w.expert = e;
   if constexpr (MODE == GRADIENT) {
-    const uint32_t per = p.f_tiles * p.k_tiles;
-    const uint32_t e = u / per, r = u - e * per;
-    w.expert = e;
     w.f0 = static_cast<int>(r % p.f_tiles) * TILE_F;
-    w.first = static_cast<int>(r / p.f_tiles) * MAX_ROWS;
-    w.count = min(MAX_ROWS, p.K - w.first);
+    w.first = static_cast<int>(r / p.f_tiles) * ROWS;
+    w.count = min(ROWS, p.K - w.first);
     w.sum0 = t.lo[e];
     w.sum = t.n[e];
   } else {
-    int e = 0, end = p.E;  // the last expert whose first unit is at most u
-    while (end - e > 1) {
-      const int mid = (e + end) >> 1;
-      if (t.parts[mid] <= u)
-        e = mid;
-      else
-        end = mid;
-    }
-    // an expert's rows in tiles of one size; its tiles of one weight tile follow one another
-    const uint32_t r = u - t.parts[e], tiles = row_tiles(t.n[e]);
-    const int size = ((t.n[e] + static_cast<int>(tiles) - 1) / static_cast<int>(tiles) + 31) & ~31;
+    const int tiles = row_tiles<ROWS>(t.n[e]), size = tile_rows<ROWS>(t.n[e]);
     const int at = static_cast<int>(r % tiles) * size;
-    w.expert = e;
     w.f0 = static_cast<int>(r / tiles) * TILE_F;
     w.first = t.lo[e] + at;
     w.count = max(0, min(size, t.n[e] - at));
@@ -130,15 +167,10 @@ __device__ __forceinline__ Unit unit_at(uint32_t u, const Params& p, const Table
   return w;
 }
 
-// The output's rows of a warp's 32 columns of TMEM from row `first` on: lane j's row
-// j, below 0 for none.
-template <int MODE>
-__device__ __forceinline__ int out_row(const Params& p, const Unit& w, int at, int lane) {
-  if (at + lane >= w.count) return -1;
-  const int r = w.first + at + lane;
-  if (MODE == GRADIENT || !p.scatter) return r;
-  const int s = p.scatter[r];
-  return s < p.out_rows ? s : -1;
+// The row that an index picks, over `top`: below 0 where it lies outside `rows`.
+__device__ __forceinline__ int picked_row(int index, int top, int rows) {
+  const int r = index >= 0 ? index / top : -1;
+  return r < rows ? r : -1;
 }
 
 __device__ __forceinline__ uint32_t pack16(int dtype, uint32_t lo, uint32_t hi) {
@@ -151,74 +183,100 @@ __device__ __forceinline__ uint32_t pack16(int dtype, uint32_t lo, uint32_t hi) 
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// 32 rows (columns of TMEM) of 32 features (lanes) to the output.
-template <int MODE>
+// 32 rows (columns of TMEM) of 32 features (lanes) to the output: of fp32 (WIDE), or of
+// 16 bits.  Values and rows first, then the stores, predicated: a branch a row made a
+// chunk take 2700 cycles, each of its shuffles waited for.
+template <int MODE, bool WIDE>
 __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Params& p,
                                             const Unit& w, int at, int feature, int lane) {
-  const int mine = out_row<MODE>(p, w, at, lane);
-  const int rows = min(32, w.count - at);
-  char* base = static_cast<char*>(p.out);
-  if constexpr (MODE == GRADIENT)
-    base += w.expert * p.stride_o * (p.out_dtype == MHR_F32 ? 4 : 2);
-  if (p.out_dtype == MHR_F32) {
-    float* out = reinterpret_cast<float*>(base) + feature;
-    const bool in = feature < p.N;
+  using Word = std::conditional_t<WIDE, uint32_t, uint16_t>;
+  Word* base = static_cast<Word*>(p.out);
+  if constexpr (MODE == GRADIENT) base += w.expert * p.stride_o;
+  const int count = w.count - at;  // rows from here on
+  // `each` rows apart from row `from` on: f(row j of the chunk, where it starts, whether it is there)
+  auto rows = [&](int from, auto each, const auto& f) {
+    constexpr int EACH = decltype(each)::value;
+    if (MODE == GRADIENT || !p.scatter) {
+      Word* dst = base + (w.first + at + from) * p.ldo;
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int row = __shfl_sync(ALL, mine, j);
-      if (j < rows && row >= 0 && in) out[row * p.ldo] = __uint_as_float(r[j]);
+      for (int j = 0; j < 32; j += EACH) {
+        f(j, dst, j + from < count);
+        dst += EACH * p.ldo;
+      }
+    } else {
+      const int mine = lane < count ? picked_row(p.scatter[w.first + at + lane], 1, p.out_rows) : -1;
+#pragma unroll
+      for (int j0 = 0; j0 < 32; j0 += 8 * EACH) {
+        int to[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(ALL, mine, j0 + i * EACH + from);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f(j0 + i * EACH, base + to[i] * p.ldo, to[i] >= 0);
+      }
     }
+  };
+  const std::integral_constant<int, 1> one;
+  if constexpr (WIDE) {
+    const bool in = feature < p.N;
+    rows(0, one, [&](int j, Word* dst, bool there) {
+      if (there && in) dst[feature] = r[j];
+    });
   } else if (p.pairs) {
     // Neighbouring lanes exchange: the even one gets two features of row j, the odd
     // one of row j + 1, so that a store of the warp is two whole runs of 64 bytes.
     const int odd = lane & 1, f = feature - odd;
-    uint16_t* out = reinterpret_cast<uint16_t*>(base) + f;
+    uint32_t v[16];
 #pragma unroll
     for (int j = 0; j < 32; j += 2) {
       const uint32_t other = __shfl_xor_sync(ALL, odd ? r[j] : r[j + 1], 1);
-      const uint32_t v = odd ? pack16(p.out_dtype, other, r[j + 1])
-                             : pack16(p.out_dtype, r[j], other);
-      const int row = __shfl_sync(ALL, mine, j + odd);
-      if (j + odd < rows && row >= 0) {
-        uint16_t* dst = out + row * p.ldo;
-        if (f + 1 < p.N)
-          *reinterpret_cast<uint32_t*>(dst) = v;
-        else if (f < p.N)
-          *dst = static_cast<uint16_t>(v);
-      }
+      v[j / 2] = odd ? pack16(p.out_dtype, other, r[j + 1]) : pack16(p.out_dtype, r[j], other);
     }
+    const bool both = f + 1 < p.N, one_in = f + 1 == p.N;
+    rows(odd, std::integral_constant<int, 2>{}, [&](int j, Word* dst, bool there) {
+      if (there && both) *reinterpret_cast<uint32_t*>(dst + f) = v[j / 2];
+    });
+    if (one_in)
+      rows(odd, std::integral_constant<int, 2>{}, [&](int j, Word* dst, bool there) {
+        if (there) dst[f] = static_cast<uint16_t>(v[j / 2]);
+      });
   } else {
-    uint16_t* out = reinterpret_cast<uint16_t*>(base) + feature;
     const bool in = feature < p.N;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int row = __shfl_sync(ALL, mine, j);
-      if (j < rows && row >= 0 && in)
-        out[row * p.ldo] = static_cast<uint16_t>(pack16(p.out_dtype, r[j], r[j]));
-    }
+    rows(0, one, [&](int j, Word* dst, bool there) {
+      if (there && in) dst[feature] = static_cast<uint16_t>(pack16(p.out_dtype, r[j], r[j]));
+    });
   }
 }
 
 // Warp roles, barriers and the way a timeout unwinds are those of the other pair
-// kernels (mxfp4_pair.cu): warp 0 producer, warp 1 MMA issuer (rank 0), warps 2-5
+// kernels (mxfp4_pair.cu): warp 0 producer, warp 1 MMA issuer (rank 0), warps 2-9
 // epilogue; full[s] and released[b] in rank 0, empty[s] and acc_full[b] in both CTAs.
-// tmW: the features' side.  tmX: x in boxes of 8 rows, or one for a gather; tmXBig:
-// in boxes of 128 rows (no gather).
-template <int MODE, bool GATHER>
+// Rank 1's epilogue hands an accumulator back to its own read[b], from where its warp 1,
+// idle otherwise, tells rank 0: an arrival that is released to the cluster waits for the
+// stores that its thread has under way.
+// tmW: the features' side (gradient: in boxes of 64 rows), tmX: the rows' in boxes of a
+// CTA's half of a whole tile (gradient: 64 rows), tmX8: in boxes of 8 rows, of one for a
+// gather (gradient: 16 rows).  Gradient only, for an expert's last rows: tmW16, in boxes
+// of 16 rows, and tmW1 and tmX1, for the gather.
+template <int MODE, bool INDEXED, bool LONG>
 __global__ void __launch_bounds__(THREADS, 1)
     routed_pair_kernel(const __grid_constant__ CUtensorMap tmW,
                        const __grid_constant__ CUtensorMap tmX,
-                       const __grid_constant__ CUtensorMap tmXBig, const Params p) {
+                       const __grid_constant__ CUtensorMap tmX8,
+                       const __grid_constant__ CUtensorMap tmW16,
+                       const __grid_constant__ CUtensorMap tmW1,
+                       const __grid_constant__ CUtensorMap tmX1, const Params p) {
+  using S = Shape<LONG>;
+  constexpr int STAGES = S::STAGES, ROWS = S::ROWS, STAGE_BYTES = S::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t bars[2 * STAGES + 6];
+  __shared__ alignas(8) uint64_t bars[2 * STAGES + 8];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ volatile uint32_t peer_loaded;          // rank 0: stages that rank 1 loaded
   __shared__ volatile uint32_t stage_tx[STAGES];     // bytes of a CTA's last load of a stage
   __shared__ volatile uint32_t peer_tx[STAGES];      // rank 0: rank 1's
   __shared__ uint32_t parts[MAX_PARTS + 1];
-  __shared__ int32_t lo[MAX_PARTS], num[MAX_PARTS];
-  __shared__ uint32_t sums[THREADS / 32];
+  __shared__ int32_t expert[MAX_PARTS], lo[MAX_PARTS], num[MAX_PARTS];
+  __shared__ uint32_t class_units[CLASSES], class_experts[CLASSES];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
@@ -226,8 +284,9 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
   auto acc_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
   auto released_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 4);
-  const uint32_t peer_done_bar = bar0 + 8u * (2 * STAGES + 5);
+  auto read_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 4 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 6);
+  const uint32_t peer_done_bar = bar0 + 8u * (2 * STAGES + 7);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -241,7 +300,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_bar(b), 1);
-      mbar_init(released_bar(b), 2 * EPI_WARPS);
+      mbar_init(released_bar(b), EPI_WARPS + 1);
+      mbar_init(read_bar(b), EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
     mbar_init(peer_done_bar, 1);
@@ -250,45 +310,63 @@ __global__ void __launch_bounds__(THREADS, 1)
     fence_mbar_init();
     if (p.K > 0) {
       tma_prefetch_desc(&tmW);
-      tma_prefetch_desc(&tmX);
-      if (!GATHER) tma_prefetch_desc(&tmXBig);
+      if (!INDEXED) tma_prefetch_desc(&tmX);
+      if (MODE != GRADIENT) tma_prefetch_desc(&tmX8);
     }
   }
   if (warp == 1) {
-    tmem_alloc_pair(smem_u32(&tmem_slot), TMEM_COLS);
+    tmem_alloc_pair(smem_u32(&tmem_slot), S::TMEM_COLS);
     tmem_relinquish_pair();
   }
+  if (threadIdx.x < CLASSES) class_units[threadIdx.x] = class_experts[threadIdx.x] = 0;
+  __syncthreads();
   grid_dependency_wait();
-  // The experts' parts, and the first unit of each.
-  uint32_t units = 0;
-  for (int e0 = 0; e0 < p.E; e0 += THREADS) {
-    const int e = e0 + static_cast<int>(threadIdx.x);
-    uint32_t c = 0;
-    if (e < p.E) {
-      // (offsets that are not ascending, or past the rows, reach nothing)
-      const int a = min(max(p.offsets[e], 0), p.rows), b = min(max(p.offsets[e + 1], a), p.rows);
-      lo[e] = a;
-      num[e] = b - a;
-      c = MODE == GRADIENT ? p.f_tiles * p.k_tiles : row_tiles(b - a) * p.f_tiles;
-    }
-    uint32_t scan = c;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t o = __shfl_up_sync(ALL, scan, d);
-      if (lane >= d) scan += o;
-    }
-    if (lane == 31) sums[warp] = scan;
-    __syncthreads();
-    uint32_t lower = 0, all = 0;
-    for (int i = 0; i < THREADS / 32; ++i) {
-      if (i < warp) lower += sums[i];
-      all += sums[i];
-    }
-    if (e < p.E) parts[e] = units + lower + scan - c;
-    units += all;
-    __syncthreads();
+  // The experts' rows, then their places: a warp takes a class, whose place is behind
+  // the dearer ones.
+  auto units_of = [&](int n) -> uint32_t {
+    return (MODE == GRADIENT ? p.k_tiles : row_tiles<ROWS>(n)) * p.f_tiles;
+  };
+  for (int e = threadIdx.x; e < p.E; e += THREADS) {
+    // (offsets that are not ascending, or past the rows, reach nothing)
+    const int a = min(max(p.offsets[e], 0), p.rows), b = min(max(p.offsets[e + 1], a), p.rows);
+    lo[e] = a;
+    num[e] = b - a;
+    const int k = cost_class<MODE, ROWS>(b - a);
+    atomicAdd(&class_units[k], units_of(b - a));
+    atomicAdd(&class_experts[k], 1u);
   }
-  const Table table{parts, lo, num};
+  __syncthreads();
+  static_assert(THREADS / 32 >= CLASSES, "a warp a class");
+  if (warp < CLASSES) {
+    uint32_t unit = 0, place = 0;
+    for (int k = CLASSES - 1; k > warp; --k) {
+      unit += class_units[k];
+      place += class_experts[k];
+    }
+    for (int e0 = 0; e0 < p.E; e0 += 32) {
+      const int e = e0 + lane;
+      const bool in = e < p.E && cost_class<MODE, ROWS>(num[e]) == warp;
+      const uint32_t c = in ? units_of(num[e]) : 0;
+      const uint32_t mask = __ballot_sync(ALL, in);
+      if (!mask) continue;
+      uint32_t scan = c;
+#pragma unroll
+      for (int i = 1; i < 32; i <<= 1) {
+        const uint32_t o = __shfl_up_sync(ALL, scan, i);
+        if (lane >= i) scan += o;
+      }
+      if (in) {
+        const uint32_t at = place + __popc(mask & ((1u << lane) - 1));
+        expert[at] = e;
+        parts[at] = unit + scan - c;
+      }
+      place += __popc(mask);
+      unit += __shfl_sync(ALL, scan, 31);
+    }
+  }
+  uint32_t units = 0;
+  for (int k = 0; k < CLASSES; ++k) units += class_units[k];
+  const Table table{parts, expert, lo, num};
   tc_fence_before();
   cluster_sync_all();
   tc_fence_after();
@@ -300,47 +378,37 @@ __global__ void __launch_bounds__(THREADS, 1)
     abort_flag = 1;
     st_shared_cluster_u32(peer_abort, 1u);
   };
-
   if (warp == 0) {
     uint32_t it = 0, s = 0, ph = 1;  // stages armed and loaded; ring position, phase to wait for
     const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
     const uint32_t fb0 = mapa_shared(full_bar(0), 0);
     bool ok = true;
     for (uint32_t u = cluster; ok && u < units; u += clusters) {
-      const Unit w = unit_at<MODE>(u, p, table);
+      const Unit w = unit_at<MODE, ROWS>(u, p, table);
       const int kbs = (w.sum + BK - 1) / BK, half = w.width / 2;
-      const uint32_t tx = MODE == GRADIENT ? 2 * A_BYTES : A_BYTES + half * 128;
       const int f = w.f0 + static_cast<int>(rank) * HALF;
-      const int mine = static_cast<int>(rank) * half;  // this CTA's first row of the tile
-      int32_t r[4], g[4];  // this lane's four rows of x, and of the gradient rows
-      if constexpr (MODE != GRADIENT && GATHER) {
+      const int mine = w.first + static_cast<int>(rank) * half;  // this CTA's first row
+      int32_t r[4];  // gather: this lane's four rows
+      if constexpr (INDEXED) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int at = mine + 4 * lane + i;
-          const int row = at < w.count ? p.gather[w.first + at] : -1;
-          r[i] = row >= 0 && row / p.top < p.x_rows ? row / p.top : p.x_rows;
+          const int at = static_cast<int>(rank) * half + 4 * lane + i;
+          const int row =
+              at < w.count ? picked_row(p.gather[w.first + at], p.top, p.x_rows) : -1;
+          r[i] = row >= 0 ? row : p.x_rows;
         }
       }
       for (int kb = 0; kb < kbs; ++kb, ++it) {
-        if constexpr (MODE == GRADIENT) {  // (before the wait: the loads take their time)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int at = kb * BK + 4 * (lane & 15) + i;
-            const bool in = at < w.sum;
-            const int pos = w.sum0 + at;
-            const int row = in ? (p.gather ? p.gather[pos] : pos) : -1;
-            const int of = p.gather ? row / p.top : row;
-            r[i] = row >= 0 && of < p.x_rows ? of : p.x_rows;
-            const int to = in ? (p.scatter ? p.scatter[pos] : pos) : -1;
-            g[i] = to >= 0 && to < p.out_rows ? to : p.out_rows;
-          }
-        }
         if (!__all_sync(ALL, mbar_wait_bounded(empty_bar(s), ph, limit, &abort_flag))) {
           if (lane == 0) give_up(kErrTimeoutProducer);
           ok = false;
           break;
         }
         const uint32_t st = sbase + s * STAGE_BYTES, fb = fb0 + 8u * s;
+        const int rows = min(BK, w.sum - kb * BK);         // gradient: positions of this stage,
+        const int read = (rows + 15) & ~15;                // and those that the MMAs read
+        const uint32_t tx = MODE == GRADIENT ? (2 + S::B_BYTES / BOX) * 128 * read
+                                             : A_BYTES + half * 128;
         if (lane == 0) {
           stage_tx[s] = tx;
           if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * tx);
@@ -348,11 +416,33 @@ __global__ void __launch_bounds__(THREADS, 1)
         __syncwarp();
         if (!(stall && it == 0)) {
           if constexpr (MODE == GRADIENT) {
-            // 64 positions x 64 features a box: lanes 0-15 the first box, 16-31 the second
-            const int box = lane >> 4;
-            const uint32_t to = st + box * BOX + (lane & 15) * 512;
-            tma_gather4_pair(to, &tmW, fb, f + 64 * box, g);
-            tma_gather4_pair(to + A_BYTES, &tmX, fb, w.first + mine + 64 * box, r);
+            // 64 features a box; the first two on the features' side
+            constexpr int BOXES = 2 + S::B_BYTES / BOX;
+            const int pos = w.sum0 + kb * BK;
+            if (rows == BK) {
+              if (elect_one()) {
+#pragma unroll
+                for (int i = 0; i < BOXES; ++i)
+                  tma_load_2d_pair(st + i * BOX, i < 2 ? &tmW : &tmX, fb,
+                                   i < 2 ? f + 64 * i : mine + 64 * (i - 2), pos);
+              }
+            } else {
+              // An expert's last rows: sixteen at a time, and the last of them by the
+              // gather, which ends in zeros and not in the next expert's rows.
+              const int whole = rows / 16;
+              if (lane < BOXES * whole) {
+                const int i = lane % BOXES, g = lane / BOXES;
+                tma_load_2d_pair(st + i * BOX + g * 2048, i < 2 ? &tmW16 : &tmX8, fb,
+                                 i < 2 ? f + 64 * i : mine + 64 * (i - 2), pos + 16 * g);
+              }
+              if (read > 16 * whole && lane < 4 * BOXES) {
+                const int i = lane % BOXES, g = 16 * whole + 4 * (lane / BOXES);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) r[j] = g + j < rows ? pos + g + j : p.rows;
+                tma_gather4_pair(st + i * BOX + g * 128, i < 2 ? &tmW1 : &tmX1, fb,
+                                 i < 2 ? f + 64 * i : mine + 64 * (i - 2), r);
+              }
+            }
           } else {
             if (elect_one()) {
               if constexpr (MODE == PRODUCT) {
@@ -361,16 +451,14 @@ __global__ void __launch_bounds__(THREADS, 1)
               } else {
                 tma_load_3d_pair(st, &tmW, fb, kb * BK, f, w.expert);
               }
+              if (!INDEXED && half == ROWS / 2)
+                tma_load_2d_pair(st + A_BYTES, &tmX, fb, kb * BK, mine);
             }
-            if constexpr (GATHER) {
+            if constexpr (INDEXED) {
               if (4 * lane < half)
-                tma_gather4_pair(st + A_BYTES + lane * 512, &tmX, fb, kb * BK, r);
-            } else if (half == HALF) {
-              if (elect_one())
-                tma_load_2d_pair(st + A_BYTES, &tmXBig, fb, kb * BK, w.first + mine);
-            } else if (8 * lane < half) {
-              tma_load_2d_pair(st + A_BYTES + lane * 1024, &tmX, fb, kb * BK,
-                               w.first + mine + 8 * lane);
+                tma_gather4_pair(st + A_BYTES + lane * 512, &tmX8, fb, kb * BK, r);
+            } else if (half < ROWS / 2 && 8 * lane < half) {
+              tma_load_2d_pair(st + A_BYTES + lane * 1024, &tmX8, fb, kb * BK, mine + 8 * lane);
             }
           }
         }
@@ -420,30 +508,29 @@ __global__ void __launch_bounds__(THREADS, 1)
     __syncwarp();
   } else if (warp == 1) {
     if (leader) {
-      uint32_t it = 0, t = 0, s = 0, ph = 0;
+      uint32_t t = 0, s = 0, ph = 0;  // accumulators filled; ring position and its phase
       bool ok = true;
       auto wait = [&](uint32_t bar, uint32_t parity) {  // a warp-uniform outcome
         return __all_sync(ALL, mbar_wait_bounded(bar, parity, limit, &abort_flag)) != 0;
       };
-      for (uint32_t u = cluster; ok && u < units; u += clusters, ++t) {
-        const Unit w = unit_at<MODE>(u, p, table);
+      for (uint32_t u = cluster; ok && u < units; u += clusters) {
+        const Unit w = unit_at<MODE, ROWS>(u, p, table);
         const int kbs = (w.sum + BK - 1) / BK;
         const int tail = (w.sum - (kbs - 1) * BK + 15) / 16;  // MMAs of the last stage
         const uint32_t idesc =
             make_idesc(p.kind, MODE != TRANSPOSED, MODE == GRADIENT, TILE_F, w.width);
-        if (t >= 2 && !wait(released_bar(t & 1u), ((t - 2) >> 1) & 1u)) {
-          if (lane == 0) give_up(kErrTimeoutMma);
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem + (t & 1u) * MAX_ROWS;
-        for (int kb = 0; kb < kbs; ++kb, ++it) {
-          if (!wait(full_bar(s), ph)) {
+        // an accumulator whose last but one filling has been read
+        auto next = [&] { return t < 2 || wait(released_bar(t & 1u), ((t - 2) >> 1) & 1u); };
+        for (int kb = 0; kb < kbs; ++kb) {
+          const int in = LONG ? kb % S::SEGMENT : kb;
+          const bool last = kb + 1 == kbs || (LONG && in + 1 == S::SEGMENT);
+          if ((in == 0 && !next()) || !wait(full_bar(s), ph)) {
             if (lane == 0) give_up(kErrTimeoutMma);
             ok = false;
             break;
           }
           tc_fence_after();
+          const uint32_t d = tmem + (t & 1u) * ROWS;
           const uint32_t st = sbase + s * STAGE_BYTES;
           const uint64_t a = MODE == TRANSPOSED ? smem_desc_sw128(st, 16, 1024)
                                                 : smem_desc_sw128(st, BOX, 1024);
@@ -457,57 +544,120 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int kk = 0; kk < BK / 16; ++kk)
               if (kk < mmas)
-                mma_f16_pair(d, a + kk * step_a, b + kk * step_b, idesc, kb > 0 || kk > 0 ? 1u : 0u);
+                mma_f16_pair(d, a + kk * step_a, b + kk * step_b, idesc, in > 0 || kk > 0 ? 1u : 0u);
             mma_commit_pair_multicast(empty_bar(s), 0x3);
-            if (kb + 1 == kbs) mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
+            if (last) mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
           }
           __syncwarp();
+          if (last) ++t;
           if (++s == STAGES) {
             s = 0;
             ph ^= 1u;
           }
         }
-        if (kbs == 0 && elect_one()) mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
-        __syncwarp();
+        if (kbs == 0) {  // (nothing to add up; the epilogue writes zeros)
+          if (!next()) {
+            if (lane == 0) give_up(kErrTimeoutMma);
+            break;
+          }
+          if (elect_one()) mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
+          __syncwarp();
+          ++t;
+        }
       }
       if (elect_one()) mma_commit_pair(drain_bar);
       __syncwarp();
       volatile int never = 0;
       if (!mbar_wait_bounded(drain_bar, 0, limit, &never) && lane == 0)
         atomicOr(p.status, kErrTimeoutDrain);
+    } else {
+      uint32_t t = 0;
+      bool ok = true;
+      for (uint32_t u = cluster; ok && u < units; u += clusters) {
+        const int kbs = (unit_at<MODE, ROWS>(u, p, table).sum + BK - 1) / BK;
+        const int fillings = LONG ? max(1, (kbs + S::SEGMENT - 1) / S::SEGMENT) : 1;
+        for (int i = 0; i < fillings; ++i, ++t) {
+          ok = __all_sync(ALL, mbar_wait_bounded(read_bar(t & 1u), (t >> 1) & 1u, limit,
+                                                 &abort_flag, 64));
+          if (!ok) {
+            if (lane == 0) give_up(kErrTimeoutEpilogue);
+            break;
+          }
+          if (lane == 0) mbar_arrive_cluster(mapa_shared(released_bar(t & 1u), 0));
+          __syncwarp();
+        }
+      }
     }
     __syncwarp();
   } else {
-    const int q = warp & 3;
+    // two warps a lane quarter, every other 32 columns each
+    const int q = warp & 3, odd = (warp - 2) >> 2;
     uint32_t t = 0;
-    for (uint32_t u = cluster; u < units; u += clusters, ++t) {
-      const uint32_t b = t & 1u;
-      const Unit w = unit_at<MODE>(u, p, table);
-      if (!__all_sync(ALL, mbar_wait_bounded(acc_bar(b), (t >> 1) & 1u, limit, &abort_flag, 128))) {
-        if (lane == 0) give_up(kErrTimeoutEpilogue);
-        __syncwarp();
-        break;
-      }
-      tc_fence_after();
-      const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * MAX_ROWS;
+    bool ok = true;
+    for (uint32_t u = cluster; ok && u < units; u += clusters) {
+      const Unit w = unit_at<MODE, ROWS>(u, p, table);
+      const int kbs = (w.sum + BK - 1) / BK;
+      const int fillings = LONG ? max(1, (kbs + S::SEGMENT - 1) / S::SEGMENT) : 1;
       const int feature = w.f0 + static_cast<int>(rank) * HALF + q * 32 + lane;
-#pragma unroll 1
-      for (int at = 0; at < w.count; at += 32) {
-        uint32_t r[32];
-        tmem_ld_32cols(taddr + at, r);
-        tmem_ld_wait();
-        if (w.sum == 0) {  // no terms: the accumulator was not written
-#pragma unroll
-          for (int j = 0; j < 32; ++j) r[j] = 0;
+      constexpr int HELD = LONG ? ROWS / 64 : 1;
+      float held[HELD][32];
+      for (int i = 0; i < fillings; ++i, ++t) {
+        const uint32_t b = t & 1u;
+        if (!__all_sync(ALL,
+                        mbar_wait_bounded(acc_bar(b), (t >> 1) & 1u, limit, &abort_flag, 64))) {
+          if (lane == 0) give_up(kErrTimeoutEpilogue);
+          __syncwarp();
+          ok = false;
+          break;
         }
-        if (at + 32 >= w.count) {  // all read
+        tc_fence_after();
+        const uint32_t taddr = tmem + (static_cast<uint32_t>(q * 32) << 16) + b * ROWS;
+        auto release = [&] {
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa_shared(released_bar(b), 0));
+          if (lane == 0) mbar_arrive(leader ? released_bar(b) : read_bar(b));
+        };
+        if constexpr (LONG) {
+#pragma unroll
+          for (int c = 0; c < HELD; ++c) {
+            const int at = (2 * c + odd) * 32;
+            if (at < w.count) {
+              uint32_t r[32];
+              tmem_ld_32cols(taddr + at, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) {
+                const float v = w.sum ? __uint_as_float(r[j]) : 0.f;
+                held[c][j] = i ? held[c][j] + v : v;
+              }
+            }
+          }
+          release();
+          if (i + 1 == fillings) {
+#pragma unroll
+            for (int c = 0; c < HELD; ++c) {
+              const int at = (2 * c + odd) * 32;
+              if (at < w.count)
+                store_chunk<MODE, LONG>(reinterpret_cast<uint32_t(&)[32]>(held[c]), p, w, at,
+                                        feature, lane);
+            }
+          }
+        } else {
+          if (32 * odd >= w.count) release();
+#pragma unroll 1
+          for (int at = 32 * odd; at < w.count; at += 64) {
+            uint32_t r[32];
+            tmem_ld_32cols(taddr + at, r);
+            tmem_ld_wait();
+            if (w.sum == 0) {  // no terms: the accumulator was not written
+#pragma unroll
+              for (int j = 0; j < 32; ++j) r[j] = 0;
+            }
+            if (at + 64 >= w.count) release();
+            store_chunk<MODE, LONG>(r, p, w, at, feature, lane);
+          }
         }
-        store_chunk<MODE>(r, p, w, at, feature, lane);
       }
-      if (w.count <= 0 && lane == 0) mbar_arrive_cluster(mapa_shared(released_bar(b), 0));
     }
   }
 
@@ -516,63 +666,97 @@ __global__ void __launch_bounds__(THREADS, 1)
   cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc_pair(tmem, TMEM_COLS);
+    tmem_dealloc_pair(tmem, S::TMEM_COLS);
   }
 }
 
-// An operand whose rows TMA cannot read, row by row into scratch with a pitch of
-// whole 16 bytes; parts (experts) without rows of tokens are left out where
-// `offsets` is given.
-__global__ void repack_kernel(const uint16_t* src, int64_t rows, int64_t cols, int64_t ld,
-                              int64_t stride, const int32_t* offsets, uint16_t* dst,
-                              int64_t dst_ld) {
+// Rows as TMA reads them, into scratch with a pitch of whole 16 bytes: of the parts
+// (experts) that have rows of tokens where `offsets` is given, or those that `index`
+// over `top` picks (zeros where it picks none).  A warp takes a row.
+template <typename Word>
+__global__ void __launch_bounds__(256)
+    rows_kernel(const uint16_t* src, int64_t src_rows, int64_t cols, int64_t ld, int64_t stride,
+                const int32_t* offsets, const int32_t* index, int top, uint16_t* dst,
+                int64_t rows, int64_t dst_ld) {
+  grid_dependency_wait();
   const int64_t part = blockIdx.y;
   if (offsets && offsets[part + 1] <= offsets[part]) return;
   src += part * stride;
   dst += part * rows * dst_ld;
-  const int lanes = 32, warp = threadIdx.x / lanes, lane = threadIdx.x % lanes;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (blockDim.x / lanes);
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (blockDim.x / lanes) + warp; r < rows;
-       r += warps)
-    for (int64_t c = lane; c < cols; c += lanes) dst[r * dst_ld + c] = src[r * ld + c];
+  constexpr int EACH = sizeof(Word) / 2, DEEP = sizeof(Word) == 16 ? 4 : 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t words = cols / EACH;  // (a whole number)
+  for (int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + warp; q < rows; q += gridDim.x * 8) {
+    const int64_t r = index ? picked_row(index[q], top, static_cast<int>(src_rows)) : q;
+    const Word* from = reinterpret_cast<const Word*>(src + r * ld);
+    Word* to = reinterpret_cast<Word*>(dst + q * dst_ld);
+    for (int64_t c = lane; c < words; c += 32 * DEEP) {
+      Word v[DEEP];
+#pragma unroll
+      for (int i = 0; i < DEEP; ++i) {
+        v[i] = Word{};
+        if (r >= 0 && c + 32 * i < words) v[i] = from[c + 32 * i];
+      }
+#pragma unroll
+      for (int i = 0; i < DEEP; ++i)
+        if (c + 32 * i < words) to[c + 32 * i] = v[i];
+    }
+  }
 }
 
 struct Ready {
   const void* p;
-  int64_t ld, stride;
+  int64_t rows, ld, stride;
 };
 
-// The operand as TMA reads it: itself, or a copy at *scratch, which moves on.
+// The operand as TMA reads it: itself, or a copy at *scratch, which moves on.  index:
+// `picked` rows of it, or null.
 cudaError_t ready(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
-                  int64_t stride, const int32_t* offsets, char** scratch, cudaStream_t s,
-                  Ready* out) {
-  if (repack_bytes(p, parts, rows, cols, ld, stride) == 0) {
-    *out = {p, ld, stride};
+                  int64_t stride, const int32_t* offsets, const int32_t* index, int64_t top,
+                  int64_t picked, char** scratch, cudaStream_t s, Ready* out) {
+  const int64_t bytes = operand_bytes(p, parts, rows, cols, ld, stride, index ? picked : 0);
+  if (bytes == 0) {
+    *out = {p, rows, ld, stride};
     return cudaSuccess;
   }
-  const int64_t dst_ld = (cols + 7) / 8 * 8;
+  const int64_t dst_ld = (cols + 7) / 8 * 8, dst_rows = index ? picked : rows;
   uint16_t* dst = reinterpret_cast<uint16_t*>(*scratch);
-  *out = {dst, dst_ld, rows * dst_ld};
-  *scratch += repack_bytes(p, parts, rows, cols, ld, stride);
-  const int64_t blocks = (rows + 7) / 8;
-  const dim3 grid(static_cast<unsigned>(blocks < 1024 ? blocks : 1024),
-                  static_cast<unsigned>(parts));
-  repack_kernel<<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(p), rows, cols, ld, stride,
-                                     offsets, dst, dst_ld);
+  *out = {dst, dst_rows, dst_ld, dst_rows * dst_ld};
+  *scratch += bytes;
+  const int64_t blocks = (dst_rows + 7) / 8;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096),
+                     static_cast<unsigned>(parts));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool vectors = reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 &&
+                       stride % 8 == 0 && cols % 8 == 0;
+  auto kern = vectors ? rows_kernel<uint4> : rows_kernel<uint16_t>;
   note_launch();
-  return cudaGetLastError();
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kern, static_cast<const uint16_t*>(p), rows, cols, ld, stride,
+                         offsets, index, static_cast<int>(top), dst, dst_rows, dst_ld);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
-template <int MODE, bool GATHER>
-cudaError_t launch_t(const CUtensorMap (&m)[3], const Params& p, cudaLaunchConfig_t cfg) {
-  auto kern = routed_pair_kernel<MODE, GATHER>;
+template <int MODE, bool INDEXED, bool LONG>
+cudaError_t launch_t(const CUtensorMap (&m)[6], const Params& p, cudaLaunchConfig_t cfg) {
+  using S = Shape<LONG>;
+  auto kern = routed_pair_kernel<MODE, INDEXED, LONG>;
+  cfg.blockDim = dim3(THREADS);
+  cfg.dynamicSmemBytes = S::SMEM;
   static int most[64];  // by device; under the library's lock
   int device = 0;
   cudaError_t e = cudaGetDevice(&device);
   if (e != cudaSuccess) return e;
   int clusters = device < 64 ? most[device] : 0;
   if (!clusters) {
-    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM)) !=
+    if ((e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, S::SMEM)) !=
         cudaSuccess)
       return e;
     cfg.numAttrs = 1;
@@ -583,30 +767,32 @@ cudaError_t launch_t(const CUtensorMap (&m)[3], const Params& p, cudaLaunchConfi
   // As many units as there can be at most: every row tile but one of an expert's full.
   const int64_t tiles = MODE == GRADIENT
                             ? static_cast<int64_t>(p.E) * p.k_tiles
-                            : (p.rows < p.E ? p.rows : p.E) + p.rows / MAX_ROWS;
+                            : (p.rows < p.E ? p.rows : p.E) + p.rows / S::ROWS;
   const int64_t units = tiles * p.f_tiles;
   if (units > 0x3fffffff) return cudaErrorInvalidConfiguration;
   if (units < clusters) clusters = static_cast<int>(units);
   cfg.gridDim = dim3(2 * clusters);
   cfg.numAttrs = 2;
-  note_main_kernel(MODE == GRADIENT     ? "routed_pair_kernel<gradient>"
-                   : MODE == TRANSPOSED ? "routed_pair_kernel<transposed>"
-                                        : "routed_pair_kernel<product>",
-                   2 * clusters, static_cast<int>(units));
-  e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], p);
+  char name[64];
+  snprintf(name, sizeof(name), "routed_pair_kernel<%s%s%s>",
+           MODE == GRADIENT ? "gradient" : MODE == TRANSPOSED ? "transposed" : "product",
+           INDEXED ? ",indexed" : "", LONG ? ",long" : "");
+  note_main_kernel(name, 2 * clusters, static_cast<int>(units));
+  e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 }  // namespace
 
-int64_t repack_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
-                     int64_t stride) {
+int64_t operand_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
+                      int64_t stride, int64_t picked) {
   if (rows == 0 || cols == 0 ||
-      (reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || ld % 8 == 0) &&
+      (picked == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0 && (rows == 1 || ld % 8 == 0) &&
        (parts == 1 || stride % 8 == 0)))
     return 0;
   int64_t n;
-  if (__builtin_mul_overflow(parts * rows, (cols + 7) / 8 * 16, &n) || n > INT64_MAX - 255)
+  if (__builtin_mul_overflow(picked ? picked : parts * rows, (cols + 7) / 8 * 16, &n) ||
+      n > INT64_MAX - 255)
     return -1;
   return (n + 255) / 256 * 256;
 }
@@ -614,7 +800,7 @@ int64_t repack_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, i
 cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl& ctl,
                            cudaStream_t s) {
   const bool gradient = a.kind == ProductKind::gradient;
-  Params p;
+  Params p = {};
   p.offsets = a.offsets;
   p.gather = a.gather;
   p.scatter = a.scatter;
@@ -632,8 +818,10 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
   if (none && gradient) p.rows = 0;
   p.N = static_cast<int32_t>(a.N);
   p.top = static_cast<int32_t>(a.top);
+  const bool wide = a.out_dtype == MHR_F32;
+  const int tile_rows = wide ? 128 : 256;
   p.f_tiles = static_cast<int32_t>((a.N + TILE_F - 1) / TILE_F);
-  p.k_tiles = static_cast<int32_t>((a.K + MAX_ROWS - 1) / MAX_ROWS);
+  p.k_tiles = static_cast<int32_t>((a.K + tile_rows - 1) / tile_rows);
   p.kind = a.dtype == MHR_BF16 ? 1 : 0;
   p.out_dtype = a.out_dtype;
   p.pairs = a.out_dtype != MHR_F32 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0 &&
@@ -650,37 +838,39 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(THREADS);
-  cfg.dynamicSmemBytes = SMEM;
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
   cfg.gridDim = dim3(2 * (ctl.sm_count / 2));
 
-  CUtensorMap m[3] = {};
+  CUtensorMap m[6] = {};
   const auto type = a.dtype == MHR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
   if (!none) {
     char* at = static_cast<char*>(scratch);
     Ready x, w;
-    cudaError_t e = ready(a.x, 1, a.x_rows, a.K, a.ldx, 0, nullptr, &at, s, &x);
+    const bool in_order = a.gather && (gradient || a.rows > FEW_ROWS);
+    cudaError_t e = ready(a.x, 1, a.x_rows, a.K, a.ldx, 0, nullptr, in_order ? a.gather : nullptr,
+                          a.top, a.rows, &at, s, &x);
     if (e != cudaSuccess) return e;
-    auto rows_map = [&](CUtensorMap* map, const Ready& r, int64_t cols, int64_t rows,
-                        uint32_t box) {
+    if (in_order) p.gather = nullptr;
+    auto rows_map = [&](int i, const Ready& r, int64_t cols, uint32_t box) {
       // (one row has no pitch of its own to go by)
-      const int64_t ld = rows == 1 ? (cols + 7) / 8 * 8 : r.ld;
-      return encode_tmap_2d(map, type, r.p, cols, rows, ld * 2, 64, box, swizzle) == CUDA_SUCCESS;
+      const int64_t ld = r.rows == 1 ? (cols + 7) / 8 * 8 : r.ld;
+      return encode_tmap_2d(&m[i], type, r.p, cols, r.rows, ld * 2, 64, box, swizzle) ==
+             CUDA_SUCCESS;
     };
     bool ok = true;
     if (gradient) {
-      e = ready(a.w, 1, a.out_rows, a.N, a.ldw, 0, nullptr, &at, s, &w);
+      e = ready(a.w, 1, a.out_rows, a.N, a.ldw, 0, nullptr, a.scatter, 1, a.rows, &at, s, &w);
       if (e != cudaSuccess) return e;
-      ok = rows_map(&m[0], w, a.N, a.out_rows, 1) && rows_map(&m[1], x, a.K, a.x_rows, 1);
+      p.scatter = nullptr;
+      ok = rows_map(0, w, a.N, 64) && rows_map(1, x, a.K, 64) && rows_map(2, x, a.K, 16) &&
+           rows_map(3, w, a.N, 16) && rows_map(4, w, a.N, 1) && rows_map(5, x, a.K, 1);
     } else {
       const bool t = a.kind == ProductKind::transposed;
       const int64_t rows = t ? a.N : a.K, cols = t ? a.K : a.N;
-      e = ready(a.w, a.E, rows, cols, a.ldw, a.stride_w, a.offsets, &at, s, &w);
+      e = ready(a.w, a.E, rows, cols, a.ldw, a.stride_w, a.offsets, nullptr, 1, 0, &at, s, &w);
       if (e != cudaSuccess) return e;
       const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(rows),
                                 static_cast<uint64_t>(a.E)};
@@ -689,19 +879,24 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
       const uint64_t pitch[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(stride) * 2};
       const uint32_t box[3] = {64, t ? 128u : 64u, 1};
       ok = encode_tmap_3d(&m[0], type, w.p, dims, pitch, box, swizzle) == CUDA_SUCCESS &&
-           rows_map(&m[1], x, a.K, a.x_rows, a.gather ? 1 : 8) &&
-           (a.gather || rows_map(&m[2], x, a.K, a.x_rows, 128));
+           rows_map(1, x, a.K, tile_rows / 2) && rows_map(2, x, a.K, p.gather ? 1 : 8);
     }
     if (!ok) return cudaErrorInvalidValue;
   }
   MainKernelEvents ev(s);
+  auto by_width = [&](auto mode, auto indexed) {
+    constexpr int MODE = decltype(mode)::value;
+    constexpr bool INDEXED = decltype(indexed)::value;
+    return wide ? launch_t<MODE, INDEXED, true>(m, p, cfg) : launch_t<MODE, INDEXED, false>(m, p, cfg);
+  };
+  auto by_index = [&](auto mode) {
+    return p.gather ? by_width(mode, std::true_type{}) : by_width(mode, std::false_type{});
+  };
   switch (a.kind) {
-    case ProductKind::gradient: return launch_t<GRADIENT, true>(m, p, cfg);
-    case ProductKind::transposed:
-      return a.gather ? launch_t<TRANSPOSED, true>(m, p, cfg)
-                      : launch_t<TRANSPOSED, false>(m, p, cfg);
-    default:
-      return a.gather ? launch_t<PRODUCT, true>(m, p, cfg) : launch_t<PRODUCT, false>(m, p, cfg);
+    case ProductKind::gradient:
+      return by_width(std::integral_constant<int, GRADIENT>{}, std::false_type{});
+    case ProductKind::transposed: return by_index(std::integral_constant<int, TRANSPOSED>{});
+    default: return by_index(std::integral_constant<int, PRODUCT>{});
   }
 }
 

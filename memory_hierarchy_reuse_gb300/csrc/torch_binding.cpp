@@ -29,7 +29,8 @@ decltype(&gemm_mxfp4_moe) g_moe;
 decltype(&gemm_routed_choose) g_choose;
 decltype(&gemm_routed_choose_grad) g_choose_grad;
 decltype(&gemm_routed_sort) g_sort;
-decltype(&gemm_routed_scratch_bytes) g_scratch_bytes;
+decltype(&gemm_routed_product_scratch) g_product_scratch;
+decltype(&gemm_routed_weight_grad_scratch) g_weight_grad_scratch;
 decltype(&gemm_routed_product) g_routed_product;
 decltype(&gemm_routed_weight_grad) g_weight_grad;
 decltype(&gemm_routed_adapters_scratch) g_adapters_scratch;
@@ -510,10 +511,10 @@ PyObject* experts(PyObject* const* v, Py_ssize_t n) {
   if (po.cols != N || (!scatter && po.rows != rows))
     raise(PyExc_TypeError, "%sout must be of shape (rows, N)");
   void* stream = stream_of(v[9], device);
-  const int64_t need_x = g_scratch_bytes(x.data_ptr(), 1, px.rows, px.cols, px.ld, 0);
-  const int64_t need_w =
-      pw.parts ? g_scratch_bytes(w.data_ptr(), pw.parts, pw.rows, pw.cols, pw.ld, pw.stride) : 0;
-  const int64_t need = (need_x > 0 ? need_x : 0) + (need_w > 0 ? need_w : 0);
+  const int64_t bytes = g_product_scratch(x.data_ptr(), px.rows, px.ld, gather != nullptr,
+                                          w.data_ptr(), pw.ld, pw.stride, transposed, pw.parts,
+                                          rows, K, N);
+  const int64_t need = bytes > 0 ? bytes : 0;  // (the call says what -1 is about)
   at::Tensor scratch;
   if (need) scratch = scratch_for(need, device, stream);
   run("gemm_routed_product", device, [&] {
@@ -557,9 +558,10 @@ PyObject* experts_grad(PyObject* const* v, Py_ssize_t n) {
   if (po.parts != E || po.rows != px.cols || po.cols != pg.cols)
     raise(PyExc_TypeError, "%sout must be of shape (experts, K, N)");
   void* stream = stream_of(v[8], device);
-  const int64_t need_x = g_scratch_bytes(x.data_ptr(), 1, px.rows, px.cols, px.ld, 0);
-  const int64_t need_g = g_scratch_bytes(grad.data_ptr(), 1, pg.rows, pg.cols, pg.ld, 0);
-  const int64_t need = (need_x > 0 ? need_x : 0) + (need_g > 0 ? need_g : 0);
+  const int64_t bytes =
+      g_weight_grad_scratch(x.data_ptr(), px.rows, px.ld, gather != nullptr, grad.data_ptr(),
+                            pg.rows, pg.ld, scatter != nullptr, rows, px.cols, pg.cols);
+  const int64_t need = bytes > 0 ? bytes : 0;
   at::Tensor scratch;
   if (need) scratch = scratch_for(need, device, stream);
   run("gemm_routed_weight_grad", device, [&] {
@@ -626,18 +628,19 @@ PyObject* adapters(PyObject* const* v, Py_ssize_t n) {
 
 // init_routed(addresses of the entry points)
 PyObject* init_routed(PyObject* const* a, Py_ssize_t n) {
-  count(n, 8);
-  void* p[8];
-  for (int i = 0; i < 8; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
+  count(n, 9);
+  void* p[9];
+  for (int i = 0; i < 9; ++i) p[i] = PyLong_AsVoidPtr(a[i]);
   if (PyErr_Occurred()) throw Raised{};
   g_choose = reinterpret_cast<decltype(g_choose)>(p[0]);
   g_choose_grad = reinterpret_cast<decltype(g_choose_grad)>(p[1]);
   g_sort = reinterpret_cast<decltype(g_sort)>(p[2]);
-  g_scratch_bytes = reinterpret_cast<decltype(g_scratch_bytes)>(p[3]);
+  g_product_scratch = reinterpret_cast<decltype(g_product_scratch)>(p[3]);
   g_routed_product = reinterpret_cast<decltype(g_routed_product)>(p[4]);
-  g_weight_grad = reinterpret_cast<decltype(g_weight_grad)>(p[5]);
-  g_adapters_scratch = reinterpret_cast<decltype(g_adapters_scratch)>(p[6]);
-  g_adapters = reinterpret_cast<decltype(g_adapters)>(p[7]);
+  g_weight_grad_scratch = reinterpret_cast<decltype(g_weight_grad_scratch)>(p[5]);
+  g_weight_grad = reinterpret_cast<decltype(g_weight_grad)>(p[6]);
+  g_adapters_scratch = reinterpret_cast<decltype(g_adapters_scratch)>(p[7]);
+  g_adapters = reinterpret_cast<decltype(g_adapters)>(p[8]);
   Py_RETURN_NONE;
 }
 

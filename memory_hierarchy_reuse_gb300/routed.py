@@ -26,8 +26,10 @@ _GROUP_SCORES = {"max": 0, "top2": 1}
 _lib = load()
 _torch_binding.init_routed(*(ctypes.cast(f, ctypes.c_void_p).value
                              for f in (_lib.gemm_routed_choose, _lib.gemm_routed_choose_grad,
-                                       _lib.gemm_routed_sort, _lib.gemm_routed_scratch_bytes,
-                                       _lib.gemm_routed_product, _lib.gemm_routed_weight_grad,
+                                       _lib.gemm_routed_sort, _lib.gemm_routed_product_scratch,
+                                       _lib.gemm_routed_product,
+                                       _lib.gemm_routed_weight_grad_scratch,
+                                       _lib.gemm_routed_weight_grad,
                                        _lib.gemm_routed_adapters_scratch,
                                        _lib.gemm_routed_adapters)))
 

@@ -93,16 +93,30 @@ def test_weight_grad_refusals(mhr):
     assert f(*dict(args, K=0, out=None).values()) == mhr.MHR_OK
 
 
-def test_scratch_bytes(mhr):
-    f = mhr.load().gemm_routed_scratch_bytes
-    assert f(P, 1, 20, 64, 64, 0) == 0 and f(P, 4, 20, 64, 72, 72 * 20) == 0
-    assert f(P, 1, 1, 7, 7, 0) == 0          # one row has no pitch
-    assert f(P, 1, 20, 63, 63, 0) == 20 * 128
-    assert f(P + 2, 1, 20, 64, 64, 0) == 20 * 128
-    assert f(P, 3, 20, 63, 63, 63 * 20) == 60 * 128
-    assert f(P, 1, 0, 63, 63, 0) == 0
-    assert f(P, 0, 20, 63, 63, 0) == -1 and f(P, 1, -1, 3, 3, 0) == -1
-    assert f(P, 1024, 1 << 30, (1 << 31) - 1024, (1 << 31) - 1023, 1 << 62) == -1
+def test_scratch(mhr):
+    f = mhr.load().gemm_routed_product_scratch
+    args = dict(x=P, x_rows=20, ldx=64, gathered=0, w=Q, ldw=64, stride_w=4096, transposed=0, E=3,
+                rows=20, K=64, N=64)
+    for change, bytes_ in [
+            (dict(), 0), (dict(ldx=72), 0), (dict(ldx=65), 20 * 128), (dict(x=P + 2), 20 * 128),
+            (dict(x_rows=1, ldx=65, gathered=1), 0),                 # one row has no pitch
+            (dict(gathered=1), 0), (dict(gathered=1, rows=257), 258 * 128),
+            (dict(gathered=1, rows=300, ldx=65), 300 * 128), (dict(w=Q + 2), 3 * 64 * 128),
+            (dict(ldw=66, stride_w=66 * 64), 3 * 64 * 128), (dict(stride_w=4100), 3 * 64 * 128),
+            (dict(E=1, stride_w=1), 0), (dict(N=60, ldw=65), 3 * 64 * 128),
+            (dict(transposed=1, N=60, ldw=65), 3 * 60 * 128), (dict(ldx=65, w=Q + 2), 212 * 128),
+            (dict(rows=0, ldx=65), 0), (dict(K=0, ldx=65), 0), (dict(E=0), -1), (dict(rows=-1), -1),
+            (dict(gathered=1, rows=(1 << 31) - 512, K=(1 << 31) - 512, N=(1 << 31) - 512, E=1024,
+                  w=Q + 2), -1)]:
+        assert f(*dict(args, **change).values()) == bytes_, change
+    f = mhr.load().gemm_routed_weight_grad_scratch
+    args = dict(x=P, x_rows=20, ldx=64, gathered=0, grad=Q, grad_rows=20, ldg=64, scattered=0,
+                rows=20, K=64, N=64)
+    for change, bytes_ in [(dict(), 0), (dict(gathered=1), 20 * 128),
+                           (dict(gathered=1, scattered=1, rows=50), 100 * 128),
+                           (dict(ldg=65), 20 * 128), (dict(rows=0, gathered=1), 0),
+                           (dict(K=-1), -1)]:
+        assert f(*dict(args, **change).values()) == bytes_, change
 
 
 def test_adapters_refusals(mhr):
