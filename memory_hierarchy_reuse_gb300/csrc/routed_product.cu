@@ -59,9 +59,10 @@ struct Shape {
   static constexpr int ROWS = LONG ? 128 : 256;            // rows of a pair's tile, at most
   static constexpr int B_BYTES = ROWS / 2 * BK * 2;        // this CTA's half of them
   static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;    // 24 or 32 KB
-  static constexpr int STAGES = LONG ? 8 : 6;
-  static constexpr int SEGMENT = LONG ? 4 : 1 << 30;       // stages an accumulator takes
-  static constexpr int SMEM = STAGES * STAGE_BYTES + 1024;
+  static constexpr int STAGES = LONG ? 7 : 6;
+  static constexpr int SEGMENT = LONG ? 6 : 1 << 30;       // stages an accumulator takes
+  static constexpr int PIECE_BYTES = 32 * 32 * (LONG ? 4 : 2);  // of an epilogue warp
+  static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * PIECE_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * ROWS;
 };
 
@@ -75,11 +76,21 @@ struct Params {
   int32_t K, N, top;       // K: columns of x
   int32_t f_tiles, k_tiles;  // tiles of features; of x's features (gradient)
   int32_t kind;            // 0 fp16, 1 bf16
-  int32_t out_dtype, pairs;  // pairs: two features of 16 bits at once
+  int32_t out_dtype;
+  int32_t out_tma, pairs;  // whole chunks by TMA; else two features of 16 bits at once
   uint32_t* status;
   uint64_t wait_limit_ns;
   int32_t inject_stall;
 };
+
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x,
+                                             int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(map)),
+      "r"(src), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 
 // Four rows r of 64 columns from x on, into 512 bytes of this CTA's shared memory.
 __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap* map,
@@ -92,6 +103,15 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       "r"(r[2]), "r"(r[3])
       : "memory");
 }
+
+// The features' side in boxes of 16, 32 and 64 rows (gradient), or whatever a product's
+// weights take (w[2]); x in boxes of 16 to 128 rows; either in single rows for a gather.
+// A TMA instruction takes some 60 cycles however little it brings, so rows come in a few
+// boxes of powers of two (4096 tokens, 8 of 128 experts of 1536 x 4096 with skewed
+// counts: 562 us with boxes of 8 rows).
+struct Maps {
+  CUtensorMap w[3], x[4], w1, x1, out;  // out: in boxes of an epilogue warp's chunk
+};
 
 // A unit of work: one tile.
 struct Unit {
@@ -109,6 +129,15 @@ struct Table {
   const int32_t* lo;
   const int32_t* n;
 };
+
+// n / d; of n that a float holds, by its quotient, which is off by one at most.
+__device__ __forceinline__ uint32_t divide(uint32_t n, uint32_t d) {
+  if (n >= 1u << 22 || d == 0) return d ? n / d : 0;
+  uint32_t q = __float2uint_rz(__fdividef(static_cast<float>(n), static_cast<float>(d)));
+  if (q * d > n) --q;
+  if (n - q * d >= d) ++q;
+  return q;
+}
 
 template <int ROWS>
 __device__ __forceinline__ int row_tiles(int n) {
@@ -134,30 +163,35 @@ __device__ __forceinline__ int cost_class(int n) {
   return tile_rows<ROWS>(n) * CLASSES / ROWS - 1;
 }
 
+// Unit u, found by a whole warp.
 template <int MODE, int ROWS>
 __device__ __forceinline__ Unit unit_at(uint32_t u, const Params& p, const Table& t) {
-  int i = 0;  // the last place whose first unit is at most u
-  for (int end = p.E; end - i > 1;) {
-    const int mid = (i + end) >> 1;
-    if (t.parts[mid] <= u)
-      i = mid;
-    else
-      end = mid;
-  }
+  // the last place whose first unit is at most u: of every step-th, then of those between
+  const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
+  auto last = [&](int from, int each) {
+    const int at = from + lane * each;
+    const bool in = at < p.E && (each > 1 || step == 1 || lane < step);
+    return from + (__popc(__ballot_sync(ALL, in && t.parts[at] <= u)) - 1) * each;
+  };
+  int i = 0;
+  if (step > 1) i = last(0, step);
+  i = last(i, 1);
   const int e = t.expert[i];
   Unit w;
   const uint32_t r = u - t.parts[i];
   w.expert = e;
   if constexpr (MODE == GRADIENT) {
-    w.f0 = static_cast<int>(r % p.f_tiles) * TILE_F;
-    w.first = static_cast<int>(r / p.f_tiles) * ROWS;
+    const uint32_t q = divide(r, p.f_tiles);
+    w.f0 = static_cast<int>(r - q * p.f_tiles) * TILE_F;
+    w.first = static_cast<int>(q) * ROWS;
     w.count = min(ROWS, p.K - w.first);
     w.sum0 = t.lo[e];
     w.sum = t.n[e];
   } else {
     const int tiles = row_tiles<ROWS>(t.n[e]), size = tile_rows<ROWS>(t.n[e]);
-    const int at = static_cast<int>(r % tiles) * size;
-    w.f0 = static_cast<int>(r / tiles) * TILE_F;
+    const uint32_t q = divide(r, tiles);
+    const int at = static_cast<int>(r - q * tiles) * size;
+    w.f0 = static_cast<int>(q) * TILE_F;
     w.first = t.lo[e] + at;
     w.count = max(0, min(size, t.n[e] - at));
     w.sum0 = 0;
@@ -173,9 +207,10 @@ __device__ __forceinline__ int picked_row(int index, int top, int rows) {
   return r < rows ? r : -1;
 }
 
-__device__ __forceinline__ uint32_t pack16(int dtype, uint32_t lo, uint32_t hi) {
+template <int DTYPE>
+__device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi) {
   const float a = __uint_as_float(lo), b = __uint_as_float(hi);
-  if (dtype == MHR_BF16) {
+  if constexpr (DTYPE == MHR_BF16) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t*>(&v);
   }
@@ -184,66 +219,112 @@ __device__ __forceinline__ uint32_t pack16(int dtype, uint32_t lo, uint32_t hi) 
 }
 
 // 32 rows (columns of TMEM) of 32 features (lanes) to the output: of fp32 (WIDE), or of
-// 16 bits.  Values and rows first, then the stores, predicated: a branch a row made a
-// chunk take 2700 cycles, each of its shuffles waited for.
+// 16 bits.  Whole chunks by TMA from the warp's piece of shared memory: a store of a lane's
+// own values, or of 16 bytes a lane, holds the SM up 5 to 10 cycles for every 128 bytes.
+// No branch a row either way -- for the row, for the type, for the lane's parity -- which
+// cost 2700 cycles a chunk.
 template <int MODE, bool WIDE>
 __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Params& p,
+                                            const CUtensorMap* out_map, uint32_t piece,
                                             const Unit& w, int at, int feature, int lane) {
   using Word = std::conditional_t<WIDE, uint32_t, uint16_t>;
   Word* base = static_cast<Word*>(p.out);
   if constexpr (MODE == GRADIENT) base += w.expert * p.stride_o;
-  const int count = w.count - at;  // rows from here on
-  // `each` rows apart from row `from` on: f(row j of the chunk, where it starts, whether it is there)
-  auto rows = [&](int from, auto each, const auto& f) {
-    constexpr int EACH = decltype(each)::value;
-    if (MODE == GRADIENT || !p.scatter) {
-      Word* dst = base + (w.first + at + from) * p.ldo;
+  const int count = min(32, w.count - at);  // rows of this chunk
+  const bool scattered = MODE != GRADIENT && p.scatter;
+  const int first = w.first + at;
+  int mine = first + lane;  // lane j's row of the output, below 0 for none
+  if (scattered) mine = lane < count ? picked_row(p.scatter[first + lane], 1, p.out_rows) : -1;
+  // Pairs: neighbouring lanes exchange, the even one gets two features of row j, the odd
+  // one of row j + 1, so that a store of the warp is two runs of 64 bytes.
+  const bool pairs = !WIDE && p.pairs;  // (as where chunks go by TMA)
+  const int odd = pairs ? lane & 1 : 0, each = pairs ? 2 : 1, f = feature - odd;
+  uint32_t v[WIDE ? 1 : 16];
+  if constexpr (!WIDE) {
+    if (pairs) {
 #pragma unroll
-      for (int j = 0; j < 32; j += EACH) {
-        f(j, dst, j + from < count);
-        dst += EACH * p.ldo;
-      }
+      for (int j = 0; j < 32; j += 2) v[j / 2] = __shfl_xor_sync(ALL, odd ? r[j] : r[j + 1], 1);
+      auto pack = [&](auto dtype) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          const uint32_t lo = odd ? v[j / 2] : r[j], hi = odd ? r[j + 1] : v[j / 2];
+          v[j / 2] = pack16<decltype(dtype)::value>(lo, hi);
+        }
+      };
+      if (p.out_dtype == MHR_BF16)
+        pack(std::integral_constant<int, MHR_BF16>{});
+      else
+        pack(std::integral_constant<int, MHR_F16>{});
+    }
+  }
+  // (TMA clips at the tensor's ends; a product's next rows are another tile's)
+  if (p.out_tma && !scattered && (MODE == GRADIENT || count == 32)) {
+    if (lane == 0) bulk_wait_group_read<0>();  // the chunk before has left the piece
+    __syncwarp();
+    if constexpr (WIDE) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(piece + j * 128 + lane * 4), "r"(r[j])
+                     : "memory");
     } else {
-      const int mine = lane < count ? picked_row(p.scatter[w.first + at + lane], 1, p.out_rows) : -1;
 #pragma unroll
-      for (int j0 = 0; j0 < 32; j0 += 8 * EACH) {
-        int to[8];
+      for (int j = 0; j < 32; j += 2)
+        asm volatile("st.shared.b32 [%0], %1;" ::"r"(piece + (j + odd) * 64 + (lane - odd) * 2),
+                     "r"(v[j / 2])
+                     : "memory");
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && f < p.N) {
+      tma_store_3d(out_map, piece, f, first, MODE == GRADIENT ? w.expert : 0);
+      bulk_commit_group();
+    }
+    return;
+  }
+  if (WIDE || pairs) {
+    const bool in = f + each <= p.N;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) to[i] = __shfl_sync(ALL, mine, j0 + i * EACH + from);
+    for (int j0 = 0; j0 < 32; j0 += WIDE ? 8 : 16) {
+      int to[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) f(j0 + i * EACH, base + to[i] * p.ldo, to[i] >= 0);
+      for (int i = 0; i < 8; ++i) {
+        const int j = j0 + i * (WIDE ? 1 : 2);
+        to[i] = __shfl_sync(ALL, mine, j + odd);
+        if (j + odd >= count || !in) to[i] = -1;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        Word* dst = base + to[i] * p.ldo + f;
+        if (to[i] >= 0) {
+          if constexpr (WIDE)
+            *dst = r[j0 + i];
+          else
+            *reinterpret_cast<uint32_t*>(dst) = v[j0 / 2 + i];
+        }
       }
     }
-  };
-  const std::integral_constant<int, 1> one;
-  if constexpr (WIDE) {
-    const bool in = feature < p.N;
-    rows(0, one, [&](int j, Word* dst, bool there) {
-      if (there && in) dst[feature] = r[j];
-    });
-  } else if (p.pairs) {
-    // Neighbouring lanes exchange: the even one gets two features of row j, the odd
-    // one of row j + 1, so that a store of the warp is two whole runs of 64 bytes.
-    const int odd = lane & 1, f = feature - odd;
-    uint32_t v[16];
+    if constexpr (!WIDE) {
+      if (__any_sync(ALL, f + 1 == p.N)) {  // the last of an odd number of features
 #pragma unroll
-    for (int j = 0; j < 32; j += 2) {
-      const uint32_t other = __shfl_xor_sync(ALL, odd ? r[j] : r[j + 1], 1);
-      v[j / 2] = odd ? pack16(p.out_dtype, other, r[j + 1]) : pack16(p.out_dtype, r[j], other);
+        for (int i = 0; i < 16; ++i) {
+          const int to = __shfl_sync(ALL, mine, 2 * i + odd);
+          if (f + 1 == p.N && 2 * i + odd < count && to >= 0)
+            base[to * p.ldo + f] = static_cast<uint16_t>(v[i]);
+        }
+      }
     }
-    const bool both = f + 1 < p.N, one_in = f + 1 == p.N;
-    rows(odd, std::integral_constant<int, 2>{}, [&](int j, Word* dst, bool there) {
-      if (there && both) *reinterpret_cast<uint32_t*>(dst + f) = v[j / 2];
-    });
-    if (one_in)
-      rows(odd, std::integral_constant<int, 2>{}, [&](int j, Word* dst, bool there) {
-        if (there) dst[f] = static_cast<uint16_t>(v[j / 2]);
-      });
   } else {
     const bool in = feature < p.N;
-    rows(0, one, [&](int j, Word* dst, bool there) {
-      if (there && in) dst[feature] = static_cast<uint16_t>(pack16(p.out_dtype, r[j], r[j]));
-    });
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      const int to = __shfl_sync(ALL, mine, j);
+      if (j < count && to >= 0 && in) {
+        const float x = __uint_as_float(r[j]);
+        base[to * p.ldo + feature] = static_cast<Word>(
+            p.out_dtype == MHR_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x))
+                                    : __half_as_ushort(__float2half_rn(x)));
+      }
+    }
   }
 }
 
@@ -253,18 +334,9 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Param
 // Rank 1's epilogue hands an accumulator back to its own read[b], from where its warp 1,
 // idle otherwise, tells rank 0: an arrival that is released to the cluster waits for the
 // stores that its thread has under way.
-// tmW: the features' side (gradient: in boxes of 64 rows), tmX: the rows' in boxes of a
-// CTA's half of a whole tile (gradient: 64 rows), tmX8: in boxes of 8 rows, of one for a
-// gather (gradient: 16 rows).  Gradient only, for an expert's last rows: tmW16, in boxes
-// of 16 rows, and tmW1 and tmX1, for the gather.
 template <int MODE, bool INDEXED, bool LONG>
 __global__ void __launch_bounds__(THREADS, 1)
-    routed_pair_kernel(const __grid_constant__ CUtensorMap tmW,
-                       const __grid_constant__ CUtensorMap tmX,
-                       const __grid_constant__ CUtensorMap tmX8,
-                       const __grid_constant__ CUtensorMap tmW16,
-                       const __grid_constant__ CUtensorMap tmW1,
-                       const __grid_constant__ CUtensorMap tmX1, const Params p) {
+    routed_pair_kernel(const __grid_constant__ Maps maps, const Params p) {
   using S = Shape<LONG>;
   constexpr int STAGES = S::STAGES, ROWS = S::ROWS, STAGE_BYTES = S::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
@@ -309,9 +381,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     peer_loaded = 0;
     fence_mbar_init();
     if (p.K > 0) {
-      tma_prefetch_desc(&tmW);
-      if (!INDEXED) tma_prefetch_desc(&tmX);
-      if (MODE != GRADIENT) tma_prefetch_desc(&tmX8);
+      tma_prefetch_desc(&maps.w[2]);
+      for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.x[i]);
     }
   }
   if (warp == 1) {
@@ -423,42 +494,43 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < BOXES; ++i)
-                  tma_load_2d_pair(st + i * BOX, i < 2 ? &tmW : &tmX, fb,
+                  tma_load_2d_pair(st + i * BOX, i < 2 ? &maps.w[2] : &maps.x[2], fb,
                                    i < 2 ? f + 64 * i : mine + 64 * (i - 2), pos);
               }
             } else {
-              // An expert's last rows: sixteen at a time, and the last of them by the
-              // gather, which ends in zeros and not in the next expert's rows.
-              const int whole = rows / 16;
-              if (lane < BOXES * whole) {
-                const int i = lane % BOXES, g = lane / BOXES;
-                tma_load_2d_pair(st + i * BOX + g * 2048, i < 2 ? &tmW16 : &tmX8, fb,
-                                 i < 2 ? f + 64 * i : mine + 64 * (i - 2), pos + 16 * g);
+              // An expert's last rows: in boxes, and the last of sixteen by the gather,
+              // which ends in zeros and not in the next expert's rows.
+              const int whole = rows & ~15;
+              const int i = lane % BOXES, g = lane / BOXES;
+              const int column = i < 2 ? f + 64 * i : mine + 64 * (i - 2);
+              if (g < 2 && (whole & (16 << g))) {
+                const int at = whole & ~((32 << g) - 1);  // behind the larger box
+                tma_load_2d_pair(st + i * BOX + at * 128, i < 2 ? &maps.w[g] : &maps.x[g], fb,
+                                 column, pos + at);
               }
-              if (read > 16 * whole && lane < 4 * BOXES) {
-                const int i = lane % BOXES, g = 16 * whole + 4 * (lane / BOXES);
+              if (read > whole && g < 4) {
+                const int at = whole + 4 * g;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = g + j < rows ? pos + g + j : p.rows;
-                tma_gather4_pair(st + i * BOX + g * 128, i < 2 ? &tmW1 : &tmX1, fb,
-                                 i < 2 ? f + 64 * i : mine + 64 * (i - 2), r);
+                for (int j = 0; j < 4; ++j) r[j] = at + j < rows ? pos + at + j : p.rows;
+                tma_gather4_pair(st + i * BOX + at * 128, i < 2 ? &maps.w1 : &maps.x1, fb, column,
+                                 r);
               }
             }
           } else {
             if (elect_one()) {
               if constexpr (MODE == PRODUCT) {
-                tma_load_3d_pair(st, &tmW, fb, f, kb * BK, w.expert);
-                tma_load_3d_pair(st + BOX, &tmW, fb, f + 64, kb * BK, w.expert);
+                tma_load_3d_pair(st, &maps.w[2], fb, f, kb * BK, w.expert);
+                tma_load_3d_pair(st + BOX, &maps.w[2], fb, f + 64, kb * BK, w.expert);
               } else {
-                tma_load_3d_pair(st, &tmW, fb, kb * BK, f, w.expert);
+                tma_load_3d_pair(st, &maps.w[2], fb, kb * BK, f, w.expert);
               }
-              if (!INDEXED && half == ROWS / 2)
-                tma_load_2d_pair(st + A_BYTES, &tmX, fb, kb * BK, mine);
             }
             if constexpr (INDEXED) {
               if (4 * lane < half)
-                tma_gather4_pair(st + A_BYTES + lane * 512, &tmX8, fb, kb * BK, r);
-            } else if (half < ROWS / 2 && 8 * lane < half) {
-              tma_load_2d_pair(st + A_BYTES + lane * 1024, &tmX8, fb, kb * BK, mine + 8 * lane);
+                tma_gather4_pair(st + A_BYTES + lane * 512, &maps.x1, fb, kb * BK, r);
+            } else if (lane < 4 && (half & (16 << lane))) {
+              const int at = half & ~((32 << lane) - 1);  // behind the larger boxes
+              tma_load_2d_pair(st + A_BYTES + at * 128, &maps.x[lane], fb, kb * BK, mine + at);
             }
           }
         }
@@ -592,6 +664,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     // two warps a lane quarter, every other 32 columns each
     const int q = warp & 3, odd = (warp - 2) >> 2;
+    const uint32_t piece = sbase + STAGES * STAGE_BYTES + (warp - 2) * S::PIECE_BYTES;
     uint32_t t = 0;
     bool ok = true;
     for (uint32_t u = cluster; ok && u < units; u += clusters) {
@@ -638,8 +711,8 @@ __global__ void __launch_bounds__(THREADS, 1)
             for (int c = 0; c < HELD; ++c) {
               const int at = (2 * c + odd) * 32;
               if (at < w.count)
-                store_chunk<MODE, LONG>(reinterpret_cast<uint32_t(&)[32]>(held[c]), p, w, at,
-                                        feature, lane);
+                store_chunk<MODE, LONG>(reinterpret_cast<uint32_t(&)[32]>(held[c]), p, &maps.out,
+                                        piece, w, at, feature, lane);
             }
           }
         } else {
@@ -654,11 +727,13 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int j = 0; j < 32; ++j) r[j] = 0;
             }
             if (at + 64 >= w.count) release();
-            store_chunk<MODE, LONG>(r, p, w, at, feature, lane);
+            store_chunk<MODE, LONG>(r, p, &maps.out, piece, w, at, feature, lane);
           }
         }
       }
     }
+    if (lane == 0) bulk_wait_group<0>();
+    __syncwarp();
   }
 
   tc_fence_before();
@@ -745,7 +820,7 @@ cudaError_t ready(const void* p, int64_t parts, int64_t rows, int64_t cols, int6
 }
 
 template <int MODE, bool INDEXED, bool LONG>
-cudaError_t launch_t(const CUtensorMap (&m)[6], const Params& p, cudaLaunchConfig_t cfg) {
+cudaError_t launch_t(const Maps& m, const Params& p, cudaLaunchConfig_t cfg) {
   using S = Shape<LONG>;
   auto kern = routed_pair_kernel<MODE, INDEXED, LONG>;
   cfg.blockDim = dim3(THREADS);
@@ -778,7 +853,7 @@ cudaError_t launch_t(const CUtensorMap (&m)[6], const Params& p, cudaLaunchConfi
            MODE == GRADIENT ? "gradient" : MODE == TRANSPOSED ? "transposed" : "product",
            INDEXED ? ",indexed" : "", LONG ? ",long" : "");
   note_main_kernel(name, 2 * clusters, static_cast<int>(units));
-  e = cudaLaunchKernelEx(&cfg, kern, m[0], m[1], m[2], m[3], m[4], m[5], p);
+  e = cudaLaunchKernelEx(&cfg, kern, m, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
@@ -824,8 +899,13 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
   p.k_tiles = static_cast<int32_t>((a.K + tile_rows - 1) / tile_rows);
   p.kind = a.dtype == MHR_BF16 ? 1 : 0;
   p.out_dtype = a.out_dtype;
-  p.pairs = a.out_dtype != MHR_F32 && reinterpret_cast<uintptr_t>(a.out) % 4 == 0 &&
-            a.ldo % 2 == 0 && (!gradient || a.stride_o % 2 == 0);
+  p.pairs = !wide && reinterpret_cast<uintptr_t>(a.out) % 4 == 0 && a.ldo % 2 == 0 &&
+            (!gradient || a.stride_o % 2 == 0);
+  // (TMA clips a box at the row's end in whole 16 bytes only)
+  const int64_t per = wide ? 4 : 8, out_rows = gradient ? a.K : a.out_rows;
+  p.out_tma = reinterpret_cast<uintptr_t>(a.out) % 16 == 0 && a.N % per == 0 &&
+              (out_rows == 1 || a.ldo % per == 0) &&
+              (!gradient || a.E == 1 || a.stride_o % per == 0) && (gradient || !a.scatter);
   p.status = ctl.status;
   p.wait_limit_ns = ctl.wait_limit_ns;
   p.inject_stall = ctl.inject_stall;
@@ -842,10 +922,23 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
   cfg.attrs = attr;
   cfg.gridDim = dim3(2 * (ctl.sm_count / 2));
 
-  CUtensorMap m[6] = {};
+  Maps m = {};
   const auto type = a.dtype == MHR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
+  if (p.out_tma) {
+    const int64_t size = wide ? 4 : 2, parts = gradient ? a.E : 1;
+    const int64_t ld = out_rows == 1 ? a.N : a.ldo;
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.N), static_cast<uint64_t>(out_rows),
+                              static_cast<uint64_t>(parts)};
+    const uint64_t pitch[2] = {static_cast<uint64_t>(ld * size),
+                               static_cast<uint64_t>((parts == 1 ? out_rows * ld : a.stride_o) * size)};
+    const uint32_t box[3] = {32, 32, 1};
+    if (encode_tmap_3d(&m.out,
+                       wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                       a.out, dims, pitch, box) != CUDA_SUCCESS)
+      p.out_tma = 0;  // (a pitch past TMA's: the rows go out from registers)
+  }
   if (!none) {
     char* at = static_cast<char*>(scratch);
     Ready x, w;
@@ -854,10 +947,10 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
                           a.top, a.rows, &at, s, &x);
     if (e != cudaSuccess) return e;
     if (in_order) p.gather = nullptr;
-    auto rows_map = [&](int i, const Ready& r, int64_t cols, uint32_t box) {
+    auto rows_map = [&](CUtensorMap* map, const Ready& r, int64_t cols, uint32_t box) {
       // (one row has no pitch of its own to go by)
       const int64_t ld = r.rows == 1 ? (cols + 7) / 8 * 8 : r.ld;
-      return encode_tmap_2d(&m[i], type, r.p, cols, r.rows, ld * 2, 64, box, swizzle) ==
+      return encode_tmap_2d(map, type, r.p, cols, r.rows, ld * 2, 64, box, swizzle) ==
              CUDA_SUCCESS;
     };
     bool ok = true;
@@ -865,8 +958,8 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
       e = ready(a.w, 1, a.out_rows, a.N, a.ldw, 0, nullptr, a.scatter, 1, a.rows, &at, s, &w);
       if (e != cudaSuccess) return e;
       p.scatter = nullptr;
-      ok = rows_map(0, w, a.N, 64) && rows_map(1, x, a.K, 64) && rows_map(2, x, a.K, 16) &&
-           rows_map(3, w, a.N, 16) && rows_map(4, w, a.N, 1) && rows_map(5, x, a.K, 1);
+      for (int i = 0; i < 3; ++i) ok = ok && rows_map(&m.w[i], w, a.N, 16u << i);
+      ok = ok && rows_map(&m.w1, w, a.N, 1);
     } else {
       const bool t = a.kind == ProductKind::transposed;
       const int64_t rows = t ? a.N : a.K, cols = t ? a.K : a.N;
@@ -878,9 +971,10 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
       const int64_t stride = a.E == 1 ? rows * ((cols + 7) / 8 * 8) : w.stride;
       const uint64_t pitch[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(stride) * 2};
       const uint32_t box[3] = {64, t ? 128u : 64u, 1};
-      ok = encode_tmap_3d(&m[0], type, w.p, dims, pitch, box, swizzle) == CUDA_SUCCESS &&
-           rows_map(1, x, a.K, tile_rows / 2) && rows_map(2, x, a.K, p.gather ? 1 : 8);
+      ok = encode_tmap_3d(&m.w[2], type, w.p, dims, pitch, box, swizzle) == CUDA_SUCCESS;
     }
+    for (int i = 0; i < 4; ++i) ok = ok && rows_map(&m.x[i], x, a.K, 16u << i);
+    ok = ok && rows_map(&m.x1, x, a.K, 1);
     if (!ok) return cudaErrorInvalidValue;
   }
   MainKernelEvents ev(s);
