@@ -25,6 +25,7 @@ namespace mhr {
 namespace routed {
 namespace {
 
+using mx::elect_one;
 using mx::from_float;
 using mx::to_float;
 
@@ -64,6 +65,37 @@ __device__ __forceinline__ void floats8(const uint4& w, float (&f)[8]) {
   }
 }
 
+// n elements by `threads` threads, 16 bytes and four loads at a time where both ends allow.
+template <typename O>
+__device__ __forceinline__ void copy_row(O* to, const O* from, int n, int thread, int threads) {
+  constexpr int PER = 16 / sizeof(O);
+  int done = 0;
+  if (((reinterpret_cast<uintptr_t>(to) | reinterpret_cast<uintptr_t>(from)) & 15u) == 0) {
+    const int words = n / PER;
+    const uint4* src = reinterpret_cast<const uint4*>(from);
+    uint4* dst = reinterpret_cast<uint4*>(to);
+    for (int c = thread; c < words; c += 4 * threads) {
+      uint4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i * threads < words) v[i] = src[c + i * threads];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i * threads < words) dst[c + i * threads] = v[i];
+    }
+    done = words * PER;
+  }
+  for (int c = done + thread; c < n; c += 4 * threads) {
+    O v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i * threads < n) v[i] = from[c + i * threads];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i * threads < n) to[c + i * threads] = v[i];
+  }
+}
+
 // ------------------------------------------------------------------ few rows
 
 constexpr int CTAS = 8;
@@ -90,7 +122,7 @@ __global__ void __launch_bounds__(ROW_THREADS) __cluster_dims__(CTAS, 1, 1)
   const int n0 = min(p.N, rank * n_each), n1 = min(p.N, n0 + n_each);
   if (!some) {  // (the whole cluster)
     if (static_cast<const void*>(y) != out)
-      for (int n = n0 + threadIdx.x; n < n1; n += ROW_THREADS) out[n] = y[n];
+      copy_row(out + n0, y + n0, n1 - n0, threadIdx.x, ROW_THREADS);
     return;
   }
   // (every CTA has to run before another writes its shared memory)
@@ -202,6 +234,682 @@ __global__ void __launch_bounds__(ROW_THREADS) __cluster_dims__(CTAS, 1, 1)
   }
 }
 
+// ------------------------------------------------------------------ many rows
+
+// Tiles: 128 rows of one adapter, in the order of routed_sort.cu.
+constexpr int TILE = 128;
+constexpr int BK = 64;                        // of x's columns a stage: 128 bytes a row
+constexpr int BLOCK_N = 128;                  // of the output's columns an accumulator
+constexpr int EPI_WARPS = 8;
+constexpr int EPI_THREADS = 32 * EPI_WARPS;
+constexpr int TILE_THREADS = 64 + EPI_THREADS;  // warp 0 loads, 1 multiplies, 2-9 the rest
+constexpr int SLOT = 32 * 128;                // 32 rows of y and of the output, 128 bytes each
+constexpr int MAX_STAGES = 6;
+constexpr uint32_t TMEM_COLS = 512, ACC0 = 256;  // v's sums up to column 256, then the output's
+
+struct TileMaps {
+  CUtensorMap x, x32, x1, down, up, y, y1, out;  // x and y: whole boxes, and single rows
+};
+
+struct TileParams {
+  const int32_t *offsets, *order;
+  const float* scales;
+  const void* y;
+  void* out;
+  int64_t ldy, ldo;
+  int32_t T, K, N, L, rank;
+  int32_t pad;          // rank, in steps of 16
+  int32_t stages, slots;
+  int32_t kind, copy;   // 0 fp16, 1 bf16; copy: rows without an adapter are copied
+  int32_t rows_tma;     // y and the output can go by TMA
+  uint32_t* status;
+  uint64_t wait_limit_ns;
+  int32_t inject_stall;
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map, uint32_t bar,
+                                            int32_t x, const int32_t (&r)[4]) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+      "r"(r[3])
+      : "memory");
+}
+__device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void st_shared_u4(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b) {
+  if constexpr (std::is_same_v<T, __half>) {
+    const __half2 v = __floats2half2_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  } else {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t*>(&v);
+  }
+}
+
+// A tile: 128 sorted rows from `first` on, `count` of them, of adapter `a` (L: of none).
+struct Tile {
+  int a, first, count;
+};
+
+// T: of x and the adapters; O: of y and the output.  BOXES: 64 columns of v each.
+//
+// v is given to the tensor cores as TERMS values of T whose sum it is to 2^-16 (two of
+// bf16) or 2^-22 and less (three; two of fp16, taken times a power of two a row so that
+// neither leaves fp16's range) of it, or of the row's largest.
+template <typename T, typename O, int BOXES>
+__global__ void __launch_bounds__(TILE_THREADS, 1)
+    adapters_tile_kernel(const __grid_constant__ TileMaps maps, const TileParams p) {
+  constexpr bool HALF = std::is_same_v<T, __half>, WIDE = sizeof(O) == 4;
+  constexpr int TERMS = WIDE && !HALF ? 3 : 2;
+  constexpr int SUMS = 4 / BOXES;              // accumulators of v (see below)
+  constexpr int BOX_COLS = WIDE ? 32 : 64;     // of the output, 128 bytes
+  constexpr int PARTS = 64 / BOX_COLS;         // boxes of a warp's half of a block
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(8) uint64_t bars[2 * MAX_STAGES + 7 + 3 * EPI_WARPS];
+  __shared__ uint32_t tmem_slot;
+  __shared__ volatile int abort_flag;
+  __shared__ Tile tile_slot;
+  __shared__ uint32_t scan_sums[TILE_THREADS / 32];
+  __shared__ int32_t rows[TILE];
+  __shared__ float row_max[2][HALF ? TILE : 1], row_unit[HALF ? TILE : 1];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  const uint32_t bar0 = smem_u32(bars);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
+  auto acc_bar = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + b); };
+  auto free_bar = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + 2 + b); };
+  const uint32_t sums_bar = bar0 + 8u * (2 * MAX_STAGES + 4);
+  const uint32_t v_bar = bar0 + 8u * (2 * MAX_STAGES + 5);
+  const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 6);
+  auto y_bar = [&](int w, int s) { return bar0 + 8u * (2 * MAX_STAGES + 7 + 3 * w + s); };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  int ctas;
+  asm volatile("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(ctas));
+  const int tile_no = blockIdx.x / ctas;
+
+  grid_dependency_wait();
+  // Which tile: the bins' tiles, summed up.  (Bin L holds the rows without an adapter.)
+  if (threadIdx.x == 0) tile_slot = {-1, 0, 0};
+  __syncthreads();
+  int base = 0;
+  for (int b0 = 0; b0 <= p.L && base <= tile_no; b0 += TILE_THREADS) {
+    const int b = b0 + static_cast<int>(threadIdx.x);
+    int lo = 0, n = 0;
+    if (b <= p.L) {
+      lo = p.offsets[b];
+      n = (b < p.L ? p.offsets[b + 1] : p.T) - lo;
+    }
+    const int tiles = b == p.L && !p.copy ? 0 : (n + TILE - 1) / TILE;
+    int scan = tiles;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const int o = __shfl_up_sync(ALL, scan, i);
+      if (lane >= i) scan += o;
+    }
+    if (lane == 31) scan_sums[warp] = scan;
+    __syncthreads();
+    int lower = base, all = 0;
+    for (int i = 0; i < TILE_THREADS / 32; ++i) {
+      if (i < warp) lower += scan_sums[i];
+      all += scan_sums[i];
+    }
+    const int at = tile_no - (lower + scan - tiles);
+    if (at >= 0 && at < tiles) tile_slot = {b, lo + at * TILE, min(TILE, n - at * TILE)};
+    base += all;
+    __syncthreads();
+  }
+  const Tile tile = tile_slot;
+  if (tile.a < 0) return;  // (the whole cluster: there are fewer tiles)
+  // This CTA's stages of x's columns, and its blocks of the output's.
+  const int kbs = (p.K + BK - 1) / BK, blocks = (p.N + BLOCK_N - 1) / BLOCK_N;
+  const int kb0 = kbs * rank / ctas, kb1 = kbs * (rank + 1) / ctas;
+  const int n0 = blocks * rank / ctas, n1 = blocks * (rank + 1) / ctas;
+  for (int i = threadIdx.x; i < TILE; i += TILE_THREADS)
+    rows[i] = i < tile.count ? p.order[tile.first + i] : -1;
+  __syncthreads();
+  if (tile.a == p.L) {  // copied: a warp a row
+    const int c0 = n0 * BLOCK_N, c1 = min(p.N, n1 * BLOCK_N);
+    for (int i = warp; i < tile.count; i += TILE_THREADS / 32) {
+      const O* from = static_cast<const O*>(p.y) + rows[i] * p.ldy;
+      O* to = static_cast<O*>(p.out) + rows[i] * p.ldo;
+      copy_row(to + c0, from + c0, c1 - c0, lane, 32);
+    }
+    return;
+  }
+
+  const int v_cols = p.pad;
+  const uint32_t stage_bytes = TILE * 128 + BOXES * 64 * 128;
+  const uint32_t v_base = smem_u32(smem);  // v's parts, then its terms
+  const uint32_t v_bytes = max(TERMS * BOXES * TILE * 128, TILE * (BOXES * 64 * 4 + 16));
+  const uint32_t ring = v_base + ((v_bytes + 1023) & ~1023u);
+  const uint32_t slots = ring + p.stages * stage_bytes;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_bar(b), 1);
+      mbar_init(free_bar(b), EPI_WARPS);
+    }
+    mbar_init(sums_bar, 1);
+    mbar_init(v_bar, EPI_THREADS);
+    mbar_init(drain_bar, 1);
+    for (int w = 0; w < EPI_WARPS; ++w)
+      for (int s = 0; s < 3; ++s) mbar_init(y_bar(w, s), 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+  const uint64_t limit = p.wait_limit_ns;
+  auto wait = [&](uint32_t bar, uint32_t parity, uint32_t sleep = 0) {  // by a whole warp
+    return __all_sync(ALL, mbar_wait_bounded(bar, parity, limit, &abort_flag, sleep)) != 0;
+  };
+  auto give_up = [&](uint32_t bit) {
+    if (lane == 0) {
+      if (!abort_flag) atomicOr(p.status, bit);
+      abort_flag = 1;
+    }
+    __syncwarp();
+  };
+  // v's sums go on in the next of SUMS accumulators every `run` stages: the tensor cores
+  // add by truncation, which takes some 1.4e-8 of a sum off for every 16 terms.
+  const int run = max(1, (kb1 - kb0 + SUMS - 1) / SUMS);
+
+  if (warp == 0) {
+    // Rows 32 by 32: a box where they lie together, else gathered, four rows a lane.
+    int32_t r[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = rows[4 * lane + i];
+      r[i] = at >= 0 ? at : p.T;
+    }
+    const int group = lane >> 3, of = rows[group * 32];
+    bool lies = true;  // this lane's four rows where they would be in a box
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int at = 4 * lane + i;
+      lies &= rows[at] < 0 || rows[at] == of + at - group * 32;
+    }
+    const uint32_t lying = __ballot_sync(ALL, lies);
+    const bool box = (lying >> (8 * group) & 0xffu) == 0xffu && of >= 0;
+    const bool whole = lying == ALL && rows[0] >= 0 &&
+                       __all_sync(ALL, rows[group * 32] < 0 ||
+                                           rows[group * 32] == rows[0] + group * 32);
+    const bool stall = p.inject_stall && blockIdx.x == 0;
+    uint32_t s = 0, ph = 1, it = 0;
+    bool ok = true;
+    const uint32_t tx1 = TILE * 128 + v_cols * 128, tx2 = 2 * v_cols * 128;
+    auto next = [&](uint32_t tx) {  // the next place of the ring, armed
+      if (!wait(empty_bar(s), ph)) {
+        give_up(kErrTimeoutProducer);
+        ok = false;
+        return false;
+      }
+      if (lane == 0) mbar_arrive_expect_tx(full_bar(s), tx);
+      __syncwarp();
+      return !(stall && it == 0);
+    };
+    auto advance = [&] {
+      __syncwarp();
+      ++it;
+      if (++s == static_cast<uint32_t>(p.stages)) {
+        s = 0;
+        ph ^= 1u;
+      }
+    };
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
+      const bool go = next(tx1);
+      if (!ok) break;
+      const uint32_t st = ring + s * stage_bytes, fb = full_bar(s);
+      if (go) {
+        if (elect_one()) {
+          tma_load_3d(st + TILE * 128, &maps.down, fb, kb * BK, 0, tile.a);
+          if (whole) tma_load_2d(st, &maps.x, fb, kb * BK, rows[0]);
+        }
+        if (!whole) {
+          if (box) {
+            if ((lane & 7) == 0) tma_load_2d(st + group * 4096, &maps.x32, fb, kb * BK, of);
+          } else {
+            tma_gather4(st + lane * 512, &maps.x1, fb, kb * BK, r);
+          }
+        }
+      }
+      advance();
+    }
+    auto load_up = [&](int n) {
+      const bool go = next(tx2);
+      if (!ok) return;
+      const uint32_t st = ring + s * stage_bytes, fb = full_bar(s);
+      if (go && elect_one()) {
+        tma_load_3d(st, &maps.up, fb, n * BLOCK_N, 0, tile.a);
+        tma_load_3d(st + v_cols * 128, &maps.up, fb, n * BLOCK_N + 64, 0, tile.a);
+      }
+      advance();
+    };
+    // the ring's worth of `up` before the CTAs meet: its places come free by v's stages
+    int n = n0;
+    for (; ok && n < n1 && n < n0 + p.stages; ++n) load_up(n);
+    cluster_sync_all();
+    cluster_sync_all();
+    for (; ok && n < n1; ++n) load_up(n);
+    if (lane == 0) {  // what is still on its way, before the CTA may leave
+      volatile int never = 0;
+      const uint32_t st = p.stages;
+      for (uint32_t i = it > st ? it - st : 0; i < it; ++i) {
+        if (stall && i == 0) {
+          mbar_wait_bounded(full_bar(0), 0, 2 * limit, &abort_flag);
+          mbar_complete_tx(full_bar(0), kb1 > kb0 ? tx1 : tx2);
+        }
+        if (!mbar_wait_bounded(full_bar(i % st), (i / st) & 1u, limit, &never))
+          atomicOr(p.status, kErrTimeoutDrain);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    uint32_t s = 0, ph = 0;
+    bool ok = true;
+    auto advance = [&] {
+      __syncwarp();
+      if (++s == static_cast<uint32_t>(p.stages)) {
+        s = 0;
+        ph ^= 1u;
+      }
+    };
+    const uint32_t id1 = make_idesc(p.kind, false, false, TILE, v_cols);
+    const uint32_t id2 = make_idesc(p.kind, false, true, TILE, BLOCK_N);
+    for (int kb = kb0; kb < kb1; ++kb) {
+      if (!wait(full_bar(s), ph)) {
+        give_up(kErrTimeoutMma);
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = ring + s * stage_bytes;
+      const int in = (kb - kb0) % run;
+      const uint32_t d = tmem + (kb - kb0) / run * (BOXES * 64);
+      if (elect_one()) {
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk)
+          mma_f16(d, smem_desc_sw128(st + kk * 32, 16, 1024),
+                  smem_desc_sw128(st + TILE * 128 + kk * 32, 16, 1024), id1,
+                  in > 0 || kk > 0 ? 1u : 0u);
+        mma_commit(empty_bar(s));
+        if (kb + 1 == kb1) mma_commit(sums_bar);
+      }
+      advance();
+    }
+    cluster_sync_all();
+    cluster_sync_all();
+    if (ok && n1 > n0 && !wait(v_bar, 0)) {
+      give_up(kErrTimeoutMma);
+      ok = false;
+    }
+    for (int n = n0; ok && n < n1; ++n) {
+      const int t = n - n0, b = t & 1;
+      if ((t >= 2 && !wait(free_bar(b), ((t - 2) >> 1) & 1u)) || !wait(full_bar(s), ph)) {
+        give_up(kErrTimeoutMma);
+        break;
+      }
+      tc_fence_after();
+      const uint32_t st = ring + s * stage_bytes;
+      if (elect_one()) {
+        uint32_t more = 0;
+        for (int term = 0; term < TERMS; ++term)
+          for (int kk = 0; kk < v_cols / 16; ++kk) {
+            mma_f16(tmem + ACC0 + b * BLOCK_N,
+                    smem_desc_sw128(v_base + (term * BOXES + kk / 4) * (TILE * 128) + kk % 4 * 32,
+                                    16, 1024),
+                    smem_desc_sw128(st + kk * 2048, v_cols * 128, 1024), id2, more);
+            more = 1;
+          }
+        mma_commit(empty_bar(s));
+        mma_commit(acc_bar(b));
+      }
+      advance();
+    }
+    if (elect_one()) mma_commit(drain_bar);
+    __syncwarp();
+    volatile int never = 0;
+    if (!mbar_wait_bounded(drain_bar, 0, limit, &never) && lane == 0)
+      atomicOr(p.status, kErrTimeoutDrain);
+    __syncwarp();
+  } else {
+    // Warp e: lane quarter q, half h of the columns.
+    const int e = warp - 2, q = warp & 3, h = e >> 2;
+    const int row = q * 32 + lane;  // of the tile
+    const int mine = rows[row];
+    const int first = rows[q * 32], n_rows = max(0, min(32, tile.count - q * 32));
+    const bool lie = __all_sync(ALL, lane >= n_rows || mine == first + lane);
+    const bool load = p.rows_tma && n_rows > 0;      // y by TMA, in a box or gathered; the
+    const bool store = load && lie && n_rows == 32;  // output in a box that is all of it
+    int32_t four[4];  // of a gather: rows 4 lane .. 4 lane + 3 of this warp's
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = __shfl_sync(ALL, mine, (4 * lane + i) & 31);
+      four[i] = r >= 0 ? r : p.T;
+    }
+    const uint32_t slot0 = slots + e * p.slots * SLOT;
+    const int boxes = n_rows > 0 ? (n1 - n0) * PARTS : 0;
+    auto box_col = [&](int i) {
+      return (n0 + i / PARTS) * BLOCK_N + h * 64 + i % PARTS * BOX_COLS;
+    };
+    int fetched = 0, done = 0;
+    // y's box i into its slot
+    auto fetch = [&](int i) {
+      const uint32_t slot = slot0 + i % p.slots * SLOT;
+      const int col = box_col(i);
+      if (load) {
+        if (col < p.N) fetched = i + 1;
+        const uint32_t bar = y_bar(e, i % p.slots);
+        if (lane == 0 && col < p.N) {
+          mbar_arrive_expect_tx(bar, SLOT);
+          if (lie) tma_load_2d(slot, &maps.y, bar, col, first);
+        }
+        __syncwarp();
+        if (!lie && lane < 8 && col < p.N) tma_gather4(slot + lane * 512, &maps.y1, bar, col, four);
+      }
+    };
+    for (int i = 0; i < min(boxes, p.slots - 1); ++i) fetch(i);
+    bool ok = true;
+    // v: this thread's half of its row's columns, summed over accumulators and CTAs.
+    constexpr int COLS = BOXES * 32;
+    const int half_cols = v_cols / 2;  // (a multiple of 8)
+    if (kb1 > kb0) {
+      ok = wait(sums_bar, 0, 128);
+      if (!ok) give_up(kErrTimeoutEpilogue);
+      tc_fence_after();
+    }
+    const uint32_t pitch = BOXES * 64 * 4 + 16;
+    const uint32_t part = v_base + row * pitch + h * half_cols * 4;
+    const int used = kb1 > kb0 ? (kb1 - kb0 + run - 1) / run : 0;
+#pragma unroll
+    for (int c = 0; c < COLS; c += 8) {
+      if (c < half_cols) {
+        float acc[8] = {};
+        if (ok)
+          for (int k = 0; k < used; ++k) {
+            uint32_t d[8];
+            mx::tmem_ld_8cols(tmem + (static_cast<uint32_t>(q * 32) << 16) + k * (BOXES * 64) +
+                                  h * half_cols + c,
+                              d);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) acc[i] += __uint_as_float(d[i]);
+          }
+        st_shared_v4(part + c * 4, make_float4(acc[0], acc[1], acc[2], acc[3]));
+        st_shared_v4(part + c * 4 + 16, make_float4(acc[4], acc[5], acc[6], acc[7]));
+      }
+    }
+    cluster_sync_all();
+    const float scale = p.scales ? p.scales[tile.a] : 1.f;
+    uint32_t terms[TERMS][COLS / 2];
+    float high = 0;
+    {
+      float v[COLS];
+#pragma unroll
+      for (int c = 0; c < COLS; c += 4) {
+        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (c < half_cols)
+          for (int k = 0; k < ctas; ++k) {
+            const float4 o = ld_shared_cluster_v4(mapa_shared(part + c * 4, k));
+            s.x += o.x;
+            s.y += o.y;
+            s.z += o.z;
+            s.w += o.w;
+          }
+        v[c] = scale * s.x;
+        v[c + 1] = scale * s.y;
+        v[c + 2] = scale * s.z;
+        v[c + 3] = scale * s.w;
+      }
+      float unit = 1.f;
+      if constexpr (HALF) {
+        // A power of two a row that brings its largest to [2^13, 2^14).
+#pragma unroll
+        for (int c = 0; c < COLS; ++c) high = fmaxf(high, fabsf(v[c]));
+        row_max[h][row] = high;
+        asm volatile("barrier.cta.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+        high = fmaxf(row_max[0][row], row_max[1][row]);
+        const int x = static_cast<int>(__float_as_uint(high) >> 23);  // 0: below 2^-126
+        // (a row that is not finite, and zero, as they are)
+        if (high > 0.f && x < 255) {
+          const int up = min(max(13 + 127 - x, -100), 100);
+          unit = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+          if (h == 0) row_unit[row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+        } else if (h == 0) {
+          row_unit[row] = 1.f;
+        }
+      }
+#pragma unroll
+      for (int c = 0; c < COLS; c += 2) {
+        float a = v[c] * unit, b = v[c + 1] * unit;
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) {
+          const uint32_t w = pack2<T>(a, b);
+          terms[k][c / 2] = w;
+          const float2 f = Pair<T>::floats(w);
+          // (what is infinite has no rest)
+          a = isfinite(f.x) ? a - f.x : 0.f;
+          b = isfinite(f.y) ? b - f.y : 0.f;
+        }
+      }
+    }
+    cluster_sync_all();  // all parts are read: the terms take their place
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k)
+#pragma unroll
+      for (int c = 0; c < COLS; c += 8)
+        if (c < half_cols) {
+          const int col = h * half_cols + c, box = col / 64, chunk = col % 64 / 8;
+          st_shared_u4(v_base + (k * BOXES + box) * (TILE * 128) + row * 128 +
+                           ((chunk ^ (row & 7)) << 4),
+                       make_uint4(terms[k][c / 2], terms[k][c / 2 + 1], terms[k][c / 2 + 2],
+                                  terms[k][c / 2 + 3]));
+        }
+    fence_proxy_async_smem();
+    mbar_arrive(v_bar);
+    if constexpr (HALF)  // (row_unit)
+      asm volatile("barrier.cta.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
+    const float unit = HALF ? row_unit[row] : 1.f;
+
+    // Element by element over a box's rows, 16 of a lane's at a time: first all the loads.
+    auto for_elements = [&](const auto& get, const auto& put, int col) {
+      constexpr int EACH = BOX_COLS / 32;
+      for (int j0 = 0; j0 < n_rows; j0 += 16 / EACH) {
+        O v[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int j = j0 + k / EACH, c = lane + k % EACH * 32;
+          v[k] = get(min(j, n_rows - 1), c, j * 128 + ((c * sizeof(O)) ^ ((j & 7) << 4)),
+                     j < n_rows && col + c < p.N);
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int j = j0 + k / EACH, c = lane + k % EACH * 32;
+          put(min(j, n_rows - 1), c, j * 128 + ((c * sizeof(O)) ^ ((j & 7) << 4)),
+              j < n_rows && col + c < p.N, v[k]);
+        }
+      }
+    };
+    const int total = (n1 - n0) * PARTS;
+    for (int i = 0; i < total; ++i) {
+      const int t = i / PARTS, b = t & 1;
+      if (ok && i % PARTS == 0 && !wait(acc_bar(b), (t >> 1) & 1u, 64)) {
+        give_up(kErrTimeoutEpilogue);
+        ok = false;
+      }
+      if (!ok) break;
+      const int col = box_col(i);
+      const uint32_t slot = slot0 + i % p.slots * SLOT;
+      const bool work = n_rows > 0 && col < p.N;
+      if (work && load) {
+        if (!wait(y_bar(e, i % p.slots), (i / p.slots) & 1u)) {
+          give_up(kErrTimeoutEpilogue);
+          ok = false;
+          break;
+        }
+        done = i + 1;
+      } else if (work) {  // rows that TMA cannot read
+        for_elements([&](int j, int c, uint32_t at, bool in) {
+          O v = O{};
+          if (in) v = static_cast<const O*>(p.y)[rows[q * 32 + j] * p.ldy + col + c];
+          return v;
+        }, [&](int, int, uint32_t at, bool, O v) {
+          if constexpr (WIDE)
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(slot + at), "r"(__float_as_uint(v)) : "memory");
+          else
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(slot + at),
+                         "h"(*reinterpret_cast<uint16_t*>(&v))
+                         : "memory");
+        }, col);
+        __syncwarp();
+      }
+      tc_fence_after();
+      const uint32_t acc = tmem + (static_cast<uint32_t>(q * 32) << 16) + ACC0 + b * BLOCK_N +
+                           h * 64 + i % PARTS * BOX_COLS;
+      uint32_t d[BOX_COLS / 32][32];
+#pragma unroll
+      for (int k = 0; k < BOX_COLS / 32; ++k) tmem_ld_32cols(acc + 32 * k, d[k]);
+      tmem_ld_wait();
+      if (i % PARTS == PARTS - 1) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(free_bar(b));
+      }
+      if (work) {
+        const uint32_t line = slot + lane * 128;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {  // 16 bytes of the row
+          const uint32_t at = line + ((k ^ (lane & 7)) << 4);
+          uint4 w = ld_shared_u4(at);
+          uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            if constexpr (WIDE) {
+              const float o = __uint_as_float(d[0][4 * k + j]) * unit;
+              u[j] = __float_as_uint(__uint_as_float(u[j]) + o);
+            } else {
+              const int c = 8 * k + 2 * j;
+              const float2 f = Pair<O>::floats(u[j]);
+              u[j] = pack2<O>(fmaf(__uint_as_float(d[c / 32][c % 32]), unit, f.x),
+                              fmaf(__uint_as_float(d[c / 32][c % 32 + 1]), unit, f.y));
+            }
+          }
+          st_shared_u4(at, make_uint4(u[0], u[1], u[2], u[3]));
+        }
+        if (store) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) tma_store_2d(&maps.out, slot, col, first);
+        } else {
+          __syncwarp();
+          if (load) {  // eight lanes a row of 128 bytes
+            constexpr int PER = 16 / sizeof(O);
+            const int c = lane & 7, left = p.N - (col + c * PER);
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int j = 4 * k + (lane >> 3);
+              v[k] = ld_shared_u4(slot + j * 128 + ((c ^ (j & 7)) << 4));
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int j = 4 * k + (lane >> 3);
+              // (N is whole 16 bytes)
+              if (j < n_rows && left > 0)
+                *reinterpret_cast<uint4*>(static_cast<O*>(p.out) + rows[q * 32 + j] * p.ldo + col +
+                                          c * PER) = v[k];
+            }
+          } else {
+            for_elements([&](int, int, uint32_t at, bool) {
+              O v;
+              if constexpr (WIDE) {
+                uint32_t u;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(u) : "r"(slot + at) : "memory");
+                v = __uint_as_float(u);
+              } else {
+                uint16_t u;
+                asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(slot + at) : "memory");
+                v = *reinterpret_cast<O*>(&u);
+              }
+              return v;
+            }, [&](int j, int c, uint32_t, bool in, O v) {
+              if (in) static_cast<O*>(p.out)[rows[q * 32 + j] * p.ldo + col + c] = v;
+            }, col);
+          }
+          __syncwarp();
+          // (what is read and written here, before TMA's next load of the slot)
+          if (load) fence_proxy_async_smem();
+        }
+      }
+      if (lane == 0) bulk_commit_group();
+      // The slot of the box before this one: its store has had a box's time to read it.
+      if (i + p.slots - 1 < boxes) {
+        if (lane == 0) bulk_wait_group_read<1>();
+        __syncwarp();
+        fetch(i + p.slots - 1);
+      }
+    }
+    if (lane == 0) {
+      bulk_wait_group<0>();
+      if (load) {  // fetched and not waited for, where a wait has run out
+        volatile int never = 0;
+        for (; done < fetched; ++done)
+          mbar_wait_bounded(y_bar(e, done % p.slots), (done / p.slots) & 1u, limit, &never);
+      }
+    }
+    __syncwarp();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
 bool aligned(const void* p, int64_t elements) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && elements % 8 == 0;
 }
@@ -233,11 +941,164 @@ cudaError_t launch_out(const AdapterArgs& a, const AdapterParams& p, cudaStream_
   return launch_rows<T, __half>(a, p, s);
 }
 
+template <typename T, typename O, int BOXES>
+cudaError_t launch_tiles(const AdapterArgs& a, const AdapterParams& r, TileParams p,
+                         const TileMaps& maps, const DeviceCtl& ctl, cudaStream_t s) {
+  auto kern = adapters_tile_kernel<T, O, BOXES>;
+  constexpr bool HALF = std::is_same_v<T, __half>;
+  constexpr int TERMS = sizeof(O) == 4 && !HALF ? 3 : 2;
+  constexpr int STAGE = TILE * 128 + BOXES * 64 * 128;
+  constexpr int TERM_BYTES = TERMS * BOXES * TILE * 128, PART_BYTES = TILE * (BOXES * 64 * 4 + 16);
+  constexpr int V = ((TERM_BYTES > PART_BYTES ? TERM_BYTES : PART_BYTES) + 1023) / 1024 * 1024;
+  constexpr int MOST = HALF ? 222 * 1024 : 224 * 1024;
+  constexpr int SLOTS = (MOST - V - 3 * EPI_WARPS * SLOT) / STAGE >= 2 ? 3 : 2;
+  constexpr int FIT = (MOST - V - SLOTS * EPI_WARPS * SLOT) / STAGE;
+  constexpr int STAGES = FIT < MAX_STAGES ? FIT : MAX_STAGES;
+  static_assert(STAGES >= 2, "shared memory");
+  constexpr int SMEM = V + STAGES * STAGE + SLOTS * EPI_WARPS * SLOT + 1024;
+  p.stages = STAGES;
+  p.slots = SLOTS;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+  if (e != cudaSuccess) return e;
+  // CTAs a tile: as many as leave every tile room to run at once.
+  const int64_t full = (a.T + TILE - 1) / TILE;
+  int ctas = 8;
+  while (ctas > 1 && full * ctas > ctl.sm_count) ctas /= 2;
+  // every bin's tiles but one are full
+  const int64_t tiles = a.T / TILE + (a.T < a.L + 1 ? a.T : a.L + 1);
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * ctas));
+  cfg.blockDim = dim3(TILE_THREADS);
+  cfg.dynamicSmemBytes = SMEM;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  note_main_kernel("adapters_tile_kernel", static_cast<int>(tiles * ctas), static_cast<int>(tiles));
+  e = cudaLaunchKernelEx(&cfg, kern, maps, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
+
+// Rows up to which every row has a cluster of its own.
+constexpr int64_t FEW = 64;
+
+cudaError_t launch_many(const AdapterArgs& a, const AdapterParams& r, void* scratch,
+                        const DeviceCtl& ctl, cudaStream_t s) {
+  char* at = static_cast<char*>(scratch);
+  int32_t* offsets = reinterpret_cast<int32_t*>(at);
+  at += align256(4 * (a.L + 1));
+  int32_t* order = reinterpret_cast<int32_t*>(at);
+  at += align256(4 * a.T);
+  cudaError_t e = launch_sort(a.which, a.T, a.L, offsets, order, s);
+  if (e != cudaSuccess) return e;
+  Operand x{}, down{}, up{};
+  if (a.K > 0) {
+    e = ready(a.x, 1, a.T, a.K, a.ldx, 0, nullptr, nullptr, 1, 0, &at, s, &x);
+    if (e != cudaSuccess) return e;
+    e = ready(a.down, a.L, a.rank, a.K, a.ldd, a.stride_d, offsets, nullptr, 1, 0, &at, s, &down);
+    if (e != cudaSuccess) return e;
+  }
+  e = ready(a.up, a.L, a.rank, a.N, a.ldu, a.stride_u, offsets, nullptr, 1, 0, &at, s, &up);
+  if (e != cudaSuccess) return e;
+
+  TileParams p = {};
+  p.offsets = offsets;
+  p.order = order;
+  p.scales = a.scales;
+  p.y = a.y;
+  p.out = a.out;
+  p.ldy = a.ldy;
+  p.ldo = a.ldo;
+  p.T = r.T;
+  p.K = r.K;
+  p.N = r.N;
+  p.L = r.L;
+  p.rank = r.rank;
+  p.pad = (r.rank + 15) / 16 * 16;
+  p.kind = a.dtype == MHR_BF16 ? 1 : 0;
+  p.copy = a.y != a.out;
+  p.status = ctl.status;
+  p.wait_limit_ns = ctl.wait_limit_ns;
+  p.inject_stall = ctl.inject_stall;
+  const int64_t size = a.out_dtype == MHR_F32 ? 4 : 2;
+  auto rows_of_16 = [&](const void* q, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(q) % 16 == 0 && ld * size % 16 == 0;
+  };
+  // (TMA clips a box at the row's end in whole 16 bytes only)
+  p.rows_tma = rows_of_16(a.y, a.ldy) && rows_of_16(a.out, a.ldo) && a.N * size % 16 == 0;
+  TileMaps m = {};
+  const auto type = a.dtype == MHR_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  const auto swizzle = CU_TENSOR_MAP_SWIZZLE_128B;
+  auto parts = [&](CUtensorMap* map, const Operand& o, int64_t cols) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(cols), static_cast<uint64_t>(a.rank),
+                              static_cast<uint64_t>(a.L)};
+    const int64_t ld = a.rank == 1 ? (cols + 7) / 8 * 8 : o.ld;
+    const int64_t stride = a.L == 1 ? a.rank * ((cols + 7) / 8 * 8) : o.stride;
+    const uint64_t pitch[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(stride) * 2};
+    const uint32_t box[3] = {64, static_cast<uint32_t>(p.pad), 1};
+    return encode_tmap_3d(map, type, o.p, dims, pitch, box, swizzle) == CUDA_SUCCESS;
+  };
+  bool ok = parts(&m.up, up, a.N);
+  if (a.K > 0) {
+    for (CUtensorMap* map : {&m.x, &m.x32, &m.x1})
+      ok = ok && encode_tmap_2d(map, type, x.p, a.K, a.T, x.ld * 2, 64,
+                                map == &m.x ? TILE : map == &m.x32 ? 32 : 1,
+                                swizzle) == CUDA_SUCCESS;
+    ok = ok && parts(&m.down, down, a.K);
+  }
+  if (p.rows_tma) {
+    const auto out_type = a.out_dtype == MHR_F32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                                 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const uint32_t cols = static_cast<uint32_t>(128 / size);
+    // (a pitch past TMA's: rows one by one)
+    p.rows_tma = encode_tmap_2d(&m.y, out_type, a.y, a.N, a.T, a.ldy * size, cols, 32, swizzle) ==
+                     CUDA_SUCCESS &&
+                 encode_tmap_2d(&m.y1, out_type, a.y, a.N, a.T, a.ldy * size, cols, 1, swizzle) ==
+                     CUDA_SUCCESS &&
+                 encode_tmap_2d(&m.out, out_type, a.out, a.N, a.T, a.ldo * size, cols, 32,
+                                swizzle) == CUDA_SUCCESS;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  MainKernelEvents ev(s);
+  auto by_rank = [&](auto t, auto o) {
+    using T = decltype(t);
+    using O = decltype(o);
+    return p.pad <= 64 ? launch_tiles<T, O, 1>(a, r, p, m, ctl, s)
+                       : launch_tiles<T, O, 2>(a, r, p, m, ctl, s);
+  };
+  auto by_out = [&](auto t) {
+    if (a.out_dtype == MHR_F32) return by_rank(t, float{});
+    if (a.out_dtype == MHR_BF16) return by_rank(t, __nv_bfloat16{});
+    return by_rank(t, __half{});
+  };
+  return a.dtype == MHR_BF16 ? by_out(__nv_bfloat16{}) : by_out(__half{});
+}
+
 }  // namespace
 
-int64_t adapters_scratch(const AdapterArgs&) { return 0; }
+int64_t adapters_scratch(const AdapterArgs& a) {
+  if (a.T <= FEW) return 0;
+  const int64_t each[3] = {
+      a.K > 0 ? operand_bytes(a.x, 1, a.T, a.K, a.ldx, 0, 0) : 0,
+      a.K > 0 ? operand_bytes(a.down, a.L, a.rank, a.K, a.ldd, a.stride_d, 0) : 0,
+      operand_bytes(a.up, a.L, a.rank, a.N, a.ldu, a.stride_u, 0)};
+  int64_t n = align256(4 * (a.L + 1)) + align256(4 * a.T);
+  for (const int64_t b : each)
+    if (b < 0 || __builtin_add_overflow(n, b, &n)) return -1;
+  return n;
+}
 
-cudaError_t launch_adapters(const AdapterArgs& a, void*, const DeviceCtl&, cudaStream_t s) {
+cudaError_t launch_adapters(const AdapterArgs& a, void* scratch, const DeviceCtl& ctl,
+                            cudaStream_t s) {
   AdapterParams p;
   p.x = a.x;
   p.down = a.down;
@@ -258,6 +1119,7 @@ cudaError_t launch_adapters(const AdapterArgs& a, void*, const DeviceCtl&, cudaS
   p.N = static_cast<int32_t>(a.N);
   p.L = static_cast<int32_t>(a.L);
   p.rank = static_cast<int32_t>(a.rank);
+  if (a.T > FEW) return launch_many(a, p, scratch, ctl, s);
   return a.dtype == MHR_BF16 ? launch_out<__nv_bfloat16>(a, p, s) : launch_out<__half>(a, p, s);
 }
 

@@ -53,6 +53,17 @@ cudaError_t launch_choose_grad(const ChooseGradArgs& a, cudaStream_t s);
 // index picks, which are put in order there; 0 without.
 int64_t operand_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
                       int64_t stride, int64_t picked);
+// An operand as TMA reads it.
+struct Operand {
+  const void* p;
+  int64_t rows, ld, stride;
+};
+// The operand itself, or its copy at *scratch, which moves on by operand_bytes.  offsets
+// (or null): parts without rows there are left out; index (or null): `picked` entries,
+// each over `top` a row, zeros where it is none.
+cudaError_t ready(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
+                  int64_t stride, const int32_t* offsets, const int32_t* index, int64_t top,
+                  int64_t picked, char** scratch, cudaStream_t s, Operand* out);
 // Up to so many rows a product picks by TMA's gather, without that.
 constexpr int64_t FEW_ROWS = 256;
 

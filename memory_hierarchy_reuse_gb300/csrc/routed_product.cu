@@ -779,46 +779,6 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-struct Ready {
-  const void* p;
-  int64_t rows, ld, stride;
-};
-
-// The operand as TMA reads it: itself, or a copy at *scratch, which moves on.  index:
-// `picked` rows of it, or null.
-cudaError_t ready(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
-                  int64_t stride, const int32_t* offsets, const int32_t* index, int64_t top,
-                  int64_t picked, char** scratch, cudaStream_t s, Ready* out) {
-  const int64_t bytes = operand_bytes(p, parts, rows, cols, ld, stride, index ? picked : 0);
-  if (bytes == 0) {
-    *out = {p, rows, ld, stride};
-    return cudaSuccess;
-  }
-  const int64_t dst_ld = (cols + 7) / 8 * 8, dst_rows = index ? picked : rows;
-  uint16_t* dst = reinterpret_cast<uint16_t*>(*scratch);
-  *out = {dst, dst_rows, dst_ld, dst_rows * dst_ld};
-  *scratch += bytes;
-  const int64_t blocks = (dst_rows + 7) / 8;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096),
-                     static_cast<unsigned>(parts));
-  cfg.blockDim = dim3(256);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const bool vectors = reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 &&
-                       stride % 8 == 0 && cols % 8 == 0;
-  auto kern = vectors ? rows_kernel<uint4> : rows_kernel<uint16_t>;
-  note_launch();
-  const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, kern, static_cast<const uint16_t*>(p), rows, cols, ld, stride,
-                         offsets, index, static_cast<int>(top), dst, dst_rows, dst_ld);
-  return e != cudaSuccess ? e : cudaGetLastError();
-}
-
 template <int MODE, bool INDEXED, bool LONG>
 cudaError_t launch_t(const Maps& m, const Params& p, cudaLaunchConfig_t cfg) {
   using S = Shape<LONG>;
@@ -870,6 +830,39 @@ int64_t operand_bytes(const void* p, int64_t parts, int64_t rows, int64_t cols, 
       n > INT64_MAX - 255)
     return -1;
   return (n + 255) / 256 * 256;
+}
+
+cudaError_t ready(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
+                  int64_t stride, const int32_t* offsets, const int32_t* index, int64_t top,
+                  int64_t picked, char** scratch, cudaStream_t s, Operand* out) {
+  const int64_t bytes = operand_bytes(p, parts, rows, cols, ld, stride, index ? picked : 0);
+  if (bytes == 0) {
+    *out = {p, rows, ld, stride};
+    return cudaSuccess;
+  }
+  const int64_t dst_ld = (cols + 7) / 8 * 8, dst_rows = index ? picked : rows;
+  uint16_t* dst = reinterpret_cast<uint16_t*>(*scratch);
+  *out = {dst, dst_rows, dst_ld, dst_rows * dst_ld};
+  *scratch += bytes;
+  const int64_t blocks = (dst_rows + 7) / 8;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks < 4096 ? blocks : 4096),
+                     static_cast<unsigned>(parts));
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const bool vectors = reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % 8 == 0 &&
+                       stride % 8 == 0 && cols % 8 == 0;
+  auto kern = vectors ? rows_kernel<uint4> : rows_kernel<uint16_t>;
+  note_launch();
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kern, static_cast<const uint16_t*>(p), rows, cols, ld, stride,
+                         offsets, index, static_cast<int>(top), dst, dst_rows, dst_ld);
+  return e != cudaSuccess ? e : cudaGetLastError();
 }
 
 cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl& ctl,
@@ -941,13 +934,13 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
   }
   if (!none) {
     char* at = static_cast<char*>(scratch);
-    Ready x, w;
+    Operand x, w;
     const bool in_order = a.gather && (gradient || a.rows > FEW_ROWS);
     cudaError_t e = ready(a.x, 1, a.x_rows, a.K, a.ldx, 0, nullptr, in_order ? a.gather : nullptr,
                           a.top, a.rows, &at, s, &x);
     if (e != cudaSuccess) return e;
     if (in_order) p.gather = nullptr;
-    auto rows_map = [&](CUtensorMap* map, const Ready& r, int64_t cols, uint32_t box) {
+    auto rows_map = [&](CUtensorMap* map, const Operand& r, int64_t cols, uint32_t box) {
       // (one row has no pitch of its own to go by)
       const int64_t ld = r.rows == 1 ? (cols + 7) / 8 * 8 : r.ld;
       return encode_tmap_2d(map, type, r.p, cols, r.rows, ld * 2, 64, box, swizzle) ==

@@ -42,6 +42,7 @@ __global__ void __launch_bounds__(MAX_WARPS * 32, 1)
 
   for (int i = threadIdx.x; i < warps * bins; i += blockDim.x) counters[i] = 0;
   __syncthreads();
+  grid_dependency_wait();
 
   const int64_t run = (n + 32 * warps * ctas - 1) / (32 * warps * ctas) * 32;
   const int64_t from = min(n, (static_cast<int64_t>(rank) * warps + warp) * run);
@@ -137,18 +138,20 @@ cudaError_t launch_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* o
   while (warps < MAX_WARPS && warps < chunks) warps *= 2;
   const int ctas = chunks > 4 * MAX_WARPS ? MAX_CTAS : 1;
   const size_t bins = static_cast<size_t>(E) + 1;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(static_cast<unsigned>(32 * warps));
   cfg.dynamicSmemBytes = (warps + 2) * bins * sizeof(uint32_t);
   cfg.stream = s;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   constexpr size_t most = (MAX_WARPS + 2) * (MAX_PARTS + 1) * sizeof(uint32_t);  // 136 KB
   cudaError_t e = cudaFuncSetAttribute(sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        static_cast<int>(most));
