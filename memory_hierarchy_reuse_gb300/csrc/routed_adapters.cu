@@ -397,6 +397,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   const int kbs = (p.K + BK - 1) / BK, blocks = (p.N + BLOCK_N - 1) / BLOCK_N;
   const int kb0 = kbs * rank / ctas, kb1 = kbs * (rank + 1) / ctas;
   const int n0 = blocks * rank / ctas, n1 = blocks * (rank + 1) / ctas;
+  // Tiles begin at columns of their own: in step, all rows' accesses would fall on the same
+  // few channels of the memory where their pitch is a power of two.
+  auto kb_at = [&](int i) {
+    const int n = kb1 - kb0;
+    return kb0 + (i + tile_no * 7) % n;
+  };
+  auto block_at = [&](int i) {
+    const int n = n1 - n0;
+    return n0 + (i + tile_no * 3) % n;
+  };
   for (int i = threadIdx.x; i < TILE; i += TILE_THREADS)
     rows[i] = i < tile.count ? p.order[tile.first + i] : -1;
   __syncthreads();
@@ -457,25 +467,17 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   const int run = max(1, (kb1 - kb0 + SUMS - 1) / SUMS);
 
   if (warp == 0) {
-    // Rows 32 by 32: a box where they lie together, else gathered, four rows a lane.
-    int32_t r[4];
+    // Rows 32 by 32: a box where they lie together (else gathered, by the epilogue's warps).
+    int from[4];
+    bool lying[4], whole = true;  // whole: one box of all
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = rows[4 * lane + i];
-      r[i] = at >= 0 ? at : p.T;
+    for (int g = 0; g < 4; ++g) {
+      from[g] = __shfl_sync(ALL, rows[g * 32], 0);
+      lying[g] = __all_sync(ALL, rows[g * 32 + lane] < 0 || rows[g * 32 + lane] == from[g] + lane) &&
+                 from[g] >= 0;
+      whole &= lying[g] ? from[g] == from[0] + 32 * g : tile.count <= 32 * g;
     }
-    const int group = lane >> 3, of = rows[group * 32];
-    bool lies = true;  // this lane's four rows where they would be in a box
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int at = 4 * lane + i;
-      lies &= rows[at] < 0 || rows[at] == of + at - group * 32;
-    }
-    const uint32_t lying = __ballot_sync(ALL, lies);
-    const bool box = (lying >> (8 * group) & 0xffu) == 0xffu && of >= 0;
-    const bool whole = lying == ALL && rows[0] >= 0 &&
-                       __all_sync(ALL, rows[group * 32] < 0 ||
-                                           rows[group * 32] == rows[0] + group * 32);
+    const int a = __shfl_sync(ALL, tile.a, 0);
     const bool stall = p.inject_stall && blockIdx.x == 0;
     uint32_t s = 0, ph = 1, it = 0;
     bool ok = true;
@@ -498,41 +500,42 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         ph ^= 1u;
       }
     };
-    for (int kb = kb0; ok && kb < kb1; ++kb) {
+    for (int i = 0; ok && i < kb1 - kb0; ++i) {
+      const int kb = kb_at(i);
       const bool go = next(tx1);
       if (!ok) break;
       const uint32_t st = ring + s * stage_bytes, fb = full_bar(s);
       if (go) {
         if (elect_one()) {
-          tma_load_3d(st + TILE * 128, &maps.down, fb, kb * BK, 0, tile.a);
-          if (whole) tma_load_2d(st, &maps.x, fb, kb * BK, rows[0]);
-        }
-        if (!whole) {
-          if (box) {
-            if ((lane & 7) == 0) tma_load_2d(st + group * 4096, &maps.x32, fb, kb * BK, of);
+          tma_load_3d(st + TILE * 128, &maps.down, fb, kb * BK, 0, a);
+          if (whole) {
+            tma_load_2d(st, &maps.x, fb, kb * BK, from[0]);
           } else {
-            tma_gather4(st + lane * 512, &maps.x1, fb, kb * BK, r);
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (lying[g]) tma_load_2d(st + g * 4096, &maps.x32, fb, kb * BK, from[g]);
           }
         }
       }
       advance();
     }
-    auto load_up = [&](int n) {
+    auto load_up = [&](int i) {
+      const int n = block_at(i);
       const bool go = next(tx2);
       if (!ok) return;
       const uint32_t st = ring + s * stage_bytes, fb = full_bar(s);
       if (go && elect_one()) {
-        tma_load_3d(st, &maps.up, fb, n * BLOCK_N, 0, tile.a);
-        tma_load_3d(st + v_cols * 128, &maps.up, fb, n * BLOCK_N + 64, 0, tile.a);
+        tma_load_3d(st, &maps.up, fb, n * BLOCK_N, 0, a);
+        tma_load_3d(st + v_cols * 128, &maps.up, fb, n * BLOCK_N + 64, 0, a);
       }
       advance();
     };
     // the ring's worth of `up` before the CTAs meet: its places come free by v's stages
-    int n = n0;
-    for (; ok && n < n1 && n < n0 + p.stages; ++n) load_up(n);
+    int n = 0;
+    for (; ok && n < n1 - n0 && n < p.stages; ++n) load_up(n);
     cluster_sync_all();
     cluster_sync_all();
-    for (; ok && n < n1; ++n) load_up(n);
+    for (; ok && n < n1 - n0; ++n) load_up(n);
     if (lane == 0) {  // what is still on its way, before the CTA may leave
       volatile int never = 0;
       const uint32_t st = p.stages;
@@ -632,7 +635,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t slot0 = slots + e * p.slots * SLOT;
     const int boxes = n_rows > 0 ? (n1 - n0) * PARTS : 0;
     auto box_col = [&](int i) {
-      return (n0 + i / PARTS) * BLOCK_N + h * 64 + i % PARTS * BOX_COLS;
+      return block_at(i / PARTS) * BLOCK_N + h * 64 + i % PARTS * BOX_COLS;
     };
     int fetched = 0, done = 0;
     // y's box i into its slot
@@ -640,69 +643,106 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       const uint32_t slot = slot0 + i % p.slots * SLOT;
       const int col = box_col(i);
       if (load) {
-        if (col < p.N) fetched = i + 1;
+        fetched = i + 1;  // (columns past N, of the last block, come as zeros)
         const uint32_t bar = y_bar(e, i % p.slots);
-        if (lane == 0 && col < p.N) {
+        if (lane == 0) {
           mbar_arrive_expect_tx(bar, SLOT);
           if (lie) tma_load_2d(slot, &maps.y, bar, col, first);
         }
         __syncwarp();
-        if (!lie && lane < 8 && col < p.N) tma_gather4(slot + lane * 512, &maps.y1, bar, col, four);
+        if (!lie && lane < 8) tma_gather4(slot + lane * 512, &maps.y1, bar, col, four);
       }
     };
     for (int i = 0; i < min(boxes, p.slots - 1); ++i) fetch(i);
     bool ok = true;
+    // x's rows that lie in no box of 32: four gathers a warp, of 16 rows.  (An operand that
+    // differs from lane to lane makes a TMA instruction some 60 cycles of the warp's; all
+    // by the loading warp, a stage took 1160 cycles and more.)
+    {
+      const int g = e >> 1, r0 = g * 32, of = rows[r0];
+      const bool box = of >= 0 && __all_sync(ALL, rows[r0 + lane] < 0 || rows[r0 + lane] == of + lane);
+      bool whole = rows[0] >= 0;  // (one box has them all)
+      for (int k = 0; k < TILE; k += 32)
+        whole &= __all_sync(ALL, rows[k + lane] < 0 || rows[k + lane] == rows[0] + k + lane) != 0;
+      if (!whole && !box) {
+        int32_t r[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int at = rows[(r0 + (e & 1) * 16 + 4 * lane + i) & (TILE - 1)];
+          r[i] = at >= 0 ? at : p.T;
+        }
+        const bool stall = p.inject_stall && blockIdx.x == 0;
+        uint32_t s = 0, ph = 1;
+        for (int i = 0; i < kb1 - kb0; ++i) {
+          if (!wait(empty_bar(s), ph)) {
+            give_up(kErrTimeoutProducer);
+            ok = false;
+            break;
+          }
+          if (lane < 4 && !(stall && i == 0))
+            tma_gather4(ring + s * stage_bytes + (r0 + (e & 1) * 16) * 128 + lane * 512, &maps.x1,
+                        full_bar(s), kb_at(i) * BK, r);
+          __syncwarp();
+          if (++s == static_cast<uint32_t>(p.stages)) {
+            s = 0;
+            ph ^= 1u;
+          }
+        }
+      }
+    }
     // v: this thread's half of its row's columns, summed over accumulators and CTAs.
     constexpr int COLS = BOXES * 32;
     const int half_cols = v_cols / 2;  // (a multiple of 8)
     if (kb1 > kb0) {
-      ok = wait(sums_bar, 0, 128);
+      ok = ok && wait(sums_bar, 0, 128);
       if (!ok) give_up(kErrTimeoutEpilogue);
       tc_fence_after();
     }
     const uint32_t pitch = BOXES * 64 * 4 + 16;
     const uint32_t part = v_base + row * pitch + h * half_cols * 4;
     const int used = kb1 > kb0 ? (kb1 - kb0 + run - 1) / run : 0;
+    {
+      float acc[COLS] = {};
+      for (int k = 0; ok && k < used; ++k) {
+        uint32_t d[COLS / 8][8];
+        const uint32_t at =
+            tmem + (static_cast<uint32_t>(q * 32) << 16) + k * (BOXES * 64) + h * half_cols;
 #pragma unroll
-    for (int c = 0; c < COLS; c += 8) {
-      if (c < half_cols) {
-        float acc[8] = {};
-        if (ok)
-          for (int k = 0; k < used; ++k) {
-            uint32_t d[8];
-            mx::tmem_ld_8cols(tmem + (static_cast<uint32_t>(q * 32) << 16) + k * (BOXES * 64) +
-                                  h * half_cols + c,
-                              d);
-            tmem_ld_wait();
+        for (int c = 0; c < COLS; c += 8)
+          if (c < half_cols) mx::tmem_ld_8cols(at + c, d[c / 8]);
+        tmem_ld_wait();
 #pragma unroll
-            for (int i = 0; i < 8; ++i) acc[i] += __uint_as_float(d[i]);
-          }
-        st_shared_v4(part + c * 4, make_float4(acc[0], acc[1], acc[2], acc[3]));
-        st_shared_v4(part + c * 4 + 16, make_float4(acc[4], acc[5], acc[6], acc[7]));
+        for (int c = 0; c < COLS; ++c)
+          if (c < half_cols) acc[c] += __uint_as_float(d[c / 8][c % 8]);
       }
+#pragma unroll
+      for (int c = 0; c < COLS; c += 4)
+        if (c < half_cols)
+          st_shared_v4(part + c * 4, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
     }
     cluster_sync_all();
     const float scale = p.scales ? p.scales[tile.a] : 1.f;
     uint32_t terms[TERMS][COLS / 2];
     float high = 0;
     {
-      float v[COLS];
+      float v[COLS] = {};
+      for (int k = 0; k < ctas; ++k) {  // a CTA's parts at once
+        const uint32_t from = mapa_shared(part, k);
+        float4 o[COLS / 4];
 #pragma unroll
-      for (int c = 0; c < COLS; c += 4) {
-        float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (c < half_cols)
-          for (int k = 0; k < ctas; ++k) {
-            const float4 o = ld_shared_cluster_v4(mapa_shared(part + c * 4, k));
-            s.x += o.x;
-            s.y += o.y;
-            s.z += o.z;
-            s.w += o.w;
+        for (int c = 0; c < COLS; c += 4)
+          if (c < half_cols) o[c / 4] = ld_shared_cluster_v4(from + c * 4);
+#pragma unroll
+        for (int c = 0; c < COLS; c += 4)
+          if (c < half_cols) {
+            v[c] += o[c / 4].x;
+            v[c + 1] += o[c / 4].y;
+            v[c + 2] += o[c / 4].z;
+            v[c + 3] += o[c / 4].w;
           }
-        v[c] = scale * s.x;
-        v[c + 1] = scale * s.y;
-        v[c + 2] = scale * s.z;
-        v[c + 3] = scale * s.w;
       }
+#pragma unroll
+      for (int c = 0; c < COLS; ++c) v[c] *= scale;
       float unit = 1.f;
       if constexpr (HALF) {
         // A power of two a row that brings its largest to [2^13, 2^14).
@@ -783,7 +823,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       const int col = box_col(i);
       const uint32_t slot = slot0 + i % p.slots * SLOT;
       const bool work = n_rows > 0 && col < p.N;
-      if (work && load) {
+      if (load) {
         if (!wait(y_bar(e, i % p.slots), (i / p.slots) & 1u)) {
           give_up(kErrTimeoutEpilogue);
           ok = false;
