@@ -244,7 +244,7 @@ constexpr int EPI_WARPS = 8;
 constexpr int EPI_THREADS = 32 * EPI_WARPS;
 constexpr int TILE_THREADS = 64 + EPI_THREADS;  // warp 0 loads, 1 multiplies, 2-9 the rest
 constexpr int SLOT = 32 * 128;                // 32 rows of y and of the output, 128 bytes each
-constexpr int MAX_STAGES = 6;
+constexpr int MAX_STAGES = 8;
 constexpr uint32_t TMEM_COLS = 512, ACC0 = 256;  // v's sums up to column 256, then the output's
 
 struct TileMaps {
@@ -259,7 +259,8 @@ struct TileParams {
   int64_t ldy, ldo;
   int32_t T, K, N, L, rank;
   int32_t pad;          // rank, in steps of 16
-  int32_t stages, slots;
+  int32_t stages, slots;  // of `up` and of y; x and `down` have the memory of both first
+  int32_t stages1;
   int32_t kind, copy;   // 0 fp16, 1 bf16; copy: rows without an adapter are copied
   int32_t rows_tma;     // y and the output can go by TMA
   uint32_t* status;
@@ -306,6 +307,13 @@ __device__ __forceinline__ void st_shared_u4(uint32_t addr, const uint4& v) {
                : "memory");
 }
 
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   if constexpr (std::is_same_v<T, __half>) {
@@ -332,11 +340,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     adapters_tile_kernel(const __grid_constant__ TileMaps maps, const TileParams p) {
   constexpr bool HALF = std::is_same_v<T, __half>, WIDE = sizeof(O) == 4;
   constexpr int TERMS = WIDE && !HALF ? 3 : 2;
-  constexpr int SUMS = 4 / BOXES;              // accumulators of v (see below)
+  constexpr int SUMS = WIDE ? 4 / BOXES : 1;   // accumulators of v (see below)
   constexpr int BOX_COLS = WIDE ? 32 : 64;     // of the output, 128 bytes
   constexpr int PARTS = 64 / BOX_COLS;         // boxes of a warp's half of a block
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t bars[2 * MAX_STAGES + 7 + 3 * EPI_WARPS];
+  __shared__ alignas(8) uint64_t bars[4 * MAX_STAGES + 7 + 3 * EPI_WARPS];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   __shared__ Tile tile_slot;
@@ -346,14 +354,16 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t bar0 = smem_u32(bars);
-  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };        // of x and `down`
   auto empty_bar = [&](int s) { return bar0 + 8u * (MAX_STAGES + s); };
-  auto acc_bar = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + b); };
-  auto free_bar = [&](int b) { return bar0 + 8u * (2 * MAX_STAGES + 2 + b); };
-  const uint32_t sums_bar = bar0 + 8u * (2 * MAX_STAGES + 4);
-  const uint32_t v_bar = bar0 + 8u * (2 * MAX_STAGES + 5);
-  const uint32_t drain_bar = bar0 + 8u * (2 * MAX_STAGES + 6);
-  auto y_bar = [&](int w, int s) { return bar0 + 8u * (2 * MAX_STAGES + 7 + 3 * w + s); };
+  auto up_bar = [&](int s) { return bar0 + 8u * (2 * MAX_STAGES + s); };
+  auto up_free_bar = [&](int s) { return bar0 + 8u * (3 * MAX_STAGES + s); };
+  auto acc_bar = [&](int b) { return bar0 + 8u * (4 * MAX_STAGES + b); };
+  auto free_bar = [&](int b) { return bar0 + 8u * (4 * MAX_STAGES + 2 + b); };
+  const uint32_t sums_bar = bar0 + 8u * (4 * MAX_STAGES + 4);
+  const uint32_t v_bar = bar0 + 8u * (4 * MAX_STAGES + 5);
+  const uint32_t drain_bar = bar0 + 8u * (4 * MAX_STAGES + 6);
+  auto y_bar = [&](int w, int s) { return bar0 + 8u * (4 * MAX_STAGES + 7 + 3 * w + s); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_ctarank());
   int ctas;
@@ -397,16 +407,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   const int kbs = (p.K + BK - 1) / BK, blocks = (p.N + BLOCK_N - 1) / BLOCK_N;
   const int kb0 = kbs * rank / ctas, kb1 = kbs * (rank + 1) / ctas;
   const int n0 = blocks * rank / ctas, n1 = blocks * (rank + 1) / ctas;
-  // Tiles begin at columns of their own: in step, all rows' accesses would fall on the same
-  // few channels of the memory where their pitch is a power of two.
-  auto kb_at = [&](int i) {
-    const int n = kb1 - kb0;
-    return kb0 + (i + tile_no * 7) % n;
-  };
-  auto block_at = [&](int i) {
-    const int n = n1 - n0;
-    return n0 + (i + tile_no * 3) % n;
-  };
   for (int i = threadIdx.x; i < TILE; i += TILE_THREADS)
     rows[i] = i < tile.count ? p.order[tile.first + i] : -1;
   __syncthreads();
@@ -427,9 +427,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
   const uint32_t ring = v_base + ((v_bytes + 1023) & ~1023u);
   const uint32_t slots = ring + p.stages * stage_bytes;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < p.stages; ++s) {
+    for (int s = 0; s < MAX_STAGES; ++s) {
       mbar_init(full_bar(s), 1);
       mbar_init(empty_bar(s), 1);
+      mbar_init(up_bar(s), 1);
+      mbar_init(up_free_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(acc_bar(b), 1);
@@ -462,8 +464,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
     __syncwarp();
   };
-  // v's sums go on in the next of SUMS accumulators every `run` stages: the tensor cores
-  // add by truncation, which takes some 1.4e-8 of a sum off for every 16 terms.
+  // For fp32 results v's sums go on in the next of SUMS accumulators every `run` stages:
+  // the tensor cores add by truncation, which takes some 1.4e-8 of a sum off for every 16
+  // terms.
   const int run = max(1, (kb1 - kb0 + SUMS - 1) / SUMS);
 
   if (warp == 0) {
@@ -479,33 +482,31 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
     const int a = __shfl_sync(ALL, tile.a, 0);
     const bool stall = p.inject_stall && blockIdx.x == 0;
-    uint32_t s = 0, ph = 1, it = 0;
+    uint32_t s = 0, ph = 1, it = 0, up_it = 0;
     bool ok = true;
     const uint32_t tx1 = TILE * 128 + v_cols * 128, tx2 = 2 * v_cols * 128;
-    auto next = [&](uint32_t tx) {  // the next place of the ring, armed
-      if (!wait(empty_bar(s), ph)) {
+    // place s of a ring of `of`, armed
+    auto next = [&](uint32_t full, uint32_t empty, uint32_t tx) {
+      if (!wait(empty, ph)) {
         give_up(kErrTimeoutProducer);
         ok = false;
-        return false;
+        return;
       }
-      if (lane == 0) mbar_arrive_expect_tx(full_bar(s), tx);
+      if (lane == 0) mbar_arrive_expect_tx(full, tx);
       __syncwarp();
-      return !(stall && it == 0);
     };
-    auto advance = [&] {
+    auto advance = [&](uint32_t of) {
       __syncwarp();
-      ++it;
-      if (++s == static_cast<uint32_t>(p.stages)) {
+      if (++s == of) {
         s = 0;
         ph ^= 1u;
       }
     };
-    for (int i = 0; ok && i < kb1 - kb0; ++i) {
-      const int kb = kb_at(i);
-      const bool go = next(tx1);
+    for (int kb = kb0; ok && kb < kb1; ++kb) {
+      next(full_bar(s), empty_bar(s), tx1);
       if (!ok) break;
       const uint32_t st = ring + s * stage_bytes, fb = full_bar(s);
-      if (go) {
+      if (!(stall && kb == kb0)) {
         if (elect_one()) {
           tma_load_3d(st + TILE * 128, &maps.down, fb, kb * BK, 0, a);
           if (whole) {
@@ -517,50 +518,63 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           }
         }
       }
-      advance();
+      ++it;
+      advance(p.stages1);
     }
-    auto load_up = [&](int i) {
-      const int n = block_at(i);
-      const bool go = next(tx2);
+    // The memory of x and `down` goes to `up` and y when v's sums are there.
+    s = 0;
+    ph = 1;
+    if (kb1 > kb0 && ok && !wait(sums_bar, 0)) {
+      give_up(kErrTimeoutProducer);
+      ok = false;
+    }
+    auto load_up = [&](int n) {
+      next(up_bar(s), up_free_bar(s), tx2);
       if (!ok) return;
-      const uint32_t st = ring + s * stage_bytes, fb = full_bar(s);
-      if (go && elect_one()) {
+      const uint32_t st = ring + s * stage_bytes, fb = up_bar(s);
+      if (!(stall && kb0 == kb1 && n == n0) && elect_one()) {
         tma_load_3d(st, &maps.up, fb, n * BLOCK_N, 0, a);
         tma_load_3d(st + v_cols * 128, &maps.up, fb, n * BLOCK_N + 64, 0, a);
       }
-      advance();
+      ++up_it;
+      advance(p.stages);
     };
-    // the ring's worth of `up` before the CTAs meet: its places come free by v's stages
-    int n = 0;
-    for (; ok && n < n1 - n0 && n < p.stages; ++n) load_up(n);
+    int n = n0;
+    for (; ok && n < n1 && n < n0 + p.stages; ++n) load_up(n);
     cluster_sync_all();
-    cluster_sync_all();
-    for (; ok && n < n1 - n0; ++n) load_up(n);
+    cluster_arrive();
+    cluster_wait();
+    for (; ok && n < n1; ++n) load_up(n);
     if (lane == 0) {  // what is still on its way, before the CTA may leave
       volatile int never = 0;
-      const uint32_t st = p.stages;
-      for (uint32_t i = it > st ? it - st : 0; i < it; ++i) {
-        if (stall && i == 0) {
-          mbar_wait_bounded(full_bar(0), 0, 2 * limit, &abort_flag);
-          mbar_complete_tx(full_bar(0), kb1 > kb0 ? tx1 : tx2);
+      auto drain = [&](auto bar, uint32_t of, uint32_t n, bool stalled, uint32_t tx) {
+        for (uint32_t i = n > of ? n - of : 0; i < n; ++i) {
+          if (stalled && i == 0) {
+            mbar_wait_bounded(bar(0), 0, 2 * limit, &abort_flag);
+            mbar_complete_tx(bar(0), tx);
+          }
+          if (!mbar_wait_bounded(bar(i % of), (i / of) & 1u, limit, &never))
+            atomicOr(p.status, kErrTimeoutDrain);
         }
-        if (!mbar_wait_bounded(full_bar(i % st), (i / st) & 1u, limit, &never))
-          atomicOr(p.status, kErrTimeoutDrain);
-      }
+      };
+      drain(full_bar, p.stages1, it, stall, tx1);
+      drain(up_bar, p.stages, up_it, stall && kb0 == kb1, tx2);
     }
     __syncwarp();
   } else if (warp == 1) {
     uint32_t s = 0, ph = 0;
     bool ok = true;
-    auto advance = [&] {
+    auto advance = [&](uint32_t of) {
       __syncwarp();
-      if (++s == static_cast<uint32_t>(p.stages)) {
+      if (++s == of) {
         s = 0;
         ph ^= 1u;
       }
     };
     const uint32_t id1 = make_idesc(p.kind, false, false, TILE, v_cols);
     const uint32_t id2 = make_idesc(p.kind, false, true, TILE, BLOCK_N);
+    int in = 0;           // stages that v's present accumulator has
+    uint32_t d = tmem;
     for (int kb = kb0; kb < kb1; ++kb) {
       if (!wait(full_bar(s), ph)) {
         give_up(kErrTimeoutMma);
@@ -569,8 +583,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       }
       tc_fence_after();
       const uint32_t st = ring + s * stage_bytes;
-      const int in = (kb - kb0) % run;
-      const uint32_t d = tmem + (kb - kb0) / run * (BOXES * 64);
+      if (in == run) {
+        in = 0;
+        d += BOXES * 64;
+      }
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
@@ -580,17 +596,20 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         mma_commit(empty_bar(s));
         if (kb + 1 == kb1) mma_commit(sums_bar);
       }
-      advance();
+      ++in;
+      advance(p.stages1);
     }
+    s = ph = 0;
     cluster_sync_all();
-    cluster_sync_all();
+    cluster_arrive();
+    cluster_wait();
     if (ok && n1 > n0 && !wait(v_bar, 0)) {
       give_up(kErrTimeoutMma);
       ok = false;
     }
     for (int n = n0; ok && n < n1; ++n) {
       const int t = n - n0, b = t & 1;
-      if ((t >= 2 && !wait(free_bar(b), ((t - 2) >> 1) & 1u)) || !wait(full_bar(s), ph)) {
+      if ((t >= 2 && !wait(free_bar(b), ((t - 2) >> 1) & 1u)) || !wait(up_bar(s), ph)) {
         give_up(kErrTimeoutMma);
         break;
       }
@@ -606,10 +625,10 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
                     smem_desc_sw128(st + kk * 2048, v_cols * 128, 1024), id2, more);
             more = 1;
           }
-        mma_commit(empty_bar(s));
+        mma_commit(up_free_bar(s));
         mma_commit(acc_bar(b));
       }
-      advance();
+      advance(p.stages);
     }
     if (elect_one()) mma_commit(drain_bar);
     __syncwarp();
@@ -635,7 +654,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const uint32_t slot0 = slots + e * p.slots * SLOT;
     const int boxes = n_rows > 0 ? (n1 - n0) * PARTS : 0;
     auto box_col = [&](int i) {
-      return block_at(i / PARTS) * BLOCK_N + h * 64 + i % PARTS * BOX_COLS;
+      return (n0 + i / PARTS) * BLOCK_N + h * 64 + i % PARTS * BOX_COLS;
     };
     int fetched = 0, done = 0;
     // y's box i into its slot
@@ -653,7 +672,6 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         if (!lie && lane < 8) tma_gather4(slot + lane * 512, &maps.y1, bar, col, four);
       }
     };
-    for (int i = 0; i < min(boxes, p.slots - 1); ++i) fetch(i);
     bool ok = true;
     // x's rows that lie in no box of 32: four gathers a warp, of 16 rows.  (An operand that
     // differs from lane to lane makes a TMA instruction some 60 cycles of the warp's; all
@@ -681,9 +699,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
           }
           if (lane < 4 && !(stall && i == 0))
             tma_gather4(ring + s * stage_bytes + (r0 + (e & 1) * 16) * 128 + lane * 512, &maps.x1,
-                        full_bar(s), kb_at(i) * BK, r);
+                        full_bar(s), (kb0 + i) * BK, r);
           __syncwarp();
-          if (++s == static_cast<uint32_t>(p.stages)) {
+          if (++s == static_cast<uint32_t>(p.stages1)) {
             s = 0;
             ph ^= 1u;
           }
@@ -698,12 +716,15 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       if (!ok) give_up(kErrTimeoutEpilogue);
       tc_fence_after();
     }
+    // (the slots have been x's until now)
+    for (int i = 0; ok && i < min(boxes, p.slots - 1); ++i) fetch(i);
     const uint32_t pitch = BOXES * 64 * 4 + 16;
     const uint32_t part = v_base + row * pitch + h * half_cols * 4;
     const int used = kb1 > kb0 ? (kb1 - kb0 + run - 1) / run : 0;
-    {
-      float acc[COLS] = {};
-      for (int k = 0; ok && k < used; ++k) {
+    float v[COLS] = {};
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k) {
+      if (ok && k < used) {
         uint32_t d[COLS / 8][8];
         const uint32_t at =
             tmem + (static_cast<uint32_t>(q * 32) << 16) + k * (BOXES * 64) + h * half_cols;
@@ -713,21 +734,24 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         tmem_ld_wait();
 #pragma unroll
         for (int c = 0; c < COLS; ++c)
-          if (c < half_cols) acc[c] += __uint_as_float(d[c / 8][c % 8]);
+          if (c < half_cols) v[c] += __uint_as_float(d[c / 8][c % 8]);
       }
+    }
+    if (ctas > 1) {
 #pragma unroll
       for (int c = 0; c < COLS; c += 4)
         if (c < half_cols)
-          st_shared_v4(part + c * 4, make_float4(acc[c], acc[c + 1], acc[c + 2], acc[c + 3]));
+          st_shared_v4(part + c * 4, make_float4(v[c], v[c + 1], v[c + 2], v[c + 3]));
     }
     cluster_sync_all();
     const float scale = p.scales ? p.scales[tile.a] : 1.f;
     uint32_t terms[TERMS][COLS / 2];
     float high = 0;
     {
-      float v[COLS] = {};
-      for (int k = 0; k < ctas; ++k) {  // a CTA's parts at once
-        const uint32_t from = mapa_shared(part, k);
+      // The others' parts, a CTA's at once: 32 KB of 64 columns, which take some 2000 cycles
+      // to come.
+      for (int i = 1; i < ctas; ++i) {
+        const uint32_t from = mapa_shared(part, (rank + i) % ctas);
         float4 o[COLS / 4];
 #pragma unroll
         for (int c = 0; c < COLS; c += 4)
@@ -743,6 +767,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       }
 #pragma unroll
       for (int c = 0; c < COLS; ++c) v[c] *= scale;
+      cluster_arrive();  // this thread has read the parts
       float unit = 1.f;
       if constexpr (HALF) {
         // A power of two a row that brings its largest to [2^13, 2^14).
@@ -775,7 +800,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         }
       }
     }
-    cluster_sync_all();  // all parts are read: the terms take their place
+    cluster_wait();  // all have: the terms take the parts' place
 #pragma unroll
     for (int k = 0; k < TERMS; ++k)
 #pragma unroll
@@ -997,6 +1022,8 @@ cudaError_t launch_tiles(const AdapterArgs& a, const AdapterParams& r, TileParam
   static_assert(STAGES >= 2, "shared memory");
   constexpr int SMEM = V + STAGES * STAGE + SLOTS * EPI_WARPS * SLOT + 1024;
   p.stages = STAGES;
+  constexpr int STAGES1 = (STAGES * STAGE + SLOTS * EPI_WARPS * SLOT) / STAGE;
+  p.stages1 = STAGES1 < MAX_STAGES ? STAGES1 : MAX_STAGES;
   p.slots = SLOTS;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
