@@ -4,8 +4,14 @@
 // A warp takes a token.  Its lanes split into `groups` runs of `per` lanes (a power
 // of two), a run holds one group's logits in registers, neighbours in neighbouring
 // registers; so a group's two best are a few shuffles inside the run, and the first
-// lane and register with a value is the one of the lowest index.  The best keys are
-// taken one by one: the largest of a lane's, then of the warp's.
+// lane and register with a value is the one of the lowest index.  Each lane sorts its
+// keys; the best of all are then taken one by one from the lists' heads.
+//
+// Bound by the issue of instructions, not by the logits' bytes (16384 x 256 fp32 logits
+// are 2.5 us of the memory's time): keys are integers that order as the floats do,
+// sorted by minima and maxima alone, their indices found again for the chosen; a token
+// with a NaN, or with keys too near for 32 bits, is done again in double by a function
+// of its own.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -49,7 +55,6 @@ __device__ __forceinline__ double key_value(uint64_t k) {
                     : __longlong_as_double(static_cast<long long>(k >> 63 ? k ^ (1ull << 63) : ~k));
 }
 
-__device__ __forceinline__ uint32_t warp_max(uint32_t k) { return __reduce_max_sync(ALL, k); }
 __device__ __forceinline__ uint64_t warp_max(uint64_t k) {
   const uint32_t hi = __reduce_max_sync(ALL, static_cast<uint32_t>(k >> 32));
   const uint32_t lo =
@@ -110,16 +115,6 @@ __device__ __forceinline__ void load_lane(const T* at, int left, bool vec, float
   }
 }
 
-// What a choice leaves in lane j <= top: the j-th best key, its expert and logit
-// (expert -1 past the last); `near`: whether groups were too near one another.
-template <typename F>
-struct Chosen {
-  F key;
-  int expert;
-  float logit;
-  bool near;
-};
-
 // Of a softmax: the row's maximum and its sum; 0 for both where all are -inf.
 template <typename F, int V>
 __device__ __forceinline__ void softmax_sums(const float (&l)[V], int count, float& most, F& sum) {
@@ -144,156 +139,286 @@ __device__ __forceinline__ F score_of(float l, int kind, float most, F sum) {
   return sum == 0 ? F(0) : exp_of(static_cast<F>(l) - static_cast<F>(most)) / sum;
 }
 
-// How far a key of 32 bits may lie from its value: the score's few roundings (expf
-// 2 ulp, sums of up to 32 + 5 terms, a division: below 2^-20 of the score together),
-// the sum with the bias 2^-24 of the key.  Twice that between two of them.
-constexpr float NEAR = 0x1p-19f;
+// The lanes' share of the row: group, first expert, number of experts.
+struct Share {
+  int group, first, count;
+};
+__device__ __forceinline__ Share share_of(const ChooseParams& p, int lane) {
+  Share s;
+  s.group = lane / p.per;
+  const int sub = lane - s.group * p.per;
+  s.count = s.group < p.groups ? max(0, min(p.each, p.size - sub * p.each)) : 0;
+  s.first = s.count ? s.group * p.size + sub * p.each : 0;
+  return s;
+}
 
-template <typename F, int V>
-__device__ __forceinline__ Chosen<F> choose(const float (&l)[V], const ChooseParams& p, int lane,
-                                            int first, int count, bool scored, float most,
-                                            F sum) {
-  using Key = std::conditional_t<sizeof(F) == 4, uint32_t, uint64_t>;
-  Key key[V];
-  Key score1 = 0, score2 = 0;  // the lane's two best scores, where groups add up scores
-  const bool sums = p.groups > 1 && p.top2;
+// The choice in double: lane j <= top gets the j-th best expert (-1 past the last) and
+// its logit; *sum the softmax's.  Every NaN is the largest.
+template <typename T, int V>
+__device__ __noinline__ void choose_double(const ChooseParams& p, int t, int lane, int* expert,
+                                           float* logit, float* most_out, float* sum_out) {
+  const Share sh = share_of(p, lane);
+  const int first = sh.first, count = sh.count;
+  float l[V];
+  load_lane<T, V>(static_cast<const T*>(p.logits) + t * p.ld + first, count, p.vec != 0, l);
+  const bool scored = p.bias != nullptr, sums = p.groups > 1 && p.top2;
+  float most = 0;
+  double sum = 0;
+  if (p.score == MHR_SOFTMAX) softmax_sums<double>(l, count, most, sum);
+  uint64_t key[V];
+  uint64_t score1 = 0, score2 = 0;  // the lane's two best scores, where groups add up scores
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     key[i] = 0;
     if (i < count) {
-      F v = static_cast<F>(l[i]);
+      double v = l[i];
       if (scored || sums) {
-        const F s = score_of<F>(l[i], p.score, most, sum) +
-                    (p.bias ? static_cast<F>(p.bias[first + i]) : F(0));
+        const double s =
+            score_of<double>(l[i], p.score, most, sum) + (p.bias ? p.bias[first + i] : 0.0);
         if (scored) v = s;
-        const Key k = ordered(s);
+        const uint64_t k = ordered(s);
         score2 = max(score2, min(score1, k));
         score1 = max(score1, k);
       }
       key[i] = ordered(v);
     }
   }
-  Chosen<F> c;
-  c.near = false;
   if (p.groups > 1) {
-    Key worth;
+    uint64_t worth = 0;
     if (sums) {
       for (int m = 1; m < p.per; m <<= 1) {
-        const Key o1 = __shfl_xor_sync(ALL, score1, m), o2 = __shfl_xor_sync(ALL, score2, m);
+        const uint64_t o1 = __shfl_xor_sync(ALL, score1, m), o2 = __shfl_xor_sync(ALL, score2, m);
         score2 = max(max(score2, o2), min(score1, o1));
         score1 = max(score1, o1);
       }
       // (a group of one has no second)
-      worth = score1 ? ordered(p.size > 1 ? key_value(score1) + key_value(score2)
-                                          : key_value(score1))
-                     : Key(0);
+      if (score1)
+        worth = ordered(p.size > 1 ? key_value(score1) + key_value(score2) : key_value(score1));
     } else {
-      worth = 0;
 #pragma unroll
       for (int i = 0; i < V; ++i) worth = max(worth, key[i]);
       for (int m = 1; m < p.per; m <<= 1) worth = max(worth, __shfl_xor_sync(ALL, worth, m));
     }
-    const int mine = lane / p.per;
     bool open = false;
-    Key last = 0;
     for (int g = 0; g < p.group_top; ++g) {
-      last = warp_max(open ? Key(0) : worth);
-      const int winner = (__ffs(__ballot_sync(ALL, !open && worth == last)) - 1) / p.per;
-      if (mine == winner) open = true;
-    }
-    if (scored || sums) {  // is the best of the closed ones as good?
-      const Key next = warp_max(open ? Key(0) : worth);
-      const float a = static_cast<float>(key_value(last)), b = static_cast<float>(key_value(next));
-      // (scores are at most 1, and a group's are at least its worth less its biases)
-      const float room = NEAR * (fabsf(a) + 2.f);
-      c.near = next && !(a - b > room) && a == a;
+      const uint64_t best = warp_max(open ? uint64_t{0} : worth);
+      if (sh.group == (__ffs(__ballot_sync(ALL, !open && worth == best)) - 1) / p.per) open = true;
     }
     if (!open) {
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = 0;
     }
   }
-  c.key = 0;
-  c.expert = -1;
-  c.logit = 0;
+  *expert = -1;
+  *logit = 0;
   for (int j = 0; j <= p.top; ++j) {
-    Key best = 0;
+    uint64_t best = 0;
     int at = 0;
+    float mine = 0;
 #pragma unroll
     for (int i = V - 1; i >= 0; --i)
       if (key[i] >= best) {
         best = key[i];
         at = i;
+        mine = l[i];
       }
-    const Key m = warp_max(best);
+    const uint64_t m = warp_max(best);
     if (m == 0) break;
     const int owner = __ffs(__ballot_sync(ALL, best == m)) - 1;
-    float logit = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (at == i) {
-        logit = l[i];
-        if (lane == owner) key[i] = 0;
-      }
-    const int expert = __shfl_sync(ALL, first + at, owner);
-    logit = __shfl_sync(ALL, logit, owner);
+      if (at == i && lane == owner) key[i] = 0;
+    const int e = __shfl_sync(ALL, first + at, owner);
+    mine = __shfl_sync(ALL, mine, owner);
     if (lane == j) {
-      c.key = key_value(m);
-      c.expert = expert;
-      c.logit = logit;
+      *expert = e;
+      *logit = mine;
     }
   }
-  return c;
+  *most_out = most;
+  *sum_out = static_cast<float>(sum);
+}
+
+// Floats that are no NaN as signed integers in the same order; -0 has to be 0.
+__device__ __forceinline__ int sortable(float v) {
+  const int b = __float_as_int(v);
+  return b ^ (b >> 31 & 0x7fffffff);
+}
+__device__ __forceinline__ float of_sortable(int k) {
+  return __int_as_float(k ^ (k >> 31 & 0x7fffffff));
+}
+constexpr int NONE = -0x7fffffff - 1;  // below every key
+
+// Descending, by a merge-exchange network.
+template <int V>
+__device__ __forceinline__ void sort_descending(int (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int q = p; q >= 1; q /= 2)
+#pragma unroll
+      for (int j = q % p; j + q < V; j += 2 * q)
+#pragma unroll
+        for (int i = 0; i < q; ++i)
+          if (i + j + q < V && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+            const int a = k[i + j], b = k[i + j + q];
+            k[i + j] = max(a, b);
+            k[i + j + q] = min(a, b);
+          }
+}
+
+// A key's score is off by expf's 2 ulp, a sum, a reciprocal and a product: 3.5 * 2^-23 of
+// it at most, and of a softmax by the rounding of its argument (2^-24 of up to 16 or so;
+// what is further down is too small to matter beside a bias) and its sum's: 2^-20; the
+// sum with the bias by 2^-24 of the key.
+__device__ __forceinline__ float near_by(int kind, float s, float s1, float key) {
+  return (kind == MHR_SIGMOID ? 0x1p-21f : 0x1p-19f) * (s + s1) + 0x1p-22f * fabsf(key);
 }
 
 template <typename T, int V>
 __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const ChooseParams p) {
-  const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * WARPS + (threadIdx.x >> 5);
+  __shared__ alignas(16) int originals[WARPS][V * 32], lists[WARPS][V * 32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * WARPS + warp;
   if (t >= p.T) return;
-  const int group = lane / p.per, sub = lane - group * p.per;
-  int count = group < p.groups ? min(p.each, p.size - sub * p.each) : 0;
-  if (count < 0) count = 0;
-  const int first = count ? group * p.size + sub * p.each : 0;
+  const Share sh = share_of(p, lane);
   float l[V];
-  load_lane<T, V>(static_cast<const T*>(p.logits) + t * p.ld + first, count, p.vec != 0, l);
+  load_lane<T, V>(static_cast<const T*>(p.logits) + t * p.ld + sh.first, sh.count, p.vec != 0, l);
 
   // Without a bias the logits' own order is the scores'.
   const bool scored = p.bias != nullptr, sums = p.groups > 1 && p.top2;
   const bool softmax = p.score == MHR_SOFTMAX;
+  bool again = false;  // in double
   float most = 0, sum = 0;
-  if (softmax && (scored || sums || !p.renormalize)) softmax_sums<float>(l, count, most, sum);
-  Chosen<float> c = choose<float, V>(l, p, lane, first, count, scored, most, sum);
-  float s = c.expert >= 0 ? score_of<float>(c.logit, p.score, most, sum) : 0.f;
-
-  // Neighbours that 32 bits do not tell apart, unless they are the same numbers.
-  bool near = c.near;
-  if (scored) {
-    const float k1 = __shfl_down_sync(ALL, c.key, 1), l1 = __shfl_down_sync(ALL, c.logit, 1);
-    const float s1 = __shfl_down_sync(ALL, s, 1);
-    const int e1 = __shfl_down_sync(ALL, c.expert, 1);
-    if (lane < p.top && e1 >= 0) {
-      const bool same = c.logit == l1 && p.bias[c.expert] == p.bias[e1];
-      near |= !same && !(c.key - k1 > NEAR * (s + s1 + fabsf(c.key))) && c.key == c.key;
+  if (softmax && (scored || sums || !p.renormalize)) {
+    most = -infinity();
+#pragma unroll
+    for (int i = 0; i < V; ++i) most = fmaxf(most, l[i]);  // (-inf past the count)
+    most = of_sortable(__reduce_max_sync(ALL, sortable(most)));
+    float part = 0;
+    if (most > -infinity()) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) part += expf(l[i] - most);
+    }
+    sum = warp_sum(part);
+    if (sum == 0) most = 0;
+    again = sum != sum;  // (a NaN or an infinity)
+  }
+  int key[V];
+  {
+    const float r = sum == 0 ? 0.f : __fdividef(1.f, sum);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float v = l[i] + 0.f;
+      if (scored) {
+        const float e = expf(softmax ? l[i] - most : -l[i]);
+        v = (softmax ? e * r : __fdividef(1.f, 1.f + e)) +
+            (i < sh.count ? p.bias[sh.first + i] : 0.f);
+        if (!softmax && e > 0x1p126f) v = i < sh.count ? p.bias[sh.first + i] : 0.f;
+      }
+      again |= v != v;
+      key[i] = i < sh.count ? sortable(v) : NONE;
     }
   }
-  if (__any_sync(ALL, near)) {
-    double sum64 = 0;
-    if (softmax) softmax_sums<double>(l, count, most, sum64);
-    const Chosen<double> d = choose<double, V>(l, p, lane, first, count, scored, most, sum64);
-    c.expert = d.expert;
-    c.logit = d.logit;
-    if (softmax) sum = static_cast<float>(sum64);
-    s = c.expert >= 0 ? score_of<float>(c.logit, p.score, most, sum) : 0.f;
+  int* original = originals[warp] + lane * V;
+  int* list = lists[warp] + lane * V;
+#pragma unroll
+  for (int i = 0; i < V; ++i) original[i] = key[i];
+  sort_descending<V>(key);
+#pragma unroll
+  for (int i = 0; i < V; ++i) list[i] = key[i];
+  int head = key[0];
+  if (p.groups > 1) {
+    int best = key[0], second = V > 1 ? key[V > 1 ? 1 : 0] : NONE;
+    for (int m = 1; m < p.per; m <<= 1) {
+      const int o = __shfl_xor_sync(ALL, best, m);
+      if (sums) second = max(max(second, __shfl_xor_sync(ALL, second, m)), min(best, o));
+      best = max(best, o);
+    }
+    int worth = best;
+    if (sums && best != NONE) {
+      float a = of_sortable(best), b = of_sortable(second);
+      if (!scored) {
+        a = score_of<float>(a, p.score, most, sum);
+        b = score_of<float>(b, p.score, most, sum);
+      }
+      a = p.size > 1 ? a + b : a;  // (a group of one has no second)
+      again |= a != a;
+      worth = sortable(a + 0.f);
+    }
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const int other = __shfl_sync(ALL, worth, g * p.per);
+      rank += other > worth || (other == worth && g < sh.group);
+    }
+    const bool open = sh.group < p.groups && rank < p.group_top;
+    if (scored || sums) {  // is the best of the closed ones as good?
+      const float a = of_sortable(__reduce_min_sync(ALL, open ? worth : 0x7f800000));
+      const int closed = __reduce_max_sync(ALL, open ? NONE : worth);
+      // (two scores of at most 1 each)
+      if (closed != NONE)
+        again |= !(a - of_sortable(closed) > near_by(p.score, 2.f, 2.f, fabsf(a) + 4.f));
+    }
+    if (!open) head = NONE;
+  }
+  __syncwarp();
+  // The best of the heads, one by one: lane j keeps the j-th, whose it is, and how many
+  // equal ones of that lane came before it.
+  int mine = NONE, owner = 0, taken = 0;
+  for (int j = 0; j <= p.top; ++j) {
+    const int m = __reduce_max_sync(ALL, head);
+    const int o = __ffs(__ballot_sync(ALL, head == m)) - 1;
+    if (lane == j) {
+      mine = m;
+      owner = o;
+    }
+    if (lane == o) {
+      ++taken;
+      head = taken < V && m != NONE ? list[taken] : NONE;
+    }
+  }
+  const int k1 = __shfl_up_sync(ALL, mine, 1), o1 = __shfl_up_sync(ALL, owner, 1);
+  const uint32_t starts = __ballot_sync(ALL, lane == 0 || k1 != mine || o1 != owner);
+  int before = lane - (31 - __clz(starts & (0xffffffffu >> (31 - lane))));
+  int expert = -1;
+  if (lane <= p.top && mine != NONE) {
+    int at = 0;
+#pragma unroll
+    for (int i = V - 1; i >= 0; --i) at = originals[warp][owner * V + i] == mine ? i : at;
+    if (before)  // (equal keys in one lane)
+      for (int i = at + 1; i < V && before; ++i)
+        if (originals[warp][owner * V + i] == mine) {
+          at = i;
+          --before;
+        }
+    const int group = owner / p.per;
+    expert = group * p.size + (owner - group * p.per) * p.each + at;
+  }
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+  float logit = expert >= 0 ? to_float(row[expert]) : 0.f;
+  float s = expert >= 0 ? score_of<float>(logit, p.score, most, sum) : 0.f;
+
+  // Neighbours that 32 bits do not tell apart, unless they are the same numbers.
+  if (scored) {
+    const float key = of_sortable(mine), key1 = __shfl_down_sync(ALL, key, 1);
+    const float l1 = __shfl_down_sync(ALL, logit, 1), s1 = __shfl_down_sync(ALL, s, 1);
+    const float b = expert >= 0 ? p.bias[expert] : 0.f, b1 = __shfl_down_sync(ALL, b, 1);
+    const int e1 = __shfl_down_sync(ALL, expert, 1);
+    if (lane < p.top && e1 >= 0)
+      again |= !(logit == l1 && b == b1) && !(key - key1 > near_by(p.score, s, s1, key));
+  }
+  if (__any_sync(ALL, again)) {
+    choose_double<T, V>(p, t, lane, &expert, &logit, &most, &sum);
+    s = expert >= 0 ? score_of<float>(logit, p.score, most, sum) : 0.f;
   }
 
   float w = s;
   if (p.renormalize) {
     const bool in = lane < p.top;
-    const float high = warp_max_float(in ? c.logit : -infinity());
+    const float high = warp_max_float(in ? logit : -infinity());
     // sigmoids of logits this low are e^x but for 1e-26 of them
     if (softmax || high < -60.f) {
-      w = in && high != -infinity() ? expf(c.logit - high) : 0.f;
+      w = in && high != -infinity() ? expf(logit - high) : 0.f;
     } else {
       w = in ? s : 0.f;
     }
@@ -302,7 +427,7 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const ChooseParams p
   }
   if (lane < p.top) {
     const int64_t at = static_cast<int64_t>(t) * p.top + lane;
-    p.experts[at] = c.expert;
+    p.experts[at] = expert;
     p.weights[at] = p.scale * w;
   }
 }
