@@ -88,7 +88,8 @@ struct ChooseParams {
   float* weights;
   int64_t ld;
   int32_t T, E, top, groups, group_top;
-  int32_t size, per, each;  // experts a group, lanes a group, experts a lane
+  int32_t size, per, each;  // experts a group, lanes a group (2^per_log2), experts a lane
+  int32_t per_log2;
   int32_t score, top2, renormalize, vec;
   float scale;
 };
@@ -145,98 +146,95 @@ struct Share {
 };
 __device__ __forceinline__ Share share_of(const ChooseParams& p, int lane) {
   Share s;
-  s.group = lane / p.per;
-  const int sub = lane - s.group * p.per;
+  s.group = lane >> p.per_log2;
+  const int sub = lane & (p.per - 1);
   s.count = s.group < p.groups ? max(0, min(p.each, p.size - sub * p.each)) : 0;
   s.first = s.count ? s.group * p.size + sub * p.each : 0;
   return s;
 }
 
 // The choice in double: lane j <= top gets the j-th best expert (-1 past the last) and
-// its logit; *sum the softmax's.  Every NaN is the largest.
+// its logit; most and sum are the softmax's.  Every NaN is the largest.
+struct Choice {
+  int expert;
+  float logit, most, sum;
+};
+// Few tokens come here, one or two at a time, so it is short, in loops over the shared
+// memory at `work` (32 V numbers): unrolled, 14 us of such a token's time went by until
+// its instructions were there.
 template <typename T, int V>
-__device__ __noinline__ void choose_double(const ChooseParams& p, int t, int lane, int* expert,
-                                           float* logit, float* most_out, float* sum_out) {
+__device__ __noinline__ Choice choose_double(const ChooseParams& p, int t, int lane,
+                                             uint64_t* work) {
   const Share sh = share_of(p, lane);
-  const int first = sh.first, count = sh.count;
-  float l[V];
-  load_lane<T, V>(static_cast<const T*>(p.logits) + t * p.ld + first, count, p.vec != 0, l);
-  const bool scored = p.bias != nullptr, sums = p.groups > 1 && p.top2;
-  float most = 0;
-  double sum = 0;
-  if (p.score == MHR_SOFTMAX) softmax_sums<double>(l, count, most, sum);
-  uint64_t key[V];
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld + sh.first;
+  const bool scored = p.bias != nullptr, softmax = p.score == MHR_SOFTMAX;
+  const bool sums = p.groups > 1 && p.top2;
+  uint32_t high = 0;  // (ordered: below -inf)
+#pragma unroll 1
+  for (int i = 0; i < sh.count; ++i) high = max(high, ordered(to_float(row[i])));
+  float most = key_value(__reduce_max_sync(ALL, high));
+  if (most == -infinity()) most = 0;
+  uint64_t* mine = work + lane;  // every 32nd
+  double part = 0;
+#pragma unroll 1
+  for (int i = 0; i < sh.count; ++i) {
+    const double x = to_float(row[i]);
+    const double e = exp(softmax ? x - most : -fabs(x));
+    mine[32 * i] = __double_as_longlong(e);
+    part += e;
+  }
+  const double sum = softmax ? warp_sum(part) : 0;
   uint64_t score1 = 0, score2 = 0;  // the lane's two best scores, where groups add up scores
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    key[i] = 0;
-    if (i < count) {
-      double v = l[i];
-      if (scored || sums) {
-        const double s =
-            score_of<double>(l[i], p.score, most, sum) + (p.bias ? p.bias[first + i] : 0.0);
-        if (scored) v = s;
-        const uint64_t k = ordered(s);
-        score2 = max(score2, min(score1, k));
-        score1 = max(score1, k);
-      }
-      key[i] = ordered(v);
-    }
+  uint64_t best = 0;                // and its best key
+#pragma unroll 1
+  for (int i = 0; i < sh.count; ++i) {
+    const double x = to_float(row[i]), e = __longlong_as_double(mine[32 * i]);
+    const double of = softmax ? (sum == 0 ? 1.0 : sum) : 1 + e;
+    const double s = (!softmax && x >= 0 ? 1.0 : e) / of + (scored ? p.bias[sh.first + i] : 0.f);
+    const uint64_t k = ordered(s), key = scored ? k : ordered(x);
+    score2 = max(score2, min(score1, k));
+    score1 = max(score1, k);
+    best = max(best, key);
+    mine[32 * i] = key;
   }
   if (p.groups > 1) {
-    uint64_t worth = 0;
-    if (sums) {
-      for (int m = 1; m < p.per; m <<= 1) {
-        const uint64_t o1 = __shfl_xor_sync(ALL, score1, m), o2 = __shfl_xor_sync(ALL, score2, m);
-        score2 = max(max(score2, o2), min(score1, o1));
-        score1 = max(score1, o1);
-      }
-      // (a group of one has no second)
-      if (score1)
-        worth = ordered(p.size > 1 ? key_value(score1) + key_value(score2) : key_value(score1));
-    } else {
-#pragma unroll
-      for (int i = 0; i < V; ++i) worth = max(worth, key[i]);
-      for (int m = 1; m < p.per; m <<= 1) worth = max(worth, __shfl_xor_sync(ALL, worth, m));
+    uint64_t worth = best;
+    if (sums) worth = score1;
+    for (int m = 1; m < p.per; m <<= 1) {
+      const uint64_t o1 = __shfl_xor_sync(ALL, worth, m), o2 = __shfl_xor_sync(ALL, score2, m);
+      score2 = max(max(score2, o2), min(worth, o1));
+      worth = max(worth, o1);
     }
+    // (a group of one has no second)
+    if (sums && worth && p.size > 1) worth = ordered(key_value(worth) + key_value(score2));
     bool open = false;
+#pragma unroll 1
     for (int g = 0; g < p.group_top; ++g) {
-      const uint64_t best = warp_max(open ? uint64_t{0} : worth);
-      if (sh.group == (__ffs(__ballot_sync(ALL, !open && worth == best)) - 1) / p.per) open = true;
+      const uint64_t m = warp_max(open ? uint64_t{0} : worth);
+      if (sh.group == (__ffs(__ballot_sync(ALL, !open && worth == m)) - 1) >> p.per_log2)
+        open = true;
     }
-    if (!open) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) key[i] = 0;
-    }
+    if (!open) best = 0;
   }
-  *expert = -1;
-  *logit = 0;
+  Choice c{-1, 0.f, most, static_cast<float>(sum)};
+#pragma unroll 1
   for (int j = 0; j <= p.top; ++j) {
-    uint64_t best = 0;
-    int at = 0;
-    float mine = 0;
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i)
-      if (key[i] >= best) {
-        best = key[i];
-        at = i;
-        mine = l[i];
-      }
     const uint64_t m = warp_max(best);
     if (m == 0) break;
     const int owner = __ffs(__ballot_sync(ALL, best == m)) - 1;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (at == i && lane == owner) key[i] = 0;
-    const int e = __shfl_sync(ALL, first + at, owner);
-    mine = __shfl_sync(ALL, mine, owner);
-    if (lane == j) {
-      *expert = e;
-      *logit = mine;
+    int at = 0;
+    if (lane == owner) {  // takes the first of it, and looks for its next
+      while (mine[32 * at] != m) ++at;
+      mine[32 * at] = 0;
+      best = 0;
+#pragma unroll 1
+      for (int i = 0; i < sh.count; ++i) best = max(best, mine[32 * i]);
     }
+    const int e = __shfl_sync(ALL, sh.first + at, owner);
+    if (lane == j) c.expert = e;
   }
-  *most_out = most;
-  *sum_out = static_cast<float>(sum);
+  if (c.expert >= 0) c.logit = to_float(row[c.expert - sh.first]);
+  return c;
 }
 
 // Floats that are no NaN as signed integers in the same order; -0 has to be 0.
@@ -275,13 +273,53 @@ __device__ __forceinline__ float near_by(int kind, float s, float s1, float key)
   return (kind == MHR_SIGMOID ? 0x1p-21f : 0x1p-19f) * (s + s1) + 0x1p-22f * fabsf(key);
 }
 
+// The order of 32 candidates, a lane each, best first but for neighbours too near: by
+// their keys in double, neighbour by neighbour until none changes places.
 template <typename T, int V>
-__global__ void __launch_bounds__(WARPS * 32) choose_kernel(const ChooseParams p) {
-  __shared__ alignas(16) int originals[WARPS][V * 32], lists[WARPS][V * 32];
+__device__ __noinline__ Choice refine(const ChooseParams& p, int t, int lane, int expert,
+                                      float logit, float most) {
+  double sum = 0;
+  if (p.score == MHR_SOFTMAX) {
+    const Share sh = share_of(p, lane);
+    float l[V];
+    load_lane<T, V>(static_cast<const T*>(p.logits) + t * p.ld + sh.first, sh.count, p.vec != 0, l);
+    double part = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) part += exp(static_cast<double>(l[i]) - most);
+    sum = warp_sum(part);
+  }
+  uint64_t key = 0;
+  if (expert >= 0)
+    key = ordered(score_of<double>(logit, p.score, most, sum) + p.bias[expert]);
+  for (int round = 0, still = 0; round < 32 && still < 2; ++round) {
+    const int with = (lane ^ 1) - (round & 1 ? ((lane & 1) ? -2 : 2) : 0);  // the neighbour
+    const bool pair = with >= 0 && with < 32;
+    const int from = pair ? with : lane;
+    const uint64_t k = __shfl_sync(ALL, key, from);
+    const int e = __shfl_sync(ALL, expert, from);
+    const float x = __shfl_sync(ALL, logit, from);
+    // the lower lane takes the better: of equal keys the lower expert; none is the worst
+    const bool other_better = k > key || (k == key && k != 0 && e < expert);
+    const bool mine_better = key > k || (k == key && k != 0 && expert < e);
+    const bool change = pair && (lane < with ? other_better : mine_better);
+    if (change) {
+      key = k;
+      expert = e;
+      logit = x;
+    }
+    still = __any_sync(ALL, change) ? 0 : still + 1;
+  }
+  return Choice{expert, logit, most, static_cast<float>(sum)};
+}
+
+template <typename T, int V>
+__global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constant__ ChooseParams p) {
+  __shared__ alignas(16) int shared[WARPS][2][V * 32];  // keys as they lie, and sorted
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int t = blockIdx.x * WARPS + warp;
   if (t >= p.T) return;
   const Share sh = share_of(p, lane);
+  grid_dependency_wait();
   float l[V];
   load_lane<T, V>(static_cast<const T*>(p.logits) + t * p.ld + sh.first, sh.count, p.vec != 0, l);
 
@@ -320,8 +358,9 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const ChooseParams p
       key[i] = i < sh.count ? sortable(v) : NONE;
     }
   }
-  int* original = originals[warp] + lane * V;
-  int* list = lists[warp] + lane * V;
+  const int* originals = shared[warp][0];
+  int* original = shared[warp][0] + lane * V;
+  int* list = shared[warp][1] + lane * V;
 #pragma unroll
   for (int i = 0; i < V; ++i) original[i] = key[i];
   sort_descending<V>(key);
@@ -365,50 +404,76 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const ChooseParams p
   // The best of the heads, one by one: lane j keeps the j-th, whose it is, and how many
   // equal ones of that lane came before it.
   int mine = NONE, owner = 0, taken = 0;
-  for (int j = 0; j <= p.top; ++j) {
-    const int m = __reduce_max_sync(ALL, head);
-    const int o = __ffs(__ballot_sync(ALL, head == m)) - 1;
-    if (lane == j) {
-      mine = m;
-      owner = o;
+  auto take = [&](int from, int to) {
+    for (int j = from; j < to; ++j) {
+      const int m = __reduce_max_sync(ALL, head);
+      const int o = __ffs(__ballot_sync(ALL, head == m)) - 1;
+      if (lane == j) {
+        mine = m;
+        owner = o;
+      }
+      if (lane == o) {
+        ++taken;
+        head = taken < V && m != NONE ? list[taken] : NONE;
+      }
     }
-    if (lane == o) {
-      ++taken;
-      head = taken < V && m != NONE ? list[taken] : NONE;
-    }
-  }
-  const int k1 = __shfl_up_sync(ALL, mine, 1), o1 = __shfl_up_sync(ALL, owner, 1);
-  const uint32_t starts = __ballot_sync(ALL, lane == 0 || k1 != mine || o1 != owner);
-  int before = lane - (31 - __clz(starts & (0xffffffffu >> (31 - lane))));
-  int expert = -1;
-  if (lane <= p.top && mine != NONE) {
-    int at = 0;
-#pragma unroll
-    for (int i = V - 1; i >= 0; --i) at = originals[warp][owner * V + i] == mine ? i : at;
-    if (before)  // (equal keys in one lane)
-      for (int i = at + 1; i < V && before; ++i)
-        if (originals[warp][owner * V + i] == mine) {
-          at = i;
-          --before;
-        }
-    const int group = owner / p.per;
-    expert = group * p.size + (owner - group * p.per) * p.each + at;
-  }
+  };
   const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  float logit = expert >= 0 ? to_float(row[expert]) : 0.f;
-  float s = expert >= 0 ? score_of<float>(logit, p.score, most, sum) : 0.f;
+  int expert;
+  float logit, s;
+  auto look_up = [&](int lanes) {
+    const int k1 = __shfl_up_sync(ALL, mine, 1), o1 = __shfl_up_sync(ALL, owner, 1);
+    const uint32_t starts = __ballot_sync(ALL, lane == 0 || k1 != mine || o1 != owner);
+    int before = lane - (31 - __clz(starts & (0xffffffffu >> (31 - lane))));
+    expert = -1;
+    if (lane < lanes && mine != NONE) {
+      int at = 0;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i) at = originals[owner * V + i] == mine ? i : at;
+      if (before)  // (equal keys in one lane)
+        for (int i = at + 1; i < V && before; ++i)
+          if (originals[owner * V + i] == mine) {
+            at = i;
+            --before;
+          }
+      expert = (owner >> p.per_log2) * p.size + (owner & (p.per - 1)) * p.each + at;
+    }
+    logit = expert >= 0 ? to_float(row[expert]) : 0.f;
+    s = expert >= 0 ? score_of<float>(logit, p.score, most, sum) : 0.f;
+  };
+  take(0, p.top + 1);
+  look_up(p.top + 1);
 
   // Neighbours that 32 bits do not tell apart, unless they are the same numbers.
+  bool near = false;
   if (scored) {
     const float key = of_sortable(mine), key1 = __shfl_down_sync(ALL, key, 1);
     const float l1 = __shfl_down_sync(ALL, logit, 1), s1 = __shfl_down_sync(ALL, s, 1);
     const float b = expert >= 0 ? p.bias[expert] : 0.f, b1 = __shfl_down_sync(ALL, b, 1);
     const int e1 = __shfl_down_sync(ALL, expert, 1);
     if (lane < p.top && e1 >= 0)
-      again |= !(logit == l1 && b == b1) && !(key - key1 > near_by(p.score, s, s1, key));
+      near = !(logit == l1 && b == b1) && !(key - key1 > near_by(p.score, s, s1, key));
   }
-  if (__any_sync(ALL, again)) {
-    choose_double<T, V>(p, t, lane, &expert, &logit, &most, &sum);
+  near = __any_sync(ALL, near);
+  again = __any_sync(ALL, again);
+  if (near && !again) {
+    // 32 candidates, if the last of them is out of the question for sure.
+    take(p.top + 1, 32);
+    look_up(32);
+    const float key = of_sortable(mine);
+    const float last = __shfl_sync(ALL, key, p.top - 1), s0 = __shfl_sync(ALL, s, p.top - 1);
+    const bool far = mine == NONE || last - key > near_by(p.score, s0, s, fabsf(last) + fabsf(key));
+    again = !__shfl_sync(ALL, static_cast<int>(far), 31);
+  }
+  if (again || near) {
+    __syncwarp();
+    const Choice c = again ? choose_double<T, V>(p, t, lane,
+                                                 reinterpret_cast<uint64_t*>(shared[warp][0]))
+                           : refine<T, V>(p, t, lane, expert, logit, most);
+    expert = c.expert;
+    logit = c.logit;
+    most = c.most;
+    sum = c.sum;
     s = expert >= 0 ? score_of<float>(logit, p.score, most, sum) : 0.f;
   }
 
@@ -458,6 +523,7 @@ __global__ void __launch_bounds__(WARPS * 32) choose_grad_kernel(const GradParam
   const int first = lane * V, count = max(0, min(V, p.E - first));
   const bool whole = p.score == MHR_SOFTMAX && !p.renormalize;
 
+  grid_dependency_wait();
   int e = -1;
   float g = 0, l = -infinity();
   if (lane < p.top) {
@@ -554,6 +620,23 @@ cudaError_t by_type_and_width(int dtype, int each, const F& f) {
   return width(__half{});
 }
 
+// A warp a token, set up while the kernel before still runs.
+template <typename P>
+cudaError_t launch_tokens(void (*kern)(P), const P& p, int64_t T, cudaStream_t s) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((T + WARPS - 1) / WARPS));
+  cfg.blockDim = dim3(WARPS * 32);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  note_launch();
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_choose(const ChooseArgs& a, cudaStream_t s) {
@@ -569,8 +652,9 @@ cudaError_t launch_choose(const ChooseArgs& a, cudaStream_t s) {
   p.groups = a.group_top == a.groups ? 1 : static_cast<int32_t>(a.groups);  // all stay: no choice
   p.group_top = static_cast<int32_t>(a.group_top);
   p.size = p.E / p.groups;
-  p.per = 32;
-  while (p.per * p.groups > 32) p.per >>= 1;
+  p.per_log2 = 5;
+  while (p.groups << p.per_log2 > 32) --p.per_log2;
+  p.per = 1 << p.per_log2;
   p.each = (p.size + p.per - 1) / p.per;
   p.score = a.score;
   p.top2 = a.group_score == MHR_GROUP_TOP2;
@@ -581,10 +665,7 @@ cudaError_t launch_choose(const ChooseArgs& a, cudaStream_t s) {
     // lanes take whole vectors where a group splits into them
     if (p.size % V == 0 && p.size / V <= p.per) p.each = V;
     p.vec = aligned16(a.logits, a.ld * size_of(a.dtype)) && p.each == V && p.size % V == 0;
-    choose_kernel<decltype(tag), V>
-        <<<static_cast<unsigned>((a.T + WARPS - 1) / WARPS), WARPS * 32, 0, s>>>(p);
-    note_launch();
-    return cudaGetLastError();
+    return launch_tokens(choose_kernel<decltype(tag), V>, p, a.T, s);
   });
 }
 
@@ -606,10 +687,7 @@ cudaError_t launch_choose_grad(const ChooseGradArgs& a, cudaStream_t s) {
   p.vec_out = aligned16(a.grad_logits, a.ldg * size_of(a.dtype));
   return by_type_and_width(a.dtype, (p.E + 31) / 32, [&](auto tag, auto width) {
     constexpr int V = decltype(width)::value;
-    choose_grad_kernel<decltype(tag), V>
-        <<<static_cast<unsigned>((a.T + WARPS - 1) / WARPS), WARPS * 32, 0, s>>>(p);
-    note_launch();
-    return cudaGetLastError();
+    return launch_tokens(choose_grad_kernel<decltype(tag), V>, p, a.T, s);
   });
 }
 

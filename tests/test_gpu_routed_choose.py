@@ -110,6 +110,30 @@ def test_neighbours_that_32_bits_do_not_tell_apart(mhr, groups):
     assert near.max() < 2.0 ** -24  # the case is what it says
 
 
+@pytest.mark.parametrize("E,groups", [(20, 1), (128, 1), (128, 4), (300, 1)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_a_few_such_neighbours(mhr, E, groups, score):
+    """Some of the best keys in runs of such neighbours, the others far off."""
+    import torch
+
+    rng = np.random.default_rng(7)
+    T, top = 300, 8
+    x = rng.uniform(-3, 3, (T, E)).astype(np.float32)
+    x[:, E // 2:] = x[0, E // 2:]  # one row's bias undoes the differences in all
+    x -= x.mean()
+    bias = np.zeros(E, np.float32)
+    if score == "softmax":  # alike sums: the other half's logits are low
+        x[:, :E // 2] -= 30
+    s = ref.scores(x.astype(np.float64), score)[0]
+    run = np.arange(E // 2, E // 2 + 6)
+    bias[run] = (s.max() + 0.5 - s[run]).astype(np.float32)
+    bias[run[3:]] -= 0.1
+    check(mhr, torch.from_numpy(x).cuda(), top, score=score, bias=bias, groups=groups,
+          group_top=max(1, groups - 1))
+    keys = np.sort(s + bias)[::-1]
+    assert np.diff(-keys[:3]).max() < 2.0 ** -23 and keys[2] - keys[3] > 0.05
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_masked_and_special_logits(mhr, score, renormalize):
