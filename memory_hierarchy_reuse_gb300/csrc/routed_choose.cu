@@ -74,11 +74,13 @@ __device__ __forceinline__ F warp_sum(F v) {
 
 __device__ __forceinline__ float exp_of(float x) { return expf(x); }
 __device__ __forceinline__ double exp_of(double x) { return exp(x); }
+__device__ __forceinline__ float quotient(float a, float b) { return __fdividef(a, b); }  // (2 ulp)
+__device__ __forceinline__ double quotient(double a, double b) { return a / b; }
 // e^x / (1 + e^x) from the side on which nothing overflows.
 template <typename F>
 __device__ __forceinline__ F sigmoid(F x) {
   const F e = exp_of(x < 0 ? x : -x);
-  return x < 0 ? e / (1 + e) : 1 / (1 + e);
+  return quotient(x < 0 ? e : F(1), 1 + e);
 }
 
 struct ChooseParams {
@@ -91,6 +93,7 @@ struct ChooseParams {
   int32_t size, per, each;  // experts a group, lanes a group (2^per_log2), experts a lane
   int32_t per_log2;
   int32_t score, top2, renormalize, vec;
+  int32_t vec_bias;
   float scale;
 };
 
@@ -224,7 +227,7 @@ __device__ __noinline__ Choice choose_double(const ChooseParams& p, int t, int l
     const int owner = __ffs(__ballot_sync(ALL, best == m)) - 1;
     int at = 0;
     if (lane == owner) {  // takes the first of it, and looks for its next
-      while (mine[32 * at] != m) ++at;
+      while (at + 1 < sh.count && mine[32 * at] != m) ++at;
       mine[32 * at] = 0;
       best = 0;
 #pragma unroll 1
@@ -265,12 +268,12 @@ __device__ __forceinline__ void sort_descending(int (&k)[V]) {
           }
 }
 
-// A key's score is off by expf's 2 ulp, a sum, a reciprocal and a product: 3.5 * 2^-23 of
-// it at most, and of a softmax by the rounding of its argument (2^-24 of up to 16 or so;
+// A key's score is off by expf's 2 ulp, a sum and a quotient: 5 * 2^-23 of it at most, and
+// of a softmax by the rounding of its argument (2^-24 of up to 16 or so;
 // what is further down is too small to matter beside a bias) and its sum's: 2^-20; the
 // sum with the bias by 2^-24 of the key.
 __device__ __forceinline__ float near_by(int kind, float s, float s1, float key) {
-  return (kind == MHR_SIGMOID ? 0x1p-21f : 0x1p-19f) * (s + s1) + 0x1p-22f * fabsf(key);
+  return (kind == MHR_SIGMOID ? 0x1p-20f : 0x1p-19f) * (s + s1) + 0x1p-22f * fabsf(key);
 }
 
 // The order of 32 candidates, a lane each, best first but for neighbours too near: by
@@ -312,6 +315,44 @@ __device__ __noinline__ Choice refine(const ChooseParams& p, int t, int lane, in
   return Choice{expert, logit, most, static_cast<float>(sum)};
 }
 
+// Whether this lane's group stays, its worth taken in double from the lanes' two best keys:
+// the `at0`-th and `at1`-th of their experts (-1: there is none).
+template <typename T, int V>
+__device__ __noinline__ bool open_in_double(const ChooseParams& p, int t, int lane, int at0,
+                                            int at1, float most) {
+  const Share sh = share_of(p, lane);
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld + sh.first;
+  double sum = 0;
+  if (p.score == MHR_SOFTMAX) {
+#pragma unroll 1
+    for (int i = 0; i < sh.count; ++i) sum += exp(static_cast<double>(to_float(row[i])) - most);
+    sum = warp_sum(sum);
+  }
+  uint64_t key[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int at = i ? at1 : at0;
+    key[i] = 0;
+    if (at >= 0)
+      key[i] = ordered(score_of<double>(to_float(row[at]), p.score, most, sum) +
+                       (p.bias ? p.bias[sh.first + at] : 0.f));
+  }
+  uint64_t score1 = max(key[0], key[1]), score2 = min(key[0], key[1]);
+  for (int m = 1; m < p.per; m <<= 1) {
+    const uint64_t o1 = __shfl_xor_sync(ALL, score1, m), o2 = __shfl_xor_sync(ALL, score2, m);
+    score2 = max(max(score2, o2), min(score1, o1));
+    score1 = max(score1, o1);
+  }
+  if (p.top2 && score1 && p.size > 1) score1 = ordered(key_value(score1) + key_value(score2));
+  int rank = 0;
+#pragma unroll 1
+  for (int g = 0; g < p.groups; ++g) {
+    const uint64_t other = __shfl_sync(ALL, score1, g << p.per_log2);
+    rank += other > score1 || (other == score1 && g < sh.group);
+  }
+  return sh.group < p.groups && rank < p.group_top;
+}
+
 template <typename T, int V>
 __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constant__ ChooseParams p) {
   __shared__ alignas(16) int shared[WARPS][2][V * 32];  // keys as they lie, and sorted
@@ -345,15 +386,13 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constan
   int key[V];
   {
     const float r = sum == 0 ? 0.f : __fdividef(1.f, sum);
+    float bias[V];
+    if (scored) load_lane<float, V>(p.bias + sh.first, sh.count, p.vec_bias != 0, bias);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float v = l[i] + 0.f;
-      if (scored) {
-        const float e = expf(softmax ? l[i] - most : -l[i]);
-        v = (softmax ? e * r : __fdividef(1.f, 1.f + e)) +
-            (i < sh.count ? p.bias[sh.first + i] : 0.f);
-        if (!softmax && e > 0x1p126f) v = i < sh.count ? p.bias[sh.first + i] : 0.f;
-      }
+      if (scored) v = (softmax ? expf(l[i] - most) * r : sigmoid(l[i])) + bias[i];
+      if (i >= sh.count) v = 0.f;
       again |= v != v;
       key[i] = i < sh.count ? sortable(v) : NONE;
     }
@@ -390,13 +429,28 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constan
       const int other = __shfl_sync(ALL, worth, g * p.per);
       rank += other > worth || (other == worth && g < sh.group);
     }
-    const bool open = sh.group < p.groups && rank < p.group_top;
+    bool open = sh.group < p.groups && rank < p.group_top;
     if (scored || sums) {  // is the best of the closed ones as good?
       const float a = of_sortable(__reduce_min_sync(ALL, open ? worth : 0x7f800000));
       const int closed = __reduce_max_sync(ALL, open ? NONE : worth);
-      // (two scores of at most 1 each)
-      if (closed != NONE)
-        again |= !(a - of_sortable(closed) > near_by(p.score, 2.f, 2.f, fabsf(a) + 4.f));
+      // (scores of at most 1: one, or two, of either)
+      const float n = sums ? 2.f : 1.f;
+      if (closed != NONE && !(a - of_sortable(closed) > near_by(p.score, n, n, 4.f * (fabsf(a) + n)))) {
+        // The lanes' best two in double, if the third is not one of them as well.
+        const int first = key[0], next = key[V > 1 ? 1 : 0];
+        int at0 = -1, at1 = -1;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (i < sh.count && original[i] == first) at0 = i;
+#pragma unroll
+        for (int i = V - 1; i >= 0; --i)
+          if (i < sh.count && i != at0 && original[i] == next) at1 = i;
+        if (V > 2 && sh.count > 2) {
+          const float third = of_sortable(key[V > 2 ? 2 : 0]), second = of_sortable(next);
+          again |= !(second - third > near_by(p.score, 1.f, 1.f, 4.f * (fabsf(second) + 1.f)));
+        }
+        open = open_in_double<T, V>(p, t, lane, at0, at1, most);
+      }
     }
     if (!open) head = NONE;
   }
@@ -439,7 +493,7 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constan
       expert = (owner >> p.per_log2) * p.size + (owner & (p.per - 1)) * p.each + at;
     }
     logit = expert >= 0 ? to_float(row[expert]) : 0.f;
-    s = expert >= 0 ? score_of<float>(logit, p.score, most, sum) : 0.f;
+    s = score_of<float>(logit, p.score, most, sum);
   };
   take(0, p.top + 1);
   look_up(p.top + 1);
@@ -474,10 +528,10 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constan
     logit = c.logit;
     most = c.most;
     sum = c.sum;
-    s = expert >= 0 ? score_of<float>(logit, p.score, most, sum) : 0.f;
+    s = score_of<float>(logit, p.score, most, sum);
   }
 
-  float w = s;
+  float w = expert >= 0 ? s : 0.f;
   if (p.renormalize) {
     const bool in = lane < p.top;
     const float high = warp_max_float(in ? logit : -infinity());
@@ -488,7 +542,7 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constan
       w = in ? s : 0.f;
     }
     const float total = warp_sum(w);
-    w = total == 0 ? 0.f : w / total;
+    w = total == 0 ? 0.f : __fdividef(w, total);
   }
   if (lane < p.top) {
     const int64_t at = static_cast<int64_t>(t) * p.top + lane;
@@ -665,6 +719,7 @@ cudaError_t launch_choose(const ChooseArgs& a, cudaStream_t s) {
     // lanes take whole vectors where a group splits into them
     if (p.size % V == 0 && p.size / V <= p.per) p.each = V;
     p.vec = aligned16(a.logits, a.ld * size_of(a.dtype)) && p.each == V && p.size % V == 0;
+    p.vec_bias = aligned16(a.bias, 0) && p.each == V && p.size % V == 0;
     return launch_tokens(choose_kernel<decltype(tag), V>, p, a.T, s);
   });
 }
