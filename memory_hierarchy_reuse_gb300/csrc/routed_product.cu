@@ -45,7 +45,7 @@ constexpr int A_BYTES = HALF * BK * 2;       // this CTA's features
 constexpr int BOX = 64 * 128;                // 64 rows of 128 bytes
 constexpr int EPI_WARPS = 8;
 constexpr int CLASSES = 8;                   // of experts, by what their units cost
-constexpr int THREADS = 32 * (2 + EPI_WARPS);
+constexpr int THREADS = 32 * (3 + EPI_WARPS);
 
 enum Mode { PRODUCT = 0, TRANSPOSED = 1, GRADIENT = 2 };
 
@@ -329,8 +329,8 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Param
 }
 
 // Warp roles, barriers and the way a timeout unwinds are those of the other pair
-// kernels (mxfp4_pair.cu): warp 0 producer, warp 1 MMA issuer (rank 0), warps 2-9
-// epilogue; full[s] and released[b] in rank 0, empty[s] and acc_full[b] in both CTAs.
+// kernels (mxfp4_pair.cu): warps 0 and 10 producers, of either side, warp 1 MMA issuer
+// (rank 0), warps 2-9 epilogue; full[.][s] and released[b] in rank 0, empty[s] and acc_full[b] in both CTAs.
 // Rank 1's epilogue hands an accumulator back to its own read[b], from where its warp 1,
 // idle otherwise, tells rank 0: an arrival that is released to the cluster waits for the
 // stores that its thread has under way.
@@ -340,25 +340,26 @@ __global__ void __launch_bounds__(THREADS, 1)
   using S = Shape<LONG>;
   constexpr int STAGES = S::STAGES, ROWS = S::ROWS, STAGE_BYTES = S::STAGE_BYTES;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t bars[2 * STAGES + 8];
+  __shared__ alignas(8) uint64_t bars[3 * STAGES + 9];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
-  __shared__ volatile uint32_t peer_loaded;          // rank 0: stages that rank 1 loaded
-  __shared__ volatile uint32_t stage_tx[STAGES];     // bytes of a CTA's last load of a stage
-  __shared__ volatile uint32_t peer_tx[STAGES];      // rank 0: rank 1's
+  // Of either side (0: features, 1: rows):
+  __shared__ volatile uint32_t peer_loaded[2];        // rank 0: stages that rank 1 loaded
+  __shared__ volatile uint32_t stage_tx[2][STAGES];   // bytes of a CTA's last load of a stage
+  __shared__ volatile uint32_t peer_tx[2][STAGES];    // rank 0: rank 1's
   __shared__ uint32_t parts[MAX_PARTS + 1];
   __shared__ int32_t expert[MAX_PARTS], lo[MAX_PARTS], num[MAX_PARTS];
   __shared__ uint32_t class_units[CLASSES], class_experts[CLASSES];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
-  auto full_bar = [&](uint32_t s) { return bar0 + 8u * s; };
-  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (STAGES + s); };
-  auto acc_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + b); };
-  auto released_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 2 + b); };
-  auto read_bar = [&](uint32_t b) { return bar0 + 8u * (2 * STAGES + 4 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 6);
-  const uint32_t peer_done_bar = bar0 + 8u * (2 * STAGES + 7);
+  auto full_bar = [&](int side, uint32_t s) { return bar0 + 8u * (side * STAGES + s); };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + s); };
+  auto acc_bar = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + b); };
+  auto released_bar = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
+  auto read_bar = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + 4 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 6);
+  auto peer_done_bar = [&](int side) { return bar0 + 8u * (3 * STAGES + 7 + side); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -367,7 +368,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
-      mbar_init(full_bar(s), 1);
+      mbar_init(full_bar(0, s), 1);
+      mbar_init(full_bar(1, s), 1);
       mbar_init(empty_bar(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -376,9 +378,11 @@ __global__ void __launch_bounds__(THREADS, 1)
       mbar_init(read_bar(b), EPI_WARPS);
     }
     mbar_init(drain_bar, 1);
-    mbar_init(peer_done_bar, 1);
+    for (int side = 0; side < 2; ++side) {
+      mbar_init(peer_done_bar(side), 1);
+      peer_loaded[side] = 0;
+    }
     abort_flag = 0;
-    peer_loaded = 0;
     fence_mbar_init();
     if (p.K > 0) {
       tma_prefetch_desc(&maps.w[2]);
@@ -449,18 +453,25 @@ __global__ void __launch_bounds__(THREADS, 1)
     abort_flag = 1;
     st_shared_cluster_u32(peer_abort, 1u);
   };
-  if (warp == 0) {
+  // One side's loads, by a warp of its own: a TMA instruction takes the warp that issues it
+  // a hundred cycles and more, and a gather, whose operands differ from lane to lane, 60 a
+  // lane.
+  auto load = [&](auto which) {
+    constexpr int side = decltype(which)::value;
     uint32_t it = 0, s = 0, ph = 1;  // stages armed and loaded; ring position, phase to wait for
     const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
-    const uint32_t fb0 = mapa_shared(full_bar(0), 0);
+    const uint32_t fb0 = mapa_shared(full_bar(side, 0), 0);
     bool ok = true;
+    auto same = [](int v) { return __shfl_sync(ALL, v, 0); };  // (in a uniform register)
     for (uint32_t u = cluster; ok && u < units; u += clusters) {
       const Unit w = unit_at<MODE, ROWS>(u, p, table);
-      const int kbs = (w.sum + BK - 1) / BK, half = w.width / 2;
-      const int f = w.f0 + static_cast<int>(rank) * HALF;
-      const int mine = w.first + static_cast<int>(rank) * half;  // this CTA's first row
+      const int kbs = same((w.sum + BK - 1) / BK), half = same(w.width / 2);
+      const int expert = same(w.expert), sum0 = same(w.sum0), sum = same(w.sum);
+      // this CTA's first feature, or row
+      const int mine = same(side == 0 ? w.f0 + static_cast<int>(rank) * HALF
+                                      : w.first + static_cast<int>(rank) * half);
       int32_t r[4];  // gather: this lane's four rows
-      if constexpr (INDEXED) {
+      if constexpr (INDEXED && side == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int at = static_cast<int>(rank) * half + 4 * lane + i;
@@ -475,63 +486,70 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        const uint32_t st = sbase + s * STAGE_BYTES, fb = fb0 + 8u * s;
-        const int rows = min(BK, w.sum - kb * BK);         // gradient: positions of this stage,
-        const int read = (rows + 15) & ~15;                // and those that the MMAs read
-        const uint32_t tx = MODE == GRADIENT ? (2 + S::B_BYTES / BOX) * 128 * read
-                                             : A_BYTES + half * 128;
+        const uint32_t st = sbase + s * STAGE_BYTES + side * A_BYTES, fb = fb0 + 8u * s;
+        const int rows = min(BK, sum - kb * BK);  // gradient: positions of this stage,
+        const int read = (rows + 15) & ~15;       // and those that the MMAs read
+        constexpr int BOXES = side == 0 ? 2 : S::B_BYTES / BOX;  // gradient: of 64 features
+        const uint32_t tx = MODE == GRADIENT ? BOXES * 128 * read
+                            : side == 0      ? A_BYTES
+                                             : half * 128;
         if (lane == 0) {
-          stage_tx[s] = tx;
-          if (leader) mbar_arrive_expect_tx(full_bar(s), 2 * tx);
+          stage_tx[side][s] = tx;
+          if (leader) mbar_arrive_expect_tx(full_bar(side, s), 2 * tx);
         }
         __syncwarp();
         if (!(stall && it == 0)) {
           if constexpr (MODE == GRADIENT) {
-            // 64 features a box; the first two on the features' side
-            constexpr int BOXES = 2 + S::B_BYTES / BOX;
-            const int pos = w.sum0 + kb * BK;
+            const CUtensorMap* map = side == 0 ? maps.w : maps.x;
+            const int pos = sum0 + kb * BK;
             if (rows == BK) {
               if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < BOXES; ++i)
-                  tma_load_2d_pair(st + i * BOX, i < 2 ? &maps.w[2] : &maps.x[2], fb,
-                                   i < 2 ? f + 64 * i : mine + 64 * (i - 2), pos);
+                  tma_load_2d_pair(st + i * BOX, map + 2, fb, mine + 64 * i, pos);
               }
             } else {
               // An expert's last rows: in boxes, and the last of sixteen by the gather,
               // which ends in zeros and not in the next expert's rows.
               const int whole = rows & ~15;
-              const int i = lane % BOXES, g = lane / BOXES;
-              const int column = i < 2 ? f + 64 * i : mine + 64 * (i - 2);
-              if (g < 2 && (whole & (16 << g))) {
-                const int at = whole & ~((32 << g) - 1);  // behind the larger box
-                tma_load_2d_pair(st + i * BOX + at * 128, i < 2 ? &maps.w[g] : &maps.x[g], fb,
-                                 column, pos + at);
+              if (elect_one()) {
+#pragma unroll
+                for (int g = 0; g < 2; ++g)
+                  if (whole & (16 << g)) {
+                    const int at = whole & ~((32 << g) - 1);  // behind the larger box
+#pragma unroll
+                    for (int i = 0; i < BOXES; ++i)
+                      tma_load_2d_pair(st + i * BOX + at * 128, map + g, fb, mine + 64 * i,
+                                       pos + at);
+                  }
               }
-              if (read > whole && g < 4) {
-                const int at = whole + 4 * g;
+              __syncwarp();
+              if (read > whole && lane < 4 * BOXES) {
+                const int i = lane % BOXES, at = whole + 4 * (lane / BOXES);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) r[j] = at + j < rows ? pos + at + j : p.rows;
-                tma_gather4_pair(st + i * BOX + at * 128, i < 2 ? &maps.w1 : &maps.x1, fb, column,
-                                 r);
+                tma_gather4_pair(st + i * BOX + at * 128, side == 0 ? &maps.w1 : &maps.x1, fb,
+                                 mine + 64 * i, r);
               }
             }
-          } else {
+          } else if constexpr (side == 0) {
             if (elect_one()) {
               if constexpr (MODE == PRODUCT) {
-                tma_load_3d_pair(st, &maps.w[2], fb, f, kb * BK, w.expert);
-                tma_load_3d_pair(st + BOX, &maps.w[2], fb, f + 64, kb * BK, w.expert);
+                tma_load_3d_pair(st, &maps.w[2], fb, mine, kb * BK, expert);
+                tma_load_3d_pair(st + BOX, &maps.w[2], fb, mine + 64, kb * BK, expert);
               } else {
-                tma_load_3d_pair(st, &maps.w[2], fb, kb * BK, f, w.expert);
+                tma_load_3d_pair(st, &maps.w[2], fb, kb * BK, mine, expert);
               }
             }
-            if constexpr (INDEXED) {
-              if (4 * lane < half)
-                tma_gather4_pair(st + A_BYTES + lane * 512, &maps.x1, fb, kb * BK, r);
-            } else if (lane < 4 && (half & (16 << lane))) {
-              const int at = half & ~((32 << lane) - 1);  // behind the larger boxes
-              tma_load_2d_pair(st + A_BYTES + at * 128, &maps.x[lane], fb, kb * BK, mine + at);
-            }
+          } else if constexpr (INDEXED) {
+            if (4 * lane < half) tma_gather4_pair(st + lane * 512, &maps.x1, fb, kb * BK, r);
+          } else if (elect_one()) {
+#pragma unroll
+            for (int i = 3; i >= 0; --i)
+              if (half & (16 << i)) {
+                const int at = half & ~((32 << i) - 1);  // behind the larger boxes
+                tma_load_2d_pair(st + at * 128, &maps.x[i], fb, kb * BK, mine + at);
+              }
           }
         }
         __syncwarp();
@@ -543,19 +561,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     if (lane == 0) {
       // Both CTAs' loads complete in rank 0, which waits for all of them -- counting as
-      // done what either side never issued -- before either CTA may leave.
+      // done what either CTA never issued -- before either may leave.
       volatile int never = 0;
       if (!leader) {
         for (int i = 0; i < STAGES; ++i)
-          st_shared_cluster_u32(mapa_shared(smem_u32(const_cast<uint32_t*>(peer_tx + i)), 0),
-                                stage_tx[i]);
+          st_shared_cluster_u32(
+              mapa_shared(smem_u32(const_cast<uint32_t*>(&peer_tx[side][i])), 0),
+              stage_tx[side][i]);
         st_shared_cluster_u32(
-            mapa_shared(smem_u32(const_cast<uint32_t*>(&peer_loaded)), 0), it);
-        mbar_arrive_cluster(mapa_shared(peer_done_bar, 0));
+            mapa_shared(smem_u32(const_cast<uint32_t*>(&peer_loaded[side])), 0), it);
+        mbar_arrive_cluster(mapa_shared(peer_done_bar(side), 0));
       } else {
         uint32_t it1 = it;
-        if (mbar_wait_bounded<true>(peer_done_bar, 0, 2 * limit, &never))
-          it1 = peer_loaded;
+        if (mbar_wait_bounded<true>(peer_done_bar(side), 0, 2 * limit, &never))
+          it1 = peer_loaded[side];
         else
           atomicOr(p.status, kErrTimeoutDrain);
         const uint32_t hi = it > it1 ? it : it1;
@@ -563,21 +582,27 @@ __global__ void __launch_bounds__(THREADS, 1)
           const uint32_t si = i % STAGES, phi = (i / STAGES) & 1u;
           const bool armed = i < it, loaded0 = armed && !(stall && i == 0), loaded1 = i < it1;
           if (!armed) {
-            mbar_arrive_expect_tx(full_bar(si), peer_tx[si]);
+            mbar_arrive_expect_tx(full_bar(side, si), peer_tx[side][si]);
           } else {
-            const uint32_t missing =
-                (loaded0 ? 0u : stage_tx[si]) + (loaded1 ? 0u : stage_tx[si]);
+            const uint32_t tx = stage_tx[side][si];
+            const uint32_t missing = (loaded0 ? 0u : tx) + (loaded1 ? 0u : tx);
             if (missing) {  // once the MMA issuer has given up on the stage
-              mbar_wait_bounded(full_bar(si), phi, 2 * limit, &abort_flag);
-              mbar_complete_tx(full_bar(si), missing);
+              mbar_wait_bounded(full_bar(side, si), phi, 2 * limit, &abort_flag);
+              mbar_complete_tx(full_bar(side, si), missing);
             }
           }
-          if (!mbar_wait_bounded(full_bar(si), phi, limit, &never))
+          if (!mbar_wait_bounded(full_bar(side, si), phi, limit, &never))
             atomicOr(p.status, kErrTimeoutDrain);
         }
       }
     }
     __syncwarp();
+  };
+
+  if (warp == 0) {
+    load(std::integral_constant<int, 0>{});
+  } else if (warp == 2 + EPI_WARPS) {
+    load(std::integral_constant<int, 1>{});
   } else if (warp == 1) {
     if (leader) {
       uint32_t t = 0, s = 0, ph = 0;  // accumulators filled; ring position and its phase
@@ -596,7 +621,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int kb = 0; kb < kbs; ++kb) {
           const int in = LONG ? kb % S::SEGMENT : kb;
           const bool last = kb + 1 == kbs || (LONG && in + 1 == S::SEGMENT);
-          if ((in == 0 && !next()) || !wait(full_bar(s), ph)) {
+          if ((in == 0 && !next()) || !wait(full_bar(0, s), ph) || !wait(full_bar(1, s), ph)) {
             if (lane == 0) give_up(kErrTimeoutMma);
             ok = false;
             break;
