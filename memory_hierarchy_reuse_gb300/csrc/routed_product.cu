@@ -40,9 +40,13 @@ using mx::tma_load_3d_pair;
 constexpr uint32_t ALL = 0xffffffffu;
 constexpr int TILE_F = 256;                  // features of a pair's tile
 constexpr int HALF = 128;
-constexpr int BK = 64;                       // of the sum a stage: one swizzle row of 128 bytes
+// Of the sum a stage: two swizzle rows of 128 bytes.  A stage costs the issuing warps some
+// 300 cycles whatever it holds; with 64 an MMA of few rows was done long before (319 MB of
+// weights for eight rows in 105 us).
+constexpr int BK = 128;
 constexpr int A_BYTES = HALF * BK * 2;       // this CTA's features
-constexpr int BOX = 64 * 128;                // 64 rows of 128 bytes
+constexpr int BOX = 128 * 128;               // 128 rows of 128 bytes
+constexpr int MAX_STAGES = 6;
 constexpr int EPI_WARPS = 8;
 constexpr int CLASSES = 8;                   // of experts, by what their units cost
 constexpr int THREADS = 32 * (3 + EPI_WARPS);
@@ -58,11 +62,10 @@ template <bool LONG>
 struct Shape {
   static constexpr int ROWS = LONG ? 128 : 256;            // rows of a pair's tile, at most
   static constexpr int B_BYTES = ROWS / 2 * BK * 2;        // this CTA's half of them
-  static constexpr int STAGE_BYTES = A_BYTES + B_BYTES;    // 24 or 32 KB
-  static constexpr int STAGES = LONG ? 7 : 6;
-  static constexpr int SEGMENT = LONG ? 6 : 1 << 30;       // stages an accumulator takes
+  static constexpr int RING_BYTES = LONG ? 168 * 1024 : 192 * 1024;
+  static constexpr int SEGMENT = LONG ? 3 : 1 << 30;       // stages an accumulator takes
   static constexpr int PIECE_BYTES = 32 * 32 * (LONG ? 4 : 2);  // of an epilogue warp
-  static constexpr int SMEM = STAGES * STAGE_BYTES + EPI_WARPS * PIECE_BYTES + 1024;
+  static constexpr int SMEM = RING_BYTES + EPI_WARPS * PIECE_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * ROWS;
 };
 
@@ -104,14 +107,33 @@ __device__ __forceinline__ void tma_gather4_pair(uint32_t dst, const CUtensorMap
       : "memory");
 }
 
-// The features' side in boxes of 16, 32 and 64 rows (gradient), or whatever a product's
-// weights take (w[2]); x in boxes of 16 to 128 rows; either in single rows for a gather.
+// The features' side in boxes of 16 to 128 rows (gradient), or whatever a product's
+// weights take (w[3]); x in boxes of 16 to 128 rows; either in single rows for a gather.
 // A TMA instruction takes some 60 cycles however little it brings, so rows come in a few
 // boxes of powers of two (4096 tokens, 8 of 128 experts of 1536 x 4096 with skewed
 // counts: 562 us with boxes of 8 rows).
 struct Maps {
-  CUtensorMap w[3], x[4], w1, x1, out;  // out: in boxes of an epilogue warp's chunk
+  CUtensorMap w[4], x[4], w1, x1, out;  // out: in boxes of an epilogue warp's chunk
 };
+
+// A value that all lanes of a warp have, for a uniform register: what a TMA or an MMA takes
+// from others costs its warp some hundred cycles an instruction to bring there.
+__device__ __forceinline__ int same(int v) { return __shfl_sync(ALL, v, 0); }
+
+// mma_f16_pair by the low words of the descriptors: the address and the leading offset.
+__device__ __forceinline__ uint32_t desc_word(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | (lbo_bytes >> 4) << 16;
+}
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(mx::DESC_HI_SW128)
+      : "memory");
+}
 
 // A unit of work: one tile.
 struct Unit {
@@ -338,28 +360,28 @@ template <int MODE, bool INDEXED, bool LONG>
 __global__ void __launch_bounds__(THREADS, 1)
     routed_pair_kernel(const __grid_constant__ Maps maps, const Params p) {
   using S = Shape<LONG>;
-  constexpr int STAGES = S::STAGES, ROWS = S::ROWS, STAGE_BYTES = S::STAGE_BYTES;
+  constexpr int ROWS = S::ROWS;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ alignas(8) uint64_t bars[3 * STAGES + 9];
+  __shared__ alignas(8) uint64_t bars[3 * MAX_STAGES + 9];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
   // Of either side (0: features, 1: rows):
   __shared__ volatile uint32_t peer_loaded[2];        // rank 0: stages that rank 1 loaded
-  __shared__ volatile uint32_t stage_tx[2][STAGES];   // bytes of a CTA's last load of a stage
-  __shared__ volatile uint32_t peer_tx[2][STAGES];    // rank 0: rank 1's
+  __shared__ volatile uint32_t stage_tx[2][MAX_STAGES];   // bytes of a CTA's last load of a stage
+  __shared__ volatile uint32_t peer_tx[2][MAX_STAGES];    // rank 0: rank 1's
   __shared__ uint32_t parts[MAX_PARTS + 1];
   __shared__ int32_t expert[MAX_PARTS], lo[MAX_PARTS], num[MAX_PARTS];
   __shared__ uint32_t class_units[CLASSES], class_experts[CLASSES];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   const uint32_t sbase = smem_u32(smem), bar0 = smem_u32(bars);
-  auto full_bar = [&](int side, uint32_t s) { return bar0 + 8u * (side * STAGES + s); };
-  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (2 * STAGES + s); };
-  auto acc_bar = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + b); };
-  auto released_bar = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + 2 + b); };
-  auto read_bar = [&](uint32_t b) { return bar0 + 8u * (3 * STAGES + 4 + b); };
-  const uint32_t drain_bar = bar0 + 8u * (3 * STAGES + 6);
-  auto peer_done_bar = [&](int side) { return bar0 + 8u * (3 * STAGES + 7 + side); };
+  auto full_bar = [&](int side, uint32_t s) { return bar0 + 8u * (side * MAX_STAGES + s); };
+  auto empty_bar = [&](uint32_t s) { return bar0 + 8u * (2 * MAX_STAGES + s); };
+  auto acc_bar = [&](uint32_t b) { return bar0 + 8u * (3 * MAX_STAGES + b); };
+  auto released_bar = [&](uint32_t b) { return bar0 + 8u * (3 * MAX_STAGES + 2 + b); };
+  auto read_bar = [&](uint32_t b) { return bar0 + 8u * (3 * MAX_STAGES + 4 + b); };
+  const uint32_t drain_bar = bar0 + 8u * (3 * MAX_STAGES + 6);
+  auto peer_done_bar = [&](int side) { return bar0 + 8u * (3 * MAX_STAGES + 7 + side); };
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
   const bool leader = rank == 0;
@@ -367,7 +389,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t peer_abort = mapa_shared(smem_u32(const_cast<int*>(&abort_flag)), rank ^ 1u);
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) {
+    for (int s = 0; s < MAX_STAGES; ++s) {
       mbar_init(full_bar(0, s), 1);
       mbar_init(full_bar(1, s), 1);
       mbar_init(empty_bar(s), 1);
@@ -385,7 +407,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     abort_flag = 0;
     fence_mbar_init();
     if (p.K > 0) {
-      tma_prefetch_desc(&maps.w[2]);
+      tma_prefetch_desc(&maps.w[3]);
       for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.x[i]);
     }
   }
@@ -440,7 +462,20 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   }
   uint32_t units = 0;
-  for (int k = 0; k < CLASSES; ++k) units += class_units[k];
+  int dearest = 0;
+  for (int k = 0; k < CLASSES; ++k) {
+    units += class_units[k];
+    if (class_experts[k]) dearest = k;
+  }
+  // The ring: as many stages as fit with the rows of the largest tile there is.  What comes
+  // from memory takes some 2 us from one stage's turn to its next, so that tiles of few rows
+  // (one row each of 8 experts of 2048 x 1536: 18.7 us with 6 stages) need all they can get.
+  units = same(units);
+  dearest = same(dearest);
+  const uint32_t b_bytes =
+      MODE == GRADIENT ? S::B_BYTES : 2 * (dearest + 1) * (ROWS / 2 / CLASSES) * 128;
+  const uint32_t stage_bytes = A_BYTES + b_bytes;
+  const uint32_t stages = min(static_cast<uint32_t>(MAX_STAGES), S::RING_BYTES / stage_bytes);
   const Table table{parts, expert, lo, num};
   tc_fence_before();
   cluster_sync_all();
@@ -462,7 +497,6 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
     const uint32_t fb0 = mapa_shared(full_bar(side, 0), 0);
     bool ok = true;
-    auto same = [](int v) { return __shfl_sync(ALL, v, 0); };  // (in a uniform register)
     for (uint32_t u = cluster; ok && u < units; u += clusters) {
       const Unit w = unit_at<MODE, ROWS>(u, p, table);
       const int kbs = same((w.sum + BK - 1) / BK), half = same(w.width / 2);
@@ -486,13 +520,13 @@ __global__ void __launch_bounds__(THREADS, 1)
           ok = false;
           break;
         }
-        const uint32_t st = sbase + s * STAGE_BYTES + side * A_BYTES, fb = fb0 + 8u * s;
+        const uint32_t st = sbase + s * stage_bytes + side * A_BYTES, fb = fb0 + 8u * s;
         const int rows = min(BK, sum - kb * BK);  // gradient: positions of this stage,
         const int read = (rows + 15) & ~15;       // and those that the MMAs read
         constexpr int BOXES = side == 0 ? 2 : S::B_BYTES / BOX;  // gradient: of 64 features
         const uint32_t tx = MODE == GRADIENT ? BOXES * 128 * read
                             : side == 0      ? A_BYTES
-                                             : half * 128;
+                                             : 2 * half * 128;
         if (lane == 0) {
           stage_tx[side][s] = tx;
           if (leader) mbar_arrive_expect_tx(full_bar(side, s), 2 * tx);
@@ -506,7 +540,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               if (elect_one()) {
 #pragma unroll
                 for (int i = 0; i < BOXES; ++i)
-                  tma_load_2d_pair(st + i * BOX, map + 2, fb, mine + 64 * i, pos);
+                  tma_load_2d_pair(st + i * BOX, map + 3, fb, mine + 64 * i, pos);
               }
             } else {
               // An expert's last rows: in boxes, and the last of sixteen by the gather,
@@ -514,9 +548,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               const int whole = rows & ~15;
               if (elect_one()) {
 #pragma unroll
-                for (int g = 0; g < 2; ++g)
+                for (int g = 0; g < 3; ++g)
                   if (whole & (16 << g)) {
-                    const int at = whole & ~((32 << g) - 1);  // behind the larger box
+                    const int at = whole & ~((32 << g) - 1);  // behind the larger boxes
 #pragma unroll
                     for (int i = 0; i < BOXES; ++i)
                       tma_load_2d_pair(st + i * BOX + at * 128, map + g, fb, mine + 64 * i,
@@ -535,25 +569,31 @@ __global__ void __launch_bounds__(THREADS, 1)
           } else if constexpr (side == 0) {
             if (elect_one()) {
               if constexpr (MODE == PRODUCT) {
-                tma_load_3d_pair(st, &maps.w[2], fb, mine, kb * BK, expert);
-                tma_load_3d_pair(st + BOX, &maps.w[2], fb, mine + 64, kb * BK, expert);
+                tma_load_3d_pair(st, &maps.w[3], fb, mine, kb * BK, expert);
+                tma_load_3d_pair(st + BOX, &maps.w[3], fb, mine + 64, kb * BK, expert);
               } else {
-                tma_load_3d_pair(st, &maps.w[2], fb, kb * BK, mine, expert);
+                tma_load_3d_pair(st, &maps.w[3], fb, kb * BK, mine, expert);
+                tma_load_3d_pair(st + BOX, &maps.w[3], fb, kb * BK + 64, mine, expert);
               }
             }
           } else if constexpr (INDEXED) {
-            if (4 * lane < half) tma_gather4_pair(st + lane * 512, &maps.x1, fb, kb * BK, r);
+            if (4 * lane < half) {
+              tma_gather4_pair(st + lane * 512, &maps.x1, fb, kb * BK, r);
+              tma_gather4_pair(st + b_bytes / 2 + lane * 512, &maps.x1, fb, kb * BK + 64, r);
+            }
           } else if (elect_one()) {
 #pragma unroll
             for (int i = 3; i >= 0; --i)
               if (half & (16 << i)) {
                 const int at = half & ~((32 << i) - 1);  // behind the larger boxes
                 tma_load_2d_pair(st + at * 128, &maps.x[i], fb, kb * BK, mine + at);
+                tma_load_2d_pair(st + b_bytes / 2 + at * 128, &maps.x[i], fb, kb * BK + 64,
+                                 mine + at);
               }
           }
         }
         __syncwarp();
-        if (++s == STAGES) {
+        if (++s == stages) {
           s = 0;
           ph ^= 1u;
         }
@@ -564,7 +604,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       // done what either CTA never issued -- before either may leave.
       volatile int never = 0;
       if (!leader) {
-        for (int i = 0; i < STAGES; ++i)
+        for (uint32_t i = 0; i < stages; ++i)
           st_shared_cluster_u32(
               mapa_shared(smem_u32(const_cast<uint32_t*>(&peer_tx[side][i])), 0),
               stage_tx[side][i]);
@@ -578,8 +618,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         else
           atomicOr(p.status, kErrTimeoutDrain);
         const uint32_t hi = it > it1 ? it : it1;
-        for (uint32_t i = hi > STAGES ? hi - STAGES : 0; i < hi; ++i) {
-          const uint32_t si = i % STAGES, phi = (i / STAGES) & 1u;
+        for (uint32_t i = hi > stages ? hi - stages : 0; i < hi; ++i) {
+          const uint32_t si = i % stages, phi = (i / stages) & 1u;
           const bool armed = i < it, loaded0 = armed && !(stall && i == 0), loaded1 = i < it1;
           if (!armed) {
             mbar_arrive_expect_tx(full_bar(side, si), peer_tx[side][si]);
@@ -612,10 +652,10 @@ __global__ void __launch_bounds__(THREADS, 1)
       };
       for (uint32_t u = cluster; ok && u < units; u += clusters) {
         const Unit w = unit_at<MODE, ROWS>(u, p, table);
-        const int kbs = (w.sum + BK - 1) / BK;
-        const int tail = (w.sum - (kbs - 1) * BK + 15) / 16;  // MMAs of the last stage
+        const int sum = same(w.sum), kbs = (sum + BK - 1) / BK;
+        const int tail = (sum - (kbs - 1) * BK + 15) / 16;  // MMAs of the last stage
         const uint32_t idesc =
-            make_idesc(p.kind, MODE != TRANSPOSED, MODE == GRADIENT, TILE_F, w.width);
+            make_idesc(p.kind, MODE != TRANSPOSED, MODE == GRADIENT, TILE_F, same(w.width));
         // an accumulator whose last but one filling has been read
         auto next = [&] { return t < 2 || wait(released_bar(t & 1u), ((t - 2) >> 1) & 1u); };
         for (int kb = 0; kb < kbs; ++kb) {
@@ -628,26 +668,33 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           tc_fence_after();
           const uint32_t d = tmem + (t & 1u) * ROWS;
-          const uint32_t st = sbase + s * STAGE_BYTES;
-          const uint64_t a = MODE == TRANSPOSED ? smem_desc_sw128(st, 16, 1024)
-                                                : smem_desc_sw128(st, BOX, 1024);
-          const uint64_t b = MODE == GRADIENT ? smem_desc_sw128(st + A_BYTES, BOX, 1024)
-                                              : smem_desc_sw128(st + A_BYTES, 16, 1024);
-          // 16 of the sum: 32 bytes along a K-major row, 16 rows of 128 bytes else
-          constexpr uint32_t step_a = (MODE == TRANSPOSED ? 32 : 2048) >> 4;
-          constexpr uint32_t step_b = (MODE == GRADIENT ? 2048 : 32) >> 4;
-          const int mmas = kb + 1 < kbs ? BK / 16 : tail;
+          const uint32_t st = sbase + s * stage_bytes;
+          const uint32_t a = desc_word(st, MODE == TRANSPOSED ? 16 : BOX);
+          const uint32_t b = desc_word(st + A_BYTES, MODE == GRADIENT ? BOX : 16);
+          // 16 of the sum: 32 bytes along a K-major row, of two halves; 16 rows of 128 bytes
+          auto at_a = [&](int kk) -> uint32_t {
+            return a + (MODE == TRANSPOSED ? kk / 4 * (BOX >> 4) + kk % 4 * 2 : kk * 128);
+          };
+          auto at_b = [&](int kk) -> uint32_t {
+            return b + (MODE == GRADIENT ? kk * 128 : kk / 4 * (b_bytes >> 5) + kk % 4 * 2);
+          };
+          const uint32_t more = in > 0 ? 1u : 0u;
+          const bool full = kb + 1 < kbs || tail == BK / 16;
           if (elect_one()) {
+            if (full) {
 #pragma unroll
-            for (int kk = 0; kk < BK / 16; ++kk)
-              if (kk < mmas)
-                mma_f16_pair(d, a + kk * step_a, b + kk * step_b, idesc, in > 0 || kk > 0 ? 1u : 0u);
+              for (int kk = 0; kk < BK / 16; ++kk)
+                mma_pair(d, at_a(kk), at_b(kk), idesc, kk > 0 ? 1u : more);
+            } else {
+              for (int kk = 0; kk < tail; ++kk)
+                mma_pair(d, at_a(kk), at_b(kk), idesc, kk > 0 ? 1u : more);
+            }
             mma_commit_pair_multicast(empty_bar(s), 0x3);
             if (last) mma_commit_pair_multicast(acc_bar(t & 1u), 0x3);
           }
           __syncwarp();
           if (last) ++t;
-          if (++s == STAGES) {
+          if (++s == stages) {
             s = 0;
             ph ^= 1u;
           }
@@ -689,7 +736,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     // two warps a lane quarter, every other 32 columns each
     const int q = warp & 3, odd = (warp - 2) >> 2;
-    const uint32_t piece = sbase + STAGES * STAGE_BYTES + (warp - 2) * S::PIECE_BYTES;
+    const uint32_t piece = sbase + S::RING_BYTES + (warp - 2) * S::PIECE_BYTES;
     uint32_t t = 0;
     bool ok = true;
     for (uint32_t u = cluster; ok && u < units; u += clusters) {
@@ -976,7 +1023,7 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
       e = ready(a.w, 1, a.out_rows, a.N, a.ldw, 0, nullptr, a.scatter, 1, a.rows, &at, s, &w);
       if (e != cudaSuccess) return e;
       p.scatter = nullptr;
-      for (int i = 0; i < 3; ++i) ok = ok && rows_map(&m.w[i], w, a.N, 16u << i);
+      for (int i = 0; i < 4; ++i) ok = ok && rows_map(&m.w[i], w, a.N, 16u << i);
       ok = ok && rows_map(&m.w1, w, a.N, 1);
     } else {
       const bool t = a.kind == ProductKind::transposed;
@@ -988,8 +1035,8 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
       const int64_t ld = rows == 1 ? (cols + 7) / 8 * 8 : w.ld;
       const int64_t stride = a.E == 1 ? rows * ((cols + 7) / 8 * 8) : w.stride;
       const uint64_t pitch[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(stride) * 2};
-      const uint32_t box[3] = {64, t ? 128u : 64u, 1};
-      ok = encode_tmap_3d(&m.w[2], type, w.p, dims, pitch, box, swizzle) == CUDA_SUCCESS;
+      const uint32_t box[3] = {64, 128, 1};
+      ok = encode_tmap_3d(&m.w[3], type, w.p, dims, pitch, box, swizzle) == CUDA_SUCCESS;
     }
     for (int i = 0; i < 4; ++i) ok = ok && rows_map(&m.x[i], x, a.K, 16u << i);
     ok = ok && rows_map(&m.x1, x, a.K, 1);
