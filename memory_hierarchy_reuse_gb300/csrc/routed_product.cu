@@ -423,18 +423,65 @@ __global__ void __launch_bounds__(THREADS, 1)
   auto units_of = [&](int n) -> uint32_t {
     return (MODE == GRADIENT ? p.k_tiles : row_tiles<ROWS>(n)) * p.f_tiles;
   };
-  for (int e = threadIdx.x; e < p.E; e += THREADS) {
-    // (offsets that are not ascending, or past the rows, reach nothing)
-    const int a = min(max(p.offsets[e], 0), p.rows), b = min(max(p.offsets[e + 1], a), p.rows);
-    lo[e] = a;
-    num[e] = b - a;
-    const int k = cost_class<MODE, ROWS>(b - a);
-    atomicAdd(&class_units[k], units_of(b - a));
-    atomicAdd(&class_experts[k], 1u);
+  auto scan_of = [&](uint32_t c) {
+    uint32_t scan = c;
+#pragma unroll
+    for (int i = 1; i < 32; i <<= 1) {
+      const uint32_t o = __shfl_up_sync(ALL, scan, i);
+      if (lane >= i) scan += o;
+    }
+    return scan;
+  };
+  const bool few = MODE != GRADIENT && p.rows <= FEW_ROWS;
+  if (few) {
+    // Units of like cost: in the experts' order, by one warp, 128 offsets at a time.
+    if (warp == 0) {
+      uint32_t unit = 0;
+      int dearest = 0;
+      for (int e0 = 0; e0 < p.E; e0 += 128) {
+        int a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = e0 + 32 * i + lane;
+          a[i] = e < p.E ? p.offsets[e] : 0;
+          b[i] = e < p.E ? p.offsets[e + 1] : 0;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = e0 + 32 * i + lane;
+          a[i] = min(max(a[i], 0), p.rows);
+          b[i] = min(max(b[i], a[i]), p.rows);
+          const uint32_t c = e < p.E ? units_of(b[i] - a[i]) : 0, scan = scan_of(c);
+          if (e < p.E) {
+            lo[e] = a[i];
+            num[e] = b[i] - a[i];
+            expert[e] = e;
+            parts[e] = unit + scan - c;
+          }
+          dearest = max(dearest, cost_class<MODE, ROWS>(b[i] - a[i]));
+          unit += __shfl_sync(ALL, scan, 31);
+        }
+      }
+      dearest = __reduce_max_sync(ALL, dearest);
+      if (lane == 0) {
+        class_units[dearest] = unit;
+        class_experts[dearest] = 1;
+      }
+    }
+  } else {
+    for (int e = threadIdx.x; e < p.E; e += THREADS) {
+      // (offsets that are not ascending, or past the rows, reach nothing)
+      const int a = min(max(p.offsets[e], 0), p.rows), b = min(max(p.offsets[e + 1], a), p.rows);
+      lo[e] = a;
+      num[e] = b - a;
+      const int k = cost_class<MODE, ROWS>(b - a);
+      atomicAdd(&class_units[k], units_of(b - a));
+      atomicAdd(&class_experts[k], 1u);
+    }
   }
   __syncthreads();
   static_assert(THREADS / 32 >= CLASSES, "a warp a class");
-  if (warp < CLASSES) {
+  if (!few && warp < CLASSES) {
     uint32_t unit = 0, place = 0;
     for (int k = CLASSES - 1; k > warp; --k) {
       unit += class_units[k];
@@ -446,12 +493,7 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t c = in ? units_of(num[e]) : 0;
       const uint32_t mask = __ballot_sync(ALL, in);
       if (!mask) continue;
-      uint32_t scan = c;
-#pragma unroll
-      for (int i = 1; i < 32; i <<= 1) {
-        const uint32_t o = __shfl_up_sync(ALL, scan, i);
-        if (lane >= i) scan += o;
-      }
+      const uint32_t scan = scan_of(c);
       if (in) {
         const uint32_t at = place + __popc(mask & ((1u << lane) - 1));
         expert[at] = e;
