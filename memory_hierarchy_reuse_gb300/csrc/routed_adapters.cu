@@ -166,7 +166,8 @@ __global__ void __launch_bounds__(ROW_THREADS) __cluster_dims__(CTAS, 1, 1)
       for (int m = 16; m; m >>= 1) acc[g] += __shfl_xor_sync(ALL, acc[g], m);
     if (first) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     first = false;
-    // lane 8 g' + c sends row g' of the group to CTA c
+    // lane 8 g' + c sends row g' of the group to CTA c: every lane has a CTA of the cluster
+    static_assert(CTAS == 8 && G * CTAS == 32, "a lane for each row and CTA");
     const int g = lane >> 3;
     float mine = acc[0];
 #pragma unroll
@@ -1027,12 +1028,20 @@ cudaError_t launch_tiles(const AdapterArgs& a, const AdapterParams& r, TileParam
   p.slots = SLOTS;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
   if (e != cudaSuccess) return e;
-  // CTAs a tile: as many as leave every tile room to run at once.
+  // CTAs a tile: as many as leave every tile room to run at once.  Clusters of 8 do not
+  // pack into all of the SMs (2048 rows of 4096 x 4096, rank 16, as 16 of them: 43 us, as
+  // clusters of 4: 30), so they stay below half; and every CTA more sends the others
+  // 128 x rank sums, which pays only against long rows (256 rows, 8 CTAs / 4: rank 16, K + N
+  // of 15104 30 / 42 us, 8192 22 / 26, 2048 17 / 16; rank 64, 8192 38 / 33, 1024 32 / 21).
+  // Where the adapters may make tiles for more than two rounds of 8, they are 4 as well
+  // (1024 rows of 4096 x 11008 with 64 adapters in no order: 167 / 93 us).
   const int64_t full = (a.T + TILE - 1) / TILE;
-  int ctas = 8;
-  while (ctas > 1 && full * ctas > ctl.sm_count) ctas /= 2;
   // every bin's tiles but one are full
   const int64_t tiles = a.T / TILE + (a.T < a.L + 1 ? a.T : a.L + 1);
+  const bool wide = full * 16 <= ctl.sm_count && tiles * 4 <= ctl.sm_count &&
+                    a.K + a.N >= 256 * a.rank;
+  int ctas = wide ? 8 : 4;
+  while (ctas > 1 && full * ctas > ctl.sm_count) ctas /= 2;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = static_cast<unsigned>(ctas);
@@ -1054,8 +1063,16 @@ cudaError_t launch_tiles(const AdapterArgs& a, const AdapterParams& r, TileParam
 
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
-// Rows up to which every row has a cluster of its own.
-constexpr int64_t FEW = 64;
+// Whether every row has a cluster of its own.  That kernel's time grows with the rows, the
+// tiles' hardly does until they fill the device.  In us (bf16, 8 adapters), rows' / tiles':
+//     K, N, rank       128 rows    256 rows    512 rows
+//     4096, 4096, 16    9.4 / 22   17.4 / 22   30.5 / 23
+//     4096, 4096, 64   17.2 / 35   30   / 33   56   / 34
+//     1024, 1024, 16    7.4 / 16   13.4 / 16   23.5 / 16
+//     4096, 11008, 16  13.8 / 33   25.5 / 30   48   / 31
+// Up to 512 rows that may have an adapter for every 8 of them keep to rows too: with 64
+// adapters in no order, a tile each, the last line's 512 rows are 48 / 160.
+bool by_rows(const AdapterArgs& a) { return a.T <= 256 || (a.T <= 512 && a.T <= 8 * a.L); }
 
 cudaError_t launch_many(const AdapterArgs& a, const AdapterParams& r, void* scratch,
                         const DeviceCtl& ctl, cudaStream_t s) {
@@ -1153,7 +1170,7 @@ cudaError_t launch_many(const AdapterArgs& a, const AdapterParams& r, void* scra
 }  // namespace
 
 int64_t adapters_scratch(const AdapterArgs& a) {
-  if (a.T <= FEW) return 0;
+  if (by_rows(a)) return 0;
   const int64_t each[3] = {
       a.K > 0 ? operand_bytes(a.x, 1, a.T, a.K, a.ldx, 0, 0) : 0,
       a.K > 0 ? operand_bytes(a.down, a.L, a.rank, a.K, a.ldd, a.stride_d, 0) : 0,
@@ -1186,7 +1203,7 @@ cudaError_t launch_adapters(const AdapterArgs& a, void* scratch, const DeviceCtl
   p.N = static_cast<int32_t>(a.N);
   p.L = static_cast<int32_t>(a.L);
   p.rank = static_cast<int32_t>(a.rank);
-  if (a.T > FEW) return launch_many(a, p, scratch, ctl, s);
+  if (!by_rows(a)) return launch_many(a, p, scratch, ctl, s);
   return a.dtype == MHR_BF16 ? launch_out<__nv_bfloat16>(a, p, s) : launch_out<__half>(a, p, s);
 }
 

@@ -51,7 +51,7 @@ def case(T, K, N, L, rank, dtype, seed=0):
             whole((L, rank, N), dtype, seed + 3, 1))
 
 
-@pytest.mark.parametrize("T,run", [(1, 1), (3, 1), (7, 2), (63, 1), (64, 64), (65, 1), (200, 33),
+@pytest.mark.parametrize("T,run", [(1, 1), (3, 1), (7, 2), (63, 1), (64, 64), (65, 1), (256, 5), (257, 5), (512, 5), (513, 5), (200, 33),
                                    (130, 1), (1000, 700), (2100, 150)])
 @pytest.mark.parametrize("K,N,L,rank", [(64, 64, 3, 16), (200, 136, 5, 4), (72, 264, 1, 64),
                                         (136, 392, 9, 11), (128, 1032, 2, 100), (64, 72, 40, 128)])
@@ -74,7 +74,7 @@ def test_adapters(mhr, T, run, K, N, L, rank):
         same(z, ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy()))
 
 
-@pytest.mark.parametrize("T", [2, 150])
+@pytest.mark.parametrize("T", [2, 150, 270])
 @pytest.mark.parametrize("K,N,rank", [(1, 1, 1), (7, 9, 3), (65, 129, 8), (131, 2, 16), (9, 300, 33)])
 def test_odd_sizes(mhr, T, K, N, rank):
     for out in ("bf16", "f32"):
@@ -120,7 +120,7 @@ def test_real_values(mhr, T, dtype, out, size):
     assert np.all(np.abs(got - want) <= bound), float((np.abs(got - want) / bound).max())
 
 
-@pytest.mark.parametrize("T", [3, 140])
+@pytest.mark.parametrize("T", [3, 140, 270])
 def test_strides_and_padding_stay(mhr, T):
     import torch
 
@@ -137,7 +137,7 @@ def test_strides_and_padding_stay(mhr, T):
         assert bool((buf[:, :4] == 7).all()) and bool((buf[:, N + 4:] == 7).all())
 
 
-@pytest.mark.parametrize("T", [5, 200])
+@pytest.mark.parametrize("T", [5, 200, 520])
 def test_none_and_empty(mhr, T):
     import torch
 
@@ -154,7 +154,7 @@ def test_none_and_empty(mhr, T):
     assert mhr.add_adapters(y[:0], x[:0], down, up, which[:0]).shape == (0, 72)
 
 
-@pytest.mark.parametrize("T", [6, 200])
+@pytest.mark.parametrize("T", [6, 200, 520])
 def test_infinities_stay_in_their_rows(mhr, T):
     import torch
 
@@ -176,7 +176,7 @@ def test_far_offsets(mhr):
 
     pitch = (1 << 31) + 64
     big = torch.zeros(pitch + 16 * 64, dtype=torch.bfloat16, device="cuda")
-    for T in (2, 130):
+    for T in (2, 130, 530):
         x, down, up = case(T, 64, 64, 2, 16, "bf16")
         d = torch.as_strided(big, (2, 16, 64), (pitch, 64, 1))
         y, which = whole((T, 64), "bf16", 4, 50), which_of(T, 2, 1, 1)
