@@ -8,7 +8,6 @@
 #include <Python.h>
 
 #include <ATen/cuda/EmptyTensor.h>
-#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -466,15 +465,14 @@ at::ScalarType type_number(PyObject* o, at::ScalarType same) {
   return type == MHR_F32 ? at::kFloat : type == MHR_BF16 ? at::kBFloat16 : at::kHalf;
 }
 
-// Scratch of a call on `stream`, kept until the stream has passed it.
+// Scratch of a call on `stream`, of that stream's own memory: what another stream gave
+// back to the allocator may still have that stream's work ahead of it.
 at::Tensor scratch_for(int64_t bytes, int device, void* stream) {
-  at::Tensor t = empty({bytes}, at::kByte, device);
-  if (bytes > 0 && stream != static_cast<void*>(c10::cuda::getCurrentCUDAStream(device).stream()))
-    c10::cuda::CUDACachingAllocator::recordStream(
-        t.storage().data_ptr(), c10::cuda::getStreamFromExternal(
-                                    static_cast<cudaStream_t>(stream),
-                                    static_cast<c10::DeviceIndex>(device)));
-  return t;
+  if (stream == static_cast<void*>(c10::cuda::getCurrentCUDAStream(device).stream()))
+    return empty({bytes}, at::kByte, device);
+  c10::cuda::CUDAStreamGuard on(c10::cuda::getStreamFromExternal(
+      static_cast<cudaStream_t>(stream), static_cast<c10::DeviceIndex>(device)));
+  return empty({bytes}, at::kByte, device);
 }
 
 // experts(x, w, offsets, gather, scatter, top, transposed, out or None, out_dtype or None,

@@ -351,3 +351,51 @@ def test_a_stalled_stage_is_a_timeout(mhr):
     same(mhr.matmul_experts(x, w, offsets),
          ref.product(f64(x), f64(w), at, 117, out=np.zeros((117, 256))))
     assert mhr.gemm_check(None) == mhr.MHR_OK
+
+
+def test_scratch_is_of_the_calls_own_stream(mhr):
+    """What the current stream gave back may still be written by its work: a call on another
+    stream takes its scratch from that stream's memory."""
+    import torch
+
+    n = 20_000
+    at, offsets = offsets_of([9_000, 11_000])
+    x, w = whole((n, 71), "bf16", 1), whole((2, 71, 65), "bf16", 2)
+    out = torch.zeros((n, 65), dtype=torch.bfloat16, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+
+    def held():
+        return sum(g["total_size"] for g in torch.cuda.memory_snapshot()
+                   if g["stream"] == s.cuda_stream)
+
+    torch.cuda.empty_cache()
+    before = held()
+    mhr.matmul_experts(x, w, offsets, out=out, stream=s.cuda_stream)
+    s.synchronize()
+    assert held() > before
+    same(out, ref.product(f64(x), f64(w), at, n, out=np.zeros((n, 65))))
+
+
+def test_two_streams_at_once(mhr):
+    """Calls that share the GPU, their scratch apart: all as if alone."""
+    import torch
+
+    at, offsets = offsets_of([300, 0, 500, 224])
+    order = torch.arange(1023, -1, -1, dtype=torch.int32, device="cuda")
+    x, w = whole((1024, 200), "bf16", 1), whole((4, 200, 328), "bf16", 2)
+    x2 = whole((1024, 200), "bf16", 3)
+    calls = [lambda a, **k: mhr.matmul_experts(a, w, offsets, order, **k),
+             lambda a, **k: mhr.matmul_experts_grad(a, a, offsets, order, order, **k)]
+    for call in calls:
+        want = [call(a) for a in (x, x2)]
+        streams = [torch.cuda.Stream() for _ in range(2)]
+        outs = [[torch.empty_like(want[0]) for _ in range(8)] for _ in range(2)]
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+        for i in range(8):
+            for j, a in enumerate((x, x2)):
+                call(a, out=outs[j][i], stream=streams[j].cuda_stream)
+        torch.cuda.synchronize()
+        for j in range(2):
+            assert all(torch.equal(o, want[j]) for o in outs[j])
