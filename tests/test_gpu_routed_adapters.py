@@ -212,3 +212,21 @@ def test_on_another_stream_and_captured(mhr, T):
     graph.replay()
     graph.replay()
     same(out, ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy()))
+
+
+@pytest.mark.parametrize("run", [1, 600])
+def test_a_stalled_stage_is_a_timeout(mhr, run):
+    """The bounded waits: the whole cluster unwinds, the next call is right."""
+    x, down, up = case(600, 1024, 1024, 2, 16, "bf16")
+    y, which = whole((600, 1024), "bf16", 4, 50), which_of(600, 2, run, 1).clamp(min=0)
+    want = mhr.add_adapters(y, x, down, up, which)
+    old = mhr.gemm_testing_set_wait_limit_ns(20_000_000)
+    mhr.gemm_testing_set_inject_stall(1)
+    try:
+        mhr.add_adapters(y, x, down, up, which)
+        assert mhr.gemm_check(None) == mhr.MHR_ERR_TIMEOUT
+    finally:
+        mhr.gemm_testing_set_inject_stall(0)
+        mhr.gemm_testing_set_wait_limit_ns(old)
+    assert mhr.add_adapters(y, x, down, up, which).equal(want)
+    assert mhr.gemm_check(None) == mhr.MHR_OK
