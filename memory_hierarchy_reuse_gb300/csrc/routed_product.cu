@@ -169,7 +169,8 @@ __device__ __forceinline__ int row_tiles(int n) {
 template <int ROWS>
 __device__ __forceinline__ int tile_rows(int n) {
   const int tiles = row_tiles<ROWS>(n);
-  return tiles ? ((n + tiles - 1) / tiles + 31) & ~31 : 32;
+  if (tiles <= 1) return max(32, (n + 31) & ~31);
+  return (static_cast<int>(divide(n + tiles - 1, tiles)) + 31) & ~31;
 }
 
 // How much a unit of an expert of n rows costs: the steps of an MMA's columns; of a
@@ -185,19 +186,17 @@ __device__ __forceinline__ int cost_class(int n) {
   return tile_rows<ROWS>(n) * CLASSES / ROWS - 1;
 }
 
-// Unit u, found by a whole warp.
+// Unit u, found by a whole warp from its place in the table on (a warp's units ascend:
+// looked up among all experts, each took 550 cycles).
 template <int MODE, int ROWS>
-__device__ __forceinline__ Unit unit_at(uint32_t u, const Params& p, const Table& t) {
-  // the last place whose first unit is at most u: of every step-th, then of those between
-  const int lane = threadIdx.x & 31, step = (p.E + 31) >> 5;
-  auto last = [&](int from, int each) {
-    const int at = from + lane * each;
-    const bool in = at < p.E && (each > 1 || step == 1 || lane < step);
-    return from + (__popc(__ballot_sync(ALL, in && t.parts[at] <= u)) - 1) * each;
-  };
-  int i = 0;
-  if (step > 1) i = last(0, step);
-  i = last(i, 1);
+__device__ __forceinline__ Unit unit_at(uint32_t u, const Params& p, const Table& t, int& place) {
+  const int lane = threadIdx.x & 31;
+  int i = place;
+  for (int behind = 32; behind == 32; i += behind) {  // the last place with a first unit <= u
+    const int at = i + 1 + lane;
+    behind = __popc(__ballot_sync(ALL, at < p.E && t.parts[at] <= u));
+  }
+  place = i;
   const int e = t.expert[i];
   Unit w;
   const uint32_t r = u - t.parts[i];
@@ -368,6 +367,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // Of either side (0: features, 1: rows):
   __shared__ volatile uint32_t peer_loaded[2];        // rank 0: stages that rank 1 loaded
   __shared__ volatile uint32_t stage_tx[2][MAX_STAGES];   // bytes of a CTA's last load of a stage
+  __shared__ volatile uint32_t other_tx[2][MAX_STAGES];   // rank 0: and of rank 1's with it
   __shared__ volatile uint32_t peer_tx[2][MAX_STAGES];    // rank 0: rank 1's
   __shared__ uint32_t parts[MAX_PARTS + 1];
   __shared__ int32_t expert[MAX_PARTS], lo[MAX_PARTS], num[MAX_PARTS];
@@ -539,14 +539,19 @@ __global__ void __launch_bounds__(THREADS, 1)
     const bool stall = p.inject_stall && blockIdx.x == 0;  // test hook: stage 0 never fills
     const uint32_t fb0 = mapa_shared(full_bar(side, 0), 0);
     bool ok = true;
+    int place = 0;
     for (uint32_t u = cluster; ok && u < units; u += clusters) {
-      const Unit w = unit_at<MODE, ROWS>(u, p, table);
+      const Unit w = unit_at<MODE, ROWS>(u, p, table, place);
       const int kbs = same((w.sum + BK - 1) / BK), half = same(w.width / 2);
       const int expert = same(w.expert), sum0 = same(w.sum0), sum = same(w.sum);
       // this CTA's first feature, or row
       const int mine = same(side == 0 ? w.f0 + static_cast<int>(rank) * HALF
                                       : w.first + static_cast<int>(rank) * half);
       int32_t r[4];  // gather: this lane's four rows
+      // Fours of rows that a CTA gathers: those with a row at all (what stands in the MMA's
+      // other columns reaches no result; a gather of zeros takes as long as any).
+      auto fours = [&](int of) { return (max(0, min(half, w.count - of * half)) + 3) / 4; };
+      const int mine4 = same(fours(static_cast<int>(rank)));
       if constexpr (INDEXED && side == 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -568,10 +573,15 @@ __global__ void __launch_bounds__(THREADS, 1)
         constexpr int BOXES = side == 0 ? 2 : S::B_BYTES / BOX;  // gradient: of 64 features
         const uint32_t tx = MODE == GRADIENT ? BOXES * 128 * read
                             : side == 0      ? A_BYTES
+                            : INDEXED        ? mine4 * 2 * 512
                                              : 2 * half * 128;
         if (lane == 0) {
           stage_tx[side][s] = tx;
-          if (leader) mbar_arrive_expect_tx(full_bar(side, s), 2 * tx);
+          if (leader) {
+            const uint32_t tx1 = INDEXED && side == 1 ? fours(1) * 2 * 512 : tx;
+            other_tx[side][s] = tx1;
+            mbar_arrive_expect_tx(full_bar(side, s), tx + tx1);
+          }
         }
         __syncwarp();
         if (!(stall && it == 0)) {
@@ -619,7 +629,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
           } else if constexpr (INDEXED) {
-            if (4 * lane < half) {
+            if (lane < mine4) {
               tma_gather4_pair(st + lane * 512, &maps.x1, fb, kb * BK, r);
               tma_gather4_pair(st + b_bytes / 2 + lane * 512, &maps.x1, fb, kb * BK + 64, r);
             }
@@ -666,8 +676,8 @@ __global__ void __launch_bounds__(THREADS, 1)
           if (!armed) {
             mbar_arrive_expect_tx(full_bar(side, si), peer_tx[side][si]);
           } else {
-            const uint32_t tx = stage_tx[side][si];
-            const uint32_t missing = (loaded0 ? 0u : tx) + (loaded1 ? 0u : tx);
+            const uint32_t missing =
+                (loaded0 ? 0u : stage_tx[side][si]) + (loaded1 ? 0u : other_tx[side][si]);
             if (missing) {  // once the MMA issuer has given up on the stage
               mbar_wait_bounded(full_bar(side, si), phi, 2 * limit, &abort_flag);
               mbar_complete_tx(full_bar(side, si), missing);
@@ -692,8 +702,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       auto wait = [&](uint32_t bar, uint32_t parity) {  // a warp-uniform outcome
         return __all_sync(ALL, mbar_wait_bounded(bar, parity, limit, &abort_flag)) != 0;
       };
+      int place = 0;
       for (uint32_t u = cluster; ok && u < units; u += clusters) {
-        const Unit w = unit_at<MODE, ROWS>(u, p, table);
+        const Unit w = unit_at<MODE, ROWS>(u, p, table, place);
         const int sum = same(w.sum), kbs = (sum + BK - 1) / BK;
         const int tail = (sum - (kbs - 1) * BK + 15) / 16;  // MMAs of the last stage
         const uint32_t idesc =
@@ -759,8 +770,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     } else {
       uint32_t t = 0;
       bool ok = true;
+      int place = 0;
       for (uint32_t u = cluster; ok && u < units; u += clusters) {
-        const int kbs = (unit_at<MODE, ROWS>(u, p, table).sum + BK - 1) / BK;
+        const int kbs = (unit_at<MODE, ROWS>(u, p, table, place).sum + BK - 1) / BK;
         const int fillings = LONG ? max(1, (kbs + S::SEGMENT - 1) / S::SEGMENT) : 1;
         for (int i = 0; i < fillings; ++i, ++t) {
           ok = __all_sync(ALL, mbar_wait_bounded(read_bar(t & 1u), (t >> 1) & 1u, limit,
@@ -781,8 +793,9 @@ __global__ void __launch_bounds__(THREADS, 1)
     const uint32_t piece = sbase + S::RING_BYTES + (warp - 2) * S::PIECE_BYTES;
     uint32_t t = 0;
     bool ok = true;
+    int place = 0;
     for (uint32_t u = cluster; ok && u < units; u += clusters) {
-      const Unit w = unit_at<MODE, ROWS>(u, p, table);
+      const Unit w = unit_at<MODE, ROWS>(u, p, table, place);
       const int kbs = (w.sum + BK - 1) / BK;
       const int fillings = LONG ? max(1, (kbs + S::SEGMENT - 1) / S::SEGMENT) : 1;
       const int feature = w.f0 + static_cast<int>(rank) * HALF + q * 32 + lane;

@@ -345,6 +345,9 @@ def test_a_stalled_stage_is_a_timeout(mhr):
         assert mhr.gemm_check(None) == mhr.MHR_ERR_TIMEOUT
         mhr.matmul_experts_grad(x, x, offsets)
         assert mhr.gemm_check(None) == mhr.MHR_ERR_TIMEOUT
+        order = torch.arange(116, -1, -1, dtype=torch.int32, device="cuda")
+        mhr.matmul_experts(x, w, offsets, gather=order)
+        assert mhr.gemm_check(None) == mhr.MHR_ERR_TIMEOUT
     finally:
         mhr.gemm_testing_set_inject_stall(0)
         mhr.gemm_testing_set_wait_limit_ns(old)
