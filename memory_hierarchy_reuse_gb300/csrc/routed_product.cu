@@ -575,30 +575,34 @@ __global__ void __launch_bounds__(THREADS, 1)
                             : side == 0      ? A_BYTES
                             : INDEXED        ? mine4 * 2 * 512
                                              : 2 * half * 128;
-        if (lane == 0) {
+        auto arm = [&] {  // by one lane, the one that loads where one does
           stage_tx[side][s] = tx;
           if (leader) {
             const uint32_t tx1 = INDEXED && side == 1 ? fours(1) * 2 * 512 : tx;
             other_tx[side][s] = tx1;
             mbar_arrive_expect_tx(full_bar(side, s), tx + tx1);
           }
-        }
-        __syncwarp();
-        if (!(stall && it == 0)) {
-          if constexpr (MODE == GRADIENT) {
-            const CUtensorMap* map = side == 0 ? maps.w : maps.x;
-            const int pos = sum0 + kb * BK;
-            if (rows == BK) {
-              if (elect_one()) {
+        };
+        const bool load = !(stall && it == 0);
+        if constexpr (MODE == GRADIENT) {
+          const CUtensorMap* map = side == 0 ? maps.w : maps.x;
+          const int pos = sum0 + kb * BK;
+          if (rows == BK) {
+            if (elect_one()) {
+              arm();
+              if (load) {
 #pragma unroll
                 for (int i = 0; i < BOXES; ++i)
                   tma_load_2d_pair(st + i * BOX, map + 3, fb, mine + 64 * i, pos);
               }
-            } else {
-              // An expert's last rows: in boxes, and the last of sixteen by the gather,
-              // which ends in zeros and not in the next expert's rows.
-              const int whole = rows & ~15;
-              if (elect_one()) {
+            }
+          } else {
+            // An expert's last rows: in boxes, and the last of sixteen by the gather,
+            // which ends in zeros and not in the next expert's rows.
+            const int whole = rows & ~15;
+            if (elect_one()) {
+              arm();
+              if (load) {
 #pragma unroll
                 for (int g = 0; g < 3; ++g)
                   if (whole & (16 << g)) {
@@ -609,17 +613,20 @@ __global__ void __launch_bounds__(THREADS, 1)
                                        pos + at);
                   }
               }
-              __syncwarp();
-              if (read > whole && lane < 4 * BOXES) {
-                const int i = lane % BOXES, at = whole + 4 * (lane / BOXES);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) r[j] = at + j < rows ? pos + at + j : p.rows;
-                tma_gather4_pair(st + i * BOX + at * 128, side == 0 ? &maps.w1 : &maps.x1, fb,
-                                 mine + 64 * i, r);
-              }
             }
-          } else if constexpr (side == 0) {
-            if (elect_one()) {
+            __syncwarp();
+            if (load && read > whole && lane < 4 * BOXES) {
+              const int i = lane % BOXES, at = whole + 4 * (lane / BOXES);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) r[j] = at + j < rows ? pos + at + j : p.rows;
+              tma_gather4_pair(st + i * BOX + at * 128, side == 0 ? &maps.w1 : &maps.x1, fb,
+                               mine + 64 * i, r);
+            }
+          }
+        } else if constexpr (side == 0) {
+          if (elect_one()) {
+            arm();
+            if (load) {
               if constexpr (MODE == PRODUCT) {
                 tma_load_3d_pair(st, &maps.w[3], fb, mine, kb * BK, expert);
                 tma_load_3d_pair(st + BOX, &maps.w[3], fb, mine + 64, kb * BK, expert);
@@ -628,12 +635,17 @@ __global__ void __launch_bounds__(THREADS, 1)
                 tma_load_3d_pair(st + BOX, &maps.w[3], fb, kb * BK + 64, mine, expert);
               }
             }
-          } else if constexpr (INDEXED) {
-            if (lane < mine4) {
-              tma_gather4_pair(st + lane * 512, &maps.x1, fb, kb * BK, r);
-              tma_gather4_pair(st + b_bytes / 2 + lane * 512, &maps.x1, fb, kb * BK + 64, r);
-            }
-          } else if (elect_one()) {
+          }
+        } else if constexpr (INDEXED) {
+          if (lane == 0) arm();
+          __syncwarp();
+          if (load && lane < mine4) {
+            tma_gather4_pair(st + lane * 512, &maps.x1, fb, kb * BK, r);
+            tma_gather4_pair(st + b_bytes / 2 + lane * 512, &maps.x1, fb, kb * BK + 64, r);
+          }
+        } else if (elect_one()) {
+          arm();
+          if (load) {
 #pragma unroll
             for (int i = 3; i >= 0; --i)
               if (half & (16 << i)) {
@@ -703,6 +715,11 @@ __global__ void __launch_bounds__(THREADS, 1)
         return __all_sync(ALL, mbar_wait_bounded(bar, parity, limit, &abort_flag)) != 0;
       };
       int place = 0;
+      auto both = [&](uint32_t s, uint32_t parity) {  // sides of a stage, asked for at once
+        const bool a = mbar_try_wait(full_bar(0, s), parity), b = mbar_try_wait(full_bar(1, s), parity);
+        return __all_sync(ALL, (a || mbar_wait_bounded(full_bar(0, s), parity, limit, &abort_flag)) &&
+                                   (b || mbar_wait_bounded(full_bar(1, s), parity, limit, &abort_flag))) != 0;
+      };
       for (uint32_t u = cluster; ok && u < units; u += clusters) {
         const Unit w = unit_at<MODE, ROWS>(u, p, table, place);
         const int sum = same(w.sum), kbs = (sum + BK - 1) / BK;
@@ -714,7 +731,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         for (int kb = 0; kb < kbs; ++kb) {
           const int in = LONG ? kb % S::SEGMENT : kb;
           const bool last = kb + 1 == kbs || (LONG && in + 1 == S::SEGMENT);
-          if ((in == 0 && !next()) || !wait(full_bar(0, s), ph) || !wait(full_bar(1, s), ph)) {
+          if ((in == 0 && !next()) || !both(s, ph)) {
             if (lane == 0) give_up(kErrTimeoutMma);
             ok = false;
             break;
