@@ -1,18 +1,19 @@
 // The experts' products (gemm_routed_product) and their weights' gradient
 // (gemm_routed_weight_grad): persistent CTA pairs (tcgen05 cta_group::2).
 //
-// A pair's tile has the output's columns -- features -- on the MMA's rows, 256 of
-// them, and rows of tokens (or, of a gradient, of features of x) on its columns, 32
-// to 256: an expert's rows are few and of any number, its features many, so the side
-// that varies is the one whose length an MMA takes in steps.  The transposed result
-// costs nothing: a lane of TMEM is a feature, so a warp's store of one row is 32
-// neighbours.  Which tiles there are stands in the offsets on the device alone; every
+// A product's tile has the output's columns -- features -- on the MMA's rows, 256 of
+// them, and rows of tokens on its columns, 32 to 256: an expert's rows are few and of
+// any number, its features many, so the side that varies is the one whose length an MMA
+// takes in steps.  The transposed result costs nothing: a lane of TMEM is a feature, so a
+// warp's store of one row is 32 neighbours.  A gradient's tile has x's features on the
+// MMA's rows and the gradient's, up to 256 of them, on its columns: a lane holds a row of
+// the result, and its neighbours go out as rows of 128 bytes.  Which tiles there are stands in the offsets on the device alone; every
 // CTA sums them up in shared memory and takes every clusters-th.
 //
 // Operands:          features side               rows side
 //   product           W_e (K x N): MN-major       x rows, K-major
 //   transposed        W_e (N x K): K-major        x rows, K-major
-//   weight gradient   gradient rows, MN-major     x rows, MN-major
+//   weight gradient   x rows, MN-major            gradient rows, MN-major
 // All come by TMA.  Rows that an index picks are put in order first by a kernel of their
 // own; of few rows, TMA's gather of four rows brings them, a lane four rows.  (The gather
 // takes some 60 cycles for its 512 bytes: 8192 tokens, 8 of 16 experts of 4096 x 4096,
@@ -64,7 +65,8 @@ struct Shape {
   static constexpr int B_BYTES = ROWS / 2 * BK * 2;        // this CTA's half of them
   static constexpr int RING_BYTES = LONG ? 168 * 1024 : 192 * 1024;
   static constexpr int SEGMENT = LONG ? 3 : 1 << 30;       // stages an accumulator takes
-  static constexpr int PIECE_BYTES = 32 * 32 * (LONG ? 4 : 2);  // of an epilogue warp
+  static constexpr int PIECE_BYTES = 32 * 32 * (LONG ? 4 : 2);  // of an epilogue warp (of two,
+                                                                // of a 16-bit gradient)
   static constexpr int SMEM = RING_BYTES + EPI_WARPS * PIECE_BYTES + 1024;
   static constexpr uint32_t TMEM_COLS = 2 * ROWS;
 };
@@ -77,7 +79,7 @@ struct Params {
   int64_t ldo, stride_o;   // stride_o: of one expert's gradient
   int32_t E, rows, x_rows, out_rows;
   int32_t K, N, top;       // K: columns of x
-  int32_t f_tiles, k_tiles;  // tiles of features; of x's features (gradient)
+  int32_t f_tiles, n_tiles;  // tiles of features; of the gradient's features on the other side
   int32_t kind;            // 0 fp16, 1 bf16
   int32_t out_dtype;
   int32_t out_tma, pairs;  // whole chunks by TMA; else two features of 16 bits at once
@@ -138,7 +140,7 @@ __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint32_t a, uint32_t b
 // A unit of work: one tile.
 struct Unit {
   int expert, f0;      // expert, first feature of the pair's tile
-  int first, count;    // its rows: sorted positions, or features of x (gradient)
+  int first, count;    // its rows: sorted positions, or columns of the output (gradient)
   int width;           // count, rounded up to what an MMA takes
   int sum0, sum;       // gradient: the expert's sorted positions, summed over
 };
@@ -205,7 +207,7 @@ __device__ __forceinline__ Unit unit_at(uint32_t u, const Params& p, const Table
     const uint32_t q = divide(r, p.f_tiles);
     w.f0 = static_cast<int>(r - q * p.f_tiles) * TILE_F;
     w.first = static_cast<int>(q) * ROWS;
-    w.count = min(ROWS, p.K - w.first);
+    w.count = min(ROWS, p.N - w.first);
     w.sum0 = t.lo[e];
     w.sum = t.n[e];
   } else {
@@ -244,15 +246,14 @@ __device__ __forceinline__ uint32_t pack16(uint32_t lo, uint32_t hi) {
 // own values, or of 16 bytes a lane, holds the SM up 5 to 10 cycles for every 128 bytes.
 // No branch a row either way -- for the row, for the type, for the lane's parity -- which
 // cost 2700 cycles a chunk.
-template <int MODE, bool WIDE>
+template <bool WIDE>
 __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Params& p,
                                             const CUtensorMap* out_map, uint32_t piece,
                                             const Unit& w, int at, int feature, int lane) {
   using Word = std::conditional_t<WIDE, uint32_t, uint16_t>;
   Word* base = static_cast<Word*>(p.out);
-  if constexpr (MODE == GRADIENT) base += w.expert * p.stride_o;
   const int count = min(32, w.count - at);  // rows of this chunk
-  const bool scattered = MODE != GRADIENT && p.scatter;
+  const bool scattered = p.scatter != nullptr;
   const int first = w.first + at;
   int mine = first + lane;  // lane j's row of the output, below 0 for none
   if (scattered) mine = lane < count ? picked_row(p.scatter[first + lane], 1, p.out_rows) : -1;
@@ -278,8 +279,8 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Param
         pack(std::integral_constant<int, MHR_F16>{});
     }
   }
-  // (TMA clips at the tensor's ends; a product's next rows are another tile's)
-  if (p.out_tma && !scattered && (MODE == GRADIENT || count == 32)) {
+  // (the rows behind a tile's are another's)
+  if (p.out_tma && !scattered && count == 32) {
     if (lane == 0) bulk_wait_group_read<0>();  // the chunk before has left the piece
     __syncwarp();
     if constexpr (WIDE) {
@@ -297,7 +298,7 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Param
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0 && f < p.N) {
-      tma_store_3d(out_map, piece, f, first, MODE == GRADIENT ? w.expert : 0);
+      tma_store_3d(out_map, piece, f, first, 0);
       bulk_commit_group();
     }
     return;
@@ -347,6 +348,88 @@ __device__ __forceinline__ void store_chunk(const uint32_t (&r)[32], const Param
       }
     }
   }
+}
+
+// A gradient's chunk of 32 rows and 32 columns where TMA cannot write it, from the warp's
+// piece on: rows 4 bytes a lane, no branch a row.  Of 16 bits a row may start between two
+// words: then a lane's word is its second value and its neighbour's first, and the row's
+// ends go out as 2 bytes.  (Inlined, it slowed results that TMA writes: the gradient of 64
+// experts of 2048 x 1408 in fp32 197 -> 235 us.)
+__device__ __noinline__ void store_ragged(uint32_t* to, int64_t ldo, int rows, int cols,
+                                          uint32_t piece, int lane) {
+  const int last = lane < cols ? rows : 0;
+#pragma unroll
+  for (int j0 = 0; j0 < 32; j0 += 8) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(w[i])
+                   : "r"(piece + (j0 + i) * 128 + (((lane >> 2) ^ i) << 4) + (lane & 3) * 4)
+                   : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i, to += ldo)
+      if (j0 + i < last) to[lane] = w[i];
+  }
+}
+__device__ __noinline__ void store_ragged(uint16_t* to, int64_t ldo, int rows, int cols,
+                                          uint32_t piece, int lane) {
+  const int sub = lane >> 4, l = lane & 15;  // two rows at once
+  to += sub * ldo;
+#pragma unroll
+  for (int j0 = 0; j0 < 32; j0 += 16) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      asm volatile("ld.shared.b32 %0, [%1];"
+                   : "=r"(w[i])
+                   : "r"(piece + (j0 + 2 * i + sub) * 64 + (((l >> 2) ^ (i & 3)) << 4) + (l & 3) * 4)
+                   : "memory");
+#pragma unroll
+    for (int i = 0; i < 8; ++i, to += 2 * ldo) {
+      const uint32_t next = __shfl_down_sync(ALL, w[i], 1, 16);
+      const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(to) >> 1 & 1);
+      const int first = 2 * l + shift;  // of the word's two columns
+      const bool in = j0 + 2 * i + sub < rows;
+      if (in && first + 1 < cols)
+        *reinterpret_cast<uint32_t*>(to + first) = __funnelshift_r(w[i], next, 16 * shift);
+      // what is left over: the first column, and the last one
+      const bool head = in && shift && l == 0, tail = in && first + 1 == cols;
+      if (head || tail)
+        to[head ? 0 : first] = static_cast<uint16_t>(head ? w[i] : w[i] >> (16 * shift));
+      if (head && tail) to[first] = static_cast<uint16_t>(w[i] >> 16);
+    }
+  }
+}
+
+// A gradient's 32 rows (lanes, from `row` on) of 128 bytes of columns from `col` on, by way
+// of the warp's piece of shared memory, swizzled.
+__device__ __forceinline__ void store_rows(const uint32_t (&v)[32], const Params& p,
+                                           const CUtensorMap* out_map, uint32_t piece, int expert,
+                                           int row, int col, int lane) {
+  if (p.out_tma) {  // (the store before has left the piece)
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece + lane * 128 +
+                                                                 ((k ^ (lane & 7)) << 4)),
+                 "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                 : "memory");
+  if (p.out_tma) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && row < p.K && col < p.N) {
+      tma_store_3d(out_map, piece, col, row, expert);
+      bulk_commit_group();
+    }
+    return;
+  }
+  __syncwarp();  // (fp32: a 16-bit gradient's ragged rows go another way)
+  store_ragged(static_cast<uint32_t*>(p.out) + expert * p.stride_o + row * p.ldo + col, p.ldo,
+               min(32, p.K - row), min(32, p.N - col), piece, lane);
+  __syncwarp();
 }
 
 // Warp roles, barriers and the way a timeout unwinds are those of the other pair
@@ -421,7 +504,7 @@ __global__ void __launch_bounds__(THREADS, 1)
   // The experts' rows, then their places: a warp takes a class, whose place is behind
   // the dearer ones.
   auto units_of = [&](int n) -> uint32_t {
-    return (MODE == GRADIENT ? p.k_tiles : row_tiles<ROWS>(n)) * p.f_tiles;
+    return (MODE == GRADIENT ? p.n_tiles : row_tiles<ROWS>(n)) * p.f_tiles;
   };
   auto scan_of = [&](uint32_t c) {
     uint32_t scan = c;
@@ -807,7 +890,11 @@ __global__ void __launch_bounds__(THREADS, 1)
   } else {
     // two warps a lane quarter, every other 32 columns each
     const int q = warp & 3, odd = (warp - 2) >> 2;
-    const uint32_t piece = sbase + S::RING_BYTES + (warp - 2) * S::PIECE_BYTES;
+    // A 16-bit gradient's rows of 128 bytes take the space of two warps: the first of a
+    // quarter's two does them all (all do where TMA cannot write them).
+    const bool alone = MODE == GRADIENT && !LONG && p.out_tma;
+    const uint32_t piece =
+        sbase + S::RING_BYTES + (warp - 2) * S::PIECE_BYTES * (alone ? 2 : 1);
     uint32_t t = 0;
     bool ok = true;
     int place = 0;
@@ -854,9 +941,61 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
             for (int c = 0; c < HELD; ++c) {
               const int at = (2 * c + odd) * 32;
-              if (at < w.count)
-                store_chunk<MODE, LONG>(reinterpret_cast<uint32_t(&)[32]>(held[c]), p, &maps.out,
-                                        piece, w, at, feature, lane);
+              if (at < w.count) {
+                auto& v = reinterpret_cast<uint32_t(&)[32]>(held[c]);
+                if constexpr (MODE == GRADIENT)
+                  store_rows(v, p, &maps.out, piece, w.expert, feature - lane, w.first + at, lane);
+                else
+                  store_chunk<true>(v, p, &maps.out, piece, w, at, feature, lane);
+              }
+            }
+          }
+        } else if constexpr (MODE == GRADIENT) {
+          // 32 columns from `at` on in 16 words (no terms: the accumulator was not written)
+          auto packed = [&](int at, auto& v, auto from) {
+            uint32_t r[32];
+            tmem_ld_32cols(taddr + at, r);
+            tmem_ld_wait();
+            auto pack = [&](auto dtype) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                v[decltype(from)::value + j] =
+                    w.sum ? pack16<decltype(dtype)::value>(r[2 * j], r[2 * j + 1]) : 0u;
+            };
+            if (p.out_dtype == MHR_BF16)
+              pack(std::integral_constant<int, MHR_BF16>{});
+            else
+              pack(std::integral_constant<int, MHR_F16>{});
+          };
+          const int row = feature - lane;
+          if (alone) {
+            if (odd) release();
+#pragma unroll 1
+            for (int at = 0; !odd && at < w.count; at += 64) {
+              uint32_t v[32];
+              packed(at, v, std::integral_constant<int, 0>{});
+              packed(at + 32, v, std::integral_constant<int, 16>{});
+              if (at + 64 >= w.count) release();
+              store_rows(v, p, &maps.out, piece, w.expert, row, w.first + at, lane);
+            }
+          } else {
+            if (32 * odd >= w.count) release();
+#pragma unroll 1
+            for (int at = 32 * odd; at < w.count; at += 64) {
+              uint32_t v[16];
+              packed(at, v, std::integral_constant<int, 0>{});
+              if (at + 64 >= w.count) release();
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 piece + lane * 64 + ((k ^ (lane >> 1 & 3)) << 4)),
+                             "r"(v[4 * k]), "r"(v[4 * k + 1]), "r"(v[4 * k + 2]), "r"(v[4 * k + 3])
+                             : "memory");
+              __syncwarp();
+              const int col = w.first + at;
+              store_ragged(static_cast<uint16_t*>(p.out) + w.expert * p.stride_o + row * p.ldo + col,
+                           p.ldo, min(32, p.K - row), min(32, p.N - col), piece, lane);
+              __syncwarp();
             }
           }
         } else {
@@ -871,7 +1010,7 @@ __global__ void __launch_bounds__(THREADS, 1)
               for (int j = 0; j < 32; ++j) r[j] = 0;
             }
             if (at + 64 >= w.count) release();
-            store_chunk<MODE, LONG>(r, p, &maps.out, piece, w, at, feature, lane);
+            store_chunk<false>(r, p, &maps.out, piece, w, at, feature, lane);
           }
         }
       }
@@ -945,7 +1084,7 @@ cudaError_t launch_t(const Maps& m, const Params& p, cudaLaunchConfig_t cfg) {
   }
   // As many units as there can be at most: every row tile but one of an expert's full.
   const int64_t tiles = MODE == GRADIENT
-                            ? static_cast<int64_t>(p.E) * p.k_tiles
+                            ? static_cast<int64_t>(p.E) * p.n_tiles
                             : (p.rows < p.E ? p.rows : p.E) + p.rows / S::ROWS;
   const int64_t units = tiles * p.f_tiles;
   if (units > 0x3fffffff) return cudaErrorInvalidConfiguration;
@@ -1032,8 +1171,8 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
   p.top = static_cast<int32_t>(a.top);
   const bool wide = a.out_dtype == MHR_F32;
   const int tile_rows = wide ? 128 : 256;
-  p.f_tiles = static_cast<int32_t>((a.N + TILE_F - 1) / TILE_F);
-  p.k_tiles = static_cast<int32_t>((a.K + tile_rows - 1) / tile_rows);
+  p.f_tiles = static_cast<int32_t>(((gradient ? a.K : a.N) + TILE_F - 1) / TILE_F);
+  p.n_tiles = static_cast<int32_t>((a.N + tile_rows - 1) / tile_rows);
   p.kind = a.dtype == MHR_BF16 ? 1 : 0;
   p.out_dtype = a.out_dtype;
   p.pairs = !wide && reinterpret_cast<uintptr_t>(a.out) % 4 == 0 && a.ldo % 2 == 0 &&
@@ -1070,10 +1209,11 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
                               static_cast<uint64_t>(parts)};
     const uint64_t pitch[2] = {static_cast<uint64_t>(ld * size),
                                static_cast<uint64_t>((parts == 1 ? out_rows * ld : a.stride_o) * size)};
-    const uint32_t box[3] = {32, 32, 1};
+    const uint32_t box[3] = {gradient && !wide ? 64u : 32u, 32, 1};
     if (encode_tmap_3d(&m.out,
                        wide ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                       a.out, dims, pitch, box) != CUDA_SUCCESS)
+                       a.out, dims, pitch, box,
+                       gradient ? swizzle : CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
       p.out_tma = 0;  // (a pitch past TMA's: the rows go out from registers)
   }
   if (!none) {
@@ -1095,8 +1235,9 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
       e = ready(a.w, 1, a.out_rows, a.N, a.ldw, 0, nullptr, a.scatter, 1, a.rows, &at, s, &w);
       if (e != cudaSuccess) return e;
       p.scatter = nullptr;
-      for (int i = 0; i < 4; ++i) ok = ok && rows_map(&m.w[i], w, a.N, 16u << i);
-      ok = ok && rows_map(&m.w1, w, a.N, 1);
+      for (int i = 0; i < 4; ++i)
+        ok = ok && rows_map(&m.w[i], x, a.K, 16u << i) && rows_map(&m.x[i], w, a.N, 16u << i);
+      ok = ok && rows_map(&m.w1, x, a.K, 1) && rows_map(&m.x1, w, a.N, 1);
     } else {
       const bool t = a.kind == ProductKind::transposed;
       const int64_t rows = t ? a.N : a.K, cols = t ? a.K : a.N;
@@ -1109,9 +1250,9 @@ cudaError_t launch_product(const ProductArgs& a, void* scratch, const DeviceCtl&
       const uint64_t pitch[2] = {static_cast<uint64_t>(ld) * 2, static_cast<uint64_t>(stride) * 2};
       const uint32_t box[3] = {64, 128, 1};
       ok = encode_tmap_3d(&m.w[3], type, w.p, dims, pitch, box, swizzle) == CUDA_SUCCESS;
+      for (int i = 0; i < 4; ++i) ok = ok && rows_map(&m.x[i], x, a.K, 16u << i);
+      ok = ok && rows_map(&m.x1, x, a.K, 1);
     }
-    for (int i = 0; i < 4; ++i) ok = ok && rows_map(&m.x[i], x, a.K, 16u << i);
-    ok = ok && rows_map(&m.x1, x, a.K, 1);
     if (!ok) return cudaErrorInvalidValue;
   }
   MainKernelEvents ev(s);
