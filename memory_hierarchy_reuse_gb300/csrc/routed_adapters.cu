@@ -239,7 +239,11 @@ __global__ void __launch_bounds__(ROW_THREADS) __cluster_dims__(CTAS, 1, 1)
 
 // Tiles: 128 rows of one adapter, in the order of routed_sort.cu.
 constexpr int TILE = 128;
-constexpr int BK = 64;                        // of x's columns a stage: 128 bytes a row
+// Of x's columns a stage: two boxes of 128 bytes a row, since a stage costs the warps that
+// load and multiply some 700 cycles whatever it holds (513 rows of 4096 x 4096 and rank 64
+// 36.5 us with one box, 34.6 with two; 4096 x 11008 and rank 16 47.4 and 43.5).
+constexpr int BK = 128;
+constexpr int XBOX = TILE * 128;
 constexpr int BLOCK_N = 128;                  // of the output's columns an accumulator
 constexpr int EPI_WARPS = 8;
 constexpr int EPI_THREADS = 32 * EPI_WARPS;
@@ -284,6 +288,20 @@ __device__ __forceinline__ void tma_gather4(uint32_t dst, const CUtensorMap* map
       " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(r[0]), "r"(r[1]), "r"(r[2]),
       "r"(r[3])
+      : "memory");
+}
+// mma_f16 by the low words of the descriptors: the address and the leading offset.
+__device__ __forceinline__ uint32_t desc_word(uint32_t saddr, uint32_t lbo_bytes) {
+  return ((saddr & 0x3FFFFu) >> 4) | (lbo_bytes >> 4) << 16;
+}
+__device__ __forceinline__ void mma_words(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t idesc,
+                                          uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 x, {%1, %5};\n\tmov.b64 y, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(mx::DESC_HI_SW128)
       : "memory");
 }
 __device__ __forceinline__ float4 ld_shared_cluster_v4(uint32_t addr) {
@@ -485,16 +503,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     const bool stall = p.inject_stall && blockIdx.x == 0;
     uint32_t s = 0, ph = 1, it = 0, up_it = 0;
     bool ok = true;
-    const uint32_t tx1 = TILE * 128 + v_cols * 128, tx2 = 2 * v_cols * 128;
-    // place s of a ring of `of`, armed
-    auto next = [&](uint32_t full, uint32_t empty, uint32_t tx) {
-      if (!wait(empty, ph)) {
-        give_up(kErrTimeoutProducer);
-        ok = false;
-        return;
-      }
-      if (lane == 0) mbar_arrive_expect_tx(full, tx);
-      __syncwarp();
+    const uint32_t tx1 = 2 * (XBOX + v_cols * 128), tx2 = 2 * v_cols * 128;
+    auto next = [&](uint32_t empty) {
+      ok = wait(empty, ph);
+      if (!ok) give_up(kErrTimeoutProducer);
+      return ok;
     };
     auto advance = [&](uint32_t of) {
       __syncwarp();
@@ -504,18 +517,22 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       }
     };
     for (int kb = kb0; ok && kb < kb1; ++kb) {
-      next(full_bar(s), empty_bar(s), tx1);
-      if (!ok) break;
-      const uint32_t st = ring + s * stage_bytes, fb = full_bar(s);
-      if (!(stall && kb == kb0)) {
-        if (elect_one()) {
-          tma_load_3d(st + TILE * 128, &maps.down, fb, kb * BK, 0, a);
-          if (whole) {
-            tma_load_2d(st, &maps.x, fb, kb * BK, from[0]);
-          } else {
+      if (!next(empty_bar(s))) break;
+      const uint32_t st = ring + s * 2 * stage_bytes, fb = full_bar(s);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(fb, tx1);
+        if (!(stall && kb == kb0)) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-              if (lying[g]) tma_load_2d(st + g * 4096, &maps.x32, fb, kb * BK, from[g]);
+          for (int h = 0; h < 2; ++h) {  // (a second box past K comes as zeros)
+            const int k = kb * BK + 64 * h;
+            if (whole) {
+              tma_load_2d(st + h * XBOX, &maps.x, fb, k, from[0]);
+            } else {
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                if (lying[g]) tma_load_2d(st + h * XBOX + g * 4096, &maps.x32, fb, k, from[g]);
+            }
+            tma_load_3d(st + 2 * XBOX + h * v_cols * 128, &maps.down, fb, k, 0, a);
           }
         }
       }
@@ -530,12 +547,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       ok = false;
     }
     auto load_up = [&](int n) {
-      next(up_bar(s), up_free_bar(s), tx2);
-      if (!ok) return;
+      if (!next(up_free_bar(s))) return;
       const uint32_t st = ring + s * stage_bytes, fb = up_bar(s);
-      if (!(stall && kb0 == kb1 && n == n0) && elect_one()) {
-        tma_load_3d(st, &maps.up, fb, n * BLOCK_N, 0, a);
-        tma_load_3d(st + v_cols * 128, &maps.up, fb, n * BLOCK_N + 64, 0, a);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(fb, tx2);
+        if (!(stall && kb0 == kb1 && n == n0)) {
+          tma_load_3d(st, &maps.up, fb, n * BLOCK_N, 0, a);
+          tma_load_3d(st + v_cols * 128, &maps.up, fb, n * BLOCK_N + 64, 0, a);
+        }
       }
       ++up_it;
       advance(p.stages);
@@ -583,17 +602,18 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         break;
       }
       tc_fence_after();
-      const uint32_t st = ring + s * stage_bytes;
+      const uint32_t st = ring + s * 2 * stage_bytes;
       if (in == run) {
         in = 0;
         d += BOXES * 64;
       }
+      const uint32_t a = desc_word(st, 16), b = desc_word(st + 2 * XBOX, 16);
+      const uint32_t more = in > 0 ? 1u : 0u;
       if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk)
-          mma_f16(d, smem_desc_sw128(st + kk * 32, 16, 1024),
-                  smem_desc_sw128(st + TILE * 128 + kk * 32, 16, 1024), id1,
-                  in > 0 || kk > 0 ? 1u : 0u);
+          mma_words(d, a + kk / 4 * (XBOX >> 4) + kk % 4 * 2, b + kk / 4 * (v_cols * 8) + kk % 4 * 2,
+                    id1, kk > 0 ? 1u : more);
         mma_commit(empty_bar(s));
         if (kb + 1 == kb1) mma_commit(sums_bar);
       }
@@ -616,16 +636,14 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
       }
       tc_fence_after();
       const uint32_t st = ring + s * stage_bytes;
+      const uint32_t v0 = desc_word(v_base, 16), up0 = desc_word(st, v_cols * 128);
       if (elect_one()) {
-        uint32_t more = 0;
-        for (int term = 0; term < TERMS; ++term)
-          for (int kk = 0; kk < v_cols / 16; ++kk) {
-            mma_f16(tmem + ACC0 + b * BLOCK_N,
-                    smem_desc_sw128(v_base + (term * BOXES + kk / 4) * (TILE * 128) + kk % 4 * 32,
-                                    16, 1024),
-                    smem_desc_sw128(st + kk * 2048, v_cols * 128, 1024), id2, more);
-            more = 1;
-          }
+        for (int kk = 0; kk < v_cols / 16; ++kk)
+#pragma unroll
+          for (int term = 0; term < TERMS; ++term)
+            mma_words(tmem + ACC0 + b * BLOCK_N,
+                      v0 + (term * BOXES + kk / 4) * (TILE * 8) + kk % 4 * 2, up0 + kk * 128, id2,
+                      kk > 0 || term > 0 ? 1u : 0u);
         mma_commit(up_free_bar(s));
         mma_commit(acc_bar(b));
       }
@@ -698,9 +716,11 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             ok = false;
             break;
           }
-          if (lane < 4 && !(stall && i == 0))
-            tma_gather4(ring + s * stage_bytes + (r0 + (e & 1) * 16) * 128 + lane * 512, &maps.x1,
-                        full_bar(s), (kb0 + i) * BK, r);
+          if (lane < 4 && !(stall && i == 0)) {
+            const uint32_t to = ring + s * 2 * stage_bytes + (r0 + (e & 1) * 16) * 128 + lane * 512;
+            tma_gather4(to, &maps.x1, full_bar(s), (kb0 + i) * BK, r);
+            tma_gather4(to + XBOX, &maps.x1, full_bar(s), (kb0 + i) * BK + 64, r);
+          }
           __syncwarp();
           if (++s == static_cast<uint32_t>(p.stages1)) {
             s = 0;
@@ -1023,7 +1043,8 @@ cudaError_t launch_tiles(const AdapterArgs& a, const AdapterParams& r, TileParam
   static_assert(STAGES >= 2, "shared memory");
   constexpr int SMEM = V + STAGES * STAGE + SLOTS * EPI_WARPS * SLOT + 1024;
   p.stages = STAGES;
-  constexpr int STAGES1 = (STAGES * STAGE + SLOTS * EPI_WARPS * SLOT) / STAGE;
+  constexpr int STAGES1 = (STAGES * STAGE + SLOTS * EPI_WARPS * SLOT) / (2 * STAGE);
+  static_assert(STAGES1 >= 2, "shared memory");
   p.stages1 = STAGES1 < MAX_STAGES ? STAGES1 : MAX_STAGES;
   p.slots = SLOTS;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
@@ -1066,9 +1087,9 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 // Whether every row has a cluster of its own.  That kernel's time grows with the rows, the
 // tiles' hardly does until they fill the device.  In us (bf16, 8 adapters), rows' / tiles':
 //     K, N, rank       128 rows    256 rows    512 rows
-//     4096, 4096, 16    9.4 / 22   17.4 / 22   30.5 / 23
-//     4096, 4096, 64   17.2 / 35   30   / 33   56   / 34
-//     1024, 1024, 16    7.4 / 16   13.4 / 16   23.5 / 16
+//     4096, 4096, 16    9.4 / 22   17.4 / 22   30.5 / 22
+//     4096, 4096, 64   17.2 / 35   30   / 33   56   / 32
+//     1024, 1024, 16    7.4 / 16   13.4 / 15   23.5 / 15
 //     4096, 11008, 16  13.8 / 33   25.5 / 30   48   / 31
 // Up to 512 rows that may have an adapter for every 8 of them keep to rows too: with 64
 // adapters in no order, a tile each, the last line's 512 rows are 48 / 160.
