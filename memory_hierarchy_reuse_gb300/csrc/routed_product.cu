@@ -489,7 +489,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     abort_flag = 0;
     fence_mbar_init();
-    if (p.K > 0) {
+    if (p.K > 0 && p.rows > 0) {  // (else there are no maps)
       tma_prefetch_desc(&maps.w[3]);
       for (int i = 0; i < 4; ++i) tma_prefetch_desc(&maps.x[i]);
     }

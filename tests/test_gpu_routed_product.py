@@ -402,3 +402,21 @@ def test_two_streams_at_once(mhr):
         torch.cuda.synchronize()
         for j in range(2):
             assert all(torch.equal(o, want[j]) for o in outs[j])
+
+
+@pytest.mark.parametrize("out_dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("K,N,left,pad", [(300, 200, 8, 16), (300, 199, 3, 8), (33, 330, 0, 2),
+                                          (513, 97, 1, 0), (256, 257, 2, 3)])
+def test_gradient_into_a_larger_matrix(mhr, out_dtype, K, N, left, pad):
+    """Rows that TMA can write and rows that start anywhere, ends inside every tile."""
+    import torch
+
+    at, offsets = offsets_of([140, 0, 300])
+    dtype = "f16" if out_dtype == "f16" else "bf16"
+    x, g = whole((440, K), dtype, 1), whole((440, N), dtype, 2)
+    buf = torch.full((3, K + 2, left + N + pad), 7.0, dtype=types()[out_dtype], device="cuda")
+    out = buf[:, 1:K + 1, left:left + N]
+    mhr.matmul_experts_grad(x, g, offsets, out=out)
+    same(out, ref.weight_grad(f64(x), f64(g), at))
+    out.fill_(7)
+    assert bool((buf == 7).all())
