@@ -20,6 +20,11 @@
 // 4283 us with it against 1143 for rows in order; copies by the threads into the same
 // layout were as slow.)  A row outside its matrix -- past an expert's last, or an index
 // out of range -- is zeros.
+//
+// GB300: few rows are bound by the weights' bytes (30 tokens, 8 of 128 experts of 2048 x
+// 1536: 100 us, 6.7 TB/s; one token 12.2 us), and so are up to 128 rows an expert (4096 x
+// 1536: 262 us, 6.9 TB/s, 790 TFLOP/s); at 256 rows 1.2 to 1.4 PFLOP/s.  The gradient of 64
+// experts of 2048 x 1408 in fp32: 179 us of sorted rows, of which the stores alone are 123.
 #include <cuda_runtime.h>
 
 #include <cstdint>

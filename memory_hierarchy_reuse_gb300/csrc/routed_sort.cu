@@ -8,7 +8,7 @@
 // puts the positions there, equal experts of 32 entries in their order.
 // Bound by latency: a run's loads, 16 a lane, go out together, and a bin's 32
 // counters, and 8 or 16 CTAs' totals, are read at once.  GB300: 131072 entries of 256
-// experts in 36 us with one load and one counter at a time and 8 CTAs.
+// experts in 11.8 us (36 with one load and one counter at a time and 8 CTAs), 64 in 5.
 #include <cuda_runtime.h>
 
 #include <cstdint>
