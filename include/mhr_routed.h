@@ -144,8 +144,9 @@ int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, int64_t ld
  * rank x N at up + a * stride_u, pitch ldu, all of type dtype (MHR_BF16 or
  * MHR_F16); scales: L floats, or NULL for 1; y, out: T x N, of type out_dtype
  * (any).  out may be y itself (the same address and pitch).  A row whose which
- * lies outside 0 .. L-1 has no adapter: out_t = y_t.  Both sums are held in fp32,
- * and so is x_t down_a^T between them; out is rounded once.
+ * lies outside 0 .. L-1 has no adapter: out_t = y_t.  Both sums are held in fp32;
+ * x_t down_a^T is kept to 2^-22 of the row's largest sum between them, whatever T
+ * and the types are; out is rounded once.
  * Limits: L <= 1024, rank <= 128.
  *
  * scratch: gemm_routed_adapters_scratch bytes (0 for few rows; -1 for arguments

@@ -13,7 +13,8 @@
 // 7), many by HBM in phases, x, v's exchange, y (8192 of 4096 x 4096, rank 64: 62 us, 3.3
 // TB/s; 17 of it the exchange, the sort and the launches).
 // v stays in 32 bits on the way: for the tensor cores it is written as a sum of 16-bit
-// terms (hi + lo, and a third for fp32 results of bf16).
+// terms (three of bf16, two of fp16), good to 2^-22 of a row's largest, whatever the
+// result's type: a row's value does not go by how many rows come with it.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -354,14 +355,14 @@ struct Tile {
 
 // T: of x and the adapters; O: of y and the output.  BOXES: 64 columns of v each.
 //
-// v is given to the tensor cores as TERMS values of T whose sum it is to 2^-16 (two of
-// bf16) or 2^-22 and less (three; two of fp16, taken times a power of two a row so that
-// neither leaves fp16's range) of it, or of the row's largest.
+// v is given to the tensor cores as TERMS values of T whose sum it is to 2^-24 of it (three
+// of bf16) or 2^-22 of the row's largest (two of fp16, taken times a power of two a row so
+// that neither leaves fp16's range).
 template <typename T, typename O, int BOXES>
 __global__ void __launch_bounds__(TILE_THREADS, 1)
     adapters_tile_kernel(const __grid_constant__ TileMaps maps, const TileParams p) {
   constexpr bool HALF = std::is_same_v<T, __half>, WIDE = sizeof(O) == 4;
-  constexpr int TERMS = WIDE && !HALF ? 3 : 2;
+  constexpr int TERMS = HALF ? 2 : 3;
   constexpr int SUMS = WIDE ? 4 / BOXES : 1;   // accumulators of v (see below)
   constexpr int BOX_COLS = WIDE ? 32 : 64;     // of the output, 128 bytes
   constexpr int PARTS = 64 / BOX_COLS;         // boxes of a warp's half of a block
@@ -1035,7 +1036,7 @@ cudaError_t launch_tiles(const AdapterArgs& a, const AdapterParams& r, TileParam
                          const TileMaps& maps, const DeviceCtl& ctl, cudaStream_t s) {
   auto kern = adapters_tile_kernel<T, O, BOXES>;
   constexpr bool HALF = std::is_same_v<T, __half>;
-  constexpr int TERMS = sizeof(O) == 4 && !HALF ? 3 : 2;
+  constexpr int TERMS = HALF ? 2 : 3;
   constexpr int STAGE = TILE * 128 + BOXES * 64 * 128;
   constexpr int TERM_BYTES = TERMS * BOXES * TILE * 128, PART_BYTES = TILE * (BOXES * 64 * 4 + 16);
   constexpr int V = ((TERM_BYTES > PART_BYTES ? TERM_BYTES : PART_BYTES) + 1023) / 1024 * 1024;
