@@ -147,6 +147,9 @@ int gemm_routed_weight_grad(int dtype, const void* x, int64_t x_rows, int64_t ld
  * lies outside 0 .. L-1 has no adapter: out_t = y_t.  Both sums are held in fp32;
  * x_t down_a^T is kept to 2^-22 of the row's largest sum between them, whatever T
  * and the types are; out is rounded once.
+ * Infinities and NaN of x, down, y and scales give what the sums above give, and in
+ * no other row; an infinity in up gives elements that are not finite, each an
+ * infinity or NaN.
  * Limits: L <= 1024, rank <= 128.
  *
  * scratch: gemm_routed_adapters_scratch bytes (0 for few rows; -1 for arguments

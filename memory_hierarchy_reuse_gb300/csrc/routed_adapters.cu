@@ -790,20 +790,21 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
             v[c + 3] += o[c / 4].w;
           }
       }
+      // (v's columns past the rank are x times down's missing rows: an infinity there would be
+      // NaN, and reach every column of the output by up's)
 #pragma unroll
-      for (int c = 0; c < COLS; ++c) v[c] *= scale;
+      for (int c = 0; c < COLS; ++c) v[c] = h * half_cols + c < p.rank ? v[c] * scale : 0.f;
       cluster_arrive();  // this thread has read the parts
       float unit = 1.f;
       if constexpr (HALF) {
-        // A power of two a row that brings its largest to [2^13, 2^14).
+        // A power of two a row that brings its largest finite value to [2^13, 2^14).
 #pragma unroll
-        for (int c = 0; c < COLS; ++c) high = fmaxf(high, fabsf(v[c]));
+        for (int c = 0; c < COLS; ++c) high = fmaxf(high, isfinite(v[c]) ? fabsf(v[c]) : 0.f);
         row_max[h][row] = high;
         asm volatile("barrier.cta.sync 1, %0;" ::"n"(EPI_THREADS) : "memory");
         high = fmaxf(row_max[0][row], row_max[1][row]);
         const int x = static_cast<int>(__float_as_uint(high) >> 23);  // 0: below 2^-126
-        // (a row that is not finite, and zero, as they are)
-        if (high > 0.f && x < 255) {
+        if (high > 0.f) {
           const int up = min(max(13 + 127 - x, -100), 100);
           unit = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
           if (h == 0) row_unit[row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);

@@ -51,3 +51,48 @@ def test_the_sum_between_an_adapters_products_is_held_to_22_bits(mhr, T, rank, d
     want = ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy())
     assert want.min() == 2.0 ** (-5 - min(T - 1, 7)) and want.max() == 2.0 ** -5
     same(got, want)
+
+
+@pytest.mark.parametrize("T", [6, 300, 700])
+@pytest.mark.parametrize("rank", [1, 8, 16, 70])
+@pytest.mark.parametrize("dtype,out", [("bf16", "bf16"), ("bf16", "f32"), ("f16", "f16")])
+def test_infinities_of_x_are_the_definitions(mhr, T, rank, dtype, out):
+    """Which outputs are an infinity, of which sign, and which are NaN does not depend on how many
+    rows there are, or on the rank's being no multiple of 16."""
+    import torch
+
+    rng = np.random.default_rng(rank)
+    K, N = 72, 136
+    x = rng.integers(-3, 4, (T, K)).astype(np.float32)
+    x[1, 5], x[2, 71], x[4, 0] = np.inf, -np.inf, np.nan
+    down = rng.choice([-1.0, 1.0], (2, rank, K)).astype(np.float32)
+    up = rng.choice([-1.0, 1.0], (2, rank, N)).astype(np.float32)
+    up[:, :, :N // 2] = down[:, :, 5:6]  # columns in which a row's infinities have one sign
+    x, down, up = (torch.from_numpy(t).to(types()[dtype]).cuda() for t in (x, down, up))
+    y = torch.from_numpy(rng.integers(-50, 51, (T, N))).to(types()[out]).cuda()
+    which = (torch.arange(T, dtype=torch.int32, device="cuda") // 3) % 2
+    which[5] = -1
+    with np.errstate(invalid="ignore"):
+        want = ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy())
+    assert np.isinf(want[1]).sum() >= N // 2 and np.isnan(want[4]).all()
+    same(mhr.add_adapters(y, x, down, up, which), want)
+
+
+@pytest.mark.parametrize("T", [6, 300])
+@pytest.mark.parametrize("dtype,out", [("bf16", "f32"), ("f16", "f16"), ("f16", "f32")])
+def test_an_infinity_of_down_leaves_the_other_sums(mhr, T, dtype, out):
+    """Beside it, sums that fp16 does not hold."""
+    import torch
+
+    rng = np.random.default_rng(7)
+    K, N, rank = 64, 72, 12
+    x = 64.0 * rng.integers(1, 4, (T, K))
+    down = 256.0 * rng.choice([-1.0, 1.0], (2, rank, K))
+    down[0, 4, 3] = np.inf
+    up = rng.choice([-1.0, 1.0], (2, rank, N))
+    x, down, up = (torch.from_numpy(t).to(types()[dtype]).cuda() for t in (x, down, up))
+    y = torch.zeros(T, N, dtype=types()[out], device="cuda")
+    which = (torch.arange(T, dtype=torch.int32, device="cuda") // 3) % 2
+    want = ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy())
+    assert np.isinf(want[:3]).all() and np.abs(want[3:6]).max() > 2.0 ** 17
+    same(mhr.add_adapters(y, x, down, up, which), want)
