@@ -805,7 +805,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
         high = fmaxf(row_max[0][row], row_max[1][row]);
         const int x = static_cast<int>(__float_as_uint(high) >> 23);  // 0: below 2^-126
         if (high > 0.f) {
-          const int up = min(max(13 + 127 - x, -100), 100);
+          const int up = min(13 + 127 - x, 126);  // (-114 at least: both powers are normal)
           unit = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
           if (h == 0) row_unit[row] = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
         } else if (h == 0) {

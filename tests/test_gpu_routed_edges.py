@@ -96,3 +96,27 @@ def test_an_infinity_of_down_leaves_the_other_sums(mhr, T, dtype, out):
     want = ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy())
     assert np.isinf(want[:3]).all() and np.abs(want[3:6]).max() > 2.0 ** 17
     same(mhr.add_adapters(y, x, down, up, which), want)
+
+
+@pytest.mark.parametrize("T", [6, 300])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("exponent", [-126, -115, -100, 100, 112, 118])
+def test_adapters_of_far_scales(mhr, T, dtype, exponent):
+    """Sums between the products next to either end of fp32's range. All values are whole numbers
+    times a power of two, and no larger than 2^127."""
+    import torch
+
+    rng = np.random.default_rng(3)
+    K, N, rank = 64, 72, 5
+    x, down, up = (torch.from_numpy(rng.integers(-3, 4, s)).to(types()[dtype]).cuda()
+                   for s in ((T, K), (2, rank, K), (2, rank, N)))
+    if exponent > 0:
+        up = up * 2.0 ** -12
+    y = torch.zeros(T, N, device="cuda")
+    which = (torch.arange(T, dtype=torch.int32, device="cuda") // 3) % 2
+    scales = torch.full((2,), 2.0 ** exponent, device="cuda")
+    assert float(scales[0]) == 2.0 ** exponent
+    got = mhr.add_adapters(y, x, down, up, which, scales)
+    want = ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy(), f64(scales))
+    assert bool(np.abs(want).max() < 2.0 ** 127)
+    same(got, want)
