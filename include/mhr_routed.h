@@ -100,7 +100,9 @@ int gemm_routed_sort(const int32_t* experts, int64_t n, int64_t E, int32_t* offs
  * its token's.  A row of x outside 0 .. x_rows-1 counts as zeros, one of out
  * outside 0 .. out_rows-1 is not written; entries of scatter are distinct.
  * Rows of out of no sorted position, and those at offsets[E] and after, stay as
- * they were.  Offsets below the one before or past `rows` count as that.
+ * they were.  Offsets below 0 or past `rows` count as that; an expert whose end lies
+ * below its start has no positions, and one that starts below an earlier expert's
+ * end starts there, so that no position is two experts'.
  * K == 0 writes zeros.  E <= 1024.
  *
  * scratch: gemm_routed_product_scratch bytes, for x's rows in the order of gather

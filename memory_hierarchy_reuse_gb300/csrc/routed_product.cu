@@ -520,7 +520,8 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
     return scan;
   };
-  const bool few = MODE != GRADIENT && p.rows <= FEW_ROWS;
+  bool few = MODE != GRADIENT && p.rows <= FEW_ROWS;
+  bool falls = false;  // an offset that this thread has seen lies below the one before
   if (few) {
     // Units of like cost: in the experts' order, by one warp, 128 offsets at a time.
     if (warp == 0) {
@@ -537,6 +538,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = e0 + 32 * i + lane;
+          falls |= b[i] < a[i];
           a[i] = min(max(a[i], 0), p.rows);
           b[i] = min(max(b[i], a[i]), p.rows);
           const uint32_t c = e < p.E ? units_of(b[i] - a[i]) : 0, scan = scan_of(c);
@@ -558,7 +560,7 @@ __global__ void __launch_bounds__(THREADS, 1)
     }
   } else {
     for (int e = threadIdx.x; e < p.E; e += THREADS) {
-      // (offsets that are not ascending, or past the rows, reach nothing)
+      falls |= p.offsets[e + 1] < p.offsets[e];
       const int a = min(max(p.offsets[e], 0), p.rows), b = min(max(p.offsets[e + 1], a), p.rows);
       lo[e] = a;
       num[e] = b - a;
@@ -567,7 +569,37 @@ __global__ void __launch_bounds__(THREADS, 1)
       atomicAdd(&class_experts[k], 1u);
     }
   }
-  __syncthreads();
+  if (__syncthreads_or(falls)) {
+    // Once more, in the experts' order: rows that an earlier expert has stay its own, so
+    // that no two clusters write one row and a gradient counts it once.
+    few = false;
+    if (threadIdx.x < CLASSES) class_units[threadIdx.x] = class_experts[threadIdx.x] = 0;
+    __syncthreads();
+    if (warp == 0) {
+      int taken = 0;  // behind the last row of the experts so far
+      for (int e0 = 0; e0 < p.E; e0 += 32) {
+        const int e = e0 + lane, last = min(e, p.E - 1);
+        const int from = min(max(p.offsets[last], 0), p.rows);
+        const int to = min(max(p.offsets[last + 1], 0), p.rows);
+        int most = to > from ? to : 0;  // of this lane's expert and those before
+#pragma unroll
+        for (int i = 1; i < 32; i <<= 1) {
+          const int o = __shfl_up_sync(ALL, most, i);
+          if (lane >= i) most = max(most, o);
+        }
+        const int before = __shfl_up_sync(ALL, most, 1);
+        const int a = max(from, max(taken, lane ? before : 0)), n = max(to - a, 0);
+        if (e < p.E) {
+          lo[e] = a;
+          num[e] = n;
+          atomicAdd(&class_units[cost_class<MODE, ROWS>(n)], units_of(n));
+          atomicAdd(&class_experts[cost_class<MODE, ROWS>(n)], 1u);
+        }
+        taken = max(taken, __shfl_sync(ALL, most, 31));
+      }
+    }
+    __syncthreads();
+  }
   static_assert(THREADS / 32 >= CLASSES, "a warp a class");
   if (!few && warp < CLASSES) {
     uint32_t unit = 0, place = 0;

@@ -120,3 +120,55 @@ def test_adapters_of_far_scales(mhr, T, dtype, exponent):
     want = ref.adapters(f64(y), f64(x), f64(down), f64(up), which.cpu().numpy(), f64(scales))
     assert bool(np.abs(want).max() < 2.0 ** 127)
     same(got, want)
+
+
+def parts_of(offsets, rows):
+    """Where each expert's rows start and end, by the header's words."""
+    parts, last = [], 0
+    for a, b in zip(offsets[:-1], offsets[1:]):
+        a, b = (min(max(v, 0), rows) for v in (a, b))
+        start = max(a, last)
+        parts.append((start, max(b, start)))
+        if b > a:
+            last = max(last, b)
+    return parts
+
+
+FALLING = [[0, 10, 0, 10], [0, 5, 3, 10], [3, 1, 99], [-7, 4, -1, 6, 2, 9], [9, 0, 4, 3, 8, 8, 1],
+           [0] + [7, 3] * 60 + [16], list(range(16, -1, -1))]
+
+
+@pytest.mark.parametrize("rows", [16, 400])
+@pytest.mark.parametrize("offsets", FALLING, ids=lambda o: str(o[:7]))
+def test_offsets_that_fall(mhr, offsets, rows):
+    """No position belongs to two experts: products and gradients repeat, and count it once."""
+    import torch
+
+    scale = rows // 16
+    at = [v * scale for v in offsets]
+    E = len(at) - 1
+    rng = np.random.default_rng(E)
+    x, w, g = (torch.from_numpy(rng.integers(-3, 4, s)).bfloat16().cuda()
+               for s in ((rows, 72), (E, 72, 136), (rows, 136)))
+    o = torch.tensor(at, dtype=torch.int32, device="cuda")
+    parts = parts_of(at, rows)
+    owner = np.zeros(rows, int)
+    for start, end in parts:
+        owner[start:end] += 1
+    assert owner.max() <= 1
+    for out_dtype in (torch.bfloat16, torch.float32):
+        out = torch.full((rows, 136), 7.0, dtype=out_dtype, device="cuda")
+        mhr.matmul_experts(x, w, o, out=out)
+        want = np.full((rows, 136), 7.0)
+        for e, part in enumerate(parts):
+            ref.product(f64(x), f64(w)[e:e + 1], part, rows, out=want)
+        same(out, want)
+        d = mhr.matmul_experts_grad(x, g, o, out_dtype=out_dtype)
+        same(d, np.concatenate([ref.weight_grad(f64(x), f64(g), part) for part in parts]))
+    # an operand that is copied first: the same rows
+    odd = torch.zeros(E, 72, 137, dtype=torch.bfloat16, device="cuda")[:, :, 1:]
+    odd.copy_(w)
+    again = torch.full((rows, 136), 7.0, device="cuda")
+    mhr.matmul_experts(x, odd, o, out=again)
+    same(again, want)
+    assert mhr.gemm_check(None) == mhr.MHR_OK
