@@ -277,6 +277,24 @@ __device__ __forceinline__ float near_by(int kind, float s, float s1, float key)
   return (kind == MHR_SIGMOID ? 0x1p-20f : 0x1p-19f) * (s + s1) + 0x1p-22f * fabsf(key);
 }
 
+// Whether 32 bits do not tell one of this lane's keys from the given one, except for the
+// same numbers.
+template <typename T, int V>
+__device__ __noinline__ bool others_near(const ChooseParams& p, int t, int lane, float logit,
+                                         float bias, float key, float s, float most, float sum) {
+  const Share sh = share_of(p, lane);
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld + sh.first;
+  bool near = false;
+#pragma unroll 1
+  for (int i = 0; i < sh.count; ++i) {
+    const float x = to_float(row[i]), b = p.bias[sh.first + i];
+    const float s1 = score_of<float>(x, p.score, most, sum);
+    near |= !(x == logit && b == bias) &&
+            !(fabsf(key - (s1 + b)) > near_by(p.score, s, s1, key));
+  }
+  return near;
+}
+
 // The order of 32 candidates, a lane each, best first but for neighbours too near: by
 // their keys in double, neighbour by neighbour until none changes places.
 template <typename T, int V>
@@ -499,15 +517,26 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constan
   take(0, p.top + 1);
   look_up(p.top + 1);
 
-  // Neighbours that 32 bits do not tell apart, unless they are the same numbers.
+  // Neighbours that 32 bits do not tell apart, unless they are the same numbers.  Behind the
+  // first key that is not chosen may follow others whose scores, and errors, are larger: the
+  // last chosen one is held against the largest score there is (or, where the one behind it
+  // is the same, against all).
+  const float high_score = softmax && sum > 0.f ? __fdividef(1.f, sum) : 1.f;
   bool near = false;
   if (scored) {
     const float key = of_sortable(mine), key1 = __shfl_down_sync(ALL, key, 1);
     const float l1 = __shfl_down_sync(ALL, logit, 1), s1 = __shfl_down_sync(ALL, s, 1);
     const float b = expert >= 0 ? p.bias[expert] : 0.f, b1 = __shfl_down_sync(ALL, b, 1);
     const int e1 = __shfl_down_sync(ALL, expert, 1);
+    const bool equal = logit == l1 && b == b1, last = lane == p.top - 1;
     if (lane < p.top && e1 >= 0)
-      near = !(logit == l1 && b == b1) && !(key - key1 > near_by(p.score, s, s1, key));
+      near = !equal && !(key - key1 > near_by(p.score, s, last ? high_score : s1, key));
+    if (__any_sync(ALL, last && e1 >= 0 && equal)) {
+      const int from = p.top - 1;
+      near |= others_near<T, V>(p, t, lane, __shfl_sync(ALL, logit, from),
+                                __shfl_sync(ALL, b, from), __shfl_sync(ALL, key, from),
+                                __shfl_sync(ALL, s, from), most, sum);
+    }
   }
   near = __any_sync(ALL, near);
   again = __any_sync(ALL, again);
@@ -517,7 +546,8 @@ __global__ void __launch_bounds__(WARPS * 32) choose_kernel(const __grid_constan
     look_up(32);
     const float key = of_sortable(mine);
     const float last = __shfl_sync(ALL, key, p.top - 1), s0 = __shfl_sync(ALL, s, p.top - 1);
-    const bool far = mine == NONE || last - key > near_by(p.score, s0, s, fabsf(last) + fabsf(key));
+    const bool far = mine == NONE ||
+                     last - key > near_by(p.score, s0, high_score, fabsf(last) + fabsf(key));
     again = !__shfl_sync(ALL, static_cast<int>(far), 31);
   }
   if (again || near) {

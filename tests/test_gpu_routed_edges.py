@@ -172,3 +172,44 @@ def test_offsets_that_fall(mhr, offsets, rows):
     mhr.matmul_experts(x, odd, o, out=again)
     same(again, want)
     assert mhr.gemm_check(None) == mhr.MHR_OK
+
+
+def chosen(mhr, x, bias, top, score, **kw):
+    import torch
+
+    e, _ = mhr.choose_experts(torch.from_numpy(x).cuda(), top, score, torch.from_numpy(bias).cuda(),
+                              **kw)
+    want, _ = ref.choose(x.astype(np.float64), top, score, bias.astype(np.float64), **kw)
+    assert np.array_equal(e.cpu().numpy(), want)
+    return want
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E", [40, 300])
+@pytest.mark.parametrize("apart", [1e-8, 0])
+def test_a_far_score_behind_the_first_rejected_key(mhr, score, E, apart):
+    """The last chosen and the first rejected key have scores near zero, which 32 bits tell apart
+    (or they are the same); behind them, within its own error of both, comes a high score with a negative bias."""
+    T, high = 1000, E - 2
+    x = np.full((T, E), -30, np.float32)
+    bias = np.full(E, -5, np.float32)
+    x[:, 3], bias[3] = (1.5, 1) if score == "sigmoid" else (0.1, 1)
+    x[:, high] = (score == "sigmoid") + np.random.default_rng(2).uniform(-4e-7, 4e-7, T)
+    s = ref.scores(x.astype(np.float64), score)[:, high]
+    bias[5], bias[E // 2], bias[high] = 0.01, 0.01 - apart, 0.01 - s.mean()
+    want = chosen(mhr, x, bias, 2, score)
+    assert set(want[:, 1]) == {5, high}  # the case is what it says
+
+
+def test_a_far_score_behind_32_candidates(mhr):
+    """The same, behind more near keys than a warp has lanes."""
+    T, E, high = 500, 128, 100
+    x = np.full((T, E), -30, np.float32)
+    bias = np.full(E, -5, np.float32)
+    x[:, 3], bias[3] = 1.5, 1
+    bias[10], bias[11], bias[12:60] = 0.01, 0.01 - 1e-9, 0.01 - 6e-9
+    x[:, high] = 1 + np.random.default_rng(2).uniform(-4e-7, 4e-7, T)
+    s = ref.scores(x.astype(np.float64), "sigmoid")[:, high]
+    bias[high] = 0.01 - s.mean()
+    want = chosen(mhr, x, bias, 2, "sigmoid")
+    assert {10, high} <= set(want[:, 1])
