@@ -269,12 +269,16 @@ __device__ __forceinline__ void sort_descending(int (&k)[V]) {
           }
 }
 
-// A key's score is off by expf's 2 ulp, a sum and a quotient: 5 * 2^-23 of it at most, and
-// of a softmax by the rounding of its argument (2^-24 of up to 16 or so;
-// what is further down is too small to matter beside a bias) and its sum's: 2^-20; the
-// sum with the bias by 2^-24 of the key.
+// How far two keys may be off together.  A sigmoid's score: expf's 2 ulp, a sum and a
+// quotient of 2 ulp, 5 * 2^-23 of it at most.  A softmax's, in parts of 2^-24: 4 of expf, 4
+// and 1 of the quotient and the product; 40 of the sum (36 roundings and its terms'), which
+// two scores share, so that the difference is off by half of that for each; and its rounded
+// argument, at most ln(1 / score): 7 down to 2^-10, 88 down to 2^-126.  Below, all these are
+// steps of 2^-149.  The sum with the bias is off by 2^-24 of the key.
 __device__ __forceinline__ float near_by(int kind, float s, float s1, float key) {
-  return (kind == MHR_SIGMOID ? 0x1p-20f : 0x1p-19f) * (s + s1) + 0x1p-22f * fabsf(key);
+  const float sum = 0x1p-22f * fabsf(key) + 0x1p-146f;
+  if (kind == MHR_SIGMOID) return 0x1p-20f * (s + s1) + sum;
+  return 0x1.2p-19f * (s + s1) + 81 * 0x1p-24f * (fminf(s, 0x1p-10f) + fminf(s1, 0x1p-10f)) + sum;
 }
 
 // Whether 32 bits do not tell one of this lane's keys from the given one, except for the

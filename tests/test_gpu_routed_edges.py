@@ -213,3 +213,19 @@ def test_a_far_score_behind_32_candidates(mhr):
     bias[high] = 0.01 - s.mean()
     want = chosen(mhr, x, bias, 2, "sigmoid")
     assert {10, high} <= set(want[:, 1])
+
+
+@pytest.mark.parametrize("depth", [80, 86, 98])
+def test_scores_far_below_the_best(mhr, depth):
+    """Biases as small as softmax scores of e^-depth, whose argument 32 bits round."""
+    rng = np.random.default_rng(1)
+    T, E = 20000, 40
+    x = np.full((T, E), -200, np.float32)
+    x[:, 0] = 40
+    step = 2.0 ** -18 if depth < 90 else 2.0 ** -9
+    x[:, 3] = 40 - depth + step * rng.integers(-40, 41, T)
+    x[:, E - 2] = 39.5 - depth + step * rng.integers(-40, 41, T)
+    bias = np.zeros(E, np.float32)
+    bias[E - 2] = np.exp(-float(depth)) - np.exp(-depth - 0.5)
+    want = chosen(mhr, x, bias, 2, "softmax")
+    assert set(want[:, 1]) == {3, E - 2}
