@@ -465,6 +465,13 @@ at::ScalarType type_number(PyObject* o, at::ScalarType same) {
   return type == MHR_F32 ? at::kFloat : type == MHR_BF16 ? at::kBFloat16 : at::kHalf;
 }
 
+// Where both are given, out is of that type.
+void out_type_ok(PyObject* out, PyObject* type) {
+  if (out != Py_None && type != Py_None &&
+      tensor(out, "out").scalar_type() != type_number(type, at::kFloat))
+    raise(PyExc_TypeError, "%sout must be of out_dtype");
+}
+
 // Scratch of a call on `stream`, of that stream's own memory: what another stream gave
 // back to the allocator may still have that stream's work ahead of it.
 at::Tensor scratch_for(int64_t bytes, int device, void* stream) {
@@ -483,6 +490,7 @@ PyObject* experts(PyObject* const* v, Py_ssize_t n) {
   const int type = half_type(x, w, "x and w");
   const Plain px = plain(x, "x");
   const Parts pw = parts(w, "w");
+  out_type_ok(v[7], v[8]);
   const at::Tensor& offsets = array(v[2], at::kInt, "offsets");
   const int device = device_of({&x, &w, &offsets});
   int64_t rows = -1;
@@ -531,6 +539,7 @@ PyObject* experts_grad(PyObject* const* v, Py_ssize_t n) {
   const at::Tensor &x = tensor(v[0], "x"), &grad = tensor(v[1], "grad");
   const int type = half_type(x, grad, "x and grad");
   const Plain px = plain(x, "x"), pg = plain(grad, "grad");
+  out_type_ok(v[6], v[7]);
   const at::Tensor& offsets = array(v[2], at::kInt, "offsets");
   const int device = device_of({&x, &grad, &offsets});
   int64_t rows = -1;

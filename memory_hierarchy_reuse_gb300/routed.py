@@ -11,7 +11,9 @@ As in ``mxfp4.py``: argument checks and marshalling only (in the compiled
 ``csrc/torch_binding.cpp``), launches on ``stream`` (default: the current torch
 stream) without synchronising, ``GemmError`` for a status other than ``MHR_OK``.
 On a stream other than the current one the caller orders the use of the returned
-tensors itself. All calls can be captured into a graph.
+tensors itself. All calls can be captured into a graph. Automatic differentiation
+records none of them: a gradient is a call of its own (that of ``add_adapters``'
+x is ``add_adapters`` with ``up`` and ``down`` in each other's place).
 """
 from __future__ import annotations
 
@@ -85,8 +87,8 @@ def matmul_experts(x, w, offsets, gather=None, scatter=None, top: int = 1,
     ``scatter`` (int32, one entry a sorted row: ``sort_by_expert``'s ``order``): row q is
     ``x[gather[q] // top]``, and is written to ``out[scatter[q]]`` -- with ``top`` the router's,
     ``x`` is the tokens, and ``out`` in (token, slot) order. ``out`` (of ``out_dtype``, x's when
-    omitted; or given, float32, bfloat16 or float16) is returned. Its rows that no expert has stay
-    as they were: undefined when it is allocated here.
+    omitted; or given, float32, bfloat16 or float16, and of ``out_dtype`` where that is given too)
+    is returned. Its rows that no expert has stay as they were: undefined when it is allocated here.
     """
     return _torch_binding.experts(x, w, offsets, gather, scatter, top, transposed, out,
                                   _out_dtype(out_dtype), stream)
