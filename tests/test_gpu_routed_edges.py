@@ -229,3 +229,38 @@ def test_scores_far_below_the_best(mhr, depth):
     bias[E - 2] = np.exp(-float(depth)) - np.exp(-depth - 0.5)
     want = chosen(mhr, x, bias, 2, "softmax")
     assert set(want[:, 1]) == {3, E - 2}
+
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("T,E,top", [(5, 8, 3), (70, 60, 6), (33, 128, 8), (40, 512, 16)])
+def test_choose_grad_term_by_term(mhr, T, E, top, dtype, score, renormalize):
+    """Each element against the size of its own terms, so that a small one counts as a large one
+    does. In parts of 2^-24, for |l| <= 8: a score or share is off by 44 of it at most (expf 4, its
+    argument 16, sums 21, quotient and product 3); g less its mean by 44 + 16 + 1 of the mean's
+    terms; 1 - s, the scale and the last sum by 8 more: 44 + 61 + 8 < 120. Then the type's
+    rounding, of fp16 half a step of its subnormals at least."""
+    import torch
+
+    rng = np.random.default_rng(T + E)
+    x = torch.from_numpy(np.clip(rng.standard_normal((T, E)) * 1.5, -8, 8)).to(types()[dtype]).cuda()
+    g = rng.standard_normal((T, top)).astype(np.float32)
+    kw = dict(score=score, renormalize=renormalize)
+    e, _ = mhr.choose_experts(x, top, **kw)
+    got = f64(mhr.choose_experts_grad(x, e, torch.from_numpy(g).cuda(), scale=2.5, **kw))
+    x64, at, g = f64(x), e.long().cpu().numpy(), g.astype(np.float64)
+    want = ref.choose_grad(x64, at, g, scale=2.5, **kw)
+    s = ref.scores(x64, score)
+    chosen = np.take_along_axis(s, at, 1)
+    total = chosen.sum(1, keepdims=True) if renormalize else 1.0
+    mean = (chosen / total * np.abs(g)).sum(1, keepdims=True)
+    of = np.zeros((T, E))  # |g| of the chosen, and the mean where it takes part
+    np.put_along_axis(of, at, np.abs(g) + (mean if renormalize else 0), 1)
+    if score == "softmax" and not renormalize:
+        of += mean
+    size = 2.5 * s / total * of * (1 - s if score == "sigmoid" else 1)
+    step = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8, "f16": 2.0 ** -11}[dtype]
+    floor = 2.0 ** -25 if dtype == "f16" else 0
+    floor = floor + 2.0 ** -46 * size.sum(1, keepdims=True)
+    assert np.all(np.abs(got - want) <= 120 * 2.0 ** -24 * size + step * np.abs(want) + floor)
