@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     adapters_tile_kernel(const __grid_constant__ TileMaps maps, const TileParams p) {
   constexpr bool HALF = std::is_same_v<T, __half>, WIDE = sizeof(O) == 4;
   constexpr int TERMS = HALF ? 2 : 3;
-  constexpr int SUMS = WIDE ? 4 / BOXES : 1;   // accumulators of v (see below)
+  constexpr int SUMS = 4 / BOXES;              // accumulators of v (see below)
   constexpr int BOX_COLS = WIDE ? 32 : 64;     // of the output, 128 bytes
   constexpr int PARTS = 64 / BOX_COLS;         // boxes of a warp's half of a block
   extern __shared__ uint8_t smem_raw[];
@@ -487,9 +487,9 @@ __global__ void __launch_bounds__(TILE_THREADS, 1)
     }
     __syncwarp();
   };
-  // For fp32 results v's sums go on in the next of SUMS accumulators every `run` stages:
-  // the tensor cores add by truncation, which takes some 1.4e-8 of a sum off for every 16
-  // terms.
+  // v's sums go on in the next of SUMS accumulators every `run` stages: the tensor cores add by
+  // truncation, which takes 1.4e-8 of a sum off with its first 16 terms and 3e-7 after 256.
+  // (One accumulator was no faster: 8192 rows of 4096 x 4096 and rank 64 62 us either way.)
   const int run = max(1, (kb1 - kb0 + SUMS - 1) / SUMS);
 
   if (warp == 0) {
@@ -1092,12 +1092,13 @@ int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 // Whether every row has a cluster of its own.  That kernel's time grows with the rows, the
 // tiles' hardly does until they fill the device.  In us (bf16, 8 adapters), rows' / tiles':
 //     K, N, rank       128 rows    256 rows    512 rows
-//     4096, 4096, 16    9.4 / 22   17.4 / 22   30.5 / 22
-//     4096, 4096, 64   17.2 / 35   30   / 33   56   / 32
-//     1024, 1024, 16    7.4 / 16   13.4 / 15   23.5 / 15
-//     4096, 11008, 16  13.8 / 33   25.5 / 30   48   / 31
+//     4096, 4096, 16    9.2 / 22   17.0 / 21   30.5 / 22
+//     4096, 4096, 64   17.0 / 34   29.8 / 32   62   / 33
+//     1024, 1024, 16    7.0 / 15   13.1 / 15   23.3 / 16
+//     4096, 11008, 16  13.4 / 32   25.3 / 30   55   / 31
 // Up to 512 rows that may have an adapter for every 8 of them keep to rows too: with 64
-// adapters in no order, a tile each, the last line's 512 rows are 48 / 160.
+// adapters in no order, a tile each, the last line's 512 rows are 57 / 100.  How many of
+// them are in use is not known here: with 4 of the 64, a run of rows each, 54 / 44.
 bool by_rows(const AdapterArgs& a) { return a.T <= 256 || (a.T <= 512 && a.T <= 8 * a.L); }
 
 cudaError_t launch_many(const AdapterArgs& a, const AdapterParams& r, void* scratch,

@@ -264,3 +264,30 @@ def test_choose_grad_term_by_term(mhr, T, E, top, dtype, score, renormalize):
     floor = 2.0 ** -25 if dtype == "f16" else 0
     floor = floor + 2.0 ** -46 * size.sum(1, keepdims=True)
     assert np.all(np.abs(got - want) <= 120 * 2.0 ** -24 * size + step * np.abs(want) + floor)
+
+
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+def test_long_sums_of_adapters_are_cut(mhr, out):
+    """x down^T of 32768 positive terms, less itself in three bf16 values: its error is left. A
+    cluster has up to 8 CTAs of up to 4 accumulators, 64 steps of 16 terms each. A step truncates
+    by a unit, 2^-23 of the sum so far at most: 64 / 2 of those on average over a growing sum, and
+    8 more for what adds up the parts and multiplies them."""
+    import torch
+
+    T, K, N = 300, 32768, 64
+    gen = torch.Generator().manual_seed(4)
+    x, down = torch.rand(T, K, generator=gen).bfloat16(), torch.zeros(1, 4, K).bfloat16()
+    down[0, 0] = torch.rand(K, generator=gen).bfloat16()
+    down[0, 0, :3] = 0
+    v = x.double() @ down[0, 0].double()
+    rest = v.clone()
+    for i in range(3):
+        x[:, i], down[0, i + 1, i] = rest.bfloat16(), 1
+        rest -= rest.bfloat16().double()
+    up = torch.tensor([1.0, -1.0, -1.0, -1.0]).bfloat16()[None, :, None].repeat(1, 1, N)
+    y = torch.zeros(T, N, dtype=types()[out], device="cuda")
+    which = torch.zeros(T, dtype=torch.int32, device="cuda")
+    got = mhr.add_adapters(y, x.cuda(), down.cuda(), up.contiguous().cuda(), which)
+    assert float(rest.abs().max()) < 2.0 ** -24 * float(v.min())
+    err = (got.double().cpu().abs() / v[:, None]).mean()
+    assert float(err) <= (32 + 8) * 2.0 ** -23, float(err)
