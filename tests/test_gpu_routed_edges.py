@@ -291,3 +291,28 @@ def test_long_sums_of_adapters_are_cut(mhr, out):
     assert float(rest.abs().max()) < 2.0 ** -24 * float(v.min())
     err = (got.double().cpu().abs() / v[:, None]).mean()
     assert float(err) <= (32 + 8) * 2.0 ** -23, float(err)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("out_dtype", ["bf16", "f32"])
+def test_a_rows_product_does_not_go_by_the_rows_beside_it(mhr, out_dtype, transposed):
+    """Alone, in a tile of few rows, and in the largest: to the last bit."""
+    import torch
+
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    x = torch.randn(700, 1000, generator=gen, device="cuda").bfloat16()
+    w = torch.randn(2, 264, 1000, generator=gen, device="cuda").bfloat16()
+    if not transposed:
+        w = w.transpose(1, 2).contiguous()
+    kw = dict(transposed=transposed, out_dtype=types()[out_dtype])
+
+    def first(rows):
+        at = torch.tensor([0, rows, 700], dtype=torch.int32, device="cuda")
+        return mhr.matmul_experts(x, w, at, **kw)[:rows]
+
+    whole = first(700)
+    for rows in (1, 33, 129, 260):
+        assert torch.equal(first(rows), whole[:rows])
+    order = torch.arange(700, dtype=torch.int32, device="cuda")
+    few = torch.tensor([0, 40, 40], dtype=torch.int32, device="cuda")
+    assert torch.equal(mhr.matmul_experts(x, w, few, gather=order[:40], **kw), whole[:40])
