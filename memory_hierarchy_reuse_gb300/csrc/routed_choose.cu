@@ -8,7 +8,7 @@
 // keys; the best of all are then taken one by one from the lists' heads.
 //
 // Bound by the issue of instructions, not by the logits' bytes (16384 x 256 fp32 logits
-// are 2.5 us of the memory's time and take 20 us on a GB300, 971 instructions a token; one
+// are 2.5 us of the memory's time and take 21 us on a GB300, 1005 instructions a token; one
 // token 4.4 us call after call, its gradient as much): keys are integers that order as the floats do,
 // sorted by minima and maxima alone, their indices found again for the chosen; a token
 // with a NaN, or with keys too near for 32 bits, is done again in double by a function

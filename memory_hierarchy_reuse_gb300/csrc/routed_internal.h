@@ -64,7 +64,14 @@ struct Operand {
 cudaError_t ready(const void* p, int64_t parts, int64_t rows, int64_t cols, int64_t ld,
                   int64_t stride, const int32_t* offsets, const int32_t* index, int64_t top,
                   int64_t picked, char** scratch, cudaStream_t s, Operand* out);
-// Up to so many rows a product picks by TMA's gather, without that.
+// Up to so many rows a product picks by TMA's gather, without that.  In us from cold L2 (bf16),
+// gathered / put in order, by rows:
+//     experts, K, N        64           256          512 (666)    1024 (2000)  8000 (4000)
+//     128, 4096, 1536      113 / 119    215 / 218    245 / 250    260 / 263    322 / 283
+//     16, 4096, 4096       102 / 107    111 / 109    111 / 109    188 / 117    315 / 137
+//     8, 1024, 1024        15.4 / 17.2  18.4 / 17.4  20.5 / 17.7  30.7 / 21.1  30.7 / 23.2
+// (in brackets: the rows of the last two lines).  The gather pays below some 20 rows an expert;
+// the limit by all rows is off by up to 5 us between.
 constexpr int64_t FEW_ROWS = 256;
 
 // One gemm_routed_product (product, transposed) or gemm_routed_weight_grad

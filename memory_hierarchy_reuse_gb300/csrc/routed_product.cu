@@ -60,10 +60,10 @@ constexpr int THREADS = 32 * (3 + EPI_WARPS);
 enum Mode { PRODUCT = 0, TRANSPOSED = 1, GRADIENT = 2 };
 
 // LONG: fp32 results.  The tensor cores add into their fp32 accumulators by truncation,
-// which takes some 4e-8 of a sum off for every 16 terms (6e-7 after 256, 4e-6 after
-// 4096, where fp32 in any order would leave 2e-7): the sum goes on in registers, rounded
-// to nearest, after every SEGMENT stages.  16-bit results, 2e-3 or 2e-4 off by their own
-// rounding, do without.  An epilogue thread holds 64 of a tile's 128 columns.
+// which takes 1.4e-8 of a sum off with its first 16 terms, 3e-7 after 256 and 1.7e-6 after
+// 1024 (means of sums of positive terms, GB300): the sum goes on in registers, rounded
+// to nearest, after every SEGMENT stages.  16-bit results, up to 4e-3 or 5e-4 off by their
+// own rounding, do without.  An epilogue thread holds 64 of a tile's 128 columns.
 template <bool LONG>
 struct Shape {
   static constexpr int ROWS = LONG ? 128 : 256;            // rows of a pair's tile, at most
